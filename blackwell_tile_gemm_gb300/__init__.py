@@ -110,6 +110,15 @@ def lib() -> ctypes.CDLL:
         L.gemm_bf16_gather.restype = i32
         L.gemm_bf16_gather.argtypes = [vp, i64, i64, vp, i64, vp, i64, vp, i64, i64, i64, i32,
                                        ctypes.POINTER(tg_epilogue), u32, vp]
+        L.gemm_bf16_grouped.restype = i32
+        L.gemm_bf16_grouped.argtypes = [vp, i64, i64, vp, vp, i64, i64, vp, i64, i64, vp, i64, i64,
+                                        i64, i32, ctypes.POINTER(tg_epilogue), u32, vp]
+        L.gemm_bf16_grouped_dgrad.restype = i32
+        L.gemm_bf16_grouped_dgrad.argtypes = [vp, i64, vp, i64, i64, vp, i64, i64, vp, i64, i64,
+                                              i64, i32, u32, vp]
+        L.gemm_bf16_grouped_wgrad.restype = i32
+        L.gemm_bf16_grouped_wgrad.argtypes = [vp, i64, vp, i64, i64, vp, vp, i64, i64, vp, i64,
+                                              i64, i64, i64, i32, u32, vp]
         L.tg_gemm_tail_split.restype = i32
         L.tg_gemm_tail_split.argtypes = [i64, i64, i64, u32]
         L.tg_gemm_multicast.restype = i32
@@ -363,6 +372,143 @@ def gemm_bf16_gather(A, row_idx, B, D=None, *, out_dtype=None, epilogue_add=None
                                 _flags(cta_pair, False) | (TG_FLAG_GATHER_TMA if gather_tma else 0),
                                 _stream_handle(stream))
     _check(rc, "gemm_bf16_gather")
+    return D
+
+
+def _slices(t, name, mult=8):
+    """(row stride, slice stride) in elements of a [slices, rows, width] tensor."""
+    if t.dim() != 3:
+        raise ValueError(f"{name} must be 3-D")
+    slices, rows, width = t.shape
+    st = t.stride()
+    if t.numel() > 0 and width > 1 and st[2] != 1:
+        raise ValueError(f"{name} must have unit inner stride")
+    ld = st[1] if rows > 1 else -(-max(width, 1) // mult) * mult
+    return ld, (st[0] if slices > 1 else ld * max(rows, 1))
+
+
+def _new_rows(shape, dtype, device, zero=False):
+    """An output whose rows start on 16-byte boundaries (a padded view where
+    the width asks for it)."""
+    import torch
+    make = torch.zeros if zero else torch.empty
+    mult = 4 if dtype == torch.float32 else 8
+    width = -(-shape[-1] // mult) * mult
+    return make(tuple(shape[:-1]) + (width,), dtype=dtype, device=device)[..., :shape[-1]]
+
+
+def _int32_vector(t, name, length=None):
+    import torch
+    if t.dtype != torch.int32 or t.dim() != 1 or not t.is_contiguous():
+        raise TypeError(f"{name} must be a contiguous int32 vector")
+    if length is not None and t.shape[0] != length:
+        raise ValueError(f"{name} must have {length} elements")
+    return t.data_ptr()
+
+
+def _bf16_only(**tensors):
+    import torch
+    for name, t in tensors.items():
+        if t.dtype != torch.bfloat16:
+            raise TypeError(f"{name} must be bfloat16")
+
+
+def _group_epilogue(bias, groups, N, epi_kw):
+    """make_epilogue with a bias of one row per group."""
+    if bias is not None:
+        if tuple(bias.shape) != (groups, N):
+            raise ValueError("bias must be [groups, N]")
+        if not bias.is_contiguous():
+            raise TypeError("bias must be contiguous")
+        bias = bias.view(-1)
+    return make_epilogue(bias=bias, **epi_kw)
+
+
+def gemm_bf16_grouped(A, B, offsets, D=None, *, row_idx=None, out_dtype=None, epilogue_add=None,
+                      silu_affine=None, bias=None, bias_silu=False, affine=None, stream=None):
+    """D[i] = A[i] @ B[g].T (+ epilogue) for the rows i of group g: offsets[g] <= i < offsets[g+1].
+
+    A: bfloat16 [M, K]; B: bfloat16 [groups, N, K]; offsets: int32 CUDA vector
+    [groups + 1], non-decreasing, in [0, M] (``group_rows`` makes it); groups
+    may be empty.  With ``row_idx`` (int32 CUDA vector [M]) row i of the
+    product is row row_idx[i] of A (which then has any number of rows).
+    ``bias`` is float32 [groups, N]; other epilogue keywords as for
+    ``make_epilogue``.  D: float32 or bfloat16 [M, N] (default float32); rows
+    in no group are zero.
+    """
+    import torch
+    _bf16_only(A=A, B=B)
+    if B.dim() != 3 or A.dim() != 2 or A.shape[1] != B.shape[2]:
+        raise ValueError("A is [rows, K] and B is [groups, N, K]")
+    groups, N, K = B.shape
+    M = A.shape[0] if row_idx is None else row_idx.shape[0]
+    if D is None:
+        D = _new_rows((M, N), out_dtype or torch.float32, A.device)
+    if tuple(D.shape) != (M, N):
+        raise ValueError("D must be [M, N]")
+    off = _int32_vector(offsets, "offsets", groups + 1)
+    idx = None if row_idx is None else _int32_vector(row_idx, "row_idx")
+    epi = _group_epilogue(bias, groups, N, dict(epilogue_add=epilogue_add, silu_affine=silu_affine,
+                                                bias_silu=bias_silu, affine=affine))
+    ldb, gsb = _slices(B, "B")
+    rc = lib().gemm_bf16_grouped(A.data_ptr(), _ld(A, "A", 8), A.shape[0], idx, off, groups, M,
+                                 B.data_ptr(), ldb, gsb, D.data_ptr(), _ld(D, "D", 8), N, K,
+                                 _d_code(D.dtype), ctypes.byref(epi), 0, _stream_handle(stream))
+    _check(rc, "gemm_bf16_grouped")
+    return D
+
+
+def gemm_bf16_grouped_dgrad(G, B, offsets, D=None, *, out_dtype=None, stream=None):
+    """Gradient of the rows of ``gemm_bf16_grouped``: D[i] = G[i] @ B[g].
+
+    G: bfloat16 [M, N]; B: bfloat16 [groups, N, K]; offsets as there.  D:
+    float32 or bfloat16 [M, K] (default float32); rows in no group are zero.
+    """
+    import torch
+    _bf16_only(G=G, B=B)
+    if B.dim() != 3 or G.dim() != 2 or G.shape[1] != B.shape[1]:
+        raise ValueError("G is [M, N] and B is [groups, N, K]")
+    groups, N, K = B.shape
+    M = G.shape[0]
+    if D is None:
+        D = _new_rows((M, K), out_dtype or torch.float32, G.device)
+    if tuple(D.shape) != (M, K):
+        raise ValueError("D must be [M, K]")
+    off = _int32_vector(offsets, "offsets", groups + 1)
+    ldb, gsb = _slices(B, "B")
+    rc = lib().gemm_bf16_grouped_dgrad(G.data_ptr(), _ld(G, "G", 8), off, groups, M, B.data_ptr(),
+                                       ldb, gsb, D.data_ptr(), _ld(D, "D", 8), N, K,
+                                       _d_code(D.dtype), 0, _stream_handle(stream))
+    _check(rc, "gemm_bf16_grouped_dgrad")
+    return D
+
+
+def gemm_bf16_grouped_wgrad(G, A, offsets, D=None, *, row_idx=None, out_dtype=None, stream=None):
+    """Gradient of the weights of ``gemm_bf16_grouped``: D[g] = G[rows of g].T @ A[rows of g].
+
+    G: bfloat16 [M, N]; A: bfloat16 [M, K], or any rows picked by ``row_idx``;
+    offsets as there.  D: float32 or bfloat16 [groups, N, K] (default
+    float32), zero for an empty group.
+    """
+    import torch
+    _bf16_only(G=G, A=A)
+    M = A.shape[0] if row_idx is None else row_idx.shape[0]
+    if A.dim() != 2 or G.dim() != 2 or G.shape[0] != M:
+        raise ValueError("G is [M, N] and A is [M, K] (or rows picked by row_idx)")
+    if offsets.shape[0] < 2:
+        raise ValueError("offsets must have groups + 1 elements")
+    groups, N, K = offsets.shape[0] - 1, G.shape[1], A.shape[1]
+    if D is None:
+        D = _new_rows((groups, N, K), out_dtype or torch.float32, G.device)
+    if tuple(D.shape) != (groups, N, K):
+        raise ValueError("D must be [groups, N, K]")
+    off = _int32_vector(offsets, "offsets")
+    idx = None if row_idx is None else _int32_vector(row_idx, "row_idx")
+    ldd, gsd = _slices(D, "D")
+    rc = lib().gemm_bf16_grouped_wgrad(G.data_ptr(), _ld(G, "G", 8), A.data_ptr(), _ld(A, "A", 8),
+                                       A.shape[0], idx, off, groups, M, D.data_ptr(), ldd, gsd, N,
+                                       K, _d_code(D.dtype), 0, _stream_handle(stream))
+    _check(rc, "gemm_bf16_grouped_wgrad")
     return D
 
 

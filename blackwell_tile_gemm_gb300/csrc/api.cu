@@ -116,20 +116,22 @@ namespace {
 // these fields, so a hit returns exactly what a fresh encode would.  Bounded
 // (cleared when full); keeps repeated calls on the same buffers off the
 // driver's encoder.
+// slices == 0: a 2-D map; otherwise the third extent and its byte stride.
 struct MapKey {
   uint64_t base, inner, outer, row_bytes;
   uint32_t dtype, box_inner, box_outer, swizzle;
+  uint64_t slices, slice_bytes;
   bool operator==(const MapKey& o) const {
     return base == o.base && inner == o.inner && outer == o.outer && row_bytes == o.row_bytes &&
            dtype == o.dtype && box_inner == o.box_inner && box_outer == o.box_outer &&
-           swizzle == o.swizzle;
+           swizzle == o.swizzle && slices == o.slices && slice_bytes == o.slice_bytes;
   }
 };
 struct MapKeyHash {
   size_t operator()(const MapKey& k) const {
     uint64_t h = 1469598103934665603ull;
-    const uint64_t v[8] = {k.base, k.inner, k.outer, k.row_bytes, k.dtype, k.box_inner,
-                           k.box_outer, k.swizzle};
+    const uint64_t v[10] = {k.base, k.inner, k.outer, k.row_bytes, k.dtype, k.box_inner,
+                            k.box_outer, k.swizzle, k.slices, k.slice_bytes};
     for (uint64_t x : v) h = (h ^ x) * 1099511628211ull;
     return static_cast<size_t>(h);
   }
@@ -139,16 +141,18 @@ std::mutex g_map_mutex;
 std::unordered_map<MapKey, CUtensorMap, MapKeyHash> g_map_cache;
 }  // namespace
 
-int make_tensor_map_2d(CUtensorMap* map, CUtensorMapDataType dtype, const void* base,
-                       uint64_t inner, uint64_t outer, uint64_t row_bytes, uint32_t box_inner,
-                       uint32_t box_outer, CUtensorMapSwizzle swizzle) {
+namespace {
+int make_tensor_map(CUtensorMap* map, CUtensorMapDataType dtype, const void* base,
+                    uint64_t inner, uint64_t outer, uint64_t row_bytes, uint32_t box_inner,
+                    uint32_t box_outer, CUtensorMapSwizzle swizzle, uint64_t slices,
+                    uint64_t slice_bytes) {
   // A zero extent is not encodable; callers never launch for empty problems,
   // but keep a valid map (extent 1) for unused descriptor parameters.
   if (inner == 0) inner = 1;
   if (outer == 0) outer = 1;
   const MapKey key{reinterpret_cast<uint64_t>(base), inner, outer, row_bytes,
                    static_cast<uint32_t>(dtype), box_inner, box_outer,
-                   static_cast<uint32_t>(swizzle)};
+                   static_cast<uint32_t>(swizzle), slices, slice_bytes};
   {
     std::lock_guard<std::mutex> lk(g_map_mutex);
     auto it = g_map_cache.find(key);
@@ -170,11 +174,11 @@ int make_tensor_map_2d(CUtensorMap* map, CUtensorMapDataType dtype, const void* 
       g_encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
     }
   }
-  cuuint64_t dims[2] = {inner, outer};
-  cuuint64_t strides[1] = {row_bytes};
-  cuuint32_t box[2] = {box_inner, box_outer};
-  cuuint32_t estr[2] = {1, 1};
-  CUresult r = g_encode(map, dtype, 2, const_cast<void*>(base), dims, strides, box, estr,
+  cuuint64_t dims[3] = {inner, outer, slices};
+  cuuint64_t strides[2] = {row_bytes, slice_bytes};
+  cuuint32_t box[3] = {box_inner, box_outer, 1};
+  cuuint32_t estr[3] = {1, 1, 1};
+  CUresult r = g_encode(map, dtype, slices ? 3 : 2, const_cast<void*>(base), dims, strides, box, estr,
                         CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   if (r != CUDA_SUCCESS) return cuda_fail(cudaErrorInvalidValue);
@@ -182,6 +186,22 @@ int make_tensor_map_2d(CUtensorMap* map, CUtensorMapDataType dtype, const void* 
   if (g_map_cache.size() >= kMapCacheMax) g_map_cache.clear();
   g_map_cache.emplace(key, *map);
   return TG_OK;
+}
+}  // namespace
+
+int make_tensor_map_2d(CUtensorMap* map, CUtensorMapDataType dtype, const void* base,
+                       uint64_t inner, uint64_t outer, uint64_t row_bytes, uint32_t box_inner,
+                       uint32_t box_outer, CUtensorMapSwizzle swizzle) {
+  return make_tensor_map(map, dtype, base, inner, outer, row_bytes, box_inner, box_outer, swizzle,
+                         0, 0);
+}
+
+int make_tensor_map_3d(CUtensorMap* map, CUtensorMapDataType dtype, const void* base,
+                       uint64_t inner, uint64_t outer, uint64_t slices, uint64_t row_bytes,
+                       uint64_t slice_bytes, uint32_t box_inner, uint32_t box_outer,
+                       CUtensorMapSwizzle swizzle) {
+  return make_tensor_map(map, dtype, base, inner, outer, row_bytes, box_inner, box_outer, swizzle,
+                         slices ? slices : 1, slice_bytes);
 }
 
 namespace {

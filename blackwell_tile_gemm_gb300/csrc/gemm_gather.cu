@@ -60,6 +60,24 @@ size_t gather_workspace_bytes(int64_t M, int64_t K) {
   return static_cast<size_t>(M) * static_cast<size_t>((K + 63) / 64 * 64) * 2u;
 }
 
+int gather_to_workspace(const void* A, int64_t lda, int a_rows, const int* row_idx, int64_t M,
+                        int64_t K, const void** rows, int64_t* ld, cudaStream_t stream,
+                        DeviceCtx* ctx) {
+  int rc = TG_OK;
+  void* ws = device_workspace(gather_workspace_bytes(M, K), stream, &rc);
+  if (ws == nullptr) return rc;
+  *ld = (K + 63) / 64 * 64;
+  int64_t blocks = (M + 7) / 8;
+  if (blocks > 16 * static_cast<int64_t>(ctx->num_sms)) blocks = 16 * ctx->num_sms;
+  gather_rows_kernel<<<static_cast<unsigned>(blocks), 256, 0, stream>>>(
+      static_cast<const uint16_t*>(A), lda, a_rows, row_idx, static_cast<int>(M),
+      static_cast<uint16_t*>(ws), *ld, static_cast<int>(K));
+  const cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return cuda_fail(e);
+  *rows = ws;
+  return TG_OK;
+}
+
 int launch_gemm_bf16_pregather_impl(const void* A, int64_t lda, int a_rows, const int* row_idx,
                                     int M, const void* B, int64_t ldb, void* D, int64_t ldd,
                                     int N, int K, int d_dtype, const Epi& epi, bool pair,

@@ -1,0 +1,990 @@
+// Products whose weights change with the row: one persistent, warp-specialised
+// tcgen05 kernel for four of them, all bf16 with f32 accumulation.
+//
+//   kGroupedForward  D[i, :] = A[i, :] * B[g]^T      rows i of group g
+//   kGroupedDgrad    dA[i, :] = G[i, :] * B[g]        (contraction over N)
+//   kGroupedWgrad    dB[g] = G[rows of g]^T * A[rows of g]
+//   kAdapter         D[i, :] = A[i, :] * B^T + H[i, :] * up[id_i]^T
+//
+// Group g owns the rows offsets[g] <= i < offsets[g+1]; the offsets live on
+// the device, so the host never learns the sizes and the tile list is made
+// here (GroupWalk).
+//
+// Orientation.  The contiguous axis of D fills the MMA's M (the "wide" axis:
+// N of the weights in the forward product, K in both gradients) and the other
+// axis of D its N ("cols" below: the rows of a group, or N for the weight
+// gradient).  The MMA's N is a runtime value in steps of 16 per CTA, so a
+// group of 40 rows costs 48 or 64 columns, not a 128- or 256-row tile; and an
+// accumulator row is a lane, so a warp's store of one accumulator column
+// writes 32 consecutive elements of one row of D: coalesced straight from
+// registers, with every ragged edge a predicate and no staging buffer.
+//
+// Operands in shared memory, 64 of the contraction index per stage, 128-byte
+// rows, 128B swizzle:
+//   K-major  [row][64 k]  (the contraction index is contiguous in memory),
+//   MN-major [k][64 m]    (the other index is): boxes of 64 x 64, next 64
+//            m at LBO = 8 KB, next 8 k at SBO = 1 KB, a K16 MMA step = 2 KB.
+// The gradients need no transposed copy of anything: dgrad reads B[g]
+// MN-major, wgrad both operands.
+//
+// Ragged contraction (wgrad): a group's last stage holds rows of the next
+// group below its own.  0 * NaN is NaN, so both operands' rows past the
+// group's end, up to the next multiple of 16 (fewer MMAs are issued instead
+// of the rest), are overwritten with zeros by a fixing warp between the
+// loads and the MMAs.
+//
+// Adapters: H[i] = scale * A[i] * down[id_i]^T was computed before and split
+// into two bf16 terms (hi + lo keep 16 bits of it, so the product with
+// up[id] is as exact as the base product).  After the tile's K stages each
+// adapter that occurs among the tile's rows adds ceil(rank / 64) * 2 stages:
+// up[id] by TMA, H written by the fixing warps with zeros in the rows of
+// other adapters.  The base product and every adapter's term meet in one
+// accumulator: D is written once.
+//
+// Few rows (kSplit, single CTAs): the product is bound by reading the
+// weights, tiles are few, so S units share a tile's contraction; each writes
+// an f32 partial and the one that arrives last adds them in piece order (the
+// same bits every time; nobody waits).  There the adapter term needs no MMA:
+// the epilogue adds up[id][n, :] . H[i, :] in f32.
+//
+// Roles: warp 0 TMA producer, warp 1 TMEM allocator and MMA issuer, warps
+// 2..9 epilogue, then kFixWarps fixing warps.  Every wait is bounded.
+#pragma once
+
+#include <cstdint>
+#include <cuda.h>
+
+#include "epilogue.cuh"
+#include "tg_ptx.cuh"
+
+namespace tg {
+
+enum : int { kGroupedForward = 0, kGroupedDgrad = 1, kGroupedWgrad = 2, kAdapter = 3 };
+
+enum : uint32_t {
+  kSiteGrEmpty = 31,
+  kSiteGrFull = 32,
+  kSiteGrFix = 33,
+  kSiteGrAccEmpty = 34,
+  kSiteGrAccFull = 35,
+  kSiteGrFixIn = 36,
+  kSiteGrOffsets = 40,   // not a wait: the offsets decrease or leave [0, M]
+};
+
+struct GroupedArgs {
+  int M;               // rows of all groups together (extent of the offsets)
+  int wide;            // extent of D's contiguous axis
+  int cols;            // wgrad: rows of one group's D; else unused
+  int num_wide_tiles;  // tiles of kCtaGroup * 128
+  int num_col_tiles;   // wgrad: tiles of kTileN over cols
+  int num_k_blocks;    // stages of 64 of the contraction index (not wgrad)
+  int groups;
+  const int* offsets;  // [groups + 1], or null: one group of all M rows
+  void* D;
+  int64_t ldd;
+  int64_t group_stride_d;  // wgrad
+  Epi epi;                 // bias: [groups][wide]
+  // adapters
+  const int* ids;          // [M]
+  int adapters, rank;
+  const float* h;          // [M][rank] f32 (few rows)
+  const uint16_t* h_hi;    // [M][rank] bf16 (MMA form)
+  const uint16_t* h_lo;
+  const uint16_t* up;
+  int64_t ld_up, group_stride_up;
+  // split contraction
+  int max_slots;           // partial tiles that fit (0: never split)
+  int max_counters;
+  float* partials;         // [tile][piece][kTileN][128] f32
+  uint32_t* counters;      // [tile], 0 between launches
+  uint32_t* status;
+  uint64_t timeout_ns;
+};
+
+template <int kMode_, int kCtaGroup_, int kTileN_, int kStages_, bool kBf16Out_>
+struct GroupedCfg {
+  static constexpr int kMode = kMode_;
+  static constexpr int kCtaGroup = kCtaGroup_;
+  static constexpr int kTileN = kTileN_;          // most MMA columns of a tile
+  static constexpr int kStages = kStages_;
+  static constexpr bool kBf16Out = kBf16Out_;
+  static constexpr bool kWideMn = kMode == kGroupedDgrad || kMode == kGroupedWgrad;
+  static constexpr bool kColMn = kMode == kGroupedWgrad;
+  static constexpr bool kSplit = kCtaGroup == 1;
+  // Adapter stages (MMA form) and ragged contractions are fixed up in shared
+  // memory before the MMAs read them.
+  static constexpr bool kExt = kMode == kAdapter && kCtaGroup == 2;
+  static constexpr int kFixWarps = kExt ? 2 : kMode == kGroupedWgrad ? 1 : 0;
+  static constexpr int kColStep = 16 * kCtaGroup;
+  static constexpr int C_ROWS = kTileN / kCtaGroup;   // column-operand rows per CTA
+  static constexpr int W_BYTES = 128 * 128;
+  static constexpr int C_BYTES = C_ROWS * 128;
+  static constexpr int OFF_W = 0;
+  static constexpr int OFF_C = OFF_W + kStages * W_BYTES;
+  static constexpr int OFF_BAR = OFF_C + kStages * C_BYTES;
+  static constexpr int kAccBufs = 2;
+  static constexpr int NUM_BARS = 2 * kStages + 2 * kAccBufs + 1 + (kFixWarps ? 2 * kStages : 0);
+  static constexpr int OFF_MISC = OFF_BAR + NUM_BARS * 8;
+  static constexpr int SMEM_BYTES = OFF_MISC + 16 + 1024;
+  static constexpr int TMEM_COLS = 2 * kTileN <= 32    ? 32
+                                   : 2 * kTileN <= 64  ? 64
+                                   : 2 * kTileN <= 128 ? 128
+                                   : 2 * kTileN <= 256 ? 256
+                                                       : 512;
+  static constexpr int kEpiWarps = 8;
+  static constexpr int kFixWarp0 = 2 + kEpiWarps;
+  static constexpr int kThreads = 64 + 32 * (kEpiWarps + kFixWarps);
+  static_assert(SMEM_BYTES <= 227 * 1024, "shared memory per CTA");
+  static_assert(kTileN % 32 == 0 && kTileN <= 256, "MMA N");
+  static_assert(C_BYTES % 1024 == 0, "swizzle atoms");
+  static_assert(!kColMn || (kCtaGroup == 2 && kTileN == 256), "wgrad tiles");
+};
+
+// One work item.
+struct GroupedWork {
+  int g;
+  int wide0;    // first element of D's contiguous axis
+  int row0;     // first row of D (wgrad: inside the group's D)
+  int rows;     // rows of D this tile stores
+  int ncols;    // MMA columns (rows rounded up)
+  int nk;       // K stages of this unit
+  int k0, ks;   // first stage, step
+  int base;     // wgrad: first row of the contraction
+  int len;      // wgrad: its length
+  int tile;     // tile index (split scratch)
+  int piece;
+};
+
+__device__ __forceinline__ int grouped_clamp(int v, int hi) { return min(max(v, 0), hi); }
+
+// Tile index -> group, by one warp.  The lanes hold the row ranges of 32
+// consecutive groups and the running sum of their tiles; tile indices only
+// grow, so the window only moves forwards.  Offsets outside [0, M] are
+// clamped and decreasing ones raised to the running maximum: whatever the
+// device holds, the ranges are disjoint and inside the arrays.
+template <class C>
+struct GroupWalk {
+  int g0, t0, lo0;   // window: first group, tiles and first row before it
+  int lo, hi, incl;  // this lane's group: rows [lo, hi), tiles up to and with it
+  bool bad;
+
+  __device__ __forceinline__ void load(const GroupedArgs& p, int lane) {
+    const int g = g0 + lane;
+    int end = lo0;
+    if (p.offsets == nullptr) {
+      end = g0 == 0 ? p.M : lo0;
+    } else if (g < p.groups) {
+      const int raw = p.offsets[g + 1];
+      end = grouped_clamp(raw, p.M);
+      bad |= raw != end;
+    }
+    const int own = end;
+#pragma unroll
+    for (int d = 1; d < 32; d *= 2) {
+      const int o = __shfl_up_sync(0xFFFFFFFFu, end, d);
+      if (lane >= d) end = max(end, o);
+    }
+    end = max(end, lo0);
+    if (g < p.groups) bad |= end != own;
+    hi = end;
+    lo = __shfl_up_sync(0xFFFFFFFFu, end, 1);
+    if (lane == 0) lo = lo0;
+    int tiles = 0;
+    if constexpr (C::kColMn) {
+      if (g < p.groups) tiles = p.num_wide_tiles * p.num_col_tiles;
+    } else {
+      tiles = (hi - lo + C::kTileN - 1) / C::kTileN * p.num_wide_tiles;
+    }
+    incl = tiles;
+#pragma unroll
+    for (int d = 1; d < 32; d *= 2) {
+      const int o = __shfl_up_sync(0xFFFFFFFFu, incl, d);
+      if (lane >= d) incl += o;
+    }
+  }
+  __device__ __forceinline__ void start(const GroupedArgs& p, int lane) {
+    g0 = 0;
+    t0 = 0;
+    bad = false;
+    lo0 = 0;
+    if (p.offsets != nullptr) {
+      const int raw = p.offsets[0];
+      lo0 = grouped_clamp(raw, p.M);
+      bad = raw != lo0;
+    }
+    load(p, lane);
+  }
+  __device__ __forceinline__ void advance(const GroupedArgs& p, int lane) {
+    t0 += __shfl_sync(0xFFFFFFFFu, incl, 31);
+    lo0 = __shfl_sync(0xFFFFFFFFu, hi, 31);
+    g0 += 32;
+    load(p, lane);
+  }
+  // Tiles of every group; first and end row of all groups.  Leaves the walk
+  // at its start.
+  __device__ __forceinline__ int total(const GroupedArgs& p, int lane, int* first, int* end) {
+    start(p, lane);
+    *first = lo0;
+    while (g0 + 32 < p.groups) advance(p, lane);
+    const int t = t0 + __shfl_sync(0xFFFFFFFFu, incl, 31);
+    *end = __shfl_sync(0xFFFFFFFFu, hi, 31);
+    if (g0 != 0) {
+      const bool b = bad;
+      start(p, lane);
+      bad = b;
+    }
+    return t;
+  }
+  // Tile t < total, t not below the last one asked for.
+  __device__ __forceinline__ void find(const GroupedArgs& p, int lane, int t, int piece, int S,
+                                       GroupedWork& w) {
+    while (t >= t0 + __shfl_sync(0xFFFFFFFFu, incl, 31) && g0 + 32 < p.groups) advance(p, lane);
+    const uint32_t above = __ballot_sync(0xFFFFFFFFu, t0 + incl > t);
+    const int src = above ? __ffs(above) - 1 : 31;
+    const int r0 = __shfl_sync(0xFFFFFFFFu, lo, src);
+    const int r1 = __shfl_sync(0xFFFFFFFFu, hi, src);
+    const int before = __shfl_sync(0xFFFFFFFFu, incl, src > 0 ? src - 1 : 0);
+    const int l = t - t0 - (src > 0 ? before : 0);
+    w.g = g0 + src;
+    w.tile = t;
+    w.piece = piece;
+    // Tiles of a group: bands of 16 column tiles, within a band the column
+    // tile fastest, so that the units running at the same time share a
+    // weight panel and the band's rows stay in L2.
+    const int nct = C::kColMn ? p.num_col_tiles : (r1 - r0 + C::kTileN - 1) / C::kTileN;
+    const int first = l / (16 * p.num_wide_tiles) * 16;
+    const int gm = min(nct - first, 16);
+    const int r = l - first * p.num_wide_tiles;
+    const int ct = first + r % gm;
+    w.wide0 = r / gm * (128 * C::kCtaGroup);
+    if constexpr (C::kColMn) {
+      w.row0 = ct * C::kTileN;
+      w.rows = min(C::kTileN, p.cols - w.row0);
+      w.ncols = w.rows <= 128 ? 128 : 256;
+      w.base = r0;
+      w.len = r1 - r0;
+      w.nk = (w.len + 63) / 64;
+      w.k0 = 0;
+      w.ks = 1;
+    } else {
+      // The group's rows in nct tiles of equal size (a multiple of kColStep).
+      const int size = ((r1 - r0 + nct - 1) / nct + C::kColStep - 1) / C::kColStep * C::kColStep;
+      w.row0 = r0 + ct * size;
+      w.rows = min(size, r1 - w.row0);
+      w.ncols = (w.rows + C::kColStep - 1) / C::kColStep * C::kColStep;
+      // Piece q of S takes stages q, q + S, ...: at any moment the pieces of
+      // a tile read neighbouring 128-byte chunks of the same rows.
+      w.k0 = piece;
+      w.ks = S;
+      w.nk = (p.num_k_blocks - piece + S - 1) / S;
+      w.base = 0;
+      w.len = 0;
+    }
+  }
+};
+
+// Pieces of the contraction per tile: the count (at most 8, each piece at
+// least 4 stages) with the least waves * (stages per piece + 4), the 4 for a
+// unit's start, partial tile and join.
+__device__ __forceinline__ int grouped_split(const GroupedArgs& p, int tiles, int units) {
+  int best = 1;
+  int cost = (tiles + units - 1) / units * (p.num_k_blocks + 2);
+  for (int c = 2; c <= 8; ++c) {
+    if (p.num_k_blocks < 4 * c || tiles * c > p.max_slots || tiles > p.max_counters) break;
+    const int v = (tiles * c + units - 1) / units * ((p.num_k_blocks + c - 1) / c + 4);
+    if (v < cost) {
+      cost = v;
+      best = c;
+    }
+  }
+  return best;
+}
+
+// The smallest adapter above `last` among the ids of a tile's rows (each lane
+// holds kTileN / 32 of them), or -1.  Rows without an adapter hold ids that
+// compare as at least `adapters`.
+template <int kPer>
+__device__ __forceinline__ int next_adapter(const uint32_t (&ids)[kPer], int last,
+                                            uint32_t adapters) {
+  uint32_t m = adapters;
+#pragma unroll
+  for (int i = 0; i < kPer; ++i)
+    if (static_cast<int>(min(ids[i], 0x7FFFFFFFu)) > last) m = min(m, ids[i]);
+  m = __reduce_min_sync(0xFFFFFFFFu, m);
+  return m < adapters ? static_cast<int>(m) : -1;
+}
+
+template <class C>
+__device__ __forceinline__ void load_tile_ids(const GroupedArgs& p, const GroupedWork& w, int lane,
+                                              uint32_t (&ids)[C::kTileN / 32]) {
+#pragma unroll
+  for (int i = 0; i < C::kTileN / 32; ++i) {
+    const int r = lane + 32 * i;
+    ids[i] = r < w.rows ? static_cast<uint32_t>(p.ids[w.row0 + r]) : 0xFFFFFFFFu;
+  }
+}
+
+// epi(v) on the accumulators of one lane, whose column of D has bias b.
+template <int kN>
+__device__ __forceinline__ void grouped_epilogue(const Epi& e, float b, float (&v)[kN]) {
+  if (e.op == kEpiNone) return;
+  if (e.op == kEpiAddScalar || e.op == kEpiBiasCol) {
+    const float a = e.op == kEpiAddScalar ? e.alpha : b;
+#pragma unroll
+    for (int i = 0; i < kN; ++i) v[i] += a;
+  } else if (e.op == kEpiAffine) {
+#pragma unroll
+    for (int i = 0; i < kN; ++i) v[i] = v[i] * e.alpha + e.beta;
+  } else if (e.op == kEpiSiluAffine) {
+#pragma unroll
+    for (int i = 0; i < kN; ++i) v[i] = silu_f32(v[i]) * e.alpha + e.beta;
+  } else {
+#pragma unroll
+    for (int i = 0; i < kN; ++i) v[i] = silu_f32(v[i] + b);
+  }
+}
+
+// Stores 32 accumulator columns (rows row .. row + 31 of D, those below
+// `end`) of one warp; this lane holds element x of each.  f32: one 128-byte
+// store a row.  bf16: lanes pair up and exchange one value for two rows, so
+// that a store writes 64 contiguous bytes in each of two rows.
+template <class C>
+__device__ __forceinline__ void grouped_store(const GroupedArgs& p, int64_t d0, int row, int end,
+                                              int x, const float (&v)[32]) {
+  if constexpr (!C::kBf16Out) {
+    if (x >= p.wide) return;
+    float* d = reinterpret_cast<float*>(p.D) + d0 + row * p.ldd + x;
+    if (row + 32 <= end) {
+#pragma unroll
+      for (int j = 0; j < 32; ++j) __stcs(d + j * p.ldd, v[j]);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 32; ++j)
+        if (row + j < end) __stcs(d + j * p.ldd, v[j]);
+    }
+  } else {
+    const int odd = x & 1;
+    const int xe = x - odd;
+    uint16_t* d = reinterpret_cast<uint16_t*>(p.D) + d0 + (row + odd) * p.ldd + xe;
+    const bool both = xe + 1 < p.wide;
+#pragma unroll
+    for (int j = 0; j < 32; j += 2) {
+      const float give = odd ? v[j] : v[j + 1];
+      const float got = __shfl_xor_sync(0xFFFFFFFFu, give, 1);
+      const uint32_t w = odd ? pack_bf16x2(got, v[j + 1]) : pack_bf16x2(v[j], got);
+      if (xe < p.wide && row + j + odd < end) {
+        uint16_t* q = d + j * p.ldd;
+        if (both)
+          __stcs(reinterpret_cast<uint32_t*>(q), w);
+        else
+          *q = static_cast<uint16_t>(w & 0xFFFFu);
+      }
+    }
+  }
+}
+
+// Rows of D in no group: [0, first) and [end, M) are set to zero, shared out
+// over the epilogue warps of the grid.
+template <class C>
+__device__ __forceinline__ void grouped_zero_rows(const GroupedArgs& p, int first, int end,
+                                                  int warp_id, int num_warps, int lane) {
+  const int count = first + (p.M - end);
+  constexpr int kEsize = C::kBf16Out ? 2 : 4;
+  constexpr int kVec = 16 / kEsize;
+  for (int i = warp_id; i < count; i += num_warps) {
+    const int row = i < first ? i : end + (i - first);
+    uint8_t* d = reinterpret_cast<uint8_t*>(p.D) + static_cast<int64_t>(row) * p.ldd * kEsize;
+    const int nv = p.wide / kVec;
+    for (int c = lane; c < nv; c += 32) st_global_v4(d + 16 * c, 0u, 0u, 0u, 0u);
+    for (int c = nv * kVec + lane; c < p.wide; c += 32) {
+      if constexpr (C::kBf16Out)
+        reinterpret_cast<uint16_t*>(d)[c] = 0;
+      else
+        reinterpret_cast<float*>(d)[c] = 0.0f;
+    }
+  }
+}
+
+// Adapter term of a few-row tile: v[j] += up[id][x, :] . H[row + j, :] for
+// the rows of this unit's piece (row j belongs to piece j mod S).
+template <class C>
+__device__ __forceinline__ void add_adapter_terms(const GroupedArgs& p, const GroupedWork& w, int row,
+                                                  int end, int x, int S, float (&v)[32]) {
+  if (x >= p.wide) return;
+#pragma unroll
+  for (int j = 0; j < 32; ++j) {
+    if (row + j >= end || (row + j) % S != w.piece) continue;
+    const uint32_t id = static_cast<uint32_t>(__ldg(p.ids + row + j));
+    if (id >= static_cast<uint32_t>(p.adapters)) continue;
+    const uint16_t* u = p.up + id * p.group_stride_up + static_cast<int64_t>(x) * p.ld_up;
+    const float* h = p.h + static_cast<int64_t>(row + j) * p.rank;
+    float sum = 0.0f;
+    for (int r = 0; r < p.rank; r += 8) {
+      const uint4 q = ld_global_nc_v4(u + r);
+      const float4 h0 = *reinterpret_cast<const float4*>(h + r);
+      const float4 h1 = *reinterpret_cast<const float4*>(h + r + 4);
+      sum += __uint_as_float(q.x << 16) * h0.x + __uint_as_float(q.x & 0xFFFF0000u) * h0.y;
+      sum += __uint_as_float(q.y << 16) * h0.z + __uint_as_float(q.y & 0xFFFF0000u) * h0.w;
+      sum += __uint_as_float(q.z << 16) * h1.x + __uint_as_float(q.z & 0xFFFF0000u) * h1.y;
+      sum += __uint_as_float(q.w << 16) * h1.z + __uint_as_float(q.w & 0xFFFF0000u) * h1.w;
+    }
+    v[j] += sum;
+  }
+}
+
+template <class C>
+__global__ void __launch_bounds__(C::kThreads, 1)
+    gemm_grouped_kernel(const __grid_constant__ CUtensorMap tmW,
+                        const __grid_constant__ CUtensorMap tmC,
+                        const __grid_constant__ CUtensorMap tmCs,
+                        const __grid_constant__ CUtensorMap tmUp, const GroupedArgs p) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);
+  uint64_t* full_bar = bars;                       // [kStages] TMA -> MMA
+  uint64_t* empty_bar = bars + C::kStages;         // [kStages] MMA -> TMA, fixing warps
+  uint64_t* accf_bar = bars + 2 * C::kStages;      // [2] MMA -> epilogue
+  uint64_t* acce_bar = accf_bar + C::kAccBufs;     // [2] epilogue -> MMA
+  uint64_t* drain_bar = acce_bar + C::kAccBufs;
+  uint64_t* fix_bar = drain_bar + 1;               // [kStages] fixing warps -> MMA
+  uint64_t* tail_bar = fix_bar + C::kStages;       // [kStages] TMA -> fixing warp (wgrad)
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::OFF_MISC);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::OFF_MISC + 4);
+  volatile int* join = reinterpret_cast<volatile int*>(smem + C::OFF_MISC + 8);
+  volatile int* go = reinterpret_cast<volatile int*>(smem + C::OFF_MISC + 12);
+
+  const int warp = threadIdx.x >> 5;
+  const int lane = static_cast<int>(threadIdx.x & 31);
+  const uint32_t rank = C::kCtaGroup == 2 ? cluster_ctarank() : 0u;
+  const bool leader = rank == 0;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < C::kStages; ++s) {
+      mbar_init(&full_bar[s], 1);
+      mbar_init(&empty_bar[s], 1);
+      if constexpr (C::kFixWarps > 0) {
+        mbar_init(&fix_bar[s], C::kFixWarps * C::kCtaGroup);
+        mbar_init(&tail_bar[s], 1);
+      }
+    }
+    for (int b = 0; b < C::kAccBufs; ++b) {
+      mbar_init(&accf_bar[b], 1);
+      mbar_init(&acce_bar[b], C::kEpiWarps * C::kCtaGroup);
+    }
+    mbar_init(drain_bar, 1);
+    *abort_flag = 0;
+    fence_barrier_init();
+  }
+  if (warp == 0 && lane == 0) {
+    prefetch_tensormap(&tmW);
+    prefetch_tensormap(&tmC);
+    prefetch_tensormap(&tmCs);
+    if constexpr (C::kExt) prefetch_tensormap(&tmUp);
+  }
+  if (warp == 1) {
+    tmem_alloc<C::kCtaGroup>(tmem_slot, C::TMEM_COLS);
+    tmem_relinquish<C::kCtaGroup>();
+  }
+  tc_fence_before_sync();
+  __syncthreads();
+  if constexpr (C::kCtaGroup == 2) cluster_sync();
+  tc_fence_after_sync();
+  const uint32_t tmem_base = *tmem_slot;
+  griddep_wait();
+
+  const WaitGuard guard{p.status, abort_flag, p.timeout_ns};
+  const int unit = blockIdx.x / C::kCtaGroup;
+  const int num_units = gridDim.x / C::kCtaGroup;
+  // Every role's warp walks the groups itself.
+  GroupWalk<C> walk;
+  int first_row, end_row;
+  const int tiles = walk.total(p, lane, &first_row, &end_row);
+  const int S = C::kSplit ? grouped_split(p, tiles, num_units) : 1;
+  const int num_items = tiles * S;
+  GroupedWork w;
+
+  if (warp == 0) {
+    // ------------------------------------------------------------ producer
+    if (blockIdx.x == 0) {
+      const bool bad = __any_sync(0xFFFFFFFFu, walk.bad);
+      if (bad && lane == 0 && atomicCAS(p.status, 0u, 1u) == 0u) {
+        p.status[1] = kSiteGrOffsets;
+        p.status[2] = 0;
+        p.status[3] = 0;
+      }
+    }
+    const uint64_t pol = policy_evict_last();
+    const uint32_t sW = smem_addr(smem + C::OFF_W);
+    const uint32_t sC = smem_addr(smem + C::OFF_C);
+    const uint32_t empty0 = smem_addr(&empty_bar[0]);
+    const uint32_t full0 = smem_addr(&full_bar[0]);
+    const uint32_t full_dst0 = C::kCtaGroup == 2 ? map_to_cta(full0, 0u) : full0;
+    int stage = 0;
+    uint32_t phase = 0;
+    uint32_t issued = 0, issued_parity = 0;    // full_bar
+    uint32_t tailed = 0, tail_parity = 0;      // tail_bar: used, parity of the last use
+    int ok = 1;
+    auto wait_slot = [&]() -> bool {
+      return mbar_try_wait(empty0 + 8u * stage, phase ^ 1u) ||
+             mbar_wait(&empty_bar[stage], phase ^ 1u, guard, kSiteGrEmpty);
+    };
+    auto next_slot = [&]() {
+      issued |= 1u << stage;
+      issued_parity = (issued_parity & ~(1u << stage)) | (phase << stage);
+      if (++stage == C::kStages) {
+        stage = 0;
+        phase ^= 1u;
+      }
+    };
+    for (int u = unit; u < num_items && ok; u += num_units) {
+      walk.find(p, lane, u / S, u % S, S, w);
+      const int wx = w.wide0 + static_cast<int>(rank) * 128;
+      const int crows = w.ncols / C::kCtaGroup;       // column-operand rows of this CTA
+      const int crow0 = w.row0 + static_cast<int>(rank) * crows;
+      if (lane == 0) {
+        const uint32_t cbytes = static_cast<uint32_t>(crows) * 128u;
+        for (int j = 0, kb = w.k0; j < w.nk; ++j, kb += w.ks) {
+          if (!wait_slot()) {
+            ok = 0;
+            break;
+          }
+          const int kx = kb * 64;
+          const uint32_t dW = sW + stage * C::W_BYTES;
+          const uint32_t dC = sC + stage * C::C_BYTES;
+          const bool tail = C::kColMn && w.len - kx < 64;
+          if (tail) {
+            // Both CTAs' loads of a ragged stage complete locally, for the
+            // CTA's own fixing warp.
+            if (leader) mbar_arrive(&full_bar[stage]);
+            const uint32_t tb = smem_addr(&tail_bar[stage]);
+            mbar_arrive_expect_tx(&tail_bar[stage], C::W_BYTES + cbytes);
+            for (int c = 0; c < 2; ++c)
+              tma_load_2d(dW + 8192 * c, &tmW, tb, wx + 64 * c, w.base + kx, pol);
+            for (int c = 0; c < crows / 64; ++c)
+              tma_load_2d(dC + 8192 * c, &tmC, tb, crow0 + 64 * c, w.base + kx, pol);
+            tail_parity = (tailed >> stage) & 1u ? tail_parity ^ (1u << stage)
+                                                 : tail_parity & ~(1u << stage);
+            tailed |= 1u << stage;
+            next_slot();
+            continue;
+          }
+          const uint32_t fb = full_dst0 + 8u * stage;
+          if (leader)
+            mbar_arrive_expect_tx(&full_bar[stage], C::kCtaGroup * (C::W_BYTES + cbytes));
+          if constexpr (C::kMode == kGroupedWgrad) {
+            for (int c = 0; c < 2; ++c)
+              tma_load_2d_pair(dW + 8192 * c, &tmW, fb, wx + 64 * c, w.base + kx, pol);
+            for (int c = 0; c < crows / 64; ++c)
+              tma_load_2d_pair(dC + 8192 * c, &tmC, fb, crow0 + 64 * c, w.base + kx, pol);
+          } else if constexpr (C::kCtaGroup == 2) {
+            if constexpr (C::kWideMn) {
+              for (int c = 0; c < 2; ++c)
+                tma_load_3d_pair(dW + 8192 * c, &tmW, fb, wx + 64 * c, kx, w.g, pol);
+            } else {
+              tma_load_3d_pair(dW, &tmW, fb, kx, wx, w.g, pol);
+            }
+            if (crows == C::C_ROWS) {
+              tma_load_2d_pair(dC, &tmC, fb, kx, crow0, pol);
+            } else {
+              for (int c = 0; c < crows; c += 16)
+                tma_load_2d_pair(dC + 128 * c, &tmCs, fb, kx, crow0 + c, pol);
+            }
+          } else {
+            if constexpr (C::kWideMn) {
+              for (int c = 0; c < 2; ++c)
+                tma_load_3d(dW + 8192 * c, &tmW, fb, wx + 64 * c, kx, w.g, pol);
+            } else {
+              tma_load_3d(dW, &tmW, fb, kx, wx, w.g, pol);
+            }
+            if (crows == C::C_ROWS) {
+              tma_load_2d(dC, &tmC, fb, kx, crow0, pol);
+            } else {
+              for (int c = 0; c < crows; c += 16)
+                tma_load_2d(dC + 128 * c, &tmCs, fb, kx, crow0 + c, pol);
+            }
+          }
+          next_slot();
+        }
+      }
+      ok = __shfl_sync(0xFFFFFFFFu, ok, 0);
+      if constexpr (C::kExt) {
+        uint32_t ids[C::kTileN / 32];
+        load_tile_ids<C>(p, w, lane, ids);
+        for (int id = next_adapter(ids, -1, p.adapters); id >= 0 && ok;
+             id = next_adapter(ids, id, p.adapters)) {
+          if (lane == 0) {
+            // Stages: rank columns 0.., 64.., ... of hi, then the same of lo.
+            const int per = (p.rank + 63) / 64 * 64;
+            for (int r = 0; r < 2 * per; r += 64) {
+              if (!wait_slot()) {
+                ok = 0;
+                break;
+              }
+              if (leader) mbar_arrive_expect_tx(&full_bar[stage], 2 * C::W_BYTES);
+              tma_load_3d_pair(sW + stage * C::W_BYTES, &tmUp, full_dst0 + 8u * stage,
+                               r < per ? r : r - per, wx, id, pol);
+              next_slot();
+            }
+          }
+          ok = __shfl_sync(0xFFFFFFFFu, ok, 0);
+        }
+      }
+    }
+    if (lane == 0) {
+      griddep_launch_dependents();
+      if (!ok) {
+        for (int s = 0; s < C::kStages; ++s) {
+          if (leader && (issued & (1u << s)))
+            mbar_wait_drain(&full_bar[s], (issued_parity >> s) & 1u, p.timeout_ns);
+          if (tailed & (1u << s))
+            mbar_wait_drain(&tail_bar[s], (tail_parity >> s) & 1u, p.timeout_ns);
+        }
+      }
+    }
+  } else if (warp == 1) {
+    // ------------------------------------------------------------ MMA issuer
+    if (leader) {
+      const uint32_t acce0 = smem_addr(&acce_bar[0]);
+      const uint32_t full0 = smem_addr(&full_bar[0]);
+      const uint64_t wdesc0 = make_smem_desc(smem_addr(smem + C::OFF_W), C::kWideMn ? 8192 : 16,
+                                             1024, kDescSwizzle128B);
+      const uint64_t cdesc0 = make_smem_desc(smem_addr(smem + C::OFF_C), C::kColMn ? 8192 : 16,
+                                             1024, kDescSwizzle128B);
+      // One K16 step: 32 bytes of a K-major row, 16 rows of an MN-major box.
+      constexpr uint32_t kStepW = C::kWideMn ? 128 : 2;
+      constexpr uint32_t kStepC = C::kColMn ? 128 : 2;
+      int stage = 0;
+      uint32_t phase = 0;
+      int acc = 0;
+      uint32_t acc_phase = 0;
+      uint32_t fix_parity = 0;      // parity of each stage's next fix
+      int ok = 1;
+      bool ready = false;
+      auto wait_fix = [&]() -> bool {
+        const uint32_t par = (fix_parity >> stage) & 1u;
+        fix_parity ^= 1u << stage;
+        const uint32_t a = smem_addr(&fix_bar[stage]);
+        if (mbar_try_wait_cluster(a, par)) return true;
+        if (!mbar_wait(&fix_bar[stage], par, guard, kSiteGrFix)) return false;
+        return mbar_try_wait_cluster(a, par);
+      };
+      for (int u = unit; u < num_items && ok; u += num_units) {
+        walk.find(p, lane, u / S, u % S, S, w);
+        const uint32_t idesc =
+            idesc_bf16_f32_major(128 * C::kCtaGroup, w.ncols, C::kWideMn, C::kColMn);
+        const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(acc * C::kTileN);
+        const bool any = w.nk > 0;    // an empty contraction takes no accumulator
+        if (any && lane == 0) {
+          if (!mbar_try_wait(acce0 + 8u * acc, acc_phase ^ 1u) &&
+              !mbar_wait(&acce_bar[acc], acc_phase ^ 1u, guard, kSiteGrAccEmpty))
+            ok = 0;
+          tc_fence_after_sync();
+          for (int j = 0, kb = w.k0; ok && j < w.nk; ++j, kb += w.ks) {
+            if (!ready && !mbar_try_wait(full0 + 8u * stage, phase) &&
+                !mbar_wait(&full_bar[stage], phase, guard, kSiteGrFull)) {
+              ok = 0;
+              break;
+            }
+            int issues = 4;
+            if constexpr (C::kColMn) {
+              const int left = w.len - kb * 64;
+              if (left < 64) {
+                issues = (left + 15) / 16;
+                if (!wait_fix()) {
+                  ok = 0;
+                  break;
+                }
+              }
+            }
+            tc_fence_after_sync();
+            const int ns = stage + 1 == C::kStages ? 0 : stage + 1;
+            const uint32_t nph = stage + 1 == C::kStages ? phase ^ 1u : phase;
+            const uint64_t wd = wdesc0 + static_cast<uint64_t>(stage * (C::W_BYTES >> 4));
+            const uint64_t cd = cdesc0 + static_cast<uint64_t>(stage * (C::C_BYTES >> 4));
+            if (!C::kColMn || issues == 4) {
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                mma_bf16<C::kCtaGroup>(d_tmem, wd + kStepW * k, cd + kStepC * k, idesc,
+                                       (j != 0 || k != 0));
+                if (k == 0) ready = mbar_try_wait(full0 + 8u * ns, nph);
+              }
+            } else {
+              for (int k = 0; k < issues; ++k)
+                mma_bf16<C::kCtaGroup>(d_tmem, wd + kStepW * k, cd + kStepC * k, idesc,
+                                       (j != 0 || k != 0));
+              ready = mbar_try_wait(full0 + 8u * ns, nph);
+            }
+            if constexpr (C::kCtaGroup == 1)
+              mma_commit(&empty_bar[stage]);
+            else
+              mma_commit_pair(&empty_bar[stage], static_cast<uint16_t>(3u));
+            stage = ns;
+            phase = nph;
+          }
+        }
+        ok = __shfl_sync(0xFFFFFFFFu, ok, 0);
+        if constexpr (C::kExt) {
+          uint32_t ids[C::kTileN / 32];
+          load_tile_ids<C>(p, w, lane, ids);
+          const int per = (p.rank + 63) / 64 * 64;
+          for (int id = next_adapter(ids, -1, p.adapters); id >= 0 && ok;
+               id = next_adapter(ids, id, p.adapters)) {
+            if (lane == 0) {
+              for (int r = 0; r < 2 * per; r += 64) {
+                if (!ready && !mbar_try_wait(full0 + 8u * stage, phase) &&
+                    !mbar_wait(&full_bar[stage], phase, guard, kSiteGrFull)) {
+                  ok = 0;
+                  break;
+                }
+                if (!wait_fix()) {
+                  ok = 0;
+                  break;
+                }
+                tc_fence_after_sync();
+                const uint64_t wd = wdesc0 + static_cast<uint64_t>(stage * (C::W_BYTES >> 4));
+                const uint64_t cd = cdesc0 + static_cast<uint64_t>(stage * (C::C_BYTES >> 4));
+                const int left = p.rank - (r < per ? r : r - per);
+                const int issues = left >= 64 ? 4 : (left + 15) / 16;
+                for (int k = 0; k < issues; ++k)
+                  mma_bf16<C::kCtaGroup>(d_tmem, wd + 2 * k, cd + 2 * k, idesc, 1u);
+                mma_commit_pair(&empty_bar[stage], static_cast<uint16_t>(3u));
+                if (++stage == C::kStages) {
+                  stage = 0;
+                  phase ^= 1u;
+                }
+                ready = false;
+              }
+            }
+            ok = __shfl_sync(0xFFFFFFFFu, ok, 0);
+          }
+        }
+        if (any && ok) {
+          if (lane == 0) {
+            if constexpr (C::kCtaGroup == 1)
+              mma_commit(&accf_bar[acc]);
+            else
+              mma_commit_pair(&accf_bar[acc], static_cast<uint16_t>(3u));
+          }
+          if (++acc == C::kAccBufs) {
+            acc = 0;
+            acc_phase ^= 1u;
+          }
+        }
+      }
+      if (lane == 0 && (!ok || *abort_flag)) {
+        if constexpr (C::kCtaGroup == 1)
+          mma_commit(drain_bar);
+        else
+          mma_commit_pair(drain_bar, static_cast<uint16_t>(1u));
+        mbar_wait_drain(drain_bar, 0, p.timeout_ns);
+      }
+    }
+  } else if (warp >= C::kFixWarp0) {
+    // ------------------------------------------------------------ fixing warps
+    if constexpr (C::kFixWarps > 0) {
+      const int fw = warp - C::kFixWarp0;
+      const uint32_t fix0 = map_to_cta(smem_addr(&fix_bar[0]), 0u);
+      const uint32_t sW = smem_addr(smem + C::OFF_W);
+      const uint32_t sC = smem_addr(smem + C::OFF_C);
+      uint32_t pos = 0;            // ring slots used so far
+      uint32_t tail_use = 0;       // parity of each stage's next tail
+      int ok = 1;
+      for (int u = unit; u < num_items && ok; u += num_units) {
+        walk.find(p, lane, u / S, u % S, S, w);
+        if constexpr (C::kMode == kGroupedWgrad) {
+          const int rest = w.len & 63;
+          if (rest != 0) {
+            const int stage = static_cast<int>((pos + w.nk - 1) % C::kStages);
+            const uint32_t par = (tail_use >> stage) & 1u;
+            tail_use ^= 1u << stage;
+            if (lane == 0)
+              ok = mbar_try_wait(smem_addr(&tail_bar[stage]), par) ||
+                   mbar_wait(&tail_bar[stage], par, guard, kSiteGrFixIn);
+            ok = __shfl_sync(0xFFFFFFFFu, ok, 0);
+            if (!ok) break;
+            // Rows rest .. next multiple of 16 of each 64 x 64 box: one
+            // contiguous piece (the swizzle permutes within a row).
+            const int pieces = (((rest + 15) & ~15) - rest) * 8;
+            const int cboxes = w.ncols / C::kCtaGroup / 64;
+            for (int b = 0; b < 2 + cboxes; ++b) {
+              const uint32_t a = (b < 2 ? sW + stage * C::W_BYTES + b * 8192
+                                        : sC + stage * C::C_BYTES + (b - 2) * 8192) +
+                                 static_cast<uint32_t>(rest) * 128u;
+              for (int i = lane; i < pieces; i += 32) st_shared_v4(a + 16 * i, 0u, 0u, 0u, 0u);
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_cluster(fix0 + 8u * stage);
+          }
+          pos += w.nk;
+        } else {
+          pos += w.nk;
+          uint32_t ids[C::kTileN / 32];
+          load_tile_ids<C>(p, w, lane, ids);
+          const int per = (p.rank + 63) / 64 * 64;
+          const int crows = w.ncols / C::kCtaGroup;
+          const int r0 = static_cast<int>(rank) * crows;   // this CTA's rows of the tile
+          for (int id = next_adapter(ids, -1, p.adapters); id >= 0 && ok;
+               id = next_adapter(ids, id, p.adapters)) {
+            for (int r = 0; r < 2 * per; r += 64, ++pos) {
+              const int stage = static_cast<int>(pos % C::kStages);
+              const uint32_t phase = (pos / C::kStages) & 1u;
+              if (lane == 0)
+                ok = mbar_try_wait(smem_addr(&empty_bar[stage]), phase ^ 1u) ||
+                     mbar_wait(&empty_bar[stage], phase ^ 1u, guard, kSiteGrFixIn);
+              ok = __shfl_sync(0xFFFFFFFFu, ok, 0);
+              if (!ok) break;
+              const int c0 = r < per ? r : r - per;
+              const uint16_t* h = r < per ? p.h_hi : p.h_lo;
+              const int cw = min(64, p.rank - c0);   // columns of this stage (rest: zeros)
+              // 16-byte piece q of row i: lanes take 4 rows x 8 pieces at a time.
+              const int q = lane & 7;
+              for (int i0 = fw * 4; i0 < crows; i0 += 4 * C::kFixWarps) {
+                const int i = i0 + (lane >> 3);
+                const int row = r0 + i;              // row of the tile
+                uint4 v = make_uint4(0u, 0u, 0u, 0u);
+                if (row < w.rows && p.ids[w.row0 + row] == id && 8 * q < cw)
+                  v = *reinterpret_cast<const uint4*>(
+                      h + static_cast<int64_t>(w.row0 + row) * p.rank + c0 + 8 * q);
+                st_shared_v4(sC + stage * C::C_BYTES + 128 * i +
+                                 ((static_cast<uint32_t>(q) ^ (static_cast<uint32_t>(i) & 7u)) << 4),
+                             v.x, v.y, v.z, v.w);
+              }
+              fence_proxy_async_smem();
+              __syncwarp();
+              if (lane == 0) mbar_arrive_cluster(fix0 + 8u * stage);
+            }
+          }
+        }
+      }
+    }
+  } else {
+    // ------------------------------------------------------------ epilogue
+    const int slab = warp & 3;                 // TMEM lanes 32 * slab ..
+    const int half = (warp - 2) >> 2;          // chunks half, half + 2, ...
+    if constexpr (!C::kColMn)
+      grouped_zero_rows<C>(p, first_row, end_row,
+                           static_cast<int>(blockIdx.x) * C::kEpiWarps + warp - 2,
+                           static_cast<int>(gridDim.x) * C::kEpiWarps, lane);
+    int acc = 0;
+    uint32_t acc_phase = 0;
+    uint32_t acce_dst = smem_addr(&acce_bar[0]);
+    if constexpr (C::kCtaGroup == 2) acce_dst = map_to_cta(acce_dst, 0u);
+    for (int u = unit; u < num_items; u += num_units) {
+      walk.find(p, lane, u / S, u % S, S, w);
+      const bool any = w.nk > 0;
+      if (any) {
+        int got = 1;
+        if (C::kSplit && S > 1) {
+          // The warps of a split tile meet at named barriers below, so one
+          // thread decides for all of them whether the accumulator arrived.
+          if (warp == 2 && lane == 0)
+            *go = mbar_wait(&accf_bar[acc], acc_phase, guard, kSiteGrAccFull) ? 1 : 0;
+          named_bar_sync(1, 32 * C::kEpiWarps);
+          got = *go;
+        } else {
+          if (lane == 0) got = mbar_wait(&accf_bar[acc], acc_phase, guard, kSiteGrAccFull) ? 1 : 0;
+          got = __shfl_sync(0xFFFFFFFFu, got, 0);
+        }
+        if (!got) break;
+        tc_fence_after_sync();
+      }
+      const int x = w.wide0 + static_cast<int>(rank) * 128 + slab * 32 + lane;
+      const float b = epi_uses_bias(p.epi.op) && x < p.wide
+                          ? p.epi.bias[static_cast<int64_t>(w.g) * p.wide + x]
+                          : 0.0f;
+      const int64_t d0 = C::kColMn ? static_cast<int64_t>(w.g) * p.group_stride_d : 0;
+      const int end = w.row0 + w.rows;
+      const int chunks = (w.rows + 31) / 32;
+      const uint32_t t_row = tmem_base + (static_cast<uint32_t>(slab * 32) << 16) +
+                             static_cast<uint32_t>(acc * C::kTileN);
+      auto hand_back = [&]() {
+        tc_fence_before_sync();
+        __syncwarp();
+        if (lane == 0) {
+          if constexpr (C::kCtaGroup == 1)
+            mbar_arrive_relaxed(&acce_bar[acc]);
+          else
+            mbar_arrive_relaxed_cluster(acce_dst + 8u * static_cast<uint32_t>(acc));
+        }
+      };
+      bool handed = false;
+      for (int ch = half; ch < chunks; ch += 2) {
+        uint32_t raw[32];
+        if (any) {
+          tmem_ld_32x32b_x32(t_row + 32 * ch, raw);
+          tmem_ld_wait();
+          if (ch + 2 >= chunks) {
+            hand_back();
+            handed = true;
+          }
+        }
+        float v[32];
+#pragma unroll
+        for (int i = 0; i < 32; ++i) v[i] = any ? __uint_as_float(raw[i]) : 0.0f;
+        const int row = w.row0 + 32 * ch;
+        if constexpr (C::kMode == kAdapter && C::kSplit)
+          add_adapter_terms<C>(p, w, row, end, x, S, v);
+        if (C::kSplit && S > 1) {
+          float* dst = p.partials +
+                       (static_cast<int64_t>(w.tile) * S + w.piece) * (C::kTileN * 128) +
+                       32 * ch * 128 + slab * 32 + lane;
+#pragma unroll
+          for (int i = 0; i < 32; ++i)
+            if (row + i < end) __stcg(dst + i * 128, v[i]);
+        } else {
+          grouped_epilogue(p.epi, b, v);
+          grouped_store<C>(p, d0, row, end, x, v);
+        }
+      }
+      if (any && !handed) hand_back();
+      if constexpr (C::kSplit) {
+        if (S > 1) {
+          __threadfence();
+          named_bar_sync(1, 32 * C::kEpiWarps);
+          if (warp == 2 && lane == 0) {
+            const uint32_t prev = arrive_counter_gpu(p.counters + w.tile);
+            const int last = prev == static_cast<uint32_t>(S - 1);
+            if (last) p.counters[w.tile] = 0u;
+            *join = last;
+          }
+          named_bar_sync(1, 32 * C::kEpiWarps);
+          if (*join) {
+            __threadfence();
+            for (int ch = half; ch < chunks; ch += 2) {
+              const int row = w.row0 + 32 * ch;
+              const float* src = p.partials + static_cast<int64_t>(w.tile) * S * (C::kTileN * 128) +
+                                 32 * ch * 128 + slab * 32 + lane;
+              float v[32];
+#pragma unroll
+              for (int i = 0; i < 32; ++i) v[i] = row + i < end ? __ldcg(src + i * 128) : 0.0f;
+              for (int q = 1; q < S; ++q) {
+                src += C::kTileN * 128;
+#pragma unroll
+                for (int i = 0; i < 32; ++i)
+                  if (row + i < end) v[i] += __ldcg(src + i * 128);
+              }
+              grouped_epilogue(p.epi, b, v);
+              grouped_store<C>(p, d0, row, end, x, v);
+            }
+          }
+        }
+      }
+      if (any && ++acc == C::kAccBufs) {
+        acc = 0;
+        acc_phase ^= 1u;
+      }
+    }
+  }
+
+  tc_fence_before_sync();
+  __syncthreads();
+  if constexpr (C::kCtaGroup == 2) cluster_sync();
+  if (warp == 1) {
+    tc_fence_after_sync();
+    tmem_dealloc<C::kCtaGroup>(tmem_base, C::TMEM_COLS);
+  }
+}
+
+}  // namespace tg

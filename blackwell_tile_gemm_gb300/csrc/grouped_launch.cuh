@@ -1,0 +1,127 @@
+// Host launch of gemm_grouped_kernel<Cfg>: tensor maps, grid, cluster
+// attribute and shared memory opt-in (once per device and configuration).
+#pragma once
+
+#include "gemm_launch.cuh"
+#include "grouped_kernel.cuh"
+
+namespace tg {
+
+// The two streamed operands.  `wide` spans D's contiguous axis: the weights
+// [slices][rows][...] (forward, dgrad, adapters) or A [rows of all groups]
+// (wgrad).  `cols` spans its rows.  k: extent of the contraction index.
+struct GroupedOperands {
+  const void* wide;
+  int64_t wide_ld, wide_rows, wide_slices, wide_slice_stride;
+  const void* cols;
+  int64_t cols_ld;
+  int64_t k;
+  const void* up;        // adapters: [adapters][wide][rank]
+  int64_t up_ld, up_slice_stride, up_slices, up_rank;
+};
+
+inline GroupedArgs grouped_args(DeviceCtx* ctx) {
+  GroupedArgs a{};
+  a.status = ctx->status;
+  a.timeout_ns = wait_timeout_ns();
+  a.groups = 1;
+  a.epi = Epi{kEpiNone, 0.0f, 0.0f, nullptr};
+  return a;
+}
+
+// Few rows per group: single CTAs with 64-column tiles, a deep ring of weight
+// boxes and a split contraction; else CTA pairs with tiles of 256 x 256.
+inline bool grouped_few_rows(int64_t M, int64_t groups) { return M <= 48 * groups; }
+
+template <class C>
+int launch_grouped(const GroupedOperands& operands, const GroupedArgs& args, cudaStream_t stream,
+                   DeviceCtx* ctx) {
+  GroupedOperands o = operands;
+  if (o.k == 0) {
+    // Nothing is read (the caller may have passed null operands): any valid
+    // map does.
+    o.wide = o.cols = args.D;
+    o.wide_ld = o.cols_ld = o.wide_slice_stride = 8;
+    o.wide_rows = o.wide_slices = 1;
+  }
+  static std::atomic<int> prepared[64];
+  auto kern = gemm_grouped_kernel<C>;
+  std::atomic<int>& slot = prepared[ctx->device];
+  int units = slot.load(std::memory_order_acquire);
+  cudaLaunchConfig_t cfg{};
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = C::kCtaGroup;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.blockDim = dim3(C::kThreads, 1, 1);
+  cfg.dynamicSmemBytes = C::SMEM_BYTES;
+  cfg.attrs = attr;
+  if (units == 0) {
+    cudaError_t e =
+        cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_BYTES);
+    if (e != cudaSuccess) return cuda_fail(e);
+    units = ctx->num_sms / C::kCtaGroup;
+    if constexpr (C::kCtaGroup == 2) {
+      cfg.gridDim = dim3(static_cast<unsigned>(2 * units), 1, 1);
+      cudaLaunchConfig_t q = cfg;
+      q.attrs = attr + 1;
+      q.numAttrs = 1;
+      int clusters = 0;
+      e = cudaOccupancyMaxActiveClusters(&clusters, kern, &q);
+      if (e != cudaSuccess) return cuda_fail(e);
+      if (clusters > 0 && clusters < units) units = clusters;
+    }
+    if (units < 1) units = 1;
+    slot.store(units, std::memory_order_release);
+  }
+  GroupedArgs a = args;
+  a.num_wide_tiles = ceil_div_i(a.wide, 128 * C::kCtaGroup);
+  if constexpr (C::kSplit) {
+    // The tail split's scratch: [tile][piece] partial tiles, one counter a tile.
+    float* part = nullptr;
+    uint32_t* counters = nullptr;
+    if (tail_scratch(stream, &part, &counters)) {
+      a.partials = part;
+      a.counters = counters;
+      a.max_slots = static_cast<int>(kTailPartialBytes / (C::kTileN * 128 * 4));
+      a.max_counters = kTailFlagWords;
+    }
+  }
+  const CUtensorMapDataType bf = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+  const CUtensorMapSwizzle sw = CU_TENSOR_MAP_SWIZZLE_128B;
+  CUtensorMap tW, tC, tCs, tUp;
+  int rc;
+  if constexpr (C::kMode == kGroupedWgrad) {
+    rc = make_tensor_map_2d(&tW, bf, o.wide, a.wide, o.wide_rows, o.wide_ld * 2, 64, 64, sw);
+    if (rc != TG_OK) return rc;
+    rc = make_tensor_map_2d(&tC, bf, o.cols, a.cols, o.wide_rows, o.cols_ld * 2, 64, 64, sw);
+    if (rc != TG_OK) return rc;
+    tCs = tC;
+  } else {
+    // Weights: the contraction index contiguous (boxes of 128 rows), or for
+    // dgrad the wide axis (boxes of 64 x 64).
+    rc = make_tensor_map_3d(&tW, bf, o.wide, C::kWideMn ? a.wide : o.k, o.wide_rows, o.wide_slices,
+                            o.wide_ld * 2, o.wide_slice_stride * 2, 64, C::kWideMn ? 64 : 128, sw);
+    if (rc != TG_OK) return rc;
+    rc = make_tensor_map_2d(&tC, bf, o.cols, o.k, a.M, o.cols_ld * 2, 64, C::C_ROWS, sw);
+    if (rc != TG_OK) return rc;
+    rc = make_tensor_map_2d(&tCs, bf, o.cols, o.k, a.M, o.cols_ld * 2, 64, 16, sw);
+    if (rc != TG_OK) return rc;
+  }
+  tUp = tW;
+  if (C::kExt && o.up != nullptr) {
+    rc = make_tensor_map_3d(&tUp, bf, o.up, o.up_rank, a.wide, o.up_slices, o.up_ld * 2,
+                            o.up_slice_stride * 2, 64, 128, sw);
+    if (rc != TG_OK) return rc;
+  }
+  cfg.gridDim = dim3(static_cast<unsigned>(units * C::kCtaGroup), 1, 1);
+  cfg.stream = stream;
+  cfg.numAttrs = C::kCtaGroup == 2 ? 2 : 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, tW, tC, tCs, tUp, a);
+  return e == cudaSuccess ? TG_OK : cuda_fail(e);
+}
+
+}  // namespace tg

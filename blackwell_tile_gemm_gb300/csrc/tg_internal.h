@@ -46,6 +46,13 @@ int make_tensor_map_2d(CUtensorMap* map, CUtensorMapDataType dtype, const void* 
                        uint64_t inner, uint64_t outer, uint64_t row_bytes, uint32_t box_inner,
                        uint32_t box_outer, CUtensorMapSwizzle swizzle);
 
+// 3-D tiled tensor map over `slices` such arrays, `slice_bytes` apart (a
+// multiple of 16); the box covers one slice.
+int make_tensor_map_3d(CUtensorMap* map, CUtensorMapDataType dtype, const void* base,
+                       uint64_t inner, uint64_t outer, uint64_t slices, uint64_t row_bytes,
+                       uint64_t slice_bytes, uint32_t box_inner, uint32_t box_outer,
+                       CUtensorMapSwizzle swizzle);
+
 // Library-owned device workspace for (current device, `stream`), at least
 // `bytes` long.  Without a reservation it is grown on demand (growing
 // synchronises the stream first); a reserved workspace never grows.  When it
@@ -165,6 +172,10 @@ int launch_gemm_bf16_pregather_impl(const void* A, int64_t lda, int a_rows, cons
                                     int N, int K, int d_dtype, const Epi& epi, bool pair,
                                     void* workspace, cudaStream_t stream, DeviceCtx* ctx);
 size_t gather_workspace_bytes(int64_t M, int64_t K);
+// The gathered copy alone: rows [M, K] of A in the stream's workspace.
+int gather_to_workspace(const void* A, int64_t lda, int a_rows, const int* row_idx, int64_t M,
+                        int64_t K, const void** rows, int64_t* ld, cudaStream_t stream,
+                        DeviceCtx* ctx);
 
 // Skinny bf16 GEMM (M <= 128): split-K pieces reduce into an f32 target.
 // `workspace` (f32, skinny_workspace_bytes) is used for bf16 D only.

@@ -275,6 +275,66 @@ int gemm_bf16_gather(const void* A, int64_t lda, int64_t a_rows, const int32_t* 
                      int64_t K, int d_dtype, const tg_epilogue* epi, unsigned flags,
                      void* cuda_stream);
 
+/*
+ * Products whose weights change with the row.
+ *
+ * Group g of `groups` (1 .. TG_MAX_GROUPS) owns the rows offsets[g] <= i <
+ * offsets[g+1] of a matrix of M rows.  The offsets stay on the device (int32
+ * [groups + 1]): the host never learns the sizes, so a call is capturable and
+ * never synchronises.  They should not decrease and lie in [0, M]; groups may
+ * be empty.  Rows before offsets[0] and from offsets[groups] on belong to no
+ * group.  Offsets that break the rule are clamped to [0, M] and to the
+ * running maximum (nothing out of range is touched) and the first such call
+ * is reported by tg_device_status as TG_ERR_INVALID_ARG with site 40.
+ * tg_group_rows makes the offsets from a group id per row.
+ *
+ * All three are bf16 with f32 accumulation.  B is [groups][N][K] with row
+ * stride ldb and group stride group_stride_b (elements, a multiple of 8; not
+ * read for one group).  A contraction is summed in an order fixed by the
+ * sizes and offsets: the same call returns the same bits.  flags: 0.
+ */
+enum { TG_MAX_GROUPS = 4096 };
+
+/*
+ * gemm_bf16_grouped -- D[i, :] = epi(A[r(i), :] * B[g]^T) for the rows i of
+ * group g, with r(i) = row_idx[i], or i where row_idx is NULL.
+ *   A       : device, bf16 [a_rows, K], row stride lda.
+ *   row_idx : device, int32 [M], or NULL (then a_rows >= M).  An index outside
+ *             [0, a_rows) gives a zero row (D = epi(0)).  The rows are
+ *             gathered into the stream's workspace first (TG_CALL_GEMM_BF16_GATHER).
+ *   D       : device, [M, N] f32 or bf16.  Rows in no group are set to zero.
+ *   epi     : as for gemm_bf16_ex, except that bias is [groups][N] (contiguous).
+ */
+int gemm_bf16_grouped(const void* A, int64_t lda, int64_t a_rows, const int32_t* row_idx,
+                      const int32_t* offsets, int64_t groups, int64_t M, const void* B,
+                      int64_t ldb, int64_t group_stride_b, void* D, int64_t ldd, int64_t N,
+                      int64_t K, int d_dtype, const tg_epilogue* epi, unsigned flags,
+                      void* cuda_stream);
+
+/*
+ * gemm_bf16_grouped_dgrad -- the gradient of the rows: D[i, :] = G[i, :] *
+ * B[g] for the rows i of group g (contraction over N; B is read as it is).
+ *   G : device, bf16 [M, N], row stride ldg (the gradient of the product).
+ *   D : device, [M, K] f32 or bf16.  Rows in no group are set to zero.
+ */
+int gemm_bf16_grouped_dgrad(const void* G, int64_t ldg, const int32_t* offsets, int64_t groups,
+                            int64_t M, const void* B, int64_t ldb, int64_t group_stride_b,
+                            void* D, int64_t ldd, int64_t N, int64_t K, int d_dtype,
+                            unsigned flags, void* cuda_stream);
+
+/*
+ * gemm_bf16_grouped_wgrad -- the gradient of the weights: D[g] = sum over the
+ * rows i of group g of G[i, :]^T * A[r(i), :], zero for an empty group.
+ *   G, A, a_rows, row_idx : as above (G is [M, N]).
+ *   D : device, [groups][N][K] f32 or bf16, row stride ldd, group stride
+ *       group_stride_d (elements; rows of different groups must not overlap).
+ */
+int gemm_bf16_grouped_wgrad(const void* G, int64_t ldg, const void* A, int64_t lda,
+                            int64_t a_rows, const int32_t* row_idx, const int32_t* offsets,
+                            int64_t groups, int64_t M, void* D, int64_t ldd,
+                            int64_t group_stride_d, int64_t N, int64_t K, int d_dtype,
+                            unsigned flags, void* cuda_stream);
+
 /* tg_gemm_tail_split -- the number of K pieces (1: none) into which
  * gemm_bf16 cuts each tile for this shape on the current device (flags: 0 or
  * TG_FLAG_CTA_PAIR), for operands in the current device's memory (a stream
