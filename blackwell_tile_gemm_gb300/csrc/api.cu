@@ -116,22 +116,24 @@ namespace {
 // these fields, so a hit returns exactly what a fresh encode would.  Bounded
 // (cleared when full); keeps repeated calls on the same buffers off the
 // driver's encoder.
-// slices == 0: a 2-D map; otherwise the third extent and its byte stride.
+// chunks != 0: a 4-D map of 64-element column chunks; else slices != 0: a 3-D
+// map; else 2-D.
 struct MapKey {
   uint64_t base, inner, outer, row_bytes;
   uint32_t dtype, box_inner, box_outer, swizzle;
-  uint64_t slices, slice_bytes;
+  uint64_t slices, slice_bytes, chunks;
   bool operator==(const MapKey& o) const {
     return base == o.base && inner == o.inner && outer == o.outer && row_bytes == o.row_bytes &&
            dtype == o.dtype && box_inner == o.box_inner && box_outer == o.box_outer &&
-           swizzle == o.swizzle && slices == o.slices && slice_bytes == o.slice_bytes;
+           swizzle == o.swizzle && slices == o.slices && slice_bytes == o.slice_bytes &&
+           chunks == o.chunks;
   }
 };
 struct MapKeyHash {
   size_t operator()(const MapKey& k) const {
     uint64_t h = 1469598103934665603ull;
-    const uint64_t v[10] = {k.base, k.inner, k.outer, k.row_bytes, k.dtype, k.box_inner,
-                            k.box_outer, k.swizzle, k.slices, k.slice_bytes};
+    const uint64_t v[11] = {k.base,      k.inner,   k.outer,  k.row_bytes,   k.dtype, k.box_inner,
+                            k.box_outer, k.swizzle, k.slices, k.slice_bytes, k.chunks};
     for (uint64_t x : v) h = (h ^ x) * 1099511628211ull;
     return static_cast<size_t>(h);
   }
@@ -145,14 +147,14 @@ namespace {
 int make_tensor_map(CUtensorMap* map, CUtensorMapDataType dtype, const void* base,
                     uint64_t inner, uint64_t outer, uint64_t row_bytes, uint32_t box_inner,
                     uint32_t box_outer, CUtensorMapSwizzle swizzle, uint64_t slices,
-                    uint64_t slice_bytes) {
+                    uint64_t slice_bytes, uint64_t chunks = 0) {
   // A zero extent is not encodable; callers never launch for empty problems,
   // but keep a valid map (extent 1) for unused descriptor parameters.
   if (inner == 0) inner = 1;
   if (outer == 0) outer = 1;
   const MapKey key{reinterpret_cast<uint64_t>(base), inner, outer, row_bytes,
                    static_cast<uint32_t>(dtype), box_inner, box_outer,
-                   static_cast<uint32_t>(swizzle), slices, slice_bytes};
+                   static_cast<uint32_t>(swizzle), slices, slice_bytes, chunks};
   {
     std::lock_guard<std::mutex> lk(g_map_mutex);
     auto it = g_map_cache.find(key);
@@ -174,11 +176,20 @@ int make_tensor_map(CUtensorMap* map, CUtensorMapDataType dtype, const void* bas
       g_encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
     }
   }
-  cuuint64_t dims[3] = {inner, outer, slices};
-  cuuint64_t strides[2] = {row_bytes, slice_bytes};
-  cuuint32_t box[3] = {box_inner, box_outer, 1};
-  cuuint32_t estr[3] = {1, 1, 1};
-  CUresult r = g_encode(map, dtype, slices ? 3 : 2, const_cast<void*>(base), dims, strides, box, estr,
+  cuuint64_t dims[4] = {inner, outer, slices, 1};
+  cuuint64_t strides[3] = {row_bytes, slice_bytes, slice_bytes};
+  cuuint32_t box[4] = {box_inner, box_outer, 1, 1};
+  cuuint32_t estr[4] = {1, 1, 1, 1};
+  cuuint32_t rank = slices ? 3 : 2;
+  if (chunks) {
+    // [slice][chunk][row][64 elements]: chunks of a row are 128 bytes apart.
+    dims[2] = chunks;
+    dims[3] = slices;
+    strides[1] = 128;
+    box[2] = 2;
+    rank = 4;
+  }
+  CUresult r = g_encode(map, dtype, rank, const_cast<void*>(base), dims, strides, box, estr,
                         CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   if (r != CUDA_SUCCESS) return cuda_fail(cudaErrorInvalidValue);
@@ -202,6 +213,12 @@ int make_tensor_map_3d(CUtensorMap* map, CUtensorMapDataType dtype, const void* 
                        CUtensorMapSwizzle swizzle) {
   return make_tensor_map(map, dtype, base, inner, outer, row_bytes, box_inner, box_outer, swizzle,
                          slices ? slices : 1, slice_bytes);
+}
+
+int make_tensor_map_chunks(CUtensorMap* map, const void* base, uint64_t width, uint64_t rows,
+                           uint64_t slices, uint64_t row_bytes, uint64_t slice_bytes) {
+  return make_tensor_map(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, base, 64, rows, row_bytes, 64, 64,
+                         CU_TENSOR_MAP_SWIZZLE_128B, slices ? slices : 1, slice_bytes, width / 64);
 }
 
 namespace {

@@ -95,8 +95,8 @@ int gemm_bf16_grouped(const void* A, int64_t lda, int64_t a_rows, const int32_t*
   if (grouped_few_rows(M, groups))
     return bf16 ? launch_grouped<GroupedCfg<kGroupedForward, 1, 64, 9, true>>(o, a, stream, ctx)
                 : launch_grouped<GroupedCfg<kGroupedForward, 1, 64, 9, false>>(o, a, stream, ctx);
-  return bf16 ? launch_grouped<GroupedCfg<kGroupedForward, 2, 256, 7, true>>(o, a, stream, ctx)
-              : launch_grouped<GroupedCfg<kGroupedForward, 2, 256, 7, false>>(o, a, stream, ctx);
+  return bf16 ? launch_grouped<GroupedCfg<kGroupedForward, 2, 256, 6, true>>(o, a, stream, ctx)
+              : launch_grouped<GroupedCfg<kGroupedForward, 2, 256, 6, false>>(o, a, stream, ctx);
 }
 
 int gemm_bf16_grouped_dgrad(const void* G, int64_t ldg, const int32_t* offsets, int64_t groups,
@@ -136,8 +136,8 @@ int gemm_bf16_grouped_dgrad(const void* G, int64_t ldg, const int32_t* offsets, 
   o.cols_ld = ldg;
   o.k = N;
   return d_dtype == TG_D_BF16
-             ? launch_grouped<GroupedCfg<kGroupedDgrad, 2, 256, 7, true>>(o, a, stream, ctx)
-             : launch_grouped<GroupedCfg<kGroupedDgrad, 2, 256, 7, false>>(o, a, stream, ctx);
+             ? launch_grouped<GroupedCfg<kGroupedDgrad, 2, 256, 6, true>>(o, a, stream, ctx)
+             : launch_grouped<GroupedCfg<kGroupedDgrad, 2, 256, 6, false>>(o, a, stream, ctx);
 }
 
 int gemm_bf16_grouped_wgrad(const void* G, int64_t ldg, const void* A, int64_t lda,
@@ -196,8 +196,8 @@ int gemm_bf16_grouped_wgrad(const void* G, int64_t ldg, const void* A, int64_t l
   o.cols_ld = ldg;
   o.k = M;
   return d_dtype == TG_D_BF16
-             ? launch_grouped<GroupedCfg<kGroupedWgrad, 2, 256, 7, true>>(o, a, stream, ctx)
-             : launch_grouped<GroupedCfg<kGroupedWgrad, 2, 256, 7, false>>(o, a, stream, ctx);
+             ? launch_grouped<GroupedCfg<kGroupedWgrad, 2, 256, 6, true>>(o, a, stream, ctx)
+             : launch_grouped<GroupedCfg<kGroupedWgrad, 2, 256, 6, false>>(o, a, stream, ctx);
 }
 
 }  // extern "C"

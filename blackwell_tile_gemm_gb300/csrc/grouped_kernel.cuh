@@ -47,11 +47,12 @@
 // same bits every time; nobody waits).  There the adapter term needs no MMA:
 // the epilogue adds up[id][n, :] . H[i, :] in f32.
 //
-// Roles: warp 0 TMA producer, warp 1 TMEM allocator and MMA issuer, warps
-// 2..9 epilogue, then kFixWarps fixing warps.  Every wait is bounded.
+// Roles: warp 0 TMA producer, warp 1 TMEM allocator and MMA issuer, warps 2
+// and 3 fixing warps, warps 4..11 epilogue.  Every wait is bounded.
 #pragma once
 
 #include <cstdint>
+#include <type_traits>
 #include <cuda.h>
 
 #include "epilogue.cuh"
@@ -121,23 +122,56 @@ struct GroupedCfg {
   static constexpr int C_BYTES = C_ROWS * 128;
   static constexpr int OFF_W = 0;
   static constexpr int OFF_C = OFF_W + kStages * W_BYTES;
-  static constexpr int OFF_BAR = OFF_C + kStages * C_BYTES;
+  // CTA pairs store D by TMA from staged boxes of 32 rows x 128 bytes (bf16:
+  // two warps fill one box); blocks that cross a group's end or D's right
+  // edge are read back from the box and stored row by row.  wgrad of 64
+  // groups x 2048 x 4096 with 64 rows each, i.e. the writing of 1.07 GB:
+  // 515 us straight from registers (64 bytes a row and instruction), 312 us
+  // with every box read back, 266 us with TMA boxes of 64 bytes.
+  static constexpr bool kStaged = kCtaGroup == 2;
+  static constexpr int OFF_STG = OFF_C + kStages * C_BYTES;
+  static constexpr int OFF_BAR = OFF_STG + (kStaged ? 8 * 4096 : 0);
   static constexpr int kAccBufs = 2;
+  // f32 D: the tensor cores truncate each time they add to an accumulator, so
+  // its error grows with the number of K16 steps (measured 1e-6 of the result
+  // after 1000 terms, 5e-6 after 5000).  Long contractions are therefore cut
+  // into chunks of at most kChunk stages that are added in f32 with rounding
+  // to nearest: each epilogue warp keeps its share of the tile (128 values a
+  // lane) in registers.  (Adding the chunks to D in memory instead cost 80%:
+  // 8192^3 wgrad 1579 us.)  bf16 D rounds at 2e-3 and needs none of it.
+  static constexpr int kChunk = 12;
   static constexpr int NUM_BARS = 2 * kStages + 2 * kAccBufs + 1 + (kFixWarps ? 2 * kStages : 0);
   static constexpr int OFF_MISC = OFF_BAR + NUM_BARS * 8;
-  static constexpr int SMEM_BYTES = OFF_MISC + 16 + 1024;
+  static constexpr int SMEM_BYTES = OFF_MISC + 32 + 1024;
   static constexpr int TMEM_COLS = 2 * kTileN <= 32    ? 32
                                    : 2 * kTileN <= 64  ? 64
                                    : 2 * kTileN <= 128 ? 128
                                    : 2 * kTileN <= 256 ? 256
                                                        : 512;
   static constexpr int kEpiWarps = 8;
-  static constexpr int kFixWarp0 = 2 + kEpiWarps;
-  static constexpr int kThreads = 64 + 32 * (kEpiWarps + kFixWarps);
+  static constexpr int kFixWarp0 = 2;
+  static constexpr int kEpiWarp0 = 4;
+  // The gradients' operands take two loads each (boxes of 64 x 64).
+  static constexpr bool kTwoProducers = kWideMn && kCtaGroup == 2;
+  static constexpr int kColWarp = 3;
+  static_assert(!kTwoProducers || kFixWarps < 2, "warp 3 is free");
+  static constexpr int kThreads = 32 * (kEpiWarp0 + kEpiWarps);
   static_assert(SMEM_BYTES <= 227 * 1024, "shared memory per CTA");
   static_assert(kTileN % 32 == 0 && kTileN <= 256, "MMA N");
   static_assert(C_BYTES % 1024 == 0, "swizzle atoms");
   static_assert(!kColMn || (kCtaGroup == 2 && kTileN == 256), "wgrad tiles");
+};
+
+// Column-operand boxes of 16, 32, ... 128 rows: a stage's rows (a multiple of
+// 16, at most 128 per CTA) come in one load of their exact size.  A stage
+// issues as few loads as it can: with 112 rows as boxes of 64 + 32 + 16 the
+// producer, not the MMAs, set the pace (64 groups of 448 rows x 2048 x 4096:
+// 493 us, against 357 us for 512 rows in single boxes).
+// wgrad: box[0] is the 64 x 64 box of the MN-major operand, box[1] the pair
+// of such boxes in one load.
+constexpr int kColBoxes = 8;
+struct ColumnMaps {
+  CUtensorMap box[kColBoxes];
 };
 
 // One work item.
@@ -283,6 +317,18 @@ struct GroupWalk {
   }
 };
 
+// Chunks of a contraction of nk stages (0 for none), and where chunk c ends.
+template <class C>
+__device__ __forceinline__ int grouped_chunks(int nk) {
+  if constexpr (C::kBf16Out) return nk > 0 ? 1 : 0;
+  return (nk + C::kChunk - 1) / C::kChunk;
+}
+template <class C>
+__device__ __forceinline__ int grouped_chunk_end(int nk, int chunks, int c) {
+  if constexpr (C::kBf16Out) return nk;
+  return static_cast<int>(static_cast<int64_t>(nk) * (c + 1) / chunks);
+}
+
 // Pieces of the contraction per tile: the count (at most 8, each piece at
 // least 4 stages) with the least waves * (stages per piece + 4), the 4 for a
 // unit's start, partial tile and join.
@@ -383,6 +429,107 @@ __device__ __forceinline__ void grouped_store(const GroupedArgs& p, int64_t d0, 
   }
 }
 
+// 32 accumulator columns of this lane's row, into v or added to it.
+template <bool kAdd>
+__device__ __forceinline__ void grouped_read(uint32_t taddr, float (&v)[32]) {
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    uint32_t raw[16];
+    tmem_ld_32x32b_x16(taddr + 16 * h, raw);
+    tmem_ld_wait();
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+      v[16 * h + i] = kAdd ? v[16 * h + i] + __uint_as_float(raw[i]) : __uint_as_float(raw[i]);
+  }
+}
+__device__ __forceinline__ void grouped_zero(float (&v)[32]) {
+#pragma unroll
+  for (int i = 0; i < 32; ++i) v[i] = 0.0f;
+}
+
+// f32: the warp's 32 x 32 block into its staging box, one 128-byte line per
+// row of D.
+__device__ __forceinline__ void grouped_stage_f32(uint32_t stg, int lane, const float (&v)[32]) {
+#pragma unroll
+  for (int j = 0; j < 32; ++j) st_shared_b32(stg + 128 * j + 4 * lane, __float_as_uint(v[j]));
+}
+
+// bf16: the warp's 32 lanes x 32 accumulator columns at `taddr` (or zeros)
+// into its half of a staging box of 32 rows x 128 bytes that it shares with
+// the warp of the neighbouring 32 lanes.  The 16x256b read leaves two
+// neighbouring columns of a lane in one thread, in the fragment layout of
+// stmatrix, whose .trans form writes the transposed 8 x 8 blocks: rows of D.
+// 128B swizzle (16-byte piece c of row r at c ^ (r & 7)) keeps that free of
+// bank conflicts.  b[i]: bias of lane 8 i + (thread / 4).
+__device__ __forceinline__ void grouped_stage_bf16(uint32_t stg, int lane, int slab, uint32_t taddr,
+                                                   bool any, const Epi& e, const float (&b)[4]) {
+  uint32_t v[2][16];
+  if (any) {
+    tmem_ld_16x256b_x4(taddr, v[0]);
+    tmem_ld_16x256b_x4(taddr + (16u << 16), v[1]);
+    tmem_ld_wait();
+  } else {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) v[0][i] = v[1][i] = 0u;
+  }
+  if (e.op != kEpiNone) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      float t[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        t[j] = __uint_as_float(v[i / 2][4 * (j / 2) + 2 * (i & 1) + (j & 1)]);
+      grouped_epilogue(e, b[i], t);
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        v[i / 2][4 * (j / 2) + 2 * (i & 1) + (j & 1)] = __float_as_uint(t[j]);
+    }
+  }
+  const uint32_t r = static_cast<uint32_t>(lane & 7);
+  const uint32_t c = static_cast<uint32_t>(4 * (slab & 1) + (lane >> 3));
+  const uint32_t a = stg + 128 * r + 16 * (c ^ r);
+#pragma unroll
+  for (int g = 0; g < 4; ++g) {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      w[i] = pack_bf16x2(__uint_as_float(v[i / 2][4 * g + 2 * (i & 1)]),
+                         __uint_as_float(v[i / 2][4 * g + 2 * (i & 1) + 1]));
+    stmatrix_x4_trans(a + 1024 * g, w[0], w[1], w[2], w[3]);
+  }
+}
+
+// Rows r0, r0 + step, ... of a staged box to D (element x0 of rows row ..,
+// below `end`): eight lanes write one 128-byte line, four rows at a time.
+template <class C>
+__device__ __forceinline__ void grouped_unstage(const GroupedArgs& p, int64_t d0, uint32_t stg,
+                                                int lane, int r0, int r1, int row, int end,
+                                                int x0) {
+  constexpr int kVec = C::kBf16Out ? 8 : 4;
+  const int x = x0 + kVec * (lane & 7);
+  using T = typename std::conditional<C::kBf16Out, uint16_t, float>::type;
+#pragma unroll 4
+  for (int r = r0 + (lane >> 3); r < r1; r += 4) {
+    if (row + r >= end) break;
+    const int c = C::kBf16Out ? (lane ^ r) & 7 : lane & 7;   // bf16 boxes are swizzled
+    const uint4 q = ld_shared_v4(stg + 128 * r + 16 * c);
+    T* d = reinterpret_cast<T*>(p.D) + d0 + (row + r) * p.ldd + x;
+    if (x + kVec <= p.wide) {
+      __stcs(reinterpret_cast<uint4*>(d), q);
+    } else {
+      const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+      for (int e = 0; e < kVec; ++e)
+        if (x + e < p.wide) {
+          if constexpr (C::kBf16Out)
+            d[e] = static_cast<uint16_t>(w[e / 2] >> (16 * (e & 1)));
+          else
+            d[e] = __uint_as_float(w[e]);
+        }
+    }
+  }
+}
+
 // Rows of D in no group: [0, first) and [end, M) are set to zero, shared out
 // over the epilogue warps of the grid.
 template <class C>
@@ -435,9 +582,10 @@ __device__ __forceinline__ void add_adapter_terms(const GroupedArgs& p, const Gr
 template <class C>
 __global__ void __launch_bounds__(C::kThreads, 1)
     gemm_grouped_kernel(const __grid_constant__ CUtensorMap tmW,
-                        const __grid_constant__ CUtensorMap tmC,
-                        const __grid_constant__ CUtensorMap tmCs,
-                        const __grid_constant__ CUtensorMap tmUp, const GroupedArgs p) {
+                        const __grid_constant__ CUtensorMap tmW2,
+                        const __grid_constant__ ColumnMaps tmC,
+                        const __grid_constant__ CUtensorMap tmUp,
+                        const __grid_constant__ CUtensorMap tmD, const GroupedArgs p) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -452,7 +600,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::OFF_MISC);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::OFF_MISC + 4);
   volatile int* join = reinterpret_cast<volatile int*>(smem + C::OFF_MISC + 8);
-  volatile int* go = reinterpret_cast<volatile int*>(smem + C::OFF_MISC + 12);
+  volatile int* go = reinterpret_cast<volatile int*>(smem + C::OFF_MISC + 16);   // [4]
 
   const int warp = threadIdx.x >> 5;
   const int lane = static_cast<int>(threadIdx.x & 31);
@@ -478,9 +626,10 @@ __global__ void __launch_bounds__(C::kThreads, 1)
   }
   if (warp == 0 && lane == 0) {
     prefetch_tensormap(&tmW);
-    prefetch_tensormap(&tmC);
-    prefetch_tensormap(&tmCs);
+    if constexpr (C::kWideMn) prefetch_tensormap(&tmW2);
+    for (int b = 0; b < kColBoxes; ++b) prefetch_tensormap(&tmC.box[b]);
     if constexpr (C::kExt) prefetch_tensormap(&tmUp);
+    if constexpr (C::kStaged) prefetch_tensormap(&tmD);
   }
   if (warp == 1) {
     tmem_alloc<C::kCtaGroup>(tmem_slot, C::TMEM_COLS);
@@ -504,9 +653,14 @@ __global__ void __launch_bounds__(C::kThreads, 1)
   const int num_items = tiles * S;
   GroupedWork w;
 
-  if (warp == 0) {
-    // ------------------------------------------------------------ producer
-    if (blockIdx.x == 0) {
+  if (warp == 0 || (C::kTwoProducers && warp == C::kColWarp)) {
+    // ------------------------------------------------------------ producers
+    // Warp 0 posts the expected bytes and loads the wide operand; the column
+    // operand is its own or, where a stage takes three or four loads, the
+    // second producer's.
+    const bool do_wide = warp == 0;
+    const bool do_cols = !C::kTwoProducers || warp != 0;
+    if (blockIdx.x == 0 && warp == 0) {
       const bool bad = __any_sync(0xFFFFFFFFu, walk.bad);
       if (bad && lane == 0 && atomicCAS(p.status, 0u, 1u) == 0u) {
         p.status[1] = kSiteGrOffsets;
@@ -542,6 +696,9 @@ __global__ void __launch_bounds__(C::kThreads, 1)
       const int wx = w.wide0 + static_cast<int>(rank) * 128;
       const int crows = w.ncols / C::kCtaGroup;       // column-operand rows of this CTA
       const int crow0 = w.row0 + static_cast<int>(rank) * crows;
+      // MN-major: both of a box pair's 64-element chunks lie inside the row.
+      const bool w_chunks = C::kWideMn && wx + 128 <= p.wide;
+      const bool c_chunks = C::kColMn && crows == 128 && crow0 + 128 <= p.cols;
       if (lane == 0) {
         const uint32_t cbytes = static_cast<uint32_t>(crows) * 128u;
         for (int j = 0, kb = w.k0; j < w.nk; ++j, kb += w.ks) {
@@ -556,13 +713,23 @@ __global__ void __launch_bounds__(C::kThreads, 1)
           if (tail) {
             // Both CTAs' loads of a ragged stage complete locally, for the
             // CTA's own fixing warp.
-            if (leader) mbar_arrive(&full_bar[stage]);
             const uint32_t tb = smem_addr(&tail_bar[stage]);
-            mbar_arrive_expect_tx(&tail_bar[stage], C::W_BYTES + cbytes);
-            for (int c = 0; c < 2; ++c)
-              tma_load_2d(dW + 8192 * c, &tmW, tb, wx + 64 * c, w.base + kx, pol);
-            for (int c = 0; c < crows / 64; ++c)
-              tma_load_2d(dC + 8192 * c, &tmC, tb, crow0 + 64 * c, w.base + kx, pol);
+            if (do_wide) {
+              if (leader) mbar_arrive(&full_bar[stage]);
+              mbar_arrive_expect_tx(&tail_bar[stage], C::W_BYTES + cbytes);
+              if (w_chunks)
+                tma_load_4d(dW, &tmW2, tb, 0, w.base + kx, wx / 64, 0, pol);
+              else
+                for (int c = 0; c < 2; ++c)
+                  tma_load_2d(dW + 8192 * c, &tmW, tb, wx + 64 * c, w.base + kx, pol);
+            }
+            if (do_cols) {
+              if (c_chunks)
+                tma_load_4d(dC, &tmC.box[1], tb, 0, w.base + kx, crow0 / 64, 0, pol);
+              else
+                for (int c = 0; c < crows / 64; ++c)
+                  tma_load_2d(dC + 8192 * c, &tmC.box[0], tb, crow0 + 64 * c, w.base + kx, pol);
+            }
             tail_parity = (tailed >> stage) & 1u ? tail_parity ^ (1u << stage)
                                                  : tail_parity & ~(1u << stage);
             tailed |= 1u << stage;
@@ -570,26 +737,36 @@ __global__ void __launch_bounds__(C::kThreads, 1)
             continue;
           }
           const uint32_t fb = full_dst0 + 8u * stage;
-          if (leader)
+          if (leader && do_wide)
             mbar_arrive_expect_tx(&full_bar[stage], C::kCtaGroup * (C::W_BYTES + cbytes));
           if constexpr (C::kMode == kGroupedWgrad) {
-            for (int c = 0; c < 2; ++c)
-              tma_load_2d_pair(dW + 8192 * c, &tmW, fb, wx + 64 * c, w.base + kx, pol);
-            for (int c = 0; c < crows / 64; ++c)
-              tma_load_2d_pair(dC + 8192 * c, &tmC, fb, crow0 + 64 * c, w.base + kx, pol);
+            if (do_wide) {
+              if (w_chunks)
+                tma_load_4d_pair(dW, &tmW2, fb, 0, w.base + kx, wx / 64, 0, pol);
+              else
+                for (int c = 0; c < 2; ++c)
+                  tma_load_2d_pair(dW + 8192 * c, &tmW, fb, wx + 64 * c, w.base + kx, pol);
+            }
+            if (do_cols) {
+              if (c_chunks)
+                tma_load_4d_pair(dC, &tmC.box[1], fb, 0, w.base + kx, crow0 / 64, 0, pol);
+              else
+                for (int c = 0; c < crows / 64; ++c)
+                  tma_load_2d_pair(dC + 8192 * c, &tmC.box[0], fb, crow0 + 64 * c, w.base + kx,
+                                   pol);
+            }
           } else if constexpr (C::kCtaGroup == 2) {
-            if constexpr (C::kWideMn) {
-              for (int c = 0; c < 2; ++c)
-                tma_load_3d_pair(dW + 8192 * c, &tmW, fb, wx + 64 * c, kx, w.g, pol);
-            } else {
-              tma_load_3d_pair(dW, &tmW, fb, kx, wx, w.g, pol);
+            if (do_wide) {
+              if (C::kWideMn && w_chunks) {
+                tma_load_4d_pair(dW, &tmW2, fb, 0, kx, wx / 64, w.g, pol);
+              } else if constexpr (C::kWideMn) {
+                for (int c = 0; c < 2; ++c)
+                  tma_load_3d_pair(dW + 8192 * c, &tmW, fb, wx + 64 * c, kx, w.g, pol);
+              } else {
+                tma_load_3d_pair(dW, &tmW, fb, kx, wx, w.g, pol);
+              }
             }
-            if (crows == C::C_ROWS) {
-              tma_load_2d_pair(dC, &tmC, fb, kx, crow0, pol);
-            } else {
-              for (int c = 0; c < crows; c += 16)
-                tma_load_2d_pair(dC + 128 * c, &tmCs, fb, kx, crow0 + c, pol);
-            }
+            if (do_cols) tma_load_2d_pair(dC, &tmC.box[crows / 16 - 1], fb, kx, crow0, pol);
           } else {
             if constexpr (C::kWideMn) {
               for (int c = 0; c < 2; ++c)
@@ -597,12 +774,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
             } else {
               tma_load_3d(dW, &tmW, fb, kx, wx, w.g, pol);
             }
-            if (crows == C::C_ROWS) {
-              tma_load_2d(dC, &tmC, fb, kx, crow0, pol);
-            } else {
-              for (int c = 0; c < crows; c += 16)
-                tma_load_2d(dC + 128 * c, &tmCs, fb, kx, crow0 + c, pol);
-            }
+            tma_load_2d(dC, &tmC.box[crows / 16 - 1], fb, kx, crow0, pol);
           }
           next_slot();
         }
@@ -632,7 +804,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
       }
     }
     if (lane == 0) {
-      griddep_launch_dependents();
+      if (do_wide) griddep_launch_dependents();
       if (!ok) {
         for (int s = 0; s < C::kStages; ++s) {
           if (leader && (issued & (1u << s)))
@@ -669,58 +841,77 @@ __global__ void __launch_bounds__(C::kThreads, 1)
         if (!mbar_wait(&fix_bar[stage], par, guard, kSiteGrFix)) return false;
         return mbar_try_wait_cluster(a, par);
       };
+      // The accumulator is complete: the next one follows.
+      auto commit_acc = [&]() {
+        if constexpr (C::kCtaGroup == 1)
+          mma_commit(&accf_bar[acc]);
+        else
+          mma_commit_pair(&accf_bar[acc], static_cast<uint16_t>(3u));
+        if (++acc == C::kAccBufs) {
+          acc = 0;
+          acc_phase ^= 1u;
+        }
+      };
       for (int u = unit; u < num_items && ok; u += num_units) {
         walk.find(p, lane, u / S, u % S, S, w);
         const uint32_t idesc =
             idesc_bf16_f32_major(128 * C::kCtaGroup, w.ncols, C::kWideMn, C::kColMn);
-        const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(acc * C::kTileN);
-        const bool any = w.nk > 0;    // an empty contraction takes no accumulator
-        if (any && lane == 0) {
-          if (!mbar_try_wait(acce0 + 8u * acc, acc_phase ^ 1u) &&
-              !mbar_wait(&acce_bar[acc], acc_phase ^ 1u, guard, kSiteGrAccEmpty))
-            ok = 0;
-          tc_fence_after_sync();
-          for (int j = 0, kb = w.k0; ok && j < w.nk; ++j, kb += w.ks) {
-            if (!ready && !mbar_try_wait(full0 + 8u * stage, phase) &&
-                !mbar_wait(&full_bar[stage], phase, guard, kSiteGrFull)) {
+        const int chunks = grouped_chunks<C>(w.nk);   // an empty contraction has none
+        uint32_t d_tmem = 0;
+        if (lane == 0) {
+          for (int c = 0, j = 0, kb = w.k0; c < chunks && ok; ++c) {
+            if (!mbar_try_wait(acce0 + 8u * acc, acc_phase ^ 1u) &&
+                !mbar_wait(&acce_bar[acc], acc_phase ^ 1u, guard, kSiteGrAccEmpty)) {
               ok = 0;
               break;
             }
-            int issues = 4;
-            if constexpr (C::kColMn) {
-              const int left = w.len - kb * 64;
-              if (left < 64) {
-                issues = (left + 15) / 16;
-                if (!wait_fix()) {
-                  ok = 0;
-                  break;
+            tc_fence_after_sync();
+            d_tmem = tmem_base + static_cast<uint32_t>(acc * C::kTileN);
+            const int j0 = j;
+            const int j1 = grouped_chunk_end<C>(w.nk, chunks, c);
+            for (; j < j1; ++j, kb += w.ks) {
+              if (!ready && !mbar_try_wait(full0 + 8u * stage, phase) &&
+                  !mbar_wait(&full_bar[stage], phase, guard, kSiteGrFull)) {
+                ok = 0;
+                break;
+              }
+              int issues = 4;
+              if constexpr (C::kColMn) {
+                const int left = w.len - kb * 64;
+                if (left < 64) {
+                  issues = (left + 15) / 16;
+                  if (!wait_fix()) {
+                    ok = 0;
+                    break;
+                  }
                 }
               }
-            }
-            tc_fence_after_sync();
-            const int ns = stage + 1 == C::kStages ? 0 : stage + 1;
-            const uint32_t nph = stage + 1 == C::kStages ? phase ^ 1u : phase;
-            const uint64_t wd = wdesc0 + static_cast<uint64_t>(stage * (C::W_BYTES >> 4));
-            const uint64_t cd = cdesc0 + static_cast<uint64_t>(stage * (C::C_BYTES >> 4));
-            if (!C::kColMn || issues == 4) {
+              tc_fence_after_sync();
+              const int ns = stage + 1 == C::kStages ? 0 : stage + 1;
+              const uint32_t nph = stage + 1 == C::kStages ? phase ^ 1u : phase;
+              const uint64_t wd = wdesc0 + static_cast<uint64_t>(stage * (C::W_BYTES >> 4));
+              const uint64_t cd = cdesc0 + static_cast<uint64_t>(stage * (C::C_BYTES >> 4));
+              if (!C::kColMn || issues == 4) {
 #pragma unroll
-              for (int k = 0; k < 4; ++k) {
-                mma_bf16<C::kCtaGroup>(d_tmem, wd + kStepW * k, cd + kStepC * k, idesc,
-                                       (j != 0 || k != 0));
-                if (k == 0) ready = mbar_try_wait(full0 + 8u * ns, nph);
+                for (int k = 0; k < 4; ++k) {
+                  mma_bf16<C::kCtaGroup>(d_tmem, wd + kStepW * k, cd + kStepC * k, idesc,
+                                         (j != j0 || k != 0));
+                  if (k == 0) ready = mbar_try_wait(full0 + 8u * ns, nph);
+                }
+              } else {
+                for (int k = 0; k < issues; ++k)
+                  mma_bf16<C::kCtaGroup>(d_tmem, wd + kStepW * k, cd + kStepC * k, idesc,
+                                         (j != j0 || k != 0));
+                ready = mbar_try_wait(full0 + 8u * ns, nph);
               }
-            } else {
-              for (int k = 0; k < issues; ++k)
-                mma_bf16<C::kCtaGroup>(d_tmem, wd + kStepW * k, cd + kStepC * k, idesc,
-                                       (j != 0 || k != 0));
-              ready = mbar_try_wait(full0 + 8u * ns, nph);
+              if constexpr (C::kCtaGroup == 1)
+                mma_commit(&empty_bar[stage]);
+              else
+                mma_commit_pair(&empty_bar[stage], static_cast<uint16_t>(3u));
+              stage = ns;
+              phase = nph;
             }
-            if constexpr (C::kCtaGroup == 1)
-              mma_commit(&empty_bar[stage]);
-            else
-              mma_commit_pair(&empty_bar[stage], static_cast<uint16_t>(3u));
-            stage = ns;
-            phase = nph;
+            if (ok && c + 1 < chunks) commit_acc();
           }
         }
         ok = __shfl_sync(0xFFFFFFFFu, ok, 0);
@@ -759,18 +950,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
             ok = __shfl_sync(0xFFFFFFFFu, ok, 0);
           }
         }
-        if (any && ok) {
-          if (lane == 0) {
-            if constexpr (C::kCtaGroup == 1)
-              mma_commit(&accf_bar[acc]);
-            else
-              mma_commit_pair(&accf_bar[acc], static_cast<uint16_t>(3u));
-          }
-          if (++acc == C::kAccBufs) {
-            acc = 0;
-            acc_phase ^= 1u;
-          }
-        }
+        if (chunks > 0 && ok && lane == 0) commit_acc();
       }
       if (lane == 0 && (!ok || *abort_flag)) {
         if constexpr (C::kCtaGroup == 1)
@@ -780,9 +960,9 @@ __global__ void __launch_bounds__(C::kThreads, 1)
         mbar_wait_drain(drain_bar, 0, p.timeout_ns);
       }
     }
-  } else if (warp >= C::kFixWarp0) {
+  } else if (warp < C::kEpiWarp0) {
     // ------------------------------------------------------------ fixing warps
-    if constexpr (C::kFixWarps > 0) {
+    if (warp < C::kFixWarp0 + C::kFixWarps) {
       const int fw = warp - C::kFixWarp0;
       const uint32_t fix0 = map_to_cta(smem_addr(&fix_bar[0]), 0u);
       const uint32_t sW = smem_addr(smem + C::OFF_W);
@@ -862,120 +1042,227 @@ __global__ void __launch_bounds__(C::kThreads, 1)
   } else {
     // ------------------------------------------------------------ epilogue
     const int slab = warp & 3;                 // TMEM lanes 32 * slab ..
-    const int half = (warp - 2) >> 2;          // chunks half, half + 2, ...
+    const int half = (warp - C::kEpiWarp0) >> 2;   // column blocks half, half + 2, ...
     if constexpr (!C::kColMn)
       grouped_zero_rows<C>(p, first_row, end_row,
-                           static_cast<int>(blockIdx.x) * C::kEpiWarps + warp - 2,
+                           static_cast<int>(blockIdx.x) * C::kEpiWarps + warp - C::kEpiWarp0,
                            static_cast<int>(gridDim.x) * C::kEpiWarps, lane);
     int acc = 0;
     uint32_t acc_phase = 0;
+    const int box = C::kBf16Out ? (warp - C::kEpiWarp0) >> 1 : warp - C::kEpiWarp0;
+    // f32: one box a warp.  bf16: two boxes for each two warps (slabs 2i, 2i + 1).
+    const uint32_t stg =
+        smem_addr(smem + C::OFF_STG) + static_cast<uint32_t>(box) * (C::kBf16Out ? 8192u : 4096u);
+    const bool box_lead = (warp & 1) == 0 && lane == 0;
+    const uint64_t pol_d = policy_evict_first();   // D is written once
+    uint32_t flip = 0;
     uint32_t acce_dst = smem_addr(&acce_bar[0]);
     if constexpr (C::kCtaGroup == 2) acce_dst = map_to_cta(acce_dst, 0u);
-    for (int u = unit; u < num_items; u += num_units) {
-      walk.find(p, lane, u / S, u % S, S, w);
-      const bool any = w.nk > 0;
-      if (any) {
-        int got = 1;
-        if (C::kSplit && S > 1) {
-          // The warps of a split tile meet at named barriers below, so one
-          // thread decides for all of them whether the accumulator arrived.
-          if (warp == 2 && lane == 0)
-            *go = mbar_wait(&accf_bar[acc], acc_phase, guard, kSiteGrAccFull) ? 1 : 0;
-          named_bar_sync(1, 32 * C::kEpiWarps);
-          got = *go;
-        } else {
-          if (lane == 0) got = mbar_wait(&accf_bar[acc], acc_phase, guard, kSiteGrAccFull) ? 1 : 0;
-          got = __shfl_sync(0xFFFFFFFFu, got, 0);
-        }
-        if (!got) break;
-        tc_fence_after_sync();
+    // Waits for the next accumulator.
+    auto acc_ready = [&]() -> bool {
+      int got = 1;
+      if ((C::kSplit && S > 1) || (C::kStaged && C::kBf16Out)) {
+        // Warps that meet at named barriers below (all of a split tile's, the
+        // two that share a staging box) must agree whether the accumulator
+        // arrived: one thread of them decides.
+        const bool decides = C::kSplit ? warp == C::kEpiWarp0 && lane == 0 : box_lead;
+        const int id = C::kSplit ? 1 : 2 + box, count = C::kSplit ? 32 * C::kEpiWarps : 64;
+        volatile int* flag = go + (C::kSplit ? 0 : box);
+        if (decides) *flag = mbar_wait(&accf_bar[acc], acc_phase, guard, kSiteGrAccFull) ? 1 : 0;
+        named_bar_sync(id, count);
+        got = *flag;
+        named_bar_sync(id, count);
+      } else {
+        if (lane == 0) got = mbar_wait(&accf_bar[acc], acc_phase, guard, kSiteGrAccFull) ? 1 : 0;
+        got = __shfl_sync(0xFFFFFFFFu, got, 0);
       }
+      tc_fence_after_sync();
+      return got != 0;
+    };
+    // Hands the accumulator back (this warp's reads of it are complete).
+    auto hand_back = [&]() {
+      tc_fence_before_sync();
+      __syncwarp();
+      if (lane == 0) {
+        if constexpr (C::kCtaGroup == 1)
+          mbar_arrive_relaxed(&acce_bar[acc]);
+        else
+          mbar_arrive_relaxed_cluster(acce_dst + 8u * static_cast<uint32_t>(acc));
+      }
+      if (++acc == C::kAccBufs) {
+        acc = 0;
+        acc_phase ^= 1u;
+      }
+    };
+    bool ok = true;
+    for (int u = unit; u < num_items && ok; u += num_units) {
+      walk.find(p, lane, u / S, u % S, S, w);
+      const int chunks = grouped_chunks<C>(w.nk);
       const int x = w.wide0 + static_cast<int>(rank) * 128 + slab * 32 + lane;
       const float b = epi_uses_bias(p.epi.op) && x < p.wide
                           ? p.epi.bias[static_cast<int64_t>(w.g) * p.wide + x]
                           : 0.0f;
       const int64_t d0 = C::kColMn ? static_cast<int64_t>(w.g) * p.group_stride_d : 0;
       const int end = w.row0 + w.rows;
-      const int chunks = (w.rows + 31) / 32;
-      const uint32_t t_row = tmem_base + (static_cast<uint32_t>(slab * 32) << 16) +
-                             static_cast<uint32_t>(acc * C::kTileN);
-      auto hand_back = [&]() {
-        tc_fence_before_sync();
-        __syncwarp();
-        if (lane == 0) {
-          if constexpr (C::kCtaGroup == 1)
-            mbar_arrive_relaxed(&acce_bar[acc]);
-          else
-            mbar_arrive_relaxed_cluster(acce_dst + 8u * static_cast<uint32_t>(acc));
-        }
-      };
-      bool handed = false;
-      for (int ch = half; ch < chunks; ch += 2) {
-        uint32_t raw[32];
-        if (any) {
-          tmem_ld_32x32b_x32(t_row + 32 * ch, raw);
-          tmem_ld_wait();
-          if (ch + 2 >= chunks) {
-            hand_back();
-            handed = true;
-          }
-        }
-        float v[32];
-#pragma unroll
-        for (int i = 0; i < 32; ++i) v[i] = any ? __uint_as_float(raw[i]) : 0.0f;
-        const int row = w.row0 + 32 * ch;
-        if constexpr (C::kMode == kAdapter && C::kSplit)
-          add_adapter_terms<C>(p, w, row, end, x, S, v);
-        if (C::kSplit && S > 1) {
-          float* dst = p.partials +
-                       (static_cast<int64_t>(w.tile) * S + w.piece) * (C::kTileN * 128) +
-                       32 * ch * 128 + slab * 32 + lane;
-#pragma unroll
-          for (int i = 0; i < 32; ++i)
-            if (row + i < end) __stcg(dst + i * 128, v[i]);
-        } else {
-          grouped_epilogue(p.epi, b, v);
-          grouped_store<C>(p, d0, row, end, x, v);
-        }
-      }
-      if (any && !handed) hand_back();
+      const int blocks = (w.rows + 31) / 32;   // of 32 accumulator columns
+      const uint32_t t_slab = tmem_base + (static_cast<uint32_t>(slab * 32) << 16);
       if constexpr (C::kSplit) {
+        // This warp's share (column blocks half, half + 2, ...) stays in
+        // registers over the chunks.
+        constexpr int kOwn = C::kTileN / 64;
+        float m[kOwn][32];
+#pragma unroll
+        for (int q = 0; q < kOwn; ++q) grouped_zero(m[q]);
+        for (int c = 0; c < chunks; ++c) {
+          if (!acc_ready()) {
+            ok = false;
+            break;
+          }
+#pragma unroll
+          for (int q = 0; q < kOwn; ++q) {
+            if (half + 2 * q < blocks)
+              grouped_read<true>(
+                  t_slab + static_cast<uint32_t>(acc * C::kTileN + 32 * (half + 2 * q)), m[q]);
+          }
+          hand_back();
+        }
+        if (!ok) break;
+        if constexpr (C::kMode == kAdapter) {
+#pragma unroll
+          for (int q = 0; q < kOwn; ++q)
+            add_adapter_terms<C>(p, w, w.row0 + 32 * (half + 2 * q), end, x, S, m[q]);
+        }
         if (S > 1) {
+          // Publish the piece's partial; the last of the tile's pieces adds
+          // them all in piece order.
+          float* part = p.partials + static_cast<int64_t>(w.tile) * S * (C::kTileN * 128) +
+                        slab * 32 + lane;
+          float* dst = part + static_cast<int64_t>(w.piece) * (C::kTileN * 128);
+#pragma unroll
+          for (int q = 0; q < kOwn; ++q) {
+            const int col = 32 * (half + 2 * q);
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              if (w.row0 + col + i < end) __stcg(dst + (col + i) * 128, m[q][i]);
+          }
           __threadfence();
           named_bar_sync(1, 32 * C::kEpiWarps);
-          if (warp == 2 && lane == 0) {
-            const uint32_t prev = arrive_counter_gpu(p.counters + w.tile);
-            const int last = prev == static_cast<uint32_t>(S - 1);
+          if (warp == C::kEpiWarp0 && lane == 0) {
+            const int last =
+                arrive_counter_gpu(p.counters + w.tile) == static_cast<uint32_t>(S - 1);
             if (last) p.counters[w.tile] = 0u;
             *join = last;
           }
           named_bar_sync(1, 32 * C::kEpiWarps);
-          if (*join) {
-            __threadfence();
-            for (int ch = half; ch < chunks; ch += 2) {
-              const int row = w.row0 + 32 * ch;
-              const float* src = p.partials + static_cast<int64_t>(w.tile) * S * (C::kTileN * 128) +
-                                 32 * ch * 128 + slab * 32 + lane;
-              float v[32];
+          if (!*join) continue;
+          __threadfence();
 #pragma unroll
-              for (int i = 0; i < 32; ++i) v[i] = row + i < end ? __ldcg(src + i * 128) : 0.0f;
-              for (int q = 1; q < S; ++q) {
-                src += C::kTileN * 128;
+          for (int q = 0; q < kOwn; ++q) {
+            const int col = 32 * (half + 2 * q);
+            const float* src = part + col * 128;
 #pragma unroll
-                for (int i = 0; i < 32; ++i)
-                  if (row + i < end) v[i] += __ldcg(src + i * 128);
-              }
-              grouped_epilogue(p.epi, b, v);
-              grouped_store<C>(p, d0, row, end, x, v);
+            for (int i = 0; i < 32; ++i)
+              m[q][i] = w.row0 + col + i < end ? __ldcg(src + i * 128) : 0.0f;
+            for (int r = 1; r < S; ++r) {
+              src += C::kTileN * 128;
+#pragma unroll
+              for (int i = 0; i < 32; ++i)
+                if (w.row0 + col + i < end) m[q][i] += __ldcg(src + i * 128);
             }
           }
         }
-      }
-      if (any && ++acc == C::kAccBufs) {
-        acc = 0;
-        acc_phase ^= 1u;
+#pragma unroll
+        for (int q = 0; q < kOwn; ++q) {
+          const int row = w.row0 + 32 * (half + 2 * q);
+          if (row < end) {
+            grouped_epilogue(p.epi, b, m[q]);
+            grouped_store<C>(p, d0, row, end, x, m[q]);
+          }
+        }
+      } else {
+        constexpr int kOwn = C::kTileN / 64;
+        if constexpr (C::kBf16Out) {
+          // One accumulator: each block goes out as it is read, through two
+          // boxes in turn.  box_lead (one thread of the box's two warps)
+          // issues the stores and, before each meeting of the two warps, waits
+          // until the store before the last has read its box.
+          if (chunks > 0 && !acc_ready()) break;
+          float bias[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int xb = x - lane + 8 * i + (lane >> 2);
+            bias[i] = epi_uses_bias(p.epi.op) && xb < p.wide
+                          ? p.epi.bias[static_cast<int64_t>(w.g) * p.wide + xb]
+                          : 0.0f;
+          }
+          const int x0 = x - lane - 32 * (slab & 1);   // first element of the box
+          for (int q = half; q < blocks; q += 2) {
+            const int row = w.row0 + 32 * q;
+            const uint32_t at = stg + 4096u * flip;
+            flip ^= 1u;
+            grouped_stage_bf16(at, lane, slab,
+                               t_slab + static_cast<uint32_t>(acc * C::kTileN + 32 * q), chunks > 0,
+                               p.epi, bias);
+            fence_proxy_async_smem();
+            if (box_lead) bulk_wait_group_read0();
+            named_bar_sync(2 + box, 64);
+            if ((C::kColMn || row + 32 <= end) && x0 + 64 <= p.wide) {
+              if (box_lead) {
+                tma_store_3d_hint(&tmD, at, x0, row, C::kColMn ? w.g : 0, pol_d);
+                bulk_commit_group();
+              }
+            } else {
+              const int r0 = 16 * (slab & 1);
+              grouped_unstage<C>(p, d0, at, lane, r0, r0 + 16, row, end, x0);
+            }
+          }
+          if (chunks > 0) hand_back();
+        } else {
+          // One block of 32 accumulator columns to D.
+          auto finish = [&](int q, float (&v)[32]) {
+            const int row = w.row0 + 32 * q;
+            grouped_epilogue(p.epi, b, v);
+            if (lane == 0) bulk_wait_group_read0();
+            __syncwarp();
+            grouped_stage_f32(stg, lane, v);
+            if ((C::kColMn || row + 32 <= end) && x - lane + 32 <= p.wide) {
+              fence_proxy_async_smem();
+              __syncwarp();
+              if (lane == 0) {
+                tma_store_3d_hint(&tmD, stg, x, row, C::kColMn ? w.g : 0, pol_d);
+                bulk_commit_group();
+              }
+            } else {
+              __syncwarp();
+              grouped_unstage<C>(p, d0, stg, lane, 0, 32, row, end, x - lane);
+            }
+          };
+          // The warp's share of the tile stays in registers over the chunks.
+          float m[kOwn][32];
+#pragma unroll
+          for (int q = 0; q < kOwn; ++q) grouped_zero(m[q]);
+          for (int c = 0; c < chunks; ++c) {
+            if (!acc_ready()) {
+              ok = false;
+              break;
+            }
+#pragma unroll
+            for (int q = 0; q < kOwn; ++q)
+              if (half + 2 * q < blocks)
+                grouped_read<true>(
+                    t_slab + static_cast<uint32_t>(acc * C::kTileN + 32 * (half + 2 * q)), m[q]);
+            hand_back();
+          }
+          if (!ok) break;
+#pragma unroll
+          for (int q = 0; q < kOwn; ++q)
+            if (half + 2 * q < blocks) finish(half + 2 * q, m[q]);
+        }
       }
     }
+    // Stores in flight finish before the block's shared memory goes away.
+    if constexpr (C::kStaged)
+      if (lane == 0) bulk_wait_group0();
   }
 
   tc_fence_before_sync();

@@ -92,23 +92,36 @@ int launch_grouped(const GroupedOperands& operands, const GroupedArgs& args, cud
   }
   const CUtensorMapDataType bf = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
   const CUtensorMapSwizzle sw = CU_TENSOR_MAP_SWIZZLE_128B;
-  CUtensorMap tW, tC, tCs, tUp;
+  CUtensorMap tW, tW2, tUp, tD;
+  ColumnMaps tC;
   int rc;
   if constexpr (C::kMode == kGroupedWgrad) {
     rc = make_tensor_map_2d(&tW, bf, o.wide, a.wide, o.wide_rows, o.wide_ld * 2, 64, 64, sw);
     if (rc != TG_OK) return rc;
-    rc = make_tensor_map_2d(&tC, bf, o.cols, a.cols, o.wide_rows, o.cols_ld * 2, 64, 64, sw);
+    rc = make_tensor_map_2d(&tC.box[0], bf, o.cols, a.cols, o.wide_rows, o.cols_ld * 2, 64, 64, sw);
     if (rc != TG_OK) return rc;
-    tCs = tC;
+    for (int b = 1; b < kColBoxes; ++b) tC.box[b] = tC.box[0];
+    if (a.cols >= 128) {
+      rc = make_tensor_map_chunks(&tC.box[1], o.cols, a.cols, o.wide_rows, 1, o.cols_ld * 2,
+                                  o.cols_ld * 2);
+      if (rc != TG_OK) return rc;
+    }
   } else {
     // Weights: the contraction index contiguous (boxes of 128 rows), or for
     // dgrad the wide axis (boxes of 64 x 64).
     rc = make_tensor_map_3d(&tW, bf, o.wide, C::kWideMn ? a.wide : o.k, o.wide_rows, o.wide_slices,
                             o.wide_ld * 2, o.wide_slice_stride * 2, 64, C::kWideMn ? 64 : 128, sw);
     if (rc != TG_OK) return rc;
-    rc = make_tensor_map_2d(&tC, bf, o.cols, o.k, a.M, o.cols_ld * 2, 64, C::C_ROWS, sw);
-    if (rc != TG_OK) return rc;
-    rc = make_tensor_map_2d(&tCs, bf, o.cols, o.k, a.M, o.cols_ld * 2, 64, 16, sw);
+    for (int b = 0; b < kColBoxes; ++b) {
+      rc = make_tensor_map_2d(&tC.box[b], bf, o.cols, o.k, a.M, o.cols_ld * 2, 64, 16 * (b + 1), sw);
+      if (rc != TG_OK) return rc;
+    }
+  }
+  tW2 = tW;
+  if (C::kWideMn && a.wide >= 128) {
+    const bool w = C::kMode == kGroupedWgrad;
+    rc = make_tensor_map_chunks(&tW2, o.wide, a.wide, o.wide_rows, w ? 1 : o.wide_slices,
+                                o.wide_ld * 2, (w ? o.wide_ld : o.wide_slice_stride) * 2);
     if (rc != TG_OK) return rc;
   }
   tUp = tW;
@@ -117,10 +130,22 @@ int launch_grouped(const GroupedOperands& operands, const GroupedArgs& args, cud
                             o.up_slice_stride * 2, 64, 128, sw);
     if (rc != TG_OK) return rc;
   }
+  tD = tW;
+  if constexpr (C::kStaged) {
+    // Boxes of 32 rows x 128 bytes; wgrad's rows end with the group's D.
+    const int64_t esize = C::kBf16Out ? 2 : 4;
+    const bool w = C::kMode == kGroupedWgrad;
+    rc = make_tensor_map_3d(
+        &tD, C::kBf16Out ? bf : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, a.D, a.wide, w ? a.cols : a.M,
+        w ? a.groups : 1, a.ldd * esize,
+        (w && a.groups > 1 ? a.group_stride_d : a.ldd * (w ? a.cols : a.M)) * esize,
+        C::kBf16Out ? 64 : 32, 32, C::kBf16Out ? sw : CU_TENSOR_MAP_SWIZZLE_NONE);
+    if (rc != TG_OK) return rc;
+  }
   cfg.gridDim = dim3(static_cast<unsigned>(units * C::kCtaGroup), 1, 1);
   cfg.stream = stream;
   cfg.numAttrs = C::kCtaGroup == 2 ? 2 : 1;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, tW, tC, tCs, tUp, a);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, tW, tW2, tC, tUp, tD, a);
   return e == cudaSuccess ? TG_OK : cuda_fail(e);
 }
 

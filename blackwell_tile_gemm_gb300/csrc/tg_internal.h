@@ -53,6 +53,13 @@ int make_tensor_map_3d(CUtensorMap* map, CUtensorMapDataType dtype, const void* 
                        uint64_t slice_bytes, uint32_t box_inner, uint32_t box_outer,
                        CUtensorMapSwizzle swizzle);
 
+// Boxes of 64 rows x two neighbouring 64-element chunks (bf16, 128B swizzle,
+// one chunk's 64 rows after the other's) over `slices` arrays of `rows` x
+// `width`; coordinates (0, row, chunk, slice).  Covers the whole chunks of a
+// row only: width >= 64, and a last width % 64 elements are not in the map.
+int make_tensor_map_chunks(CUtensorMap* map, const void* base, uint64_t width, uint64_t rows,
+                           uint64_t slices, uint64_t row_bytes, uint64_t slice_bytes);
+
 // Library-owned device workspace for (current device, `stream`), at least
 // `bytes` long.  Without a reservation it is grown on demand (growing
 // synchronises the stream first); a reserved workspace never grows.  When it
