@@ -47,6 +47,7 @@ TG_CALL_GEMM_MXFP4 = 2
 TG_CALL_GEMM_NVFP4 = 3
 TG_CALL_GEMM_BF16_SKINNY = 4
 TG_CALL_GEMM_BF16_GATHER = 5
+TG_CALL_GROUP_ROWS = 6
 TG_CLOCK_BF16 = 0
 TG_CLOCK_MXFP8 = 1
 TG_CLOCK_MXFP4 = 2
@@ -110,6 +111,8 @@ def lib() -> ctypes.CDLL:
         L.gemm_bf16_gather.restype = i32
         L.gemm_bf16_gather.argtypes = [vp, i64, i64, vp, i64, vp, i64, vp, i64, i64, i64, i32,
                                        ctypes.POINTER(tg_epilogue), u32, vp]
+        L.tg_group_rows.restype = i32
+        L.tg_group_rows.argtypes = [vp, i64, i64, vp, vp, vp, vp]
         L.gemm_bf16_grouped.restype = i32
         L.gemm_bf16_grouped.argtypes = [vp, i64, i64, vp, vp, i64, i64, vp, i64, i64, vp, i64, i64,
                                         i64, i32, ctypes.POINTER(tg_epilogue), u32, vp]
@@ -373,6 +376,26 @@ def gemm_bf16_gather(A, row_idx, B, D=None, *, out_dtype=None, epilogue_add=None
                                 _stream_handle(stream))
     _check(rc, "gemm_bf16_gather")
     return D
+
+
+def group_rows(ids, groups, *, stream=None):
+    """(offsets, order, slot): the rows of each group, from a group id per row.
+
+    ids: int32 CUDA vector [n]; ids outside [0, groups) mean no group.
+    offsets [groups + 1] counts the rows of smaller ids; order [n] lists the
+    rows group by group, ascending within a group and rows in no group last;
+    slot [n] is its inverse (slot[order[j]] = j).  All int32, on the device.
+    """
+    import torch
+    p = _int32_vector(ids, "ids")
+    n = ids.shape[0]
+    offsets = torch.empty(int(groups) + 1, dtype=torch.int32, device=ids.device)
+    order = torch.empty_like(ids)
+    slot = torch.empty_like(ids)
+    rc = lib().tg_group_rows(p, n, int(groups), offsets.data_ptr(), order.data_ptr(),
+                             slot.data_ptr(), _stream_handle(stream))
+    _check(rc, "tg_group_rows")
+    return offsets, order, slot
 
 
 def _slices(t, name, mult=8):

@@ -194,6 +194,9 @@ size_t skinny_workspace_bytes(int64_t M, int64_t N, int d_dtype, int epi_op);
 // stages per piece.
 int skinny_splits(int64_t N, int64_t K, int split_k, int num_sms, int* per_split);
 
+// Workspace of tg_group_rows (0 where one CTA does it).
+size_t group_rows_workspace_bytes(int64_t n, int64_t groups);
+
 // D = epilogue(0) when K == 0.
 int launch_fill_epilogue(void* D, int64_t ldd, int64_t M, int64_t N, int d_dtype, const Epi& epi,
                          cudaStream_t stream);

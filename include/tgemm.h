@@ -296,6 +296,24 @@ int gemm_bf16_gather(const void* A, int64_t lda, int64_t a_rows, const int32_t* 
 enum { TG_MAX_GROUPS = 4096 };
 
 /*
+ * tg_group_rows -- the rows of each group, from a group id per row (a stable
+ * counting sort).
+ *   ids     : device, int32 [n]: an expert per (token, choice), an adapter per
+ *             token, ...  An id outside [0, groups) means no group.
+ *   offsets : device, int32 [groups + 1]: rows of smaller ids; offsets[groups]
+ *             is the number of rows in groups.
+ *   order   : device, int32 [n]: order[offsets[g]] .. order[offsets[g+1] - 1]
+ *             are the rows of group g, ascending; rows in no group come last.
+ *   slot    : device, int32 [n] or NULL: the inverse, slot[order[j]] = j.
+ *   The arrays must not overlap.  0 <= n <= 2^30; n = 0 sets the offsets to
+ *   zero.  More than 2048 rows use the stream's workspace (TG_CALL_GROUP_ROWS).
+ * With row_idx = order (or order / k for k choices a token) the grouped
+ * products read their rows in place, and slot finds a row's result again.
+ */
+int tg_group_rows(const int32_t* ids, int64_t n, int64_t groups, int32_t* offsets,
+                  int32_t* order, int32_t* slot, void* cuda_stream);
+
+/*
  * gemm_bf16_grouped -- D[i, :] = epi(A[r(i), :] * B[g]^T) for the rows i of
  * group g, with r(i) = row_idx[i], or i where row_idx is NULL.
  *   A       : device, bf16 [a_rows, K], row stride lda.
@@ -358,7 +376,9 @@ enum {
   TG_CALL_GEMM_MXFP4 = 2,       /* gemm_mxfp4_blockscaled                      */
   TG_CALL_GEMM_NVFP4 = 3,       /* gemm_nvfp4_blockscaled                      */
   TG_CALL_GEMM_BF16_SKINNY = 4, /* gemm_bf16_skinny                            */
-  TG_CALL_GEMM_BF16_GATHER = 5  /* gemm_bf16_gather (M = gathered rows)        */
+  TG_CALL_GEMM_BF16_GATHER = 5, /* gemm_bf16_gather (M = gathered rows), and the
+                                   grouped products with a row_idx             */
+  TG_CALL_GROUP_ROWS = 6        /* tg_group_rows (M = n, N = groups, K = 1)    */
 };
 
 /*
