@@ -48,6 +48,7 @@ TG_CALL_GEMM_NVFP4 = 3
 TG_CALL_GEMM_BF16_SKINNY = 4
 TG_CALL_GEMM_BF16_GATHER = 5
 TG_CALL_GROUP_ROWS = 6
+TG_CALL_GEMM_BF16_LORA = 7
 TG_CLOCK_BF16 = 0
 TG_CLOCK_MXFP8 = 1
 TG_CLOCK_MXFP4 = 2
@@ -122,6 +123,10 @@ def lib() -> ctypes.CDLL:
         L.gemm_bf16_grouped_wgrad.restype = i32
         L.gemm_bf16_grouped_wgrad.argtypes = [vp, i64, vp, i64, i64, vp, vp, i64, i64, vp, i64,
                                               i64, i64, i64, i32, u32, vp]
+        L.gemm_bf16_lora.restype = i32
+        L.gemm_bf16_lora.argtypes = [vp, i64, vp, i64, vp, vp, i64, i64, vp, i64, i64, vp, i64, i64,
+                                     vp, i64, i64, i64, i64, i32, ctypes.POINTER(tg_epilogue), u32,
+                                     vp]
         L.tg_gemm_tail_split.restype = i32
         L.tg_gemm_tail_split.argtypes = [i64, i64, i64, u32]
         L.tg_gemm_multicast.restype = i32
@@ -532,6 +537,48 @@ def gemm_bf16_grouped_wgrad(G, A, offsets, D=None, *, row_idx=None, out_dtype=No
                                        A.shape[0], idx, off, groups, M, D.data_ptr(), ldd, gsd, N,
                                        K, _d_code(D.dtype), 0, _stream_handle(stream))
     _check(rc, "gemm_bf16_grouped_wgrad")
+    return D
+
+
+def gemm_bf16_lora(A, B, ids, down, up, D=None, *, scales=None, out_dtype=None, epilogue_add=None,
+                   silu_affine=None, bias=None, bias_silu=False, affine=None, stream=None):
+    """D[i] = A[i] @ B.T + scales[id] * (A[i] @ down[id].T) @ up[id].T (+ epilogue), id = ids[i].
+
+    A shared projection with a low-rank adapter per row.  A: bfloat16 [M, K];
+    B: bfloat16 [N, K]; ids: int32 CUDA vector [M], ids outside [0, adapters)
+    mean no adapter; down: bfloat16 [adapters, rank, K]; up: bfloat16
+    [adapters, N, rank], rank a multiple of 8 up to 256; scales: float32
+    [adapters] or None.  D: float32 or bfloat16 [M, N] (default float32).
+    Epilogue keywords: see ``make_epilogue``.
+    """
+    import torch
+    _bf16_only(A=A, B=B, down=down, up=up)
+    M, K = A.shape
+    N, K2 = B.shape
+    adapters, rank = down.shape[:2] if down.dim() == 3 else (0, 0)
+    if K2 != K:
+        raise ValueError("A is [M, K] and B is [N, K]")
+    if tuple(down.shape) != (adapters, rank, K) or tuple(up.shape) != (adapters, N, rank):
+        raise ValueError("down is [adapters, rank, K] and up is [adapters, N, rank]")
+    if scales is not None and (scales.dtype != torch.float32 or not scales.is_contiguous()
+                               or tuple(scales.shape) != (adapters,)):
+        raise TypeError("scales must be a contiguous float32 vector of one value per adapter")
+    if bias is not None and bias.shape[0] != N:
+        raise ValueError("bias must have N elements")
+    if D is None:
+        D = _new_rows((M, N), out_dtype or torch.float32, A.device)
+    if tuple(D.shape) != (M, N):
+        raise ValueError("D must be [M, N]")
+    idp = _int32_vector(ids, "ids", M)
+    epi = make_epilogue(epilogue_add, silu_affine, bias, bias_silu, affine)
+    ldd_, sd = _slices(down, "down")
+    ldu, su = _slices(up, "up")
+    rc = lib().gemm_bf16_lora(A.data_ptr(), _ld(A, "A", 8), B.data_ptr(), _ld(B, "B", 8), idp,
+                              down.data_ptr(), ldd_, sd, up.data_ptr(), ldu, su,
+                              None if scales is None else scales.data_ptr(), adapters, rank,
+                              D.data_ptr(), _ld(D, "D", 8), M, N, K, _d_code(D.dtype),
+                              ctypes.byref(epi), 0, _stream_handle(stream))
+    _check(rc, "gemm_bf16_lora")
     return D
 
 

@@ -676,6 +676,8 @@ int64_t tg_workspace_bytes(int call, int64_t M, int64_t N, int64_t K, int64_t ld
       return (flags & TG_FLAG_GATHER_TMA) ? 0 : static_cast<int64_t>(gather_workspace_bytes(M, K));
     case TG_CALL_GROUP_ROWS:
       return static_cast<int64_t>(group_rows_workspace_bytes(M, N));
+    case TG_CALL_GEMM_BF16_LORA:
+      return static_cast<int64_t>(lora_workspace_bytes(M, N));
     default:
       return -TG_ERR_INVALID_ARG;
   }

@@ -1,0 +1,356 @@
+// A shared projection with a low-rank adapter per row:
+//
+//   D[i, :] = epi( A[i, :] * B^T + s[id_i] * (A[i, :] * down[id_i]^T) * up[id_i]^T )
+//
+// Two launches.  lora_down_kernel computes H[i, :] = s[id_i] * A[i, :] *
+// down[id_i]^T (rank values a row); the grouped kernel (kAdapter) runs the
+// shared product and adds H[i, :] * up[id_i]^T inside it, so that D is
+// written once and the second term costs no pass of its own.
+//
+// lora_down_kernel.  2 M K rank flop against (M + adapters * rank) K values
+// read: at most a few tens of flop per byte, so reading A and `down` bounds it
+// and warp-level MMAs (m16n8k16, f32 accumulation) are ample.  The roles are
+// swapped: 16 rows of `down` fill the MMA's M, 8 rows of A its N, so that
+// one row of A alone wastes no more than 7 idle columns.  A fragment's k
+// indices need not be neighbours in memory as long as both operands agree, so
+// each thread loads 16 contiguous bytes of a row (8 values, two MMAs' worth)
+// straight into its fragments: no shared memory, no transposition.
+//
+// A block takes kTok consecutive rows and a slice of K: its warps share the
+// slice, the CTAs of the cluster share K, and the partial sums meet in
+// (distributed) shared memory in a fixed order.  A tile's rows may belong to
+// several adapters: each distinct one is computed for the whole tile and kept
+// for its own rows (prompts have one or two to a tile; with 8-row tiles, the
+// decoding case, the adapters of a tile run in different blocks).
+#include <cfloat>
+
+#include "grouped_launch.cuh"
+
+namespace tg {
+namespace {
+
+constexpr int kDownWarps = 8;
+
+struct DownArgs {
+  const uint16_t* A;
+  int64_t lda;
+  int M, K;
+  const int* ids;
+  const uint16_t* down;
+  int64_t ld_down, stride_down;
+  const float* scales;   // may be null: 1
+  int adapters, rank;
+  int k_per_cta;         // multiple of 32 * kDownWarps
+  float* h;              // [M][rank], or null
+  uint16_t* hi;          // [M][rank]: bf16 terms of the same
+  uint16_t* lo;
+};
+
+__device__ __forceinline__ void mma_m16n8k16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                             uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+      "{%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// Values k .. k + 7 of a row; those from `end` on are zero and not read.
+__device__ __forceinline__ uint4 load8(const uint16_t* row, int k, int end) {
+  if (k + 8 <= end) return __ldg(reinterpret_cast<const uint4*>(row + k));
+  uint32_t w[4] = {0u, 0u, 0u, 0u};
+#pragma unroll
+  for (int e = 0; e < 8; ++e)
+    if (k + e < end) w[e / 2] |= static_cast<uint32_t>(row[k + e]) << (16 * (e & 1));
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+__device__ __forceinline__ float ld_dsmem(uint32_t addr) {
+  float v;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+  return v;
+}
+
+// kTok rows a tile; kRt 16-row tiles of `down` at a time (rank > 16 kRt: in
+// several passes over the rows).
+template <int kTok, int kRt>
+__global__ void __launch_bounds__(32 * kDownWarps) lora_down_kernel(const DownArgs p) {
+  constexpr int kNt = kTok / 8;
+  constexpr int kElems = 16 * kRt * kTok;
+  constexpr int kPer = (kTok + 31) / 32;
+  extern __shared__ float part[];      // [warp][kElems], then the CTA's sum in [0]
+  griddep_wait();
+  // What the next kernel reads early (A, B, ids) was there before this one.
+  griddep_launch_dependents();
+  const int warp = threadIdx.x >> 5;
+  const int lane = static_cast<int>(threadIdx.x & 31);
+  const int g = lane >> 2, q = lane & 3;
+  const int csize = static_cast<int>(gridDim.z);
+  const int crank = static_cast<int>(blockIdx.z);     // one cluster spans z
+  const int row0 = static_cast<int>(blockIdx.x) * kTok;
+  const int rows = min(kTok, p.M - row0);
+  uint32_t ids[kPer];
+#pragma unroll
+  for (int i = 0; i < kPer; ++i)
+    ids[i] = lane + 32 * i < rows ? static_cast<uint32_t>(p.ids[row0 + lane + 32 * i]) : 0xFFFFFFFFu;
+  const int kbeg = crank * p.k_per_cta;
+  const int kend = min(p.K, kbeg + p.k_per_cta);
+  // Adapter number blockIdx.y, + gridDim.y, ... of the tile (the same in every
+  // CTA of the cluster, so all of them meet at its barriers).
+  int ordinal = 0;
+  for (int id = next_adapter(ids, -1, p.adapters); id >= 0; id = next_adapter(ids, id, p.adapters)) {
+    if (ordinal++ % static_cast<int>(gridDim.y) != static_cast<int>(blockIdx.y)) continue;
+    const uint16_t* down = p.down + id * p.stride_down;
+    const float scale = p.scales ? p.scales[id] : 1.0f;
+    for (int r0 = 0; r0 < p.rank; r0 += 16 * kRt) {
+      float acc[kRt][kNt][4];
+#pragma unroll
+      for (int t = 0; t < kRt; ++t)
+#pragma unroll
+        for (int n = 0; n < kNt; ++n)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) acc[t][n][e] = 0.0f;
+#pragma unroll 2
+      for (int k = kbeg + 32 * warp; k < kend; k += 32 * kDownWarps) {
+        const int kk = k + 8 * q;
+        uint4 a[kRt][2], b[kNt];
+#pragma unroll
+        for (int t = 0; t < kRt; ++t)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const int r = r0 + 16 * t + 8 * h + g;
+            a[t][h] = r < p.rank ? load8(down + r * p.ld_down, kk, kend) : make_uint4(0u, 0u, 0u, 0u);
+          }
+#pragma unroll
+        for (int n = 0; n < kNt; ++n) {
+          const int i = 8 * n + g;
+          b[n] = i < rows ? load8(p.A + static_cast<int64_t>(row0 + i) * p.lda, kk, kend)
+                          : make_uint4(0u, 0u, 0u, 0u);
+        }
+#pragma unroll
+        for (int t = 0; t < kRt; ++t)
+#pragma unroll
+          for (int n = 0; n < kNt; ++n) {
+            mma_m16n8k16(acc[t][n], a[t][0].x, a[t][1].x, a[t][0].y, a[t][1].y, b[n].x, b[n].y);
+            mma_m16n8k16(acc[t][n], a[t][0].z, a[t][1].z, a[t][0].w, a[t][1].w, b[n].z, b[n].w);
+          }
+      }
+      // [down row][row of A]: c0, c1 at (g, 2q), (g, 2q + 1); c2, c3 8 rows on.
+      float* mine = part + warp * kElems;
+#pragma unroll
+      for (int t = 0; t < kRt; ++t)
+#pragma unroll
+        for (int n = 0; n < kNt; ++n)
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            mine[(16 * t + g + 8 * (e >> 1)) * kTok + 8 * n + 2 * q + (e & 1)] = acc[t][n][e];
+      __syncthreads();
+      for (int e = threadIdx.x; e < kElems; e += 32 * kDownWarps) {
+        float s = part[e];
+#pragma unroll
+        for (int w = 1; w < kDownWarps; ++w) s += part[w * kElems + e];
+        part[e] = s;     // read and written by this thread only
+      }
+      if (csize > 1)
+        cluster_sync();
+      else
+        __syncthreads();
+      // Each CTA finishes a share of the tile's values.
+      for (int e = crank * 32 * kDownWarps + static_cast<int>(threadIdx.x); e < kElems;
+           e += csize * 32 * kDownWarps) {
+        const int i = e / (16 * kRt), r = r0 + e % (16 * kRt);
+        const int at = (e % (16 * kRt)) * kTok + i;
+        if (i < rows && r < p.rank && p.ids[row0 + i] == id) {
+          float s = 0.0f;
+          if (csize > 1) {
+            const uint32_t a = smem_addr(part + at);
+            for (int c = 0; c < csize; ++c) s += ld_dsmem(map_to_cta(a, c));
+          } else {
+            s = part[at];
+          }
+          s *= scale;
+          const int64_t o = static_cast<int64_t>(row0 + i) * p.rank + r;
+          if (p.h != nullptr) {
+            p.h[o] = s;
+          } else {
+            const uint32_t hi = pack_bf16x2(s, s) & 0xFFFFu;
+            const float rest = s - __uint_as_float(hi << 16);
+            p.hi[o] = static_cast<uint16_t>(hi);
+            // What is infinite or NaN in hi is in hi alone.
+            p.lo[o] = static_cast<uint16_t>(
+                pack_bf16x2(fabsf(rest) <= FLT_MAX ? rest : 0.0f, 0.0f) & 0xFFFFu);
+          }
+        }
+      }
+      // The partial sums are free again once every CTA has read them.
+      if (csize > 1)
+        cluster_sync();
+      else
+        __syncthreads();
+    }
+  }
+}
+
+template <int kTok, int kRt>
+int launch_down(DownArgs a, cudaStream_t stream, DeviceCtx* ctx) {
+  static std::atomic<int> prepared[64];
+  auto kern = lora_down_kernel<kTok, kRt>;
+  constexpr int kSmem = kDownWarps * 16 * kRt * kTok * 4;
+  if (prepared[ctx->device].load(std::memory_order_acquire) == 0) {
+    const cudaError_t e =
+        cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+    if (e != cudaSuccess) return cuda_fail(e);
+    prepared[ctx->device].store(1, std::memory_order_release);
+  }
+  const int tiles = ceil_div_i(a.M, kTok);
+  // K over a cluster of up to 8 CTAs, while that adds blocks the SMs have
+  // room for and leaves a CTA at least one step per warp.
+  int c = 1;
+  const int y = kTok < 8 ? kTok : kTok == 8 ? (a.M < 8 ? a.M : 8) : 1;
+  while (c < 8 && tiles * y * c < 2 * ctx->num_sms && a.K > 32 * kDownWarps * c) c *= 2;
+  a.k_per_cta = ceil_div_i(ceil_div_i(a.K, c), 32 * kDownWarps) * 32 * kDownWarps;
+  cudaLaunchConfig_t cfg{};
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = 1;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = static_cast<unsigned>(c);
+  cfg.gridDim = dim3(static_cast<unsigned>(tiles), static_cast<unsigned>(y), static_cast<unsigned>(c));
+  cfg.blockDim = dim3(32 * kDownWarps, 1, 1);
+  cfg.dynamicSmemBytes = kSmem;
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = c > 1 ? 2 : 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, a);
+  return e == cudaSuccess ? TG_OK : cuda_fail(e);
+}
+
+bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
+// Rows up to which the weights' stream bounds the product: single CTAs with a
+// split contraction and the adapter term in the epilogue.
+constexpr int kLoraFewRows = 128;
+
+}  // namespace
+
+// H: f32 for few rows, else two bf16 terms: 4 bytes a value either way.
+size_t lora_workspace_bytes(int64_t M, int64_t rank) {
+  return (static_cast<size_t>(M) * static_cast<size_t>(rank) * 4u + 255u) / 256u * 256u;
+}
+
+}  // namespace tg
+
+using namespace tg;
+
+extern "C" int gemm_bf16_lora(const void* A, int64_t lda, const void* B, int64_t ldb,
+                              const int32_t* ids, const void* down, int64_t ld_down,
+                              int64_t stride_down, const void* up, int64_t ld_up,
+                              int64_t stride_up, const float* scales, int64_t adapters,
+                              int64_t rank, void* D, int64_t ldd, int64_t M, int64_t N, int64_t K,
+                              int d_dtype, const tg_epilogue* epi, unsigned flags,
+                              void* cuda_stream) {
+  constexpr int64_t kMaxDim = (int64_t{1} << 31) - 1;
+  Epi e;
+  int rc = check_epilogue(epi, &e);
+  if (rc != TG_OK) return rc;
+  if (flags != 0) return TG_ERR_UNSUPPORTED;
+  if (M < 0 || N < 0 || K < 0 || M > kMaxDim || N > kMaxDim || K > kMaxDim)
+    return TG_ERR_INVALID_ARG;
+  if (d_dtype != TG_D_F32 && d_dtype != TG_D_BF16) return TG_ERR_INVALID_ARG;
+  if (adapters < 0 || adapters > kMaxDim || rank < 1) return TG_ERR_INVALID_ARG;
+  if (rank % 8 != 0 || rank > TG_MAX_RANK) return TG_ERR_UNSUPPORTED;
+  if ((M / 64 + 1) * (N / 128 + 1) > kMaxDim) return TG_ERR_UNSUPPORTED;
+  if (M == 0 || N == 0) return TG_OK;
+  const int d_esize = d_dtype == TG_D_F32 ? 4 : 2;
+  if (D == nullptr || ldd < N) return TG_ERR_INVALID_ARG;
+  if (!aligned16(D) || (ldd * d_esize) % 16 != 0) return TG_ERR_MISALIGNED;
+  if (K > 0) {
+    if (A == nullptr || B == nullptr || lda < K || ldb < K) return TG_ERR_INVALID_ARG;
+    if (!aligned16(A) || !aligned16(B) || lda % 8 != 0 || ldb % 8 != 0) return TG_ERR_MISALIGNED;
+    if (adapters > 0) {
+      if (ids == nullptr || down == nullptr || up == nullptr || ld_down < K || ld_up < rank)
+        return TG_ERR_INVALID_ARG;
+      if (adapters > 1 &&
+          (stride_down < (rank - 1) * ld_down + K || stride_up < (N - 1) * ld_up + rank))
+        return TG_ERR_INVALID_ARG;
+      if (!aligned16(down) || !aligned16(up) || ld_down % 8 != 0 || ld_up % 8 != 0)
+        return TG_ERR_MISALIGNED;
+      if (adapters > 1 && (stride_down % 8 != 0 || stride_up % 8 != 0)) return TG_ERR_MISALIGNED;
+    }
+  }
+  DeviceCtx* ctx = current_ctx();
+  if (!ctx) return TG_ERR_CUDA;
+  cudaStream_t stream = static_cast<cudaStream_t>(cuda_stream);
+  if (K == 0) return launch_fill_epilogue(D, ldd, M, N, d_dtype, e, stream);
+  if (adapters == 0)
+    return launch_gemm(kKindBf16, A, lda, B, ldb, nullptr, 0, nullptr, 0, D, ldd, M, N, K, d_dtype,
+                       e, 0, stream, ctx);
+  const bool few = M <= kLoraFewRows;
+  void* ws = device_workspace(lora_workspace_bytes(M, rank), stream, &rc);
+  if (ws == nullptr) return rc;
+  DownArgs d{};
+  d.A = static_cast<const uint16_t*>(A);
+  d.lda = lda;
+  d.M = static_cast<int>(M);
+  d.K = static_cast<int>(K);
+  d.ids = ids;
+  d.down = static_cast<const uint16_t*>(down);
+  d.ld_down = ld_down;
+  d.stride_down = adapters > 1 ? stride_down : 0;
+  d.scales = scales;
+  d.adapters = static_cast<int>(adapters);
+  d.rank = static_cast<int>(rank);
+  d.h = few ? static_cast<float*>(ws) : nullptr;
+  d.hi = few ? nullptr : static_cast<uint16_t*>(ws);
+  d.lo = few ? nullptr : d.hi + M * rank;
+  if (few)
+    rc = rank <= 16   ? launch_down<8, 1>(d, stream, ctx)
+         : rank <= 32 ? launch_down<8, 2>(d, stream, ctx)
+                      : launch_down<8, 4>(d, stream, ctx);
+  else
+    rc = rank <= 16   ? launch_down<64, 1>(d, stream, ctx)
+         : rank <= 32 ? launch_down<64, 2>(d, stream, ctx)
+                      : launch_down<64, 4>(d, stream, ctx);
+  if (rc != TG_OK) return rc;
+  GroupedArgs a = grouped_args(ctx);
+  a.M = static_cast<int>(M);
+  a.wide = static_cast<int>(N);
+  a.num_k_blocks = ceil_div_i(K, 64);
+  a.D = D;
+  a.ldd = ldd;
+  a.epi = e;
+  a.ids = ids;
+  a.adapters = static_cast<int>(adapters);
+  a.rank = static_cast<int>(rank);
+  a.h = d.h;
+  a.h_hi = d.hi;
+  a.h_lo = d.lo;
+  a.up = static_cast<const uint16_t*>(up);
+  a.ld_up = ld_up;
+  a.group_stride_up = adapters > 1 ? stride_up : 0;
+  GroupedOperands o{};
+  o.wide = B;
+  o.wide_ld = ldb;
+  o.wide_rows = N;
+  o.wide_slices = 1;
+  o.wide_slice_stride = ldb * N;
+  o.cols = A;
+  o.cols_ld = lda;
+  o.k = K;
+  o.up = up;
+  o.up_ld = ld_up;
+  o.up_slices = adapters;
+  o.up_slice_stride = adapters > 1 ? stride_up : ld_up * N;
+  o.up_rank = rank;
+  const bool bf16 = d_dtype == TG_D_BF16;
+  if (M <= 64)
+    return bf16 ? launch_grouped<GroupedCfg<kAdapter, 1, 64, 8, true>>(o, a, stream, ctx)
+                : launch_grouped<GroupedCfg<kAdapter, 1, 64, 8, false>>(o, a, stream, ctx);
+  if (few)
+    return bf16 ? launch_grouped<GroupedCfg<kAdapter, 1, 128, 6, true>>(o, a, stream, ctx)
+                : launch_grouped<GroupedCfg<kAdapter, 1, 128, 6, false>>(o, a, stream, ctx);
+  return bf16 ? launch_grouped<GroupedCfg<kAdapter, 2, 256, 6, true>>(o, a, stream, ctx)
+              : launch_grouped<GroupedCfg<kAdapter, 2, 256, 6, false>>(o, a, stream, ctx);
+}

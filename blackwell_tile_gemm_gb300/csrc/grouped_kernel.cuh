@@ -39,7 +39,10 @@
 // adapter that occurs among the tile's rows adds ceil(rank / 64) * 2 stages:
 // up[id] by TMA, H written by the fixing warps with zeros in the rows of
 // other adapters.  The base product and every adapter's term meet in one
-// accumulator: D is written once.
+// accumulator: D is written once.  A zero row times an infinite or NaN
+// weight would still be NaN, so where a tile's rows differ in their adapter
+// the fixing warps take such weights out of up[id] and mark the tile; the
+// epilogue of a marked tile adds what they give in the rows they belong to.
 //
 // Few rows (kSplit, single CTAs): the product is bound by reading the
 // weights, tiles are few, so S units share a tile's contraction; each writes
@@ -142,7 +145,7 @@ struct GroupedCfg {
   static constexpr int kChunk = 12;
   static constexpr int NUM_BARS = 2 * kStages + 2 * kAccBufs + 1 + (kFixWarps ? 2 * kStages : 0);
   static constexpr int OFF_MISC = OFF_BAR + NUM_BARS * 8;
-  static constexpr int SMEM_BYTES = OFF_MISC + 32 + 1024;
+  static constexpr int SMEM_BYTES = OFF_MISC + 32 + (kExt ? 64 : 0) + 1024;
   static constexpr int TMEM_COLS = 2 * kTileN <= 32    ? 32
                                    : 2 * kTileN <= 64  ? 64
                                    : 2 * kTileN <= 128 ? 128
@@ -370,6 +373,27 @@ __device__ __forceinline__ void load_tile_ids(const GroupedArgs& p, const Groupe
   }
 }
 
+// Whether the tile's rows differ in their adapter (or some have none).
+template <int kPer>
+__device__ __forceinline__ bool mixed_adapters(const uint32_t (&ids)[kPer], int rows, int lane,
+                                               uint32_t adapters) {
+  uint32_t lo = 0xFFFFFFFFu, hi = 0u;
+#pragma unroll
+  for (int i = 0; i < kPer; ++i)
+    if (lane + 32 * i < rows) {
+      lo = min(lo, min(ids[i], adapters));
+      hi = max(hi, min(ids[i], adapters));
+    }
+  return __reduce_min_sync(0xFFFFFFFFu, lo) != __reduce_max_sync(0xFFFFFFFFu, hi);
+}
+
+// A word of two bf16 values without its infinite and NaN ones.
+__device__ __forceinline__ uint32_t finite_bf16x2(uint32_t w) {
+  if ((w & 0x7F800000u) == 0x7F800000u) w &= 0x0000FFFFu;
+  if ((w & 0x00007F80u) == 0x00007F80u) w &= 0xFFFF0000u;
+  return w;
+}
+
 // epi(v) on the accumulators of one lane, whose column of D has bias b.
 template <int kN>
 __device__ __forceinline__ void grouped_epilogue(const Epi& e, float b, float (&v)[kN]) {
@@ -552,30 +576,71 @@ __device__ __forceinline__ void grouped_zero_rows(const GroupedArgs& p, int firs
   }
 }
 
-// Adapter term of a few-row tile: v[j] += up[id][x, :] . H[row + j, :] for
-// the rows of this unit's piece (row j belongs to piece j mod S).
-template <class C>
-__device__ __forceinline__ void add_adapter_terms(const GroupedArgs& p, const GroupedWork& w, int row,
-                                                  int end, int x, int S, float (&v)[32]) {
+// What the infinite and NaN weights of up[id] that were taken out of a marked
+// tile give in the rows they belong to.
+static __device__ __noinline__ float marked_term(const GroupedArgs& p, int row, int x) {
+  const uint32_t id = static_cast<uint32_t>(p.ids[row]);
+  float s = 0.0f;
+  if (id >= static_cast<uint32_t>(p.adapters)) return s;
+  const uint16_t* u = p.up + id * p.group_stride_up + static_cast<int64_t>(x) * p.ld_up;
+  const int64_t h = static_cast<int64_t>(row) * p.rank;
+  for (int r = 0; r < p.rank; ++r)
+    if ((u[r] & 0x7F80u) == 0x7F80u)
+      s += __uint_as_float(static_cast<uint32_t>(u[r]) << 16) *
+           (__uint_as_float(static_cast<uint32_t>(p.h_hi[h + r]) << 16) +
+            __uint_as_float(static_cast<uint32_t>(p.h_lo[h + r]) << 16));
+  return s;
+}
+__device__ __forceinline__ void add_marked_terms(const GroupedArgs& p, int row, int end, int x,
+                                                 float (&v)[32]) {
   if (x >= p.wide) return;
 #pragma unroll
-  for (int j = 0; j < 32; ++j) {
-    if (row + j >= end || (row + j) % S != w.piece) continue;
-    const uint32_t id = static_cast<uint32_t>(__ldg(p.ids + row + j));
-    if (id >= static_cast<uint32_t>(p.adapters)) continue;
-    const uint16_t* u = p.up + id * p.group_stride_up + static_cast<int64_t>(x) * p.ld_up;
-    const float* h = p.h + static_cast<int64_t>(row + j) * p.rank;
-    float sum = 0.0f;
-    for (int r = 0; r < p.rank; r += 8) {
-      const uint4 q = ld_global_nc_v4(u + r);
-      const float4 h0 = *reinterpret_cast<const float4*>(h + r);
-      const float4 h1 = *reinterpret_cast<const float4*>(h + r + 4);
-      sum += __uint_as_float(q.x << 16) * h0.x + __uint_as_float(q.x & 0xFFFF0000u) * h0.y;
-      sum += __uint_as_float(q.y << 16) * h0.z + __uint_as_float(q.y & 0xFFFF0000u) * h0.w;
-      sum += __uint_as_float(q.z << 16) * h1.x + __uint_as_float(q.z & 0xFFFF0000u) * h1.y;
-      sum += __uint_as_float(q.w << 16) * h1.z + __uint_as_float(q.w & 0xFFFF0000u) * h1.w;
+  for (int j = 0; j < 32; ++j)
+    if (row + j < end) v[j] += marked_term(p, row + j, x);
+}
+
+// Adapter term of 32 rows of a few-row tile: v[j] += up[id][x, :] . H[row + j, :]
+// in f32, for the batches of eight rows whose number is the unit's piece
+// modulo S (the pieces of a tile share the rows out).  The loads of a batch
+// are in flight together; this runs before the accumulator is waited for,
+// i.e. beside the stream of the weights.
+__device__ __forceinline__ void add_adapter_terms(const GroupedArgs& p, int piece, int S, int row,
+                                                  int end, int x, float (&v)[32]) {
+  const bool in = x < p.wide;
+#pragma unroll
+  for (int b = 0; b < 4; ++b) {
+    const int r0 = row + 8 * b;
+    if (r0 >= end || (r0 >> 3) % S != piece) continue;
+    const uint16_t* u[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const uint32_t id = r0 + j < end ? static_cast<uint32_t>(__ldg(p.ids + r0 + j)) : 0xFFFFFFFFu;
+      u[j] = in && id < static_cast<uint32_t>(p.adapters)
+                 ? p.up + id * p.group_stride_up + static_cast<int64_t>(x) * p.ld_up
+                 : nullptr;
     }
-    v[j] += sum;
+    for (int r = 0; r < p.rank; r += 8) {
+      uint4 q[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) q[j] = u[j] ? ld_global_nc_v4(u[j] + r) : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        if (u[j] == nullptr) continue;   // (H has no row there)
+        const float* h = p.h + static_cast<int64_t>(r0 + j) * p.rank + r;
+        const float4 h0 = __ldcg(reinterpret_cast<const float4*>(h));
+        const float4 h1 = __ldcg(reinterpret_cast<const float4*>(h + 4));
+        float s = v[8 * b + j];
+        s = fmaf(__uint_as_float(q[j].x << 16), h0.x, s);
+        s = fmaf(__uint_as_float(q[j].x & 0xFFFF0000u), h0.y, s);
+        s = fmaf(__uint_as_float(q[j].y << 16), h0.z, s);
+        s = fmaf(__uint_as_float(q[j].y & 0xFFFF0000u), h0.w, s);
+        s = fmaf(__uint_as_float(q[j].z << 16), h1.x, s);
+        s = fmaf(__uint_as_float(q[j].z & 0xFFFF0000u), h1.y, s);
+        s = fmaf(__uint_as_float(q[j].w << 16), h1.z, s);
+        s = fmaf(__uint_as_float(q[j].w & 0xFFFF0000u), h1.w, s);
+        v[8 * b + j] = s;
+      }
+    }
   }
 }
 
@@ -591,16 +656,19 @@ __global__ void __launch_bounds__(C::kThreads, 1)
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);
   uint64_t* full_bar = bars;                       // [kStages] TMA -> MMA
-  uint64_t* empty_bar = bars + C::kStages;         // [kStages] MMA -> TMA, fixing warps
+  uint64_t* empty_bar = bars + C::kStages;         // [kStages] MMA -> TMA
   uint64_t* accf_bar = bars + 2 * C::kStages;      // [2] MMA -> epilogue
   uint64_t* acce_bar = accf_bar + C::kAccBufs;     // [2] epilogue -> MMA
   uint64_t* drain_bar = acce_bar + C::kAccBufs;
   uint64_t* fix_bar = drain_bar + 1;               // [kStages] fixing warps -> MMA
-  uint64_t* tail_bar = fix_bar + C::kStages;       // [kStages] TMA -> fixing warp (wgrad)
+  uint64_t* tail_bar = fix_bar + C::kStages;       // [kStages] TMA -> this CTA's fixing warps
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::OFF_MISC);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::OFF_MISC + 4);
   volatile int* join = reinterpret_cast<volatile int*>(smem + C::OFF_MISC + 8);
   volatile int* go = reinterpret_cast<volatile int*>(smem + C::OFF_MISC + 16);   // [4]
+  // Marked tiles: entry n % 16 is n + 1 for the unit's n-th tile (the fixing
+  // warps are never 16 tiles ahead: the ring is shorter).
+  volatile int* marked = reinterpret_cast<volatile int*>(smem + C::OFF_MISC + 32);
 
   const int warp = threadIdx.x >> 5;
   const int lane = static_cast<int>(threadIdx.x & 31);
@@ -622,6 +690,8 @@ __global__ void __launch_bounds__(C::kThreads, 1)
     }
     mbar_init(drain_bar, 1);
     *abort_flag = 0;
+    if constexpr (C::kExt)
+      for (int i = 0; i < 16; ++i) marked[i] = 0;
     fence_barrier_init();
   }
   if (warp == 0 && lane == 0) {
@@ -640,7 +710,11 @@ __global__ void __launch_bounds__(C::kThreads, 1)
   if constexpr (C::kCtaGroup == 2) cluster_sync();
   tc_fence_after_sync();
   const uint32_t tmem_base = *tmem_slot;
-  griddep_wait();
+  // The few-row adapter product streams its weights beside the kernel that
+  // computes H, which started only when its own inputs (this one's A, B and
+  // ids among them) were there: only the epilogue, which reads H and writes,
+  // waits for it.
+  if (!(C::kMode == kAdapter && C::kSplit) || warp >= C::kEpiWarp0) griddep_wait();
 
   const WaitGuard guard{p.status, abort_flag, p.timeout_ns};
   const int unit = blockIdx.x / C::kCtaGroup;
@@ -682,6 +756,11 @@ __global__ void __launch_bounds__(C::kThreads, 1)
     auto wait_slot = [&]() -> bool {
       return mbar_try_wait(empty0 + 8u * stage, phase ^ 1u) ||
              mbar_wait(&empty_bar[stage], phase ^ 1u, guard, kSiteGrEmpty);
+    };
+    auto note_tail = [&]() {
+      tail_parity = (tailed >> stage) & 1u ? tail_parity ^ (1u << stage)
+                                           : tail_parity & ~(1u << stage);
+      tailed |= 1u << stage;
     };
     auto next_slot = [&]() {
       issued |= 1u << stage;
@@ -730,9 +809,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
                 for (int c = 0; c < crows / 64; ++c)
                   tma_load_2d(dC + 8192 * c, &tmC.box[0], tb, crow0 + 64 * c, w.base + kx, pol);
             }
-            tail_parity = (tailed >> stage) & 1u ? tail_parity ^ (1u << stage)
-                                                 : tail_parity & ~(1u << stage);
-            tailed |= 1u << stage;
+            note_tail();
             next_slot();
             continue;
           }
@@ -786,6 +863,8 @@ __global__ void __launch_bounds__(C::kThreads, 1)
         for (int id = next_adapter(ids, -1, p.adapters); id >= 0 && ok;
              id = next_adapter(ids, id, p.adapters)) {
           if (lane == 0) {
+            // Like a ragged stage's, an adapter stage's load completes in each
+            // CTA for its own fixing warps.
             // Stages: rank columns 0.., 64.., ... of hi, then the same of lo.
             const int per = (p.rank + 63) / 64 * 64;
             for (int r = 0; r < 2 * per; r += 64) {
@@ -793,9 +872,11 @@ __global__ void __launch_bounds__(C::kThreads, 1)
                 ok = 0;
                 break;
               }
-              if (leader) mbar_arrive_expect_tx(&full_bar[stage], 2 * C::W_BYTES);
-              tma_load_3d_pair(sW + stage * C::W_BYTES, &tmUp, full_dst0 + 8u * stage,
-                               r < per ? r : r - per, wx, id, pol);
+              if (leader) mbar_arrive(&full_bar[stage]);
+              mbar_arrive_expect_tx(&tail_bar[stage], C::W_BYTES);
+              tma_load_3d(sW + stage * C::W_BYTES, &tmUp, smem_addr(&tail_bar[stage]),
+                          r < per ? r : r - per, wx, id, pol);
+              note_tail();
               next_slot();
             }
           }
@@ -970,7 +1051,8 @@ __global__ void __launch_bounds__(C::kThreads, 1)
       uint32_t pos = 0;            // ring slots used so far
       uint32_t tail_use = 0;       // parity of each stage's next tail
       int ok = 1;
-      for (int u = unit; u < num_items && ok; u += num_units) {
+      int count = 0;               // tiles of this unit so far
+      for (int u = unit; u < num_items && ok; u += num_units, ++count) {
         walk.find(p, lane, u / S, u % S, S, w);
         if constexpr (C::kMode == kGroupedWgrad) {
           const int rest = w.len & 63;
@@ -1005,31 +1087,61 @@ __global__ void __launch_bounds__(C::kThreads, 1)
           const int per = (p.rank + 63) / 64 * 64;
           const int crows = w.ncols / C::kCtaGroup;
           const int r0 = static_cast<int>(rank) * crows;   // this CTA's rows of the tile
+          const bool mixed = mixed_adapters(ids, w.rows, lane, p.adapters);
           for (int id = next_adapter(ids, -1, p.adapters); id >= 0 && ok;
                id = next_adapter(ids, id, p.adapters)) {
             for (int r = 0; r < 2 * per; r += 64, ++pos) {
               const int stage = static_cast<int>(pos % C::kStages);
-              const uint32_t phase = (pos / C::kStages) & 1u;
-              if (lane == 0)
-                ok = mbar_try_wait(smem_addr(&empty_bar[stage]), phase ^ 1u) ||
-                     mbar_wait(&empty_bar[stage], phase ^ 1u, guard, kSiteGrFixIn);
-              ok = __shfl_sync(0xFFFFFFFFu, ok, 0);
-              if (!ok) break;
               const int c0 = r < per ? r : r - per;
               const uint16_t* h = r < per ? p.h_hi : p.h_lo;
               const int cw = min(64, p.rank - c0);   // columns of this stage (rest: zeros)
-              // 16-byte piece q of row i: lanes take 4 rows x 8 pieces at a time.
+              // 16-byte piece q of row i: a warp takes 4 rows x 8 pieces at a
+              // time, eight such at once; the first eight before it waits.
               const int q = lane & 7;
-              for (int i0 = fw * 4; i0 < crows; i0 += 4 * C::kFixWarps) {
-                const int i = i0 + (lane >> 3);
-                const int row = r0 + i;              // row of the tile
-                uint4 v = make_uint4(0u, 0u, 0u, 0u);
-                if (row < w.rows && p.ids[w.row0 + row] == id && 8 * q < cw)
-                  v = *reinterpret_cast<const uint4*>(
-                      h + static_cast<int64_t>(w.row0 + row) * p.rank + c0 + 8 * q);
-                st_shared_v4(sC + stage * C::C_BYTES + 128 * i +
-                                 ((static_cast<uint32_t>(q) ^ (static_cast<uint32_t>(i) & 7u)) << 4),
-                             v.x, v.y, v.z, v.w);
+              constexpr int kBatch = 8;
+              uint4 v[kBatch];
+              auto read = [&](int i0) {
+#pragma unroll
+                for (int t = 0; t < kBatch; ++t) {
+                  const int i = i0 + 4 * (fw + C::kFixWarps * t) + (lane >> 3);
+                  const int row = r0 + i;            // row of the tile
+                  v[t] = make_uint4(0u, 0u, 0u, 0u);
+                  if (i < crows && row < w.rows && 8 * q < cw && p.ids[w.row0 + row] == id)
+                    v[t] = *reinterpret_cast<const uint4*>(
+                        h + static_cast<int64_t>(w.row0 + row) * p.rank + c0 + 8 * q);
+                }
+              };
+              read(0);
+              const uint32_t par = (tail_use >> stage) & 1u;
+              tail_use ^= 1u << stage;
+              if (lane == 0)
+                ok = mbar_try_wait(smem_addr(&tail_bar[stage]), par) ||
+                     mbar_wait(&tail_bar[stage], par, guard, kSiteGrFixIn);
+              ok = __shfl_sync(0xFFFFFFFFu, ok, 0);
+              if (!ok) break;
+              for (int i0 = 0; i0 < crows; i0 += 4 * kBatch * C::kFixWarps) {
+                if (i0 > 0) read(i0);
+#pragma unroll
+                for (int t = 0; t < kBatch; ++t) {
+                  const int i = i0 + 4 * (fw + C::kFixWarps * t) + (lane >> 3);
+                  if (i < crows)
+                    st_shared_v4(
+                        sC + stage * C::C_BYTES + 128 * i +
+                            ((static_cast<uint32_t>(q) ^ (static_cast<uint32_t>(i) & 7u)) << 4),
+                        v[t].x, v[t].y, v[t].z, v[t].w);
+                }
+              }
+              if (mixed) {
+                const uint32_t half = sW + stage * C::W_BYTES + fw * (C::W_BYTES / 2);
+                for (int j = lane; j < C::W_BYTES / 32; j += 32) {
+                  const uint4 v = ld_shared_v4(half + 16 * j);
+                  const uint4 f = make_uint4(finite_bf16x2(v.x), finite_bf16x2(v.y),
+                                             finite_bf16x2(v.z), finite_bf16x2(v.w));
+                  if (f.x != v.x || f.y != v.y || f.z != v.z || f.w != v.w) {
+                    st_shared_v4(half + 16 * j, f.x, f.y, f.z, f.w);
+                    marked[count & 15] = count + 1;
+                  }
+                }
               }
               fence_proxy_async_smem();
               __syncwarp();
@@ -1095,7 +1207,8 @@ __global__ void __launch_bounds__(C::kThreads, 1)
       }
     };
     bool ok = true;
-    for (int u = unit; u < num_items && ok; u += num_units) {
+    int count = 0;                             // tiles of this unit so far
+    for (int u = unit; u < num_items && ok; u += num_units, ++count) {
       walk.find(p, lane, u / S, u % S, S, w);
       const int chunks = grouped_chunks<C>(w.nk);
       const int x = w.wide0 + static_cast<int>(rank) * 128 + slab * 32 + lane;
@@ -1112,7 +1225,11 @@ __global__ void __launch_bounds__(C::kThreads, 1)
         constexpr int kOwn = C::kTileN / 64;
         float m[kOwn][32];
 #pragma unroll
-        for (int q = 0; q < kOwn; ++q) grouped_zero(m[q]);
+        for (int q = 0; q < kOwn; ++q) {
+          grouped_zero(m[q]);
+          if constexpr (C::kMode == kAdapter)
+            add_adapter_terms(p, w.piece, S, w.row0 + 32 * (half + 2 * q), end, x, m[q]);
+        }
         for (int c = 0; c < chunks; ++c) {
           if (!acc_ready()) {
             ok = false;
@@ -1127,11 +1244,6 @@ __global__ void __launch_bounds__(C::kThreads, 1)
           hand_back();
         }
         if (!ok) break;
-        if constexpr (C::kMode == kAdapter) {
-#pragma unroll
-          for (int q = 0; q < kOwn; ++q)
-            add_adapter_terms<C>(p, w, w.row0 + 32 * (half + 2 * q), end, x, S, m[q]);
-        }
         if (S > 1) {
           // Publish the piece's partial; the last of the tile's pieces adds
           // them all in piece order.
@@ -1195,6 +1307,18 @@ __global__ void __launch_bounds__(C::kThreads, 1)
                           ? p.epi.bias[static_cast<int64_t>(w.g) * p.wide + xb]
                           : 0.0f;
           }
+          if (C::kExt && marked[count & 15] == count + 1) {
+            for (int q = half; q < blocks; q += 2) {
+              const int row = w.row0 + 32 * q;
+              float v[32];
+              grouped_read<false>(t_slab + static_cast<uint32_t>(acc * C::kTileN + 32 * q), v);
+              add_marked_terms(p, row, end, x, v);
+              grouped_epilogue(p.epi, b, v);
+              grouped_store<C>(p, d0, row, end, x, v);
+            }
+            hand_back();
+            continue;
+          }
           const int x0 = x - lane - 32 * (slab & 1);   // first element of the box
           for (int q = half; q < blocks; q += 2) {
             const int row = w.row0 + 32 * q;
@@ -1254,9 +1378,13 @@ __global__ void __launch_bounds__(C::kThreads, 1)
             hand_back();
           }
           if (!ok) break;
+          const bool mark = C::kExt && marked[count & 15] == count + 1;
 #pragma unroll
           for (int q = 0; q < kOwn; ++q)
-            if (half + 2 * q < blocks) finish(half + 2 * q, m[q]);
+            if (half + 2 * q < blocks) {
+              if (mark) add_marked_terms(p, w.row0 + 32 * (half + 2 * q), end, x, m[q]);
+              finish(half + 2 * q, m[q]);
+            }
         }
       }
     }

@@ -197,6 +197,9 @@ int skinny_splits(int64_t N, int64_t K, int split_k, int num_sms, int* per_split
 // Workspace of tg_group_rows (0 where one CTA does it).
 size_t group_rows_workspace_bytes(int64_t n, int64_t groups);
 
+// Workspace of gemm_bf16_lora.
+size_t lora_workspace_bytes(int64_t M, int64_t rank);
+
 // D = epilogue(0) when K == 0.
 int launch_fill_epilogue(void* D, int64_t ldd, int64_t M, int64_t N, int d_dtype, const Epi& epi,
                          cudaStream_t stream);

@@ -353,6 +353,31 @@ int gemm_bf16_grouped_wgrad(const void* G, int64_t ldg, const void* A, int64_t l
                             int64_t group_stride_d, int64_t N, int64_t K, int d_dtype,
                             unsigned flags, void* cuda_stream);
 
+/*
+ * gemm_bf16_lora -- a shared projection with a low-rank adapter per row:
+ *   D[i, :] = epi(A[i, :] * B^T + s[id] * (A[i, :] * down[id]^T) * up[id]^T),
+ * id = ids[i]; rows whose id is outside [0, adapters) have no second term.
+ * Rows of different adapters may come in any order (decoding: one row a
+ * request; prompts: a request's rows together, which is the fast order).
+ *   A, B, D : as for gemm_bf16_ex.
+ *   ids     : device, int32 [M].
+ *   down    : device, bf16 [adapters][rank][K], strides ld_down, stride_down.
+ *   up      : device, bf16 [adapters][N][rank], strides ld_up, stride_up (the
+ *             slice strides are not read for one adapter).
+ *   scales  : device, f32 [adapters], or NULL for 1.
+ *   rank    : a multiple of 8, at most TG_MAX_RANK (smaller adapters are
+ *             padded with zeros); otherwise TG_ERR_UNSUPPORTED.  flags: 0.
+ * The rank values a row between the two adapter products are kept in f32 (M
+ * <= 128) or as two bf16 terms (16 significant bits) in the stream's
+ * workspace (TG_CALL_GEMM_BF16_LORA); both terms of D meet in f32.
+ */
+enum { TG_MAX_RANK = 256 };
+int gemm_bf16_lora(const void* A, int64_t lda, const void* B, int64_t ldb, const int32_t* ids,
+                   const void* down, int64_t ld_down, int64_t stride_down, const void* up,
+                   int64_t ld_up, int64_t stride_up, const float* scales, int64_t adapters,
+                   int64_t rank, void* D, int64_t ldd, int64_t M, int64_t N, int64_t K,
+                   int d_dtype, const tg_epilogue* epi, unsigned flags, void* cuda_stream);
+
 /* tg_gemm_tail_split -- the number of K pieces (1: none) into which
  * gemm_bf16 cuts each tile for this shape on the current device (flags: 0 or
  * TG_FLAG_CTA_PAIR), for operands in the current device's memory (a stream
@@ -378,7 +403,8 @@ enum {
   TG_CALL_GEMM_BF16_SKINNY = 4, /* gemm_bf16_skinny                            */
   TG_CALL_GEMM_BF16_GATHER = 5, /* gemm_bf16_gather (M = gathered rows), and the
                                    grouped products with a row_idx             */
-  TG_CALL_GROUP_ROWS = 6        /* tg_group_rows (M = n, N = groups, K = 1)    */
+  TG_CALL_GROUP_ROWS = 6,       /* tg_group_rows (M = n, N = groups, K = 1)    */
+  TG_CALL_GEMM_BF16_LORA = 7    /* gemm_bf16_lora (N = rank, K = 1)            */
 };
 
 /*
