@@ -2,10 +2,12 @@
 //
 //   D[i, :] = epi( A[i, :] * B^T + s[id_i] * (A[i, :] * down[id_i]^T) * up[id_i]^T )
 //
-// Two launches.  lora_down_kernel computes H[i, :] = s[id_i] * A[i, :] *
-// down[id_i]^T (rank values a row); the grouped kernel (kAdapter) runs the
-// shared product and adds H[i, :] * up[id_i]^T inside it, so that D is
-// written once and the second term costs no pass of its own.
+// H[i, :] = s[id_i] * A[i, :] * down[id_i]^T (rank values a row) comes first; the
+// grouped kernel (kAdapter) then runs the shared product and adds H[i, :] *
+// up[id_i]^T inside it, so that D is written once and the second term costs no
+// pass of its own.  For many rows H is computed by the same tcgen05 kernel
+// (kAdapterDown) in tiles of 64 rows; few rows, and tiles with more than
+// kDownAdapters adapters, go through lora_down_kernel.
 //
 // lora_down_kernel.  2 M K rank flop against (M + adapters * rank) K values
 // read: at most a few tens of flop per byte, so reading A and `down` bounds it
@@ -16,14 +18,11 @@
 // each thread loads 16 contiguous bytes of a row (8 values, two MMAs' worth)
 // straight into its fragments: no shared memory, no transposition.
 //
-// A block takes kTok consecutive rows and a slice of K: its warps share the
+// A block takes 8 consecutive rows and a slice of K: its warps share the
 // slice, the CTAs of the cluster share K, and the partial sums meet in
-// (distributed) shared memory in a fixed order.  A tile's rows may belong to
-// several adapters: each distinct one is computed for the whole tile and kept
-// for its own rows (prompts have one or two to a tile; with 8-row tiles, the
-// decoding case, the adapters of a tile run in different blocks).
-#include <cfloat>
-
+// (distributed) shared memory in a fixed order.  The rows' adapters are
+// computed for the whole tile and kept for their own rows, each in a block of
+// its own (blockIdx.y).
 #include "grouped_launch.cuh"
 
 namespace tg {
@@ -41,6 +40,7 @@ struct DownArgs {
   const float* scales;   // may be null: 1
   int adapters, rank;
   int k_per_cta;         // multiple of 32 * kDownWarps
+  bool leave_few;        // kAdapterDown does the 64-row tiles of few adapters
   float* h;              // [M][rank], or null
   uint16_t* hi;          // [M][rank]: bf16 terms of the same
   uint16_t* lo;
@@ -71,13 +71,11 @@ __device__ __forceinline__ float ld_dsmem(uint32_t addr) {
   return v;
 }
 
-// kTok rows a tile; kRt 16-row tiles of `down` at a time (rank > 16 kRt: in
-// several passes over the rows).
-template <int kTok, int kRt>
+// kRt 16-row tiles of `down` at a time (rank > 16 kRt: in several passes).
+template <int kRt>
 __global__ void __launch_bounds__(32 * kDownWarps) lora_down_kernel(const DownArgs p) {
-  constexpr int kNt = kTok / 8;
+  constexpr int kTok = 8;
   constexpr int kElems = 16 * kRt * kTok;
-  constexpr int kPer = (kTok + 31) / 32;
   extern __shared__ float part[];      // [warp][kElems], then the CTA's sum in [0]
   griddep_wait();
   // What the next kernel reads early (A, B, ids) was there before this one.
@@ -89,10 +87,16 @@ __global__ void __launch_bounds__(32 * kDownWarps) lora_down_kernel(const DownAr
   const int crank = static_cast<int>(blockIdx.z);     // one cluster spans z
   const int row0 = static_cast<int>(blockIdx.x) * kTok;
   const int rows = min(kTok, p.M - row0);
-  uint32_t ids[kPer];
+  if (p.leave_few) {
+    uint32_t all[2];
 #pragma unroll
-  for (int i = 0; i < kPer; ++i)
-    ids[i] = lane + 32 * i < rows ? static_cast<uint32_t>(p.ids[row0 + lane + 32 * i]) : 0xFFFFFFFFu;
+    for (int i = 0; i < 2; ++i) {
+      const int r = row0 / 64 * 64 + lane + 32 * i;
+      all[i] = r < p.M ? static_cast<uint32_t>(p.ids[r]) : 0xFFFFFFFFu;
+    }
+    if (few_adapters(all, p.adapters)) return;   // every CTA of the cluster
+  }
+  uint32_t ids[1] = {lane < rows ? static_cast<uint32_t>(p.ids[row0 + lane]) : 0xFFFFFFFFu};
   const int kbeg = crank * p.k_per_cta;
   const int kend = min(p.K, kbeg + p.k_per_cta);
   // Adapter number blockIdx.y, + gridDim.y, ... of the tile (the same in every
@@ -103,17 +107,15 @@ __global__ void __launch_bounds__(32 * kDownWarps) lora_down_kernel(const DownAr
     const uint16_t* down = p.down + id * p.stride_down;
     const float scale = p.scales ? p.scales[id] : 1.0f;
     for (int r0 = 0; r0 < p.rank; r0 += 16 * kRt) {
-      float acc[kRt][kNt][4];
+      float acc[kRt][4];
 #pragma unroll
       for (int t = 0; t < kRt; ++t)
 #pragma unroll
-        for (int n = 0; n < kNt; ++n)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) acc[t][n][e] = 0.0f;
+        for (int e = 0; e < 4; ++e) acc[t][e] = 0.0f;
 #pragma unroll 2
       for (int k = kbeg + 32 * warp; k < kend; k += 32 * kDownWarps) {
         const int kk = k + 8 * q;
-        uint4 a[kRt][2], b[kNt];
+        uint4 a[kRt][2];
 #pragma unroll
         for (int t = 0; t < kRt; ++t)
 #pragma unroll
@@ -121,29 +123,21 @@ __global__ void __launch_bounds__(32 * kDownWarps) lora_down_kernel(const DownAr
             const int r = r0 + 16 * t + 8 * h + g;
             a[t][h] = r < p.rank ? load8(down + r * p.ld_down, kk, kend) : make_uint4(0u, 0u, 0u, 0u);
           }
+        const uint4 b = g < rows ? load8(p.A + static_cast<int64_t>(row0 + g) * p.lda, kk, kend)
+                                 : make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
-        for (int n = 0; n < kNt; ++n) {
-          const int i = 8 * n + g;
-          b[n] = i < rows ? load8(p.A + static_cast<int64_t>(row0 + i) * p.lda, kk, kend)
-                          : make_uint4(0u, 0u, 0u, 0u);
+        for (int t = 0; t < kRt; ++t) {
+          mma_m16n8k16(acc[t], a[t][0].x, a[t][1].x, a[t][0].y, a[t][1].y, b.x, b.y);
+          mma_m16n8k16(acc[t], a[t][0].z, a[t][1].z, a[t][0].w, a[t][1].w, b.z, b.w);
         }
-#pragma unroll
-        for (int t = 0; t < kRt; ++t)
-#pragma unroll
-          for (int n = 0; n < kNt; ++n) {
-            mma_m16n8k16(acc[t][n], a[t][0].x, a[t][1].x, a[t][0].y, a[t][1].y, b[n].x, b[n].y);
-            mma_m16n8k16(acc[t][n], a[t][0].z, a[t][1].z, a[t][0].w, a[t][1].w, b[n].z, b[n].w);
-          }
       }
       // [down row][row of A]: c0, c1 at (g, 2q), (g, 2q + 1); c2, c3 8 rows on.
       float* mine = part + warp * kElems;
 #pragma unroll
       for (int t = 0; t < kRt; ++t)
 #pragma unroll
-        for (int n = 0; n < kNt; ++n)
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            mine[(16 * t + g + 8 * (e >> 1)) * kTok + 8 * n + 2 * q + (e & 1)] = acc[t][n][e];
+        for (int e = 0; e < 4; ++e)
+          mine[(16 * t + g + 8 * (e >> 1)) * kTok + 2 * q + (e & 1)] = acc[t][e];
       __syncthreads();
       for (int e = threadIdx.x; e < kElems; e += 32 * kDownWarps) {
         float s = part[e];
@@ -170,16 +164,10 @@ __global__ void __launch_bounds__(32 * kDownWarps) lora_down_kernel(const DownAr
           }
           s *= scale;
           const int64_t o = static_cast<int64_t>(row0 + i) * p.rank + r;
-          if (p.h != nullptr) {
+          if (p.h != nullptr)
             p.h[o] = s;
-          } else {
-            const uint32_t hi = pack_bf16x2(s, s) & 0xFFFFu;
-            const float rest = s - __uint_as_float(hi << 16);
-            p.hi[o] = static_cast<uint16_t>(hi);
-            // What is infinite or NaN in hi is in hi alone.
-            p.lo[o] = static_cast<uint16_t>(
-                pack_bf16x2(fabsf(rest) <= FLT_MAX ? rest : 0.0f, 0.0f) & 0xFFFFu);
-          }
+          else
+            split_bf16(s, p.hi[o], p.lo[o]);
         }
       }
       // The partial sums are free again once every CTA has read them.
@@ -191,10 +179,11 @@ __global__ void __launch_bounds__(32 * kDownWarps) lora_down_kernel(const DownAr
   }
 }
 
-template <int kTok, int kRt>
+template <int kRt>
 int launch_down(DownArgs a, cudaStream_t stream, DeviceCtx* ctx) {
   static std::atomic<int> prepared[64];
-  auto kern = lora_down_kernel<kTok, kRt>;
+  auto kern = lora_down_kernel<kRt>;
+  constexpr int kTok = 8;
   constexpr int kSmem = kDownWarps * 16 * kRt * kTok * 4;
   if (prepared[ctx->device].load(std::memory_order_acquire) == 0) {
     const cudaError_t e =
@@ -206,7 +195,7 @@ int launch_down(DownArgs a, cudaStream_t stream, DeviceCtx* ctx) {
   // K over a cluster of up to 8 CTAs, while that adds blocks the SMs have
   // room for and leaves a CTA at least one step per warp.
   int c = 1;
-  const int y = kTok < 8 ? kTok : kTok == 8 ? (a.M < 8 ? a.M : 8) : 1;
+  const int y = a.M < kTok ? a.M : kTok;
   while (c < 8 && tiles * y * c < 2 * ctx->num_sms && a.K > 32 * kDownWarps * c) c *= 2;
   a.k_per_cta = ceil_div_i(ceil_div_i(a.K, c), 32 * kDownWarps) * 32 * kDownWarps;
   cudaLaunchConfig_t cfg{};
@@ -232,6 +221,9 @@ bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) ==
 // Rows up to which the weights' stream bounds the product: single CTAs with a
 // split contraction and the adapter term in the epilogue.
 constexpr int kLoraFewRows = 128;
+// Rows up to which lora_down_kernel alone computes H (it reads `down` once per
+// 8 rows).
+constexpr int kLoraDownRows = 1024;
 
 }  // namespace
 
@@ -305,40 +297,49 @@ extern "C" int gemm_bf16_lora(const void* A, int64_t lda, const void* B, int64_t
   d.h = few ? static_cast<float*>(ws) : nullptr;
   d.hi = few ? nullptr : static_cast<uint16_t*>(ws);
   d.lo = few ? nullptr : d.hi + M * rank;
-  if (few)
-    rc = rank <= 16   ? launch_down<8, 1>(d, stream, ctx)
-         : rank <= 32 ? launch_down<8, 2>(d, stream, ctx)
-                      : launch_down<8, 4>(d, stream, ctx);
-  else
-    rc = rank <= 16   ? launch_down<64, 1>(d, stream, ctx)
-         : rank <= 32 ? launch_down<64, 2>(d, stream, ctx)
-                      : launch_down<64, 4>(d, stream, ctx);
-  if (rc != TG_OK) return rc;
   GroupedArgs a = grouped_args(ctx);
   a.M = static_cast<int>(M);
-  a.wide = static_cast<int>(N);
   a.num_k_blocks = ceil_div_i(K, 64);
-  a.D = D;
-  a.ldd = ldd;
-  a.epi = e;
   a.ids = ids;
   a.adapters = static_cast<int>(adapters);
   a.rank = static_cast<int>(rank);
   a.h = d.h;
   a.h_hi = d.hi;
   a.h_lo = d.lo;
-  a.up = static_cast<const uint16_t*>(up);
-  a.ld_up = ld_up;
-  a.group_stride_up = adapters > 1 ? stride_up : 0;
   GroupedOperands o{};
-  o.wide = B;
-  o.wide_ld = ldb;
-  o.wide_rows = N;
   o.wide_slices = 1;
-  o.wide_slice_stride = ldb * N;
   o.cols = A;
   o.cols_ld = lda;
   o.k = K;
+  d.leave_few = M > kLoraDownRows;
+  rc = rank <= 16   ? launch_down<1>(d, stream, ctx)
+       : rank <= 32 ? launch_down<2>(d, stream, ctx)
+                    : launch_down<4>(d, stream, ctx);
+  if (rc != TG_OK) return rc;
+  if (d.leave_few) {
+    GroupedArgs h = a;
+    h.wide = static_cast<int>(rank);
+    h.scales = scales;
+    GroupedOperands od = o;
+    od.wide = down;
+    od.wide_ld = ld_down;
+    od.wide_rows = rank;
+    od.wide_slices = adapters;
+    od.wide_slice_stride = adapters > 1 ? stride_down : ld_down * rank;
+    rc = launch_grouped<GroupedCfg<kAdapterDown, 1, 64, 8, true>>(od, h, stream, ctx);
+    if (rc != TG_OK) return rc;
+  }
+  a.wide = static_cast<int>(N);
+  a.D = D;
+  a.ldd = ldd;
+  a.epi = e;
+  a.up = static_cast<const uint16_t*>(up);
+  a.ld_up = ld_up;
+  a.group_stride_up = adapters > 1 ? stride_up : 0;
+  o.wide = B;
+  o.wide_ld = ldb;
+  o.wide_rows = N;
+  o.wide_slice_stride = ldb * N;
   o.up = up;
   o.up_ld = ld_up;
   o.up_slices = adapters;

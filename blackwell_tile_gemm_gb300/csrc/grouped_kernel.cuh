@@ -1,10 +1,11 @@
 // Products whose weights change with the row: one persistent, warp-specialised
-// tcgen05 kernel for four of them, all bf16 with f32 accumulation.
+// tcgen05 kernel for five of them, all bf16 with f32 accumulation.
 //
 //   kGroupedForward  D[i, :] = A[i, :] * B[g]^T      rows i of group g
 //   kGroupedDgrad    dA[i, :] = G[i, :] * B[g]        (contraction over N)
 //   kGroupedWgrad    dB[g] = G[rows of g]^T * A[rows of g]
 //   kAdapter         D[i, :] = A[i, :] * B^T + H[i, :] * up[id_i]^T
+//   kAdapterDown     H[i, :] = s * A[i, :] * down[id_i]^T
 //
 // Group g owns the rows offsets[g] <= i < offsets[g+1]; the offsets live on
 // the device, so the host never learns the sizes and the tile list is made
@@ -36,9 +37,10 @@
 // Adapters: H[i] = scale * A[i] * down[id_i]^T was computed before and split
 // into two bf16 terms (hi + lo keep 16 bits of it, so the product with
 // up[id] is as exact as the base product).  After the tile's K stages each
-// adapter that occurs among the tile's rows adds ceil(rank / 64) * 2 stages:
-// up[id] by TMA, H written by the fixing warps with zeros in the rows of
-// other adapters.  The base product and every adapter's term meet in one
+// adapter that occurs among the tile's rows adds ceil(rank / 64) * 2 stages of
+// up[id] and H.  Where all rows of the tile have one adapter, TMA loads both;
+// else the fixing warps write H with zeros in the rows of other adapters.
+// The base product and every adapter's term meet in one
 // accumulator: D is written once.  A zero row times an infinite or NaN
 // weight would still be NaN, so where a tile's rows differ in their adapter
 // the fixing warps take such weights out of up[id] and mark the tile; the
@@ -63,7 +65,7 @@
 
 namespace tg {
 
-enum : int { kGroupedForward = 0, kGroupedDgrad = 1, kGroupedWgrad = 2, kAdapter = 3 };
+enum : int { kGroupedForward = 0, kGroupedDgrad = 1, kGroupedWgrad = 2, kAdapter = 3, kAdapterDown = 4 };
 
 enum : uint32_t {
   kSiteGrEmpty = 31,
@@ -92,8 +94,9 @@ struct GroupedArgs {
   const int* ids;          // [M]
   int adapters, rank;
   const float* h;          // [M][rank] f32 (few rows)
-  const uint16_t* h_hi;    // [M][rank] bf16 (MMA form)
-  const uint16_t* h_lo;
+  uint16_t* h_hi;          // [M][rank] bf16 (MMA form); kAdapterDown writes them
+  uint16_t* h_lo;
+  const float* scales;     // kAdapterDown: [adapters], or null for 1
   const uint16_t* up;
   int64_t ld_up, group_stride_up;
   // split contraction
@@ -175,6 +178,7 @@ struct GroupedCfg {
 constexpr int kColBoxes = 8;
 struct ColumnMaps {
   CUtensorMap box[kColBoxes];
+  CUtensorMap h[2];   // adapters: the two terms of H, boxes of 128 rows
 };
 
 // One work item.
@@ -305,7 +309,10 @@ struct GroupWalk {
       w.ks = 1;
     } else {
       // The group's rows in nct tiles of equal size (a multiple of kColStep).
-      const int size = ((r1 - r0 + nct - 1) / nct + C::kColStep - 1) / C::kColStep * C::kColStep;
+      const int size =
+          C::kMode == kAdapterDown
+              ? C::kTileN
+              : ((r1 - r0 + nct - 1) / nct + C::kColStep - 1) / C::kColStep * C::kColStep;
       w.row0 = r0 + ct * size;
       w.rows = min(size, r1 - w.row0);
       w.ncols = (w.rows + C::kColStep - 1) / C::kColStep * C::kColStep;
@@ -385,6 +392,30 @@ __device__ __forceinline__ bool mixed_adapters(const uint32_t (&ids)[kPer], int 
       hi = max(hi, min(ids[i], adapters));
     }
   return __reduce_min_sync(0xFFFFFFFFu, lo) != __reduce_max_sync(0xFFFFFFFFu, hi);
+}
+
+// kAdapterDown leaves tiles of more than kDownAdapters adapters to
+// lora_down_kernel, which spreads them over more blocks: here they would run
+// one after the other.
+constexpr int kDownAdapters = 2;
+template <int kPer>
+__device__ __forceinline__ bool few_adapters(const uint32_t (&ids)[kPer], uint32_t adapters) {
+  int id = -1;
+  for (int n = 0; n <= kDownAdapters; ++n) {
+    id = next_adapter(ids, id, adapters);
+    if (id < 0) return true;
+  }
+  return false;
+}
+
+// x as two bf16 terms; what is infinite or NaN in hi is in hi alone.
+__device__ __forceinline__ void split_bf16(float x, uint16_t& hi, uint16_t& lo) {
+  const uint32_t h = pack_bf16x2(x, x) & 0xFFFFu;
+  const float rest = x - __uint_as_float(h << 16);
+  hi = static_cast<uint16_t>(h);
+  lo = static_cast<uint16_t>(pack_bf16x2(fabsf(rest) < __uint_as_float(0x7F800000u) ? rest : 0.0f,
+                                         0.0f) &
+                             0xFFFFu);
 }
 
 // A word of two bf16 values without its infinite and NaN ones.
@@ -778,6 +809,30 @@ __global__ void __launch_bounds__(C::kThreads, 1)
       // MN-major: both of a box pair's 64-element chunks lie inside the row.
       const bool w_chunks = C::kWideMn && wx + 128 <= p.wide;
       const bool c_chunks = C::kColMn && crows == 128 && crow0 + 128 <= p.cols;
+      if constexpr (C::kMode == kAdapterDown) {
+        uint32_t ids[C::kTileN / 32];
+        load_tile_ids<C>(p, w, lane, ids);
+        if (!few_adapters(ids, p.adapters)) continue;
+        for (int id = next_adapter(ids, -1, p.adapters); id >= 0 && ok;
+             id = next_adapter(ids, id, p.adapters)) {
+          if (lane == 0) {
+            for (int j = 0, kb = w.k0; j < w.nk; ++j, kb += w.ks) {
+              if (!wait_slot()) {
+                ok = 0;
+                break;
+              }
+              mbar_arrive_expect_tx(&full_bar[stage],
+                                    C::W_BYTES + static_cast<uint32_t>(crows) * 128u);
+              tma_load_3d(sW + stage * C::W_BYTES, &tmW, full0 + 8u * stage, kb * 64, wx, id, pol);
+              tma_load_2d(sC + stage * C::C_BYTES, &tmC.box[crows / 16 - 1], full0 + 8u * stage,
+                          kb * 64, crow0, pol);
+              next_slot();
+            }
+          }
+          ok = __shfl_sync(0xFFFFFFFFu, ok, 0);
+        }
+        continue;
+      }
       if (lane == 0) {
         const uint32_t cbytes = static_cast<uint32_t>(crows) * 128u;
         for (int j = 0, kb = w.k0; j < w.nk; ++j, kb += w.ks) {
@@ -860,11 +915,10 @@ __global__ void __launch_bounds__(C::kThreads, 1)
       if constexpr (C::kExt) {
         uint32_t ids[C::kTileN / 32];
         load_tile_ids<C>(p, w, lane, ids);
+        const bool mixed = mixed_adapters(ids, w.rows, lane, p.adapters);
         for (int id = next_adapter(ids, -1, p.adapters); id >= 0 && ok;
              id = next_adapter(ids, id, p.adapters)) {
           if (lane == 0) {
-            // Like a ragged stage's, an adapter stage's load completes in each
-            // CTA for its own fixing warps.
             // Stages: rank columns 0.., 64.., ... of hi, then the same of lo.
             const int per = (p.rank + 63) / 64 * 64;
             for (int r = 0; r < 2 * per; r += 64) {
@@ -872,11 +926,22 @@ __global__ void __launch_bounds__(C::kThreads, 1)
                 ok = 0;
                 break;
               }
-              if (leader) mbar_arrive(&full_bar[stage]);
-              mbar_arrive_expect_tx(&tail_bar[stage], C::W_BYTES);
-              tma_load_3d(sW + stage * C::W_BYTES, &tmUp, smem_addr(&tail_bar[stage]),
-                          r < per ? r : r - per, wx, id, pol);
-              note_tail();
+              const int rx = r < per ? r : r - per;
+              if (mixed) {
+                // Like a ragged stage's, the load completes in each CTA for
+                // its own fixing warps.
+                if (leader) mbar_arrive(&full_bar[stage]);
+                mbar_arrive_expect_tx(&tail_bar[stage], C::W_BYTES);
+                tma_load_3d(sW + stage * C::W_BYTES, &tmUp, smem_addr(&tail_bar[stage]), rx, wx, id,
+                            pol);
+                note_tail();
+              } else {
+                if (leader) mbar_arrive_expect_tx(&full_bar[stage], 2 * (C::W_BYTES + C::C_BYTES));
+                const uint32_t fb = full_dst0 + 8u * stage;
+                tma_load_3d_pair(sW + stage * C::W_BYTES, &tmUp, fb, rx, wx, id, pol);
+                tma_load_2d_pair(sC + stage * C::C_BYTES, &tmC.h[r < per ? 0 : 1], fb, rx, crow0,
+                                 pol);
+              }
               next_slot();
             }
           }
@@ -937,8 +1002,20 @@ __global__ void __launch_bounds__(C::kThreads, 1)
         walk.find(p, lane, u / S, u % S, S, w);
         const uint32_t idesc =
             idesc_bf16_f32_major(128 * C::kCtaGroup, w.ncols, C::kWideMn, C::kColMn);
+        // kAdapterDown: one contraction for each adapter of the tile.
+        int passes = 1;
+        if constexpr (C::kMode == kAdapterDown) {
+          uint32_t ids[C::kTileN / 32];
+          load_tile_ids<C>(p, w, lane, ids);
+          passes = 0;
+          if (few_adapters(ids, p.adapters))
+            for (int id = next_adapter(ids, -1, p.adapters); id >= 0;
+                 id = next_adapter(ids, id, p.adapters))
+              ++passes;
+        }
         const int chunks = grouped_chunks<C>(w.nk);   // an empty contraction has none
         uint32_t d_tmem = 0;
+        for (int pass = 0; pass < passes && ok; ++pass) {
         if (lane == 0) {
           for (int c = 0, j = 0, kb = w.k0; c < chunks && ok; ++c) {
             if (!mbar_try_wait(acce0 + 8u * acc, acc_phase ^ 1u) &&
@@ -992,14 +1069,16 @@ __global__ void __launch_bounds__(C::kThreads, 1)
               stage = ns;
               phase = nph;
             }
-            if (ok && c + 1 < chunks) commit_acc();
+            if (ok && (c + 1 < chunks || C::kMode == kAdapterDown)) commit_acc();
           }
         }
         ok = __shfl_sync(0xFFFFFFFFu, ok, 0);
+        }
         if constexpr (C::kExt) {
           uint32_t ids[C::kTileN / 32];
           load_tile_ids<C>(p, w, lane, ids);
           const int per = (p.rank + 63) / 64 * 64;
+          const bool mixed = mixed_adapters(ids, w.rows, lane, p.adapters);
           for (int id = next_adapter(ids, -1, p.adapters); id >= 0 && ok;
                id = next_adapter(ids, id, p.adapters)) {
             if (lane == 0) {
@@ -1009,7 +1088,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
                   ok = 0;
                   break;
                 }
-                if (!wait_fix()) {
+                if (mixed && !wait_fix()) {
                   ok = 0;
                   break;
                 }
@@ -1031,7 +1110,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
             ok = __shfl_sync(0xFFFFFFFFu, ok, 0);
           }
         }
-        if (chunks > 0 && ok && lane == 0) commit_acc();
+        if (C::kMode != kAdapterDown && chunks > 0 && ok && lane == 0) commit_acc();
       }
       if (lane == 0 && (!ok || *abort_flag)) {
         if constexpr (C::kCtaGroup == 1)
@@ -1087,7 +1166,20 @@ __global__ void __launch_bounds__(C::kThreads, 1)
           const int per = (p.rank + 63) / 64 * 64;
           const int crows = w.ncols / C::kCtaGroup;
           const int r0 = static_cast<int>(rank) * crows;   // this CTA's rows of the tile
-          const bool mixed = mixed_adapters(ids, w.rows, lane, p.adapters);
+          if (!mixed_adapters(ids, w.rows, lane, p.adapters)) {
+            if (next_adapter(ids, -1, p.adapters) >= 0) pos += 2 * per / 64;
+            continue;
+          }
+          // A warp takes 4 rows x 8 16-byte pieces at a time: this lane's rows.
+          constexpr int kSteps = C::C_ROWS / (4 * (C::kFixWarps ? C::kFixWarps : 1));
+          uint32_t own[kSteps];
+#pragma unroll
+          for (int t = 0; t < kSteps; ++t) {
+            const int i = 4 * (fw + C::kFixWarps * t) + (lane >> 3);
+            own[t] = i < crows && r0 + i < w.rows
+                         ? static_cast<uint32_t>(p.ids[w.row0 + r0 + i])
+                         : 0xFFFFFFFFu;
+          }
           for (int id = next_adapter(ids, -1, p.adapters); id >= 0 && ok;
                id = next_adapter(ids, id, p.adapters)) {
             for (int r = 0; r < 2 * per; r += 64, ++pos) {
@@ -1095,23 +1187,16 @@ __global__ void __launch_bounds__(C::kThreads, 1)
               const int c0 = r < per ? r : r - per;
               const uint16_t* h = r < per ? p.h_hi : p.h_lo;
               const int cw = min(64, p.rank - c0);   // columns of this stage (rest: zeros)
-              // 16-byte piece q of row i: a warp takes 4 rows x 8 pieces at a
-              // time, eight such at once; the first eight before it waits.
               const int q = lane & 7;
-              constexpr int kBatch = 8;
-              uint4 v[kBatch];
-              auto read = [&](int i0) {
+              uint4 v[kSteps];
 #pragma unroll
-                for (int t = 0; t < kBatch; ++t) {
-                  const int i = i0 + 4 * (fw + C::kFixWarps * t) + (lane >> 3);
-                  const int row = r0 + i;            // row of the tile
-                  v[t] = make_uint4(0u, 0u, 0u, 0u);
-                  if (i < crows && row < w.rows && 8 * q < cw && p.ids[w.row0 + row] == id)
-                    v[t] = *reinterpret_cast<const uint4*>(
-                        h + static_cast<int64_t>(w.row0 + row) * p.rank + c0 + 8 * q);
-                }
-              };
-              read(0);
+              for (int t = 0; t < kSteps; ++t) {
+                const int row = w.row0 + r0 + 4 * (fw + C::kFixWarps * t) + (lane >> 3);
+                v[t] = make_uint4(0u, 0u, 0u, 0u);
+                if (own[t] == static_cast<uint32_t>(id) && 8 * q < cw)
+                  v[t] = *reinterpret_cast<const uint4*>(
+                      h + static_cast<int64_t>(row) * p.rank + c0 + 8 * q);
+              }
               const uint32_t par = (tail_use >> stage) & 1u;
               tail_use ^= 1u << stage;
               if (lane == 0)
@@ -1119,28 +1204,24 @@ __global__ void __launch_bounds__(C::kThreads, 1)
                      mbar_wait(&tail_bar[stage], par, guard, kSiteGrFixIn);
               ok = __shfl_sync(0xFFFFFFFFu, ok, 0);
               if (!ok) break;
-              for (int i0 = 0; i0 < crows; i0 += 4 * kBatch * C::kFixWarps) {
-                if (i0 > 0) read(i0);
 #pragma unroll
-                for (int t = 0; t < kBatch; ++t) {
-                  const int i = i0 + 4 * (fw + C::kFixWarps * t) + (lane >> 3);
-                  if (i < crows)
-                    st_shared_v4(
-                        sC + stage * C::C_BYTES + 128 * i +
-                            ((static_cast<uint32_t>(q) ^ (static_cast<uint32_t>(i) & 7u)) << 4),
-                        v[t].x, v[t].y, v[t].z, v[t].w);
-                }
+              for (int t = 0; t < kSteps; ++t) {
+                const int i = 4 * (fw + C::kFixWarps * t) + (lane >> 3);
+                if (i < crows)
+                  st_shared_v4(
+                      sC + stage * C::C_BYTES + 128 * i +
+                          ((static_cast<uint32_t>(q) ^ (static_cast<uint32_t>(i) & 7u)) << 4),
+                      v[t].x, v[t].y, v[t].z, v[t].w);
               }
-              if (mixed) {
-                const uint32_t half = sW + stage * C::W_BYTES + fw * (C::W_BYTES / 2);
-                for (int j = lane; j < C::W_BYTES / 32; j += 32) {
-                  const uint4 v = ld_shared_v4(half + 16 * j);
-                  const uint4 f = make_uint4(finite_bf16x2(v.x), finite_bf16x2(v.y),
-                                             finite_bf16x2(v.z), finite_bf16x2(v.w));
-                  if (f.x != v.x || f.y != v.y || f.z != v.z || f.w != v.w) {
-                    st_shared_v4(half + 16 * j, f.x, f.y, f.z, f.w);
-                    marked[count & 15] = count + 1;
-                  }
+              const uint32_t part = sW + stage * C::W_BYTES + fw * (C::W_BYTES / 2);
+#pragma unroll 4
+              for (int j = lane; j < C::W_BYTES / 32; j += 32) {
+                const uint4 u4 = ld_shared_v4(part + 16 * j);
+                const uint4 f = make_uint4(finite_bf16x2(u4.x), finite_bf16x2(u4.y),
+                                           finite_bf16x2(u4.z), finite_bf16x2(u4.w));
+                if (f.x != u4.x || f.y != u4.y || f.z != u4.z || f.w != u4.w) {
+                  st_shared_v4(part + 16 * j, f.x, f.y, f.z, f.w);
+                  marked[count & 15] = count + 1;
                 }
               }
               fence_proxy_async_smem();
@@ -1219,7 +1300,60 @@ __global__ void __launch_bounds__(C::kThreads, 1)
       const int end = w.row0 + w.rows;
       const int blocks = (w.rows + 31) / 32;   // of 32 accumulator columns
       const uint32_t t_slab = tmem_base + (static_cast<uint32_t>(slab * 32) << 16);
-      if constexpr (C::kSplit) {
+      if constexpr (C::kMode == kAdapterDown) {
+        // Column block `half` is this warp's 32 rows; x is the rank index.
+        // Every row is written once, by its own adapter's pass.
+        uint32_t ids[C::kTileN / 32];
+        load_tile_ids<C>(p, w, lane, ids);
+        if (!few_adapters(ids, p.adapters)) continue;
+        const int row0 = w.row0 + 32 * half;
+        float* part = p.partials + static_cast<int64_t>(w.piece) * p.M * p.rank;
+        auto keep = [&](int row, float s) {
+          const int64_t o = static_cast<int64_t>(row) * p.rank + x;
+          split_bf16(s, p.h_hi[o], p.h_lo[o]);
+        };
+        for (int id = next_adapter(ids, -1, p.adapters); id >= 0;
+             id = next_adapter(ids, id, p.adapters)) {
+          if (!acc_ready()) {
+            ok = false;
+            break;
+          }
+          float v[32];
+          grouped_read<false>(t_slab + static_cast<uint32_t>(acc * C::kTileN + 32 * half), v);
+          hand_back();
+          const float scale = p.scales ? p.scales[id] : 1.0f;
+#pragma unroll
+          for (int j = 0; j < 32; ++j) {
+            if (row0 + j >= end || x >= p.wide || p.ids[row0 + j] != id) continue;
+            if (S > 1)
+              __stcg(part + static_cast<int64_t>(row0 + j) * p.rank + x, v[j] * scale);
+            else
+              keep(row0 + j, v[j] * scale);
+          }
+        }
+        if (!ok) break;
+        if (S > 1) {
+          __threadfence();
+          named_bar_sync(1, 32 * C::kEpiWarps);
+          if (warp == C::kEpiWarp0 && lane == 0) {
+            const int last =
+                arrive_counter_gpu(p.counters + w.tile) == static_cast<uint32_t>(S - 1);
+            if (last) p.counters[w.tile] = 0u;
+            *join = last;
+          }
+          named_bar_sync(1, 32 * C::kEpiWarps);
+          if (!*join) continue;
+          __threadfence();
+          for (int j = 0; j < 32 && row0 + j < end; ++j) {
+            const uint32_t id = static_cast<uint32_t>(p.ids[row0 + j]);
+            if (x >= p.wide || id >= static_cast<uint32_t>(p.adapters)) continue;
+            const float* src = p.partials + static_cast<int64_t>(row0 + j) * p.rank + x;
+            float s = __ldcg(src);
+            for (int q = 1; q < S; ++q) s += __ldcg(src + static_cast<int64_t>(q) * p.M * p.rank);
+            keep(row0 + j, s);
+          }
+        }
+      } else if constexpr (C::kSplit) {
         // This warp's share (column blocks half, half + 2, ...) stays in
         // registers over the chunks.
         constexpr int kOwn = C::kTileN / 64;

@@ -86,7 +86,9 @@ int launch_grouped(const GroupedOperands& operands, const GroupedArgs& args, cud
     if (tail_scratch(stream, &part, &counters)) {
       a.partials = part;
       a.counters = counters;
-      a.max_slots = static_cast<int>(kTailPartialBytes / (C::kTileN * 128 * 4));
+      // kAdapterDown: [piece][row][rank] instead.
+      const int wide = C::kMode == kAdapterDown && a.wide < 128 ? a.wide : 128;
+      a.max_slots = static_cast<int>(kTailPartialBytes / (C::kTileN * wide * 4));
       a.max_counters = kTailFlagWords;
     }
   }
@@ -117,7 +119,7 @@ int launch_grouped(const GroupedOperands& operands, const GroupedArgs& args, cud
       if (rc != TG_OK) return rc;
     }
   }
-  tW2 = tW;
+  tW2 = tC.h[0] = tC.h[1] = tW;
   if (C::kWideMn && a.wide >= 128) {
     const bool w = C::kMode == kGroupedWgrad;
     rc = make_tensor_map_chunks(&tW2, o.wide, a.wide, o.wide_rows, w ? 1 : o.wide_slices,
@@ -128,6 +130,10 @@ int launch_grouped(const GroupedOperands& operands, const GroupedArgs& args, cud
   if (C::kExt && o.up != nullptr) {
     rc = make_tensor_map_3d(&tUp, bf, o.up, o.up_rank, a.wide, o.up_slices, o.up_ld * 2,
                             o.up_slice_stride * 2, 64, 128, sw);
+    if (rc != TG_OK) return rc;
+    rc = make_tensor_map_2d(&tC.h[0], bf, a.h_hi, a.rank, a.M, a.rank * 2, 64, 128, sw);
+    if (rc != TG_OK) return rc;
+    rc = make_tensor_map_2d(&tC.h[1], bf, a.h_lo, a.rank, a.M, a.rank * 2, 64, 128, sw);
     if (rc != TG_OK) return rc;
   }
   tD = tW;

@@ -146,3 +146,41 @@ def test_views_strides_and_an_output_of_the_callers(tg):
         out = tg.gemm_bf16_lora(A[:m], B, ids[:m].contiguous(), down, up, D[:, :N])
         assert out.data_ptr() == D.data_ptr()
         assert torch.equal(D[:, :N].double(), want[:m]) and (D[:, N:] == 7.0).all()
+
+
+@pytest.mark.parametrize("M", [1025, 1500, 5000])
+@pytest.mark.parametrize("kind", ["one", "none", "requests", "any"])
+@pytest.mark.parametrize("shape", [(136, 200, 5, 24), (264, 1001, 9, 72), (96, 520, 3, 136),
+                                   (128, 1600, 70, 8)])
+def test_many_rows_exact(tg, M, kind, shape):
+    """Rows enough for the tiled computation of the rank values, split and
+    unsplit, one and two tiles of the rank; tiles of one, two, many adapters."""
+    torch = torch_cuda()
+    N, K, adapters, rank = shape
+    gen = torch.Generator(device="cuda").manual_seed(M + N)
+    A, B, down, up = case(gen, quarters, M, N, K, adapters, rank)
+    down[..., 64:] = 0          # few terms: the rank values fit two bf16 terms
+    ids = ids_of(kind, M, adapters, M + rank)
+    scales = 2.0 ** torch.randint(-2, 3, (adapters,), generator=gen, device="cuda").float()
+    want, _, _ = definition(torch, A, B, ids, down, up, scales)
+    got = tg.gemm_bf16_lora(A, B, ids, down, up, scales=scales)
+    assert torch.equal(got.double(), want)
+    assert tg.tg_device_status()[0] == tg.TG_OK
+
+
+def test_many_rows_normal_and_broken_adapter(tg):
+    torch = torch_cuda()
+    M, N, K, adapters, rank = 3000, 520, 2048, 6, 64
+    gen = torch.Generator(device="cuda").manual_seed(9)
+    A, B, down, up = case(gen, normal, M, N, K, adapters, rank)
+    for kind in ("requests", "any"):
+        ids = ids_of(kind, M, adapters, 4)
+        ref, mag, low = definition(torch, A, B, ids, down, up, None)
+        clean = tg.gemm_bf16_lora(A, B, ids, down, up)
+        tol = F32_RTOL * (mag + low) + 2.0 ** -15 * low + F32_ATOL
+        assert float(((clean.double() - ref).abs() / tol).max()) <= 1.0
+        down2 = down.clone()
+        down2[2, 5, 7] = float("nan")
+        got = tg.gemm_bf16_lora(A, B, ids, down2, up)
+        assert torch.equal(got[ids != 2], clean[ids != 2])
+        assert torch.isnan(got[ids == 2]).all()
