@@ -195,7 +195,10 @@ int launch_down(DownArgs a, cudaStream_t stream, DeviceCtx* ctx) {
   // K over a cluster of up to 8 CTAs, while that adds blocks the SMs have
   // room for and leaves a CTA at least one step per warp.
   int c = 1;
-  const int y = a.M < kTok ? a.M : kTok;
+  // A block per adapter of the tile; where most tiles are left to the other
+  // kernel, one block per tile does them in turn (8000 rows of 16 requests:
+  // 15 us of blocks that return at once, against 4).
+  const int y = a.leave_few ? 1 : a.M < kTok ? a.M : kTok;
   while (c < 8 && tiles * y * c < 2 * ctx->num_sms && a.K > 32 * kDownWarps * c) c *= 2;
   a.k_per_cta = ceil_div_i(ceil_div_i(a.K, c), 32 * kDownWarps) * 32 * kDownWarps;
   cudaLaunchConfig_t cfg{};

@@ -97,6 +97,8 @@ struct GroupedArgs {
   uint16_t* h_hi;          // [M][rank] bf16 (MMA form); kAdapterDown writes them
   uint16_t* h_lo;
   const float* scales;     // kAdapterDown: [adapters], or null for 1
+  int wide_box;            // kAdapterDown: rows of `down` per load (the lanes
+                           // above them hold leftovers and are not stored)
   const uint16_t* up;
   int64_t ld_up, group_stride_up;
   // split contraction
@@ -418,11 +420,27 @@ __device__ __forceinline__ void split_bf16(float x, uint16_t& hi, uint16_t& lo) 
                              0xFFFFu);
 }
 
+// Adapter stages of 64 columns.  Alone: rank columns 0.., 64.., ... against hi,
+// then the same against lo.  In a mixed tile, where the fixing warps write the
+// stage anyway, a rank of at most 32 takes one: hi and lo next to each other
+// (lo from column 16 or 32 on), and up[id] twice.
+__device__ __forceinline__ bool adapter_packed(int rank, bool mixed) { return mixed && rank <= 32; }
+__device__ __forceinline__ int adapter_stages(int rank, bool mixed) {
+  return adapter_packed(rank, mixed) ? 1 : 2 * ((rank + 63) / 64);
+}
+
 // A word of two bf16 values without its infinite and NaN ones.
 __device__ __forceinline__ uint32_t finite_bf16x2(uint32_t w) {
   if ((w & 0x7F800000u) == 0x7F800000u) w &= 0x0000FFFFu;
   if ((w & 0x00007F80u) == 0x00007F80u) w &= 0xFFFF0000u;
   return w;
+}
+
+// Whether one of eight bf16 values has an exponent of all ones: then, and only
+// then, adding 0x80 to its 15 magnitude bits reaches bit 15.
+__device__ __forceinline__ bool has_nonfinite(const uint4& v) {
+  auto carry = [](uint32_t w) { return (w & 0x7FFF7FFFu) + 0x00800080u; };
+  return ((carry(v.x) | carry(v.y) | carry(v.z) | carry(v.w)) & 0x80008000u) != 0u;
 }
 
 // epi(v) on the accumulators of one lane, whose column of D has bias b.
@@ -822,7 +840,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
                 break;
               }
               mbar_arrive_expect_tx(&full_bar[stage],
-                                    C::W_BYTES + static_cast<uint32_t>(crows) * 128u);
+                                    static_cast<uint32_t>(p.wide_box + crows) * 128u);
               tma_load_3d(sW + stage * C::W_BYTES, &tmW, full0 + 8u * stage, kb * 64, wx, id, pol);
               tma_load_2d(sC + stage * C::C_BYTES, &tmC.box[crows / 16 - 1], full0 + 8u * stage,
                           kb * 64, crow0, pol);
@@ -919,9 +937,9 @@ __global__ void __launch_bounds__(C::kThreads, 1)
         for (int id = next_adapter(ids, -1, p.adapters); id >= 0 && ok;
              id = next_adapter(ids, id, p.adapters)) {
           if (lane == 0) {
-            // Stages: rank columns 0.., 64.., ... of hi, then the same of lo.
             const int per = (p.rank + 63) / 64 * 64;
-            for (int r = 0; r < 2 * per; r += 64) {
+            const int stages = adapter_stages(p.rank, mixed);
+            for (int r = 0; r < 64 * stages; r += 64) {
               if (!wait_slot()) {
                 ok = 0;
                 break;
@@ -982,10 +1000,8 @@ __global__ void __launch_bounds__(C::kThreads, 1)
       auto wait_fix = [&]() -> bool {
         const uint32_t par = (fix_parity >> stage) & 1u;
         fix_parity ^= 1u << stage;
-        const uint32_t a = smem_addr(&fix_bar[stage]);
-        if (mbar_try_wait_cluster(a, par)) return true;
-        if (!mbar_wait(&fix_bar[stage], par, guard, kSiteGrFix)) return false;
-        return mbar_try_wait_cluster(a, par);
+        return mbar_try_wait_cluster(smem_addr(&fix_bar[stage]), par) ||
+               mbar_wait_cluster(&fix_bar[stage], par, guard, kSiteGrFix);
       };
       // The accumulator is complete: the next one follows.
       auto commit_acc = [&]() {
@@ -1082,7 +1098,8 @@ __global__ void __launch_bounds__(C::kThreads, 1)
           for (int id = next_adapter(ids, -1, p.adapters); id >= 0 && ok;
                id = next_adapter(ids, id, p.adapters)) {
             if (lane == 0) {
-              for (int r = 0; r < 2 * per; r += 64) {
+              const int stages = adapter_stages(p.rank, mixed);
+              for (int r = 0; r < 64 * stages; r += 64) {
                 if (!ready && !mbar_try_wait(full0 + 8u * stage, phase) &&
                     !mbar_wait(&full_bar[stage], phase, guard, kSiteGrFull)) {
                   ok = 0;
@@ -1096,7 +1113,9 @@ __global__ void __launch_bounds__(C::kThreads, 1)
                 const uint64_t wd = wdesc0 + static_cast<uint64_t>(stage * (C::W_BYTES >> 4));
                 const uint64_t cd = cdesc0 + static_cast<uint64_t>(stage * (C::C_BYTES >> 4));
                 const int left = p.rank - (r < per ? r : r - per);
-                const int issues = left >= 64 ? 4 : (left + 15) / 16;
+                const int issues = adapter_packed(p.rank, mixed) ? (p.rank <= 16 ? 2 : 4)
+                                   : left >= 64                  ? 4
+                                                                 : (left + 15) / 16;
                 for (int k = 0; k < issues; ++k)
                   mma_bf16<C::kCtaGroup>(d_tmem, wd + 2 * k, cd + 2 * k, idesc, 1u);
                 mma_commit_pair(&empty_bar[stage], static_cast<uint16_t>(3u));
@@ -1167,7 +1186,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
           const int crows = w.ncols / C::kCtaGroup;
           const int r0 = static_cast<int>(rank) * crows;   // this CTA's rows of the tile
           if (!mixed_adapters(ids, w.rows, lane, p.adapters)) {
-            if (next_adapter(ids, -1, p.adapters) >= 0) pos += 2 * per / 64;
+            if (next_adapter(ids, -1, p.adapters) >= 0) pos += adapter_stages(p.rank, false);
             continue;
           }
           // A warp takes 4 rows x 8 16-byte pieces at a time: this lane's rows.
@@ -1182,20 +1201,24 @@ __global__ void __launch_bounds__(C::kThreads, 1)
           }
           for (int id = next_adapter(ids, -1, p.adapters); id >= 0 && ok;
                id = next_adapter(ids, id, p.adapters)) {
-            for (int r = 0; r < 2 * per; r += 64, ++pos) {
+            for (int r = 0; r < 64 * adapter_stages(p.rank, true); r += 64, ++pos) {
               const int stage = static_cast<int>(pos % C::kStages);
               const int c0 = r < per ? r : r - per;
-              const uint16_t* h = r < per ? p.h_hi : p.h_lo;
               const int cw = min(64, p.rank - c0);   // columns of this stage (rest: zeros)
+              // Packed: hi in pieces 0 .., lo in pieces lq ..
+              const bool packed = adapter_packed(p.rank, true);
+              const int lq = packed ? (p.rank <= 16 ? 2 : 4) : 8;
+              const int q0 = packed && (lane & 7) >= lq ? (lane & 7) - lq : (lane & 7);
+              const uint16_t* h = r < per && (lane & 7) < lq ? p.h_hi : p.h_lo;
               const int q = lane & 7;
               uint4 v[kSteps];
 #pragma unroll
               for (int t = 0; t < kSteps; ++t) {
                 const int row = w.row0 + r0 + 4 * (fw + C::kFixWarps * t) + (lane >> 3);
                 v[t] = make_uint4(0u, 0u, 0u, 0u);
-                if (own[t] == static_cast<uint32_t>(id) && 8 * q < cw)
+                if (own[t] == static_cast<uint32_t>(id) && 8 * q0 < cw)
                   v[t] = *reinterpret_cast<const uint4*>(
-                      h + static_cast<int64_t>(row) * p.rank + c0 + 8 * q);
+                      h + static_cast<int64_t>(row) * p.rank + c0 + 8 * q0);
               }
               const uint32_t par = (tail_use >> stage) & 1u;
               tail_use ^= 1u << stage;
@@ -1213,16 +1236,22 @@ __global__ void __launch_bounds__(C::kThreads, 1)
                           ((static_cast<uint32_t>(q) ^ (static_cast<uint32_t>(i) & 7u)) << 4),
                       v[t].x, v[t].y, v[t].z, v[t].w);
               }
+              // up[id]: this warp's 64 rows, the pieces that hold weights.
+              const int np = cw / 8;
               const uint32_t part = sW + stage * C::W_BYTES + fw * (C::W_BYTES / 2);
 #pragma unroll 4
-              for (int j = lane; j < C::W_BYTES / 32; j += 32) {
-                const uint4 u4 = ld_shared_v4(part + 16 * j);
-                const uint4 f = make_uint4(finite_bf16x2(u4.x), finite_bf16x2(u4.y),
-                                           finite_bf16x2(u4.z), finite_bf16x2(u4.w));
-                if (f.x != u4.x || f.y != u4.y || f.z != u4.z || f.w != u4.w) {
-                  st_shared_v4(part + 16 * j, f.x, f.y, f.z, f.w);
+              for (int j = lane; j < 64 * np; j += 32) {
+                const uint32_t row = static_cast<uint32_t>(j / np), c = static_cast<uint32_t>(j % np);
+                const uint32_t a = part + 128 * row;
+                uint4 u4 = ld_shared_v4(a + ((c ^ (row & 7u)) << 4));
+                if (has_nonfinite(u4)) {
+                  u4 = make_uint4(finite_bf16x2(u4.x), finite_bf16x2(u4.y), finite_bf16x2(u4.z),
+                                  finite_bf16x2(u4.w));
+                  st_shared_v4(a + ((c ^ (row & 7u)) << 4), u4.x, u4.y, u4.z, u4.w);
                   marked[count & 15] = count + 1;
                 }
+                if (packed)
+                  st_shared_v4(a + (((c + lq) ^ (row & 7u)) << 4), u4.x, u4.y, u4.z, u4.w);
               }
               fence_proxy_async_smem();
               __syncwarp();

@@ -111,8 +111,11 @@ int launch_grouped(const GroupedOperands& operands, const GroupedArgs& args, cud
   } else {
     // Weights: the contraction index contiguous (boxes of 128 rows), or for
     // dgrad the wide axis (boxes of 64 x 64).
-    rc = make_tensor_map_3d(&tW, bf, o.wide, C::kWideMn ? a.wide : o.k, o.wide_rows, o.wide_slices,
-                            o.wide_ld * 2, o.wide_slice_stride * 2, 64, C::kWideMn ? 64 : 128, sw);
+    a.wide_box = a.wide < 128 ? (a.wide + 15) / 16 * 16 : 128;
+    rc = make_tensor_map_3d(
+        &tW, bf, o.wide, C::kWideMn ? a.wide : o.k, o.wide_rows, o.wide_slices, o.wide_ld * 2,
+        o.wide_slice_stride * 2, 64,
+        C::kWideMn ? 64 : C::kMode == kAdapterDown ? a.wide_box : 128, sw);
     if (rc != TG_OK) return rc;
     for (int b = 0; b < kColBoxes; ++b) {
       rc = make_tensor_map_2d(&tC.box[b], bf, o.cols, o.k, a.M, o.cols_ld * 2, 64, 16 * (b + 1), sw);

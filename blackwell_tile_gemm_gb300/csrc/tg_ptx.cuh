@@ -213,6 +213,23 @@ static __device__ __noinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, co
   return false;
 }
 
+// mbar_wait for a barrier that threads of another CTA of the cluster arrive
+// on: acquires at cluster scope.
+static __device__ __noinline__ bool mbar_wait_cluster(uint64_t* bar, uint32_t parity,
+                                                      const WaitGuard g, uint32_t site) {
+  const uint32_t a = smem_addr(bar);
+  const uint64_t t0 = global_timer_ns();
+  for (uint32_t spin = 1; spin != 0; ++spin) {
+    if (mbar_try_wait_cluster(a, parity)) return true;
+    if ((spin & 31u) == 0) {
+      if (*g.abort_flag) return false;
+      if (global_timer_ns() - t0 > g.timeout_ns) break;
+    }
+  }
+  report_timeout(g, site);
+  return false;
+}
+
 // Arrival on a global counter shared by the CTAs of a grid: adds 1 and
 // returns the previous value, ordered after this thread's earlier memory
 // operations and before its later ones at GPU scope (acq_rel).  Nobody waits
