@@ -11,6 +11,11 @@ Entry points (same names as the C ABI):
 * ``gemm_bf16(A, B, D=None, ...)``                -- bf16 x bf16 -> f32 / bf16
 * ``gemm_mxfp8_blockscaled(A, B, SFA, SFB, ...)`` -- E4M3 x E8M0/32 -> f32 / bf16
 * ``tile_transpose_b16(X, out=None)``             -- 16-bit transpose, bit-exact
+* ``group_rows(ids, groups)``                     -- rows grouped by id
+* ``gemm_bf16_grouped(A, B, offsets, ...)``       -- weights by group of rows; with
+  ``_dgrad`` and ``_wgrad`` its gradients
+* ``gemm_bf16_lora(A, B, ids, down, up, ...)``    -- shared weights and a low-rank
+  adapter per row
 * ``tg_device_status(stream=None)``               -- device-side error record
 """
 from __future__ import annotations
@@ -383,6 +388,95 @@ def gemm_bf16_gather(A, row_idx, B, D=None, *, out_dtype=None, epilogue_add=None
     return D
 
 
+# The checks below read each tensor's attributes once: a call of a few
+# microseconds on the device is otherwise bound by its own binding.
+_TORCH = None
+
+
+def _torch():
+    global _TORCH
+    if _TORCH is None:
+        import torch
+        _TORCH = torch
+    return _TORCH
+
+
+def _matrix(t, name, dtype):
+    """(rows, width, row stride, address) of a 2-D operand."""
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} must be {str(dtype)[6:]}")
+    shape = t.shape
+    if len(shape) != 2:
+        raise ValueError(f"{name} must be 2-D")
+    rows, width = shape
+    ld, inner = t.stride()
+    if inner != 1 and width > 1 and rows > 0:
+        raise ValueError(f"{name} must have unit inner stride")
+    if rows <= 1:                       # a single row may report any stride
+        ld = (width + 7) // 8 * 8 or 8
+    return rows, width, ld, t.data_ptr()
+
+
+def _stack(t, name, dtype=None):
+    """(slices, rows, width, row stride, slice stride, address) of a 3-D operand."""
+    if dtype is not None and t.dtype is not dtype:
+        raise TypeError(f"{name} must be {str(dtype)[6:]}")
+    shape = t.shape
+    if len(shape) != 3:
+        raise ValueError(f"{name} must be 3-D")
+    slices, rows, width = shape
+    step, ld, inner = t.stride()
+    if inner != 1 and width > 1 and slices > 0 and rows > 0:
+        raise ValueError(f"{name} must have unit inner stride")
+    if rows <= 1:
+        ld = (width + 7) // 8 * 8 or 8
+    return slices, rows, width, ld, step if slices > 1 else ld * (rows or 1), t.data_ptr()
+
+
+def _int32_vector(t, name, length=None):
+    """(length, address) of a contiguous int32 vector."""
+    n = t.shape
+    if t.dtype is not _torch().int32 or len(n) != 1 or not t.is_contiguous():
+        raise TypeError(f"{name} must be a contiguous int32 vector")
+    if length is not None and n[0] != length:
+        raise ValueError(f"{name} must have {length} elements")
+    return n[0], t.data_ptr()
+
+
+def _result(D, shape, out_dtype, device):
+    """(D, its type's code), allocated where the caller gave none: rows start
+    on 16-byte boundaries (a padded view where the width asks for it)."""
+    if D is None:
+        torch = _torch()
+        dtype = out_dtype or torch.float32
+        code = _d_code(dtype)
+        width = shape[-1]
+        pad = -width % (4 if code == TG_D_F32 else 8)
+        if pad:
+            return torch.empty(shape[:-1] + (width + pad,), dtype=dtype,
+                               device=device)[..., :width], code
+        return torch.empty(shape, dtype=dtype, device=device), code
+    if D.shape != shape:
+        raise ValueError(f"D must be {list(shape)}")
+    return D, _d_code(D.dtype)
+
+
+def _epilogue(bias, bias_shape, bias_silu, epilogue_add, silu_affine, affine):
+    """make_epilogue, with a bias of the given shape."""
+    if bias is None:
+        if epilogue_add is None and silu_affine is None and affine is None:
+            return _EPI_NONE
+        return make_epilogue(epilogue_add, silu_affine, None, bias_silu, affine)
+    if bias.shape != bias_shape:
+        raise ValueError(f"bias must be {list(bias_shape)}")
+    if not (epilogue_add is None and silu_affine is None and affine is None):
+        raise ValueError("choose one epilogue")
+    if bias.dtype is not _torch().float32 or not bias.is_contiguous():
+        raise TypeError("bias must be contiguous float32")
+    return tg_epilogue(TG_EPI_BIAS_COL_SILU if bias_silu else TG_EPI_BIAS_COL, 0.0, 0.0,
+                       bias.data_ptr())
+
+
 def group_rows(ids, groups, *, stream=None):
     """(offsets, order, slot): the rows of each group, from a group id per row.
 
@@ -391,65 +485,16 @@ def group_rows(ids, groups, *, stream=None):
     rows group by group, ascending within a group and rows in no group last;
     slot [n] is its inverse (slot[order[j]] = j).  All int32, on the device.
     """
-    import torch
-    p = _int32_vector(ids, "ids")
-    n = ids.shape[0]
-    offsets = torch.empty(int(groups) + 1, dtype=torch.int32, device=ids.device)
+    n, ptr = _int32_vector(ids, "ids")
+    torch = _torch()
     order = torch.empty_like(ids)
     slot = torch.empty_like(ids)
-    rc = lib().tg_group_rows(p, n, int(groups), offsets.data_ptr(), order.data_ptr(),
-                             slot.data_ptr(), _stream_handle(stream))
-    _check(rc, "tg_group_rows")
+    offsets = ids.new_empty(int(groups) + 1)
+    rc = (_lib or lib()).tg_group_rows(ptr, n, int(groups), offsets.data_ptr(), order.data_ptr(),
+                                       slot.data_ptr(), _stream_handle(stream))
+    if rc:
+        _check(rc, "tg_group_rows")
     return offsets, order, slot
-
-
-def _slices(t, name, mult=8):
-    """(row stride, slice stride) in elements of a [slices, rows, width] tensor."""
-    if t.dim() != 3:
-        raise ValueError(f"{name} must be 3-D")
-    slices, rows, width = t.shape
-    st = t.stride()
-    if t.numel() > 0 and width > 1 and st[2] != 1:
-        raise ValueError(f"{name} must have unit inner stride")
-    ld = st[1] if rows > 1 else -(-max(width, 1) // mult) * mult
-    return ld, (st[0] if slices > 1 else ld * max(rows, 1))
-
-
-def _new_rows(shape, dtype, device, zero=False):
-    """An output whose rows start on 16-byte boundaries (a padded view where
-    the width asks for it)."""
-    import torch
-    make = torch.zeros if zero else torch.empty
-    mult = 4 if dtype == torch.float32 else 8
-    width = -(-shape[-1] // mult) * mult
-    return make(tuple(shape[:-1]) + (width,), dtype=dtype, device=device)[..., :shape[-1]]
-
-
-def _int32_vector(t, name, length=None):
-    import torch
-    if t.dtype != torch.int32 or t.dim() != 1 or not t.is_contiguous():
-        raise TypeError(f"{name} must be a contiguous int32 vector")
-    if length is not None and t.shape[0] != length:
-        raise ValueError(f"{name} must have {length} elements")
-    return t.data_ptr()
-
-
-def _bf16_only(**tensors):
-    import torch
-    for name, t in tensors.items():
-        if t.dtype != torch.bfloat16:
-            raise TypeError(f"{name} must be bfloat16")
-
-
-def _group_epilogue(bias, groups, N, epi_kw):
-    """make_epilogue with a bias of one row per group."""
-    if bias is not None:
-        if tuple(bias.shape) != (groups, N):
-            raise ValueError("bias must be [groups, N]")
-        if not bias.is_contiguous():
-            raise TypeError("bias must be contiguous")
-        bias = bias.view(-1)
-    return make_epilogue(bias=bias, **epi_kw)
 
 
 def gemm_bf16_grouped(A, B, offsets, D=None, *, row_idx=None, out_dtype=None, epilogue_add=None,
@@ -464,25 +509,22 @@ def gemm_bf16_grouped(A, B, offsets, D=None, *, row_idx=None, out_dtype=None, ep
     ``make_epilogue``.  D: float32 or bfloat16 [M, N] (default float32); rows
     in no group are zero.
     """
-    import torch
-    _bf16_only(A=A, B=B)
-    if B.dim() != 3 or A.dim() != 2 or A.shape[1] != B.shape[2]:
+    bf16 = _torch().bfloat16
+    M, K, lda, a = _matrix(A, "A", bf16)
+    groups, N, K2, ldb, step, b = _stack(B, "B", bf16)
+    if K != K2:
         raise ValueError("A is [rows, K] and B is [groups, N, K]")
-    groups, N, K = B.shape
-    M = A.shape[0] if row_idx is None else row_idx.shape[0]
-    if D is None:
-        D = _new_rows((M, N), out_dtype or torch.float32, A.device)
-    if tuple(D.shape) != (M, N):
-        raise ValueError("D must be [M, N]")
-    off = _int32_vector(offsets, "offsets", groups + 1)
-    idx = None if row_idx is None else _int32_vector(row_idx, "row_idx")
-    epi = _group_epilogue(bias, groups, N, dict(epilogue_add=epilogue_add, silu_affine=silu_affine,
-                                                bias_silu=bias_silu, affine=affine))
-    ldb, gsb = _slices(B, "B")
-    rc = lib().gemm_bf16_grouped(A.data_ptr(), _ld(A, "A", 8), A.shape[0], idx, off, groups, M,
-                                 B.data_ptr(), ldb, gsb, D.data_ptr(), _ld(D, "D", 8), N, K,
-                                 _d_code(D.dtype), ctypes.byref(epi), 0, _stream_handle(stream))
-    _check(rc, "gemm_bf16_grouped")
+    _, off = _int32_vector(offsets, "offsets", groups + 1)
+    a_rows, idx = M, None
+    if row_idx is not None:
+        M, idx = _int32_vector(row_idx, "row_idx")
+    D, code = _result(D, (M, N), out_dtype, A.device)
+    epi = _epilogue(bias, (groups, N), bias_silu, epilogue_add, silu_affine, affine)
+    rc = (_lib or lib()).gemm_bf16_grouped(a, lda, a_rows, idx, off, groups, M, b, ldb, step,
+                                           D.data_ptr(), _ld(D, "D", 8), N, K, code,
+                                           ctypes.byref(epi), 0, _stream_handle(stream))
+    if rc:
+        _check(rc, "gemm_bf16_grouped")
     return D
 
 
@@ -492,22 +534,18 @@ def gemm_bf16_grouped_dgrad(G, B, offsets, D=None, *, out_dtype=None, stream=Non
     G: bfloat16 [M, N]; B: bfloat16 [groups, N, K]; offsets as there.  D:
     float32 or bfloat16 [M, K] (default float32); rows in no group are zero.
     """
-    import torch
-    _bf16_only(G=G, B=B)
-    if B.dim() != 3 or G.dim() != 2 or G.shape[1] != B.shape[1]:
+    bf16 = _torch().bfloat16
+    M, N, ldg, g = _matrix(G, "G", bf16)
+    groups, N2, K, ldb, step, b = _stack(B, "B", bf16)
+    if N != N2:
         raise ValueError("G is [M, N] and B is [groups, N, K]")
-    groups, N, K = B.shape
-    M = G.shape[0]
-    if D is None:
-        D = _new_rows((M, K), out_dtype or torch.float32, G.device)
-    if tuple(D.shape) != (M, K):
-        raise ValueError("D must be [M, K]")
-    off = _int32_vector(offsets, "offsets", groups + 1)
-    ldb, gsb = _slices(B, "B")
-    rc = lib().gemm_bf16_grouped_dgrad(G.data_ptr(), _ld(G, "G", 8), off, groups, M, B.data_ptr(),
-                                       ldb, gsb, D.data_ptr(), _ld(D, "D", 8), N, K,
-                                       _d_code(D.dtype), 0, _stream_handle(stream))
-    _check(rc, "gemm_bf16_grouped_dgrad")
+    _, off = _int32_vector(offsets, "offsets", groups + 1)
+    D, code = _result(D, (M, K), out_dtype, G.device)
+    rc = (_lib or lib()).gemm_bf16_grouped_dgrad(g, ldg, off, groups, M, b, ldb, step,
+                                                 D.data_ptr(), _ld(D, "D", 8), N, K, code, 0,
+                                                 _stream_handle(stream))
+    if rc:
+        _check(rc, "gemm_bf16_grouped_dgrad")
     return D
 
 
@@ -518,25 +556,25 @@ def gemm_bf16_grouped_wgrad(G, A, offsets, D=None, *, row_idx=None, out_dtype=No
     offsets as there.  D: float32 or bfloat16 [groups, N, K] (default
     float32), zero for an empty group.
     """
-    import torch
-    _bf16_only(G=G, A=A)
-    M = A.shape[0] if row_idx is None else row_idx.shape[0]
-    if A.dim() != 2 or G.dim() != 2 or G.shape[0] != M:
+    bf16 = _torch().bfloat16
+    M, N, ldg, g = _matrix(G, "G", bf16)
+    a_rows, K, lda, a = _matrix(A, "A", bf16)
+    idx = None
+    if row_idx is not None:
+        _, idx = _int32_vector(row_idx, "row_idx", M)
+    elif a_rows != M:
         raise ValueError("G is [M, N] and A is [M, K] (or rows picked by row_idx)")
-    if offsets.shape[0] < 2:
+    groups, off = _int32_vector(offsets, "offsets")
+    groups -= 1
+    if groups < 1:
         raise ValueError("offsets must have groups + 1 elements")
-    groups, N, K = offsets.shape[0] - 1, G.shape[1], A.shape[1]
-    if D is None:
-        D = _new_rows((groups, N, K), out_dtype or torch.float32, G.device)
-    if tuple(D.shape) != (groups, N, K):
-        raise ValueError("D must be [groups, N, K]")
-    off = _int32_vector(offsets, "offsets")
-    idx = None if row_idx is None else _int32_vector(row_idx, "row_idx")
-    ldd, gsd = _slices(D, "D")
-    rc = lib().gemm_bf16_grouped_wgrad(G.data_ptr(), _ld(G, "G", 8), A.data_ptr(), _ld(A, "A", 8),
-                                       A.shape[0], idx, off, groups, M, D.data_ptr(), ldd, gsd, N,
-                                       K, _d_code(D.dtype), 0, _stream_handle(stream))
-    _check(rc, "gemm_bf16_grouped_wgrad")
+    D, code = _result(D, (groups, N, K), out_dtype, G.device)
+    _, _, _, ldd, step, d = _stack(D, "D")
+    rc = (_lib or lib()).gemm_bf16_grouped_wgrad(g, ldg, a, lda, a_rows, idx, off, groups, M, d,
+                                                 ldd, step, N, K, code, 0,
+                                                 _stream_handle(stream))
+    if rc:
+        _check(rc, "gemm_bf16_grouped_wgrad")
     return D
 
 
@@ -551,34 +589,30 @@ def gemm_bf16_lora(A, B, ids, down, up, D=None, *, scales=None, out_dtype=None, 
     [adapters] or None.  D: float32 or bfloat16 [M, N] (default float32).
     Epilogue keywords: see ``make_epilogue``.
     """
-    import torch
-    _bf16_only(A=A, B=B, down=down, up=up)
-    M, K = A.shape
-    N, K2 = B.shape
-    adapters, rank = down.shape[:2] if down.dim() == 3 else (0, 0)
-    if K2 != K:
+    bf16 = _torch().bfloat16
+    M, K, lda, a = _matrix(A, "A", bf16)
+    N, K2, ldb, b = _matrix(B, "B", bf16)
+    if K != K2:
         raise ValueError("A is [M, K] and B is [N, K]")
-    if tuple(down.shape) != (adapters, rank, K) or tuple(up.shape) != (adapters, N, rank):
+    adapters, rank, K2, ld_down, step_down, pd = _stack(down, "down", bf16)
+    adapters2, N2, rank2, ld_up, step_up, pu = _stack(up, "up", bf16)
+    if K2 != K or N2 != N or rank2 != rank or adapters2 != adapters:
         raise ValueError("down is [adapters, rank, K] and up is [adapters, N, rank]")
-    if scales is not None and (scales.dtype != torch.float32 or not scales.is_contiguous()
-                               or tuple(scales.shape) != (adapters,)):
-        raise TypeError("scales must be a contiguous float32 vector of one value per adapter")
-    if bias is not None and bias.shape[0] != N:
-        raise ValueError("bias must have N elements")
-    if D is None:
-        D = _new_rows((M, N), out_dtype or torch.float32, A.device)
-    if tuple(D.shape) != (M, N):
-        raise ValueError("D must be [M, N]")
-    idp = _int32_vector(ids, "ids", M)
-    epi = make_epilogue(epilogue_add, silu_affine, bias, bias_silu, affine)
-    ldd_, sd = _slices(down, "down")
-    ldu, su = _slices(up, "up")
-    rc = lib().gemm_bf16_lora(A.data_ptr(), _ld(A, "A", 8), B.data_ptr(), _ld(B, "B", 8), idp,
-                              down.data_ptr(), ldd_, sd, up.data_ptr(), ldu, su,
-                              None if scales is None else scales.data_ptr(), adapters, rank,
-                              D.data_ptr(), _ld(D, "D", 8), M, N, K, _d_code(D.dtype),
-                              ctypes.byref(epi), 0, _stream_handle(stream))
-    _check(rc, "gemm_bf16_lora")
+    ps = None
+    if scales is not None:
+        if (scales.dtype is not _torch().float32 or not scales.is_contiguous()
+                or scales.shape != (adapters,)):
+            raise TypeError("scales must be a contiguous float32 vector of one value per adapter")
+        ps = scales.data_ptr()
+    _, idp = _int32_vector(ids, "ids", M)
+    D, code = _result(D, (M, N), out_dtype, A.device)
+    epi = _epilogue(bias, (N,), bias_silu, epilogue_add, silu_affine, affine)
+    rc = (_lib or lib()).gemm_bf16_lora(a, lda, b, ldb, idp, pd, ld_down, step_down, pu, ld_up,
+                                        step_up, ps, adapters, rank, D.data_ptr(),
+                                        _ld(D, "D", 8), M, N, K, code, ctypes.byref(epi), 0,
+                                        _stream_handle(stream))
+    if rc:
+        _check(rc, "gemm_bf16_lora")
     return D
 
 
