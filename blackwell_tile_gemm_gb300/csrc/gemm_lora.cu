@@ -41,19 +41,9 @@ struct DownArgs {
   int adapters, rank;
   int k_per_cta;         // multiple of 32 * kDownWarps
   bool leave_few;        // kAdapterDown does the 64-row tiles of few adapters
-  float* h;              // [M][rank], or null
-  uint16_t* hi;          // [M][rank]: bf16 terms of the same
+  uint16_t* hi;          // [M][rank]: H in two bf16 terms
   uint16_t* lo;
 };
-
-__device__ __forceinline__ void mma_m16n8k16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
-                                             uint32_t a3, uint32_t b0, uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
-      "{%8, %9}, {%0, %1, %2, %3};"
-      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
 
 // Values k .. k + 7 of a row; those from `end` on are zero and not read.
 __device__ __forceinline__ uint4 load8(const uint16_t* row, int k, int end) {
@@ -164,10 +154,7 @@ __global__ void __launch_bounds__(32 * kDownWarps) lora_down_kernel(const DownAr
           }
           s *= scale;
           const int64_t o = static_cast<int64_t>(row0 + i) * p.rank + r;
-          if (p.h != nullptr)
-            p.h[o] = s;
-          else
-            split_bf16(s, p.hi[o], p.lo[o]);
+          split_bf16(s, p.hi[o], p.lo[o]);
         }
       }
       // The partial sums are free again once every CTA has read them.
@@ -230,7 +217,7 @@ constexpr int kLoraDownRows = 1024;
 
 }  // namespace
 
-// H: f32 for few rows, else two bf16 terms: 4 bytes a value either way.
+// H: two bf16 terms.
 size_t lora_workspace_bytes(int64_t M, int64_t rank) {
   return (static_cast<size_t>(M) * static_cast<size_t>(rank) * 4u + 255u) / 256u * 256u;
 }
@@ -297,16 +284,14 @@ extern "C" int gemm_bf16_lora(const void* A, int64_t lda, const void* B, int64_t
   d.scales = scales;
   d.adapters = static_cast<int>(adapters);
   d.rank = static_cast<int>(rank);
-  d.h = few ? static_cast<float*>(ws) : nullptr;
-  d.hi = few ? nullptr : static_cast<uint16_t*>(ws);
-  d.lo = few ? nullptr : d.hi + M * rank;
+  d.hi = static_cast<uint16_t*>(ws);
+  d.lo = d.hi + M * rank;
   GroupedArgs a = grouped_args(ctx);
   a.M = static_cast<int>(M);
   a.num_k_blocks = ceil_div_i(K, 64);
   a.ids = ids;
   a.adapters = static_cast<int>(adapters);
   a.rank = static_cast<int>(rank);
-  a.h = d.h;
   a.h_hi = d.hi;
   a.h_lo = d.lo;
   GroupedOperands o{};

@@ -49,8 +49,8 @@
 // Few rows (kSplit, single CTAs): the product is bound by reading the
 // weights, tiles are few, so S units share a tile's contraction; each writes
 // an f32 partial and the one that arrives last adds them in piece order (the
-// same bits every time; nobody waits).  There the adapter term needs no MMA:
-// the epilogue adds up[id][n, :] . H[i, :] in f32.
+// same bits every time; nobody waits).  There the adapter term stays out of
+// the pipeline: the epilogue's warps compute it while the weights stream in.
 //
 // Roles: warp 0 TMA producer, warp 1 TMEM allocator and MMA issuer, warps 2
 // and 3 fixing warps, warps 4..11 epilogue.  Every wait is bounded.
@@ -93,8 +93,7 @@ struct GroupedArgs {
   // adapters
   const int* ids;          // [M]
   int adapters, rank;
-  const float* h;          // [M][rank] f32 (few rows)
-  uint16_t* h_hi;          // [M][rank] bf16 (MMA form); kAdapterDown writes them
+  uint16_t* h_hi;          // [M][rank] bf16: the two terms; kAdapterDown writes them
   uint16_t* h_lo;
   const float* scales;     // kAdapterDown: [adapters], or null for 1
   int wide_box;            // kAdapterDown: rows of `down` per load (the lanes
@@ -341,21 +340,46 @@ __device__ __forceinline__ int grouped_chunk_end(int nk, int chunks, int c) {
   return static_cast<int>(static_cast<int64_t>(nk) * (c + 1) / chunks);
 }
 
-// Pieces of the contraction per tile: the count (at most 8, each piece at
-// least 4 stages) with the least waves * (stages per piece + 4), the 4 for a
-// unit's start, partial tile and join.
-__device__ __forceinline__ int grouped_split(const GroupedArgs& p, int tiles, int units) {
-  int best = 1;
-  int cost = (tiles + units - 1) / units * (p.num_k_blocks + 2);
-  for (int c = 2; c <= 8; ++c) {
-    if (p.num_k_blocks < 4 * c || tiles * c > p.max_slots || tiles > p.max_counters) break;
-    const int v = (tiles * c + units - 1) / units * ((p.num_k_blocks + c - 1) / c + 4);
-    if (v < cost) {
-      cost = v;
-      best = c;
+// Full waves of whole tiles, then the tiles of a last, partial wave in pieces
+// of their contraction: the count (at most 8, each piece at least 4 stages)
+// with the least waves * (stages per piece + 14), against the whole tiles'
+// stages + 2.  The 14 stages, 5 us, are what a piece's partial tile, arrival
+// and join take (with 0: 16 rows in 8 groups x 2048 x 2048 43 us instead of 14;
+// without pieces: 4 rows x 4096 x 4096 24 us instead of 14).
+struct GroupedPlan {
+  int full;    // tiles run whole
+  int S;       // pieces of the others
+  int items;   // units of work
+};
+template <bool kSplit>
+__device__ __forceinline__ GroupedPlan grouped_plan(const GroupedArgs& p, int tiles, int units) {
+  GroupedPlan g{tiles, 1, tiles};
+  if constexpr (kSplit) {
+    const int full = tiles / units * units;
+    const int rest = tiles - full;
+    int cost = p.num_k_blocks + 2;
+    for (int c = 2; c <= 8 && rest > 0; ++c) {
+      if (p.num_k_blocks < 4 * c || rest * c > p.max_slots || rest > p.max_counters) break;
+      const int v = (rest * c + units - 1) / units * ((p.num_k_blocks + c - 1) / c + 14);
+      if (v < cost) {
+        cost = v;
+        g = GroupedPlan{full, c, full + rest * c};
+      }
     }
   }
-  return best;
+  return g;
+}
+
+// Warp-level MMA, 16 x 8 x 16, bf16 with f32 accumulation: a0, a1: rows
+// lane / 4 and + 8 at k = 2 (lane % 4); a2, a3: the same at k + 8; b0, b1:
+// column lane / 4; c: rows lane / 4 and + 8, columns 2 (lane % 4) and + 1.
+__device__ __forceinline__ void mma_m16n8k16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                             uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+      "{%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
 // The smallest adapter above `last` among the ids of a tile's rows (each lane
@@ -648,47 +672,95 @@ __device__ __forceinline__ void add_marked_terms(const GroupedArgs& p, int row, 
     if (row + j < end) v[j] += marked_term(p, row + j, x);
 }
 
-// Adapter term of 32 rows of a few-row tile: v[j] += up[id][x, :] . H[row + j, :]
-// in f32, for the batches of eight rows whose number is the unit's piece
-// modulo S (the pieces of a tile share the rows out).  The loads of a batch
-// are in flight together; this runs before the accumulator is waited for,
-// i.e. beside the stream of the weights.
+// Adapter term of a few-row tile: v[j] += up[id][x, :] . H[row + j, :] for 32
+// rows, shared out over the S pieces of the tile in batches of eight rows.
+// It runs before the accumulator is waited for, beside the stream of the
+// weights, on warp-level MMAs: 32 rows of up[id] by 8 rows of H, once for each
+// adapter of the batch, whose result is kept in its own rows' columns only
+// (whatever the other columns hold).  Both operands come from memory in
+// 16-byte pieces, 64 bytes of a row to each four lanes, so that a load
+// instruction touches 8 lines; one lane per row of up[id] (32 lines each) took
+// 71 us instead for 128 rows x 4096 with 48 adapters of rank 64.
 __device__ __forceinline__ void add_adapter_terms(const GroupedArgs& p, int piece, int S, int row,
-                                                  int end, int x, float (&v)[32]) {
-  const bool in = x < p.wide;
-#pragma unroll
+                                                  int end, int x0, int lane, float (&v)[32]) {
+  const int g = lane >> 2, q = lane & 3;
+#pragma unroll 1   // (one copy of a long body: instruction fetches are what a short call waits for)
   for (int b = 0; b < 4; ++b) {
     const int r0 = row + 8 * b;
     if (r0 >= end || (r0 >> 3) % S != piece) continue;
-    const uint16_t* u[8];
+    const int mine = r0 + (lane & 7);
+    uint32_t ids[1] = {mine < end ? static_cast<uint32_t>(p.ids[mine]) : 0xFFFFFFFFu};
+    const uint32_t id_b = __shfl_sync(0xFFFFFFFFu, ids[0], g);   // of the row this lane loads
+    const uint32_t id_c0 = __shfl_sync(0xFFFFFFFFu, ids[0], 2 * q);
+    const uint32_t id_c1 = __shfl_sync(0xFFFFFFFFu, ids[0], 2 * q + 1);
+    const uint16_t* hi = p.h_hi + static_cast<int64_t>(r0 + g) * p.rank + 8 * q;
+    const uint16_t* lo = p.h_lo + static_cast<int64_t>(r0 + g) * p.rank + 8 * q;
+    const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+    float sum[2][4] = {};
+    int id = next_adapter(ids, -1, p.adapters);
+    if (id < 0) continue;
+    int k = 0;
+    uint4 a[2][2], h[2];
+    auto load = [&]() {
+      const bool in = 8 * q + k < p.rank;
+      const uint16_t* u = p.up + id * p.group_stride_up + 8 * q + k;
+#pragma unroll
+      for (int t = 0; t < 2; ++t)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int x = x0 + 16 * t + 8 * i + g;
+          a[t][i] = in && x < p.wide ? ld_global_nc_v4(u + static_cast<int64_t>(x) * p.ld_up) : zero;
+        }
+      const bool own = in && id_b == static_cast<uint32_t>(id);
+      h[0] = own ? *reinterpret_cast<const uint4*>(hi + k) : zero;
+      h[1] = own ? *reinterpret_cast<const uint4*>(lo + k) : zero;
+    };
+    load();
+    while (id >= 0) {
+      float c[2][4] = {};
+      const uint32_t cur = static_cast<uint32_t>(id);
+      bool more;
+      do {
+        uint4 a0[2][2], h0[2];
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          a0[t][0] = a[t][0];
+          a0[t][1] = a[t][1];
+          h0[t] = h[t];
+        }
+        // The next step's loads are in flight during this one's products.
+        more = k + 32 < p.rank;
+        k = more ? k + 32 : 0;
+        if (!more) id = next_adapter(ids, id, p.adapters);
+        if (id >= 0) load();
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            mma_m16n8k16(c[t], a0[t][0].x, a0[t][1].x, a0[t][0].y, a0[t][1].y, h0[i].x, h0[i].y);
+            mma_m16n8k16(c[t], a0[t][0].z, a0[t][1].z, a0[t][0].w, a0[t][1].w, h0[i].z, h0[i].w);
+          }
+      } while (more);
+#pragma unroll
+      for (int t = 0; t < 2; ++t)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if ((e & 1 ? id_c1 : id_c0) == cur) sum[t][e] += c[t][e];
+    }
+    // From (row of up g + 8 (e / 2) + 16 t, row of H 2 q + e % 2) to one lane
+    // per row of up.
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      const uint32_t id = r0 + j < end ? static_cast<uint32_t>(__ldg(p.ids + r0 + j)) : 0xFFFFFFFFu;
-      u[j] = in && id < static_cast<uint32_t>(p.adapters)
-                 ? p.up + id * p.group_stride_up + static_cast<int64_t>(x) * p.ld_up
-                 : nullptr;
-    }
-    for (int r = 0; r < p.rank; r += 8) {
-      uint4 q[8];
+      const int src = 4 * (lane & 7) + j / 2;
+      float w[4];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) q[j] = u[j] ? ld_global_nc_v4(u[j] + r) : make_uint4(0u, 0u, 0u, 0u);
+      for (int i = 0; i < 4; ++i)
+        w[i] = __shfl_sync(0xFFFFFFFFu, sum[i >> 1][2 * (i & 1) + (j & 1)], src);
+      const float lo8 = lane & 16 ? w[2] : w[0], hi8 = lane & 16 ? w[3] : w[1];
+      const float term = lane & 8 ? hi8 : lo8;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        if (u[j] == nullptr) continue;   // (H has no row there)
-        const float* h = p.h + static_cast<int64_t>(r0 + j) * p.rank + r;
-        const float4 h0 = __ldcg(reinterpret_cast<const float4*>(h));
-        const float4 h1 = __ldcg(reinterpret_cast<const float4*>(h + 4));
-        float s = v[8 * b + j];
-        s = fmaf(__uint_as_float(q[j].x << 16), h0.x, s);
-        s = fmaf(__uint_as_float(q[j].x & 0xFFFF0000u), h0.y, s);
-        s = fmaf(__uint_as_float(q[j].y << 16), h0.z, s);
-        s = fmaf(__uint_as_float(q[j].y & 0xFFFF0000u), h0.w, s);
-        s = fmaf(__uint_as_float(q[j].z << 16), h1.x, s);
-        s = fmaf(__uint_as_float(q[j].z & 0xFFFF0000u), h1.y, s);
-        s = fmaf(__uint_as_float(q[j].w << 16), h1.z, s);
-        s = fmaf(__uint_as_float(q[j].w & 0xFFFF0000u), h1.w, s);
-        v[8 * b + j] = s;
-      }
+      for (int i = 0; i < 4; ++i)
+        if (b == i) v[8 * i + j] += term;
     }
   }
 }
@@ -772,9 +844,22 @@ __global__ void __launch_bounds__(C::kThreads, 1)
   GroupWalk<C> walk;
   int first_row, end_row;
   const int tiles = walk.total(p, lane, &first_row, &end_row);
-  const int S = C::kSplit ? grouped_split(p, tiles, num_units) : 1;
-  const int num_items = tiles * S;
+  const GroupedPlan plan = grouped_plan<C::kSplit>(p, tiles, num_units);
+  const int num_items = plan.items;
   GroupedWork w;
+  // Work item u of the grid: S pieces from tile plan.full on.
+  int S = 1;
+  auto take = [&](int u) {
+    if (C::kSplit && u >= plan.full) {
+      const int v = u - plan.full;
+      S = plan.S;
+      walk.find(p, lane, plan.full + v / S, v % S, S, w);
+      w.tile -= plan.full;
+    } else {
+      S = 1;
+      walk.find(p, lane, u, 0, 1, w);
+    }
+  };
 
   if (warp == 0 || (C::kTwoProducers && warp == C::kColWarp)) {
     // ------------------------------------------------------------ producers
@@ -820,7 +905,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
       }
     };
     for (int u = unit; u < num_items && ok; u += num_units) {
-      walk.find(p, lane, u / S, u % S, S, w);
+      take(u);
       const int wx = w.wide0 + static_cast<int>(rank) * 128;
       const int crows = w.ncols / C::kCtaGroup;       // column-operand rows of this CTA
       const int crow0 = w.row0 + static_cast<int>(rank) * crows;
@@ -1015,7 +1100,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
         }
       };
       for (int u = unit; u < num_items && ok; u += num_units) {
-        walk.find(p, lane, u / S, u % S, S, w);
+        take(u);
         const uint32_t idesc =
             idesc_bf16_f32_major(128 * C::kCtaGroup, w.ncols, C::kWideMn, C::kColMn);
         // kAdapterDown: one contraction for each adapter of the tile.
@@ -1151,7 +1236,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
       int ok = 1;
       int count = 0;               // tiles of this unit so far
       for (int u = unit; u < num_items && ok; u += num_units, ++count) {
-        walk.find(p, lane, u / S, u % S, S, w);
+        take(u);
         if constexpr (C::kMode == kGroupedWgrad) {
           const int rest = w.len & 63;
           if (rest != 0) {
@@ -1319,7 +1404,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
     bool ok = true;
     int count = 0;                             // tiles of this unit so far
     for (int u = unit; u < num_items && ok; u += num_units, ++count) {
-      walk.find(p, lane, u / S, u % S, S, w);
+      take(u);
       const int chunks = grouped_chunks<C>(w.nk);
       const int x = w.wide0 + static_cast<int>(rank) * 128 + slab * 32 + lane;
       const float b = epi_uses_bias(p.epi.op) && x < p.wide
@@ -1373,13 +1458,28 @@ __global__ void __launch_bounds__(C::kThreads, 1)
           named_bar_sync(1, 32 * C::kEpiWarps);
           if (!*join) continue;
           __threadfence();
-          for (int j = 0; j < 32 && row0 + j < end; ++j) {
-            const uint32_t id = static_cast<uint32_t>(p.ids[row0 + j]);
-            if (x >= p.wide || id >= static_cast<uint32_t>(p.adapters)) continue;
-            const float* src = p.partials + static_cast<int64_t>(row0 + j) * p.rank + x;
-            float s = __ldcg(src);
-            for (int q = 1; q < S; ++q) s += __ldcg(src + static_cast<int64_t>(q) * p.M * p.rank);
-            keep(row0 + j, s);
+          for (int j0 = 0; j0 < 32 && row0 + j0 < end && x < p.wide; j0 += 8) {
+            // Rows past the end read the last one's again: the loads of eight
+            // rows fly together.
+            float s[8];
+            const float* src[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+              src[j] = p.partials + static_cast<int64_t>(min(row0 + j0 + j, end - 1)) * p.rank + x;
+              s[j] = __ldcg(src[j]);
+            }
+            for (int q = 1; q < S; ++q) {
+              float t[8];
+#pragma unroll
+              for (int j = 0; j < 8; ++j) t[j] = __ldcg(src[j] + static_cast<int64_t>(q) * p.M * p.rank);
+#pragma unroll
+              for (int j = 0; j < 8; ++j) s[j] += t[j];
+            }
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+              if (row0 + j0 + j < end && static_cast<uint32_t>(p.ids[row0 + j0 + j]) <
+                                             static_cast<uint32_t>(p.adapters))
+                keep(row0 + j0 + j, s[j]);
           }
         }
       } else if constexpr (C::kSplit) {
@@ -1391,7 +1491,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
         for (int q = 0; q < kOwn; ++q) {
           grouped_zero(m[q]);
           if constexpr (C::kMode == kAdapter)
-            add_adapter_terms(p, w.piece, S, w.row0 + 32 * (half + 2 * q), end, x, m[q]);
+            add_adapter_terms(p, w.piece, S, w.row0 + 32 * (half + 2 * q), end, x - lane, lane, m[q]);
         }
         for (int c = 0; c < chunks; ++c) {
           if (!acc_ready()) {
@@ -1434,15 +1534,19 @@ __global__ void __launch_bounds__(C::kThreads, 1)
 #pragma unroll
           for (int q = 0; q < kOwn; ++q) {
             const int col = 32 * (half + 2 * q);
+            if (w.row0 + col >= end) continue;
+            // All 32 columns, also those past the tile's rows (the slot has
+            // them; they are not stored): unconditional loads fly together.
             const float* src = part + col * 128;
 #pragma unroll
-            for (int i = 0; i < 32; ++i)
-              m[q][i] = w.row0 + col + i < end ? __ldcg(src + i * 128) : 0.0f;
+            for (int i = 0; i < 32; ++i) m[q][i] = __ldcg(src + i * 128);
             for (int r = 1; r < S; ++r) {
               src += C::kTileN * 128;
+              float t[32];
 #pragma unroll
-              for (int i = 0; i < 32; ++i)
-                if (w.row0 + col + i < end) m[q][i] += __ldcg(src + i * 128);
+              for (int i = 0; i < 32; ++i) t[i] = __ldcg(src + i * 128);
+#pragma unroll
+              for (int i = 0; i < 32; ++i) m[q][i] += t[i];
             }
           }
         }

@@ -367,9 +367,10 @@ int gemm_bf16_grouped_wgrad(const void* G, int64_t ldg, const void* A, int64_t l
  *   scales  : device, f32 [adapters], or NULL for 1.
  *   rank    : a multiple of 8, at most TG_MAX_RANK (smaller adapters are
  *             padded with zeros); otherwise TG_ERR_UNSUPPORTED.  flags: 0.
- * The rank values a row between the two adapter products are kept in f32 (M
- * <= 128) or as two bf16 terms (16 significant bits) in the stream's
- * workspace (TG_CALL_GEMM_BF16_LORA); both terms of D meet in f32.
+ * The rank values a row between the two adapter products are kept as two bf16
+ * terms (16 significant bits) in the stream's workspace
+ * (TG_CALL_GEMM_BF16_LORA); the shared and the adapter term of D meet in f32.
+ * Infinite or NaN weights of an adapter reach its own rows only.
  */
 enum { TG_MAX_RANK = 256 };
 int gemm_bf16_lora(const void* A, int64_t lda, const void* B, int64_t ldb, const int32_t* ids,
