@@ -166,6 +166,104 @@ __global__ void __launch_bounds__(32 * kDownWarps) lora_down_kernel(const DownAr
   }
 }
 
+// Where the tiles of the shared product start: at the first row of each run of
+// at least kLongRun rows with one adapter, and after it.  Shorter runs between
+// them stay together.  One block: two ordered compactions (rows where the
+// adapter changes; of those, the ones next to a long run).
+constexpr int kLongRun = 128;
+constexpr int kRunThreads = 1024;
+
+// Position of the first of this thread's `items` among the block's, after
+// *count of earlier steps (updated).
+__device__ __forceinline__ int ordered_slot(int items, int* part, int* count) {
+  const int warp = threadIdx.x >> 5, lane = static_cast<int>(threadIdx.x & 31);
+  int incl = items;
+#pragma unroll
+  for (int d = 1; d < 32; d *= 2) {
+    const int o = __shfl_up_sync(0xFFFFFFFFu, incl, d);
+    if (lane >= d) incl += o;
+  }
+  if (lane == 31) part[warp] = incl;
+  __syncthreads();
+  int v = part[lane];
+#pragma unroll
+  for (int d = 1; d < 32; d *= 2) {
+    const int o = __shfl_up_sync(0xFFFFFFFFu, v, d);
+    if (lane >= d) v += o;
+  }
+  const int all = __shfl_sync(0xFFFFFFFFu, v, 31);
+  const int before = warp ? __shfl_sync(0xFFFFFFFFu, v, warp - 1) : 0;
+  __syncthreads();
+  const int at = *count + before + incl - items;
+  *count += all;
+  return at;
+}
+
+__global__ void __launch_bounds__(kRunThreads) lora_runs_kernel(const int* ids, int M, int adapters,
+                                                                int* runs, int* offsets, int most) {
+  constexpr int kOwn = 8;   // consecutive rows of one thread
+  __shared__ int part[kRunThreads / 32];
+  static_assert(kRunThreads == 1024, "one partial sum a lane");
+  // ids are older than the kernel before this one, and what this one writes
+  // is read only after it (launch order in gemm_bf16_lora): it waits at its
+  // end, so that whoever waits for it has waited for both.
+  griddep_launch_dependents();
+  int count = 0;
+  for (int64_t b = 0; b < M; b += kOwn * kRunThreads) {
+    const int64_t i0 = b + kOwn * static_cast<int64_t>(threadIdx.x);
+    uint32_t key[kOwn + 1];
+#pragma unroll
+    for (int j = 0; j <= kOwn; ++j) {
+      const int64_t i = i0 + j - 1;
+      key[j] = i >= 0 && i < M ? min(static_cast<uint32_t>(ids[i]), static_cast<uint32_t>(adapters))
+                               : 0xFFFFFFFFu;   // before the first row: unlike any key
+    }
+    uint32_t flags = 0;
+#pragma unroll
+    for (int j = 0; j < kOwn; ++j)
+      if (i0 + j < M && key[j + 1] != key[j]) flags |= 1u << j;
+    int at = ordered_slot(__popc(flags), part, &count);
+#pragma unroll
+    for (int j = 0; j < kOwn; ++j)
+      if (flags & (1u << j)) runs[at++] = static_cast<int>(i0 + j);
+  }
+  __syncthreads();
+  const int num = count;
+  count = 0;
+  for (int b = 0; b < num; b += kRunThreads) {
+    const int j = b + static_cast<int>(threadIdx.x);
+    bool flag = false;
+    int start = 0;
+    if (j < num) {
+      start = runs[j];
+      const int next = j + 1 < num ? runs[j + 1] : M;
+      flag = j == 0 || next - start >= kLongRun || start - runs[j - 1] >= kLongRun;
+    }
+    const int at = ordered_slot(flag ? 1 : 0, part, &count);
+    if (flag) offsets[at] = start;
+  }
+  for (int j = count + static_cast<int>(threadIdx.x); j <= most; j += kRunThreads) offsets[j] = M;
+  griddep_wait();
+}
+
+// Most runs' starts there can be: two for each long run, and the first row.
+int64_t lora_most_tiles(int64_t M) { return 2 * (M / kLongRun) + 1; }
+
+int launch_runs(const int* ids, int M, int adapters, int* runs, int* offsets, cudaStream_t stream) {
+  cudaLaunchConfig_t cfg{};
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.gridDim = dim3(1, 1, 1);
+  cfg.blockDim = dim3(kRunThreads, 1, 1);
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, lora_runs_kernel, ids, M, adapters, runs, offsets,
+                                           static_cast<int>(lora_most_tiles(M)));
+  return e == cudaSuccess ? TG_OK : cuda_fail(e);
+}
+
 template <int kRt>
 int launch_down(DownArgs a, cudaStream_t stream, DeviceCtx* ctx) {
   static std::atomic<int> prepared[64];
@@ -210,16 +308,19 @@ bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) ==
 
 // Rows up to which the weights' stream bounds the product: single CTAs with a
 // split contraction and the adapter term in the epilogue.
-constexpr int kLoraFewRows = 128;
+constexpr int kLoraFewRows = 256;
 // Rows up to which lora_down_kernel alone computes H (it reads `down` once per
 // 8 rows).
 constexpr int kLoraDownRows = 1024;
 
 }  // namespace
 
-// H: two bf16 terms.
+// H: two bf16 terms; for many rows also the runs and the tile starts.
 size_t lora_workspace_bytes(int64_t M, int64_t rank) {
-  return (static_cast<size_t>(M) * static_cast<size_t>(rank) * 4u + 255u) / 256u * 256u;
+  const size_t h = (static_cast<size_t>(M) * static_cast<size_t>(rank) * 4u + 255u) / 256u * 256u;
+  return M <= kLoraFewRows
+             ? h
+             : h + (static_cast<size_t>(M) + static_cast<size_t>(lora_most_tiles(M)) + 1u) * 4u;
 }
 
 }  // namespace tg
@@ -300,10 +401,17 @@ extern "C" int gemm_bf16_lora(const void* A, int64_t lda, const void* B, int64_t
   o.cols_ld = lda;
   o.k = K;
   d.leave_few = M > kLoraDownRows;
+  int* runs = reinterpret_cast<int*>(static_cast<uint8_t*>(ws) +
+                                     (static_cast<size_t>(M) * rank * 4u + 255u) / 256u * 256u);
+  int* starts = runs + M;
   rc = rank <= 16   ? launch_down<1>(d, stream, ctx)
        : rank <= 32 ? launch_down<2>(d, stream, ctx)
                     : launch_down<4>(d, stream, ctx);
   if (rc != TG_OK) return rc;
+  if (!few) {
+    rc = launch_runs(ids, static_cast<int>(M), static_cast<int>(adapters), runs, starts, stream);
+    if (rc != TG_OK) return rc;
+  }
   if (d.leave_few) {
     GroupedArgs h = a;
     h.wide = static_cast<int>(rank);
@@ -340,6 +448,8 @@ extern "C" int gemm_bf16_lora(const void* A, int64_t lda, const void* B, int64_t
   if (few)
     return bf16 ? launch_grouped<GroupedCfg<kAdapter, 1, 128, 6, true>>(o, a, stream, ctx)
                 : launch_grouped<GroupedCfg<kAdapter, 1, 128, 6, false>>(o, a, stream, ctx);
+  a.offsets = starts;
+  a.groups = static_cast<int>(lora_most_tiles(M));
   return bf16 ? launch_grouped<GroupedCfg<kAdapter, 2, 256, 6, true>>(o, a, stream, ctx)
               : launch_grouped<GroupedCfg<kAdapter, 2, 256, 6, false>>(o, a, stream, ctx);
 }

@@ -38,8 +38,10 @@
 // into two bf16 terms (hi + lo keep 16 bits of it, so the product with
 // up[id] is as exact as the base product).  After the tile's K stages each
 // adapter that occurs among the tile's rows adds ceil(rank / 64) * 2 stages of
-// up[id] and H.  Where all rows of the tile have one adapter, TMA loads both;
-// else the fixing warps write H with zeros in the rows of other adapters.
+// up[id] and H.  Where all rows of the tile have one adapter, TMA loads both
+// (tiles start where a long run of rows with one adapter does: there the
+// offsets are those of the runs); else the fixing warps write H with zeros in
+// the rows of other adapters.
 // The base product and every adapter's term meet in one
 // accumulator: D is written once.  A zero row times an infinite or NaN
 // weight would still be NaN, so where a tile's rows differ in their adapter
@@ -287,7 +289,7 @@ struct GroupWalk {
     const int r1 = __shfl_sync(0xFFFFFFFFu, hi, src);
     const int before = __shfl_sync(0xFFFFFFFFu, incl, src > 0 ? src - 1 : 0);
     const int l = t - t0 - (src > 0 ? before : 0);
-    w.g = g0 + src;
+    w.g = C::kMode == kAdapter ? 0 : g0 + src;   // (adapters: one shared operand)
     w.tile = t;
     w.piece = piece;
     // Tiles of a group: bands of 16 column tiles, within a band the column
@@ -432,6 +434,27 @@ __device__ __forceinline__ bool few_adapters(const uint32_t (&ids)[kPer], uint32
     if (id < 0) return true;
   }
   return false;
+}
+
+// Where the rank leaves room in the 128 lanes, one pass over a tile's rows does
+// several of its adapters: slots of 32, 64 or 128 lanes, one adapter each.
+__device__ __forceinline__ int down_slot(int rank) { return rank <= 32 ? 32 : rank <= 64 ? 64 : 128; }
+// The pass's adapters: up to 128 / slot of them, -1 where there are no more;
+// `last` moves on to the last one taken.
+template <int kPer>
+__device__ __forceinline__ int next_adapters(const uint32_t (&ids)[kPer], int& last, int most,
+                                             uint32_t adapters, int (&out)[4]) {
+  int n = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    out[i] = i < most && (i == 0 || out[i > 0 ? i - 1 : 0] >= 0) ? next_adapter(ids, last, adapters)
+                                                                 : -1;
+    if (out[i] >= 0) {
+      last = out[i];
+      ++n;
+    }
+  }
+  return n;
 }
 
 // x as two bf16 terms; what is infinite or NaN in hi is in hi alone.
@@ -833,9 +856,10 @@ __global__ void __launch_bounds__(C::kThreads, 1)
   const uint32_t tmem_base = *tmem_slot;
   // The few-row adapter product streams its weights beside the kernel that
   // computes H, which started only when its own inputs (this one's A, B and
-  // ids among them) were there: only the epilogue, which reads H and writes,
-  // waits for it.
-  if (!(C::kMode == kAdapter && C::kSplit) || warp >= C::kEpiWarp0) griddep_wait();
+  // ids among them) were there, and so does kAdapterDown beside the kernels
+  // before it: only the epilogue, which reads H and writes, waits for them.
+  constexpr bool kEarly = (C::kMode == kAdapter && C::kSplit) || C::kMode == kAdapterDown;
+  if (!kEarly || warp >= C::kEpiWarp0) griddep_wait();
 
   const WaitGuard guard{p.status, abort_flag, p.timeout_ns};
   const int unit = blockIdx.x / C::kCtaGroup;
@@ -916,19 +940,25 @@ __global__ void __launch_bounds__(C::kThreads, 1)
         uint32_t ids[C::kTileN / 32];
         load_tile_ids<C>(p, w, lane, ids);
         if (!few_adapters(ids, p.adapters)) continue;
-        for (int id = next_adapter(ids, -1, p.adapters); id >= 0 && ok;
-             id = next_adapter(ids, id, p.adapters)) {
+        const int slot = down_slot(p.rank);
+        int last = -1, group[4];
+        for (int n = next_adapters(ids, last, 128 / slot, p.adapters, group); n > 0 && ok;
+             n = next_adapters(ids, last, 128 / slot, p.adapters, group)) {
           if (lane == 0) {
             for (int j = 0, kb = w.k0; j < w.nk; ++j, kb += w.ks) {
               if (!wait_slot()) {
                 ok = 0;
                 break;
               }
+              const uint32_t fb = full0 + 8u * stage;
               mbar_arrive_expect_tx(&full_bar[stage],
-                                    static_cast<uint32_t>(p.wide_box + crows) * 128u);
-              tma_load_3d(sW + stage * C::W_BYTES, &tmW, full0 + 8u * stage, kb * 64, wx, id, pol);
-              tma_load_2d(sC + stage * C::C_BYTES, &tmC.box[crows / 16 - 1], full0 + 8u * stage,
-                          kb * 64, crow0, pol);
+                                    static_cast<uint32_t>(n * p.wide_box + crows) * 128u);
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                if (group[i] >= 0)
+                  tma_load_3d(sW + stage * C::W_BYTES + 128 * slot * i, &tmW, fb, kb * 64, wx,
+                              group[i], pol);
+              tma_load_2d(sC + stage * C::C_BYTES, &tmC.box[crows / 16 - 1], fb, kb * 64, crow0, pol);
               next_slot();
             }
           }
@@ -1103,16 +1133,15 @@ __global__ void __launch_bounds__(C::kThreads, 1)
         take(u);
         const uint32_t idesc =
             idesc_bf16_f32_major(128 * C::kCtaGroup, w.ncols, C::kWideMn, C::kColMn);
-        // kAdapterDown: one contraction for each adapter of the tile.
+        // kAdapterDown: one contraction for each of the tile's passes.
         int passes = 1;
         if constexpr (C::kMode == kAdapterDown) {
           uint32_t ids[C::kTileN / 32];
           load_tile_ids<C>(p, w, lane, ids);
           passes = 0;
+          int last = -1, group[4];
           if (few_adapters(ids, p.adapters))
-            for (int id = next_adapter(ids, -1, p.adapters); id >= 0;
-                 id = next_adapter(ids, id, p.adapters))
-              ++passes;
+            while (next_adapters(ids, last, 128 / down_slot(p.rank), p.adapters, group) > 0) ++passes;
         }
         const int chunks = grouped_chunks<C>(w.nk);   // an empty contraction has none
         uint32_t d_tmem = 0;
@@ -1325,8 +1354,10 @@ __global__ void __launch_bounds__(C::kThreads, 1)
               const int np = cw / 8;
               const uint32_t part = sW + stage * C::W_BYTES + fw * (C::W_BYTES / 2);
 #pragma unroll 4
-              for (int j = lane; j < 64 * np; j += 32) {
-                const uint32_t row = static_cast<uint32_t>(j / np), c = static_cast<uint32_t>(j % np);
+              for (int i = 0; i < 16; ++i) {
+                const uint32_t row = static_cast<uint32_t>(4 * i + (lane >> 3));
+                const uint32_t c = static_cast<uint32_t>(q);
+                if (q >= np) break;
                 const uint32_t a = part + 128 * row;
                 uint4 u4 = ld_shared_v4(a + ((c ^ (row & 7u)) << 4));
                 if (has_nonfinite(u4)) {
@@ -1415,19 +1446,23 @@ __global__ void __launch_bounds__(C::kThreads, 1)
       const int blocks = (w.rows + 31) / 32;   // of 32 accumulator columns
       const uint32_t t_slab = tmem_base + (static_cast<uint32_t>(slab * 32) << 16);
       if constexpr (C::kMode == kAdapterDown) {
-        // Column block `half` is this warp's 32 rows; x is the rank index.
-        // Every row is written once, by its own adapter's pass.
+        // Column block `half` is this warp's 32 rows; its lanes are rank
+        // indices xr of slot number `mine`.  Every row is written once, by its
+        // own adapter's slot.
         uint32_t ids[C::kTileN / 32];
         load_tile_ids<C>(p, w, lane, ids);
         if (!few_adapters(ids, p.adapters)) continue;
+        const int slot = down_slot(p.rank);
+        const int mine = 32 * slab / slot;
+        const int xr = w.wide0 + 32 * slab % slot + lane;
         const int row0 = w.row0 + 32 * half;
         float* part = p.partials + static_cast<int64_t>(w.piece) * p.M * p.rank;
-        auto keep = [&](int row, float s) {
-          const int64_t o = static_cast<int64_t>(row) * p.rank + x;
+        auto keep = [&](int row, int r, float s) {
+          const int64_t o = static_cast<int64_t>(row) * p.rank + r;
           split_bf16(s, p.h_hi[o], p.h_lo[o]);
         };
-        for (int id = next_adapter(ids, -1, p.adapters); id >= 0;
-             id = next_adapter(ids, id, p.adapters)) {
+        int last_id = -1, group[4];
+        while (next_adapters(ids, last_id, 128 / slot, p.adapters, group) > 0) {
           if (!acc_ready()) {
             ok = false;
             break;
@@ -1435,14 +1470,16 @@ __global__ void __launch_bounds__(C::kThreads, 1)
           float v[32];
           grouped_read<false>(t_slab + static_cast<uint32_t>(acc * C::kTileN + 32 * half), v);
           hand_back();
+          const int id = mine == 0 ? group[0] : mine == 1 ? group[1] : mine == 2 ? group[2] : group[3];
+          if (id < 0 || xr >= p.wide) continue;
           const float scale = p.scales ? p.scales[id] : 1.0f;
 #pragma unroll
           for (int j = 0; j < 32; ++j) {
-            if (row0 + j >= end || x >= p.wide || p.ids[row0 + j] != id) continue;
+            if (row0 + j >= end || p.ids[row0 + j] != id) continue;
             if (S > 1)
-              __stcg(part + static_cast<int64_t>(row0 + j) * p.rank + x, v[j] * scale);
+              __stcg(part + static_cast<int64_t>(row0 + j) * p.rank + xr, v[j] * scale);
             else
-              keep(row0 + j, v[j] * scale);
+              keep(row0 + j, xr, v[j] * scale);
           }
         }
         if (!ok) break;
@@ -1479,7 +1516,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
             for (int j = 0; j < 8; ++j)
               if (row0 + j0 + j < end && static_cast<uint32_t>(p.ids[row0 + j0 + j]) <
                                              static_cast<uint32_t>(p.adapters))
-                keep(row0 + j0 + j, s[j]);
+                keep(row0 + j0 + j, x, s[j]);
           }
         }
       } else if constexpr (C::kSplit) {
