@@ -170,7 +170,7 @@ __global__ void __launch_bounds__(32 * kDownWarps) lora_down_kernel(const DownAr
 // at least kLongRun rows with one adapter, and after it.  Shorter runs between
 // them stay together.  One block: two ordered compactions (rows where the
 // adapter changes; of those, the ones next to a long run).
-constexpr int kLongRun = 128;
+constexpr int kLongRun = 192;
 constexpr int kRunThreads = 1024;
 
 // Position of the first of this thread's `items` among the block's, after

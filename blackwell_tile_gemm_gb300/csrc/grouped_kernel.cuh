@@ -199,6 +199,17 @@ struct GroupedWork {
   int piece;
 };
 
+// a / b for a >= 0, b > 0: the float quotient of numbers below 2^22 is off by
+// less than one.
+__device__ __forceinline__ int small_div(int a, int b) {
+  if (a >= 1 << 22) return a / b;
+  int q = __float2int_rd(__fdividef(static_cast<float>(a), static_cast<float>(b)));
+  const int r = a - q * b;
+  if (r < 0) --q;
+  if (r >= b) ++q;
+  return q;
+}
+
 __device__ __forceinline__ int grouped_clamp(int v, int hi) { return min(max(v, 0), hi); }
 
 // Tile index -> group, by one warp.  The lanes hold the row ranges of 32
@@ -211,6 +222,8 @@ struct GroupWalk {
   int g0, t0, lo0;   // window: first group, tiles and first row before it
   int lo, hi, incl;  // this lane's group: rows [lo, hi), tiles up to and with it
   bool bad;
+  // The group found last: its tiles [begin, end), rows [r0, r1), column tiles.
+  int begin, end, r0, r1, group, nct, size;
 
   __device__ __forceinline__ void load(const GroupedArgs& p, int lane) {
     const int g = g0 + lane;
@@ -249,6 +262,7 @@ struct GroupWalk {
   __device__ __forceinline__ void start(const GroupedArgs& p, int lane) {
     g0 = 0;
     t0 = 0;
+    begin = end = 0;
     bad = false;
     lo0 = 0;
     if (p.offsets != nullptr) {
@@ -279,28 +293,44 @@ struct GroupWalk {
     }
     return t;
   }
-  // Tile t < total, t not below the last one asked for.
-  __device__ __forceinline__ void find(const GroupedArgs& p, int lane, int t, int piece, int S,
-                                       GroupedWork& w) {
+  // The group that holds tile t (< total, not below the last one asked for).
+  __device__ __forceinline__ void seek(const GroupedArgs& p, int lane, int t) {
     while (t >= t0 + __shfl_sync(0xFFFFFFFFu, incl, 31) && g0 + 32 < p.groups) advance(p, lane);
     const uint32_t above = __ballot_sync(0xFFFFFFFFu, t0 + incl > t);
     const int src = above ? __ffs(above) - 1 : 31;
-    const int r0 = __shfl_sync(0xFFFFFFFFu, lo, src);
-    const int r1 = __shfl_sync(0xFFFFFFFFu, hi, src);
+    r0 = __shfl_sync(0xFFFFFFFFu, lo, src);
+    r1 = __shfl_sync(0xFFFFFFFFu, hi, src);
     const int before = __shfl_sync(0xFFFFFFFFu, incl, src > 0 ? src - 1 : 0);
-    const int l = t - t0 - (src > 0 ? before : 0);
-    w.g = C::kMode == kAdapter ? 0 : g0 + src;   // (adapters: one shared operand)
+    begin = t0 + (src > 0 ? before : 0);
+    end = t0 + __shfl_sync(0xFFFFFFFFu, incl, src);
+    group = C::kMode == kAdapter ? 0 : g0 + src;   // (adapters: one shared operand)
+    nct = C::kColMn ? p.num_col_tiles : (r1 - r0 + C::kTileN - 1) / C::kTileN;
+    // The group's rows in nct tiles of equal size (a multiple of kColStep).
+    size = C::kMode == kAdapterDown || C::kColMn
+               ? C::kTileN
+               : ((r1 - r0 + nct - 1) / nct + C::kColStep - 1) / C::kColStep * C::kColStep;
+  }
+  __device__ __forceinline__ void find(const GroupedArgs& p, int lane, int t, int piece, int S,
+                                       GroupedWork& w) {
+    // Most tiles are in the last one's group: every role's warp asks for
+    // every tile, and a short tile waits for the answer.
+    if (t >= end || t < begin) seek(p, lane, t);
+    const int l = t - begin;
+    w.g = group;
     w.tile = t;
     w.piece = piece;
     // Tiles of a group: bands of 16 column tiles, within a band the column
     // tile fastest, so that the units running at the same time share a
     // weight panel and the band's rows stay in L2.
-    const int nct = C::kColMn ? p.num_col_tiles : (r1 - r0 + C::kTileN - 1) / C::kTileN;
-    const int first = l / (16 * p.num_wide_tiles) * 16;
-    const int gm = min(nct - first, 16);
-    const int r = l - first * p.num_wide_tiles;
-    const int ct = first + r % gm;
-    w.wide0 = r / gm * (128 * C::kCtaGroup);
+    int first = 0, gm = nct, r = l;
+    if (nct > 16) {
+      first = l / (16 * p.num_wide_tiles) * 16;
+      gm = min(nct - first, 16);
+      r = l - first * p.num_wide_tiles;
+    }
+    const int wt = small_div(r, gm);
+    const int ct = first + r - wt * gm;
+    w.wide0 = wt * (128 * C::kCtaGroup);
     if constexpr (C::kColMn) {
       w.row0 = ct * C::kTileN;
       w.rows = min(C::kTileN, p.cols - w.row0);
@@ -311,11 +341,6 @@ struct GroupWalk {
       w.k0 = 0;
       w.ks = 1;
     } else {
-      // The group's rows in nct tiles of equal size (a multiple of kColStep).
-      const int size =
-          C::kMode == kAdapterDown
-              ? C::kTileN
-              : ((r1 - r0 + nct - 1) / nct + C::kColStep - 1) / C::kColStep * C::kColStep;
       w.row0 = r0 + ct * size;
       w.rows = min(size, r1 - w.row0);
       w.ncols = (w.rows + C::kColStep - 1) / C::kColStep * C::kColStep;
