@@ -54,6 +54,8 @@ TG_CALL_GEMM_BF16_SKINNY = 4
 TG_CALL_GEMM_BF16_GATHER = 5
 TG_CALL_GROUP_ROWS = 6
 TG_CALL_GEMM_BF16_LORA = 7
+TG_MAX_GROUPS = 4096
+TG_MAX_RANK = 256
 TG_CLOCK_BF16 = 0
 TG_CLOCK_MXFP8 = 1
 TG_CLOCK_MXFP4 = 2

@@ -91,12 +91,7 @@ int gemm_bf16_grouped(const void* A, int64_t lda, int64_t a_rows, const int32_t*
   o.cols = A;
   o.cols_ld = lda;
   o.k = K;
-  const bool bf16 = d_dtype == TG_D_BF16;
-  if (grouped_few_rows(M, groups))
-    return bf16 ? launch_grouped<GroupedCfg<kGroupedForward, 1, 64, 9, true>>(o, a, stream, ctx)
-                : launch_grouped<GroupedCfg<kGroupedForward, 1, 64, 9, false>>(o, a, stream, ctx);
-  return bf16 ? launch_grouped<GroupedCfg<kGroupedForward, 2, 256, 6, true>>(o, a, stream, ctx)
-              : launch_grouped<GroupedCfg<kGroupedForward, 2, 256, 6, false>>(o, a, stream, ctx);
+  return launch_grouped_forward(d_dtype == TG_D_BF16, o, a, stream, ctx);
 }
 
 int gemm_bf16_grouped_dgrad(const void* G, int64_t ldg, const int32_t* offsets, int64_t groups,
@@ -135,9 +130,7 @@ int gemm_bf16_grouped_dgrad(const void* G, int64_t ldg, const int32_t* offsets, 
   o.cols = G;
   o.cols_ld = ldg;
   o.k = N;
-  return d_dtype == TG_D_BF16
-             ? launch_grouped<GroupedCfg<kGroupedDgrad, 2, 256, 6, true>>(o, a, stream, ctx)
-             : launch_grouped<GroupedCfg<kGroupedDgrad, 2, 256, 6, false>>(o, a, stream, ctx);
+  return launch_grouped_dgrad(d_dtype == TG_D_BF16, o, a, stream, ctx);
 }
 
 int gemm_bf16_grouped_wgrad(const void* G, int64_t ldg, const void* A, int64_t lda,
@@ -182,6 +175,7 @@ int gemm_bf16_grouped_wgrad(const void* G, int64_t ldg, const void* A, int64_t l
   a.wide = static_cast<int>(K);
   a.cols = static_cast<int>(N);
   a.num_col_tiles = ceil_div_i(N, 256);
+  a.num_k_blocks = ceil_div_i(M, 64 * groups);
   a.groups = static_cast<int>(groups);
   a.offsets = offsets;
   a.D = D;
@@ -195,9 +189,7 @@ int gemm_bf16_grouped_wgrad(const void* G, int64_t ldg, const void* A, int64_t l
   o.cols = G;
   o.cols_ld = ldg;
   o.k = M;
-  return d_dtype == TG_D_BF16
-             ? launch_grouped<GroupedCfg<kGroupedWgrad, 2, 256, 6, true>>(o, a, stream, ctx)
-             : launch_grouped<GroupedCfg<kGroupedWgrad, 2, 256, 6, false>>(o, a, stream, ctx);
+  return launch_grouped_wgrad(d_dtype == TG_D_BF16, o, a, stream, ctx);
 }
 
 }  // extern "C"

@@ -85,7 +85,8 @@ struct GroupedArgs {
   int cols;            // wgrad: rows of one group's D; else unused
   int num_wide_tiles;  // tiles of kCtaGroup * 128
   int num_col_tiles;   // wgrad: tiles of kTileN over cols
-  int num_k_blocks;    // stages of 64 of the contraction index (not wgrad)
+  int num_k_blocks;    // stages of 64 of the contraction index (wgrad: of an
+                       // average group, for the choice of pieces only)
   int groups;
   const int* offsets;  // [groups + 1], or null: one group of all M rows
   void* D;
@@ -105,13 +106,14 @@ struct GroupedArgs {
   // split contraction
   int max_slots;           // partial tiles that fit (0: never split)
   int max_counters;
-  float* partials;         // [tile][piece][kTileN][128] f32
-  uint32_t* counters;      // [tile], 0 between launches
+  float* partials;         // [tile][piece][CTA of pair][kTileN][128] f32
+  uint32_t* counters;      // [tile][CTA of pair], 0 between launches
   uint32_t* status;
   uint64_t timeout_ns;
 };
 
-template <int kMode_, int kCtaGroup_, int kTileN_, int kStages_, bool kBf16Out_>
+template <int kMode_, int kCtaGroup_, int kTileN_, int kStages_, bool kBf16Out_,
+          bool kTail_ = kCtaGroup_ == 1>
 struct GroupedCfg {
   static constexpr int kMode = kMode_;
   static constexpr int kCtaGroup = kCtaGroup_;
@@ -121,6 +123,10 @@ struct GroupedCfg {
   static constexpr bool kWideMn = kMode == kGroupedDgrad || kMode == kGroupedWgrad;
   static constexpr bool kColMn = kMode == kGroupedWgrad;
   static constexpr bool kSplit = kCtaGroup == 1;
+  // Whether a last wave may be cut into pieces (grouped_plan).  Pairs carry the
+  // join only where it can pay: it costs the others registers and up to 8%
+  // (wgrad of 16 groups x 2048 x 4096 with 128 rows each: 56 -> 60 us).
+  static constexpr bool kTail = kTail_;
   // Adapter stages (MMA form) and ragged contractions are fixed up in shared
   // memory before the MMAs read them.
   static constexpr bool kExt = kMode == kAdapter && kCtaGroup == 2;
@@ -337,9 +343,9 @@ struct GroupWalk {
       w.ncols = w.rows <= 128 ? 128 : 256;
       w.base = r0;
       w.len = r1 - r0;
-      w.nk = (w.len + 63) / 64;
-      w.k0 = 0;
-      w.ks = 1;
+      w.nk = ((w.len + 63) / 64 - piece + S - 1) / S;   // (0 for more pieces than stages)
+      w.k0 = piece;
+      w.ks = S;
     } else {
       w.row0 = r0 + ct * size;
       w.rows = min(size, r1 - w.row0);
@@ -369,29 +375,39 @@ __device__ __forceinline__ int grouped_chunk_end(int nk, int chunks, int c) {
 
 // Full waves of whole tiles, then the tiles of a last, partial wave in pieces
 // of their contraction: the count (at most 8, each piece at least 4 stages)
-// with the least waves * (stages per piece + 14), against the whole tiles'
-// stages + 2.  The 14 stages, 5 us, are what a piece's partial tile, arrival
-// and join take (with 0: 16 rows in 8 groups x 2048 x 2048 43 us instead of 14;
-// without pieces: 4 rows x 4096 x 4096 24 us instead of 14).
+// with the least waves * (stages per piece + join), against the whole tiles'
+// stages + 2.  The join -- a piece's partial tile, its arrival, and the last
+// piece's sum -- takes 14 stages (5 us) for single CTAs (with 0: 16 rows in 8
+// groups x 2048 x 2048 43 us instead of 14; without pieces: 4 rows x 4096 x
+// 4096 24 us instead of 14), and 20 + 6 a piece for CTA pairs, whose partial
+// tiles are 128 KB a CTA (wgrad of 22374 rows in 2 groups x 896 x 768 62 -> 40
+// us, 1444 rows x 1086 x 7085 40 -> 34 us).
 struct GroupedPlan {
   int full;    // tiles run whole
   int S;       // pieces of the others
   int items;   // units of work
 };
-template <bool kSplit>
+// A few-row tile's adapter term, which its pieces share out too, runs beside
+// the contraction: about 6 stages' time for each 8 rows of a warp and 32 of
+// the rank (39 rows x 1229 x 638, rank 128: 36 -> 28 us).
+template <class C>
 __device__ __forceinline__ GroupedPlan grouped_plan(const GroupedArgs& p, int tiles, int units) {
   GroupedPlan g{tiles, 1, tiles};
-  if constexpr (kSplit) {
-    const int full = tiles / units * units;
-    const int rest = tiles - full;
-    int cost = p.num_k_blocks + 2;
-    for (int c = 2; c <= 8 && rest > 0; ++c) {
-      if (p.num_k_blocks < 4 * c || rest * c > p.max_slots || rest > p.max_counters) break;
-      const int v = (rest * c + units - 1) / units * ((p.num_k_blocks + c - 1) / c + 14);
-      if (v < cost) {
-        cost = v;
-        g = GroupedPlan{full, c, full + rest * c};
-      }
+  if constexpr (!C::kTail) return g;
+  constexpr bool kTerms = C::kMode == kAdapter && C::kSplit;
+  const int full = tiles / units * units;
+  const int rest = tiles - full;
+  const int terms = kTerms ? (min(p.M, C::kTileN) + 15) / 16 * ((p.rank + 31) / 32) * 6 : 0;
+  int cost = (max(p.num_k_blocks, terms) + 2) * 4 / 5;   // pieces have to gain a fifth
+  for (int c = 2; c <= 8 && rest > 0; ++c) {
+    if (p.num_k_blocks < (kTerms ? c : 4 * c) || rest * c > p.max_slots || rest > p.max_counters)
+      break;
+    const int join = C::kCtaGroup == 1 ? 14 : 20 + 6 * c;
+    const int v = (rest * c + units - 1) / units *
+                  ((max(p.num_k_blocks, terms) + c - 1) / c + join);
+    if (v < cost) {
+      cost = v;
+      g = GroupedPlan{full, c, full + rest * c};
     }
   }
   return g;
@@ -893,13 +909,13 @@ __global__ void __launch_bounds__(C::kThreads, 1)
   GroupWalk<C> walk;
   int first_row, end_row;
   const int tiles = walk.total(p, lane, &first_row, &end_row);
-  const GroupedPlan plan = grouped_plan<C::kSplit>(p, tiles, num_units);
+  const GroupedPlan plan = grouped_plan<C>(p, tiles, num_units);
   const int num_items = plan.items;
   GroupedWork w;
   // Work item u of the grid: S pieces from tile plan.full on.
   int S = 1;
   auto take = [&](int u) {
-    if (C::kSplit && u >= plan.full) {
+    if (C::kTail && u >= plan.full) {
       const int v = u - plan.full;
       S = plan.S;
       walk.find(p, lane, plan.full + v / S, v % S, S, w);
@@ -1074,7 +1090,8 @@ __global__ void __launch_bounds__(C::kThreads, 1)
         uint32_t ids[C::kTileN / 32];
         load_tile_ids<C>(p, w, lane, ids);
         const bool mixed = mixed_adapters(ids, w.rows, lane, p.adapters);
-        for (int id = next_adapter(ids, -1, p.adapters); id >= 0 && ok;
+        // (A split tile's adapter stages belong to its first piece.)
+        for (int id = w.piece == 0 ? next_adapter(ids, -1, p.adapters) : -1; id >= 0 && ok;
              id = next_adapter(ids, id, p.adapters)) {
           if (lane == 0) {
             const int per = (p.rank + 63) / 64 * 64;
@@ -1234,7 +1251,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
           load_tile_ids<C>(p, w, lane, ids);
           const int per = (p.rank + 63) / 64 * 64;
           const bool mixed = mixed_adapters(ids, w.rows, lane, p.adapters);
-          for (int id = next_adapter(ids, -1, p.adapters); id >= 0 && ok;
+          for (int id = w.piece == 0 ? next_adapter(ids, -1, p.adapters) : -1; id >= 0 && ok;
                id = next_adapter(ids, id, p.adapters)) {
             if (lane == 0) {
               const int stages = adapter_stages(p.rank, mixed);
@@ -1293,7 +1310,8 @@ __global__ void __launch_bounds__(C::kThreads, 1)
         take(u);
         if constexpr (C::kMode == kGroupedWgrad) {
           const int rest = w.len & 63;
-          if (rest != 0) {
+          // The ragged stage is the last one of the piece that has it.
+          if (rest != 0 && w.len / 64 % w.ks == w.k0) {
             const int stage = static_cast<int>((pos + w.nk - 1) % C::kStages);
             const uint32_t par = (tail_use >> stage) & 1u;
             tail_use ^= 1u << stage;
@@ -1319,6 +1337,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
           pos += w.nk;
         } else {
           pos += w.nk;
+          if (w.piece != 0) continue;
           uint32_t ids[C::kTileN / 32];
           load_tile_ids<C>(p, w, lane, ids);
           const int per = (p.rank + 63) / 64 * 64;
@@ -1424,13 +1443,13 @@ __global__ void __launch_bounds__(C::kThreads, 1)
     // Waits for the next accumulator.
     auto acc_ready = [&]() -> bool {
       int got = 1;
-      if ((C::kSplit && S > 1) || (C::kStaged && C::kBf16Out)) {
+      if ((C::kTail && S > 1) || (C::kStaged && C::kBf16Out)) {
         // Warps that meet at named barriers below (all of a split tile's, the
         // two that share a staging box) must agree whether the accumulator
         // arrived: one thread of them decides.
-        const bool decides = C::kSplit ? warp == C::kEpiWarp0 && lane == 0 : box_lead;
-        const int id = C::kSplit ? 1 : 2 + box, count = C::kSplit ? 32 * C::kEpiWarps : 64;
-        volatile int* flag = go + (C::kSplit ? 0 : box);
+        const bool decides = C::kTail && S > 1 ? warp == C::kEpiWarp0 && lane == 0 : box_lead;
+        const int id = C::kTail && S > 1 ? 1 : 2 + box, count = C::kTail && S > 1 ? 32 * C::kEpiWarps : 64;
+        volatile int* flag = go + (C::kTail && S > 1 ? 0 : box);
         if (decides) *flag = mbar_wait(&accf_bar[acc], acc_phase, guard, kSiteGrAccFull) ? 1 : 0;
         named_bar_sync(id, count);
         got = *flag;
@@ -1455,6 +1474,54 @@ __global__ void __launch_bounds__(C::kThreads, 1)
       if (++acc == C::kAccBufs) {
         acc = 0;
         acc_phase ^= 1u;
+      }
+    };
+    // Split tiles: this lane's column of the piece's partial tile, [column of
+    // the accumulator][128 lanes] for each CTA.
+    constexpr int64_t kPart = C::kTileN * 128;
+    auto part_of = [&](int piece) {
+      return p.partials +
+             ((static_cast<int64_t>(w.tile) * S + piece) * C::kCtaGroup + rank) * kPart + slab * 32 +
+             lane;
+    };
+    auto publish = [&](int col, int left, const float (&v)[32]) {
+      float* dst = part_of(w.piece) + col * 128;
+#pragma unroll
+      for (int i = 0; i < 32; ++i)
+        if (i < left) __stcg(dst + i * 128, v[i]);
+    };
+    // True in the CTA whose arrival is the tile's last: all partials are there.
+    auto joined = [&]() -> bool {
+      __threadfence();
+      named_bar_sync(1, 32 * C::kEpiWarps);
+      if (warp == C::kEpiWarp0 && lane == 0) {
+        uint32_t* counter = p.counters + w.tile * C::kCtaGroup + static_cast<int>(rank);
+        const int last = arrive_counter_gpu(counter) == static_cast<uint32_t>(S - 1);
+        if (last) *counter = 0u;
+        *join = last;
+      }
+      named_bar_sync(1, 32 * C::kEpiWarps);
+      if (!*join) return false;
+      __threadfence();
+      return true;
+    };
+    // The pieces' sum, in piece order.  All 32 columns, also those past the
+    // tile's rows (the slot has them; they are not stored): unconditional
+    // loads fly together.
+    auto collect = [&](int col, float (&v)[32]) {
+      const float* src = part_of(0) + col * 128;
+#pragma unroll
+      for (int i = 0; i < 32; ++i) v[i] = __ldcg(src + i * 128);
+      for (int r = 1; r < S; ++r) {
+        src += C::kCtaGroup * kPart;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          float t[16];
+#pragma unroll
+          for (int i = 0; i < 16; ++i) t[i] = __ldcg(src + (16 * h + i) * 128);
+#pragma unroll
+          for (int i = 0; i < 16; ++i) v[16 * h + i] += t[i];
+        }
       }
     };
     bool ok = true;
@@ -1501,14 +1568,14 @@ __global__ void __launch_bounds__(C::kThreads, 1)
 #pragma unroll
           for (int j = 0; j < 32; ++j) {
             if (row0 + j >= end || p.ids[row0 + j] != id) continue;
-            if (S > 1)
+            if (C::kTail && S > 1)
               __stcg(part + static_cast<int64_t>(row0 + j) * p.rank + xr, v[j] * scale);
             else
               keep(row0 + j, xr, v[j] * scale);
           }
         }
         if (!ok) break;
-        if (S > 1) {
+        if (C::kTail && S > 1) {
           __threadfence();
           named_bar_sync(1, 32 * C::kEpiWarps);
           if (warp == C::kEpiWarp0 && lane == 0) {
@@ -1569,48 +1636,15 @@ __global__ void __launch_bounds__(C::kThreads, 1)
           hand_back();
         }
         if (!ok) break;
-        if (S > 1) {
-          // Publish the piece's partial; the last of the tile's pieces adds
-          // them all in piece order.
-          float* part = p.partials + static_cast<int64_t>(w.tile) * S * (C::kTileN * 128) +
-                        slab * 32 + lane;
-          float* dst = part + static_cast<int64_t>(w.piece) * (C::kTileN * 128);
+        if (C::kTail && S > 1) {
+          // The last of the tile's pieces adds them all.
 #pragma unroll
-          for (int q = 0; q < kOwn; ++q) {
-            const int col = 32 * (half + 2 * q);
+          for (int q = 0; q < kOwn; ++q)
+            publish(32 * (half + 2 * q), w.rows - 32 * (half + 2 * q), m[q]);
+          if (!joined()) continue;
 #pragma unroll
-            for (int i = 0; i < 32; ++i)
-              if (w.row0 + col + i < end) __stcg(dst + (col + i) * 128, m[q][i]);
-          }
-          __threadfence();
-          named_bar_sync(1, 32 * C::kEpiWarps);
-          if (warp == C::kEpiWarp0 && lane == 0) {
-            const int last =
-                arrive_counter_gpu(p.counters + w.tile) == static_cast<uint32_t>(S - 1);
-            if (last) p.counters[w.tile] = 0u;
-            *join = last;
-          }
-          named_bar_sync(1, 32 * C::kEpiWarps);
-          if (!*join) continue;
-          __threadfence();
-#pragma unroll
-          for (int q = 0; q < kOwn; ++q) {
-            const int col = 32 * (half + 2 * q);
-            if (w.row0 + col >= end) continue;
-            // All 32 columns, also those past the tile's rows (the slot has
-            // them; they are not stored): unconditional loads fly together.
-            const float* src = part + col * 128;
-#pragma unroll
-            for (int i = 0; i < 32; ++i) m[q][i] = __ldcg(src + i * 128);
-            for (int r = 1; r < S; ++r) {
-              src += C::kTileN * 128;
-              float t[32];
-#pragma unroll
-              for (int i = 0; i < 32; ++i) t[i] = __ldcg(src + i * 128);
-#pragma unroll
-              for (int i = 0; i < 32; ++i) m[q][i] += t[i];
-            }
-          }
+          for (int q = 0; q < kOwn; ++q)
+            if (half + 2 * q < blocks) collect(32 * (half + 2 * q), m[q]);
         }
 #pragma unroll
         for (int q = 0; q < kOwn; ++q) {
@@ -1635,6 +1669,27 @@ __global__ void __launch_bounds__(C::kThreads, 1)
             bias[i] = epi_uses_bias(p.epi.op) && xb < p.wide
                           ? p.epi.bias[static_cast<int64_t>(w.g) * p.wide + xb]
                           : 0.0f;
+          }
+          if (C::kTail && S > 1) {
+            const bool mark = C::kExt && marked[count & 15] == count + 1;
+            for (int q = half; q < blocks; q += 2) {
+              float v[32];
+              if (chunks > 0)
+                grouped_read<false>(t_slab + static_cast<uint32_t>(acc * C::kTileN + 32 * q), v);
+              else
+                grouped_zero(v);
+              if (mark) add_marked_terms(p, w.row0 + 32 * q, end, x, v);
+              publish(32 * q, w.rows - 32 * q, v);
+            }
+            if (chunks > 0) hand_back();
+            if (!joined()) continue;
+            for (int q = half; q < blocks; q += 2) {
+              float v[32];
+              collect(32 * q, v);
+              grouped_epilogue(p.epi, b, v);
+              grouped_store<C>(p, d0, w.row0 + 32 * q, end, x, v);
+            }
+            continue;
           }
           if (C::kExt && marked[count & 15] == count + 1) {
             for (int q = half; q < blocks; q += 2) {
@@ -1707,13 +1762,23 @@ __global__ void __launch_bounds__(C::kThreads, 1)
             hand_back();
           }
           if (!ok) break;
-          const bool mark = C::kExt && marked[count & 15] == count + 1;
+          if (C::kExt && marked[count & 15] == count + 1) {
+#pragma unroll
+            for (int q = 0; q < kOwn; ++q)
+              add_marked_terms(p, w.row0 + 32 * (half + 2 * q), end, x, m[q]);
+          }
+          if (C::kTail && S > 1) {
+#pragma unroll
+            for (int q = 0; q < kOwn; ++q)
+              publish(32 * (half + 2 * q), w.rows - 32 * (half + 2 * q), m[q]);
+            if (!joined()) continue;
+#pragma unroll
+            for (int q = 0; q < kOwn; ++q)
+              if (half + 2 * q < blocks) collect(32 * (half + 2 * q), m[q]);
+          }
 #pragma unroll
           for (int q = 0; q < kOwn; ++q)
-            if (half + 2 * q < blocks) {
-              if (mark) add_marked_terms(p, w.row0 + 32 * (half + 2 * q), end, x, m[q]);
-              finish(half + 2 * q, m[q]);
-            }
+            if (half + 2 * q < blocks) finish(half + 2 * q, m[q]);
         }
       }
     }

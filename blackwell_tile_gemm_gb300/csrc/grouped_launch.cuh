@@ -33,6 +33,15 @@ inline GroupedArgs grouped_args(DeviceCtx* ctx) {
 // boxes and a split contraction; else CTA pairs with tiles of 256 x 256.
 inline bool grouped_few_rows(int64_t M, int64_t groups) { return M <= 48 * groups; }
 
+// CTA pairs with a split last wave: a contraction of at least 96 stages and
+// tiles for less than two waves (`tiles`: at least so many, sizes of groups
+// being the device's).  22374 rows in 2 groups x 896 x 768, wgrad (24 tiles of
+// 175 stages) 62 -> 40 us; 14613 rows x 640 x 3456, forward (174 tiles of 54)
+// 59 -> 62 us.
+inline bool grouped_tail_pays(int64_t tiles, int64_t k_blocks, DeviceCtx* ctx) {
+  return k_blocks >= 96 && tiles < ctx->num_sms;
+}
+
 template <class C>
 int launch_grouped(const GroupedOperands& operands, const GroupedArgs& args, cudaStream_t stream,
                    DeviceCtx* ctx) {
@@ -79,18 +88,17 @@ int launch_grouped(const GroupedOperands& operands, const GroupedArgs& args, cud
   }
   GroupedArgs a = args;
   a.num_wide_tiles = ceil_div_i(a.wide, 128 * C::kCtaGroup);
-  if constexpr (C::kSplit) {
-    // The tail split's scratch: [tile][piece] partial tiles, one counter a tile.
-    float* part = nullptr;
-    uint32_t* counters = nullptr;
-    if (tail_scratch(stream, &part, &counters)) {
-      a.partials = part;
-      a.counters = counters;
-      // kAdapterDown: [piece][row][rank] instead.
-      const int wide = C::kMode == kAdapterDown && a.wide < 128 ? a.wide : 128;
-      a.max_slots = static_cast<int>(kTailPartialBytes / (C::kTileN * wide * 4));
-      a.max_counters = kTailFlagWords;
-    }
+  // The tail split's scratch: [tile][piece][CTA] partial tiles, a counter for
+  // each tile and CTA.
+  float* part = nullptr;
+  uint32_t* counters = nullptr;
+  if (tail_scratch(stream, &part, &counters)) {
+    a.partials = part;
+    a.counters = counters;
+    // kAdapterDown: [piece][row][rank] instead.
+    const int wide = C::kMode == kAdapterDown && a.wide < 128 ? a.wide : 128;
+    a.max_slots = static_cast<int>(kTailPartialBytes / (C::kTileN * C::kCtaGroup * wide * 4));
+    a.max_counters = kTailFlagWords / C::kCtaGroup;
   }
   const CUtensorMapDataType bf = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
   const CUtensorMapSwizzle sw = CU_TENSOR_MAP_SWIZZLE_128B;
@@ -157,5 +165,24 @@ int launch_grouped(const GroupedOperands& operands, const GroupedArgs& args, cud
   const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, tW, tW2, tC, tUp, tD, a);
   return e == cudaSuccess ? TG_OK : cuda_fail(e);
 }
+
+// CTA pairs in the form `tail` asks for.
+template <int kMode, int kStages, bool kBf16Out>
+int launch_grouped_pairs(bool tail, const GroupedOperands& o, const GroupedArgs& a,
+                         cudaStream_t stream, DeviceCtx* ctx) {
+  return tail ? launch_grouped<GroupedCfg<kMode, 2, 256, kStages, kBf16Out, true>>(o, a, stream, ctx)
+              : launch_grouped<GroupedCfg<kMode, 2, 256, kStages, kBf16Out, false>>(o, a, stream,
+                                                                                   ctx);
+}
+
+// One translation unit for each (they compile in parallel).
+int launch_grouped_forward(bool bf16, const GroupedOperands& o, const GroupedArgs& a,
+                           cudaStream_t stream, DeviceCtx* ctx);
+int launch_grouped_dgrad(bool bf16, const GroupedOperands& o, const GroupedArgs& a,
+                         cudaStream_t stream, DeviceCtx* ctx);
+int launch_grouped_wgrad(bool bf16, const GroupedOperands& o, const GroupedArgs& a,
+                         cudaStream_t stream, DeviceCtx* ctx);
+int launch_grouped_adapter(bool bf16, const GroupedOperands& o, const GroupedArgs& a,
+                           cudaStream_t stream, DeviceCtx* ctx);
 
 }  // namespace tg
