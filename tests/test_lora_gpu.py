@@ -184,3 +184,58 @@ def test_many_rows_normal_and_broken_adapter(tg):
         got = tg.gemm_bf16_lora(A, B, ids, down2, up)
         assert torch.equal(got[ids != 2], clean[ids != 2])
         assert torch.isnan(got[ids == 2]).all()
+
+
+@pytest.mark.parametrize("M", [24, 200, 1444, 2300])
+def test_same_bits_every_time(tg, M):
+    """Also where a tile's contraction is split between units."""
+    torch = torch_cuda()
+    gen = torch.Generator(device="cuda").manual_seed(M)
+    A, B, down, up = case(gen, normal, M, 520, 7000, 5, 40)
+    ids = ids_of("any", M, 5, M)
+    for dt in (torch.float32, torch.bfloat16):
+        first = tg.gemm_bf16_lora(A, B, ids, down, up, out_dtype=dt)
+        for _ in range(3):
+            assert torch.equal(tg.gemm_bf16_lora(A, B, ids, down, up, out_dtype=dt), first)
+
+
+def test_streams_reservation_and_graphs(tg):
+    torch = torch_cuda()
+    N, K, adapters, rank = 264, 320, 4, 24
+    gen = torch.Generator(device="cuda").manual_seed(3)
+    s = torch.cuda.Stream()
+    for M in (40, 300, 1200):
+        A, B, down, up = case(gen, quarters, M, N, K, adapters, rank)
+        down[..., 64:] = 0
+        kinds = [ids_of(kind, M, adapters, 7) for kind in ("any", "requests", "one")]
+        ids = kinds[0].clone()
+        D = torch.empty(M, N, device="cuda")
+        s.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(s):
+            tg.reserve_workspace(tg.workspace_bytes(tg.TG_CALL_GEMM_BF16_LORA, M, rank, 1))
+            tg.gemm_bf16_lora(A, B, ids, down, up, D)
+            s.synchronize()
+            before = tg.workspace_alloc_count()
+            graph = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(graph, stream=s):
+                tg.gemm_bf16_lora(A, B, ids, down, up, D)
+            for now in kinds:
+                ids.copy_(now)
+                D.fill_(float("nan"))
+                graph.replay()
+                s.synchronize()
+                assert torch.equal(D.double(), definition(torch, A, B, now, down, up, None)[0])
+            assert tg.workspace_alloc_count() == before
+    assert tg.tg_device_status()[0] == tg.TG_OK
+
+
+def test_no_adapters_and_an_empty_contraction(tg):
+    torch = torch_cuda()
+    gen = torch.Generator(device="cuda").manual_seed(4)
+    A, B, down, up = case(gen, quarters, 30, 40, 64, 2, 8)
+    ids = ids_of("any", 30, 2, 1)
+    none = tg.gemm_bf16_lora(A, B, ids, down[:0], up[:0])
+    assert torch.equal(none.double(), A.double() @ B.double().T)
+    got = tg.gemm_bf16_lora(A[:, :0], B[:, :0], ids, down[..., :0], up, epilogue_add=2.0)
+    assert (got == 2.0).all()
+    assert tg.gemm_bf16_lora(A[:0], B, ids[:0], down, up).shape == (0, 40)
