@@ -446,21 +446,33 @@ def _int32_vector(t, name, length=None):
 
 
 def _result(D, shape, out_dtype, device):
-    """(D, its type's code), allocated where the caller gave none: rows start
-    on 16-byte boundaries (a padded view where the width asks for it)."""
+    """(D, its type's code, its row stride), allocated where the caller gave
+    none: rows start on 16-byte boundaries (a padded view where the width asks
+    for it)."""
     if D is None:
         torch = _torch()
         dtype = out_dtype or torch.float32
         code = _d_code(dtype)
         width = shape[-1]
         pad = -width % (4 if code == TG_D_F32 else 8)
-        if pad:
-            return torch.empty(shape[:-1] + (width + pad,), dtype=dtype,
-                               device=device)[..., :width], code
-        return torch.empty(shape, dtype=dtype, device=device), code
+        if pad or not width:
+            ld = width + pad or 8
+            return torch.empty(shape[:-1] + (ld,), dtype=dtype,
+                               device=device)[..., :width], code, ld
+        return torch.empty(shape, dtype=dtype, device=device), code, width
     if D.shape != shape:
         raise ValueError(f"D must be {list(shape)}")
-    return D, _d_code(D.dtype)
+    if len(shape) == 3:
+        return D, _d_code(D.dtype), _stack(D, "D")[3]
+    return D, _d_code(D.dtype), _ld(D, "D", 8)
+
+
+def _raw_stream(stream):
+    """The handle of `stream`, or of the current one, as an integer."""
+    if stream is None:
+        c = _torch()._C
+        return c._cuda_getCurrentRawStream(c._cuda_getDevice())
+    return stream if isinstance(stream, int) else stream.cuda_stream
 
 
 def _epilogue(bias, bias_shape, bias_silu, epilogue_add, silu_affine, affine):
@@ -491,9 +503,9 @@ def group_rows(ids, groups, *, stream=None):
     torch = _torch()
     order = torch.empty_like(ids)
     slot = torch.empty_like(ids)
-    offsets = ids.new_empty(int(groups) + 1)
+    offsets = torch.empty(int(groups) + 1, dtype=torch.int32, device=ids.device)
     rc = (_lib or lib()).tg_group_rows(ptr, n, int(groups), offsets.data_ptr(), order.data_ptr(),
-                                       slot.data_ptr(), _stream_handle(stream))
+                                       slot.data_ptr(), _raw_stream(stream))
     if rc:
         _check(rc, "tg_group_rows")
     return offsets, order, slot
@@ -520,11 +532,11 @@ def gemm_bf16_grouped(A, B, offsets, D=None, *, row_idx=None, out_dtype=None, ep
     a_rows, idx = M, None
     if row_idx is not None:
         M, idx = _int32_vector(row_idx, "row_idx")
-    D, code = _result(D, (M, N), out_dtype, A.device)
+    D, code, ldd = _result(D, (M, N), out_dtype, A.device)
     epi = _epilogue(bias, (groups, N), bias_silu, epilogue_add, silu_affine, affine)
     rc = (_lib or lib()).gemm_bf16_grouped(a, lda, a_rows, idx, off, groups, M, b, ldb, step,
-                                           D.data_ptr(), _ld(D, "D", 8), N, K, code,
-                                           ctypes.byref(epi), 0, _stream_handle(stream))
+                                           D.data_ptr(), ldd, N, K, code,
+                                           ctypes.byref(epi), 0, _raw_stream(stream))
     if rc:
         _check(rc, "gemm_bf16_grouped")
     return D
@@ -542,10 +554,10 @@ def gemm_bf16_grouped_dgrad(G, B, offsets, D=None, *, out_dtype=None, stream=Non
     if N != N2:
         raise ValueError("G is [M, N] and B is [groups, N, K]")
     _, off = _int32_vector(offsets, "offsets", groups + 1)
-    D, code = _result(D, (M, K), out_dtype, G.device)
+    D, code, ldd = _result(D, (M, K), out_dtype, G.device)
     rc = (_lib or lib()).gemm_bf16_grouped_dgrad(g, ldg, off, groups, M, b, ldb, step,
-                                                 D.data_ptr(), _ld(D, "D", 8), N, K, code, 0,
-                                                 _stream_handle(stream))
+                                                 D.data_ptr(), ldd, N, K, code, 0,
+                                                 _raw_stream(stream))
     if rc:
         _check(rc, "gemm_bf16_grouped_dgrad")
     return D
@@ -570,11 +582,11 @@ def gemm_bf16_grouped_wgrad(G, A, offsets, D=None, *, row_idx=None, out_dtype=No
     groups -= 1
     if groups < 1:
         raise ValueError("offsets must have groups + 1 elements")
-    D, code = _result(D, (groups, N, K), out_dtype, G.device)
-    _, _, _, ldd, step, d = _stack(D, "D")
-    rc = (_lib or lib()).gemm_bf16_grouped_wgrad(g, ldg, a, lda, a_rows, idx, off, groups, M, d,
-                                                 ldd, step, N, K, code, 0,
-                                                 _stream_handle(stream))
+    D, code, ldd = _result(D, (groups, N, K), out_dtype, G.device)
+    step = D.stride(0) if groups > 1 else ldd * N
+    rc = (_lib or lib()).gemm_bf16_grouped_wgrad(g, ldg, a, lda, a_rows, idx, off, groups, M,
+                                                 D.data_ptr(), ldd, step, N, K, code, 0,
+                                                 _raw_stream(stream))
     if rc:
         _check(rc, "gemm_bf16_grouped_wgrad")
     return D
@@ -607,12 +619,12 @@ def gemm_bf16_lora(A, B, ids, down, up, D=None, *, scales=None, out_dtype=None, 
             raise TypeError("scales must be a contiguous float32 vector of one value per adapter")
         ps = scales.data_ptr()
     _, idp = _int32_vector(ids, "ids", M)
-    D, code = _result(D, (M, N), out_dtype, A.device)
+    D, code, ldd = _result(D, (M, N), out_dtype, A.device)
     epi = _epilogue(bias, (N,), bias_silu, epilogue_add, silu_affine, affine)
     rc = (_lib or lib()).gemm_bf16_lora(a, lda, b, ldb, idp, pd, ld_down, step_down, pu, ld_up,
                                         step_up, ps, adapters, rank, D.data_ptr(),
-                                        _ld(D, "D", 8), M, N, K, code, ctypes.byref(epi), 0,
-                                        _stream_handle(stream))
+                                        ldd, M, N, K, code, ctypes.byref(epi), 0,
+                                        _raw_stream(stream))
     if rc:
         _check(rc, "gemm_bf16_lora")
     return D

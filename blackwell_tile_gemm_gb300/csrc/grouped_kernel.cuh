@@ -112,6 +112,19 @@ struct GroupedArgs {
   uint64_t timeout_ns;
 };
 
+// Column-operand boxes of a quarter, half, three quarters and the whole of a
+// CTA's rows of the operand: a stage's rows come in one load of the next size.
+// A stage issues as few loads as it can: with 112 rows as boxes of 64 + 32 +
+// 16 the producer, not the MMAs, set the pace (64 groups of 448 rows x 2048 x
+// 4096: 493 us, against 357 us for 512 rows in single boxes).
+// wgrad: box[0] is the 64 x 64 box of the MN-major operand, box[1] the pair
+// of such boxes in one load.
+constexpr int kColBoxes = 4;
+struct ColumnMaps {
+  CUtensorMap box[kColBoxes];
+  CUtensorMap h[2];   // adapters: the two terms of H, boxes of 128 rows
+};
+
 template <int kMode_, int kCtaGroup_, int kTileN_, int kStages_, bool kBf16Out_,
           bool kTail_ = kCtaGroup_ == 1>
 struct GroupedCfg {
@@ -133,6 +146,7 @@ struct GroupedCfg {
   static constexpr int kFixWarps = kExt ? 2 : kMode == kGroupedWgrad ? 1 : 0;
   static constexpr int kColStep = 16 * kCtaGroup;
   static constexpr int C_ROWS = kTileN / kCtaGroup;   // column-operand rows per CTA
+  static constexpr int kBoxStep = C_ROWS / kColBoxes;
   static constexpr int W_BYTES = 128 * 128;
   static constexpr int C_BYTES = C_ROWS * 128;
   static constexpr int OFF_W = 0;
@@ -175,19 +189,6 @@ struct GroupedCfg {
   static_assert(kTileN % 32 == 0 && kTileN <= 256, "MMA N");
   static_assert(C_BYTES % 1024 == 0, "swizzle atoms");
   static_assert(!kColMn || (kCtaGroup == 2 && kTileN == 256), "wgrad tiles");
-};
-
-// Column-operand boxes of 16, 32, ... 128 rows: a stage's rows (a multiple of
-// 16, at most 128 per CTA) come in one load of their exact size.  A stage
-// issues as few loads as it can: with 112 rows as boxes of 64 + 32 + 16 the
-// producer, not the MMAs, set the pace (64 groups of 448 rows x 2048 x 4096:
-// 493 us, against 357 us for 512 rows in single boxes).
-// wgrad: box[0] is the 64 x 64 box of the MN-major operand, box[1] the pair
-// of such boxes in one load.
-constexpr int kColBoxes = 8;
-struct ColumnMaps {
-  CUtensorMap box[kColBoxes];
-  CUtensorMap h[2];   // adapters: the two terms of H, boxes of 128 rows
 };
 
 // One work item.
@@ -973,6 +974,8 @@ __global__ void __launch_bounds__(C::kThreads, 1)
       take(u);
       const int wx = w.wide0 + static_cast<int>(rank) * 128;
       const int crows = w.ncols / C::kCtaGroup;       // column-operand rows of this CTA
+      const int cbox = (crows - 1) / C::kBoxStep;     // K-major: the box that holds them
+      const int loaded = C::kColMn ? crows : (cbox + 1) * C::kBoxStep;
       const int crow0 = w.row0 + static_cast<int>(rank) * crows;
       // MN-major: both of a box pair's 64-element chunks lie inside the row.
       const bool w_chunks = C::kWideMn && wx + 128 <= p.wide;
@@ -993,13 +996,13 @@ __global__ void __launch_bounds__(C::kThreads, 1)
               }
               const uint32_t fb = full0 + 8u * stage;
               mbar_arrive_expect_tx(&full_bar[stage],
-                                    static_cast<uint32_t>(n * p.wide_box + crows) * 128u);
+                                    static_cast<uint32_t>(n * p.wide_box + loaded) * 128u);
 #pragma unroll
               for (int i = 0; i < 4; ++i)
                 if (group[i] >= 0)
                   tma_load_3d(sW + stage * C::W_BYTES + 128 * slot * i, &tmW, fb, kb * 64, wx,
                               group[i], pol);
-              tma_load_2d(sC + stage * C::C_BYTES, &tmC.box[crows / 16 - 1], fb, kb * 64, crow0, pol);
+              tma_load_2d(sC + stage * C::C_BYTES, &tmC.box[cbox], fb, kb * 64, crow0, pol);
               next_slot();
             }
           }
@@ -1008,7 +1011,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
         continue;
       }
       if (lane == 0) {
-        const uint32_t cbytes = static_cast<uint32_t>(crows) * 128u;
+        const uint32_t cbytes = static_cast<uint32_t>(loaded) * 128u;
         for (int j = 0, kb = w.k0; j < w.nk; ++j, kb += w.ks) {
           if (!wait_slot()) {
             ok = 0;
@@ -1072,7 +1075,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
                 tma_load_3d_pair(dW, &tmW, fb, kx, wx, w.g, pol);
               }
             }
-            if (do_cols) tma_load_2d_pair(dC, &tmC.box[crows / 16 - 1], fb, kx, crow0, pol);
+            if (do_cols) tma_load_2d_pair(dC, &tmC.box[cbox], fb, kx, crow0, pol);
           } else {
             if constexpr (C::kWideMn) {
               for (int c = 0; c < 2; ++c)
@@ -1080,7 +1083,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
             } else {
               tma_load_3d(dW, &tmW, fb, kx, wx, w.g, pol);
             }
-            tma_load_2d(dC, &tmC.box[crows / 16 - 1], fb, kx, crow0, pol);
+            tma_load_2d(dC, &tmC.box[cbox], fb, kx, crow0, pol);
           }
           next_slot();
         }

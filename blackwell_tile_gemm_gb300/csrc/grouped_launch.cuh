@@ -126,7 +126,8 @@ int launch_grouped(const GroupedOperands& operands, const GroupedArgs& args, cud
         C::kWideMn ? 64 : C::kMode == kAdapterDown ? a.wide_box : 128, sw);
     if (rc != TG_OK) return rc;
     for (int b = 0; b < kColBoxes; ++b) {
-      rc = make_tensor_map_2d(&tC.box[b], bf, o.cols, o.k, a.M, o.cols_ld * 2, 64, 16 * (b + 1), sw);
+      rc = make_tensor_map_2d(&tC.box[b], bf, o.cols, o.k, a.M, o.cols_ld * 2, 64,
+                              C::kBoxStep * (b + 1), sw);
       if (rc != TG_OK) return rc;
     }
   }
