@@ -41,8 +41,7 @@ struct DownArgs {
   int adapters, rank;
   int k_per_cta;         // multiple of 32 * kDownWarps
   bool leave_few;        // kAdapterDown does the 64-row tiles of few adapters
-  uint16_t* hi;          // [M][rank]: H in two bf16 terms
-  uint16_t* lo;
+  uint16_t* h;           // [M][2][rank]: H in two bf16 terms
 };
 
 // Values k .. k + 7 of a row; those from `end` on are zero and not read.
@@ -153,8 +152,8 @@ __global__ void __launch_bounds__(32 * kDownWarps) lora_down_kernel(const DownAr
             s = part[at];
           }
           s *= scale;
-          const int64_t o = static_cast<int64_t>(row0 + i) * p.rank + r;
-          split_bf16(s, p.hi[o], p.lo[o]);
+          uint16_t* h = p.h + static_cast<int64_t>(row0 + i) * (2 * p.rank) + r;
+          split_bf16(s, h[0], h[p.rank]);
         }
       }
       // The partial sums are free again once every CTA has read them.
@@ -392,16 +391,14 @@ extern "C" int gemm_bf16_lora(const void* A, int64_t lda, const void* B, int64_t
   d.scales = scales;
   d.adapters = static_cast<int>(adapters);
   d.rank = static_cast<int>(rank);
-  d.hi = static_cast<uint16_t*>(ws);
-  d.lo = d.hi + M * rank;
+  d.h = static_cast<uint16_t*>(ws);
   GroupedArgs a = grouped_args(ctx);
   a.M = static_cast<int>(M);
   a.num_k_blocks = ceil_div_i(K, 64);
   a.ids = ids;
   a.adapters = static_cast<int>(adapters);
   a.rank = static_cast<int>(rank);
-  a.h_hi = d.hi;
-  a.h_lo = d.lo;
+  a.h = d.h;
   GroupedOperands o{};
   o.wide_slices = 1;
   o.cols = A;

@@ -40,8 +40,8 @@
 // adapter that occurs among the tile's rows adds ceil(rank / 64) * 2 stages of
 // up[id] and H.  Where all rows of the tile have one adapter, TMA loads both
 // (tiles start where a long run of rows with one adapter does: there the
-// offsets are those of the runs); else the fixing warps write H with zeros in
-// the rows of other adapters.
+// offsets are those of the runs); else the fixing warps put zeros over H's rows
+// of other adapters.
 // The base product and every adapter's term meet in one
 // accumulator: D is written once.  A zero row times an infinite or NaN
 // weight would still be NaN, so where a tile's rows differ in their adapter
@@ -96,8 +96,8 @@ struct GroupedArgs {
   // adapters
   const int* ids;          // [M]
   int adapters, rank;
-  uint16_t* h_hi;          // [M][rank] bf16: the two terms; kAdapterDown writes them
-  uint16_t* h_lo;
+  uint16_t* h;             // [M][2][rank] bf16: the two terms of each row of H; kAdapterDown
+                           // writes them
   const float* scales;     // kAdapterDown: [adapters], or null for 1
   int wide_box;            // kAdapterDown: rows of `down` per load (the lanes
                            // above them hold leftovers and are not stored)
@@ -122,7 +122,7 @@ struct GroupedArgs {
 constexpr int kColBoxes = 4;
 struct ColumnMaps {
   CUtensorMap box[kColBoxes];
-  CUtensorMap h[2];   // adapters: the two terms of H, boxes of 128 rows
+  CUtensorMap h[3];   // adapters: H's first term, its second, and both; boxes of 128 rows
 };
 
 template <int kMode_, int kCtaGroup_, int kTileN_, int kStages_, bool kBf16Out_,
@@ -509,10 +509,10 @@ __device__ __forceinline__ void split_bf16(float x, uint16_t& hi, uint16_t& lo) 
                              0xFFFFu);
 }
 
-// Adapter stages of 64 columns.  Alone: rank columns 0.., 64.., ... against hi,
-// then the same against lo.  In a mixed tile, where the fixing warps write the
-// stage anyway, a rank of at most 32 takes one: hi and lo next to each other
-// (lo from column 16 or 32 on), and up[id] twice.
+// Adapter stages of 64 columns: columns 0.., 64.., ... of up[id] against H's
+// first term, then the same against its second.  In a mixed tile, whose stages
+// the fixing warps go over anyway, a rank of at most 32 takes one stage: both
+// terms next to each other, as they lie in memory, and up[id] twice.
 __device__ __forceinline__ bool adapter_packed(int rank, bool mixed) { return mixed && rank <= 32; }
 __device__ __forceinline__ int adapter_stages(int rank, bool mixed) {
   return adapter_packed(rank, mixed) ? 1 : 2 * ((rank + 63) / 64);
@@ -525,11 +525,12 @@ __device__ __forceinline__ uint32_t finite_bf16x2(uint32_t w) {
   return w;
 }
 
-// Whether one of eight bf16 values has an exponent of all ones: then, and only
-// then, adding 0x80 to its 15 magnitude bits reaches bit 15.
-__device__ __forceinline__ bool has_nonfinite(const uint4& v) {
-  auto carry = [](uint32_t w) { return (w & 0x7FFF7FFFu) + 0x00800080u; };
-  return ((carry(v.x) | carry(v.y) | carry(v.z) | carry(v.w)) & 0x80008000u) != 0u;
+// w * 0 + z on two bf16 values: z stays zero (of either sign) as long as every
+// w is finite, and is NaN from the first that is not.
+__device__ __forceinline__ uint32_t times_zero_bf16x2(uint32_t w, uint32_t z) {
+  uint32_t d;
+  asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(w), "r"(0u), "r"(z));
+  return d;
 }
 
 // epi(v) on the accumulators of one lane, whose column of D has bias b.
@@ -721,12 +722,12 @@ static __device__ __noinline__ float marked_term(const GroupedArgs& p, int row, 
   float s = 0.0f;
   if (id >= static_cast<uint32_t>(p.adapters)) return s;
   const uint16_t* u = p.up + id * p.group_stride_up + static_cast<int64_t>(x) * p.ld_up;
-  const int64_t h = static_cast<int64_t>(row) * p.rank;
+  const uint16_t* h = p.h + static_cast<int64_t>(row) * (2 * p.rank);
   for (int r = 0; r < p.rank; ++r)
     if ((u[r] & 0x7F80u) == 0x7F80u)
       s += __uint_as_float(static_cast<uint32_t>(u[r]) << 16) *
-           (__uint_as_float(static_cast<uint32_t>(p.h_hi[h + r]) << 16) +
-            __uint_as_float(static_cast<uint32_t>(p.h_lo[h + r]) << 16));
+           (__uint_as_float(static_cast<uint32_t>(h[r]) << 16) +
+            __uint_as_float(static_cast<uint32_t>(h[p.rank + r]) << 16));
   return s;
 }
 __device__ __forceinline__ void add_marked_terms(const GroupedArgs& p, int row, int end, int x,
@@ -758,8 +759,8 @@ __device__ __forceinline__ void add_adapter_terms(const GroupedArgs& p, int piec
     const uint32_t id_b = __shfl_sync(0xFFFFFFFFu, ids[0], g);   // of the row this lane loads
     const uint32_t id_c0 = __shfl_sync(0xFFFFFFFFu, ids[0], 2 * q);
     const uint32_t id_c1 = __shfl_sync(0xFFFFFFFFu, ids[0], 2 * q + 1);
-    const uint16_t* hi = p.h_hi + static_cast<int64_t>(r0 + g) * p.rank + 8 * q;
-    const uint16_t* lo = p.h_lo + static_cast<int64_t>(r0 + g) * p.rank + 8 * q;
+    const uint16_t* hi = p.h + static_cast<int64_t>(r0 + g) * (2 * p.rank) + 8 * q;
+    const uint16_t* lo = hi + p.rank;
     const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
     float sum[2][4] = {};
     int id = next_adapter(ids, -1, p.adapters);
@@ -866,7 +867,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
       mbar_init(&full_bar[s], 1);
       mbar_init(&empty_bar[s], 1);
       if constexpr (C::kFixWarps > 0) {
-        mbar_init(&fix_bar[s], C::kFixWarps * C::kCtaGroup);
+        mbar_init(&fix_bar[s], C::kCtaGroup);
         mbar_init(&tail_bar[s], 1);
       }
     }
@@ -1094,36 +1095,39 @@ __global__ void __launch_bounds__(C::kThreads, 1)
         load_tile_ids<C>(p, w, lane, ids);
         const bool mixed = mixed_adapters(ids, w.rows, lane, p.adapters);
         // (A split tile's adapter stages belong to its first piece.)
-        for (int id = w.piece == 0 ? next_adapter(ids, -1, p.adapters) : -1; id >= 0 && ok;
-             id = next_adapter(ids, id, p.adapters)) {
-          if (lane == 0) {
-            const int per = (p.rank + 63) / 64 * 64;
-            const int stages = adapter_stages(p.rank, mixed);
-            for (int r = 0; r < 64 * stages; r += 64) {
-              if (!wait_slot()) {
-                ok = 0;
-                break;
+        const int per = (p.rank + 63) / 64 * 64;
+        const int end = w.piece == 0 ? 64 * adapter_stages(p.rank, mixed) : 0;
+        for (int r = 0; r < end && ok; r += 64) {
+          for (int id = next_adapter(ids, -1, p.adapters); id >= 0 && ok;
+               id = next_adapter(ids, id, p.adapters)) {
+            if (lane == 0) {
+              ok = wait_slot();
+              if (ok) {
+                const int rx = r < per ? r : r - per;
+                if (mixed) {
+                  // Like a ragged stage's, the load completes in each CTA for
+                  // its own fixing warps.
+                  if (leader) mbar_arrive(&full_bar[stage]);
+                  mbar_arrive_expect_tx(&tail_bar[stage], C::W_BYTES + C::C_BYTES);
+                  const uint32_t tb = smem_addr(&tail_bar[stage]);
+                  tma_load_3d(sW + stage * C::W_BYTES, &tmUp, tb, rx, wx, id, pol);
+                  tma_load_2d(sC + stage * C::C_BYTES,
+                              &tmC.h[adapter_packed(p.rank, true) ? 2 : r < per ? 0 : 1], tb, rx,
+                              crow0, pol);
+                  note_tail();
+                } else {
+                  if (leader)
+                    mbar_arrive_expect_tx(&full_bar[stage], 2 * (C::W_BYTES + C::C_BYTES));
+                  const uint32_t fb = full_dst0 + 8u * stage;
+                  tma_load_3d_pair(sW + stage * C::W_BYTES, &tmUp, fb, rx, wx, id, pol);
+                  tma_load_2d_pair(sC + stage * C::C_BYTES, &tmC.h[r < per ? 0 : 1], fb, rx,
+                                   crow0, pol);
+                }
+                next_slot();
               }
-              const int rx = r < per ? r : r - per;
-              if (mixed) {
-                // Like a ragged stage's, the load completes in each CTA for
-                // its own fixing warps.
-                if (leader) mbar_arrive(&full_bar[stage]);
-                mbar_arrive_expect_tx(&tail_bar[stage], C::W_BYTES);
-                tma_load_3d(sW + stage * C::W_BYTES, &tmUp, smem_addr(&tail_bar[stage]), rx, wx, id,
-                            pol);
-                note_tail();
-              } else {
-                if (leader) mbar_arrive_expect_tx(&full_bar[stage], 2 * (C::W_BYTES + C::C_BYTES));
-                const uint32_t fb = full_dst0 + 8u * stage;
-                tma_load_3d_pair(sW + stage * C::W_BYTES, &tmUp, fb, rx, wx, id, pol);
-                tma_load_2d_pair(sC + stage * C::C_BYTES, &tmC.h[r < per ? 0 : 1], fb, rx, crow0,
-                                 pol);
-              }
-              next_slot();
             }
+            ok = __shfl_sync(0xFFFFFFFFu, ok, 0);
           }
-          ok = __shfl_sync(0xFFFFFFFFu, ok, 0);
         }
       }
     }
@@ -1254,38 +1258,34 @@ __global__ void __launch_bounds__(C::kThreads, 1)
           load_tile_ids<C>(p, w, lane, ids);
           const int per = (p.rank + 63) / 64 * 64;
           const bool mixed = mixed_adapters(ids, w.rows, lane, p.adapters);
-          for (int id = w.piece == 0 ? next_adapter(ids, -1, p.adapters) : -1; id >= 0 && ok;
-               id = next_adapter(ids, id, p.adapters)) {
-            if (lane == 0) {
-              const int stages = adapter_stages(p.rank, mixed);
-              for (int r = 0; r < 64 * stages; r += 64) {
-                if (!ready && !mbar_try_wait(full0 + 8u * stage, phase) &&
-                    !mbar_wait(&full_bar[stage], phase, guard, kSiteGrFull)) {
-                  ok = 0;
-                  break;
+          const int end = w.piece == 0 ? 64 * adapter_stages(p.rank, mixed) : 0;
+          for (int r = 0; r < end && ok; r += 64) {
+            for (int id = next_adapter(ids, -1, p.adapters); id >= 0 && ok;
+                 id = next_adapter(ids, id, p.adapters)) {
+              if (lane == 0) {
+                ok = (ready || mbar_try_wait(full0 + 8u * stage, phase) ||
+                      mbar_wait(&full_bar[stage], phase, guard, kSiteGrFull)) &&
+                     (!mixed || wait_fix());
+                if (ok) {
+                  tc_fence_after_sync();
+                  const uint64_t wd = wdesc0 + static_cast<uint64_t>(stage * (C::W_BYTES >> 4));
+                  const uint64_t cd = cdesc0 + static_cast<uint64_t>(stage * (C::C_BYTES >> 4));
+                  const int left = p.rank - (r < per ? r : r - per);
+                  const int issues = adapter_packed(p.rank, mixed) ? p.rank / 8
+                                     : left >= 64                  ? 4
+                                                                   : (left + 15) / 16;
+                  for (int k = 0; k < issues; ++k)
+                    mma_bf16<C::kCtaGroup>(d_tmem, wd + 2 * k, cd + 2 * k, idesc, 1u);
+                  mma_commit_pair(&empty_bar[stage], static_cast<uint16_t>(3u));
+                  if (++stage == C::kStages) {
+                    stage = 0;
+                    phase ^= 1u;
+                  }
+                  ready = false;
                 }
-                if (mixed && !wait_fix()) {
-                  ok = 0;
-                  break;
-                }
-                tc_fence_after_sync();
-                const uint64_t wd = wdesc0 + static_cast<uint64_t>(stage * (C::W_BYTES >> 4));
-                const uint64_t cd = cdesc0 + static_cast<uint64_t>(stage * (C::C_BYTES >> 4));
-                const int left = p.rank - (r < per ? r : r - per);
-                const int issues = adapter_packed(p.rank, mixed) ? (p.rank <= 16 ? 2 : 4)
-                                   : left >= 64                  ? 4
-                                                                 : (left + 15) / 16;
-                for (int k = 0; k < issues; ++k)
-                  mma_bf16<C::kCtaGroup>(d_tmem, wd + 2 * k, cd + 2 * k, idesc, 1u);
-                mma_commit_pair(&empty_bar[stage], static_cast<uint16_t>(3u));
-                if (++stage == C::kStages) {
-                  stage = 0;
-                  phase ^= 1u;
-                }
-                ready = false;
               }
+              ok = __shfl_sync(0xFFFFFFFFu, ok, 0);
             }
-            ok = __shfl_sync(0xFFFFFFFFu, ok, 0);
           }
         }
         if (C::kMode != kAdapterDown && chunks > 0 && ok && lane == 0) commit_acc();
@@ -1350,71 +1350,84 @@ __global__ void __launch_bounds__(C::kThreads, 1)
             if (next_adapter(ids, -1, p.adapters) >= 0) pos += adapter_stages(p.rank, false);
             continue;
           }
-          // A warp takes 4 rows x 8 16-byte pieces at a time: this lane's rows.
-          constexpr int kSteps = C::C_ROWS / (4 * (C::kFixWarps ? C::kFixWarps : 1));
-          uint32_t own[kSteps];
+          // The adapters of this CTA's rows lane, lane + 32, ...
+          uint32_t own[C::C_ROWS / 32];
 #pragma unroll
-          for (int t = 0; t < kSteps; ++t) {
-            const int i = 4 * (fw + C::kFixWarps * t) + (lane >> 3);
-            own[t] = i < crows && r0 + i < w.rows
-                         ? static_cast<uint32_t>(p.ids[w.row0 + r0 + i])
-                         : 0xFFFFFFFFu;
+          for (int i = 0; i < C::C_ROWS / 32; ++i) {
+            const int r = lane + 32 * i;
+            own[i] = r < crows && r0 + r < w.rows ? static_cast<uint32_t>(p.ids[w.row0 + r0 + r])
+                                                  : 0xFFFFFFFFu;
           }
-          for (int id = next_adapter(ids, -1, p.adapters); id >= 0 && ok;
-               id = next_adapter(ids, id, p.adapters)) {
-            for (int r = 0; r < 64 * adapter_stages(p.rank, true); r += 64, ++pos) {
+          // A warp goes over 4 rows x 8 16-byte pieces at a time; this lane's
+          // piece, by the step's parity, with the rows' swizzle.  Packed:
+          // up[id] again from piece `copy` on.
+          const bool packed = adapter_packed(p.rank, true);
+          const uint32_t lr = static_cast<uint32_t>(lane >> 3), q = static_cast<uint32_t>(lane & 7);
+          const uint32_t copy = static_cast<uint32_t>(p.rank / 8);
+          const uint32_t at[2] = {128u * lr + ((q ^ lr) << 4), 128u * lr + ((q ^ (lr + 4u)) << 4)};
+          const uint32_t at2[2] = {128u * lr + (((q + copy) ^ lr) << 4),
+                                   128u * lr + (((q + copy) ^ (lr + 4u)) << 4)};
+          for (int r = 0; r < 64 * adapter_stages(p.rank, true) && ok; r += 64) {
+            const int cw = min(64, p.rank - (r < per ? r : r - per));   // columns (rest: zeros)
+            for (int id = next_adapter(ids, -1, p.adapters); id >= 0 && ok;
+                 id = next_adapter(ids, id, p.adapters), ++pos) {
               const int stage = static_cast<int>(pos % C::kStages);
-              const int c0 = r < per ? r : r - per;
-              const int cw = min(64, p.rank - c0);   // columns of this stage (rest: zeros)
-              // Packed: hi in pieces 0 .., lo in pieces lq ..
-              const bool packed = adapter_packed(p.rank, true);
-              const int lq = packed ? (p.rank <= 16 ? 2 : 4) : 8;
-              const int q0 = packed && (lane & 7) >= lq ? (lane & 7) - lq : (lane & 7);
-              const uint16_t* h = r < per && (lane & 7) < lq ? p.h_hi : p.h_lo;
-              const int q = lane & 7;
-              uint4 v[kSteps];
-#pragma unroll
-              for (int t = 0; t < kSteps; ++t) {
-                const int row = w.row0 + r0 + 4 * (fw + C::kFixWarps * t) + (lane >> 3);
-                v[t] = make_uint4(0u, 0u, 0u, 0u);
-                if (own[t] == static_cast<uint32_t>(id) && 8 * q0 < cw)
-                  v[t] = *reinterpret_cast<const uint4*>(
-                      h + static_cast<int64_t>(row) * p.rank + c0 + 8 * q0);
-              }
               const uint32_t par = (tail_use >> stage) & 1u;
               tail_use ^= 1u << stage;
+              // The warps take turns: one's waits are the other's work.
+              if ((pos & 1u) != static_cast<uint32_t>(fw)) continue;
               if (lane == 0)
                 ok = mbar_try_wait(smem_addr(&tail_bar[stage]), par) ||
                      mbar_wait(&tail_bar[stage], par, guard, kSiteGrFixIn);
               ok = __shfl_sync(0xFFFFFFFFu, ok, 0);
               if (!ok) break;
+              // H: zeros in the rows of other adapters.
+              const uint32_t hdst = sC + stage * C::C_BYTES;
 #pragma unroll
-              for (int t = 0; t < kSteps; ++t) {
-                const int i = 4 * (fw + C::kFixWarps * t) + (lane >> 3);
-                if (i < crows)
-                  st_shared_v4(
-                      sC + stage * C::C_BYTES + 128 * i +
-                          ((static_cast<uint32_t>(q) ^ (static_cast<uint32_t>(i) & 7u)) << 4),
-                      v[t].x, v[t].y, v[t].z, v[t].w);
-              }
-              // up[id]: this warp's 64 rows, the pieces that hold weights.
-              const int np = cw / 8;
-              const uint32_t part = sW + stage * C::W_BYTES + fw * (C::W_BYTES / 2);
-#pragma unroll 4
-              for (int i = 0; i < 16; ++i) {
-                const uint32_t row = static_cast<uint32_t>(4 * i + (lane >> 3));
-                const uint32_t c = static_cast<uint32_t>(q);
-                if (q >= np) break;
-                const uint32_t a = part + 128 * row;
-                uint4 u4 = ld_shared_v4(a + ((c ^ (row & 7u)) << 4));
-                if (has_nonfinite(u4)) {
-                  u4 = make_uint4(finite_bf16x2(u4.x), finite_bf16x2(u4.y), finite_bf16x2(u4.z),
-                                  finite_bf16x2(u4.w));
-                  st_shared_v4(a + ((c ^ (row & 7u)) << 4), u4.x, u4.y, u4.z, u4.w);
-                  marked[count & 15] = count + 1;
+              for (int i = 0; i < C::C_ROWS / 32; ++i) {
+                const uint32_t others =
+                    ~__ballot_sync(0xFFFFFFFFu, own[i] == static_cast<uint32_t>(id)) >> lr;
+                if (32 * i < crows) {
+#pragma unroll
+                  for (int t = 0; t < 8; ++t)
+                    if (others & (1u << (4 * t)))
+                      st_shared_v4(hdst + 4096u * i + 512u * t + at[t & 1], 0u, 0u, 0u, 0u);
                 }
-                if (packed)
-                  st_shared_v4(a + (((c + lq) ^ (row & 7u)) << 4), u4.x, u4.y, u4.z, u4.w);
+              }
+              // up[id]: the pieces that hold weights, eight loads on their way
+              // at a time.
+              const uint32_t wsrc = sW + stage * C::W_BYTES;
+              if (8 * static_cast<int>(q) < cw) {
+#pragma unroll
+                for (int i0 = 0; i0 < 32; i0 += 8) {
+                  uint4 u[8];
+#pragma unroll
+                  for (int i = 0; i < 8; ++i) u[i] = ld_shared_v4(wsrc + 512u * (i0 + i) + at[i & 1]);
+                  uint32_t z[4] = {0u, 0u, 0u, 0u};
+#pragma unroll
+                  for (int i = 0; i < 8; ++i) {
+                    z[0] = times_zero_bf16x2(u[i].x, z[0]);
+                    z[1] = times_zero_bf16x2(u[i].y, z[1]);
+                    z[2] = times_zero_bf16x2(u[i].z, z[2]);
+                    z[3] = times_zero_bf16x2(u[i].w, z[3]);
+                  }
+                  if (((z[0] | z[1] | z[2] | z[3]) & 0x7FFF7FFFu) != 0u) {
+                    marked[count & 15] = count + 1;
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                      u[i] = make_uint4(finite_bf16x2(u[i].x), finite_bf16x2(u[i].y),
+                                        finite_bf16x2(u[i].z), finite_bf16x2(u[i].w));
+                      st_shared_v4(wsrc + 512u * (i0 + i) + at[i & 1], u[i].x, u[i].y, u[i].z,
+                                   u[i].w);
+                    }
+                  }
+                  if (packed) {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                      st_shared_v4(wsrc + 512u * (i0 + i) + at2[i & 1], u[i].x, u[i].y, u[i].z,
+                                   u[i].w);
+                  }
+                }
               }
               fence_proxy_async_smem();
               __syncwarp();
@@ -1553,8 +1566,8 @@ __global__ void __launch_bounds__(C::kThreads, 1)
         const int row0 = w.row0 + 32 * half;
         float* part = p.partials + static_cast<int64_t>(w.piece) * p.M * p.rank;
         auto keep = [&](int row, int r, float s) {
-          const int64_t o = static_cast<int64_t>(row) * p.rank + r;
-          split_bf16(s, p.h_hi[o], p.h_lo[o]);
+          uint16_t* h = p.h + static_cast<int64_t>(row) * (2 * p.rank) + r;
+          split_bf16(s, h[0], h[p.rank]);
         };
         int last_id = -1, group[4];
         while (next_adapters(ids, last_id, 128 / slot, p.adapters, group) > 0) {
