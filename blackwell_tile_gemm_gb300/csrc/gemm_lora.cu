@@ -21,8 +21,10 @@
 // A block takes 8 consecutive rows and a slice of K: its warps share the
 // slice, the CTAs of the cluster share K, and the partial sums meet in
 // (distributed) shared memory in a fixed order.  The rows' adapters are
-// computed for the whole tile and kept for their own rows, each in a block of
-// its own (blockIdx.y).
+// computed for the whole tile and kept for their own rows, each, and each
+// 16 kRt of the rank, in a block of its own (blockIdx.y).
+#include <algorithm>
+
 #include "grouped_launch.cuh"
 
 namespace tg {
@@ -40,6 +42,7 @@ struct DownArgs {
   const float* scales;   // may be null: 1
   int adapters, rank;
   int k_per_cta;         // multiple of 32 * kDownWarps
+  int parts;             // blocks that share an adapter's rank
   bool leave_few;        // kAdapterDown does the 64-row tiles of few adapters
   uint16_t* h;           // [M][2][rank]: H in two bf16 terms
 };
@@ -60,7 +63,7 @@ __device__ __forceinline__ float ld_dsmem(uint32_t addr) {
   return v;
 }
 
-// kRt 16-row tiles of `down` at a time (rank > 16 kRt: in several passes).
+// kRt 16-row tiles of `down` at a time.
 template <int kRt>
 __global__ void __launch_bounds__(32 * kDownWarps) lora_down_kernel(const DownArgs p) {
   constexpr int kTok = 8;
@@ -88,14 +91,18 @@ __global__ void __launch_bounds__(32 * kDownWarps) lora_down_kernel(const DownAr
   uint32_t ids[1] = {lane < rows ? static_cast<uint32_t>(p.ids[row0 + lane]) : 0xFFFFFFFFu};
   const int kbeg = crank * p.k_per_cta;
   const int kend = min(p.K, kbeg + p.k_per_cta);
-  // Adapter number blockIdx.y, + gridDim.y, ... of the tile (the same in every
-  // CTA of the cluster, so all of them meet at its barriers).
+  // Adapter number blockIdx.y / parts, + gridDim.y / parts, ... of the tile (the
+  // same in every CTA of the cluster, so all of them meet at its barriers), and
+  // of its rank the pieces blockIdx.y % parts, + parts, ...
+  const int per = static_cast<int>(gridDim.y) / p.parts;
+  const int first = static_cast<int>(blockIdx.y) / p.parts;
+  const int part0 = static_cast<int>(blockIdx.y) - first * p.parts;
   int ordinal = 0;
   for (int id = next_adapter(ids, -1, p.adapters); id >= 0; id = next_adapter(ids, id, p.adapters)) {
-    if (ordinal++ % static_cast<int>(gridDim.y) != static_cast<int>(blockIdx.y)) continue;
+    if (ordinal++ % per != first) continue;
     const uint16_t* down = p.down + id * p.stride_down;
     const float scale = p.scales ? p.scales[id] : 1.0f;
-    for (int r0 = 0; r0 < p.rank; r0 += 16 * kRt) {
+    for (int r0 = 16 * kRt * part0; r0 < p.rank; r0 += 16 * kRt * p.parts) {
       float acc[kRt][4];
 #pragma unroll
       for (int t = 0; t < kRt; ++t)
@@ -276,13 +283,15 @@ int launch_down(DownArgs a, cudaStream_t stream, DeviceCtx* ctx) {
     prepared[ctx->device].store(1, std::memory_order_release);
   }
   const int tiles = ceil_div_i(a.M, kTok);
+  // A block per adapter of the tile and part of the rank; where most tiles are
+  // left to the other kernel, one block per tile does them in turn (8000 rows
+  // of 16 requests: 15 us of blocks that return at once, against 4).
+  const int adapters = std::min(std::min(a.M, kTok), a.adapters);
+  a.parts = a.leave_few ? 1 : ceil_div_i(a.rank, 16 * kRt);
+  const int y = a.leave_few ? 1 : adapters * a.parts;
   // K over a cluster of up to 8 CTAs, while that adds blocks the SMs have
   // room for and leaves a CTA at least one step per warp.
   int c = 1;
-  // A block per adapter of the tile; where most tiles are left to the other
-  // kernel, one block per tile does them in turn (8000 rows of 16 requests:
-  // 15 us of blocks that return at once, against 4).
-  const int y = a.leave_few ? 1 : a.M < kTok ? a.M : kTok;
   while (c < 8 && tiles * y * c < 2 * ctx->num_sms && a.K > 32 * kDownWarps * c) c *= 2;
   a.k_per_cta = ceil_div_i(ceil_div_i(a.K, c), 32 * kDownWarps) * 32 * kDownWarps;
   cudaLaunchConfig_t cfg{};
@@ -408,9 +417,15 @@ extern "C" int gemm_bf16_lora(const void* A, int64_t lda, const void* B, int64_t
   int* runs = reinterpret_cast<int*>(static_cast<uint8_t*>(ws) +
                                      (static_cast<size_t>(M) * rank * 4u + 255u) / 256u * 256u);
   int* starts = runs + M;
-  rc = rank <= 16   ? launch_down<1>(d, stream, ctx)
-       : rank <= 32 ? launch_down<2>(d, stream, ctx)
-                    : launch_down<4>(d, stream, ctx);
+  // 64 of the rank a block, or less where that leaves SMs without one (1 row,
+  // rank 128, 1260 x 7563: the call 22 us with 8 blocks of two passes, 14 with
+  // 64 of 16).
+  int rt = rank <= 16 ? 1 : rank <= 32 ? 2 : 4;
+  while (!d.leave_few && rt > 1 && ceil_div_i(M, 8) * ceil_div_i(rank, 16 * rt) < ctx->num_sms)
+    rt /= 2;
+  rc = rt == 1   ? launch_down<1>(d, stream, ctx)
+       : rt == 2 ? launch_down<2>(d, stream, ctx)
+                 : launch_down<4>(d, stream, ctx);
   if (rc != TG_OK) return rc;
   if (!few) {
     rc = launch_runs(ids, static_cast<int>(M), static_cast<int>(adapters), runs, starts, stream);

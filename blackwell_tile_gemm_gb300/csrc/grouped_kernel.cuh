@@ -739,21 +739,35 @@ __device__ __forceinline__ void add_marked_terms(const GroupedArgs& p, int row, 
 }
 
 // Adapter term of a few-row tile: v[j] += up[id][x, :] . H[row + j, :] for 32
-// rows, shared out over the S pieces of the tile in batches of eight rows.
-// It runs before the accumulator is waited for, beside the stream of the
-// weights, on warp-level MMAs: 32 rows of up[id] by 8 rows of H, once for each
-// adapter of the batch, whose result is kept in its own rows' columns only
-// (whatever the other columns hold).  Both operands come from memory in
-// 16-byte pieces, 64 bytes of a row to each four lanes, so that a load
-// instruction touches 8 lines; one lane per row of up[id] (32 lines each) took
-// 71 us instead for 128 rows x 4096 with 48 adapters of rank 64.
-__device__ __forceinline__ void add_adapter_terms(const GroupedArgs& p, int piece, int S, int row,
-                                                  int end, int x0, int lane, float (&v)[32]) {
+// rows.  It runs before the accumulator is waited for, beside the stream of
+// the weights, on warp-level MMAs, in batches of 8 rows and steps of one
+// adapter and 32 of the rank: 32 rows of up[id] by 8 rows of H, the result
+// kept in the adapter's own rows' columns only (whatever the other columns
+// hold).  Both operands come from memory in 16-byte pieces, 64 bytes of a row
+// to each four lanes, so that a load instruction touches 8 lines; one lane per
+// row of up[id] (32 lines each) took 71 us instead for 128 rows x 4096 with 48
+// adapters of rank 64.
+//
+// A step takes about one trip to memory, so the tile's S pieces share the steps
+// out: its batches first (batch0: this warp's before row), then, where there
+// are more pieces than batches, each batch's steps.  (114 rows, 6 adapters of
+// rank 32, x 1125 x 1721: 26 -> 22 us; 39 rows, 12 adapters of rank 128, x 1229 x
+// 638, with H's ranks spread over blocks too: 28 -> 17.)
+// Before `ready` only what the caller handed in is read: ids and up.
+__device__ __forceinline__ void add_adapter_terms(const GroupedArgs& p, const GroupedWork& w, int S,
+                                                  int batch0, int row, int end, int x0, int lane,
+                                                  bool& ready, float (&v)[32]) {
   const int g = lane >> 2, q = lane & 3;
+  // The most batches one warp has: blocks of 32 rows go to two warps in turn.
+  const int batches = min(4, (w.rows + 7) / 8) + (w.rows > 64 ? min(4, (w.rows - 57) / 8) : 0);
+  const int share = S > batches ? small_div(S, batches) : 1;
+  const int sets = S > batches ? small_div(S, share) : S;
+  const int set = share > 1 ? small_div(w.piece, share) : w.piece;
+  const int turn = w.piece - set * share;
 #pragma unroll 1   // (one copy of a long body: instruction fetches are what a short call waits for)
   for (int b = 0; b < 4; ++b) {
     const int r0 = row + 8 * b;
-    if (r0 >= end || (r0 >> 3) % S != piece) continue;
+    if (r0 >= end || (batch0 + b) % sets != set) continue;
     const int mine = r0 + (lane & 7);
     uint32_t ids[1] = {mine < end ? static_cast<uint32_t>(p.ids[mine]) : 0xFFFFFFFFu};
     const uint32_t id_b = __shfl_sync(0xFFFFFFFFu, ids[0], g);   // of the row this lane loads
@@ -763,9 +777,17 @@ __device__ __forceinline__ void add_adapter_terms(const GroupedArgs& p, int piec
     const uint16_t* lo = hi + p.rank;
     const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
     float sum[2][4] = {};
-    int id = next_adapter(ids, -1, p.adapters);
+    int id = next_adapter(ids, -1, p.adapters), k = 0;
+    // The step `n` steps on (id < 0: there is none).
+    auto advance = [&](int n) {
+      k += 32 * n;
+      while (k >= p.rank && id >= 0) {
+        k -= (p.rank + 31) / 32 * 32;
+        id = next_adapter(ids, id, p.adapters);
+      }
+    };
+    advance(turn);
     if (id < 0) continue;
-    int k = 0;
     uint4 a[2][2], h[2];
     auto load = [&]() {
       const bool in = 8 * q + k < p.rank;
@@ -777,36 +799,35 @@ __device__ __forceinline__ void add_adapter_terms(const GroupedArgs& p, int piec
           const int x = x0 + 16 * t + 8 * i + g;
           a[t][i] = in && x < p.wide ? ld_global_nc_v4(u + static_cast<int64_t>(x) * p.ld_up) : zero;
         }
+      if (!ready) {
+        griddep_wait();
+        ready = true;
+      }
       const bool own = in && id_b == static_cast<uint32_t>(id);
       h[0] = own ? *reinterpret_cast<const uint4*>(hi + k) : zero;
       h[1] = own ? *reinterpret_cast<const uint4*>(lo + k) : zero;
     };
     load();
     while (id >= 0) {
-      float c[2][4] = {};
       const uint32_t cur = static_cast<uint32_t>(id);
-      bool more;
-      do {
-        uint4 a0[2][2], h0[2];
+      uint4 a0[2][2], h0[2];
 #pragma unroll
-        for (int t = 0; t < 2; ++t) {
-          a0[t][0] = a[t][0];
-          a0[t][1] = a[t][1];
-          h0[t] = h[t];
+      for (int t = 0; t < 2; ++t) {
+        a0[t][0] = a[t][0];
+        a0[t][1] = a[t][1];
+        h0[t] = h[t];
+      }
+      // The next step's loads are in flight during this one's products.
+      advance(share);
+      if (id >= 0) load();
+      float c[2][4] = {};
+#pragma unroll
+      for (int t = 0; t < 2; ++t)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          mma_m16n8k16(c[t], a0[t][0].x, a0[t][1].x, a0[t][0].y, a0[t][1].y, h0[i].x, h0[i].y);
+          mma_m16n8k16(c[t], a0[t][0].z, a0[t][1].z, a0[t][0].w, a0[t][1].w, h0[i].z, h0[i].w);
         }
-        // The next step's loads are in flight during this one's products.
-        more = k + 32 < p.rank;
-        k = more ? k + 32 : 0;
-        if (!more) id = next_adapter(ids, id, p.adapters);
-        if (id >= 0) load();
-#pragma unroll
-        for (int t = 0; t < 2; ++t)
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            mma_m16n8k16(c[t], a0[t][0].x, a0[t][1].x, a0[t][0].y, a0[t][1].y, h0[i].x, h0[i].y);
-            mma_m16n8k16(c[t], a0[t][0].z, a0[t][1].z, a0[t][0].w, a0[t][1].w, h0[i].z, h0[i].w);
-          }
-      } while (more);
 #pragma unroll
       for (int t = 0; t < 2; ++t)
 #pragma unroll
@@ -898,11 +919,14 @@ __global__ void __launch_bounds__(C::kThreads, 1)
   tc_fence_after_sync();
   const uint32_t tmem_base = *tmem_slot;
   // The few-row adapter product streams its weights beside the kernel that
-  // computes H, which started only when its own inputs (this one's A, B and
-  // ids among them) were there, and so does kAdapterDown beside the kernels
-  // before it: only the epilogue, which reads H and writes, waits for them.
-  constexpr bool kEarly = (C::kMode == kAdapter && C::kSplit) || C::kMode == kAdapterDown;
-  if (!kEarly || warp >= C::kEpiWarp0) griddep_wait();
+  // computes H, which started only when its own inputs (this one's A, B, up
+  // and ids among them) were there, and so does kAdapterDown beside the kernels
+  // before it: only the epilogue, which reads H and writes, waits for them
+  // (the few-row product's only where it does either).
+  constexpr bool kFewRows = C::kMode == kAdapter && C::kSplit;
+  constexpr bool kEarly = kFewRows || C::kMode == kAdapterDown;
+  bool inputs_ready = !kFewRows;
+  if (!kEarly || (!kFewRows && warp >= C::kEpiWarp0)) griddep_wait();
 
   const WaitGuard guard{p.status, abort_flag, p.timeout_ns};
   const int unit = blockIdx.x / C::kCtaGroup;
@@ -1441,7 +1465,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
     // ------------------------------------------------------------ epilogue
     const int slab = warp & 3;                 // TMEM lanes 32 * slab ..
     const int half = (warp - C::kEpiWarp0) >> 2;   // column blocks half, half + 2, ...
-    if constexpr (!C::kColMn)
+    if constexpr (!C::kColMn && C::kMode != kAdapter)   // (adapters: every row has a tile)
       grouped_zero_rows<C>(p, first_row, end_row,
                            static_cast<int>(blockIdx.x) * C::kEpiWarps + warp - C::kEpiWarp0,
                            static_cast<int>(gridDim.x) * C::kEpiWarps, lane);
@@ -1636,8 +1660,14 @@ __global__ void __launch_bounds__(C::kThreads, 1)
         for (int q = 0; q < kOwn; ++q) {
           grouped_zero(m[q]);
           if constexpr (C::kMode == kAdapter)
-            add_adapter_terms(p, w.piece, S, w.row0 + 32 * (half + 2 * q), end, x - lane, lane, m[q]);
+            add_adapter_terms(p, w, S, 4 * q, w.row0 + 32 * (half + 2 * q), end, x - lane, lane,
+                              inputs_ready, m[q]);
         }
+        if constexpr (C::kMode == kAdapter)
+          if (!inputs_ready) {
+            griddep_wait();
+            inputs_ready = true;
+          }
         for (int c = 0; c < chunks; ++c) {
           if (!acc_ready()) {
             ok = false;
