@@ -283,12 +283,13 @@ int launch_down(DownArgs a, cudaStream_t stream, DeviceCtx* ctx) {
     prepared[ctx->device].store(1, std::memory_order_release);
   }
   const int tiles = ceil_div_i(a.M, kTok);
-  // A block per adapter of the tile and part of the rank; where most tiles are
-  // left to the other kernel, one block per tile does them in turn (8000 rows
-  // of 16 requests: 15 us of blocks that return at once, against 4).
-  const int adapters = std::min(std::min(a.M, kTok), a.adapters);
-  a.parts = a.leave_few ? 1 : ceil_div_i(a.rank, 16 * kRt);
-  const int y = a.leave_few ? 1 : adapters * a.parts;
+  // A block per adapter of the tile and part of the rank; where many tiles are
+  // left to the other kernel, fewer (8000 rows of 16 requests: 15 us of 8000
+  // blocks that return at once; 1536 rows of 32, rank 128, x 1000 x 6000: the
+  // call takes 122 us with one block a tile, 84 with 10).
+  const int budget = a.leave_few ? std::max(1, 2048 / tiles) : 1 << 16;
+  a.parts = std::min(budget, ceil_div_i(a.rank, 16 * kRt));
+  const int y = std::min(budget / a.parts, std::min(std::min(a.M, kTok), a.adapters)) * a.parts;
   // K over a cluster of up to 8 CTAs, while that adds blocks the SMs have
   // room for and leaves a CTA at least one step per warp.
   int c = 1;
@@ -314,26 +315,27 @@ int launch_down(DownArgs a, cudaStream_t stream, DeviceCtx* ctx) {
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
-// Rows up to which the product runs on single CTAs, with a split contraction
-// and the adapter term beside the weights' stream: always up to 256, and up to
-// 512 where reading the weights once more for each 128 rows costs little
-// (M = 384, 16 adapters: 4096 x 4096, rank 64 37 us against 75 for CTA pairs;
-// 8192 x 8192, rank 16 90 against 84).
-constexpr int64_t kLoraFewRows = 256, kLoraFewRowsSmall = 512;
-constexpr int64_t kLoraSmallWeights = int64_t{1} << 25;   // N * K
-bool lora_few_rows(int64_t M, int64_t N, int64_t K) {
-  return M <= kLoraFewRows || (M <= kLoraFewRowsSmall && N * K <= kLoraSmallWeights);
+// Whether the product runs on single CTAs, with a split contraction and the
+// adapter term beside the weights' stream: always for one tile of rows, and as
+// long as its tiles of 128 x 128 make one wave.  16 bf16 adapters, 1 / 32
+// requests, against CTA pairs: 512 rows, rank 64, x 4096 x 4096 (128 tiles) 36 /
+// 40 us against 36 / 58; 1024 rows, rank 128, x 1000 x 6000 (64) 51 / 65 against
+// 70 / 108; 512 rows, rank 128, x 6000 x 1000 (188) 56 / 73 against 26 / 69.
+bool lora_few_rows(int64_t M, int64_t N, const DeviceCtx* ctx) {
+  return M <= 128 || ceil_div_i(M, 128) * ceil_div_i(N, 128) <= ctx->num_sms;
 }
-// Rows up to which lora_down_kernel alone computes H (it reads `down` once per
-// 8 rows).
-constexpr int kLoraDownRows = 1024;
+// H values (M * rank) up to which lora_down_kernel alone computes H; it reads
+// `down` once per 8 rows.  1 / 32 requests, against kAdapterDown: rank 64, 2048
+// rows x 4096 x 4096 73 / 122 us against 75 / 142, and 5000 rows 165 / 224
+// against 148 / 208; rank 128, 1024 rows x 1000 x 6000 70 / 108 against 60 / 132.
+constexpr int64_t kLoraDownValues = 1 << 17;
 
 }  // namespace
 
-// H: two bf16 terms; for many rows also the runs and the tile starts.
+// H: two bf16 terms; where CTA pairs may run also the runs and the tile starts.
 size_t lora_workspace_bytes(int64_t M, int64_t rank) {
   const size_t h = (static_cast<size_t>(M) * static_cast<size_t>(rank) * 4u + 255u) / 256u * 256u;
-  return M <= kLoraFewRows
+  return M <= 128
              ? h
              : h + (static_cast<size_t>(M) + static_cast<size_t>(lora_most_tiles(M)) + 1u) * 4u;
 }
@@ -385,7 +387,7 @@ extern "C" int gemm_bf16_lora(const void* A, int64_t lda, const void* B, int64_t
   if (adapters == 0)
     return launch_gemm(kKindBf16, A, lda, B, ldb, nullptr, 0, nullptr, 0, D, ldd, M, N, K, d_dtype,
                        e, 0, stream, ctx);
-  const bool few = lora_few_rows(M, N, K);
+  const bool few = lora_few_rows(M, N, ctx);
   void* ws = device_workspace(lora_workspace_bytes(M, rank), stream, &rc);
   if (ws == nullptr) return rc;
   DownArgs d{};
@@ -413,7 +415,7 @@ extern "C" int gemm_bf16_lora(const void* A, int64_t lda, const void* B, int64_t
   o.cols = A;
   o.cols_ld = lda;
   o.k = K;
-  d.leave_few = M > kLoraDownRows;
+  d.leave_few = M * rank > kLoraDownValues;
   int* runs = reinterpret_cast<int*>(static_cast<uint8_t*>(ws) +
                                      (static_cast<size_t>(M) * rank * 4u + 255u) / 256u * 256u);
   int* starts = runs + M;
