@@ -44,7 +44,8 @@ struct DownArgs {
   int k_per_cta;         // multiple of 32 * kDownWarps
   int parts;             // blocks that share an adapter's rank
   bool leave_few;        // kAdapterDown does the 64-row tiles of few adapters
-  uint16_t* h;           // [M][2][rank]: H in two bf16 terms
+  uint16_t* h;           // [M][h_terms][rank]: H as a sum of bf16 terms
+  int h_terms;
 };
 
 // Values k .. k + 7 of a row; those from `end` on are zero and not read.
@@ -159,8 +160,8 @@ __global__ void __launch_bounds__(32 * kDownWarps) lora_down_kernel(const DownAr
             s = part[at];
           }
           s *= scale;
-          uint16_t* h = p.h + static_cast<int64_t>(row0 + i) * (2 * p.rank) + r;
-          split_bf16(s, h[0], h[p.rank]);
+          split_bf16(s, p.h + static_cast<int64_t>(row0 + i) * (p.h_terms * p.rank) + r, p.rank,
+                     p.h_terms);
         }
       }
       // The partial sums are free again once every CTA has read them.
@@ -332,9 +333,9 @@ constexpr int64_t kLoraDownValues = 1 << 17;
 
 }  // namespace
 
-// H: two bf16 terms; where CTA pairs may run also the runs and the tile starts.
+// H: up to three bf16 terms; where CTA pairs may run also the runs and the tile starts.
 size_t lora_workspace_bytes(int64_t M, int64_t rank) {
-  const size_t h = (static_cast<size_t>(M) * static_cast<size_t>(rank) * 4u + 255u) / 256u * 256u;
+  const size_t h = (static_cast<size_t>(M) * static_cast<size_t>(rank) * 6u + 255u) / 256u * 256u;
   return M <= 128
              ? h
              : h + (static_cast<size_t>(M) + static_cast<size_t>(lora_most_tiles(M)) + 1u) * 4u;
@@ -409,7 +410,9 @@ extern "C" int gemm_bf16_lora(const void* A, int64_t lda, const void* B, int64_t
   a.ids = ids;
   a.adapters = static_cast<int>(adapters);
   a.rank = static_cast<int>(rank);
+  d.h_terms = d_dtype == TG_D_BF16 ? 2 : 3;
   a.h = d.h;
+  a.h_terms = d.h_terms;
   GroupedOperands o{};
   o.wide_slices = 1;
   o.cols = A;
@@ -417,7 +420,7 @@ extern "C" int gemm_bf16_lora(const void* A, int64_t lda, const void* B, int64_t
   o.k = K;
   d.leave_few = M * rank > kLoraDownValues;
   int* runs = reinterpret_cast<int*>(static_cast<uint8_t*>(ws) +
-                                     (static_cast<size_t>(M) * rank * 4u + 255u) / 256u * 256u);
+                                     (static_cast<size_t>(M) * rank * 6u + 255u) / 256u * 256u);
   int* starts = runs + M;
   // 64 of the rank a block, or less where that leaves SMs without one (1 row,
   // rank 128, 1260 x 7563: the call 22 us with 8 blocks of two passes, 14 with

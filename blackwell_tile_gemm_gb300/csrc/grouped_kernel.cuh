@@ -35,10 +35,10 @@
 // loads and the MMAs.
 //
 // Adapters: H[i] = scale * A[i] * down[id_i]^T was computed before and split
-// into two bf16 terms (hi + lo keep 16 bits of it, so the product with
-// up[id] is as exact as the base product).  After the tile's K stages each
-// adapter that occurs among the tile's rows adds ceil(rank / 64) * 2 stages of
-// up[id] and H.  Where all rows of the tile have one adapter, TMA loads both
+// into bf16 terms: two (17 bits) where D is rounded to bf16, three where D is
+// f32 and the base product as exact as that (with two: 1.5e-6 of the term).  After the tile's K stages each
+// adapter that occurs among the tile's rows adds ceil(rank / 64) stages of
+// up[id] and H for each term.  Where all rows of the tile have one adapter, TMA loads both
 // (tiles start where a long run of rows with one adapter does: there the
 // offsets are those of the runs); else the fixing warps put zeros over H's rows
 // of other adapters.
@@ -96,8 +96,8 @@ struct GroupedArgs {
   // adapters
   const int* ids;          // [M]
   int adapters, rank;
-  uint16_t* h;             // [M][2][rank] bf16: the two terms of each row of H; kAdapterDown
-                           // writes them
+  uint16_t* h;             // [M][h_terms][rank] bf16: each row of H as a sum of terms, which
+  int h_terms;             // kAdapterDown writes: 2, or 3 where D is f32
   const float* scales;     // kAdapterDown: [adapters], or null for 1
   int wide_box;            // kAdapterDown: rows of `down` per load (the lanes
                            // above them hold leftovers and are not stored)
@@ -122,7 +122,7 @@ struct GroupedArgs {
 constexpr int kColBoxes = 4;
 struct ColumnMaps {
   CUtensorMap box[kColBoxes];
-  CUtensorMap h[3];   // adapters: H's first term, its second, and both; boxes of 128 rows
+  CUtensorMap h[4];   // adapters: H's terms and, last, all of them; boxes of 128 rows
 };
 
 template <int kMode_, int kCtaGroup_, int kTileN_, int kStages_, bool kBf16Out_,
@@ -143,6 +143,7 @@ struct GroupedCfg {
   // Adapter stages (MMA form) and ragged contractions are fixed up in shared
   // memory before the MMAs read them.
   static constexpr bool kExt = kMode == kAdapter && kCtaGroup == 2;
+  static constexpr int kTerms = kBf16Out ? 2 : 3;   // bf16 terms of H
   static constexpr int kFixWarps = kExt ? 2 : kMode == kGroupedWgrad ? 1 : 0;
   static constexpr int kColStep = 16 * kCtaGroup;
   static constexpr int C_ROWS = kTileN / kCtaGroup;   // column-operand rows per CTA
@@ -499,23 +500,29 @@ __device__ __forceinline__ int next_adapters(const uint32_t (&ids)[kPer], int& l
   return n;
 }
 
-// x as two bf16 terms; what is infinite or NaN in hi is in hi alone.
-__device__ __forceinline__ void split_bf16(float x, uint16_t& hi, uint16_t& lo) {
-  const uint32_t h = pack_bf16x2(x, x) & 0xFFFFu;
-  const float rest = x - __uint_as_float(h << 16);
-  hi = static_cast<uint16_t>(h);
-  lo = static_cast<uint16_t>(pack_bf16x2(fabsf(rest) < __uint_as_float(0x7F800000u) ? rest : 0.0f,
-                                         0.0f) &
-                             0xFFFFu);
+// x as a sum of bf16 terms, `step` apart; what is infinite or NaN in the first
+// is in the first alone.
+__device__ __forceinline__ void split_bf16(float x, uint16_t* h, int step, int terms) {
+  for (int t = 0; t < terms; ++t) {
+    const uint32_t w = pack_bf16x2(x, x) & 0xFFFFu;
+    h[t * step] = static_cast<uint16_t>(w);
+    const float rest = x - __uint_as_float(w << 16);
+    x = fabsf(rest) < __uint_as_float(0x7F800000u) ? rest : 0.0f;
+  }
 }
 
 // Adapter stages of 64 columns: columns 0.., 64.., ... of up[id] against H's
-// first term, then the same against its second.  In a mixed tile, whose stages
-// the fixing warps go over anyway, a rank of at most 32 takes one stage: both
-// terms next to each other, as they lie in memory, and up[id] twice.
-__device__ __forceinline__ bool adapter_packed(int rank, bool mixed) { return mixed && rank <= 32; }
+// first term, then the same against each other.  In a mixed tile, whose stages
+// the fixing warps go over anyway, terms that fit into 64 columns together
+// take one stage: next to each other, as they lie in memory, and up[id] as
+// often.
+template <int kTerms>
+__device__ __forceinline__ bool adapter_packed(int rank, bool mixed) {
+  return mixed && kTerms * rank <= 64;
+}
+template <int kTerms>
 __device__ __forceinline__ int adapter_stages(int rank, bool mixed) {
-  return adapter_packed(rank, mixed) ? 1 : 2 * ((rank + 63) / 64);
+  return adapter_packed<kTerms>(rank, mixed) ? 1 : kTerms * ((rank + 63) / 64);
 }
 
 // A word of two bf16 values without its infinite and NaN ones.
@@ -722,12 +729,14 @@ static __device__ __noinline__ float marked_term(const GroupedArgs& p, int row, 
   float s = 0.0f;
   if (id >= static_cast<uint32_t>(p.adapters)) return s;
   const uint16_t* u = p.up + id * p.group_stride_up + static_cast<int64_t>(x) * p.ld_up;
-  const uint16_t* h = p.h + static_cast<int64_t>(row) * (2 * p.rank);
+  const uint16_t* h = p.h + static_cast<int64_t>(row) * (p.h_terms * p.rank);
   for (int r = 0; r < p.rank; ++r)
-    if ((u[r] & 0x7F80u) == 0x7F80u)
-      s += __uint_as_float(static_cast<uint32_t>(u[r]) << 16) *
-           (__uint_as_float(static_cast<uint32_t>(h[r]) << 16) +
-            __uint_as_float(static_cast<uint32_t>(h[p.rank + r]) << 16));
+    if ((u[r] & 0x7F80u) == 0x7F80u) {
+      float sum = __uint_as_float(static_cast<uint32_t>(h[r]) << 16);
+      for (int t = 1; t < p.h_terms; ++t)
+        sum += __uint_as_float(static_cast<uint32_t>(h[t * p.rank + r]) << 16);
+      s += __uint_as_float(static_cast<uint32_t>(u[r]) << 16) * sum;
+    }
   return s;
 }
 __device__ __forceinline__ void add_marked_terms(const GroupedArgs& p, int row, int end, int x,
@@ -754,6 +763,7 @@ __device__ __forceinline__ void add_marked_terms(const GroupedArgs& p, int row, 
 // rank 32, x 1125 x 1721: 26 -> 22 us; 39 rows, 12 adapters of rank 128, x 1229 x
 // 638, with H's ranks spread over blocks too: 28 -> 17.)
 // Before `ready` only what the caller handed in is read: ids and up.
+template <int kTerms>
 __device__ __forceinline__ void add_adapter_terms(const GroupedArgs& p, const GroupedWork& w, int S,
                                                   int batch0, int row, int end, int x0, int lane,
                                                   bool& ready, float (&v)[32]) {
@@ -773,8 +783,7 @@ __device__ __forceinline__ void add_adapter_terms(const GroupedArgs& p, const Gr
     const uint32_t id_b = __shfl_sync(0xFFFFFFFFu, ids[0], g);   // of the row this lane loads
     const uint32_t id_c0 = __shfl_sync(0xFFFFFFFFu, ids[0], 2 * q);
     const uint32_t id_c1 = __shfl_sync(0xFFFFFFFFu, ids[0], 2 * q + 1);
-    const uint16_t* hi = p.h + static_cast<int64_t>(r0 + g) * (2 * p.rank) + 8 * q;
-    const uint16_t* lo = hi + p.rank;
+    const uint16_t* hrow = p.h + static_cast<int64_t>(r0 + g) * (kTerms * p.rank) + 8 * q;
     const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
     float sum[2][4] = {};
     int id = next_adapter(ids, -1, p.adapters), k = 0;
@@ -788,7 +797,7 @@ __device__ __forceinline__ void add_adapter_terms(const GroupedArgs& p, const Gr
     };
     advance(turn);
     if (id < 0) continue;
-    uint4 a[2][2], h[2];
+    uint4 a[2][2], h[kTerms];
     auto load = [&]() {
       const bool in = 8 * q + k < p.rank;
       const uint16_t* u = p.up + id * p.group_stride_up + 8 * q + k;
@@ -804,19 +813,21 @@ __device__ __forceinline__ void add_adapter_terms(const GroupedArgs& p, const Gr
         ready = true;
       }
       const bool own = in && id_b == static_cast<uint32_t>(id);
-      h[0] = own ? *reinterpret_cast<const uint4*>(hi + k) : zero;
-      h[1] = own ? *reinterpret_cast<const uint4*>(lo + k) : zero;
+#pragma unroll
+      for (int t = 0; t < kTerms; ++t)
+        h[t] = own ? *reinterpret_cast<const uint4*>(hrow + t * p.rank + k) : zero;
     };
     load();
     while (id >= 0) {
       const uint32_t cur = static_cast<uint32_t>(id);
-      uint4 a0[2][2], h0[2];
+      uint4 a0[2][2], h0[kTerms];
 #pragma unroll
       for (int t = 0; t < 2; ++t) {
         a0[t][0] = a[t][0];
         a0[t][1] = a[t][1];
-        h0[t] = h[t];
       }
+#pragma unroll
+      for (int t = 0; t < kTerms; ++t) h0[t] = h[t];
       // The next step's loads are in flight during this one's products.
       advance(share);
       if (id >= 0) load();
@@ -824,7 +835,7 @@ __device__ __forceinline__ void add_adapter_terms(const GroupedArgs& p, const Gr
 #pragma unroll
       for (int t = 0; t < 2; ++t)
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < kTerms; ++i) {
           mma_m16n8k16(c[t], a0[t][0].x, a0[t][1].x, a0[t][0].y, a0[t][1].y, h0[i].x, h0[i].y);
           mma_m16n8k16(c[t], a0[t][0].z, a0[t][1].z, a0[t][0].w, a0[t][1].w, h0[i].z, h0[i].w);
         }
@@ -1120,14 +1131,14 @@ __global__ void __launch_bounds__(C::kThreads, 1)
         const bool mixed = mixed_adapters(ids, w.rows, lane, p.adapters);
         // (A split tile's adapter stages belong to its first piece.)
         const int per = (p.rank + 63) / 64 * 64;
-        const int end = w.piece == 0 ? 64 * adapter_stages(p.rank, mixed) : 0;
+        const int end = w.piece == 0 ? 64 * adapter_stages<C::kTerms>(p.rank, mixed) : 0;
         for (int r = 0; r < end && ok; r += 64) {
           for (int id = next_adapter(ids, -1, p.adapters); id >= 0 && ok;
                id = next_adapter(ids, id, p.adapters)) {
             if (lane == 0) {
               ok = wait_slot();
               if (ok) {
-                const int rx = r < per ? r : r - per;
+                const int term = small_div(r, per), rx = r - term * per;
                 if (mixed) {
                   // Like a ragged stage's, the load completes in each CTA for
                   // its own fixing warps.
@@ -1136,7 +1147,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
                   const uint32_t tb = smem_addr(&tail_bar[stage]);
                   tma_load_3d(sW + stage * C::W_BYTES, &tmUp, tb, rx, wx, id, pol);
                   tma_load_2d(sC + stage * C::C_BYTES,
-                              &tmC.h[adapter_packed(p.rank, true) ? 2 : r < per ? 0 : 1], tb, rx,
+                              &tmC.h[adapter_packed<C::kTerms>(p.rank, true) ? 3 : term], tb, rx,
                               crow0, pol);
                   note_tail();
                 } else {
@@ -1144,7 +1155,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
                     mbar_arrive_expect_tx(&full_bar[stage], 2 * (C::W_BYTES + C::C_BYTES));
                   const uint32_t fb = full_dst0 + 8u * stage;
                   tma_load_3d_pair(sW + stage * C::W_BYTES, &tmUp, fb, rx, wx, id, pol);
-                  tma_load_2d_pair(sC + stage * C::C_BYTES, &tmC.h[r < per ? 0 : 1], fb, rx,
+                  tma_load_2d_pair(sC + stage * C::C_BYTES, &tmC.h[term], fb, rx,
                                    crow0, pol);
                 }
                 next_slot();
@@ -1282,7 +1293,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
           load_tile_ids<C>(p, w, lane, ids);
           const int per = (p.rank + 63) / 64 * 64;
           const bool mixed = mixed_adapters(ids, w.rows, lane, p.adapters);
-          const int end = w.piece == 0 ? 64 * adapter_stages(p.rank, mixed) : 0;
+          const int end = w.piece == 0 ? 64 * adapter_stages<C::kTerms>(p.rank, mixed) : 0;
           for (int r = 0; r < end && ok; r += 64) {
             for (int id = next_adapter(ids, -1, p.adapters); id >= 0 && ok;
                  id = next_adapter(ids, id, p.adapters)) {
@@ -1294,8 +1305,9 @@ __global__ void __launch_bounds__(C::kThreads, 1)
                   tc_fence_after_sync();
                   const uint64_t wd = wdesc0 + static_cast<uint64_t>(stage * (C::W_BYTES >> 4));
                   const uint64_t cd = cdesc0 + static_cast<uint64_t>(stage * (C::C_BYTES >> 4));
-                  const int left = p.rank - (r < per ? r : r - per);
-                  const int issues = adapter_packed(p.rank, mixed) ? p.rank / 8
+                  const int left = p.rank - (r - small_div(r, per) * per);
+                  const int issues = adapter_packed<C::kTerms>(p.rank, mixed)
+                                         ? (C::kTerms * p.rank + 15) / 16
                                      : left >= 64                  ? 4
                                                                    : (left + 15) / 16;
                   for (int k = 0; k < issues; ++k)
@@ -1371,7 +1383,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
           const int crows = w.ncols / C::kCtaGroup;
           const int r0 = static_cast<int>(rank) * crows;   // this CTA's rows of the tile
           if (!mixed_adapters(ids, w.rows, lane, p.adapters)) {
-            if (next_adapter(ids, -1, p.adapters) >= 0) pos += adapter_stages(p.rank, false);
+            if (next_adapter(ids, -1, p.adapters) >= 0) pos += adapter_stages<C::kTerms>(p.rank, false);
             continue;
           }
           // The adapters of this CTA's rows lane, lane + 32, ...
@@ -1384,15 +1396,13 @@ __global__ void __launch_bounds__(C::kThreads, 1)
           }
           // A warp goes over 4 rows x 8 16-byte pieces at a time; this lane's
           // piece, by the step's parity, with the rows' swizzle.  Packed:
-          // up[id] again from piece `copy` on.
-          const bool packed = adapter_packed(p.rank, true);
+          // up[id] again every `copy` pieces.
+          const bool packed = adapter_packed<C::kTerms>(p.rank, true);
           const uint32_t lr = static_cast<uint32_t>(lane >> 3), q = static_cast<uint32_t>(lane & 7);
           const uint32_t copy = static_cast<uint32_t>(p.rank / 8);
           const uint32_t at[2] = {128u * lr + ((q ^ lr) << 4), 128u * lr + ((q ^ (lr + 4u)) << 4)};
-          const uint32_t at2[2] = {128u * lr + (((q + copy) ^ lr) << 4),
-                                   128u * lr + (((q + copy) ^ (lr + 4u)) << 4)};
-          for (int r = 0; r < 64 * adapter_stages(p.rank, true) && ok; r += 64) {
-            const int cw = min(64, p.rank - (r < per ? r : r - per));   // columns (rest: zeros)
+          for (int r = 0; r < 64 * adapter_stages<C::kTerms>(p.rank, true) && ok; r += 64) {
+            const int cw = min(64, p.rank - (r - small_div(r, per) * per));   // columns (rest: zeros)
             for (int id = next_adapter(ids, -1, p.adapters); id >= 0 && ok;
                  id = next_adapter(ids, id, p.adapters), ++pos) {
               const int stage = static_cast<int>(pos % C::kStages);
@@ -1447,9 +1457,14 @@ __global__ void __launch_bounds__(C::kThreads, 1)
                   }
                   if (packed) {
 #pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                      st_shared_v4(wsrc + 512u * (i0 + i) + at2[i & 1], u[i].x, u[i].y, u[i].z,
-                                   u[i].w);
+                    for (int t = 1; t < C::kTerms; ++t) {
+                      const uint32_t c = q + t * copy;
+#pragma unroll
+                      for (int i = 0; i < 8; ++i)
+                        st_shared_v4(wsrc + 512u * (i0 + i) + 128u * lr +
+                                         ((c ^ (lr + 4u * (i & 1))) << 4),
+                                     u[i].x, u[i].y, u[i].z, u[i].w);
+                    }
                   }
                 }
               }
@@ -1590,8 +1605,8 @@ __global__ void __launch_bounds__(C::kThreads, 1)
         const int row0 = w.row0 + 32 * half;
         float* part = p.partials + static_cast<int64_t>(w.piece) * p.M * p.rank;
         auto keep = [&](int row, int r, float s) {
-          uint16_t* h = p.h + static_cast<int64_t>(row) * (2 * p.rank) + r;
-          split_bf16(s, h[0], h[p.rank]);
+          split_bf16(s, p.h + static_cast<int64_t>(row) * (p.h_terms * p.rank) + r, p.rank,
+                     p.h_terms);
         };
         int last_id = -1, group[4];
         while (next_adapters(ids, last_id, 128 / slot, p.adapters, group) > 0) {
@@ -1660,7 +1675,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
         for (int q = 0; q < kOwn; ++q) {
           grouped_zero(m[q]);
           if constexpr (C::kMode == kAdapter)
-            add_adapter_terms(p, w, S, 4 * q, w.row0 + 32 * (half + 2 * q), end, x - lane, lane,
+            add_adapter_terms<C::kTerms>(p, w, S, 4 * q, w.row0 + 32 * (half + 2 * q), end, x - lane, lane,
                               inputs_ready, m[q]);
         }
         if constexpr (C::kMode == kAdapter)

@@ -131,7 +131,7 @@ int launch_grouped(const GroupedOperands& operands, const GroupedArgs& args, cud
       if (rc != TG_OK) return rc;
     }
   }
-  tW2 = tC.h[0] = tC.h[1] = tC.h[2] = tW;
+  tW2 = tC.h[0] = tC.h[1] = tC.h[2] = tC.h[3] = tW;
   if (C::kWideMn && a.wide >= 128) {
     const bool w = C::kMode == kGroupedWgrad;
     rc = make_tensor_map_chunks(&tW2, o.wide, a.wide, o.wide_rows, w ? 1 : o.wide_slices,
@@ -143,9 +143,11 @@ int launch_grouped(const GroupedOperands& operands, const GroupedArgs& args, cud
     rc = make_tensor_map_3d(&tUp, bf, o.up, o.up_rank, a.wide, o.up_slices, o.up_ld * 2,
                             o.up_slice_stride * 2, 64, 128, sw);
     if (rc != TG_OK) return rc;
-    for (int t = 0; t < 3; ++t) {
-      rc = make_tensor_map_2d(&tC.h[t], bf, t == 1 ? a.h + a.rank : a.h, t == 2 ? 2 * a.rank : a.rank,
-                              a.M, a.rank * 4, 64, 128, sw);
+    for (int t = 0; t <= C::kTerms; ++t) {
+      const bool all = t == C::kTerms;
+      rc = make_tensor_map_2d(&tC.h[all ? 3 : t], bf, all ? a.h : a.h + t * a.rank,
+                              all ? C::kTerms * a.rank : a.rank, a.M, C::kTerms * a.rank * 2, 64,
+                              128, sw);
       if (rc != TG_OK) return rc;
     }
   }

@@ -119,8 +119,8 @@ def test_lora_rejects_before_launch(L, kw, code):
     (tg.TG_CALL_GROUP_ROWS, (2048, 64, 1), 0),                    # one CTA
     (tg.TG_CALL_GROUP_ROWS, (2049, 64, 1), 2 * 65 * 4),           # CTAs of 2048 rows
     (tg.TG_CALL_GROUP_ROWS, (1 << 22, 256, 1), 256 * 257 * 4),    # at most 256 of them
-    (tg.TG_CALL_GEMM_BF16_LORA, (64, 16, 1), 64 * 16 * 4),
-    (tg.TG_CALL_GEMM_BF16_LORA, (1000, 24, 1), 96000 + 1000 * 4 + (2 * (1000 // 192) + 2) * 4),
+    (tg.TG_CALL_GEMM_BF16_LORA, (64, 16, 1), 64 * 16 * 6),
+    (tg.TG_CALL_GEMM_BF16_LORA, (1000, 24, 1), 144128 + 1000 * 4 + (2 * (1000 // 192) + 2) * 4),
 ])
 def test_workspace_bytes(L, call, shape, want):
     assert tg.workspace_bytes(call, *shape) == want
