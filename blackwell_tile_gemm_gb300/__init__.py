@@ -22,6 +22,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 import threading
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
@@ -119,6 +120,8 @@ def lib() -> ctypes.CDLL:
         L.gemm_bf16_gather.restype = i32
         L.gemm_bf16_gather.argtypes = [vp, i64, i64, vp, i64, vp, i64, vp, i64, i64, i64, i32,
                                        ctypes.POINTER(tg_epilogue), u32, vp]
+        L.tg_call_packed.restype = i32
+        L.tg_call_packed.argtypes = [i32, ctypes.c_char_p, i32]
         L.tg_group_rows.restype = i32
         L.tg_group_rows.argtypes = [vp, i64, i64, vp, vp, vp, vp]
         L.gemm_bf16_grouped.restype = i32
@@ -475,11 +478,29 @@ def _raw_stream(stream):
     return stream if isinstance(stream, int) else stream.cuda_stream
 
 
+TG_FN_GROUP_ROWS = 0
+TG_FN_GEMM_BF16_GROUPED = 1
+TG_FN_GEMM_BF16_GROUPED_DGRAD = 2
+TG_FN_GEMM_BF16_GROUPED_WGRAD = 3
+TG_FN_GEMM_BF16_LORA = 4
+# Each call's arguments as 64-bit words (pointers as addresses, None as 0).
+_WORDS = [struct.Struct("=%dq" % n).pack for n in (7, 18, 15, 17, 23)]
+_COUNT = (7, 18, 15, 17, 23)
+_NAMES = ("tg_group_rows", "gemm_bf16_grouped", "gemm_bf16_grouped_dgrad",
+          "gemm_bf16_grouped_wgrad", "gemm_bf16_lora")
+
+
+def _call(fn, *words):
+    rc = (_lib or lib()).tg_call_packed(fn, _WORDS[fn](*words), _COUNT[fn])
+    if rc:
+        _check(rc, _NAMES[fn])
+
+
 def _epilogue(bias, bias_shape, bias_silu, epilogue_add, silu_affine, affine):
-    """make_epilogue, with a bias of the given shape."""
+    """make_epilogue, with a bias of the given shape; None for no epilogue."""
     if bias is None:
         if epilogue_add is None and silu_affine is None and affine is None:
-            return _EPI_NONE
+            return None
         return make_epilogue(epilogue_add, silu_affine, None, bias_silu, affine)
     if bias.shape != bias_shape:
         raise ValueError(f"bias must be {list(bias_shape)}")
@@ -504,10 +525,8 @@ def group_rows(ids, groups, *, stream=None):
     order = torch.empty_like(ids)
     slot = torch.empty_like(ids)
     offsets = torch.empty(int(groups) + 1, dtype=torch.int32, device=ids.device)
-    rc = (_lib or lib()).tg_group_rows(ptr, n, int(groups), offsets.data_ptr(), order.data_ptr(),
-                                       slot.data_ptr(), _raw_stream(stream))
-    if rc:
-        _check(rc, "tg_group_rows")
+    _call(TG_FN_GROUP_ROWS, ptr, n, int(groups), offsets.data_ptr(), order.data_ptr(),
+          slot.data_ptr(), _raw_stream(stream))
     return offsets, order, slot
 
 
@@ -529,16 +548,13 @@ def gemm_bf16_grouped(A, B, offsets, D=None, *, row_idx=None, out_dtype=None, ep
     if K != K2:
         raise ValueError("A is [rows, K] and B is [groups, N, K]")
     _, off = _int32_vector(offsets, "offsets", groups + 1)
-    a_rows, idx = M, None
+    a_rows, idx = M, 0
     if row_idx is not None:
         M, idx = _int32_vector(row_idx, "row_idx")
     D, code, ldd = _result(D, (M, N), out_dtype, A.device)
     epi = _epilogue(bias, (groups, N), bias_silu, epilogue_add, silu_affine, affine)
-    rc = (_lib or lib()).gemm_bf16_grouped(a, lda, a_rows, idx, off, groups, M, b, ldb, step,
-                                           D.data_ptr(), ldd, N, K, code,
-                                           ctypes.byref(epi), 0, _raw_stream(stream))
-    if rc:
-        _check(rc, "gemm_bf16_grouped")
+    _call(TG_FN_GEMM_BF16_GROUPED, a, lda, a_rows, idx, off, groups, M, b, ldb, step, D.data_ptr(),
+          ldd, N, K, code, ctypes.addressof(epi) if epi else 0, 0, _raw_stream(stream))
     return D
 
 
@@ -555,11 +571,8 @@ def gemm_bf16_grouped_dgrad(G, B, offsets, D=None, *, out_dtype=None, stream=Non
         raise ValueError("G is [M, N] and B is [groups, N, K]")
     _, off = _int32_vector(offsets, "offsets", groups + 1)
     D, code, ldd = _result(D, (M, K), out_dtype, G.device)
-    rc = (_lib or lib()).gemm_bf16_grouped_dgrad(g, ldg, off, groups, M, b, ldb, step,
-                                                 D.data_ptr(), ldd, N, K, code, 0,
-                                                 _raw_stream(stream))
-    if rc:
-        _check(rc, "gemm_bf16_grouped_dgrad")
+    _call(TG_FN_GEMM_BF16_GROUPED_DGRAD, g, ldg, off, groups, M, b, ldb, step, D.data_ptr(), ldd,
+          N, K, code, 0, _raw_stream(stream))
     return D
 
 
@@ -573,7 +586,7 @@ def gemm_bf16_grouped_wgrad(G, A, offsets, D=None, *, row_idx=None, out_dtype=No
     bf16 = _torch().bfloat16
     M, N, ldg, g = _matrix(G, "G", bf16)
     a_rows, K, lda, a = _matrix(A, "A", bf16)
-    idx = None
+    idx = 0
     if row_idx is not None:
         _, idx = _int32_vector(row_idx, "row_idx", M)
     elif a_rows != M:
@@ -584,11 +597,8 @@ def gemm_bf16_grouped_wgrad(G, A, offsets, D=None, *, row_idx=None, out_dtype=No
         raise ValueError("offsets must have groups + 1 elements")
     D, code, ldd = _result(D, (groups, N, K), out_dtype, G.device)
     step = D.stride(0) if groups > 1 else ldd * N
-    rc = (_lib or lib()).gemm_bf16_grouped_wgrad(g, ldg, a, lda, a_rows, idx, off, groups, M,
-                                                 D.data_ptr(), ldd, step, N, K, code, 0,
-                                                 _raw_stream(stream))
-    if rc:
-        _check(rc, "gemm_bf16_grouped_wgrad")
+    _call(TG_FN_GEMM_BF16_GROUPED_WGRAD, g, ldg, a, lda, a_rows, idx, off, groups, M, D.data_ptr(),
+          ldd, step, N, K, code, 0, _raw_stream(stream))
     return D
 
 
@@ -612,7 +622,7 @@ def gemm_bf16_lora(A, B, ids, down, up, D=None, *, scales=None, out_dtype=None, 
     adapters2, N2, rank2, ld_up, step_up, pu = _stack(up, "up", bf16)
     if K2 != K or N2 != N or rank2 != rank or adapters2 != adapters:
         raise ValueError("down is [adapters, rank, K] and up is [adapters, N, rank]")
-    ps = None
+    ps = 0
     if scales is not None:
         if (scales.dtype is not _torch().float32 or not scales.is_contiguous()
                 or scales.shape != (adapters,)):
@@ -621,12 +631,9 @@ def gemm_bf16_lora(A, B, ids, down, up, D=None, *, scales=None, out_dtype=None, 
     _, idp = _int32_vector(ids, "ids", M)
     D, code, ldd = _result(D, (M, N), out_dtype, A.device)
     epi = _epilogue(bias, (N,), bias_silu, epilogue_add, silu_affine, affine)
-    rc = (_lib or lib()).gemm_bf16_lora(a, lda, b, ldb, idp, pd, ld_down, step_down, pu, ld_up,
-                                        step_up, ps, adapters, rank, D.data_ptr(),
-                                        ldd, M, N, K, code, ctypes.byref(epi), 0,
-                                        _raw_stream(stream))
-    if rc:
-        _check(rc, "gemm_bf16_lora")
+    _call(TG_FN_GEMM_BF16_LORA, a, lda, b, ldb, idp, pd, ld_down, step_down, pu, ld_up, step_up, ps,
+          adapters, rank, D.data_ptr(), ldd, M, N, K, code, ctypes.addressof(epi) if epi else 0, 0,
+          _raw_stream(stream))
     return D
 
 

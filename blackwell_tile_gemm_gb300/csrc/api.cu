@@ -6,6 +6,9 @@
 // patterns", section "Group, repeat, and atom axes": a failed contract is an
 // error, never a search for another layout; "cp.async.bulk.tensor", section
 // "Legality conditions": 16-byte aligned bases and outer byte strides).
+#include <utility>
+#include <type_traits>
+#include <tuple>
 #include <cstdint>
 #include <cstdio>
 #include <cstring>
@@ -815,3 +818,43 @@ int tg_last_cuda_error(void) { return t_last_cuda_error; }
 int tg_version(void) { return 200; }
 
 }  // extern "C"
+
+namespace {
+
+template <class T>
+bool unpack(int64_t word, T* out) {
+  if constexpr (std::is_pointer_v<T>) {
+    *out = reinterpret_cast<T>(static_cast<uintptr_t>(word));
+  } else {
+    *out = static_cast<T>(word);
+    if (static_cast<int64_t>(*out) != word) return false;
+  }
+  return true;
+}
+
+template <class... T, size_t... I>
+int call_packed(int (*fn)(T...), const int64_t* args, int count, std::index_sequence<I...>) {
+  std::tuple<T...> a;
+  if (args == nullptr || count != static_cast<int>(sizeof...(T)) ||
+      !(unpack(args[I], &std::get<I>(a)) && ...))
+    return TG_ERR_INVALID_ARG;
+  return std::apply(fn, a);
+}
+
+template <class... T>
+int call_packed(int (*fn)(T...), const int64_t* args, int count) {
+  return call_packed(fn, args, count, std::index_sequence_for<T...>{});
+}
+
+}  // namespace
+
+extern "C" int tg_call_packed(int fn, const int64_t* args, int count) {
+  switch (fn) {
+    case TG_FN_GROUP_ROWS: return call_packed(tg_group_rows, args, count);
+    case TG_FN_GEMM_BF16_GROUPED: return call_packed(gemm_bf16_grouped, args, count);
+    case TG_FN_GEMM_BF16_GROUPED_DGRAD: return call_packed(gemm_bf16_grouped_dgrad, args, count);
+    case TG_FN_GEMM_BF16_GROUPED_WGRAD: return call_packed(gemm_bf16_grouped_wgrad, args, count);
+    case TG_FN_GEMM_BF16_LORA: return call_packed(gemm_bf16_lora, args, count);
+    default: return TG_ERR_INVALID_ARG;
+  }
+}

@@ -379,6 +379,23 @@ int gemm_bf16_lora(const void* A, int64_t lda, const void* B, int64_t ldb, const
                    int64_t rank, void* D, int64_t ldd, int64_t M, int64_t N, int64_t K,
                    int d_dtype, const tg_epilogue* epi, unsigned flags, void* cuda_stream);
 
+/*
+ * tg_call_packed -- one of the five calls above with its arguments as `count`
+ * 64-bit words in order, pointers as addresses: for bindings to languages that
+ * convert arguments one by one (Python's ctypes takes 2.3 us for the 23 of
+ * gemm_bf16_lora, 0.5 us this way).  Returns what the call returns, or
+ * TG_ERR_INVALID_ARG for an unknown `fn`, another count, or a word outside a
+ * 32-bit argument's range.
+ */
+enum {
+  TG_FN_GROUP_ROWS = 0,
+  TG_FN_GEMM_BF16_GROUPED = 1,
+  TG_FN_GEMM_BF16_GROUPED_DGRAD = 2,
+  TG_FN_GEMM_BF16_GROUPED_WGRAD = 3,
+  TG_FN_GEMM_BF16_LORA = 4
+};
+int tg_call_packed(int fn, const int64_t* args, int count);
+
 /* tg_gemm_tail_split -- the number of K pieces (1: none) into which
  * gemm_bf16 cuts each tile for this shape on the current device (flags: 0 or
  * TG_FLAG_CTA_PAIR), for operands in the current device's memory (a stream

@@ -173,3 +173,25 @@ def test_binding_rejects_before_calling_the_library(monkeypatch, call, exc):
     monkeypatch.setattr(tg, "_lib", Refuse())
     with pytest.raises(exc):
         call()
+
+
+def test_packed_calls(L):
+    """tg_call_packed checks what it unpacks and returns what the call does."""
+    import struct
+    rows = [A16, 0, 4, A16, A16, A16, 0]
+    lora = [A16, 64, A16, 64, A16, A16, 64, 1024, A16, 16, 1024, 0, 4, 16, A16, 64, 0, 64, 64, 0, 0,
+            0, 0]
+
+    def call(fn, words, count=None):
+        return L.tg_call_packed(fn, struct.pack("=%dq" % len(words), *words),
+                                len(words) if count is None else count)
+    assert call(tg.TG_FN_GEMM_BF16_LORA, lora) == 0                       # M = 0: nothing to do
+    assert call(tg.TG_FN_GEMM_BF16_LORA, lora[:1] + [60] + lora[2:]) == 0
+    assert call(tg.TG_FN_GEMM_BF16_LORA, lora[:13] + [12] + lora[14:]) == UNSUP   # rank 12
+    assert call(tg.TG_FN_GEMM_BF16_LORA, lora[:16] + [-1] + lora[17:]) == BAD
+    assert call(tg.TG_FN_GEMM_BF16_LORA, lora, 22) == BAD
+    assert call(tg.TG_FN_GEMM_BF16_LORA, lora[:19] + [1 << 32] + lora[20:]) == BAD   # not an int
+    assert call(tg.TG_FN_GROUP_ROWS, [A16, -1, 4, A16, A16, A16, 0]) == BAD
+    assert call(5, rows) == BAD
+    assert call(-1, rows) == BAD
+    assert L.tg_call_packed(tg.TG_FN_GROUP_ROWS, None, 7) == BAD
