@@ -16,8 +16,10 @@
 // Up to kOneCta rows run in one CTA and one launch.  Above, a counting kernel
 // writes every CTA's histogram to the workspace, and each CTA of the placing
 // kernel sums the ones before its own: two launches, the second of which
-// counts its own rows while the first ends.  (One cluster of 8 CTAs, in one
-// launch: 262144 rows in 256 groups 44 us.)
+// counts its own rows while the first ends.  256 rows in 64 groups take 3.0 us,
+// 262144 rows in 256 groups 11.4 us in a replayed graph (one cluster of 8 CTAs,
+// in one launch: 44 us); 3.1 MB are 0.5 us of HBM traffic, so what bounds it is
+// the chain of a launch, two walks and the sums between them.
 #include "tg_internal.h"
 #include "tg_ptx.cuh"
 

@@ -22,8 +22,9 @@
  *   - Ownership: the caller allocates and owns every buffer it passes.  The
  *     library keeps its own device memory per (device, stream): a workspace
  *     (scale images of the block-scaled calls, gathered or re-pitched rows,
- *     the skinny call's f32 partial sums) and the tail split's scratch (see
- *     "Tail split").  Calls on different streams never share it; it is never
+ *     the skinny call's f32 partial sums, histograms of tg_group_rows, the
+ *     rank values of gemm_bf16_lora) and the tail split's scratch (see "Tail
+ *     split"), which the grouped and adapter products use as well.  Calls on different streams never share it; it is never
  *     shrunk and lives until process exit.  The transpose allocates nothing.
  *   - Reserved workspace (see tg_reserve_workspace): after a reservation on a
  *     stream, no call on that stream allocates device memory or synchronises
@@ -368,7 +369,7 @@ int gemm_bf16_grouped_wgrad(const void* G, int64_t ldg, const void* A, int64_t l
  *   rank    : a multiple of 8, at most TG_MAX_RANK (smaller adapters are
  *             padded with zeros); otherwise TG_ERR_UNSUPPORTED.  flags: 0.
  * The rank values a row between the two adapter products are kept as two bf16
- * terms (16 significant bits) in the stream's workspace
+ * terms (17 significant bits; f32 D: three) in the stream's workspace
  * (TG_CALL_GEMM_BF16_LORA); the shared and the adapter term of D meet in f32.
  * Infinite or NaN weights of an adapter reach its own rows only.
  */
