@@ -32,15 +32,23 @@ using CfgGatherPairBf16 = GemmCfg<2, kKindBf16, 256, 2, 6, true, false, true>;
 // 16-byte row stride, which the TMA row-stride rule already requires).
 // One warp per gathered row: exactly K elements (16-byte vectors, then the
 // last K % 8 one by one), so nothing past column K of A is read.
+// kChained: launched beside the kernel before it (programmatic dependent
+// launch), for which it waits; so is what follows it.
+template <bool kChained>
 __global__ void gather_rows_kernel(const uint16_t* __restrict__ A, int64_t lda, int a_rows,
                                    const int* __restrict__ idx, int M, uint16_t* __restrict__ G,
                                    int64_t ldg, int K) {
+  if constexpr (kChained) {
+    griddep_wait();
+    griddep_launch_dependents();
+  }
   const int lane = threadIdx.x & 31;
   const int64_t warps = static_cast<int64_t>(gridDim.x) * (blockDim.x >> 5);
   const int kv = K / 8;
   for (int64_t i = blockIdx.x * static_cast<int64_t>(blockDim.x >> 5) + (threadIdx.x >> 5);
        i < M; i += warps) {
-    const int src = __ldg(idx + i);
+    // (Chained: not the read-only path, whose loads need not stay behind the wait.)
+    const int src = kChained ? __ldcg(idx + i) : __ldg(idx + i);
     const bool valid = src >= 0 && src < a_rows;
     const uint16_t* a = A + static_cast<int64_t>(valid ? src : 0) * lda;
     uint16_t* g = G + i * ldg;
@@ -69,10 +77,18 @@ int gather_to_workspace(const void* A, int64_t lda, int a_rows, const int* row_i
   *ld = (K + 63) / 64 * 64;
   int64_t blocks = (M + 7) / 8;
   if (blocks > 16 * static_cast<int64_t>(ctx->num_sms)) blocks = 16 * ctx->num_sms;
-  gather_rows_kernel<<<static_cast<unsigned>(blocks), 256, 0, stream>>>(
-      static_cast<const uint16_t*>(A), lda, a_rows, row_idx, static_cast<int>(M),
-      static_cast<uint16_t*>(ws), *ld, static_cast<int>(K));
-  const cudaError_t e = cudaGetLastError();
+  cudaLaunchConfig_t cfg{};
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.gridDim = dim3(static_cast<unsigned>(blocks), 1, 1);
+  cfg.blockDim = dim3(256, 1, 1);
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  const cudaError_t e = cudaLaunchKernelEx(
+      &cfg, gather_rows_kernel<true>, static_cast<const uint16_t*>(A), lda, a_rows, row_idx,
+      static_cast<int>(M), static_cast<uint16_t*>(ws), *ld, static_cast<int>(K));
   if (e != cudaSuccess) return cuda_fail(e);
   *rows = ws;
   return TG_OK;
@@ -85,7 +101,7 @@ int launch_gemm_bf16_pregather_impl(const void* A, int64_t lda, int a_rows, cons
   const int64_t ldg = (K + 63) / 64 * 64;
   int64_t blocks = (static_cast<int64_t>(M) + 7) / 8;
   if (blocks > 16 * static_cast<int64_t>(ctx->num_sms)) blocks = 16 * ctx->num_sms;
-  gather_rows_kernel<<<static_cast<unsigned>(blocks), 256, 0, stream>>>(
+  gather_rows_kernel<false><<<static_cast<unsigned>(blocks), 256, 0, stream>>>(
       static_cast<const uint16_t*>(A), lda, a_rows, row_idx, M,
       static_cast<uint16_t*>(workspace), ldg, K);
   cudaError_t e = cudaGetLastError();

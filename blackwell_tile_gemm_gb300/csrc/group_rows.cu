@@ -45,7 +45,7 @@ struct RowsArgs {
 };
 
 __device__ __forceinline__ int key_of(const RowsArgs& p, int i) {
-  const int id = __ldg(p.ids + i);
+  const int id = p.ids[i];   // (a read-only load need not stay behind griddep_wait)
   return static_cast<unsigned>(id) < static_cast<unsigned>(p.groups) ? id : p.groups;
 }
 
