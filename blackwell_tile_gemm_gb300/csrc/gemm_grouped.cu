@@ -66,7 +66,8 @@ int gemm_bf16_grouped(const void* A, int64_t lda, int64_t a_rows, const int32_t*
   DeviceCtx* ctx = current_ctx();
   if (!ctx) return TG_ERR_CUDA;
   cudaStream_t stream = static_cast<cudaStream_t>(cuda_stream);
-  if (row_idx != nullptr && K > 0) {
+  const bool in_place = grouped_gathers(M, groups);
+  if (row_idx != nullptr && K > 0 && !in_place) {
     const void* rows = nullptr;
     rc = gather_to_workspace(A, lda, static_cast<int>(a_rows), row_idx, M, K, &rows, &lda, stream,
                              ctx);
@@ -82,6 +83,10 @@ int gemm_bf16_grouped(const void* A, int64_t lda, int64_t a_rows, const int32_t*
   a.D = D;
   a.ldd = ldd;
   a.epi = e;
+  if (K > 0 && in_place) {
+    a.row_idx = row_idx;
+    a.num_rows = static_cast<int>(a_rows);
+  }
   GroupedOperands o{};
   o.wide = B;
   o.wide_ld = ldb;

@@ -105,6 +105,8 @@ struct GroupedArgs {
   // adapters
   const int* ids;          // [M]
   int adapters, rank;
+  const int* row_idx;      // few rows forward, or null: row i is row row_idx[i] of the
+  int num_rows;            // column operand's num_rows
   uint16_t* h;             // [M][h_terms][rank] bf16: each row of H as a sum of terms, which
   int h_terms;             // kAdapterDown writes: 2, or 3 where D is f32
   const float* scales;     // kAdapterDown: [adapters], or null for 1
@@ -145,6 +147,7 @@ struct GroupedCfg {
   static constexpr bool kWideMn = kMode == kGroupedDgrad || kMode == kGroupedWgrad;
   static constexpr bool kColMn = kMode == kGroupedWgrad;
   static constexpr bool kSplit = kCtaGroup == 1;
+  static constexpr bool kGather = kMode == kGroupedForward && kSplit;   // row_idx is read here
   // Whether a last wave may be cut into pieces (grouped_plan).  Pairs carry the
   // join only where it can pay: it costs the others registers and up to 8%
   // (wgrad of 16 groups x 2048 x 4096 with 128 rows each: 56 -> 60 us).
@@ -1054,6 +1057,37 @@ __global__ void __launch_bounds__(C::kThreads, 1)
           ok = __shfl_sync(0xFFFFFFFFu, ok, 0);
         }
         continue;
+      }
+      if constexpr (C::kGather) {
+        if (p.row_idx != nullptr) {
+          // Rows picked by index: each lane four of them, in one gather (box
+          // one row high); rows past the tile or outside the operand read zeros.
+          int r[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const int i = 4 * lane + j;
+            const int src = i < w.rows ? p.row_idx[w.row0 + i] : -1;
+            r[j] = static_cast<uint32_t>(src) < static_cast<uint32_t>(p.num_rows) ? src : p.num_rows;
+          }
+          for (int j = 0, kb = w.k0; j < w.nk; ++j, kb += w.ks) {
+            if (lane == 0) {
+              ok = wait_slot();
+              if (ok)
+                mbar_arrive_expect_tx(&full_bar[stage],
+                                      C::W_BYTES + static_cast<uint32_t>(w.ncols) * 128u);
+            }
+            ok = __shfl_sync(0xFFFFFFFFu, ok, 0);
+            if (!ok) break;
+            const uint32_t fb = full0 + 8u * stage;
+            if (4 * lane < w.ncols)
+              tma_gather4_2d(sC + stage * C::C_BYTES + 512u * static_cast<uint32_t>(lane),
+                             &tmC.box[0], fb, kb * 64, r[0], r[1], r[2], r[3], pol);
+            if (lane == 0)
+              tma_load_3d(sW + stage * C::W_BYTES, &tmW, fb, kb * 64, wx, w.g, pol);
+            next_slot();
+          }
+          continue;
+        }
       }
       if (lane == 0) {
         const uint32_t cbytes = static_cast<uint32_t>(loaded) * 128u;

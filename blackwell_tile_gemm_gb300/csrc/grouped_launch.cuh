@@ -36,6 +36,12 @@ inline GroupedArgs grouped_args(DeviceCtx* ctx) {
 // groups x 1024 x 1024 10.1 against 8.7.
 inline bool grouped_few_rows(int64_t M, int64_t groups) { return M <= 48 * groups; }
 
+// Of those, rows picked by index are gathered by the product's own loads (four
+// rows an operation, which a short tile hides behind its weights), else copied
+// together first.  64 groups x 2048 x 4096, 16 rows each: 173 us against 177,
+// 32 rows 223 against 181; 5 rows in 10 groups x 896 x 2816 12.0 against 13.2.
+inline bool grouped_gathers(int64_t M, int64_t groups) { return M <= 16 * groups; }
+
 // CTA pairs with a split last wave: a contraction of at least 96 stages and
 // tiles for less than two waves (`tiles`: at least so many, sizes of groups
 // being the device's).  22374 rows in 2 groups x 896 x 768, wgrad (24 tiles of
@@ -129,8 +135,9 @@ int launch_grouped(const GroupedOperands& operands, const GroupedArgs& args, cud
         C::kWideMn ? 64 : C::kMode == kAdapterDown ? a.wide_box : 128, sw);
     if (rc != TG_OK) return rc;
     for (int b = 0; b < kColBoxes; ++b) {
-      rc = make_tensor_map_2d(&tC.box[b], bf, o.cols, o.k, a.M, o.cols_ld * 2, 64,
-                              C::kBoxStep * (b + 1), sw);
+      const bool gather = C::kGather && a.row_idx != nullptr;
+      rc = make_tensor_map_2d(&tC.box[b], bf, o.cols, o.k, gather ? a.num_rows : a.M,
+                              o.cols_ld * 2, 64, gather ? 1 : C::kBoxStep * (b + 1), sw);
       if (rc != TG_OK) return rc;
     }
   }

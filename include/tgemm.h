@@ -319,8 +319,9 @@ int tg_group_rows(const int32_t* ids, int64_t n, int64_t groups, int32_t* offset
  * group g, with r(i) = row_idx[i], or i where row_idx is NULL.
  *   A       : device, bf16 [a_rows, K], row stride lda.
  *   row_idx : device, int32 [M], or NULL (then a_rows >= M).  An index outside
- *             [0, a_rows) gives a zero row (D = epi(0)).  The rows are
- *             gathered into the stream's workspace first (TG_CALL_GEMM_BF16_GATHER).
+ *             [0, a_rows) gives a zero row (D = epi(0)).  More than 16 rows a
+ *             group (M > 16 groups) are gathered into the stream's workspace
+ *             first (TG_CALL_GEMM_BF16_GATHER).
  *   D       : device, [M, N] f32 or bf16.  Rows in no group are set to zero.
  *   epi     : as for gemm_bf16_ex, except that bias is [groups][N] (contiguous).
  */
