@@ -1715,18 +1715,23 @@ __global__ void __launch_bounds__(C::kThreads, 1)
         constexpr int kOwn = C::kTileN / 64;
         float m[kOwn][32];
 #pragma unroll
-        for (int q = 0; q < kOwn; ++q) {
-          grouped_zero(m[q]);
-          if constexpr (C::kMode == kAdapter)
-            add_adapter_terms<C::kTerms>(p, w, S, 4 * q, w.row0 + 32 * (half + 2 * q), end, x - lane, lane,
-                              inputs_ready, m[q]);
-        }
-        if constexpr (C::kMode == kAdapter)
-          if (!inputs_ready) {
-            griddep_wait();
-            inputs_ready = true;
+        for (int q = 0; q < kOwn; ++q) grouped_zero(m[q]);
+        // The adapter term comes before the last accumulators: while it waits
+        // for H and for its own loads, the MMAs have those to fill.  (First of
+        // all, the chunks of a long f32 contraction would wait for it: 256 rows
+        // x 8192 x 8192, rank 16, 71 us instead of 64; 1444 x 1086 x 7085, rank
+        // 128, 92 instead of 84.)
+        const int before = max(0, chunks - C::kAccBufs);
+        for (int c = 0; c <= chunks; ++c) {
+          if constexpr (C::kMode == kAdapter) {
+            if (c == before) {
+#pragma unroll
+              for (int q = 0; q < kOwn; ++q)
+                add_adapter_terms<C::kTerms>(p, w, S, 4 * q, w.row0 + 32 * (half + 2 * q), end,
+                                             x - lane, lane, inputs_ready, m[q]);
+            }
           }
-        for (int c = 0; c < chunks; ++c) {
+          if (c == chunks) break;
           if (!acc_ready()) {
             ok = false;
             break;
@@ -1739,6 +1744,11 @@ __global__ void __launch_bounds__(C::kThreads, 1)
           }
           hand_back();
         }
+        if constexpr (C::kMode == kAdapter)
+          if (!inputs_ready) {
+            griddep_wait();
+            inputs_ready = true;
+          }
         if (!ok) break;
         if (C::kTail && S > 1) {
           // The last of the tile's pieces adds them all.
