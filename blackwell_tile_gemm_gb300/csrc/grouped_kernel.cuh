@@ -393,9 +393,11 @@ __device__ __forceinline__ int grouped_chunk_end(int nk, int chunks, int c) {
 // stages + 2.  The join -- a piece's partial tile, its arrival, and the last
 // piece's sum -- takes 14 stages (5 us) for single CTAs (with 0: 16 rows in 8
 // groups x 2048 x 2048 43 us instead of 14; without pieces: 4 rows x 4096 x
-// 4096 24 us instead of 14), and 20 + 6 a piece for CTA pairs, whose partial
-// tiles are 128 KB a CTA (wgrad of 22374 rows in 2 groups x 896 x 768 62 -> 40
-// us, 1444 rows x 1086 x 7085 40 -> 34 us).
+// 4096 24 us instead of 14); with the adapter term, where the tile's rows are
+// known, 10 (3.7 us for 4 rows and 4 pieces) and the last piece's reads (7.8 us
+// for 118 rows and 8); and 20 + 6 a piece for CTA pairs, whose partial tiles
+// are 128 KB a CTA (wgrad of 22374 rows in 2 groups x 896 x 768 62 -> 40 us,
+// 1444 rows x 1086 x 7085 40 -> 34 us).
 struct GroupedPlan {
   int full;    // tiles run whole
   int S;       // pieces of the others
@@ -404,25 +406,34 @@ struct GroupedPlan {
 // A few-row tile's adapter term, which its pieces share out too, runs beside
 // the contraction: about 6 stages' time for each 8 rows of a warp and 32 of
 // the rank (39 rows x 1229 x 638, rank 128: 36 -> 28 us).
+//
+// Lane c weighs c pieces: one after the other, the divisions took 1.2 us before
+// the first load (4 rows x 4096 x 4096, rank 16: the call 14.6 -> 14.0 us; 118
+// rows x 667 x 735, rank 8, with fewer pieces too: 19.4 -> 18.0).
 template <class C>
-__device__ __forceinline__ GroupedPlan grouped_plan(const GroupedArgs& p, int tiles, int units) {
+__device__ __forceinline__ GroupedPlan grouped_plan(const GroupedArgs& p, int tiles, int units,
+                                                    int lane) {
   GroupedPlan g{tiles, 1, tiles};
   if constexpr (!C::kTail) return g;
   constexpr bool kTerms = C::kMode == kAdapter && C::kSplit;
   const int full = tiles / units * units;
   const int rest = tiles - full;
-  const int terms = kTerms ? (min(p.M, C::kTileN) + 15) / 16 * ((p.rank + 31) / 32) * 6 : 0;
-  int cost = (max(p.num_k_blocks, terms) + 2) * 4 / 5;   // pieces have to gain a fifth
-  for (int c = 2; c <= 8 && rest > 0; ++c) {
-    if (p.num_k_blocks < (kTerms ? c : 4 * c) || rest * c > p.max_slots || rest > p.max_counters)
-      break;
-    const int join = C::kCtaGroup == 1 ? 14 : 20 + 6 * c;
-    const int v = (rest * c + units - 1) / units *
-                  ((max(p.num_k_blocks, terms) + c - 1) / c + join);
-    if (v < cost) {
-      cost = v;
-      g = GroupedPlan{full, c, full + rest * c};
-    }
+  const int rows = min(p.M, C::kTileN);
+  const int terms = kTerms ? (rows + 15) / 16 * ((p.rank + 31) / 32) * 6 : 0;
+  const int work = max(p.num_k_blocks, terms);
+  const int whole = (work + 2) * 4 / 5;   // pieces have to gain a fifth
+  const int c = max(lane, 1);
+  uint32_t cost = 0xFFFFFFFFu;
+  if (c >= 2 && c <= 8 && rest > 0 && p.num_k_blocks >= (kTerms ? c : 4 * c) &&
+      rest * c <= p.max_slots && rest <= p.max_counters) {
+    const int join = kTerms ? 10 + 3 * c * rows / 256 : C::kCtaGroup == 1 ? 14 : 20 + 6 * c;
+    cost = static_cast<uint32_t>((rest * c + units - 1) / units) *
+           static_cast<uint32_t>((work + c - 1) / c + join);
+  }
+  const uint32_t least = __reduce_min_sync(0xFFFFFFFFu, cost);
+  if (least < static_cast<uint32_t>(whole)) {
+    const int S = __ffs(__ballot_sync(0xFFFFFFFFu, cost == least)) - 1;
+    g = GroupedPlan{full, S, full + rest * S};
   }
   return g;
 }
@@ -958,7 +969,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
   GroupWalk<C> walk;
   int first_row, end_row;
   const int tiles = walk.total(p, lane, &first_row, &end_row);
-  const GroupedPlan plan = grouped_plan<C>(p, tiles, num_units);
+  const GroupedPlan plan = grouped_plan<C>(p, tiles, num_units, lane);
   const int num_items = plan.items;
   GroupedWork w;
   // Work item u of the grid: S pieces from tile plan.full on.
