@@ -219,10 +219,12 @@ struct GroupedWork {
   int piece;
 };
 
+static __device__ __noinline__ int large_div(int a, int b) { return a / b; }
 // a / b for a >= 0, b > 0: the float quotient of numbers below 2^22 is off by
-// less than one.
+// less than one.  (A call for the others: inlined, they made every use longer
+// than the division it replaces.)
 __device__ __forceinline__ int small_div(int a, int b) {
-  if (a >= 1 << 22) return a / b;
+  if (a >= 1 << 22) return large_div(a, b);
   int q = __float2int_rd(__fdividef(static_cast<float>(a), static_cast<float>(b)));
   const int r = a - q * b;
   if (r < 0) --q;
@@ -328,7 +330,8 @@ struct GroupWalk {
     // The group's rows in nct tiles of equal size (a multiple of kColStep).
     size = C::kMode == kAdapterDown || C::kColMn
                ? C::kTileN
-               : ((r1 - r0 + nct - 1) / nct + C::kColStep - 1) / C::kColStep * C::kColStep;
+               : (small_div(r1 - r0 + nct - 1, max(nct, 1)) + C::kColStep - 1) / C::kColStep *
+                     C::kColStep;
   }
   __device__ __forceinline__ void find(const GroupedArgs& p, int lane, int t, int piece, int S,
                                        GroupedWork& w) {
@@ -357,7 +360,8 @@ struct GroupWalk {
       w.ncols = w.rows <= 128 ? 128 : 256;
       w.base = r0;
       w.len = r1 - r0;
-      w.nk = ((w.len + 63) / 64 - piece + S - 1) / S;   // (0 for more pieces than stages)
+      // (0 for more pieces than stages)
+      w.nk = small_div((w.len + 63) / 64 - piece + S - 1, S);
       w.k0 = piece;
       w.ks = S;
     } else {
@@ -368,7 +372,7 @@ struct GroupWalk {
       // a tile read neighbouring 128-byte chunks of the same rows.
       w.k0 = piece;
       w.ks = S;
-      w.nk = (p.num_k_blocks - piece + S - 1) / S;
+      w.nk = small_div(p.num_k_blocks - piece + S - 1, S);
       w.base = 0;
       w.len = 0;
     }
@@ -416,7 +420,7 @@ __device__ __forceinline__ GroupedPlan grouped_plan(const GroupedArgs& p, int ti
   GroupedPlan g{tiles, 1, tiles};
   if constexpr (!C::kTail) return g;
   constexpr bool kTerms = C::kMode == kAdapter && C::kSplit;
-  const int full = tiles / units * units;
+  const int full = small_div(tiles, units) * units;
   const int rest = tiles - full;
   const int rows = min(p.M, C::kTileN);
   const int terms = kTerms ? (rows + 15) / 16 * ((p.rank + 31) / 32) * 6 : 0;
@@ -978,7 +982,8 @@ __global__ void __launch_bounds__(C::kThreads, 1)
     if (C::kTail && u >= plan.full) {
       const int v = u - plan.full;
       S = plan.S;
-      walk.find(p, lane, plan.full + v / S, v % S, S, w);
+      const int t = small_div(v, S);
+      walk.find(p, lane, plan.full + t, v - t * S, S, w);
       w.tile -= plan.full;
     } else {
       S = 1;
