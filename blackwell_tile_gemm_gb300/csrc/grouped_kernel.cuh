@@ -72,7 +72,7 @@
 #include <cuda.h>
 
 #include "epilogue.cuh"
-#include "tg_ptx.cuh"
+#include "grouped_ptx.cuh"
 
 namespace tg {
 
