@@ -73,6 +73,7 @@
 
 #include "epilogue.cuh"
 #include "grouped_ptx.cuh"
+#include "tail_plan.h"
 
 namespace tg {
 
@@ -117,7 +118,7 @@ struct GroupedArgs {
   // split contraction
   int max_slots;           // partial tiles that fit (0: never split)
   int max_counters;
-  float* partials;         // [tile][piece][CTA of pair][kTileN][128] f32
+  float* partials;         // [tile][piece][CTA of pair][kTileN][128] f32 (tail_plan.h)
   uint32_t* counters;      // [tile][CTA of pair], 0 between launches
   uint32_t* status;
   uint64_t timeout_ns;
@@ -391,26 +392,6 @@ __device__ __forceinline__ int grouped_chunk_end(int nk, int chunks, int c) {
   return static_cast<int>(static_cast<int64_t>(nk) * (c + 1) / chunks);
 }
 
-// Full waves of whole tiles, then the tiles of a last, partial wave in pieces
-// of their contraction: the count (at most 8, each piece at least 4 stages)
-// with the least waves * (stages per piece + join), against the whole tiles'
-// stages + 2.  The join -- a piece's partial tile, its arrival, and the last
-// piece's sum -- takes 14 stages (5 us) for single CTAs (with 0: 16 rows in 8
-// groups x 2048 x 2048 43 us instead of 14; without pieces: 4 rows x 4096 x
-// 4096 24 us instead of 14); with the adapter term, where the tile's rows are
-// known, 10 (3.7 us for 4 rows and 4 pieces) and the last piece's reads (7.8 us
-// for 118 rows and 8); and 20 + 6 a piece for CTA pairs, whose partial tiles
-// are 128 KB a CTA (wgrad of 22374 rows in 2 groups x 896 x 768 62 -> 40 us,
-// 1444 rows x 1086 x 7085 40 -> 34 us).
-struct GroupedPlan {
-  int full;    // tiles run whole
-  int S;       // pieces of the others
-  int items;   // units of work
-};
-// A few-row tile's adapter term, which its pieces share out too, runs beside
-// the contraction: about 6 stages' time for each 8 rows of a warp and 32 of
-// the rank (39 rows x 1229 x 638, rank 128: 36 -> 28 us).
-//
 // Lane c weighs c pieces: one after the other, the divisions took 1.2 us before
 // the first load (4 rows x 4096 x 4096, rank 16: the call 14.6 -> 14.0 us; 118
 // rows x 667 x 735, rank 8, with fewer pieces too: 19.4 -> 18.0).
@@ -419,25 +400,21 @@ __device__ __forceinline__ GroupedPlan grouped_plan(const GroupedArgs& p, int ti
                                                     int lane) {
   GroupedPlan g{tiles, 1, tiles};
   if constexpr (!C::kTail) return g;
-  constexpr bool kTerms = C::kMode == kAdapter && C::kSplit;
   const int full = small_div(tiles, units) * units;
-  const int rest = tiles - full;
-  const int rows = min(p.M, C::kTileN);
-  const int terms = kTerms ? (rows + 15) / 16 * ((p.rank + 31) / 32) * 6 : 0;
-  const int work = max(p.num_k_blocks, terms);
-  const int whole = (work + 2) * 4 / 5;   // pieces have to gain a fifth
-  const int c = max(lane, 1);
-  uint32_t cost = 0xFFFFFFFFu;
-  if (c >= 2 && c <= 8 && rest > 0 && p.num_k_blocks >= (kTerms ? c : 4 * c) &&
-      rest * c <= p.max_slots && rest <= p.max_counters) {
-    const int join = kTerms ? 10 + 3 * c * rows / 256 : C::kCtaGroup == 1 ? 14 : 20 + 6 * c;
-    cost = static_cast<uint32_t>((rest * c + units - 1) / units) *
-           static_cast<uint32_t>((work + c - 1) / c + join);
-  }
+  const TailShape shape{tiles - full,
+                        units,
+                        p.num_k_blocks,
+                        C::kCtaGroup,
+                        C::kMode == kAdapter && C::kSplit,
+                        min(p.M, C::kTileN),
+                        p.rank,
+                        p.max_slots,
+                        p.max_counters};
+  const uint32_t cost = tail_cost(shape, lane);
   const uint32_t least = __reduce_min_sync(0xFFFFFFFFu, cost);
-  if (least < static_cast<uint32_t>(whole)) {
+  if (least < tail_limit(shape)) {
     const int S = __ffs(__ballot_sync(0xFFFFFFFFu, cost == least)) - 1;
-    g = GroupedPlan{full, S, full + rest * S};
+    g = GroupedPlan{full, S, full + shape.rest * S};
   }
   return g;
 }
@@ -1595,8 +1572,8 @@ __global__ void __launch_bounds__(C::kThreads, 1)
     constexpr int64_t kPart = C::kTileN * 128;
     auto part_of = [&](int piece) {
       return p.partials +
-             ((static_cast<int64_t>(w.tile) * S + piece) * C::kCtaGroup + rank) * kPart + slab * 32 +
-             lane;
+             tail_column(w.tile, piece, S, C::kCtaGroup, static_cast<int>(rank), C::kTileN, 0, 128) +
+             slab * 32 + lane;
     };
     auto publish = [&](int col, int left, const float (&v)[32]) {
       float* dst = part_of(w.piece) + col * 128;
@@ -1662,7 +1639,12 @@ __global__ void __launch_bounds__(C::kThreads, 1)
         const int mine = 32 * slab / slot;
         const int xr = w.wide0 + 32 * slab % slot + lane;
         const int row0 = w.row0 + 32 * half;
-        float* part = p.partials + static_cast<int64_t>(w.piece) * p.M * p.rank;
+        // A split tile's partial sums: [row of the tile][rank value of it].
+        const int width = tail_slot_width(true, p.rank);
+        auto part_at = [&](int piece, int row, int r) {
+          return p.partials +
+                 tail_column(w.tile, piece, S, 1, 0, C::kTileN, row - w.row0, width) + (r - w.wide0);
+        };
         auto keep = [&](int row, int r, float s) {
           split_bf16(s, p.h + static_cast<int64_t>(row) * (p.h_terms * p.rank) + r, p.rank,
                      p.h_terms);
@@ -1683,7 +1665,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
           for (int j = 0; j < 32; ++j) {
             if (row0 + j >= end || p.ids[row0 + j] != id) continue;
             if (C::kTail && S > 1)
-              __stcg(part + static_cast<int64_t>(row0 + j) * p.rank + xr, v[j] * scale);
+              __stcg(part_at(w.piece, row0 + j, xr), v[j] * scale);
             else
               keep(row0 + j, xr, v[j] * scale);
           }
@@ -1708,13 +1690,13 @@ __global__ void __launch_bounds__(C::kThreads, 1)
             const float* src[8];
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-              src[j] = p.partials + static_cast<int64_t>(min(row0 + j0 + j, end - 1)) * p.rank + x;
+              src[j] = part_at(0, min(row0 + j0 + j, end - 1), x);
               s[j] = __ldcg(src[j]);
             }
             for (int q = 1; q < S; ++q) {
               float t[8];
 #pragma unroll
-              for (int j = 0; j < 8; ++j) t[j] = __ldcg(src[j] + static_cast<int64_t>(q) * p.M * p.rank);
+              for (int j = 0; j < 8; ++j) t[j] = __ldcg(src[j] + q * (C::kTileN * width));
 #pragma unroll
               for (int j = 0; j < 8; ++j) s[j] += t[j];
             }

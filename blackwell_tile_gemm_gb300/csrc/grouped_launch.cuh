@@ -104,10 +104,9 @@ int launch_grouped(const GroupedOperands& operands, const GroupedArgs& args, cud
   if (tail_scratch(stream, &part, &counters)) {
     a.partials = part;
     a.counters = counters;
-    // kAdapterDown: [piece][row][rank] instead.
-    const int wide = C::kMode == kAdapterDown && a.wide < 128 ? a.wide : 128;
-    a.max_slots = static_cast<int>(kTailPartialBytes / (C::kTileN * C::kCtaGroup * wide * 4));
-    a.max_counters = kTailFlagWords / C::kCtaGroup;
+    a.max_slots = tail_max_slots(C::kTileN, C::kCtaGroup,
+                                 tail_slot_width(C::kMode == kAdapterDown, a.wide));
+    a.max_counters = tail_max_counters(C::kCtaGroup);
   }
   const CUtensorMapDataType bf = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
   const CUtensorMapSwizzle sw = CU_TENSOR_MAP_SWIZZLE_128B;

@@ -9,6 +9,7 @@
 #include "../../include/tgemm.h"
 #include "epilogue.cuh"
 #include "gemm_kinds.h"
+#include "tail_plan.h"
 
 namespace tg {
 
@@ -80,8 +81,7 @@ uint64_t alloc_count();
 // reservation or on the first call that splits on that stream; the counters
 // start at zero and every launch leaves them at zero.  false if it cannot be
 // had (the call then runs without a split).
-constexpr size_t kTailPartialBytes = size_t{20} << 20;   // >= 152 slots of 128 KiB
-constexpr int kTailFlagWords = 1024;
+// Its sizes: kTailPartialBytes, kTailFlagWords (tail_plan.h).
 bool tail_scratch(cudaStream_t stream, float** partials, uint32_t** counters);
 // Zero the tail counters of the current device (after a device-side error, a
 // launch may have left some set).
