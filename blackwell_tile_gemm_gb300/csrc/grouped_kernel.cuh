@@ -42,12 +42,19 @@
 // ceil(rank / 64) stages of up[id] and H for each term, into the same
 // accumulator: D is written once.  Where all rows of the tile have one adapter,
 // TMA's loads are all it takes (tiles start where a long run of rows with one
-// adapter does: there the offsets are those of the runs); else the fixing warps
-// put zeros over H's rows of other adapters.  A zero row times an infinite or
-// NaN weight would still be NaN, so there they also take such weights out of
-// up[id] and mark the tile; the epilogue of a marked tile adds what they give
-// in the rows they belong to.  A mixed stage takes about 0.65 us, a plain one
-// 0.34 (551 rows of 50 requests, rank 128, x 6463 x 6084: 134 us).
+// adapter does: there the offsets are those of the runs), unless up[id] holds
+// infinite or NaN weights: times a later term of H, which is zero or of either
+// sign, they would turn an infinite sum into NaN, so the fixing warps take them
+// out for the terms after the first.  (Whether it does they find out in memory
+// while the tile's K stages run: 8000 rows, rank 64, x 8192 x 4096 431 us, with
+// no look at the weights 421, with every such stage gone over in shared memory
+// 455.)
+// In other tiles the fixing warps put zeros over H's rows of other adapters.  A
+// zero row times an infinite or NaN weight would still be NaN, so there they
+// take such weights out for the first term too and mark the tile; the epilogue
+// of a marked tile adds what they give in the rows they belong to.  A mixed
+// stage takes about 0.65 us, a plain one 0.34 (551 rows of 50 requests, rank 128,
+// x 6463 x 6084: 134 us).
 //
 // Few rows (kSplit, single CTAs): the product is bound by reading the
 // weights, tiles are few, so S units share a tile's contraction; each writes
@@ -183,9 +190,10 @@ struct GroupedCfg {
   // lane) in registers.  (Adding the chunks to D in memory instead cost 80%:
   // 8192^3 wgrad 1579 us.)  bf16 D rounds at 2e-3 and needs none of it.
   static constexpr int kChunk = 12;
-  static constexpr int NUM_BARS = 2 * kStages + 2 * kAccBufs + 1 + (kFixWarps ? 2 * kStages : 0);
+  static constexpr int NUM_BARS = 2 * kStages + 2 * kAccBufs + 1 + (kFixWarps ? 2 * kStages : 0) +
+                                  (kExt ? 2 : 0);
   static constexpr int OFF_MISC = OFF_BAR + NUM_BARS * 8;
-  static constexpr int SMEM_BYTES = OFF_MISC + 32 + (kExt ? 64 : 0) + 1024;
+  static constexpr int SMEM_BYTES = OFF_MISC + 32 + (kExt ? 72 : 0) + 1024;
   static constexpr int TMEM_COLS = 2 * kTileN <= 32    ? 32
                                    : 2 * kTileN <= 64  ? 64
                                    : 2 * kTileN <= 128 ? 128
@@ -544,6 +552,32 @@ __device__ __forceinline__ uint32_t times_zero_bf16x2(uint32_t w, uint32_t z) {
   return d;
 }
 
+// Whether rows x0 .. x0 + 127 and columns r .. r + 63 of up[id] hold finite
+// weights only.  By one warp: 4 rows of 8 16-byte pieces a step.
+__device__ __forceinline__ bool finite_box(const GroupedArgs& p, int id, int x0, int r, int lane) {
+  const int col = r + 8 * (lane & 7);
+  uint32_t z[4] = {0u, 0u, 0u, 0u};
+  if (col < p.rank) {
+    const uint16_t* u = p.up + id * p.group_stride_up + col;
+    const int rows = min(128, p.wide - x0);
+#pragma unroll 1
+    for (int i0 = lane >> 3; i0 < rows; i0 += 32) {
+      uint4 v[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i)   // (past the last row: that again)
+        v[i] = ld_global_nc_v4(u + static_cast<int64_t>(x0 + min(i0 + 4 * i, rows - 1)) * p.ld_up);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        z[0] = times_zero_bf16x2(v[i].x, z[0]);
+        z[1] = times_zero_bf16x2(v[i].y, z[1]);
+        z[2] = times_zero_bf16x2(v[i].z, z[2]);
+        z[3] = times_zero_bf16x2(v[i].w, z[3]);
+      }
+    }
+  }
+  return !__any_sync(0xFFFFFFFFu, ((z[0] | z[1] | z[2] | z[3]) & 0x7FFF7FFFu) != 0u);
+}
+
 // epi(v) on the accumulators of one lane, whose column of D has bias b.
 template <int kN>
 __device__ __forceinline__ void grouped_epilogue(const Epi& e, float b, float (&v)[kN]) {
@@ -726,21 +760,49 @@ __device__ __forceinline__ void grouped_zero_rows(const GroupedArgs& p, int firs
   }
 }
 
-// What the infinite and NaN weights of up[id] that were taken out of a marked
-// tile give in the rows they belong to.
-static __device__ __noinline__ float marked_term(const GroupedArgs& p, int row, int x) {
-  const uint32_t id = static_cast<uint32_t>(p.ids[row]);
+// up[id][x, r] * H[row, r], summed over the rank values r in [from, to): all, or
+// those of infinite and NaN weights.
+__device__ __forceinline__ float scalar_term(const GroupedArgs& p, uint32_t id, int row, int x,
+                                             int from, int to, bool all) {
   float s = 0.0f;
-  if (id >= static_cast<uint32_t>(p.adapters)) return s;
   const uint16_t* u = p.up + id * p.group_stride_up + static_cast<int64_t>(x) * p.ld_up;
   const uint16_t* h = p.h + static_cast<int64_t>(row) * (p.h_terms * p.rank);
-  for (int r = 0; r < p.rank; ++r)
-    if ((u[r] & 0x7F80u) == 0x7F80u) {
+  for (int r = from; r < to; ++r)
+    if (all || (u[r] & 0x7F80u) == 0x7F80u) {
       float sum = __uint_as_float(static_cast<uint32_t>(h[r]) << 16);
       for (int t = 1; t < p.h_terms; ++t)
         sum += __uint_as_float(static_cast<uint32_t>(h[t * p.rank + r]) << 16);
       s += __uint_as_float(static_cast<uint32_t>(u[r]) << 16) * sum;
     }
+  return s;
+}
+// What the infinite and NaN weights of up[id] that were taken out of a marked
+// tile give in the rows they belong to.
+static __device__ __noinline__ float marked_term(const GroupedArgs& p, int row, int x) {
+  const uint32_t id = static_cast<uint32_t>(p.ids[row]);
+  return id < static_cast<uint32_t>(p.adapters) ? scalar_term(p, id, row, x, 0, p.rank, false) : 0.0f;
+}
+// The adapter term of row r0 + j of a few-row tile's batch, as far as it is this
+// piece's: steps turn, turn + share, ... of the batch, of 32 rank values each.
+// An infinite weight meets the whole rank value here; times a later term of H
+// alone, which is zero or of either sign, it would give a NaN that the
+// definition does not.
+static __device__ __noinline__ float shared_term(const GroupedArgs& p, int r0, int j, int rows, int x,
+                                                 int turn, int share) {
+  if (j >= rows || x >= p.wide) return 0.0f;   // (neither is stored)
+  const uint32_t id = static_cast<uint32_t>(p.ids[r0 + j]);
+  if (id >= static_cast<uint32_t>(p.adapters)) return 0.0f;
+  // The batch's adapters below this one, each counted at its first row.
+  int step = 0;
+  for (int i = 0; i < rows; ++i) {
+    const uint32_t other = static_cast<uint32_t>(p.ids[r0 + i]);
+    bool first = other < id;
+    for (int k = 0; k < i; ++k) first = first && static_cast<uint32_t>(p.ids[r0 + k]) != other;
+    if (first) step += (p.rank + 31) / 32;
+  }
+  float s = 0.0f;
+  for (int r = 0; r < p.rank; r += 32, ++step)
+    if (step % share == turn) s += scalar_term(p, id, r0 + j, x, r, min(r + 32, p.rank), true);
   return s;
 }
 __device__ __forceinline__ void add_marked_terms(const GroupedArgs& p, int row, int end, int x,
@@ -778,6 +840,7 @@ __device__ __forceinline__ void add_adapter_terms(const GroupedArgs& p, const Gr
   const int sets = S > batches ? small_div(S, share) : S;
   const int set = share > 1 ? small_div(w.piece, share) : w.piece;
   const int turn = w.piece - set * share;
+  uint32_t again = 0;
 #pragma unroll 1   // (one copy of a long body: instruction fetches are what a short call waits for)
   for (int b = 0; b < 4; ++b) {
     const int r0 = row + 8 * b;
@@ -799,8 +862,6 @@ __device__ __forceinline__ void add_adapter_terms(const GroupedArgs& p, const Gr
         id = next_adapter(ids, id, p.adapters);
       }
     };
-    advance(turn);
-    if (id < 0) continue;
     uint4 a[2][2], h[kTerms];
     auto load = [&]() {
       const bool in = 8 * q + k < p.rank;
@@ -821,6 +882,8 @@ __device__ __forceinline__ void add_adapter_terms(const GroupedArgs& p, const Gr
       for (int t = 0; t < kTerms; ++t)
         h[t] = own ? *reinterpret_cast<const uint4*>(hrow + t * p.rank + k) : zero;
     };
+    advance(turn);
+    if (id < 0) continue;
     load();
     while (id >= 0) {
       const uint32_t cur = static_cast<uint32_t>(id);
@@ -849,6 +912,18 @@ __device__ __forceinline__ void add_adapter_terms(const GroupedArgs& p, const Gr
         for (int e = 0; e < 4; ++e)
           if ((e & 1 ? id_c1 : id_c0) == cur) sum[t][e] += c[t][e];
     }
+    // NaN: an infinite weight may have met a later term of H.  Nothing for now,
+    // the batch's infinite and NaN sums after the others.
+    bool nan = false;
+#pragma unroll
+    for (int t = 0; t < 2; ++t)
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (sum[t][e] != sum[t][e]) {
+          sum[t][e] = 0.0f;
+          nan = true;
+        }
+    if (__any_sync(0xFFFFFFFFu, nan)) again |= 1u << b;
     // From (row of up g + 8 (e / 2) + 16 t, row of H 2 q + e % 2) to one lane
     // per row of up.
 #pragma unroll
@@ -865,6 +940,17 @@ __device__ __forceinline__ void add_adapter_terms(const GroupedArgs& p, const Gr
         if (b == i) v[8 * i + j] += term;
     }
   }
+  if (again == 0) return;
+#pragma unroll 1
+  for (int i = 0; i < 32; ++i) {
+    if (!(again & (1u << (i / 8)))) continue;
+    const int r0 = row + i / 8 * 8;
+    const float term = shared_term(p, r0, i % 8, min(8, end - r0), x0 + lane, turn, share);
+#pragma unroll
+    for (int j = 0; j < 32; ++j)
+      if (i == j && !(fabsf(term) < __uint_as_float(0x7F800000u))) v[j] += term;
+  }
+  __syncwarp();
 }
 
 template <class C>
@@ -885,6 +971,8 @@ __global__ void __launch_bounds__(C::kThreads, 1)
   uint64_t* drain_bar = acce_bar + C::kAccBufs;
   uint64_t* fix_bar = drain_bar + 1;               // [kStages] fixing warps -> MMA
   uint64_t* tail_bar = fix_bar + C::kStages;       // [kStages] TMA -> this CTA's fixing warps
+  uint64_t* checked_bar = tail_bar + C::kStages;   // fixing warps -> take_check
+  uint64_t* checked_empty = checked_bar + 1;       // and back
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::OFF_MISC);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::OFF_MISC + 4);
   volatile int* join = reinterpret_cast<volatile int*>(smem + C::OFF_MISC + 8);
@@ -892,6 +980,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
   // Marked tiles: entry n % 16 is n + 1 for the unit's n-th tile (the fixing
   // warps are never 16 tiles ahead: the ring is shorter).
   volatile int* marked = reinterpret_cast<volatile int*>(smem + C::OFF_MISC + 32);
+  volatile int* checked = reinterpret_cast<volatile int*>(smem + C::OFF_MISC + 96);   // [2]
 
   const int warp = threadIdx.x >> 5;
   const int lane = static_cast<int>(threadIdx.x & 31);
@@ -913,6 +1002,10 @@ __global__ void __launch_bounds__(C::kThreads, 1)
     }
     mbar_init(drain_bar, 1);
     *abort_flag = 0;
+    if constexpr (C::kExt) {
+      mbar_init(checked_bar, C::kFixWarps);
+      mbar_init(checked_empty, C::kFixWarps + (leader ? 2 : 1));   // (one MMA issuer a pair)
+    }
     if constexpr (C::kExt)
       for (int i = 0; i < 16; ++i) marked[i] = 0;
     fence_barrier_init();
@@ -944,6 +1037,18 @@ __global__ void __launch_bounds__(C::kThreads, 1)
   if (!kEarly || (!kFewRows && warp >= C::kEpiWarp0)) griddep_wait();
 
   const WaitGuard guard{p.status, abort_flag, p.timeout_ns};
+  // The fixing warps' word on the next tile of one adapter, whether the terms of
+  // H after the first need care: by one thread each of the producer, the MMA
+  // issuer and the fixing warps themselves.
+  auto take_check = [&](uint32_t& parity, int& care) -> bool {
+    if (!mbar_try_wait(smem_addr(checked_bar), parity) &&
+        !mbar_wait(checked_bar, parity, guard, kSiteGrFixIn))
+      return false;
+    care = checked[0] | checked[1];
+    mbar_arrive(checked_empty);
+    parity ^= 1u;
+    return true;
+  };
   const int unit = blockIdx.x / C::kCtaGroup;
   const int num_units = gridDim.x / C::kCtaGroup;
   // Every role's warp walks the groups itself.
@@ -993,6 +1098,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
     uint32_t phase = 0;
     uint32_t issued = 0, issued_parity = 0;    // full_bar
     uint32_t tailed = 0, tail_parity = 0;      // tail_bar: used, parity of the last use
+    uint32_t check_parity = 0;
     int ok = 1;
     auto wait_slot = [&]() -> bool {
       return mbar_try_wait(empty0 + 8u * stage, phase ^ 1u) ||
@@ -1020,6 +1126,9 @@ __global__ void __launch_bounds__(C::kThreads, 1)
       const int crow0 = w.row0 + static_cast<int>(rank) * crows;
       // MN-major: both of a box pair's 64-element chunks lie inside the row.
       const bool w_chunks = C::kWideMn && wx + 128 <= p.wide;
+      // Read here, used after the K stages.
+      uint32_t tile_ids[C::kTileN / 32];
+      if constexpr (C::kExt) load_tile_ids<C>(p, w, lane, tile_ids);
       const bool c_chunks = C::kColMn && crows == 128 && crow0 + 128 <= p.cols;
       if constexpr (C::kMode == kAdapterDown) {
         uint32_t ids[C::kTileN / 32];
@@ -1162,20 +1271,23 @@ __global__ void __launch_bounds__(C::kThreads, 1)
       }
       ok = __shfl_sync(0xFFFFFFFFu, ok, 0);
       if constexpr (C::kExt) {
-        uint32_t ids[C::kTileN / 32];
-        load_tile_ids<C>(p, w, lane, ids);
-        const bool mixed = mixed_adapters(ids, w.rows, lane, p.adapters);
+        const bool mixed = mixed_adapters(tile_ids, w.rows, lane, p.adapters);
         // (A split tile's adapter stages belong to its first piece.)
         const int per = (p.rank + 63) / 64 * 64;
         const int end = w.piece == 0 ? 64 * adapter_stages<C::kTerms>(p.rank, mixed) : 0;
+        int care = 0;
+        if (end > 0 && !mixed && next_adapter(tile_ids, -1, p.adapters) >= 0 && ok) {
+          if (lane == 0) ok = take_check(check_parity, care);
+          ok = __shfl_sync(0xFFFFFFFFu, ok, 0);
+        }
         for (int r = 0; r < end && ok; r += 64) {
-          for (int id = next_adapter(ids, -1, p.adapters); id >= 0 && ok;
-               id = next_adapter(ids, id, p.adapters)) {
+          for (int id = next_adapter(tile_ids, -1, p.adapters); id >= 0 && ok;
+               id = next_adapter(tile_ids, id, p.adapters)) {
             if (lane == 0) {
               ok = wait_slot();
               if (ok) {
                 const int term = small_div(r, per), rx = r - term * per;
-                if (mixed) {
+                if (mixed || (care && term > 0)) {
                   // Like a ragged stage's, the load completes in each CTA for
                   // its own fixing warps.
                   if (leader) mbar_arrive(&full_bar[stage]);
@@ -1183,7 +1295,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
                   const uint32_t tb = smem_addr(&tail_bar[stage]);
                   tma_load_3d(sW + stage * C::W_BYTES, &tmUp, tb, rx, wx, id, pol);
                   tma_load_2d(sC + stage * C::C_BYTES,
-                              &tmC.h[adapter_packed<C::kTerms>(p.rank, true) ? 3 : term], tb, rx,
+                              &tmC.h[adapter_packed<C::kTerms>(p.rank, mixed) ? 3 : term], tb, rx,
                               crow0, pol);
                   note_tail();
                 } else {
@@ -1230,6 +1342,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
       int acc = 0;
       uint32_t acc_phase = 0;
       uint32_t fix_parity = 0;      // parity of each stage's next fix
+      uint32_t check_parity = 0;
       int ok = 1;
       bool ready = false;
       auto wait_fix = [&]() -> bool {
@@ -1253,6 +1366,8 @@ __global__ void __launch_bounds__(C::kThreads, 1)
         take(u);
         const uint32_t idesc =
             idesc_bf16_f32_major(128 * C::kCtaGroup, w.ncols, C::kWideMn, C::kColMn);
+        uint32_t tile_ids[C::kTileN / 32];
+        if constexpr (C::kExt) load_tile_ids<C>(p, w, lane, tile_ids);
         // kAdapterDown: one contraction for each of the tile's passes.
         int passes = 1;
         if constexpr (C::kMode == kAdapterDown) {
@@ -1325,18 +1440,21 @@ __global__ void __launch_bounds__(C::kThreads, 1)
         ok = __shfl_sync(0xFFFFFFFFu, ok, 0);
         }
         if constexpr (C::kExt) {
-          uint32_t ids[C::kTileN / 32];
-          load_tile_ids<C>(p, w, lane, ids);
           const int per = (p.rank + 63) / 64 * 64;
-          const bool mixed = mixed_adapters(ids, w.rows, lane, p.adapters);
+          const bool mixed = mixed_adapters(tile_ids, w.rows, lane, p.adapters);
           const int end = w.piece == 0 ? 64 * adapter_stages<C::kTerms>(p.rank, mixed) : 0;
+          int care = 0;
+          if (end > 0 && !mixed && next_adapter(tile_ids, -1, p.adapters) >= 0 && ok) {
+            if (lane == 0) ok = take_check(check_parity, care);
+            ok = __shfl_sync(0xFFFFFFFFu, ok, 0);
+          }
           for (int r = 0; r < end && ok; r += 64) {
-            for (int id = next_adapter(ids, -1, p.adapters); id >= 0 && ok;
-                 id = next_adapter(ids, id, p.adapters)) {
+            for (int id = next_adapter(tile_ids, -1, p.adapters); id >= 0 && ok;
+                 id = next_adapter(tile_ids, id, p.adapters)) {
               if (lane == 0) {
                 ok = (ready || mbar_try_wait(full0 + 8u * stage, phase) ||
                       mbar_wait(&full_bar[stage], phase, guard, kSiteGrFull)) &&
-                     (!mixed || wait_fix());
+                     ((!mixed && (!care || r < per)) || wait_fix());
                 if (ok) {
                   tc_fence_after_sync();
                   const uint64_t wd = wdesc0 + static_cast<uint64_t>(stage * (C::W_BYTES >> 4));
@@ -1379,6 +1497,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
       const uint32_t sC = smem_addr(smem + C::OFF_C);
       uint32_t pos = 0;            // ring slots used so far
       uint32_t tail_use = 0;       // parity of each stage's next tail
+      uint32_t check_parity = 0;
       int ok = 1;
       int count = 0;               // tiles of this unit so far
       for (int u = unit; u < num_items && ok; u += num_units, ++count) {
@@ -1418,9 +1537,34 @@ __global__ void __launch_bounds__(C::kThreads, 1)
           const int per = (p.rank + 63) / 64 * 64;
           const int crows = w.ncols / C::kCtaGroup;
           const int r0 = static_cast<int>(rank) * crows;   // this CTA's rows of the tile
-          if (!mixed_adapters(ids, w.rows, lane, p.adapters)) {
-            if (next_adapter(ids, -1, p.adapters) >= 0) pos += adapter_stages<C::kTerms>(p.rank, false);
-            continue;
+          const bool mixed = mixed_adapters(ids, w.rows, lane, p.adapters);
+          if (!mixed) {
+            // One adapter: its stages are as TMA loads them, but for the terms
+            // after the first where up[id] holds infinite or NaN weights.  Each
+            // warp looks at one CTA's box in memory while the tile's K stages
+            // run, and both CTAs at both.
+            const int id = next_adapter(ids, -1, p.adapters);
+            if (id < 0) continue;
+            bool finite = true;
+            for (int r = 0; r < p.rank && finite; r += 64)
+              finite = finite_box(p, id, w.wide0 + 128 * fw, r, lane);
+            int care = 0;
+            if (lane == 0) {
+              ok = mbar_try_wait(smem_addr(checked_empty), check_parity ^ 1u) ||
+                   mbar_wait(checked_empty, check_parity ^ 1u, guard, kSiteGrFixIn);
+              if (ok) {
+                checked[fw] = finite ? 0 : 1;
+                mbar_arrive(checked_bar);
+                ok = take_check(check_parity, care);
+              }
+            }
+            ok = __shfl_sync(0xFFFFFFFFu, ok, 0);
+            if (!ok) break;
+            if (!__shfl_sync(0xFFFFFFFFu, care, 0)) {
+              pos += adapter_stages<C::kTerms>(p.rank, false);
+              continue;
+            }
+            pos += per / 64;
           }
           // The adapters of this CTA's rows lane, lane + 32, ...
           uint32_t own[C::C_ROWS / 32];
@@ -1433,11 +1577,12 @@ __global__ void __launch_bounds__(C::kThreads, 1)
           // A warp goes over 4 rows x 8 16-byte pieces at a time; this lane's
           // piece, by the step's parity, with the rows' swizzle.  Packed:
           // up[id] again every `copy` pieces.
-          const bool packed = adapter_packed<C::kTerms>(p.rank, true);
+          const bool packed = adapter_packed<C::kTerms>(p.rank, mixed);
           const uint32_t lr = static_cast<uint32_t>(lane >> 3), q = static_cast<uint32_t>(lane & 7);
           const uint32_t copy = static_cast<uint32_t>(p.rank / 8);
           const uint32_t at[2] = {128u * lr + ((q ^ lr) << 4), 128u * lr + ((q ^ (lr + 4u)) << 4)};
-          for (int r = 0; r < 64 * adapter_stages<C::kTerms>(p.rank, true) && ok; r += 64) {
+          const int stages = 64 * adapter_stages<C::kTerms>(p.rank, mixed);
+          for (int r = mixed ? 0 : per; r < stages && ok; r += 64) {
             const int cw = min(64, p.rank - (r - small_div(r, per) * per));   // columns (rest: zeros)
             for (int id = next_adapter(ids, -1, p.adapters); id >= 0 && ok;
                  id = next_adapter(ids, id, p.adapters), ++pos) {
@@ -1457,15 +1602,16 @@ __global__ void __launch_bounds__(C::kThreads, 1)
               for (int i = 0; i < C::C_ROWS / 32; ++i) {
                 const uint32_t others =
                     ~__ballot_sync(0xFFFFFFFFu, own[i] == static_cast<uint32_t>(id)) >> lr;
-                if (32 * i < crows) {
+                if (mixed && 32 * i < crows) {
 #pragma unroll
                   for (int t = 0; t < 8; ++t)
                     if (others & (1u << (4 * t)))
                       st_shared_v4(hdst + 4096u * i + 512u * t + at[t & 1], 0u, 0u, 0u, 0u);
                 }
               }
-              // up[id]: the pieces that hold weights, eight loads on their way
-              // at a time.
+              // up[id]: infinite and NaN weights go (those of one adapter's
+              // tile have met the first term).  The pieces that hold weights,
+              // eight loads on their way at a time.
               const uint32_t wsrc = sW + stage * C::W_BYTES;
               if (8 * static_cast<int>(q) < cw) {
 #pragma unroll
@@ -1482,7 +1628,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
                     z[3] = times_zero_bf16x2(u[i].w, z[3]);
                   }
                   if (((z[0] | z[1] | z[2] | z[3]) & 0x7FFF7FFFu) != 0u) {
-                    marked[count & 15] = count + 1;
+                    if (mixed) marked[count & 15] = count + 1;
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
                       u[i] = make_uint4(finite_bf16x2(u[i].x), finite_bf16x2(u[i].y),
