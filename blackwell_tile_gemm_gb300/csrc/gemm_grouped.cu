@@ -15,6 +15,8 @@ int check_sizes(int64_t M, int64_t N, int64_t K, int64_t groups, int d_dtype) {
     return TG_ERR_INVALID_ARG;
   if (groups < 1 || groups > TG_MAX_GROUPS) return TG_ERR_INVALID_ARG;
   if (d_dtype != TG_D_F32 && d_dtype != TG_D_BF16) return TG_ERR_INVALID_ARG;
+  if (M > kGroupedMaxExtent || N > kGroupedMaxExtent || K > kGroupedMaxExtent)
+    return TG_ERR_UNSUPPORTED;
   // Tiles of every group together stay below 2^31.
   const int64_t tiles = (M / 64 + groups) * ((N > K ? N : K) / 128 + 1);
   if (tiles > kMaxDim) return TG_ERR_UNSUPPORTED;

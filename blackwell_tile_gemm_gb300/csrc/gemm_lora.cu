@@ -369,6 +369,8 @@ extern "C" int gemm_bf16_lora(const void* A, int64_t lda, const void* B, int64_t
   if (d_dtype != TG_D_F32 && d_dtype != TG_D_BF16) return TG_ERR_INVALID_ARG;
   if (adapters < 0 || adapters > kMaxDim || rank < 1) return TG_ERR_INVALID_ARG;
   if (rank % 8 != 0 || rank > TG_MAX_RANK) return TG_ERR_UNSUPPORTED;
+  if (M > kGroupedMaxExtent || N > kGroupedMaxExtent || K > kGroupedMaxExtent)
+    return TG_ERR_UNSUPPORTED;
   if ((M / 64 + 1) * (N / 128 + 1) > kMaxDim) return TG_ERR_UNSUPPORTED;
   if (M == 0 || N == 0) return TG_OK;
   const int d_esize = d_dtype == TG_D_F32 ? 4 : 2;

@@ -20,6 +20,12 @@ struct GroupedOperands {
   int64_t up_ld, up_slice_stride, up_slices, up_rank;
 };
 
+// Most rows, columns and contraction terms.  The kernels count in 32 bits and go
+// past an extent by less than this: whole tiles, boxes and a K step of a cluster
+// (256 rows + 255, 128, 8 CTAs x 256).  2^31 - 1 rows in one group wrapped to no
+// tile at all.
+constexpr int64_t kGroupedMaxExtent = (int64_t{1} << 31) - 4096;
+
 inline GroupedArgs grouped_args(DeviceCtx* ctx) {
   GroupedArgs a{};
   a.status = ctx->status;

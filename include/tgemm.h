@@ -293,6 +293,8 @@ int gemm_bf16_gather(const void* A, int64_t lda, int64_t a_rows, const int32_t* 
  * stride ldb and group stride group_stride_b (elements, a multiple of 8; not
  * read for one group).  A contraction is summed in an order fixed by the
  * sizes and offsets: the same call returns the same bits.  flags: 0.
+ * M, N and K of these calls and of gemm_bf16_lora are at most 2^31 - 4096
+ * (TG_ERR_UNSUPPORTED above; TG_ERR_INVALID_ARG above 2^31 - 1).
  */
 enum { TG_MAX_GROUPS = 4096 };
 
