@@ -71,8 +71,13 @@ __device__ __forceinline__ float ld_dsmem(uint32_t addr) {
   return v;
 }
 
-// kRt 16-row tiles of `down` at a time.
-template <int kRt>
+// kRt 16-row tiles of `down` at a time.  kLong (f32 D): the tensor core truncates
+// at every addition to an accumulator, so after kDownChunk steps (768 terms, as in
+// grouped_kernel.cuh) a warp adds it to a total with rounding to nearest: adapter
+// term against 64 bits, K 65536, 9.3e-6 -> 8.6e-7.  (kAdapterDown, K 16384: 9.2e-6
+// -> 8.5e-7; 4447 rows of 30 requests, rank 16, x 634 x 4389 63 -> 66 us.)
+constexpr int kDownChunk = 24;
+template <int kRt, bool kLong>
 __global__ void __launch_bounds__(32 * kDownWarps) lora_down_kernel(const DownArgs p) {
   constexpr int kTok = 8;
   constexpr int kElems = 16 * kRt * kTok;
@@ -111,11 +116,9 @@ __global__ void __launch_bounds__(32 * kDownWarps) lora_down_kernel(const DownAr
     const uint16_t* down = p.down + id * p.stride_down;
     const float scale = p.scales ? p.scales[id] : 1.0f;
     for (int r0 = 16 * kRt * part0; r0 < p.rank; r0 += 16 * kRt * p.parts) {
-      float acc[kRt][4];
-#pragma unroll
-      for (int t = 0; t < kRt; ++t)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) acc[t][e] = 0.0f;
+      float acc[kRt][4] = {};
+      float total[kLong ? kRt : 1][4] = {};
+      int left = kDownChunk;
 #pragma unroll 2
       for (int k = kbeg + 32 * warp; k < kend; k += 32 * kDownWarps) {
         const int kk = k + 8 * q;
@@ -134,6 +137,24 @@ __global__ void __launch_bounds__(32 * kDownWarps) lora_down_kernel(const DownAr
           mma_m16n8k16(acc[t], a[t][0].x, a[t][1].x, a[t][0].y, a[t][1].y, b.x, b.y);
           mma_m16n8k16(acc[t], a[t][0].z, a[t][1].z, a[t][0].w, a[t][1].w, b.z, b.w);
         }
+        if constexpr (kLong) {
+          if (--left == 0) {
+            left = kDownChunk;
+#pragma unroll
+            for (int t = 0; t < kRt; ++t)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                total[t][e] += acc[t][e];
+                acc[t][e] = 0.0f;
+              }
+          }
+        }
+      }
+      if constexpr (kLong) {
+#pragma unroll
+        for (int t = 0; t < kRt; ++t)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) acc[t][e] += total[t][e];
       }
       // [down row][row of A]: c0, c1 at (g, 2q), (g, 2q + 1); c2, c3 8 rows on.
       float* mine = part + warp * kElems;
@@ -278,10 +299,10 @@ int launch_runs(const int* ids, int M, int adapters, int* runs, int* offsets, cu
   return e == cudaSuccess ? TG_OK : cuda_fail(e);
 }
 
-template <int kRt>
+template <int kRt, bool kLong>
 int launch_down(DownArgs a, cudaStream_t stream, DeviceCtx* ctx) {
   static std::atomic<int> prepared[64];
-  auto kern = lora_down_kernel<kRt>;
+  auto kern = lora_down_kernel<kRt, kLong>;
   constexpr int kTok = 8;
   constexpr int kSmem = kDownWarps * 16 * kRt * kTok * 4;
   if (prepared[ctx->device].load(std::memory_order_acquire) == 0) {
@@ -437,9 +458,14 @@ extern "C" int gemm_bf16_lora(const void* A, int64_t lda, const void* B, int64_t
   int rt = rank <= 16 ? 1 : rank <= 32 ? 2 : 4;
   while (!d.leave_few && rt > 1 && ceil_div_i(M, 8) * ceil_div_i(rank, 16 * rt) < ctx->num_sms)
     rt /= 2;
-  rc = rt == 1   ? launch_down<1>(d, stream, ctx)
-       : rt == 2 ? launch_down<2>(d, stream, ctx)
-                 : launch_down<4>(d, stream, ctx);
+  if (d_dtype == TG_D_BF16)
+    rc = rt == 1   ? launch_down<1, false>(d, stream, ctx)
+         : rt == 2 ? launch_down<2, false>(d, stream, ctx)
+                   : launch_down<4, false>(d, stream, ctx);
+  else
+    rc = rt == 1   ? launch_down<1, true>(d, stream, ctx)
+         : rt == 2 ? launch_down<2, true>(d, stream, ctx)
+                   : launch_down<4, true>(d, stream, ctx);
   if (rc != TG_OK) return rc;
   if (!few) {
     rc = launch_runs(ids, static_cast<int>(M), static_cast<int>(adapters), runs, starts, stream);
@@ -455,7 +481,9 @@ extern "C" int gemm_bf16_lora(const void* A, int64_t lda, const void* B, int64_t
     od.wide_rows = rank;
     od.wide_slices = adapters;
     od.wide_slice_stride = adapters > 1 ? stride_down : ld_down * rank;
-    rc = launch_grouped<GroupedCfg<kAdapterDown, 1, 64, 8, true>>(od, h, stream, ctx);
+    rc = d_dtype == TG_D_BF16
+             ? launch_grouped<GroupedCfg<kAdapterDown, 1, 64, 8, true>>(od, h, stream, ctx)
+             : launch_grouped<GroupedCfg<kAdapterDown, 1, 64, 8, false>>(od, h, stream, ctx);
     if (rc != TG_OK) return rc;
   }
   a.wide = static_cast<int>(N);

@@ -188,7 +188,8 @@ struct GroupedCfg {
   // into chunks of at most kChunk stages that are added in f32 with rounding
   // to nearest: each epilogue warp keeps its share of the tile (128 values a
   // lane) in registers.  (Adding the chunks to D in memory instead cost 80%:
-  // 8192^3 wgrad 1579 us.)  bf16 D rounds at 2e-3 and needs none of it.
+  // 8192^3 wgrad 1579 us.)  bf16 D rounds at 2e-3 and needs none of it.  (kAdapterDown:
+  // by the D that H is for, whose terms keep what the sums have.)
   static constexpr int kChunk = 12;
   static constexpr int NUM_BARS = 2 * kStages + 2 * kAccBufs + 1 + (kFixWarps ? 2 * kStages : 0) +
                                   (kExt ? 2 : 0);
@@ -1797,13 +1798,15 @@ __global__ void __launch_bounds__(C::kThreads, 1)
         };
         int last_id = -1, group[4];
         while (next_adapters(ids, last_id, 128 / slot, p.adapters, group) > 0) {
-          if (!acc_ready()) {
-            ok = false;
-            break;
-          }
           float v[32];
-          grouped_read<false>(t_slab + static_cast<uint32_t>(acc * C::kTileN + 32 * half), v);
-          hand_back();
+          grouped_zero(v);
+          for (int c = 0; c < chunks && ok; ++c) {
+            ok = acc_ready();
+            if (!ok) break;
+            grouped_read<true>(t_slab + static_cast<uint32_t>(acc * C::kTileN + 32 * half), v);
+            hand_back();
+          }
+          if (!ok) break;
           const int id = mine == 0 ? group[0] : mine == 1 ? group[1] : mine == 2 ? group[2] : group[3];
           if (id < 0 || xr >= p.wide) continue;
           const float scale = p.scales ? p.scales[id] : 1.0f;
