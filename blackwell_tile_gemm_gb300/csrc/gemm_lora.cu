@@ -75,14 +75,26 @@ __device__ __forceinline__ float ld_dsmem(uint32_t addr) {
 // at every addition to an accumulator, so after kDownChunk steps (768 terms, as in
 // grouped_kernel.cuh) a warp adds it to a total with rounding to nearest: adapter
 // term against 64 bits, K 65536, 9.3e-6 -> 8.6e-7.  (kAdapterDown, K 16384: 9.2e-6
-// -> 8.5e-7; 4447 rows of 30 requests, rank 16, x 634 x 4389 63 -> 66 us.)
+// -> 8.5e-7.)
+//
+// Blocks an SM holds hide the loads' latency: with kRt = 1 five instead of four
+// take 110 rows of 110 requests, rank 128, x 613 x 6740 from 82 to 69 us, with kRt
+// = 2 three instead of two 3077 rows of 46, rank 32, x 725 x 2004 from 34 to 30.
+// (kLong and kRt = 1 spill at five: 4447 rows of 30, rank 16, x 634 x 4389 66 us,
+// with four 60.)
 constexpr int kDownChunk = 24;
 template <int kRt, bool kLong>
-__global__ void __launch_bounds__(32 * kDownWarps) lora_down_kernel(const DownArgs p) {
+__global__ void __launch_bounds__(32 * kDownWarps, kRt == 1 ? (kLong ? 4 : 5) : kRt == 2 ? 3 : 2)
+    lora_down_kernel(const DownArgs p) {
   constexpr int kTok = 8;
   constexpr int kElems = 16 * kRt * kTok;
   extern __shared__ float part[];      // [warp][kElems], then the CTA's sum in [0]
   griddep_wait();
+  // The kernel before may have written A, and a read-only load of an address
+  // known before the wait need not stay behind it: A's address is made unknown
+  // until here.  (`down` is read where the ids say, which are plain loads.)
+  const uint16_t* A = p.A;
+  asm volatile("" : "+l"(A));
   // What the next kernel reads early (A, B, ids) was there before this one.
   griddep_launch_dependents();
   const int warp = threadIdx.x >> 5;
@@ -130,7 +142,7 @@ __global__ void __launch_bounds__(32 * kDownWarps) lora_down_kernel(const DownAr
             const int r = r0 + 16 * t + 8 * h + g;
             a[t][h] = r < p.rank ? load8(down + r * p.ld_down, kk, kend) : make_uint4(0u, 0u, 0u, 0u);
           }
-        const uint4 b = g < rows ? load8(p.A + static_cast<int64_t>(row0 + g) * p.lda, kk, kend)
+        const uint4 b = g < rows ? load8(A + static_cast<int64_t>(row0 + g) * p.lda, kk, kend)
                                  : make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
         for (int t = 0; t < kRt; ++t) {
