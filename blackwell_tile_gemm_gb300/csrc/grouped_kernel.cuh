@@ -1681,13 +1681,16 @@ __global__ void __launch_bounds__(C::kThreads, 1)
     // Waits for the next accumulator.
     auto acc_ready = [&]() -> bool {
       int got = 1;
-      if ((C::kTail && S > 1) || (C::kStaged && C::kBf16Out)) {
+      const bool all = C::kTail && plan.S > 1;
+      if (all || (C::kStaged && C::kBf16Out)) {
         // Warps that meet at named barriers below (all of a split tile's, the
         // two that share a staging box) must agree whether the accumulator
-        // arrived: one thread of them decides.
-        const bool decides = C::kTail && S > 1 ? warp == C::kEpiWarp0 && lane == 0 : box_lead;
-        const int id = C::kTail && S > 1 ? 1 : 2 + box, count = C::kTail && S > 1 ? 32 * C::kEpiWarps : 64;
-        volatile int* flag = go + (C::kTail && S > 1 ? 0 : box);
+        // arrived: one thread of them decides.  Where split tiles are to come,
+        // it does for the whole tiles before them as well: a warp that gave up
+        // there would be missing at the first split tile's barrier.
+        const bool decides = all ? warp == C::kEpiWarp0 && lane == 0 : box_lead;
+        const int id = all ? 1 : 2 + box, count = all ? 32 * C::kEpiWarps : 64;
+        volatile int* flag = go + (all ? 0 : box);
         if (decides) *flag = mbar_wait(&accf_bar[acc], acc_phase, guard, kSiteGrAccFull) ? 1 : 0;
         named_bar_sync(id, count);
         got = *flag;

@@ -42,3 +42,16 @@ def test_the_chained_row_copy_reads_its_index_behind_the_wait():
     body = text[text.index("void gather_rows_kernel"):text.index("size_t gather_workspace_bytes")]
     assert "kChained ? __ldcg(idx + i)" in body
     assert body.index("griddep_wait()") < body.index("__ldcg(idx + i)") < body.index("__ldg(av + k)")
+
+
+def test_epilogue_warps_that_meet_later_agree_on_every_wait():
+    """A wait that runs out in one warp and completes in the next must not send
+    the one home and the other to a barrier of both: where a plan has split
+    tiles, whose warps all meet, one thread decides every wait of the epilogue,
+    also those of the whole tiles before (whose own S is 1)."""
+    text = code("grouped_kernel.cuh")
+    body = text[text.index("auto acc_ready = "):text.index("auto hand_back = ")]
+    assert "C::kTail && plan.S > 1" in body
+    assert not re.search(r"(?<!plan\.)\bS > 1", body)
+    # Every wait for an accumulator goes through it.
+    assert text.count("mbar_wait(&accf_bar") == body.count("mbar_wait(&accf_bar") == 2
