@@ -448,6 +448,17 @@ def _int32_vector(t, name, length=None):
     return n[0], t.data_ptr()
 
 
+def _on_device(first, *others):
+    """Refuses tensors (None: not given) that are not on the current CUDA device:
+    their addresses would go to its kernels as they are."""
+    device = first.get_device()         # -1 for host memory
+    for t in others:
+        if t is not None and t.get_device() != device:
+            raise ValueError("operands must be on one device")
+    if device < 0 or device != _torch()._C._cuda_getDevice():
+        raise ValueError("operands must be on the current CUDA device")
+
+
 def _result(D, shape, out_dtype, device):
     """(D, its type's code, its row stride), allocated where the caller gave
     none: rows start on 16-byte boundaries (a padded view where the width asks
@@ -521,6 +532,7 @@ def group_rows(ids, groups, *, stream=None):
     slot [n] is its inverse (slot[order[j]] = j).  All int32, on the device.
     """
     n, ptr = _int32_vector(ids, "ids")
+    _on_device(ids)
     torch = _torch()
     order = torch.empty_like(ids)
     slot = torch.empty_like(ids)
@@ -553,6 +565,7 @@ def gemm_bf16_grouped(A, B, offsets, D=None, *, row_idx=None, out_dtype=None, ep
         M, idx = _int32_vector(row_idx, "row_idx")
     D, code, ldd = _result(D, (M, N), out_dtype, A.device)
     epi = _epilogue(bias, (groups, N), bias_silu, epilogue_add, silu_affine, affine)
+    _on_device(A, B, offsets, D, row_idx, bias)
     _call(TG_FN_GEMM_BF16_GROUPED, a, lda, a_rows, idx, off, groups, M, b, ldb, step, D.data_ptr(),
           ldd, N, K, code, ctypes.addressof(epi) if epi else 0, 0, _raw_stream(stream))
     return D
@@ -571,6 +584,7 @@ def gemm_bf16_grouped_dgrad(G, B, offsets, D=None, *, out_dtype=None, stream=Non
         raise ValueError("G is [M, N] and B is [groups, N, K]")
     _, off = _int32_vector(offsets, "offsets", groups + 1)
     D, code, ldd = _result(D, (M, K), out_dtype, G.device)
+    _on_device(G, B, offsets, D)
     _call(TG_FN_GEMM_BF16_GROUPED_DGRAD, g, ldg, off, groups, M, b, ldb, step, D.data_ptr(), ldd,
           N, K, code, 0, _raw_stream(stream))
     return D
@@ -596,6 +610,7 @@ def gemm_bf16_grouped_wgrad(G, A, offsets, D=None, *, row_idx=None, out_dtype=No
     if groups < 1:
         raise ValueError("offsets must have groups + 1 elements")
     D, code, ldd = _result(D, (groups, N, K), out_dtype, G.device)
+    _on_device(G, A, offsets, D, row_idx)
     step = D.stride(0) if groups > 1 else ldd * N
     _call(TG_FN_GEMM_BF16_GROUPED_WGRAD, g, ldg, a, lda, a_rows, idx, off, groups, M, D.data_ptr(),
           ldd, step, N, K, code, 0, _raw_stream(stream))
@@ -631,6 +646,7 @@ def gemm_bf16_lora(A, B, ids, down, up, D=None, *, scales=None, out_dtype=None, 
     _, idp = _int32_vector(ids, "ids", M)
     D, code, ldd = _result(D, (M, N), out_dtype, A.device)
     epi = _epilogue(bias, (N,), bias_silu, epilogue_add, silu_affine, affine)
+    _on_device(A, B, ids, down, up, D, scales, bias)
     _call(TG_FN_GEMM_BF16_LORA, a, lda, b, ldb, idp, pd, ld_down, step_down, pu, ld_up, step_up, ps,
           adapters, rank, D.data_ptr(), ldd, M, N, K, code, ctypes.addressof(epi) if epi else 0, 0,
           _raw_stream(stream))
