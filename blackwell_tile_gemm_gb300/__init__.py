@@ -552,7 +552,9 @@ def gemm_bf16_grouped(A, B, offsets, D=None, *, row_idx=None, out_dtype=None, ep
     product is row row_idx[i] of A (which then has any number of rows).
     ``bias`` is float32 [groups, N]; other epilogue keywords as for
     ``make_epilogue``.  D: float32 or bfloat16 [M, N] (default float32); rows
-    in no group are zero.
+    in no group are zero.  Where none is given it is allocated with rows that
+    start on 16-byte boundaries: a view of a wider tensor where N asks for it
+    (not a multiple of 4, for bfloat16 of 8).  So do the three calls below.
     """
     bf16 = _torch().bfloat16
     M, K, lda, a = _matrix(A, "A", bf16)

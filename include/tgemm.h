@@ -131,7 +131,8 @@ typedef struct tg_epilogue {
  * by the persistent schedule: forwards, or backwards in every other wave of
  * tiles (which keeps the K slices a unit needs next in L2), and split into
  * pieces in a tail split.  The same call (shape, flags, strides, device)
- * therefore always returns the same bits; calls with other flags, or on a
+ * therefore always returns the same bits (once the stream has the tail split's
+ * scratch: captured before that, a call runs unsplit); calls with other flags, or on a
  * device with another SM count, may differ in the last bits, within the
  * tolerances.  Exact inputs (every partial sum representable) give the exact
  * result whatever the order.
@@ -292,7 +293,10 @@ int gemm_bf16_gather(const void* A, int64_t lda, int64_t a_rows, const int32_t* 
  * All three are bf16 with f32 accumulation.  B is [groups][N][K] with row
  * stride ldb and group stride group_stride_b (elements, a multiple of 8; not
  * read for one group).  A contraction is summed in an order fixed by the
- * sizes and offsets: the same call returns the same bits.  flags: 0.
+ * sizes, the offsets and whether the stream has its tail scratch: it gets it by
+ * tg_reserve_workspace or by its first such call outside a capture, and from
+ * then on the same call returns the same bits, captured or not.  (Captured
+ * before that, the call runs unsplit and may differ in the last bits.)  flags: 0.
  * M, N and K of these calls and of gemm_bf16_lora are at most 2^31 - 4096
  * (TG_ERR_UNSUPPORTED above; TG_ERR_INVALID_ARG above 2^31 - 1).
  */
@@ -374,7 +378,8 @@ int gemm_bf16_grouped_wgrad(const void* G, int64_t ldg, const void* A, int64_t l
  * The rank values a row between the two adapter products are kept as two bf16
  * terms (17 significant bits; f32 D: three) in the stream's workspace
  * (TG_CALL_GEMM_BF16_LORA); the shared and the adapter term of D meet in f32.
- * Infinite or NaN weights of an adapter reach its own rows only.
+ * Infinite or NaN weights of an adapter reach its own rows only, and give there
+ * what the formula gives.  adapters = 0 runs gemm_bf16_ex, with its workspace.
  */
 enum { TG_MAX_RANK = 256 };
 int gemm_bf16_lora(const void* A, int64_t lda, const void* B, int64_t ldb, const int32_t* ids,
@@ -573,7 +578,8 @@ int tg_device_status(void* cuda_stream, uint32_t* site);
  *
  * tg_kernel_clock_record -- enable != 0: clear the sums and record the
  *   launches made after this call; 0: stop recording (the sums are kept).
- *   Synchronises the device.  The skinny GEMM and the transpose do not record.
+ *   Synchronises the device.  The skinny GEMM, the grouped and adapter products
+ *   and the transpose do not record.
  *   A launch captured into a CUDA graph while recording is on keeps adding
  *   whenever the graph is replayed, also after recording was stopped.
  * tg_kernel_clock_read -- the average SM clock in MHz (0 if nothing was
