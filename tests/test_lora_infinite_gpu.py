@@ -56,3 +56,30 @@ def test_infinite_weights_give_what_the_definition_gives(tg, M, N, kind, rank):
     bf = tg.gemm_bf16_lora(A, B, ids, down, up, out_dtype=torch.bfloat16)
     assert same(torch, bf, got.to(torch.bfloat16))
     assert tg.tg_device_status()[0] == tg.TG_OK
+
+
+@pytest.mark.parametrize("M,N,K", [(5, 264, 2048), (40, 136, 4096), (100, 264, 2048),
+                                   (700, WIDE[700], 6208)])
+@pytest.mark.parametrize("kind", ["one", "requests", "any"])
+@pytest.mark.parametrize("rank", [16, 72])
+def test_infinite_weights_in_split_tiles(tg, M, N, K, kind, rank):
+    """Tiles whose contraction, and for few rows whose adapter steps, are shared
+    out over several units: an infinity in one part, finite sums in the others."""
+    torch = torch_cuda()
+    adapters = 4
+    inf = float("inf")
+    gen = torch.Generator(device="cuda").manual_seed(M + rank)
+    A, B, down, up = case(gen, quarters, M, N, K, adapters, rank)
+    down[..., 64:] = 0
+    ids = plan(kind, M, adapters, M)
+    for n in list(range(3, N, 128)) + [N - 1]:
+        up[:, n, 0] = inf
+        up[:, n - 1, rank - 1] = -inf
+        up[1, n - 2, [1, rank - 2]] = inf
+        up[2, n - 2, 1], up[2, n - 2, rank - 1] = inf, -inf
+    want, _, _ = definition(torch, A, B, ids, down, up, None)
+    got = tg.gemm_bf16_lora(A, B, ids, down, up)
+    assert same(torch, got.double(), want)
+    bf = tg.gemm_bf16_lora(A, B, ids, down, up, out_dtype=torch.bfloat16)
+    assert same(torch, bf, got.to(torch.bfloat16))
+    assert tg.tg_device_status()[0] == tg.TG_OK
