@@ -212,6 +212,7 @@ struct GroupedCfg {
   static_assert(kTileN % 32 == 0 && kTileN <= 256, "MMA N");
   static_assert(C_BYTES % 1024 == 0, "swizzle atoms");
   static_assert(!kColMn || (kCtaGroup == 2 && kTileN == 256), "wgrad tiles");
+  static_assert(!kWideMn || kCtaGroup == 2, "the gradients run as CTA pairs");
 };
 
 // One work item.
@@ -1259,12 +1260,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
             }
             if (do_cols) tma_load_2d_pair(dC, &tmC.box[cbox], fb, kx, crow0, pol);
           } else {
-            if constexpr (C::kWideMn) {
-              for (int c = 0; c < 2; ++c)
-                tma_load_3d(dW + 8192 * c, &tmW, fb, wx + 64 * c, kx, w.g, pol);
-            } else {
-              tma_load_3d(dW, &tmW, fb, kx, wx, w.g, pol);
-            }
+            tma_load_3d(dW, &tmW, fb, kx, wx, w.g, pol);
             tma_load_2d(dC, &tmC.box[cbox], fb, kx, crow0, pol);
           }
           next_slot();

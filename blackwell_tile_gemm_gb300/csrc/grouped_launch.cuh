@@ -35,11 +35,13 @@ inline GroupedArgs grouped_args(DeviceCtx* ctx) {
   return a;
 }
 
-// Few rows per group: single CTAs with 64-column tiles, a deep ring of weight
-// boxes and a split contraction; else CTA pairs with tiles of 256 x 256.  64
-// groups x 2048 x 4096, 32 rows each: 174 us against 179 for pairs, 96 rows 277
+// The forward product with few rows per group on average: single CTAs with
+// 64-column tiles, a deep ring of weight boxes and a split contraction; else CTA
+// pairs with tiles of 256 x 256 (so the gradients always).  Groups of equal size,
+// 64 x 2048 x 4096, 32 rows each: 174 us against 179 for pairs, 96 rows 277
 // against 187; 5 rows in 10 groups x 896 x 2816 14 against 21; 32 rows in 8
-// groups x 1024 x 1024 10.1 against 8.7.
+// groups x 1024 x 1024 10.1 against 8.7.  (The sizes are the device's, so uneven
+// groups go by their mean.)
 inline bool grouped_few_rows(int64_t M, int64_t groups) { return M <= 48 * groups; }
 
 // Of those, rows picked by index are gathered by the product's own loads (four
