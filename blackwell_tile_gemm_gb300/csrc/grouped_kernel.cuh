@@ -515,10 +515,12 @@ __device__ __forceinline__ int next_adapters(const uint32_t (&ids)[kPer], int& l
 }
 
 // x as a sum of bf16 terms, `step` apart; what is infinite or NaN in the first
-// is in the first alone.
+// is in the first alone.  (Finite values that would round to infinity take the
+// largest finite term first.)
 __device__ __forceinline__ void split_bf16(float x, uint16_t* h, int step, int terms) {
   for (int t = 0; t < terms; ++t) {
-    const uint32_t w = pack_bf16x2(x, x) & 0xFFFFu;
+    uint32_t w = pack_bf16x2(x, x) & 0xFFFFu;
+    if ((w & 0x7FFFu) == 0x7F80u && fabsf(x) < __uint_as_float(0x7F800000u)) --w;
     h[t * step] = static_cast<uint16_t>(w);
     const float rest = x - __uint_as_float(w << 16);
     x = fabsf(rest) < __uint_as_float(0x7F800000u) ? rest : 0.0f;
