@@ -46,8 +46,8 @@
 // infinite or NaN weights: times a later term of H, which is zero or of either
 // sign, they would turn an infinite sum into NaN, so the fixing warps take them
 // out for the terms after the first.  (Whether it does they find out in memory
-// while the tile's K stages run: 8000 rows, rank 64, x 8192 x 4096 431 us, with
-// no look at the weights 421, with every such stage gone over in shared memory
+// while the tile's K stages run: 8000 rows, rank 64, x 8192 x 4096 423 us, with
+// no look at the weights 420, with every such stage gone over in shared memory
 // 455.)
 // In other tiles the fixing warps put zeros over H's rows of other adapters.  A
 // zero row times an infinite or NaN weight would still be NaN, so there they
@@ -518,12 +518,14 @@ __device__ __forceinline__ int next_adapters(const uint32_t (&ids)[kPer], int& l
 // is in the first alone.  (Finite values that would round to infinity take the
 // largest finite term first.)
 __device__ __forceinline__ void split_bf16(float x, uint16_t* h, int step, int terms) {
-  for (int t = 0; t < terms; ++t) {
-    uint32_t w = pack_bf16x2(x, x) & 0xFFFFu;
-    if ((w & 0x7FFFu) == 0x7F80u && fabsf(x) < __uint_as_float(0x7F800000u)) --w;
-    h[t * step] = static_cast<uint16_t>(w);
+  uint32_t w = pack_bf16x2(x, x) & 0xFFFFu;
+  if ((w & 0x7FFFu) == 0x7F80u && fabsf(x) < __uint_as_float(0x7F800000u)) --w;
+  h[0] = static_cast<uint16_t>(w);
+  for (int t = 1; t < terms; ++t) {
     const float rest = x - __uint_as_float(w << 16);
     x = fabsf(rest) < __uint_as_float(0x7F800000u) ? rest : 0.0f;
+    w = pack_bf16x2(x, x) & 0xFFFFu;
+    h[t * step] = static_cast<uint16_t>(w);
   }
 }
 
@@ -1275,15 +1277,12 @@ __global__ void __launch_bounds__(C::kThreads, 1)
         const int per = (p.rank + 63) / 64 * 64;
         const int end = w.piece == 0 ? 64 * adapter_stages<C::kTerms>(p.rank, mixed) : 0;
         int care = 0;
-        if (end > 0 && !mixed && next_adapter(tile_ids, -1, p.adapters) >= 0 && ok) {
-          if (lane == 0) ok = take_check(check_parity, care);
-          ok = __shfl_sync(0xFFFFFFFFu, ok, 0);
-        }
         for (int r = 0; r < end && ok; r += 64) {
           for (int id = next_adapter(tile_ids, -1, p.adapters); id >= 0 && ok;
                id = next_adapter(tile_ids, id, p.adapters)) {
             if (lane == 0) {
-              ok = wait_slot();
+              // One adapter: the check's word before the second term's first stage.
+              ok = (mixed || r != per || take_check(check_parity, care)) && wait_slot();
               if (ok) {
                 const int term = small_div(r, per), rx = r - term * per;
                 if (mixed || (care && term > 0)) {
@@ -1443,15 +1442,12 @@ __global__ void __launch_bounds__(C::kThreads, 1)
           const bool mixed = mixed_adapters(tile_ids, w.rows, lane, p.adapters);
           const int end = w.piece == 0 ? 64 * adapter_stages<C::kTerms>(p.rank, mixed) : 0;
           int care = 0;
-          if (end > 0 && !mixed && next_adapter(tile_ids, -1, p.adapters) >= 0 && ok) {
-            if (lane == 0) ok = take_check(check_parity, care);
-            ok = __shfl_sync(0xFFFFFFFFu, ok, 0);
-          }
           for (int r = 0; r < end && ok; r += 64) {
             for (int id = next_adapter(tile_ids, -1, p.adapters); id >= 0 && ok;
                  id = next_adapter(tile_ids, id, p.adapters)) {
               if (lane == 0) {
-                ok = (ready || mbar_try_wait(full0 + 8u * stage, phase) ||
+                ok = (mixed || r != per || take_check(check_parity, care)) &&
+                     (ready || mbar_try_wait(full0 + 8u * stage, phase) ||
                       mbar_wait(&full_bar[stage], phase, guard, kSiteGrFull)) &&
                      ((!mixed && (!care || r < per)) || wait_fix());
                 if (ok) {
@@ -1800,11 +1796,12 @@ __global__ void __launch_bounds__(C::kThreads, 1)
         int last_id = -1, group[4];
         while (next_adapters(ids, last_id, 128 / slot, p.adapters, group) > 0) {
           float v[32];
-          grouped_zero(v);
-          for (int c = 0; c < chunks && ok; ++c) {
+          if constexpr (!C::kBf16Out) grouped_zero(v);
+          for (int c = 0; c < chunks && ok; ++c) {   // (bf16 D: one)
             ok = acc_ready();
             if (!ok) break;
-            grouped_read<true>(t_slab + static_cast<uint32_t>(acc * C::kTileN + 32 * half), v);
+            grouped_read<!C::kBf16Out>(
+                t_slab + static_cast<uint32_t>(acc * C::kTileN + 32 * half), v);
             hand_back();
           }
           if (!ok) break;
