@@ -26,10 +26,10 @@
 // adapters of rank 16, K = 8192: 11 us from a cold cache for 14 MB.
 //
 // The whole call in a replayed graph: 4 rows over 32 adapters of rank 16 x 4096
-// x 4096 14 us (floor 5: two kernels, each a launch, a trip to memory and a
-// join), 64 rows x 8192 x 8192 39 us (floor 24, the weights), 8000 rows of 16
-// requests, rank 64, x 8192 x 4096 420 us (floor 295, the tensor pipe: 1300
-// TFLOP/s).
+// x 4096 16 us (floor 5: two kernels, each a launch, a trip to memory and a
+// join), 64 rows x 8192 x 8192 40 us (floor 24, the weights: 128 of 152 SMs read
+// them), 8000 rows of 16 requests, rank 64, x 8192 x 4096 423 us (floor 295, the
+// tensor pipe: 1300 TFLOP/s).
 #include <algorithm>
 
 #include "grouped_launch.cuh"

@@ -70,8 +70,10 @@
 // groups of 2048 rows 310 us forward and dgrad, 319 wgrad (1770, 1770 and 1720
 // TFLOP/s: the tensor pipe); 64 groups of 512 rows 342, 344 and 417 us: a tile
 // takes in 64 KB and the weights' 1 GB of HBM traffic shares the time with the
-// MMAs; f32 D 384 and 613 (wgrad) us: the stores, through the same port of an
-// SM as the loads.  64 groups of 32 rows 174 us: 1.07 GB at 6.2 TB/s.
+// MMAs; f32 D 384 and 613 (wgrad) us: stores and loads take turns (32 groups of
+// 1024 rows: tensor pipe 43%, DRAM 33%, L2 34%).  64 groups of 32 rows 174 us:
+// 1.07 GB at 6.2 TB/s.  The walk over the offsets at the start: 512 rows in one of
+// 64 groups of 128 x 128 6.6 us, of 1024 25, of 4096 87.
 #pragma once
 
 #include <cstdint>
