@@ -16,6 +16,12 @@ Entry points (same names as the C ABI):
   ``_dgrad`` and ``_wgrad`` its gradients
 * ``gemm_bf16_lora(A, B, ids, down, up, ...)``    -- shared weights and a low-rank
   adapter per row
+* ``gemm_bf16_xent(A, B, targets, ...)``          -- softmax cross entropy over a
+  vocabulary; with ``_grad`` its gradients
+* ``embed_rows(W, ids, ...)``                     -- rows of a table by token id; with
+  ``_grad`` the table's gradient
+* ``balance_loss(logits, ids)``                   -- balance loss and counts of a
+  router; with ``_grad`` its gradient
 * ``tg_device_status(stream=None)``               -- device-side error record
 """
 from __future__ import annotations
@@ -55,6 +61,10 @@ TG_CALL_GEMM_BF16_SKINNY = 4
 TG_CALL_GEMM_BF16_GATHER = 5
 TG_CALL_GROUP_ROWS = 6
 TG_CALL_GEMM_BF16_LORA = 7
+TG_CALL_GEMM_BF16_XENT = 8
+TG_CALL_GEMM_BF16_XENT_GRAD = 9
+TG_CALL_EMBED_ROWS_GRAD = 10
+TG_CALL_BALANCE_LOSS = 11
 TG_MAX_GROUPS = 4096
 TG_MAX_RANK = 256
 TG_CLOCK_BF16 = 0
@@ -137,6 +147,20 @@ def lib() -> ctypes.CDLL:
         L.gemm_bf16_lora.argtypes = [vp, i64, vp, i64, vp, vp, i64, i64, vp, i64, i64, vp, i64, i64,
                                      vp, i64, i64, i64, i64, i32, ctypes.POINTER(tg_epilogue), u32,
                                      vp]
+        f32 = ctypes.c_float
+        L.gemm_bf16_xent.restype = i32
+        L.gemm_bf16_xent.argtypes = [vp, i64, vp, i64, vp, f32, vp, vp, i64, i64, i64, u32, vp]
+        L.gemm_bf16_xent_grad.restype = i32
+        L.gemm_bf16_xent_grad.argtypes = [vp, i64, vp, i64, vp, vp, vp, f32, vp, i64, vp, i64, i64,
+                                          i64, i64, i32, u32, vp]
+        L.embed_rows.restype = i32
+        L.embed_rows.argtypes = [vp, i64, i64, vp, i64, i64, f32, vp, i64, i32, vp]
+        L.embed_rows_grad.restype = i32
+        L.embed_rows_grad.argtypes = [vp, i64, i32, vp, i64, i64, i64, f32, vp, i64, i32, i32, vp]
+        L.tg_balance_loss.restype = i32
+        L.tg_balance_loss.argtypes = [vp, i64, i32, vp, i64, i64, i64, vp, vp, vp, vp]
+        L.tg_balance_loss_grad.restype = i32
+        L.tg_balance_loss_grad.argtypes = [vp, i64, i32, vp, i64, i64, i64, vp, vp, vp, i64, i32, vp]
         L.tg_gemm_tail_split.restype = i32
         L.tg_gemm_tail_split.argtypes = [i64, i64, i64, u32]
         L.tg_gemm_multicast.restype = i32
@@ -494,11 +518,21 @@ TG_FN_GEMM_BF16_GROUPED = 1
 TG_FN_GEMM_BF16_GROUPED_DGRAD = 2
 TG_FN_GEMM_BF16_GROUPED_WGRAD = 3
 TG_FN_GEMM_BF16_LORA = 4
-# Each call's arguments as 64-bit words (pointers as addresses, None as 0).
-_WORDS = [struct.Struct("=%dq" % n).pack for n in (7, 18, 15, 17, 23)]
-_COUNT = (7, 18, 15, 17, 23)
+TG_FN_GEMM_BF16_XENT = 5
+TG_FN_GEMM_BF16_XENT_GRAD = 6
+TG_FN_EMBED_ROWS = 7
+TG_FN_EMBED_ROWS_GRAD = 8
+TG_FN_BALANCE_LOSS = 9
+TG_FN_BALANCE_LOSS_GRAD = 10
+# Each call's arguments as 64-bit words (pointers as addresses, None as 0; "f4x":
+# a float and the word's other half).
+_WORDS = [struct.Struct(f).pack for f in
+          ("=7q", "=18q", "=15q", "=17q", "=23q", "=5qf4x7q", "=7qf4x10q", "=6qf4x4q", "=7qf4x5q",
+           "=11q", "=13q")]
+_COUNT = (7, 18, 15, 17, 23, 13, 18, 11, 13, 11, 13)
 _NAMES = ("tg_group_rows", "gemm_bf16_grouped", "gemm_bf16_grouped_dgrad",
-          "gemm_bf16_grouped_wgrad", "gemm_bf16_lora")
+          "gemm_bf16_grouped_wgrad", "gemm_bf16_lora", "gemm_bf16_xent", "gemm_bf16_xent_grad",
+          "embed_rows", "embed_rows_grad", "tg_balance_loss", "tg_balance_loss_grad")
 
 
 def _call(fn, *words):
@@ -652,6 +686,185 @@ def gemm_bf16_lora(A, B, ids, down, up, D=None, *, scales=None, out_dtype=None, 
     _call(TG_FN_GEMM_BF16_LORA, a, lda, b, ldb, idp, pd, ld_down, step_down, pu, ld_up, step_up, ps,
           adapters, rank, D.data_ptr(), ldd, M, N, K, code, ctypes.addressof(epi) if epi else 0, 0,
           _raw_stream(stream))
+    return D
+
+
+def _f32_vector(t, name, length):
+    """Address of a contiguous float32 vector; 0 for None."""
+    if t is None:
+        return 0
+    if t.dtype is not _torch().float32 or t.shape != (length,) or not t.is_contiguous():
+        raise TypeError(f"{name} must be a contiguous float32 vector of {length} elements")
+    return t.data_ptr()
+
+
+def gemm_bf16_xent(A, B, targets, *, scale=1.0, stream=None):
+    """(loss, lse) of softmax cross entropy over z = scale * A @ B.T, which is never stored.
+
+    A: bfloat16 [M, K]; B: bfloat16 [N, K], the vocabulary; targets: int32 CUDA
+    vector [M].  lse[i] = log(sum_j exp(z[i, j])) and loss[i] = lse[i] -
+    z[i, targets[i]], or 0 where the target is outside [0, N).  Both float32 [M].
+    ``scale`` is positive.
+    """
+    torch = _torch()
+    M, K, lda, a = _matrix(A, "A", torch.bfloat16)
+    N, K2, ldb, b = _matrix(B, "B", torch.bfloat16)
+    if K != K2:
+        raise ValueError("A is [M, K] and B is [N, K]")
+    _, t = _int32_vector(targets, "targets", M)
+    _on_device(A, B, targets)
+    loss = torch.empty(M, dtype=torch.float32, device=A.device)
+    lse = torch.empty_like(loss)
+    _call(TG_FN_GEMM_BF16_XENT, a, lda, b, ldb, t, scale, loss.data_ptr(), lse.data_ptr(), M, N, K,
+          0, _raw_stream(stream))
+    return loss, lse
+
+
+def gemm_bf16_xent_grad(A, B, targets, lse, grad=None, dA=None, dB=None, *, scale=1.0,
+                        out_dtype=None, rows=True, weights=True, stream=None):
+    """(dA, dB): the gradients of sum(grad * loss) of ``gemm_bf16_xent``.
+
+    lse: its second result for the same A, B and scale; grad: float32 [M], or
+    None for 1.  Rows without a target get a zero row of dA and have no part in
+    dB.  ``rows=False`` or ``weights=False`` leaves out dA or dB (None then).
+    dA: [M, K], dB: [N, K], both of one type, bfloat16 or float32 (default
+    bfloat16); where none is given it is allocated with rows that start on
+    16-byte boundaries, as for ``gemm_bf16_grouped``.
+    """
+    torch = _torch()
+    M, K, lda, a = _matrix(A, "A", torch.bfloat16)
+    N, K2, ldb, b = _matrix(B, "B", torch.bfloat16)
+    if K != K2:
+        raise ValueError("A is [M, K] and B is [N, K]")
+    _, t = _int32_vector(targets, "targets", M)
+    if lse is None:
+        raise TypeError("lse is the second result of gemm_bf16_xent")
+    pl, pg = _f32_vector(lse, "lse", M), _f32_vector(grad, "grad", M)
+    for D in (dA, dB):
+        if out_dtype is None and D is not None:
+            out_dtype = D.dtype
+    out_dtype = out_dtype or torch.bfloat16
+    code, pa, ldda, pb, lddb = _d_code(out_dtype), 0, 0, 0, 0
+    if rows:
+        dA, own, ldda = _result(dA, (M, K), out_dtype, A.device)
+        pa = dA.data_ptr()
+        if own != code:
+            raise ValueError("dA and dB must have one type")
+    elif dA is not None:
+        raise ValueError("dA is given, but rows=False")
+    if weights:
+        dB, own, lddb = _result(dB, (N, K), out_dtype, A.device)
+        pb = dB.data_ptr()
+        if own != code:
+            raise ValueError("dA and dB must have one type")
+    elif dB is not None:
+        raise ValueError("dB is given, but weights=False")
+    _on_device(A, B, targets, lse, grad, dA, dB)
+    _call(TG_FN_GEMM_BF16_XENT_GRAD, a, lda, b, ldb, t, pl, pg, scale, pa, ldda, pb, lddb, M, N, K,
+          code, 0, _raw_stream(stream))
+    return dA, dB
+
+
+def embed_rows(W, ids, D=None, *, scale=1.0, out_dtype=None, stream=None):
+    """D[i] = scale * W[ids[i]], zeros where the id is outside [0, rows of W).
+
+    W: bfloat16 [rows, K]; ids: int32 CUDA vector [n].  D: float32 or bfloat16
+    [n, K] (default bfloat16), allocated as for ``gemm_bf16_grouped``.
+    """
+    torch = _torch()
+    rows, K, ldw, w = _matrix(W, "W", torch.bfloat16)
+    n, ip = _int32_vector(ids, "ids")
+    D, code, ldd = _result(D, (n, K), out_dtype or torch.bfloat16, W.device)
+    _on_device(W, ids, D)
+    _call(TG_FN_EMBED_ROWS, w, ldw, rows, ip, n, K, scale, D.data_ptr(), ldd, code,
+          _raw_stream(stream))
+    return D
+
+
+def embed_rows_grad(G, ids, rows, D=None, *, scale=1.0, out_dtype=None, accumulate=False,
+                    stream=None):
+    """D[v] = scale * sum of G[i] over ids[i] == v: the gradient of ``embed_rows``' table.
+
+    G: float32 or bfloat16 [n, K]; ids: int32 CUDA vector [n]; ids outside
+    [0, rows) have no part.  D: float32 or bfloat16 [rows, K] (default G's
+    type); rows without tokens are zero.  With ``accumulate`` the sums are
+    added to the given D instead, whose other rows stay as they are: a table
+    that is also the vocabulary of ``gemm_bf16_xent`` gets its gradient whole
+    that way.
+    """
+    torch = _torch()
+    if G.dtype is not torch.float32 and G.dtype is not torch.bfloat16:
+        raise TypeError("G must be float32 or bfloat16")
+    n, K, ldg, g = _matrix(G, "G", G.dtype)
+    _, ip = _int32_vector(ids, "ids", n)
+    if accumulate and D is None:
+        raise ValueError("accumulate adds to a given D")
+    if rows < 0:
+        raise ValueError("rows must not be negative")
+    D, code, ldd = _result(D, (int(rows), K), out_dtype or G.dtype, G.device)
+    _on_device(G, ids, D)
+    _call(TG_FN_EMBED_ROWS_GRAD, g, ldg, _d_code(G.dtype), ip, n, int(rows), K, scale, D.data_ptr(),
+          ldd, code, 1 if accumulate else 0, _raw_stream(stream))
+    return D
+
+
+def _router(logits, ids):
+    """(M, E, row stride, address, type's code, choices, address of ids)."""
+    torch = _torch()
+    if logits.dtype is not torch.float32 and logits.dtype is not torch.bfloat16:
+        raise TypeError("logits must be float32 or bfloat16")
+    M, E, ld, z = _matrix(logits, "logits", logits.dtype)
+    if ids.dtype is not torch.int32 or len(ids.shape) != 2 or not ids.is_contiguous():
+        raise TypeError("ids must be a contiguous int32 matrix")
+    if ids.shape[0] != M:
+        raise ValueError("logits are [tokens, experts] and ids [tokens, choices]")
+    return M, E, max(ld, E), z, _d_code(logits.dtype), ids.shape[1], ids.data_ptr()
+
+
+def balance_loss(logits, ids, *, stream=None):
+    """(loss, counts, shares): how unevenly a router spreads its tokens over its experts.
+
+    logits: float32 or bfloat16 [tokens, E]; ids: int32 [tokens, choices], the
+    experts of each token (as ``group_rows`` takes them, flattened); a token
+    whose ids are all outside [0, E) is padding and has no part.  With p =
+    softmax(logits): counts[e] (int32 [E]) is how often e was chosen, shares[e]
+    = E * counts[e] / (counts.sum() * tokens) (float32 [E]) and loss =
+    (shares * p.sum(0)).sum() (float32, 0-d): 1 where everything is even.
+    """
+    torch = _torch()
+    M, E, ld, z, code, choices, ip = _router(logits, ids)
+    _on_device(logits, ids)
+    loss = torch.empty((), dtype=torch.float32, device=logits.device)
+    counts = torch.empty(E, dtype=torch.int32, device=logits.device)
+    shares = torch.empty(E, dtype=torch.float32, device=logits.device)
+    _call(TG_FN_BALANCE_LOSS, z, ld, code, ip, choices, M, E, loss.data_ptr(), counts.data_ptr(),
+          shares.data_ptr(), _raw_stream(stream))
+    return loss, counts, shares
+
+
+def balance_loss_grad(logits, ids, shares, grad=None, D=None, *, out_dtype=None, stream=None):
+    """D = grad * p * (shares - (p * shares).sum(1)): the gradient of ``balance_loss``' logits.
+
+    shares: its third result; grad: float32 tensor of one element on the device,
+    or None for 1.  D: float32 or bfloat16 [tokens, E] (default the logits'
+    type); rows of padding are zero.
+    """
+    torch = _torch()
+    M, E, ld, z, code, choices, ip = _router(logits, ids)
+    ps = _f32_vector(shares, "shares", E)
+    pg = 0
+    if grad is not None:
+        if grad.dtype is not torch.float32 or grad.numel() != 1:
+            raise TypeError("grad must be a float32 tensor of one element")
+        pg = grad.data_ptr()
+    if D is None:
+        D = torch.empty((M, E), dtype=out_dtype or logits.dtype, device=logits.device)
+    elif D.shape != (M, E):
+        raise ValueError(f"D must be {[M, E]}")
+    _, _, ldd, d = _matrix(D, "D", D.dtype)
+    _on_device(logits, ids, shares, grad, D)
+    _call(TG_FN_BALANCE_LOSS_GRAD, z, ld, code, ip, choices, M, E, ps, pg, d, max(ldd, E),
+          _d_code(D.dtype), _raw_stream(stream))
     return D
 
 

@@ -681,6 +681,15 @@ int64_t tg_workspace_bytes(int call, int64_t M, int64_t N, int64_t K, int64_t ld
       return static_cast<int64_t>(group_rows_workspace_bytes(M, N));
     case TG_CALL_GEMM_BF16_LORA:
       return static_cast<int64_t>(lora_workspace_bytes(M, N));
+    case TG_CALL_GEMM_BF16_XENT:
+      return static_cast<int64_t>(xent_workspace_bytes(M, N));
+    case TG_CALL_GEMM_BF16_XENT_GRAD:
+      if (d_dtype != TG_D_F32 && d_dtype != TG_D_BF16) return -TG_ERR_INVALID_ARG;
+      return static_cast<int64_t>(xent_grad_workspace_bytes(M, N, K, d_dtype));
+    case TG_CALL_EMBED_ROWS_GRAD:
+      return static_cast<int64_t>(embed_grad_workspace_bytes(M, N, K));
+    case TG_CALL_BALANCE_LOSS:
+      return static_cast<int64_t>(balance_workspace_bytes(M, N));
     default:
       return -TG_ERR_INVALID_ARG;
   }
@@ -825,6 +834,10 @@ template <class T>
 bool unpack(int64_t word, T* out) {
   if constexpr (std::is_pointer_v<T>) {
     *out = reinterpret_cast<T>(static_cast<uintptr_t>(word));
+  } else if constexpr (std::is_same_v<T, float>) {
+    if (word < 0 || word > 0xFFFFFFFFll) return false;
+    const uint32_t bits = static_cast<uint32_t>(word);
+    std::memcpy(out, &bits, sizeof(bits));
   } else {
     *out = static_cast<T>(word);
     if (static_cast<int64_t>(*out) != word) return false;
@@ -855,6 +868,12 @@ extern "C" int tg_call_packed(int fn, const int64_t* args, int count) {
     case TG_FN_GEMM_BF16_GROUPED_DGRAD: return call_packed(gemm_bf16_grouped_dgrad, args, count);
     case TG_FN_GEMM_BF16_GROUPED_WGRAD: return call_packed(gemm_bf16_grouped_wgrad, args, count);
     case TG_FN_GEMM_BF16_LORA: return call_packed(gemm_bf16_lora, args, count);
+    case TG_FN_GEMM_BF16_XENT: return call_packed(gemm_bf16_xent, args, count);
+    case TG_FN_GEMM_BF16_XENT_GRAD: return call_packed(gemm_bf16_xent_grad, args, count);
+    case TG_FN_EMBED_ROWS: return call_packed(embed_rows, args, count);
+    case TG_FN_EMBED_ROWS_GRAD: return call_packed(embed_rows_grad, args, count);
+    case TG_FN_BALANCE_LOSS: return call_packed(tg_balance_loss, args, count);
+    case TG_FN_BALANCE_LOSS_GRAD: return call_packed(tg_balance_loss_grad, args, count);
     default: return TG_ERR_INVALID_ARG;
   }
 }

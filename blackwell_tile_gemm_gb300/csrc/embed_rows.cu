@@ -1,0 +1,474 @@
+// Rows of a table by token id, and the table's gradient.
+//
+//   embed_rows       D[i] = scale * W[ids[i]]
+//   embed_rows_grad  dW[v] (+)= scale * sum over {i : ids[i] = v} of G[i]
+//
+// Both are bound by HBM: every row is moved once.  The lookup gives each warp a
+// part of a row.  The gradient must not depend on the order in which anything
+// runs, so the rows are first sorted by id (stable; group_rows.cu, digit by
+// digit), and a run of equal ids is summed in the order of its rows, in f32.
+// Runs are as uneven as words are: the sorted rows are cut into chunks of equal
+// length, a block each; a run that lies inside its chunk goes straight to dW,
+// what crosses a chunk's end goes to the workspace as an f32 partial sum, and a
+// second kernel adds a run's partial sums in their order.  The rows of dW that no
+// token has (nearly all of a large table's) are written as zeros by further
+// blocks of the first kernel, meanwhile.
+#include <atomic>
+
+#include "tg_internal.h"
+#include "tg_ptx.cuh"
+
+using namespace tg;
+
+namespace tg {
+namespace {
+
+constexpr int64_t kMaxDim = (int64_t{1} << 31) - 1;
+constexpr int64_t kMaxTokens = int64_t{1} << 30;   // as tg_group_rows
+
+template <class K, class... T>
+int launch_chained(K kern, int64_t blocks, int threads, cudaStream_t stream, T... args) {
+  cudaLaunchConfig_t cfg{};
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.gridDim = dim3(static_cast<unsigned>(blocks), 1, 1);
+  cfg.blockDim = dim3(static_cast<unsigned>(threads), 1, 1);
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, args...);
+  return e == cudaSuccess ? TG_OK : cuda_fail(e);
+}
+
+// Eight values of a row, from column k on; what lies past column K is neither
+// read nor written.
+template <class T>
+__device__ __forceinline__ void load8(const T* row, int k, int K, float (&v)[8]) {
+  if constexpr (sizeof(T) == 2) {
+    uint4 q = make_uint4(0u, 0u, 0u, 0u);
+    if (k + 8 <= K) {
+      q = __ldcs(reinterpret_cast<const uint4*>(row + k));
+    } else {
+      uint32_t w[4] = {0u, 0u, 0u, 0u};
+      for (int e = 0; k + e < K; ++e) w[e / 2] |= static_cast<uint32_t>(row[k + e]) << (16 * (e & 1));
+      q = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      v[e] = __uint_as_float(e & 1 ? w[e / 2] & 0xFFFF0000u : w[e / 2] << 16);
+  } else {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      float4 q = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      if (k + 4 * h + 4 <= K) {
+        q = __ldcs(reinterpret_cast<const float4*>(row + k + 4 * h));
+      } else {
+        float t[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (k + 4 * h + e < K) t[e] = row[k + 4 * h + e];
+        q = make_float4(t[0], t[1], t[2], t[3]);
+      }
+      v[4 * h] = q.x;
+      v[4 * h + 1] = q.y;
+      v[4 * h + 2] = q.z;
+      v[4 * h + 3] = q.w;
+    }
+  }
+}
+
+template <class T>
+__device__ __forceinline__ void store8(T* row, int k, int K, const float (&v)[8]) {
+  if constexpr (sizeof(T) == 2) {
+    uint32_t w[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) w[e] = pack_bf16x2(v[2 * e], v[2 * e + 1]);
+    if (k + 8 <= K)
+      __stcs(reinterpret_cast<uint4*>(row + k), make_uint4(w[0], w[1], w[2], w[3]));
+    else
+      for (int e = 0; k + e < K; ++e) row[k + e] = static_cast<T>(w[e / 2] >> (16 * (e & 1)));
+  } else {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      if (k + 4 * h + 4 <= K)
+        __stcs(reinterpret_cast<float4*>(row + k + 4 * h),
+               make_float4(v[4 * h], v[4 * h + 1], v[4 * h + 2], v[4 * h + 3]));
+      else
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (k + 4 * h + e < K) row[k + 4 * h + e] = v[4 * h + e];
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Lookup
+// ---------------------------------------------------------------------------
+
+// A warp's item: up to kLookup * 256 columns of one row, all loads in flight.
+constexpr int kLookup = 4;
+
+template <class TD>
+__global__ void __launch_bounds__(256) embed_kernel(const uint16_t* W, int64_t ldw, int vocab,
+                                                    const int* ids, int64_t n, int K, int parts,
+                                                    float scale, TD* D, int64_t ldd) {
+  griddep_wait();
+  griddep_launch_dependents();
+  const int lane = static_cast<int>(threadIdx.x & 31);
+  const int64_t items = n * parts;
+  for (int64_t i = blockIdx.x * 8LL + (threadIdx.x >> 5); i < items; i += gridDim.x * 8LL) {
+    const int64_t row = i / parts;
+    const int k0 = static_cast<int>(i - row * parts) * (256 * kLookup) + 8 * lane;
+    const int id = ids[row];
+    const bool in = static_cast<unsigned>(id) < static_cast<unsigned>(vocab);
+    float v[kLookup][8];
+#pragma unroll
+    for (int u = 0; u < kLookup; ++u) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[u][e] = 0.0f;
+      if (in && k0 + 256 * u < K) load8(W + id * ldw, k0 + 256 * u, K, v[u]);
+    }
+#pragma unroll
+    for (int u = 0; u < kLookup; ++u) {
+      if (k0 + 256 * u >= K) continue;
+      if (in) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[u][e] *= scale;
+      }
+      store8(D + row * ldd, k0 + 256 * u, K, v[u]);
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Gradient
+// ---------------------------------------------------------------------------
+
+struct EmbedGradArgs {
+  const void* G;
+  int64_t ldg;
+  int n, vocab, K;
+  const int* order;       // rows by id
+  const int* sorted;      // their ids, -1 for rows of none (last)
+  const unsigned* marks;  // a bit for each id that occurs; null: D is added to
+  float scale;
+  void* D;
+  int64_t ldd;
+  float* parts;           // [chunk][2][ldp]: sums of a chunk's first and last run
+  int64_t ldp;
+  int chunk;              // sorted rows per block
+  int chunks, slices;     // blocks of sums: chunks x slices of kSlice columns
+};
+
+constexpr int kSlice = 1024;      // columns of a block: 128 threads x 8
+constexpr int kBatch = 8;         // rows loaded together
+
+// The finished sum of an id's rows.
+template <class TD, bool kAdd>
+__device__ __forceinline__ void finish_run(const EmbedGradArgs& p, int id, int k, float (&v)[8]) {
+  TD* d = static_cast<TD*>(p.D) + id * p.ldd;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) v[e] *= p.scale;
+  if constexpr (kAdd) {
+    float old[8];
+    load8(d, k, p.K, old);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] += old[e];
+  }
+  store8(d, k, p.K, v);
+}
+
+template <class TG, class TD, bool kAdd>
+__global__ void __launch_bounds__(128) sum_runs_kernel(const EmbedGradArgs p) {
+  griddep_wait();
+  griddep_launch_dependents();
+  const int64_t sums = static_cast<int64_t>(p.chunks) * p.slices;
+  if (static_cast<int64_t>(blockIdx.x) >= sums) {
+    // Rows that no token has, a warp each.
+    const int lane = static_cast<int>(threadIdx.x & 31);
+    const int64_t warps = (gridDim.x - sums) * 4;
+    const float zero[8] = {};
+    for (int64_t v = (blockIdx.x - sums) * 4 + (threadIdx.x >> 5); v < p.vocab; v += warps) {
+      if (p.n > 0 && (__ldcg(p.marks + (v >> 5)) >> (v & 31)) & 1u) continue;
+      TD* d = static_cast<TD*>(p.D) + v * p.ldd;
+      for (int k = 8 * lane; k < p.K; k += 256) store8(d, k, p.K, zero);
+    }
+    return;
+  }
+  const int c = static_cast<int>(blockIdx.x) / p.slices;
+  const int k = (static_cast<int>(blockIdx.x) - c * p.slices) * kSlice +
+                8 * static_cast<int>(threadIdx.x);
+  if (k >= p.K) return;
+  const int lo = c * p.chunk;
+  const int hi = p.n - lo > p.chunk ? lo + p.chunk : p.n;
+  const TG* G = static_cast<const TG*>(p.G);
+  int id = p.sorted[lo];
+  if (id < 0) return;
+  // The first run may have begun in an earlier chunk: then its sum is a part.
+  bool whole = lo == 0 || p.sorted[lo - 1] != id;
+  float sum[8] = {};
+  for (int j0 = lo; j0 < hi; j0 += kBatch) {
+    int row[kBatch], of[kBatch];
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) {
+      of[u] = j0 + u < hi ? p.sorted[j0 + u] : -1;
+      row[u] = of[u] >= 0 ? p.order[j0 + u] : 0;
+    }
+    float v[kBatch][8];
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u)
+      if (of[u] >= 0) load8(G + row[u] * p.ldg, k, p.K, v[u]);
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) {
+      if (j0 + u >= hi) break;
+      if (of[u] != id) {
+        if (whole)
+          finish_run<TD, kAdd>(p, id, k, sum);
+        else
+          store8(p.parts + 2LL * c * p.ldp, k, p.K, sum);
+        id = of[u];
+        if (id < 0) return;   // the rest has no id
+        whole = true;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) sum[e] = 0.0f;
+      }
+#pragma unroll
+      for (int e = 0; e < 8; ++e) sum[e] += v[u][e];
+    }
+  }
+  const bool goes_on = hi < p.n && p.sorted[hi] == id;
+  if (whole && !goes_on)
+    finish_run<TD, kAdd>(p, id, k, sum);
+  else
+    store8(p.parts + (2LL * c + (whole ? 1 : 0)) * p.ldp, k, p.K, sum);
+}
+
+// Runs that cross the end of the chunk they begin in: the last part of that
+// chunk and the first of each further one, eight warps in turn, then the warps'
+// sums in order.
+template <class TD, bool kAdd>
+__global__ void __launch_bounds__(256) join_runs_kernel(const EmbedGradArgs p) {
+  __shared__ float shared[8][32][8];
+  griddep_wait();
+  griddep_launch_dependents();
+  const int c = static_cast<int>(blockIdx.x);
+  const int64_t lo = static_cast<int64_t>(c) * p.chunk;
+  const int64_t end = lo + p.chunk;   // (there is a chunk behind this one)
+  const int id = p.sorted[end - 1];
+  if (id < 0 || p.sorted[end] != id) return;
+  if (p.sorted[lo] == id && c > 0 && p.sorted[lo - 1] == id) return;   // begun before
+  const int lane = static_cast<int>(threadIdx.x & 31), warp = static_cast<int>(threadIdx.x >> 5);
+  // The chunk in which the run ends.
+  int last = c + 1;
+  for (;; last += 32) {
+    const int64_t behind = static_cast<int64_t>(last + lane + 1) * p.chunk;
+    const unsigned over =
+        __ballot_sync(0xFFFFFFFFu, behind >= p.n || p.sorted[behind < p.n ? behind : 0] != id);
+    if (over) {
+      last += __ffs(over) - 1;
+      break;
+    }
+  }
+  const int count = last - c + 1;
+  const int k = static_cast<int>(blockIdx.y) * 256 + 8 * lane;
+  float sum[8] = {};
+  if (k < p.K) {
+    const int64_t step = 2 * p.ldp;
+    for (int q = warp; q < count; q += 8) {
+      float v[8];
+      load8(p.parts + (c + q) * step + (q == 0 ? p.ldp : 0), k, p.K, v);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) sum[e] += v[e];
+    }
+  }
+#pragma unroll
+  for (int e = 0; e < 8; ++e) shared[warp][lane][e] = sum[e];
+  __syncthreads();
+  if (warp != 0 || k >= p.K) return;
+  for (int w = 1; w < 8 && w < count; ++w)
+#pragma unroll
+    for (int e = 0; e < 8; ++e) sum[e] += shared[w][lane][e];
+  finish_run<TD, kAdd>(p, id, k, sum);
+}
+
+// Sorted rows per block: about a thousand chunks, so that a run as long as all of
+// them still joins in little time, and no block has few rows for its launch.
+int grad_chunk(int64_t n) {
+  int64_t c = kBatch;
+  while (c * 1024 < n) c *= 2;
+  return static_cast<int>(c);
+}
+
+struct EmbedPlan {
+  int chunk, chunks;
+  int64_t ldp;
+  size_t other, sorted, count, marks, hist, parts, bytes;
+};
+EmbedPlan embed_plan(int64_t n, int64_t rows, int64_t K) {
+  EmbedPlan q{};
+  q.chunk = grad_chunk(n);
+  q.chunks = static_cast<int>((n + q.chunk - 1) / q.chunk);
+  q.ldp = (K + 7) / 8 * 8;
+  size_t at = 0;
+  auto take = [&](size_t bytes) {
+    const size_t was = at;
+    at += (bytes + 255) / 256 * 256;
+    return was;
+  };
+  const size_t list = static_cast<size_t>(4 * n);
+  take(list);
+  q.other = take(list);
+  q.sorted = take(list);
+  q.count = take(4 * ((size_t{1} << kSortDigit) + 1));
+  q.marks = take(static_cast<size_t>((rows + 31) / 32 * 4));
+  q.hist = take(sort_ids_workspace_bytes(n));
+  q.parts = take(q.chunks > 1 ? static_cast<size_t>(8 * q.chunks) * static_cast<size_t>(q.ldp) : 0);
+  q.bytes = at;
+  return q;
+}
+
+template <class TG, class TD, bool kAdd>
+int launch_grad(const EmbedGradArgs& a, DeviceCtx* ctx, cudaStream_t stream) {
+  int64_t zero_blocks = 0;
+  if (!kAdd) {
+    zero_blocks = (a.vocab + 3) / 4;
+    const int64_t most = 16 * static_cast<int64_t>(ctx->num_sms);
+    if (zero_blocks > most) zero_blocks = most;
+  }
+  const int64_t blocks = static_cast<int64_t>(a.chunks) * a.slices + zero_blocks;
+  if (blocks == 0) return TG_OK;
+  int rc = launch_chained(sum_runs_kernel<TG, TD, kAdd>, blocks, 128, stream, a);
+  if (rc != TG_OK || a.chunks < 2) return rc;
+  cudaLaunchConfig_t cfg{};
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.gridDim = dim3(static_cast<unsigned>(a.chunks - 1), static_cast<unsigned>((a.K + 255) / 256));
+  cfg.blockDim = dim3(256);
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, join_runs_kernel<TD, kAdd>, a);
+  return e == cudaSuccess ? TG_OK : cuda_fail(e);
+}
+
+template <class TG, class TD>
+int launch_grad(const EmbedGradArgs& a, bool add, DeviceCtx* ctx, cudaStream_t stream) {
+  return add ? launch_grad<TG, TD, true>(a, ctx, stream) : launch_grad<TG, TD, false>(a, ctx, stream);
+}
+
+int check_rows(const void* p, int64_t ld, int64_t width, int esize) {
+  if (p == nullptr || ld < width) return TG_ERR_INVALID_ARG;
+  if ((reinterpret_cast<uintptr_t>(p) & 15u) != 0 || (ld * esize) % 16 != 0)
+    return TG_ERR_MISALIGNED;
+  return TG_OK;
+}
+
+int check_embed(int64_t n, int64_t rows, int64_t K, int a_dtype, int d_dtype) {
+  if (n < 0 || n > kMaxTokens || rows < 0 || rows > kMaxDim || K < 0 || K > kMaxDim)
+    return TG_ERR_INVALID_ARG;
+  if (a_dtype != TG_D_F32 && a_dtype != TG_D_BF16) return TG_ERR_INVALID_ARG;
+  if (d_dtype != TG_D_F32 && d_dtype != TG_D_BF16) return TG_ERR_INVALID_ARG;
+  // Blocks of a launch: slices of columns in its second dimension.
+  if (K > int64_t{256} * 65535) return TG_ERR_UNSUPPORTED;
+  return TG_OK;
+}
+
+int esize(int dtype) { return dtype == TG_D_BF16 ? 2 : 4; }
+
+}  // namespace
+
+size_t embed_grad_workspace_bytes(int64_t n, int64_t rows, int64_t K) {
+  return embed_plan(n, rows, K).bytes;
+}
+
+}  // namespace tg
+
+extern "C" {
+
+int embed_rows(const void* W, int64_t ldw, int64_t rows, const int32_t* ids, int64_t n, int64_t K,
+               float scale, void* D, int64_t ldd, int d_dtype, void* cuda_stream) {
+  int rc = check_embed(n, rows, K, TG_D_BF16, d_dtype);
+  if (rc != TG_OK || n == 0 || K == 0) return rc;
+  if (ids == nullptr) return TG_ERR_INVALID_ARG;
+  rc = check_rows(D, ldd, K, esize(d_dtype));
+  if (rc == TG_OK && rows > 0) rc = check_rows(W, ldw, K, 2);
+  if (rc != TG_OK) return rc;
+  DeviceCtx* ctx = current_ctx();
+  if (!ctx) return TG_ERR_CUDA;
+  cudaStream_t stream = static_cast<cudaStream_t>(cuda_stream);
+  const int parts = static_cast<int>((K + 256 * kLookup - 1) / (256 * kLookup));
+  int64_t blocks = (n * parts + 7) / 8;
+  const int64_t most = 8 * static_cast<int64_t>(ctx->num_sms);
+  if (blocks > most) blocks = most;
+  const uint16_t* w = static_cast<const uint16_t*>(W);
+  const int v = static_cast<int>(rows), k = static_cast<int>(K);
+  if (d_dtype == TG_D_BF16)
+    return launch_chained(embed_kernel<uint16_t>, blocks, 256, stream, w, ldw, v, ids, n, k, parts,
+                          scale, static_cast<uint16_t*>(D), ldd);
+  return launch_chained(embed_kernel<float>, blocks, 256, stream, w, ldw, v, ids, n, k, parts,
+                        scale, static_cast<float*>(D), ldd);
+}
+
+int embed_rows_grad(const void* G, int64_t ldg, int g_dtype, const int32_t* ids, int64_t n,
+                    int64_t rows, int64_t K, float scale, void* D, int64_t ldd, int d_dtype,
+                    int accumulate, void* cuda_stream) {
+  int rc = check_embed(n, rows, K, g_dtype, d_dtype);
+  if (rc != TG_OK) return rc;
+  if (accumulate != 0 && accumulate != 1) return TG_ERR_INVALID_ARG;
+  if (rows == 0 || K == 0 || (accumulate && n == 0)) return TG_OK;
+  rc = check_rows(D, ldd, K, esize(d_dtype));
+  if (rc != TG_OK) return rc;
+  if (n > 0) {
+    if (ids == nullptr) return TG_ERR_INVALID_ARG;
+    rc = check_rows(G, ldg, K, esize(g_dtype));
+    if (rc != TG_OK) return rc;
+  }
+  DeviceCtx* ctx = current_ctx();
+  if (!ctx) return TG_ERR_CUDA;
+  cudaStream_t stream = static_cast<cudaStream_t>(cuda_stream);
+  EmbedGradArgs a{};
+  a.G = G;
+  a.ldg = ldg;
+  a.n = static_cast<int>(n);
+  a.vocab = static_cast<int>(rows);
+  a.K = static_cast<int>(K);
+  a.scale = scale;
+  a.D = D;
+  a.ldd = ldd;
+  if (n > 0) {
+    const EmbedPlan plan = embed_plan(n, rows, K);
+    if (static_cast<int64_t>(plan.chunks) * ((K + kSlice - 1) / kSlice) > kMaxDim / 2)
+      return TG_ERR_UNSUPPORTED;
+    uint8_t* ws = static_cast<uint8_t*>(device_workspace(plan.bytes, stream, &rc));
+    if (ws == nullptr) return rc;
+    unsigned* marks = accumulate ? nullptr : reinterpret_cast<unsigned*>(ws + plan.marks);
+    if (marks != nullptr) {
+      const cudaError_t e =
+          cudaMemsetAsync(marks, 0, static_cast<size_t>((rows + 31) / 32 * 4), stream);
+      if (e != cudaSuccess) return cuda_fail(e);
+    }
+    int* order = reinterpret_cast<int*>(ws);
+    int* sorted = reinterpret_cast<int*>(ws + plan.sorted);
+    rc = sort_ids(ids, n, rows, order, reinterpret_cast<int*>(ws + plan.other), sorted,
+                  reinterpret_cast<int*>(ws + plan.count), marks, ws + plan.hist, stream, ctx);
+    if (rc != TG_OK) return rc;
+    a.order = order;
+    a.sorted = sorted;
+    a.marks = marks;
+    a.parts = reinterpret_cast<float*>(ws + plan.parts);
+    a.ldp = plan.ldp;
+    a.chunk = plan.chunk;
+    a.chunks = plan.chunks;
+    a.slices = static_cast<int>((K + kSlice - 1) / kSlice);
+  }
+  const bool add = accumulate != 0, g16 = g_dtype == TG_D_BF16, d16 = d_dtype == TG_D_BF16;
+  if (g16 && d16) return launch_grad<uint16_t, uint16_t>(a, add, ctx, stream);
+  if (g16) return launch_grad<uint16_t, float>(a, add, ctx, stream);
+  if (d16) return launch_grad<float, uint16_t>(a, add, ctx, stream);
+  return launch_grad<float, float>(a, add, ctx, stream);
+}
+
+}  // extern "C"

@@ -1,0 +1,490 @@
+// Softmax cross entropy over a vocabulary and its gradient, logits never kept.
+//
+//   z = scale * A * B^T,  lse_i = log(sum_j exp z_ij),  loss_i = lse_i - z_i,t(i)
+//   dz_ij = grad_i * scale * (exp(z_ij - lse_i) - [j = t(i)])
+//   dA = dz * B,  dB = dz^T * A          (rows without a target: loss 0, dz 0)
+//
+// Forward: one pass of the product (xent_kernel.cuh) leaves a maximum and a sum
+// per row and 128 columns, which xent_finish_kernel joins.  Backward: the
+// vocabulary in pieces; for each, dz from the product made again, then the
+// grouped gradients' kernels on it: dA's share (added up in f32 over the pieces)
+// and the piece's rows of dB, which are complete.  dz passes between them as
+// bf16, rounded once at 2^-9, as any gradient of a bf16 layer is; for f32
+// gradients as two bf16 terms (2^-17), in one contraction over both.
+#include <atomic>
+
+#include "grouped_launch.cuh"
+#include "xent_kernel.cuh"
+#include "xent_plan.h"
+
+using namespace tg;
+
+namespace tg {
+namespace {
+
+template <class K, class... T>
+int launch_chained(K kern, int64_t blocks, int threads, cudaStream_t stream, T... args) {
+  cudaLaunchConfig_t cfg{};
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.gridDim = dim3(static_cast<unsigned>(blocks), 1, 1);
+  cfg.blockDim = dim3(static_cast<unsigned>(threads), 1, 1);
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, args...);
+  return e == cudaSuccess ? TG_OK : cuda_fail(e);
+}
+
+// ---------------------------------------------------------------------------
+// The product
+// ---------------------------------------------------------------------------
+
+template <class C>
+int xent_units(DeviceCtx* ctx) {
+  static std::atomic<int> prepared[64];
+  std::atomic<int>& slot = prepared[ctx->device];
+  int units = slot.load(std::memory_order_acquire);
+  if (units > 0) return units;
+  auto kern = xent_kernel<C>;
+  cudaError_t e =
+      cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_BYTES);
+  if (e != cudaSuccess) return -cuda_fail(e);
+  units = ctx->num_sms / C::kCtaGroup;
+  if constexpr (C::kCtaGroup == 2) {
+    cudaLaunchConfig_t cfg{};
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.gridDim = dim3(static_cast<unsigned>(2 * units), 1, 1);
+    cfg.blockDim = dim3(C::kThreads, 1, 1);
+    cfg.dynamicSmemBytes = C::SMEM_BYTES;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    int clusters = 0;
+    e = cudaOccupancyMaxActiveClusters(&clusters, kern, &cfg);
+    if (e != cudaSuccess) return -cuda_fail(e);
+    if (clusters > 0 && clusters < units) units = clusters;
+  }
+  if (units < 1) units = 1;
+  slot.store(units, std::memory_order_release);
+  return units;
+}
+
+struct XentOperands {
+  const void* A;
+  int64_t lda;
+  const void* B;
+  int64_t ldb;
+  int64_t K;
+  void* dz;            // kXentGrad: [terms][M][ld_dz]
+  int64_t ld_dz;
+};
+
+template <int kCtaGroup, int kMode>
+int launch_xent_cfg(const XentOperands& o, const XentArgs& args, const XentTiles& tiles,
+                    cudaStream_t stream, DeviceCtx* ctx) {
+  using C = XentCfg<kCtaGroup, kMode>;
+  const int units = xent_units<C>(ctx);
+  if (units < 0) return TG_ERR_CUDA;
+  XentArgs a = args;
+  a.num_k_blocks = ceil_div_i(o.K, 64);
+  a.num_m_tiles = tiles.m_tiles;
+  a.num_n_tiles = tiles.n_tiles;
+  a.bn = tiles.bn;
+  // Bands of 4096 rows: the units that run at the same time share panels of B.
+  a.raster_group = 4096 / (128 * kCtaGroup);
+  a.a_box = kCtaGroup == 2 ? 128 : ceil_div_i(a.M, 8) * 8;
+  a.status = ctx->status;
+  a.timeout_ns = wait_timeout_ns();
+  const CUtensorMapDataType bf = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+  const CUtensorMapSwizzle sw = CU_TENSOR_MAP_SWIZZLE_128B;
+  CUtensorMap tA, tB;
+  int rc = make_tensor_map_2d(&tA, bf, o.A, o.K, a.M, o.lda * 2, 64, a.a_box, sw);
+  if (rc != TG_OK) return rc;
+  rc = make_tensor_map_2d(&tB, bf, o.B, o.K, a.N, o.ldb * 2, 64, a.bn / kCtaGroup, sw);
+  if (rc != TG_OK) return rc;
+  CUtensorMap tD = tA, tD2 = tA;
+  if constexpr (kMode != kXentLoss) {
+    rc = make_tensor_map_2d(&tD, bf, o.dz, o.ld_dz, a.M, o.ld_dz * 2, 64, 32, sw);
+    if (rc != TG_OK) return rc;
+    if constexpr (C::kTwo) {
+      rc = make_tensor_map_2d(&tD2, bf, static_cast<uint16_t*>(o.dz) + a.M * o.ld_dz, o.ld_dz, a.M,
+                              o.ld_dz * 2, 64, 32, sw);
+      if (rc != TG_OK) return rc;
+    }
+  }
+  const int64_t num_tiles = static_cast<int64_t>(tiles.m_tiles) * tiles.n_tiles;
+  cudaLaunchConfig_t cfg{};
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = kCtaGroup;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.gridDim = dim3(static_cast<unsigned>((num_tiles < units ? num_tiles : units) * kCtaGroup));
+  cfg.blockDim = dim3(C::kThreads);
+  cfg.dynamicSmemBytes = C::SMEM_BYTES;
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = kCtaGroup == 2 ? 2 : 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, xent_kernel<C>, tA, tB, tD, tD2, a);
+  return e == cudaSuccess ? TG_OK : cuda_fail(e);
+}
+
+template <int kMode>
+int launch_xent(const XentOperands& o, const XentArgs& a, const XentTiles& tiles,
+                cudaStream_t stream, DeviceCtx* ctx) {
+  return a.M <= kXentFewRows ? launch_xent_cfg<1, kMode>(o, a, tiles, stream, ctx)
+                             : launch_xent_cfg<2, kMode>(o, a, tiles, stream, ctx);
+}
+
+// ---------------------------------------------------------------------------
+// Joining the tiles' maxima and sums
+// ---------------------------------------------------------------------------
+
+// Sums of exp(scale (a - m)): those of m2 join those of m.  The larger reference
+// keeps its sum as it is, which also makes an infinite one meet itself without inf -
+// inf.
+__device__ __forceinline__ void join_sums(float& m, float& s, float m2, float s2, float scale2) {
+  const float top = fmaxf(m, m2);
+  s = s * (m == top ? 1.0f : exp2f((m - top) * scale2)) +
+      s2 * (m2 == top ? 1.0f : exp2f((m2 - top) * scale2));
+  m = top;
+}
+
+// Blocks of `rows` rows: neighbouring threads hold neighbouring rows, the block's
+// others every 256 / rows-th part of them; joined in a fixed order.
+__global__ void __launch_bounds__(256) xent_finish_kernel(const float2* parts, int count,
+                                                          const float* target_z, const int* targets,
+                                                          float* loss, float* lse, int M, int vocab,
+                                                          int rows, float scale, float scale2) {
+  __shared__ float2 shared[256];
+  griddep_wait();
+  griddep_launch_dependents();
+  const int r = static_cast<int>(threadIdx.x) % rows;
+  const int group = static_cast<int>(threadIdx.x) / rows;
+  const int groups = 256 / rows;
+  const int row = static_cast<int>(blockIdx.x) * rows + r;
+  float m = __uint_as_float(0xFF800000u), s = 0.0f;
+  if (row < M) {
+    const float2* at = parts + row;
+    int q = group;
+    for (; q + 3 * groups < count; q += 4 * groups) {
+      float2 v[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[i] = __ldcg(at + static_cast<int64_t>(q + i * groups) * M);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) join_sums(m, s, v[i].x, v[i].y, scale2);
+    }
+    for (; q < count; q += groups) {
+      const float2 v = __ldcg(at + static_cast<int64_t>(q) * M);
+      join_sums(m, s, v.x, v.y, scale2);
+    }
+  }
+  shared[threadIdx.x] = make_float2(m, s);
+  __syncthreads();
+  for (int half = groups / 2; half > 0; half /= 2) {
+    if (group < half) {
+      const float2 v = shared[threadIdx.x + half * rows];
+      join_sums(m, s, v.x, v.y, scale2);
+      shared[threadIdx.x] = make_float2(m, s);
+    }
+    __syncthreads();
+  }
+  if (group == 0 && row < M) {
+    // The loss from the reference, not from lse: where the target is the largest
+    // logit, the difference is 0 and the small rest keeps its digits.
+    const float l = logf(s);
+    const int t = targets[row];
+    lse[row] = fmaf(m, scale, l);
+    loss[row] = t >= 0 && t < vocab ? fmaf(m - __ldcg(target_z + row), scale, l) : 0.0f;
+  }
+}
+
+// K = 0: every logit is 0.  (No column: lse = log 0.)
+__global__ void xent_zero_kernel(const int* targets, float* loss, float* lse, int M, int vocab) {
+  const int64_t row = blockIdx.x * static_cast<int64_t>(blockDim.x) + threadIdx.x;
+  if (row >= M) return;
+  const float l = logf(static_cast<float>(vocab));
+  const int t = targets[row];
+  lse[row] = l;
+  loss[row] = t >= 0 && t < vocab ? l : 0.0f;
+}
+
+// ---------------------------------------------------------------------------
+// The gradient's rows of A, and dA's rounding
+// ---------------------------------------------------------------------------
+
+// dst[i] (and dst[M + i] for two terms) = A[i] where row i has a target, else
+// zeros: dz is 0 there, but 0 times what padding holds may be NaN.  Whole
+// 16-byte pieces, a warp a row; the pitch makes room for the last.
+__global__ void __launch_bounds__(256) learned_rows_kernel(const uint16_t* A, int64_t lda,
+                                                           const int* targets, int vocab,
+                                                           uint16_t* dst, int64_t ld, int M, int K,
+                                                           int terms) {
+  griddep_wait();
+  griddep_launch_dependents();
+  const int lane = static_cast<int>(threadIdx.x & 31);
+  const int64_t warps = static_cast<int64_t>(gridDim.x) * 8;
+  const int whole = K / 8;
+  for (int64_t i = blockIdx.x * 8LL + (threadIdx.x >> 5); i < M; i += warps) {
+    const int t = targets[i];
+    const bool learned = t >= 0 && t < vocab;
+    const uint16_t* s = A + i * lda;
+    uint16_t* d = dst + i * ld;
+    for (int k0 = 0; k0 < whole; k0 += 128) {
+      uint4 v[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const int k = k0 + 32 * u + lane;
+        v[u] = make_uint4(0u, 0u, 0u, 0u);
+        if (learned && k < whole) v[u] = __ldcs(reinterpret_cast<const uint4*>(s) + k);
+      }
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const int k = k0 + 32 * u + lane;
+        if (k < whole)
+          for (int h = 0; h < terms; ++h)
+            reinterpret_cast<uint4*>(d + static_cast<int64_t>(h) * M * ld)[k] = v[u];
+      }
+    }
+    const int k = whole * 8 + lane;
+    if (lane < 8 && k < K)
+      for (int h = 0; h < terms; ++h) d[static_cast<int64_t>(h) * M * ld + k] = learned ? s[k] : 0;
+  }
+}
+
+__global__ void __launch_bounds__(256) round_rows_kernel(const float* src, int64_t ld,
+                                                         uint16_t* dst, int64_t ldd, int M, int K) {
+  griddep_wait();
+  griddep_launch_dependents();
+  const int per = (K + 3) / 4;       // the sums' rows end on 16 bytes
+  const int64_t total = static_cast<int64_t>(M) * per;
+  for (int64_t i = blockIdx.x * 256LL + threadIdx.x; i < total; i += 256LL * gridDim.x) {
+    const int64_t row = i / per;
+    const int k = 4 * static_cast<int>(i - row * per);
+    const float4 v = __ldcs(reinterpret_cast<const float4*>(src + row * ld + k));
+    uint16_t* d = dst + row * ldd + k;
+    const uint32_t lo = pack_bf16x2(v.x, v.y), hi = pack_bf16x2(v.z, v.w);
+    if (k + 4 <= K) {
+      *reinterpret_cast<uint2*>(d) = make_uint2(lo, hi);
+    } else {
+      const uint32_t w[2] = {lo, hi};
+      for (int e = 0; k + e < K; ++e) d[e] = static_cast<uint16_t>(w[e / 2] >> (16 * (e & 1)));
+    }
+  }
+}
+
+int clear_rows(void* D, int64_t ldd, int64_t rows, int64_t width, int esize, cudaStream_t stream) {
+  if (rows == 0 || width == 0) return TG_OK;
+  const cudaError_t e = cudaMemset2DAsync(D, static_cast<size_t>(ldd * esize), 0,
+                                          static_cast<size_t>(width * esize),
+                                          static_cast<size_t>(rows), stream);
+  return e == cudaSuccess ? TG_OK : cuda_fail(e);
+}
+
+// ---------------------------------------------------------------------------
+// Checks
+// ---------------------------------------------------------------------------
+
+constexpr int64_t kMaxDim = (int64_t{1} << 31) - 1;
+
+int check_rows(const void* p, int64_t ld, int64_t width, int esize) {
+  if (p == nullptr || ld < width) return TG_ERR_INVALID_ARG;
+  if ((reinterpret_cast<uintptr_t>(p) & 15u) != 0 || (ld * esize) % 16 != 0)
+    return TG_ERR_MISALIGNED;
+  return TG_OK;
+}
+
+int check_xent(int64_t M, int64_t N, int64_t K, float scale, unsigned flags) {
+  if (M < 0 || N < 0 || K < 0 || M > kMaxDim || N > kMaxDim || K > kMaxDim)
+    return TG_ERR_INVALID_ARG;
+  // (A negative scale would make the smallest product the largest logit.)
+  if (!(scale > 0.0f) || scale > 3.0e38f) return TG_ERR_INVALID_ARG;
+  if (flags != 0) return TG_ERR_UNSUPPORTED;
+  if (M > kGroupedMaxExtent || N > kGroupedMaxExtent || K > kGroupedMaxExtent)
+    return TG_ERR_UNSUPPORTED;
+  // Tile counts stay below 2^31, also those of the gradients' products.
+  if ((M / 256 + 1) * (N / 64 + 1) > kMaxDim || (M / 256 + 1) * (K / 128 + 1) > kMaxDim ||
+      (N / 256 + 1) * (K / 128 + 1) > kMaxDim)
+    return TG_ERR_UNSUPPORTED;
+  return TG_OK;
+}
+
+}  // namespace
+
+size_t xent_workspace_bytes(int64_t M, int64_t N) { return xent_loss_plan(M, N).bytes; }
+size_t xent_grad_workspace_bytes(int64_t M, int64_t N, int64_t K, int d_dtype) {
+  return xent_grad_plan(M, N, K, d_dtype == TG_D_BF16).bytes;
+}
+
+}  // namespace tg
+
+extern "C" {
+
+int gemm_bf16_xent(const void* A, int64_t lda, const void* B, int64_t ldb, const int32_t* targets,
+                   float scale, float* loss, float* lse, int64_t M, int64_t N, int64_t K,
+                   unsigned flags, void* cuda_stream) {
+  int rc = check_xent(M, N, K, scale, flags);
+  if (rc != TG_OK || M == 0) return rc;
+  if (targets == nullptr || loss == nullptr || lse == nullptr) return TG_ERR_INVALID_ARG;
+  if (N > 0 && K > 0) {
+    rc = check_rows(A, lda, K, 2);
+    if (rc == TG_OK) rc = check_rows(B, ldb, K, 2);
+    if (rc != TG_OK) return rc;
+  }
+  DeviceCtx* ctx = current_ctx();
+  if (!ctx) return TG_ERR_CUDA;
+  cudaStream_t stream = static_cast<cudaStream_t>(cuda_stream);
+  const int m = static_cast<int>(M), n = static_cast<int>(N);
+  if (N == 0 || K == 0) {
+    xent_zero_kernel<<<static_cast<unsigned>((M + 255) / 256), 256, 0, stream>>>(targets, loss, lse,
+                                                                                m, n);
+    const cudaError_t e = cudaGetLastError();
+    return e == cudaSuccess ? TG_OK : cuda_fail(e);
+  }
+  const XentLossPlan plan = xent_loss_plan(M, N);
+  uint8_t* ws = static_cast<uint8_t*>(device_workspace(plan.bytes, stream, &rc));
+  if (ws == nullptr) return rc;
+  XentArgs a{};
+  a.M = m;
+  a.N = a.vocab = n;
+  a.scale = scale;
+  a.scale2 = scale * 1.4426950408889634f;
+  a.targets = targets;
+  a.parts = reinterpret_cast<float2*>(ws);
+  a.target_z = reinterpret_cast<float*>(ws + plan.off_z);
+  const XentOperands o{A, lda, B, ldb, K, nullptr, 0};
+  rc = launch_xent<kXentLoss>(o, a, plan.tiles, stream, ctx);
+  if (rc != TG_OK) return rc;
+  int rows = 1;
+  while (rows < 32 && rows < m) rows *= 2;
+  return launch_chained(xent_finish_kernel, (M + rows - 1) / rows, 256, stream,
+                        static_cast<const float2*>(a.parts), 2 * plan.tiles.n_tiles,
+                        static_cast<const float*>(a.target_z), targets, loss, lse, m, n, rows, a.scale, a.scale2);
+}
+
+int gemm_bf16_xent_grad(const void* A, int64_t lda, const void* B, int64_t ldb,
+                        const int32_t* targets, const float* lse, const float* grad, float scale,
+                        void* dA, int64_t ldda, void* dB, int64_t lddb, int64_t M, int64_t N,
+                        int64_t K, int d_dtype, unsigned flags, void* cuda_stream) {
+  int rc = check_xent(M, N, K, scale, flags);
+  if (rc != TG_OK) return rc;
+  if (d_dtype != TG_D_F32 && d_dtype != TG_D_BF16) return TG_ERR_INVALID_ARG;
+  const bool bf16 = d_dtype == TG_D_BF16;
+  if (!bf16 && 2 * M > kGroupedMaxExtent) return TG_ERR_UNSUPPORTED;
+  if (K == 0) return TG_OK;
+  const int esize = bf16 ? 2 : 4;
+  const bool rows = dA != nullptr && M > 0, weights = dB != nullptr && N > 0;
+  if (rows) rc = check_rows(dA, ldda, K, esize);
+  if (rc == TG_OK && weights) rc = check_rows(dB, lddb, K, esize);
+  if (rc != TG_OK || (!rows && !weights)) return rc;
+  if (M > 0 && N > 0) {
+    if (targets == nullptr || lse == nullptr) return TG_ERR_INVALID_ARG;
+    rc = check_rows(A, lda, K, 2);
+    if (rc == TG_OK) rc = check_rows(B, ldb, K, 2);
+    if (rc != TG_OK) return rc;
+  }
+  DeviceCtx* ctx = current_ctx();
+  if (!ctx) return TG_ERR_CUDA;
+  cudaStream_t stream = static_cast<cudaStream_t>(cuda_stream);
+  if (M == 0) return clear_rows(dB, lddb, N, K, esize, stream);
+  if (N == 0) return clear_rows(dA, ldda, M, K, esize, stream);
+
+  const XentGradPlan plan = xent_grad_plan(M, N, K, bf16);
+  uint8_t* ws = static_cast<uint8_t*>(device_workspace(plan.bytes, stream, &rc));
+  if (ws == nullptr) return rc;
+  uint16_t* a_rows = reinterpret_cast<uint16_t*>(ws);
+  uint16_t* dz = reinterpret_cast<uint16_t*>(ws + plan.off_dz);
+  float* sums = reinterpret_cast<float*>(ws + plan.off_sum);
+  const int m = static_cast<int>(M);
+  const int64_t row_blocks = (M + 7) / 8 < 16 * ctx->num_sms ? (M + 7) / 8 : 16 * ctx->num_sms;
+  rc = launch_chained(learned_rows_kernel, row_blocks, 256, stream,
+                      static_cast<const uint16_t*>(A), lda, targets, static_cast<int>(N), a_rows,
+                      plan.ld_a, m, static_cast<int>(K), plan.terms);
+  if (rc != TG_OK) return rc;
+
+  XentArgs a{};
+  a.M = m;
+  a.vocab = static_cast<int>(N);
+  a.scale = scale;
+  a.scale2 = scale * 1.4426950408889634f;
+  a.targets = targets;
+  a.lse = lse;
+  a.grad = grad;
+  for (int64_t col0 = 0; col0 < N; col0 += plan.piece) {
+    const int64_t n = N - col0 < plan.piece ? N - col0 : plan.piece;
+    const uint16_t* b = static_cast<const uint16_t*>(B) + col0 * ldb;
+    a.N = static_cast<int>(n);
+    a.col0 = static_cast<int>(col0);
+    const XentOperands o{a_rows, plan.ld_a, b, ldb, K, dz, plan.ld_dz};
+    const XentTiles tiles = xent_tiles(M, n, 64);
+    rc = bf16 ? launch_xent<kXentGrad>(o, a, tiles, stream, ctx)
+              : launch_xent<kXentGradTwo>(o, a, tiles, stream, ctx);
+    if (rc != TG_OK) return rc;
+    if (rows) {
+      GroupedArgs g = grouped_args(ctx);
+      g.M = m;
+      g.wide = static_cast<int>(K);
+      g.num_k_blocks = ceil_div_i(n, 64);
+      GroupedOperands p{};
+      p.wide = b;
+      p.wide_ld = ldb;
+      p.wide_rows = n;
+      p.wide_slices = 1;
+      p.wide_slice_stride = ldb * n;
+      p.cols_ld = plan.ld_dz;
+      p.k = n;
+      for (int term = 0; term < plan.terms; ++term) {
+        p.cols = dz + static_cast<int64_t>(term) * M * plan.ld_dz;
+        g.add = col0 > 0 || term > 0;
+        if (bf16 && plan.pieces == 1) {
+          g.D = dA;
+          g.ldd = ldda;
+          rc = launch_grouped_dgrad(true, p, g, stream, ctx);
+        } else {
+          g.D = bf16 ? static_cast<void*>(sums) : dA;
+          g.ldd = bf16 ? plan.ld_sum : ldda;
+          rc = launch_grouped_dgrad_add(!bf16, p, g, stream, ctx);
+        }
+        if (rc != TG_OK) return rc;
+      }
+    }
+    if (weights) {
+      // Both terms in one contraction: dz and the rows of A lie below each other.
+      const int64_t terms_rows = plan.terms * M;
+      GroupedArgs g = grouped_args(ctx);
+      g.M = static_cast<int>(terms_rows);
+      g.wide = static_cast<int>(K);
+      g.cols = static_cast<int>(n);
+      g.num_col_tiles = ceil_div_i(n, 256);
+      g.num_k_blocks = ceil_div_i(terms_rows, 64);
+      g.D = static_cast<uint8_t*>(dB) + col0 * lddb * esize;
+      g.ldd = lddb;
+      GroupedOperands p{};
+      p.wide = a_rows;
+      p.wide_ld = plan.ld_a;
+      p.wide_rows = terms_rows;
+      p.wide_slices = 1;
+      p.cols = dz;
+      p.cols_ld = plan.ld_dz;
+      p.k = terms_rows;
+      rc = launch_grouped_wgrad(bf16, p, g, stream, ctx);
+      if (rc != TG_OK) return rc;
+    }
+  }
+  if (rows && bf16 && plan.pieces > 1) {
+    const int64_t blocks = (M * ((K + 3) / 4) + 255) / 256;
+    rc = launch_chained(round_rows_kernel, blocks < 16 * ctx->num_sms ? blocks : 16 * ctx->num_sms,
+                        256, stream, static_cast<const float*>(sums), plan.ld_sum,
+                        static_cast<uint16_t*>(dA), ldda, m, static_cast<int>(K));
+  }
+  return rc;
+}
+
+}  // extern "C"

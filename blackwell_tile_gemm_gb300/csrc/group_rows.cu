@@ -42,10 +42,25 @@ struct RowsArgs {
   int* order;
   int* slot;     // may be null
   int* counts;   // [keys][CTA] of the counting kernel
+  // One digit of a longer id (kDigit): keys are (id >> shift) & (2^digit - 1) of the
+  // ids below `limit`, in the order `from` of the digits before (null: as given).
+  // The last digit sends the ids outside [0, limit) behind all others and writes
+  // the ids in their order (-1 for those); the first marks the ids that occur.
+  const int* from;
+  int shift, digit, limit, last;
+  int* sorted;
+  unsigned* marks;   // a bit for each id, zero before; may be null
 };
 
+template <bool kDigit>
 __device__ __forceinline__ int key_of(const RowsArgs& p, int i) {
-  const int id = p.ids[i];   // (a read-only load need not stay behind griddep_wait)
+  const int id = p.ids[kDigit && p.from ? p.from[i] : i];   // (a read-only load need not stay
+                                                            // behind griddep_wait)
+  if constexpr (kDigit) {
+    if (static_cast<unsigned>(id) < static_cast<unsigned>(p.limit))
+      return (id >> p.shift) & ((1 << p.digit) - 1);
+    return p.last ? p.groups : 0;
+  }
   return static_cast<unsigned>(id) < static_cast<unsigned>(p.groups) ? id : p.groups;
 }
 
@@ -65,13 +80,13 @@ __device__ __forceinline__ unsigned same_key(int key, int bits) {
 // Calls f(key, lanes with that key, row) for the rows [lo, hi), 32 at a time;
 // key is -1 past the end.  The ids of kAhead steps are loaded together: one
 // load a step left a warp waiting about 1 us for each.
-template <class F>
+template <bool kDigit, class F>
 __device__ __forceinline__ void walk(const RowsArgs& p, int lo, int hi, int lane, F f) {
   constexpr int kAhead = 8;
   for (int b = lo; b < hi; b += 32 * kAhead) {
     int key[kAhead];
 #pragma unroll
-    for (int j = 0; j < kAhead; ++j) key[j] = hi - b > 32 * j + lane ? key_of(p, b + 32 * j + lane) : -1;
+    for (int j = 0; j < kAhead; ++j) key[j] = hi - b > 32 * j + lane ? key_of<kDigit>(p, b + 32 * j + lane) : -1;
 #pragma unroll
     for (int j = 0; j < kAhead; ++j) {
       if (hi - b <= 32 * j) break;
@@ -81,6 +96,7 @@ __device__ __forceinline__ void walk(const RowsArgs& p, int lo, int hi, int lane
 }
 
 // Rows of each key among this CTA's rows.
+template <bool kDigit>
 __global__ void __launch_bounds__(1024, 1) count_rows_kernel(const RowsArgs p) {
   extern __shared__ int smem[];
   const int keys = p.groups + 1;
@@ -92,13 +108,13 @@ __global__ void __launch_bounds__(1024, 1) count_rows_kernel(const RowsArgs p) {
   const int64_t lo = blockIdx.x * per;
   const int64_t hi = lo + per < p.n ? lo + per : p.n;
   for (int64_t i = lo + threadIdx.x; i < hi; i += blockDim.x)
-    atomicAdd(smem + key_of(p, static_cast<int>(i)), 1);   // a count: any order gives it
+    atomicAdd(smem + key_of<kDigit>(p, static_cast<int>(i)), 1);   // a count: any order gives it
   __syncthreads();
   for (int g = threadIdx.x; g < keys; g += blockDim.x)
     p.counts[static_cast<int64_t>(g) * gridDim.x + blockIdx.x] = smem[g];
 }
 
-template <bool kMany>
+template <bool kMany, bool kDigit>
 __global__ void __launch_bounds__(32 * kMaxWarps, 1) place_rows_kernel(const RowsArgs p) {
   extern __shared__ int smem[];
   const int keys = p.groups + 1;
@@ -121,7 +137,7 @@ __global__ void __launch_bounds__(32 * kMaxWarps, 1) place_rows_kernel(const Row
   const int lo = warp < p.warps && lo64 < p.n ? static_cast<int>(lo64) : p.n;
   const int hi = p.n - lo > p.chunk ? lo + p.chunk : p.n;
   int* mine = hist + warp * keys;   // (only warps below p.warps have rows)
-  walk(p, lo, hi, lane, [&](int key, unsigned peers, int) {
+  walk<kDigit>(p, lo, hi, lane, [&](int key, unsigned peers, int) {
     if (key >= 0 && __ffs(peers) - 1 == lane) mine[key] += __popc(peers);
     __syncwarp();
   });
@@ -197,13 +213,22 @@ __global__ void __launch_bounds__(32 * kMaxWarps, 1) place_rows_kernel(const Row
     }
     __syncthreads();
   }
-  walk(p, lo, hi, lane, [&](int key, unsigned peers, int i) {
+  walk<kDigit>(p, lo, hi, lane, [&](int key, unsigned peers, int i) {
     int seen = 0;
     if (key >= 0) seen = mine[key];
     __syncwarp();
     if (key >= 0) {
       const int at = start[key] + seen + __popc(peers & ((1u << lane) - 1u));
-      p.order[at] = i;
+      if constexpr (kDigit) {
+        const int row = p.from ? p.from[i] : i;
+        p.order[at] = row;
+        const int id = p.ids[row];
+        const bool in = static_cast<unsigned>(id) < static_cast<unsigned>(p.limit);
+        if (p.sorted != nullptr) p.sorted[at] = in ? id : -1;
+        if (p.marks != nullptr && in) atomicOr(p.marks + (id >> 5), 1u << (id & 31));
+      } else {
+        p.order[at] = i;
+      }
       if (p.slot != nullptr) p.slot[i] = at;
       if (__ffs(peers) - 1 == lane) mine[key] = seen + __popc(peers);
     }
@@ -241,6 +266,9 @@ int rows_ctas(int64_t n, int num_sms) {
   return static_cast<int>(c < num_sms ? c : num_sms);
 }
 
+// counts: the counting kernel's histograms (group_rows_workspace_bytes), or null: the
+// stream's workspace.
+template <bool kDigit>
 int launch_rows(RowsArgs a, cudaStream_t stream, DeviceCtx* ctx) {
   static std::atomic<int> prepared[3][64];
   const int keys = a.groups + 1;
@@ -255,14 +283,15 @@ int launch_rows(RowsArgs a, cudaStream_t stream, DeviceCtx* ctx) {
   while ((1 << a.bits) < keys) ++a.bits;
   const size_t smem = static_cast<size_t>(4) * keys * (warps + 2);
   if (ctas == 1)
-    return launch_one(place_rows_kernel<false>, 1, 32 * warps, smem, a, stream, ctx, prepared[0]);
+    return launch_one(place_rows_kernel<false, kDigit>, 1, 32 * warps, smem, a, stream, ctx, prepared[0]);
   int rc = TG_OK;
-  a.counts = static_cast<int*>(device_workspace(group_rows_workspace_bytes(a.n, a.groups), stream, &rc));
+  if (a.counts == nullptr)
+    a.counts = static_cast<int*>(device_workspace(group_rows_workspace_bytes(a.n, a.groups), stream, &rc));
   if (a.counts == nullptr) return rc;
-  rc = launch_one(count_rows_kernel, ctas, 1024, static_cast<size_t>(4) * keys, a, stream, ctx,
+  rc = launch_one(count_rows_kernel<kDigit>, ctas, 1024, static_cast<size_t>(4) * keys, a, stream, ctx,
                   prepared[1]);
   if (rc != TG_OK) return rc;
-  return launch_one(place_rows_kernel<true>, ctas, 1024, smem, a, stream, ctx, prepared[2]);
+  return launch_one(place_rows_kernel<true, kDigit>, ctas, 1024, smem, a, stream, ctx, prepared[2]);
 }
 
 }  // namespace
@@ -271,6 +300,48 @@ int launch_rows(RowsArgs a, cudaStream_t stream, DeviceCtx* ctx) {
 size_t group_rows_workspace_bytes(int64_t n, int64_t groups) {
   const int c = rows_ctas(n, 256);
   return c == 1 ? 0 : static_cast<size_t>(c) * static_cast<size_t>(groups + 1) * 4u;
+}
+
+// Rows by id for more ids than one sort has keys: digit by digit from the lowest,
+// each sort being stable.
+int sort_digits(int64_t ids) {
+  int bits = 1;
+  while (bits < 31 && (int64_t{1} << bits) < ids) ++bits;
+  return (bits + kSortDigit - 1) / kSortDigit;
+}
+
+size_t sort_ids_workspace_bytes(int64_t n) {
+  return group_rows_workspace_bytes(n, int64_t{1} << kSortDigit);
+}
+
+int sort_ids(const int* ids, int64_t n, int64_t limit, int* order, int* other, int* sorted,
+             int* count, unsigned* marks, void* histograms, cudaStream_t stream, DeviceCtx* ctx) {
+  int bits = 1;
+  while (bits < 31 && (int64_t{1} << bits) < limit) ++bits;
+  const int digits = sort_digits(limit);
+  const int digit = (bits + digits - 1) / digits;
+  const int* from = nullptr;
+  for (int d = 0; d < digits; ++d) {
+    RowsArgs a{};
+    a.ids = ids;
+    a.n = static_cast<int>(n);
+    a.last = d + 1 == digits;
+    a.shift = d * digit;
+    a.digit = digit;
+    a.limit = static_cast<int>(limit);
+    a.groups = a.last ? static_cast<int>(((limit - 1) >> a.shift) + 1) : 1 << digit;
+    // The buffers take turns so that the last digit writes `order`.
+    a.order = (digits - 1 - d) % 2 == 0 ? order : other;
+    a.from = from;
+    a.offsets = count;
+    a.sorted = a.last ? sorted : nullptr;
+    a.marks = d == 0 ? marks : nullptr;
+    a.counts = static_cast<int*>(histograms);
+    const int rc = launch_rows<true>(a, stream, ctx);
+    if (rc != TG_OK) return rc;
+    from = a.order;
+  }
+  return TG_OK;
 }
 
 }  // namespace tg
@@ -294,5 +365,5 @@ extern "C" int tg_group_rows(const int32_t* ids, int64_t n, int64_t groups, int3
   a.order = order;
   a.slot = slot;
   cudaStream_t stream = static_cast<cudaStream_t>(cuda_stream);
-  return launch_rows(a, stream, ctx);
+  return launch_rows<false>(a, stream, ctx);
 }

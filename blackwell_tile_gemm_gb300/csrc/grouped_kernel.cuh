@@ -111,6 +111,7 @@ struct GroupedArgs {
   void* D;
   int64_t ldd;
   int64_t group_stride_d;  // wgrad
+  int add;                 // kAdd: D += instead of D =
   Epi epi;                 // bias: [groups][wide]
   // adapters
   const int* ids;          // [M]
@@ -147,7 +148,7 @@ struct ColumnMaps {
 };
 
 template <int kMode_, int kCtaGroup_, int kTileN_, int kStages_, bool kBf16Out_,
-          bool kTail_ = kCtaGroup_ == 1>
+          bool kTail_ = kCtaGroup_ == 1, int kAdd_ = 0>
 struct GroupedCfg {
   static constexpr int kMode = kMode_;
   static constexpr int kCtaGroup = kCtaGroup_;
@@ -165,6 +166,10 @@ struct GroupedCfg {
   // Adapter stages (MMA form) and ragged contractions are fixed up in shared
   // memory before the MMAs read them.
   static constexpr bool kExt = kMode == kAdapter && kCtaGroup == 2;
+  // A contraction given in parts (f32 D of CTA pairs): GroupedArgs::add adds the
+  // tile to D instead of writing it.  1: sums that a rounding to bf16 follows, one
+  // accumulator each; 2: sums that stay f32, in chunks.
+  static constexpr int kAdd = kAdd_;
   static constexpr int kTerms = kBf16Out ? 2 : 3;   // bf16 terms of H
   static constexpr int kFixWarps = kExt ? 2 : kMode == kGroupedWgrad ? 1 : 0;
   static constexpr int kColStep = 16 * kCtaGroup;
@@ -192,7 +197,7 @@ struct GroupedCfg {
   // lane) in registers.  (Adding the chunks to D in memory instead cost 80%:
   // 8192^3 wgrad 1579 us.)  bf16 D rounds at 2e-3 and needs none of it.  (kAdapterDown:
   // by the D that H is for, whose terms keep what the sums have.)
-  static constexpr int kChunk = 12;
+  static constexpr int kChunk = kAdd == 1 ? 1 << 30 : 12;
   static constexpr int NUM_BARS = 2 * kStages + 2 * kAccBufs + 1 + (kFixWarps ? 2 * kStages : 0) +
                                   (kExt ? 2 : 0);
   static constexpr int OFF_MISC = OFF_BAR + NUM_BARS * 8;
@@ -215,6 +220,7 @@ struct GroupedCfg {
   static_assert(C_BYTES % 1024 == 0, "swizzle atoms");
   static_assert(!kColMn || (kCtaGroup == 2 && kTileN == 256), "wgrad tiles");
   static_assert(!kWideMn || kCtaGroup == 2, "the gradients run as CTA pairs");
+  static_assert(!kAdd || (kCtaGroup == 2 && !kBf16Out && !kColMn), "added to in f32");
 };
 
 // One work item.
@@ -730,6 +736,16 @@ __device__ __forceinline__ void grouped_unstage(const GroupedArgs& p, int64_t d0
     const int c = C::kBf16Out ? (lane ^ r) & 7 : lane & 7;   // bf16 boxes are swizzled
     const uint4 q = ld_shared_v4(stg + 128 * r + 16 * c);
     T* d = reinterpret_cast<T*>(p.D) + d0 + (row + r) * p.ldd + x;
+    if constexpr (C::kAdd) {
+      if (p.add) {
+        const float v[4] = {__uint_as_float(q.x), __uint_as_float(q.y), __uint_as_float(q.z),
+                            __uint_as_float(q.w)};
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (x + e < p.wide) d[e] += v[e];
+        continue;
+      }
+    }
     if (x + kVec <= p.wide) {
       __stcs(reinterpret_cast<uint4*>(d), q);
     } else {
@@ -1998,7 +2014,10 @@ __global__ void __launch_bounds__(C::kThreads, 1)
               fence_proxy_async_smem();
               __syncwarp();
               if (lane == 0) {
-                tma_store_3d_hint(&tmD, stg, x, row, C::kColMn ? w.g : 0, pol_d);
+                if (C::kAdd && p.add)   // (one addend for each element: the same bits every time)
+                  tma_reduce_add_3d(&tmD, stg, x, row, 0);
+                else
+                  tma_store_3d_hint(&tmD, stg, x, row, C::kColMn ? w.g : 0, pol_d);
                 bulk_commit_group();
               }
             } else {

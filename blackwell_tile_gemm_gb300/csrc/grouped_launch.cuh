@@ -203,6 +203,9 @@ int launch_grouped_dgrad(bool bf16, const GroupedOperands& o, const GroupedArgs&
                          cudaStream_t stream, DeviceCtx* ctx);
 int launch_grouped_wgrad(bool bf16, const GroupedOperands& o, const GroupedArgs& a,
                          cudaStream_t stream, DeviceCtx* ctx);
+// D += (a.add) or D = in f32; `chunked`: for sums that stay f32.
+int launch_grouped_dgrad_add(bool chunked, const GroupedOperands& o, const GroupedArgs& a,
+                             cudaStream_t stream, DeviceCtx* ctx);
 int launch_grouped_adapter(bool bf16, const GroupedOperands& o, const GroupedArgs& a,
                            cudaStream_t stream, DeviceCtx* ctx);
 

@@ -197,6 +197,23 @@ int skinny_splits(int64_t N, int64_t K, int split_k, int num_sms, int* per_split
 // Workspace of tg_group_rows (0 where one CTA does it).
 size_t group_rows_workspace_bytes(int64_t n, int64_t groups);
 
+// Rows 0 .. n - 1 by (id, row), ids outside [0, limit) last: order [n], with
+// other [n] beside it for the digits in between; sorted [n], their ids (-1
+// outside); count [2^kSortDigit + 1], rows by digit; marks (or null) a bit for
+// each id that occurs, zero before the call; histograms: sort_ids_workspace_bytes.
+constexpr int kSortDigit = 9;
+int sort_digits(int64_t ids);
+size_t sort_ids_workspace_bytes(int64_t n);
+int sort_ids(const int* ids, int64_t n, int64_t limit, int* order, int* other, int* sorted,
+             int* count, unsigned* marks, void* histograms, cudaStream_t stream, DeviceCtx* ctx);
+
+// Workspaces of gemm_bf16_xent, gemm_bf16_xent_grad, embed_rows_grad and
+// tg_balance_loss.
+size_t xent_workspace_bytes(int64_t M, int64_t N);
+size_t xent_grad_workspace_bytes(int64_t M, int64_t N, int64_t K, int d_dtype);
+size_t embed_grad_workspace_bytes(int64_t n, int64_t rows, int64_t K);
+size_t balance_workspace_bytes(int64_t M, int64_t N);
+
 // Workspace of gemm_bf16_lora.
 size_t lora_workspace_bytes(int64_t M, int64_t rank);
 

@@ -1,0 +1,91 @@
+// Plans of the vocabulary loss: tile widths, pieces of the vocabulary and the
+// layout of the workspace.  Plain arithmetic, the same with and without a GPU.
+#pragma once
+
+#include <cstddef>
+#include <cstdint>
+
+namespace tg {
+
+// SMs the widths are balanced for (another count changes the balance, not the
+// results' validity).
+constexpr int kXentSms = 152;
+// Up to this many rows run as single CTAs.
+constexpr int64_t kXentFewRows = 128;
+
+inline int64_t xent_up(int64_t a, int64_t b) { return (a + b - 1) / b * b; }
+
+struct XentTiles {
+  int bn;        // columns of a tile
+  int m_tiles, n_tiles;
+};
+
+// Columns per tile: the width whose waves over the units take least.  A stage of
+// a CTA pair costs the larger of its MMAs (2 cycles a column) and its loads (128
+// rows of A and half the columns of B at 64 bytes a cycle); one of few rows
+// streams B from HBM, and what it adds to a tile is A and the epilogue.
+inline XentTiles xent_tiles(int64_t M, int64_t N, int step) {
+  const bool few = M <= kXentFewRows;
+  const int64_t units = few ? kXentSms : kXentSms / 2;
+  const int64_t mt = few ? 1 : (M + 255) / 256;
+  const int64_t least = few ? (step > 32 ? step : 32) : (step > 64 ? step : 64);
+  int64_t best = 0, bn = 256;
+  for (int64_t c = 256; c >= least; c -= step) {
+    const int64_t waves = (mt * ((N + c - 1) / c) + units - 1) / units;
+    const int64_t tile = few ? c + 8 + M / 8 : (2 * c > 256 + c ? 2 * c : 256 + c) + 48;
+    if (best == 0 || waves * tile < best) {
+      best = waves * tile;
+      bn = c;
+    }
+  }
+  return XentTiles{static_cast<int>(bn), static_cast<int>(mt), static_cast<int>((N + bn - 1) / bn)};
+}
+
+// Workspace of the loss: [2 * n_tiles][M] pairs, then the targets' logits.
+struct XentLossPlan {
+  XentTiles tiles;
+  size_t off_z, bytes;
+};
+inline XentLossPlan xent_loss_plan(int64_t M, int64_t N) {
+  XentLossPlan q{};
+  q.tiles = xent_tiles(M, N, M <= kXentFewRows ? 16 : 32);   // (MMAs of a pair: 16 a CTA)
+  q.off_z = static_cast<size_t>(xent_up(16 * static_cast<int64_t>(q.tiles.n_tiles) * M, 256));
+  q.bytes = q.off_z + static_cast<size_t>(4 * M);
+  return q;
+}
+
+// Workspace of the gradient: the rows of A that have a target (the others as
+// zeros; `terms` times below each other), dz of one piece of the vocabulary
+// (`terms` of M rows) and the f32 sums of dA.
+//
+// Pieces are as wide as kXentDzBytes allow, but at least kXentLeastPiece columns:
+// every piece adds its share of dA to all of it in memory, 8 bytes for 2 * width
+// operations.
+constexpr int64_t kXentDzBytes = int64_t{256} << 20;
+constexpr int64_t kXentLeastPiece = 8192;
+
+struct XentGradPlan {
+  int terms;          // of dz: 2 where the gradients are f32
+  int64_t piece;      // columns of a piece, a multiple of 256 (or all)
+  int64_t pieces;
+  int64_t ld_a, ld_dz, ld_sum;
+  size_t off_dz, off_sum, bytes;
+};
+inline XentGradPlan xent_grad_plan(int64_t M, int64_t N, int64_t K, bool bf16) {
+  XentGradPlan q{};
+  q.terms = bf16 ? 1 : 2;
+  int64_t most = kXentDzBytes / (2 * q.terms * M) / 256 * 256;
+  if (most < kXentLeastPiece) most = kXentLeastPiece;
+  q.pieces = (N + most - 1) / most;
+  q.piece = q.pieces == 1 ? N : xent_up((N + q.pieces - 1) / q.pieces, 256);
+  q.pieces = (N + q.piece - 1) / q.piece;
+  q.ld_a = xent_up(K, 64);
+  q.ld_dz = xent_up(q.piece, 64);
+  q.ld_sum = xent_up(K, 4);
+  q.off_dz = static_cast<size_t>(xent_up(2 * q.terms * M * q.ld_a, 1024));
+  q.off_sum = q.off_dz + static_cast<size_t>(xent_up(2 * q.terms * M * q.ld_dz, 1024));
+  q.bytes = q.off_sum + (bf16 && q.pieces > 1 ? static_cast<size_t>(4 * M * q.ld_sum) : 0);
+  return q;
+}
+
+}  // namespace tg

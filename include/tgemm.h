@@ -23,7 +23,8 @@
  *     library keeps its own device memory per (device, stream): a workspace
  *     (scale images of the block-scaled calls, gathered or re-pitched rows,
  *     the skinny call's f32 partial sums, histograms of tg_group_rows, the
- *     rank values of gemm_bf16_lora) and the tail split's scratch (see "Tail
+ *     rank values of gemm_bf16_lora, what the vocabulary loss, embed_rows_grad
+ *     and tg_balance_loss keep in between) and the tail split's scratch (see "Tail
  *     split"), which the grouped and adapter products use as well.  Calls on different streams never share it; it is never
  *     shrunk and lives until process exit.  The transpose allocates nothing.
  *   - Reserved workspace (see tg_reserve_workspace): after a reservation on a
@@ -389,8 +390,115 @@ int gemm_bf16_lora(const void* A, int64_t lda, const void* B, int64_t ldb, const
                    int d_dtype, const tg_epilogue* epi, unsigned flags, void* cuda_stream);
 
 /*
- * tg_call_packed -- one of the five calls above with its arguments as `count`
- * 64-bit words in order, pointers as addresses: for bindings to languages that
+ * The two ends of a language model's training step: its loss over a vocabulary,
+ * the rows of its tokens, and the balance of its router.  These calls take the
+ * current stream like all others; vectors (targets, ids, losses, ...) need only
+ * their type's alignment.  Results have the same bits every time, with one
+ * exception: gemm_bf16_xent_grad's products may be split as described above
+ * ("Products whose weights change with the row").
+ */
+
+/*
+ * gemm_bf16_xent -- softmax cross entropy of z = scale * A * B^T over B's rows
+ * (the vocabulary), without keeping z:
+ *   lse[i]  = log(sum_j exp z[i, j])
+ *   loss[i] = lse[i] - z[i, targets[i]], 0 where targets[i] is outside [0, N).
+ *   A       : device, bf16 [M, K], row stride lda (tokens).
+ *   B       : device, bf16 [N, K], row stride ldb.
+ *   targets : device, int32 [M].
+ *   scale   : positive and finite (a temperature's inverse); otherwise
+ *             TG_ERR_INVALID_ARG.
+ *   loss, lse : device, f32 [M].  flags: 0.
+ * M, N and K are at most 2^31 - 4096.  N = 0 gives lse = -inf; K = 0 gives
+ * lse = log N.  An infinite or NaN logit gives what the formulas give, in its own
+ * row.  Workspace: TG_CALL_GEMM_BF16_XENT.
+ */
+int gemm_bf16_xent(const void* A, int64_t lda, const void* B, int64_t ldb, const int32_t* targets,
+                   float scale, float* loss, float* lse, int64_t M, int64_t N, int64_t K,
+                   unsigned flags, void* cuda_stream);
+
+/*
+ * gemm_bf16_xent_grad -- the gradients of sum_i grad[i] * loss[i]:
+ *   dz[i, j] = grad[i] * scale * (exp(z[i, j] - lse[i]) - [j = targets[i]])
+ *   dA = dz * B,  dB = dz^T * A
+ * Rows without a target have dz = 0: their row of dA is 0 and they have no part in
+ * dB, whatever their row of A holds.  z is computed again in pieces of the
+ * vocabulary; dz passes to the products as bf16, for f32 gradients as two bf16
+ * terms (17 significant bits).
+ *   lse     : device, f32 [M], of gemm_bf16_xent with the same A, B and scale.
+ *   grad    : device, f32 [M], or NULL for 1.
+ *   dA      : device, [M, K] of d_dtype, row stride ldda, or NULL: not wanted.
+ *   dB      : device, [N, K] of d_dtype, row stride lddb, or NULL: not wanted.
+ * dA and dB must not overlap the inputs.  f32 gradients take M <= 2^30 - 2048.
+ * Workspace: TG_CALL_GEMM_BF16_XENT_GRAD (M rows of A and dz of a piece, 256 MiB
+ * or 8192 columns, once or, for f32, twice; M rows of f32 sums).
+ */
+int gemm_bf16_xent_grad(const void* A, int64_t lda, const void* B, int64_t ldb,
+                        const int32_t* targets, const float* lse, const float* grad, float scale,
+                        void* dA, int64_t ldda, void* dB, int64_t lddb, int64_t M, int64_t N,
+                        int64_t K, int d_dtype, unsigned flags, void* cuda_stream);
+
+/*
+ * embed_rows -- D[i, :] = scale * W[ids[i], :], zeros where ids[i] is outside
+ * [0, rows).
+ *   W   : device, bf16 [rows, K], row stride ldw.
+ *   ids : device, int32 [n], n <= 2^30.
+ *   D   : device, [n, K] of d_dtype, row stride ldd.
+ */
+int embed_rows(const void* W, int64_t ldw, int64_t rows, const int32_t* ids, int64_t n, int64_t K,
+               float scale, void* D, int64_t ldd, int d_dtype, void* cuda_stream);
+
+/*
+ * embed_rows_grad -- the gradient of the table of embed_rows:
+ *   D[v, :] = scale * sum of G[i, :] over the i with ids[i] = v
+ * for every row v of [0, rows) (zeros where there is none), or with accumulate = 1
+ * D[v, :] += that, which leaves rows without tokens as they are.  Sums are f32, in
+ * an order fixed by ids; D is rounded once.
+ *   G   : device, [n, K] of g_dtype (TG_D_F32 or TG_D_BF16), row stride ldg.
+ *   D   : device, [rows, K] of d_dtype, row stride ldd.
+ * n <= 2^30, rows <= 2^31 - 1.  Workspace: TG_CALL_EMBED_ROWS_GRAD.
+ */
+int embed_rows_grad(const void* G, int64_t ldg, int g_dtype, const int32_t* ids, int64_t n,
+                    int64_t rows, int64_t K, float scale, void* D, int64_t ldd, int d_dtype,
+                    int accumulate, void* cuda_stream);
+
+/*
+ * tg_balance_loss -- how unevenly a router spreads its tokens over E experts:
+ *   p[t, :]   = softmax(logits[t, :])
+ *   counts[e] = number of choices e among ids
+ *   shares[e] = E * counts[e] / (sum of counts * tokens)
+ *   loss      = sum_e shares[e] * sum_t p[t, e]
+ * over the `tokens` rows t with at least one choice inside [0, E); the others
+ * (padding) have no part.  An expert that is -inf in a row has p = 0 there; a row of
+ * nothing but -inf has p = 0 throughout.  Without a token everything is 0.
+ *   logits  : device, f32 or bf16 (dtype: TG_D_F32, TG_D_BF16) [M, E], row stride
+ *             ld >= E.  Any alignment of its type.
+ *   ids     : device, int32 [M, choices]: the experts of each token, as for
+ *             tg_group_rows.  1 <= choices <= 1024, M * choices < 2^31.
+ *   E       : 1 .. TG_MAX_GROUPS.
+ *   loss    : device, f32 [1].  counts: int32 [E].  shares: f32 [E].
+ * Workspace: TG_CALL_BALANCE_LOSS.
+ */
+int tg_balance_loss(const void* logits, int64_t ld, int dtype, const int32_t* ids, int64_t choices,
+                    int64_t M, int64_t E, float* loss, int32_t* counts, float* shares,
+                    void* cuda_stream);
+
+/*
+ * tg_balance_loss_grad -- its gradient, the counts being constants:
+ *   D[t, e] = grad * p[t, e] * (shares[e] - sum_f p[t, f] shares[f]),
+ * 0 in rows that are no token.
+ *   shares  : device, f32 [E], of tg_balance_loss (or any weights).
+ *   grad    : device, f32 [1], or NULL for 1.
+ *   D       : device, [M, E] of d_dtype, row stride ldd >= E.  D may be the logits
+ *             themselves where both have one type and stride.
+ */
+int tg_balance_loss_grad(const void* logits, int64_t ld, int dtype, const int32_t* ids,
+                         int64_t choices, int64_t M, int64_t E, const float* shares,
+                         const float* grad, void* D, int64_t ldd, int d_dtype, void* cuda_stream);
+
+/*
+ * tg_call_packed -- one of the calls named below with its arguments as `count`
+ * 64-bit words in order, pointers as addresses, floats as their 32 bits: for bindings to languages that
  * convert arguments one by one (Python's ctypes takes 2.3 us for the 23 of
  * gemm_bf16_lora, 0.5 us this way).  Returns what the call returns, or
  * TG_ERR_INVALID_ARG for an unknown `fn`, another count, or a word outside a
@@ -401,7 +509,13 @@ enum {
   TG_FN_GEMM_BF16_GROUPED = 1,
   TG_FN_GEMM_BF16_GROUPED_DGRAD = 2,
   TG_FN_GEMM_BF16_GROUPED_WGRAD = 3,
-  TG_FN_GEMM_BF16_LORA = 4
+  TG_FN_GEMM_BF16_LORA = 4,
+  TG_FN_GEMM_BF16_XENT = 5,
+  TG_FN_GEMM_BF16_XENT_GRAD = 6,
+  TG_FN_EMBED_ROWS = 7,
+  TG_FN_EMBED_ROWS_GRAD = 8,
+  TG_FN_BALANCE_LOSS = 9,
+  TG_FN_BALANCE_LOSS_GRAD = 10
 };
 int tg_call_packed(int fn, const int64_t* args, int count);
 
@@ -431,7 +545,11 @@ enum {
   TG_CALL_GEMM_BF16_GATHER = 5, /* gemm_bf16_gather (M = gathered rows), and the
                                    grouped products with a row_idx             */
   TG_CALL_GROUP_ROWS = 6,       /* tg_group_rows (M = n, N = groups, K = 1)    */
-  TG_CALL_GEMM_BF16_LORA = 7    /* gemm_bf16_lora (N = rank, K = 1)            */
+  TG_CALL_GEMM_BF16_LORA = 7,   /* gemm_bf16_lora (N = rank, K = 1)            */
+  TG_CALL_GEMM_BF16_XENT = 8,   /* gemm_bf16_xent                              */
+  TG_CALL_GEMM_BF16_XENT_GRAD = 9, /* gemm_bf16_xent_grad (d_dtype counts)     */
+  TG_CALL_EMBED_ROWS_GRAD = 10, /* embed_rows_grad (M = n, N = rows)           */
+  TG_CALL_BALANCE_LOSS = 11     /* tg_balance_loss (N = E, K = 1)              */
 };
 
 /*
