@@ -11,10 +11,13 @@
 //
 // Both directions read the logits once and are bound by HBM, short ones by the
 // chain of launches.  A row belongs to a group of lanes (a power of two, a whole
-// block from 513 experts on), each of which keeps its experts' p in registers and,
+// block from 513 experts on), each of which keeps 16 experts' p in registers and,
 // in the forward pass, their sums over the group's rows; those are added over a
-// block's groups as a tree and over the blocks by the one block of a second
-// kernel, always in the same order.
+// block's groups as a tree and over the blocks by one cluster of a second kernel,
+// always in the same order.  Few lanes with many experts each, not the reverse: a
+// row's maximum and sum cross the lanes of its group one step after the other (32
+// lanes with 8 experts each, read by 2 bytes: 65536 x 256 bf16 60 us forward, 47
+// backward).
 #include <type_traits>
 
 #include "tg_internal.h"
@@ -33,9 +36,11 @@ struct BalanceArgs {
   int64_t ld;
   const int* ids;       // [M][choices]
   int choices, M, E;
-  int lanes;            // of a row's group (warps: 1 .. 32)
   float* sums;          // [blocks][E]: sums of p
   int* counts_of;       // [blocks][E + 1]: choices of each expert; tokens
+  float* loss;          // results (one block alone writes them)
+  int* counts;
+  float* out_shares;
   // gradient
   const float* shares;  // [E]
   const float* grad;    // one value, or null for 1
@@ -43,342 +48,478 @@ struct BalanceArgs {
   int64_t ldd;
 };
 
+constexpr int kV = 16;               // experts of a lane
+constexpr int kThreads = 640;        // 20 warps of 96 registers
+constexpr int kBlockLanes = 256;     // of a row's group from 513 experts on: a block
+constexpr int kGroupExperts = 512;
+// Rows that a group takes together; the next ones' loads are in flight meanwhile.
 template <class T>
-__device__ __forceinline__ float value_of(const T* p) {
-  if constexpr (sizeof(T) == 2)
-    return __uint_as_float(static_cast<uint32_t>(*reinterpret_cast<const uint16_t*>(p)) << 16);
-  else
-    return *reinterpret_cast<const float*>(p);
+constexpr int rows_together() { return sizeof(T) == 2 ? 2 : 1; }
+
+// Threads of a block whose rows' groups have kLanes lanes.
+template <int kLanes>
+constexpr int block_threads() { return kLanes == kBlockLanes ? kBlockLanes : kThreads; }
+
+// The expert of a lane's i-th value.  kVec: 16 bytes at a time, the lanes side by
+// side; else one.
+template <class T, bool kVec, int kLanes>
+__device__ __forceinline__ int expert_of(int lane, int i) {
+  constexpr int kW = kVec ? 16 / static_cast<int>(sizeof(T)) : 1;
+  return (lane + i / kW * kLanes) * kW + i % kW;
 }
 
 __device__ __forceinline__ float no_logit() { return __uint_as_float(0xFF800000u); }
 
-// Softmax of a row spread over a group's lanes (experts lane, lane + lanes, ...):
-// z becomes p.  kBlock: the group is the block.
-template <bool kMax>
-__device__ __forceinline__ float over_block(float v, float* shared) {
-  const int warp = threadIdx.x >> 5;
+// This lane's logits of a row as they lie in memory (-inf past the last expert, and
+// without a row).
+template <class T>
+struct Logits {
+  uint32_t w[kV * sizeof(T) / 4];
+
+  template <bool kVec, int kLanes>
+  __device__ __forceinline__ void load(const T* row, bool in, int E, int lane) {
+    constexpr int kPer = 4 / static_cast<int>(sizeof(T));       // values of a word
+    constexpr uint32_t kNone = sizeof(T) == 4 ? 0xFF800000u : 0xFF80FF80u;
+    if constexpr (kVec) {
+      constexpr int kW = 4 * kPer;
 #pragma unroll
-  for (int d = 16; d > 0; d /= 2) {
+      for (int i = 0; i < kV; i += kW) {
+        const int e = expert_of<T, kVec, kLanes>(lane, i);
+        uint4 q = make_uint4(kNone, kNone, kNone, kNone);
+        if (in && e + kW <= E) {
+          q = *reinterpret_cast<const uint4*>(row + e);
+        } else if (in && e < E) {
+          uint32_t t[4] = {kNone, kNone, kNone, kNone};
+#pragma unroll
+          for (int j = 0; j < kW; ++j)
+            if (e + j < E) put(t[j / kPer], j % kPer, row + e + j);
+          q = make_uint4(t[0], t[1], t[2], t[3]);
+        }
+        w[i / kPer] = q.x;
+        w[i / kPer + 1] = q.y;
+        w[i / kPer + 2] = q.z;
+        w[i / kPer + 3] = q.w;
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < kV; ++i) {
+        if (i % kPer == 0) w[i / kPer] = kNone;
+        const int e = expert_of<T, kVec, kLanes>(lane, i);
+        if (in && e < E) put(w[i / kPer], i % kPer, row + e);
+      }
+    }
+  }
+  static __device__ __forceinline__ void put(uint32_t& word, int at, const T* p) {
+    if constexpr (sizeof(T) == 4)
+      word = *reinterpret_cast<const uint32_t*>(p);
+    else
+      word = (word & (at ? 0x0000FFFFu : 0xFFFF0000u)) |
+             static_cast<uint32_t>(*reinterpret_cast<const uint16_t*>(p)) << (16 * at);
+  }
+  __device__ __forceinline__ float value(int i) const {
+    if constexpr (sizeof(T) == 4)
+      return __uint_as_float(w[i]);
+    else
+      return __uint_as_float(i & 1 ? w[i / 2] & 0xFFFF0000u : w[i / 2] << 16);
+  }
+};
+
+// Maximum or sum over a group's lanes (kBlockLanes: over the block, through
+// `shared`), in every lane.
+template <bool kMax, int kLanes>
+__device__ __forceinline__ float over_group(float v, float* shared) {
+#pragma unroll
+  for (int d = (kLanes > 32 ? 32 : kLanes) / 2; d > 0; d /= 2) {
     const float o = __shfl_xor_sync(0xFFFFFFFFu, v, d);
     v = kMax ? fmaxf(v, o) : v + o;
   }
-  __syncthreads();   // (the last call's values are read)
-  if ((threadIdx.x & 31) == 0) shared[warp] = v;
-  __syncthreads();
-  v = shared[0];
-  for (int w = 1; w < static_cast<int>(blockDim.x) / 32; ++w)
-    v = kMax ? fmaxf(v, shared[w]) : v + shared[w];
+  if constexpr (kLanes > 32) {
+    __syncthreads();   // (the last call's values are read)
+    if ((threadIdx.x & 31) == 0) shared[threadIdx.x >> 5] = v;
+    __syncthreads();
+    v = shared[0];
+#pragma unroll
+    for (int w = 1; w < kLanes / 32; ++w) v = kMax ? fmaxf(v, shared[w]) : v + shared[w];
+  }
   return v;
 }
 
-template <bool kMax, bool kBlock>
-__device__ __forceinline__ float over_group(float v, int lanes, float* shared) {
-  if constexpr (kBlock) {
-    return over_block<kMax>(v, shared);
-  } else {
-    for (int d = lanes / 2; d > 0; d /= 2) {
-      const float o = __shfl_xor_sync(0xFFFFFFFFu, v, d);
-      v = kMax ? fmaxf(v, o) : v + o;
-    }
-    return v;
-  }
-}
-
-template <int kV, bool kBlock>
-__device__ __forceinline__ void softmax_row(float (&z)[kV], int lanes, float* shared) {
+// Softmax of a row spread over a group's lanes: z becomes exp(z - the largest), and
+// 1 / their sum is returned.
+template <int kLanes>
+__device__ __forceinline__ float softmax_row(float (&z)[kV], float* shared) {
+  constexpr float kLog2e = 1.4426950408889634f;
   float m = no_logit();
 #pragma unroll
   for (int i = 0; i < kV; ++i) m = fmaxf(m, z[i]);
-  m = over_group<true, kBlock>(m, lanes, shared);
+  m = over_group<true, kLanes>(m, shared);
   // Nothing but -inf: every exponential below is exp(-inf) = 0.
   const float ref = m == no_logit() ? 0.0f : m;
   float s = 0.0f;
 #pragma unroll
   for (int i = 0; i < kV; ++i) {
-    z[i] = expf(z[i] - ref);
+    // (The difference first: m log2(e) of the lowest f32 is none.)
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(z[i]) : "f"((z[i] - ref) * kLog2e));
     s += z[i];
   }
-  s = over_group<false, kBlock>(s, lanes, shared);
-  const float inv = m == no_logit() && s == 0.0f ? 0.0f : 1.0f / s;
-#pragma unroll
-  for (int i = 0; i < kV; ++i) z[i] *= inv;
+  s = over_group<false, kLanes>(s, shared);
+  return m == no_logit() && s == 0.0f ? 0.0f : __fdividef(1.0f, s);
 }
 
-// Rows that a group takes together, their loads in flight at the same time.
-template <int kV>
-constexpr int rows_together() { return kV >= 8 ? 1 : kV >= 4 ? 2 : 4; }
-
-// The walk over rows that both kernels share.  f(row, p, some): the row's p and
-// whether it is a token; count(id) for each choice inside.
-template <class T, int kV, bool kBlock, class F, class N>
+// The walk over rows that both kernels share.  f(row, e, inv, some): p is e inv, and
+// whether the row is a token; count(id) for each choice inside.
+template <class T, bool kVec, int kLanes, class F, class N>
 __device__ __forceinline__ void walk_rows(const BalanceArgs& p, float* shared, F f, N count) {
-  constexpr int kR = kBlock ? 1 : rows_together<kV>();
-  const int lanes = kBlock ? static_cast<int>(blockDim.x) : p.lanes;
-  const int lane = static_cast<int>(threadIdx.x) % lanes;
-  const int groups = static_cast<int>(blockDim.x) / lanes;
-  const int64_t all = static_cast<int64_t>(gridDim.x) * groups;
-  const int64_t mine = static_cast<int64_t>(blockIdx.x) * groups + threadIdx.x / lanes;
-  const T* logits = static_cast<const T*>(p.logits);
-  // Whole warps walk together (their shuffles and votes): as many steps for all.
-  const int64_t steps = (p.M + all * kR - 1) / (all * kR);
-  for (int64_t s = 0; s < steps; ++s) {
-    const int64_t r0 = (s * kR) * all + mine;
+  constexpr int kR = rows_together<T>();
+  constexpr int kGroups = block_threads<kLanes>() / kLanes;
+  const int lane = static_cast<int>(threadIdx.x) % kLanes;
+  const int all = static_cast<int>(gridDim.x) * kGroups;
+  const int mine = static_cast<int>(blockIdx.x) * kGroups + static_cast<int>(threadIdx.x) / kLanes;
+  const unsigned group =
+      kLanes >= 32 ? 0xFFFFFFFFu
+                   : ((1u << (kLanes & 31)) - 1u) << ((threadIdx.x & 31) / kLanes * kLanes);
+  // Rows mine, mine + all, ...; whole warps walk together (their shuffles and votes):
+  // as many steps for all.
+  const T* at = static_cast<const T*>(p.logits) + mine * p.ld;
+  const int64_t stride = all * p.ld;
+  Logits<T> next[kR];
+  auto load = [&](int64_t row) {
+#pragma unroll
+    for (int r = 0; r < kR; ++r) {
+      next[r].template load<kVec, kLanes>(at, row + static_cast<int64_t>(r) * all < p.M, p.E, lane);
+      at += stride;
+    }
+  };
+  load(mine);
+  for (int64_t first = mine; first - mine < p.M; first += static_cast<int64_t>(all) * kR) {
     float z[kR][kV];
     int some[kR];
 #pragma unroll
     for (int r = 0; r < kR; ++r) {
-      const int64_t row = r0 + r * all;
-#pragma unroll
-      for (int i = 0; i < kV; ++i) {
-        const int e = lane + i * lanes;
-        z[r][i] = row < p.M && e < p.E ? value_of(logits + row * p.ld + e) : no_logit();
-      }
+      const int64_t row = first + static_cast<int64_t>(r) * all;
       some[r] = 0;
       if (row < p.M)
-        for (int c = lane; c < p.choices; c += lanes) {
+        for (int c = lane; c < p.choices; c += kLanes) {
           const int id = p.ids[row * p.choices + c];
           if (static_cast<unsigned>(id) < static_cast<unsigned>(p.E)) {
             some[r] = 1;
             count(id);
           }
         }
+#pragma unroll
+      for (int i = 0; i < kV; ++i) z[r][i] = next[r].value(i);
     }
+    load(first + static_cast<int64_t>(all) * kR);
 #pragma unroll
     for (int r = 0; r < kR; ++r) {
-      const int64_t row = r0 + r * all;
-      int any;
-      if constexpr (kBlock) {
-        any = __syncthreads_or(some[r]);
-      } else {
-        const unsigned votes = __ballot_sync(0xFFFFFFFFu, some[r]);
-        const unsigned group = lanes == 32 ? 0xFFFFFFFFu : ((1u << lanes) - 1u)
-                                                               << ((threadIdx.x & 31) / lanes * lanes);
-        any = (votes & group) != 0;
-      }
-      softmax_row<kV, kBlock>(z[r], lanes, shared);
-      f(row, z[r], any != 0 && row < p.M, lane, lanes);
+      const int64_t row = first + static_cast<int64_t>(r) * all;
+      bool any;
+      if constexpr (kLanes == kBlockLanes)
+        any = __syncthreads_or(some[r]) != 0;
+      else
+        any = (__ballot_sync(0xFFFFFFFFu, some[r]) & group) != 0;
+      const float inv = softmax_row<kLanes>(z[r], shared);
+      f(row, z[r], inv, any && row < p.M);
     }
   }
 }
 
-template <class T, int kV, bool kBlock>
-__global__ void __launch_bounds__(kBlock ? 256 : 512) balance_sums_kernel(const BalanceArgs p) {
-  extern __shared__ float smem[];   // [E] counts, [1] tokens, then the tree's sums
-  __shared__ float warp_part[32];
-  int* hist = reinterpret_cast<int*>(smem);
-  float* tree = smem + p.E + 1;
-  for (int e = threadIdx.x; e <= p.E; e += blockDim.x) hist[e] = 0;
-  griddep_wait();
-  griddep_launch_dependents();
-  __syncthreads();
-  float sum[kV] = {};
-  walk_rows<T, kV, kBlock>(
-      p, warp_part,
-      [&](int64_t, const float (&q)[kV], bool some, int lane, int) {
-        if (!some) return;
-        if (lane == 0) atomicAdd(hist + p.E, 1);
-#pragma unroll
-        for (int i = 0; i < kV; ++i) sum[i] += q[i];
-      },
-      [&](int id) { atomicAdd(hist + id, 1); });   // (counts: any order gives them)
-  // Over the groups: halves of them add to the others until one is left.
-  const int lanes = kBlock ? static_cast<int>(blockDim.x) : p.lanes;
-  const int lane = static_cast<int>(threadIdx.x) % lanes;
-  const int group = static_cast<int>(threadIdx.x) / lanes;
-  for (int half = static_cast<int>(blockDim.x) / lanes / 2; half > 0; half /= 2) {
-    __syncthreads();
-    if (group >= half && group < 2 * half) {
-#pragma unroll
-      for (int i = 0; i < kV; ++i)
-        if (lane + i * lanes < p.E) tree[(group - half) * p.E + lane + i * lanes] = sum[i];
-    }
-    __syncthreads();
-    if (group < half) {
-#pragma unroll
-      for (int i = 0; i < kV; ++i)
-        if (lane + i * lanes < p.E) sum[i] += tree[group * p.E + lane + i * lanes];
-    }
+// The results, from every expert's sum of p and count (and the tokens behind them)
+// in shared memory.  By a whole block.
+__device__ __forceinline__ void finish_loss(const float* sum_of, const int* count_of, int E,
+                                            float* loss, int* counts, float* shares) {
+  __shared__ int choice_part[32];
+  __shared__ float loss_part[32];
+  const int tid = static_cast<int>(threadIdx.x), warp = tid >> 5, lane = tid & 31;
+  const int warps = static_cast<int>(blockDim.x) / 32;
+  int choices = 0;
+  for (int e = tid; e < E; e += blockDim.x) {
+    counts[e] = count_of[e];
+    choices += count_of[e];
   }
-  if (group == 0) {
-#pragma unroll
-    for (int i = 0; i < kV; ++i)
-      if (lane + i * lanes < p.E)
-        p.sums[static_cast<int64_t>(blockIdx.x) * p.E + lane + i * lanes] = sum[i];
-  }
-  __syncthreads();
-  for (int e = threadIdx.x; e <= p.E; e += blockDim.x)
-    p.counts_of[static_cast<int64_t>(blockIdx.x) * (p.E + 1) + e] = hist[e];
-}
-
-// One block: sums over the blocks, shares and the loss.
-__global__ void __launch_bounds__(1024) balance_join_kernel(const float* sums, const int* counts_of,
-                                                            int blocks, int E, float* loss,
-                                                            int* counts, float* shares) {
-  extern __shared__ float smem[];          // [parts][E] sums, [parts][E + 1] counts
-  __shared__ float part[32];
-  griddep_wait();
-  griddep_launch_dependents();
-  // A power of two of threads for each expert, as many as there are.
-  int width = 1;
-  while (width < E + 1 && width < 1024) width *= 2;
-  const int parts = 1024 / width;
-  float* sum_of = smem;
-  int* count_of = reinterpret_cast<int*>(smem + parts * E);
-  const int x = static_cast<int>(threadIdx.x) % width, q = static_cast<int>(threadIdx.x) / width;
-  for (int e = x; e <= E; e += width) {
-    float s = 0.0f;
-    int n = 0;
-#pragma unroll 8
-    for (int b = q; b < blocks; b += parts) {
-      if (e < E) s += __ldcg(sums + static_cast<int64_t>(b) * E + e);
-      n += __ldcg(counts_of + static_cast<int64_t>(b) * (E + 1) + e);
-    }
-    if (e < E) sum_of[q * E + e] = s;
-    count_of[q * (E + 1) + e] = n;
-  }
-  __syncthreads();
-  // Each expert's sum to the first part; the sum of all counts.
-  int mine = 0;
-  for (int e = threadIdx.x; e <= E; e += 1024) {
-    float s = e < E ? sum_of[e] : 0.0f;
-    int n = count_of[e];
-    for (int r = 1; r < parts; ++r) {
-      if (e < E) s += sum_of[r * E + e];
-      n += count_of[r * (E + 1) + e];
-    }
-    if (e < E) {
-      sum_of[e] = s;
-      counts[e] = n;
-      mine += n;
-    }
-    count_of[e] = n;
-  }
-  mine = __reduce_add_sync(0xFFFFFFFFu, mine);
-  __shared__ int whole[32];
-  if ((threadIdx.x & 31) == 0) whole[threadIdx.x >> 5] = mine;
+  choices = __reduce_add_sync(0xFFFFFFFFu, choices);
+  if (lane == 0) choice_part[warp] = choices;
   __syncthreads();
   int64_t total = 0;
-  for (int w = 0; w < 32; ++w) total += whole[w];
+  for (int w = 0; w < warps; ++w) total += choice_part[w];
   const int tokens = count_of[E];
   float l = 0.0f;
-  for (int e = threadIdx.x; e < E; e += 1024) {
+  for (int e = tid; e < E; e += blockDim.x) {
     // (In 64 bits: a count, and the product below, may pass 2^24.)
-    const float share = tokens > 0 ? static_cast<float>(static_cast<double>(E) * count_of[e] /
-                                                        (static_cast<double>(total) * tokens))
-                                   : 0.0f;
-    shares[e] = share;
-    l += share * sum_of[e];
+    const float s = tokens > 0 ? static_cast<float>(static_cast<double>(E) * count_of[e] /
+                                                    (static_cast<double>(total) * tokens))
+                               : 0.0f;
+    shares[e] = s;
+    l = fmaf(s, sum_of[e], l);
   }
 #pragma unroll
   for (int d = 16; d > 0; d /= 2) l += __shfl_xor_sync(0xFFFFFFFFu, l, d);
-  if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = l;
+  if (lane == 0) loss_part[warp] = l;
   __syncthreads();
-  if (threadIdx.x == 0) {
+  if (tid == 0) {
     l = 0.0f;
-    for (int w = 0; w < 32; ++w) l += part[w];
+    for (int w = 0; w < warps; ++w) l += loss_part[w];
     *loss = l;
   }
 }
 
-template <class T, class TD, int kV, bool kBlock>
-__global__ void __launch_bounds__(kBlock ? 256 : 512) balance_grad_kernel(const BalanceArgs p) {
+template <class T, bool kVec, int kLanes>
+__global__ void __launch_bounds__(block_threads<kLanes>(), 1)
+    balance_sums_kernel(const BalanceArgs p) {
+  extern __shared__ float smem[];   // [E] counts, [1] tokens, then the groups' sums
+  __shared__ float warp_part[32];
+  int* hist = reinterpret_cast<int*>(smem);
+  float* sums_of = smem + p.E + 1;
+  for (int e = threadIdx.x; e <= p.E; e += blockDim.x) hist[e] = 0;
+  griddep_wait();
+  griddep_launch_dependents();
+  __syncthreads();
+  const int lane = static_cast<int>(threadIdx.x) % kLanes;
+  float sum[kV] = {};
+  walk_rows<T, kVec, kLanes>(
+      p, warp_part,
+      [&](int64_t, const float (&e)[kV], float inv, bool some) {
+        if (!some) return;
+        if (lane == 0) atomicAdd(hist + p.E, 1);
+#pragma unroll
+        for (int i = 0; i < kV; ++i) sum[i] = fmaf(e[i], inv, sum[i]);
+      },
+      [&](int id) { atomicAdd(hist + id, 1); });   // (counts: any order gives them)
+  // Over the groups: all of their sums, then each expert's in order.
+  const int group = static_cast<int>(threadIdx.x) / kLanes;
+  constexpr int kGroups = block_threads<kLanes>() / kLanes;
+#pragma unroll
+  for (int i = 0; i < kV; ++i) {
+    const int e = expert_of<T, kVec, kLanes>(lane, i);
+    if (e < p.E) sums_of[group * p.E + e] = sum[i];
+  }
+  __syncthreads();
+  const bool alone = gridDim.x == 1;
+  for (int e = threadIdx.x; e < p.E; e += blockDim.x) {
+    float s[4] = {};
+    for (int g = 0; g < kGroups; g += 4) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (g + j < kGroups) s[j] += sums_of[(g + j) * p.E + e];
+    }
+    const float all = (s[0] + s[1]) + (s[2] + s[3]);
+    if (alone)
+      sums_of[e] = all;             // (this thread's own column)
+    else
+      p.sums[static_cast<int64_t>(blockIdx.x) * p.E + e] = all;
+  }
+  __syncthreads();
+  if (alone) {
+    finish_loss(sums_of, hist, p.E, p.loss, p.counts, p.out_shares);
+    return;
+  }
+  for (int e = threadIdx.x; e <= p.E; e += blockDim.x)
+    p.counts_of[static_cast<int64_t>(blockIdx.x) * (p.E + 1) + e] = hist[e];
+}
+
+// Sums over the blocks, and the results: by one cluster, an eighth of the experts to
+// each CTA, whose sums and counts the first one collects.  (One block of 1024
+// threads: 16 us for 152 blocks of 256 experts.)
+constexpr int kJoinCtas = 8;
+constexpr int kJoinThreads = 1024;
+
+__device__ __forceinline__ void st_cluster(uint32_t addr, uint32_t v) {
+  asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
+
+__global__ void __launch_bounds__(kJoinThreads)
+    balance_join_kernel(const float* sums, const int* counts_of, int blocks, int E, float* loss,
+                        int* counts, float* shares) {
+  extern __shared__ float smem[];            // of the first CTA: [E] sums, [E + 1] counts
+  __shared__ float sum_part[kJoinThreads];
+  __shared__ int count_part[kJoinThreads];
+  const int rank = static_cast<int>(cluster_ctarank());
+  const int tid = static_cast<int>(threadIdx.x);
+  const int share = (E + kJoinCtas) / kJoinCtas;          // of E + 1 counts, the tokens last
+  const int first = rank * share;
+  const int mine = min(E + 1 - first, share);             // (may be negative)
+  // A power of two of neighbouring threads for the experts, the others its parts.
+  int width = 1;
+  while (width < share && width < kJoinThreads) width *= 2;
+  const int parts = kJoinThreads / width;
+  const int x = tid % width, part = tid / width;
+  const uint32_t sum_dst = map_to_cta(smem_addr(smem), 0u);
+  const uint32_t count_dst = map_to_cta(smem_addr(smem + E), 0u);
+  cluster_sync();                            // (the first CTA is there)
+  griddep_wait();
+  griddep_launch_dependents();
+  for (int e0 = 0; e0 < share; e0 += width) {
+    const int e = first + e0 + x;
+    float s = 0.0f;
+    int n = 0;
+    if (e0 + x < mine) {
+#pragma unroll 10
+      for (int b = part; b < blocks; b += parts) {
+        if (e < E) s += __ldcg(sums + static_cast<int64_t>(b) * E + e);
+        n += __ldcg(counts_of + static_cast<int64_t>(b) * (E + 1) + e);
+      }
+    }
+    sum_part[tid] = s;
+    count_part[tid] = n;
+    __syncthreads();
+    for (int half = parts / 2; half > 0; half /= 2) {
+      if (part < half) {
+        sum_part[tid] += sum_part[tid + half * width];
+        count_part[tid] += count_part[tid + half * width];
+      }
+      __syncthreads();
+    }
+    if (part == 0 && e0 + x < mine) {
+      if (e < E) st_cluster(sum_dst + 4u * static_cast<uint32_t>(e), __float_as_uint(sum_part[tid]));
+      st_cluster(count_dst + 4u * static_cast<uint32_t>(e), static_cast<uint32_t>(count_part[tid]));
+    }
+    __syncthreads();
+  }
+  cluster_sync();
+  if (rank == 0)
+    finish_loss(smem, reinterpret_cast<const int*>(smem + E), E, loss, counts, shares);
+}
+
+// A lane's gradients of a row.
+template <class T, class TD, bool kVec, int kLanes>
+__device__ __forceinline__ void store_gradients(TD* row, int E, int lane, const float (&v)[kV]) {
+  // (Where the types differ in size, a lane's 16 bytes of one are 8 or 32 of the other.)
+  constexpr int kW = kVec ? 16 / static_cast<int>(sizeof(T)) : 1;
+#pragma unroll
+  for (int i = 0; i < kV; i += kW) {
+    const int e = expert_of<T, kVec, kLanes>(lane, i);
+    if (kVec && e + kW <= E) {
+      if constexpr (sizeof(TD) == 4) {
+#pragma unroll
+        for (int j = 0; j < kW; j += 4)
+          *reinterpret_cast<float4*>(row + e + j) =
+              make_float4(v[(i + j) % kV], v[(i + j + 1) % kV], v[(i + j + 2) % kV], v[(i + j + 3) % kV]);
+      } else {
+        uint32_t w[kW > 1 ? kW / 2 : 1];
+#pragma unroll
+        for (int j = 0; j + 1 < kW; j += 2) w[j / 2] = pack_bf16x2(v[i + j], v[(i + j + 1) % kV]);
+        if constexpr (kW == 8)
+          *reinterpret_cast<uint4*>(row + e) = make_uint4(w[0], w[1], w[2], w[3]);
+        else if constexpr (kW == 4)
+          *reinterpret_cast<uint2*>(row + e) = make_uint2(w[0], w[1]);
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < kW; ++j) {
+        if (e + j >= E) continue;
+        if constexpr (sizeof(TD) == 2)
+          *reinterpret_cast<uint16_t*>(row + e + j) =
+              static_cast<uint16_t>(pack_bf16x2(v[i + j], v[i + j]) & 0xFFFFu);
+        else
+          *reinterpret_cast<float*>(row + e + j) = v[i + j];
+      }
+    }
+  }
+}
+
+template <class T, class TD, bool kVec, int kLanes>
+__global__ void __launch_bounds__(block_threads<kLanes>(), 1)
+    balance_grad_kernel(const BalanceArgs p) {
   __shared__ float warp_part[32];
   griddep_wait();
   griddep_launch_dependents();
-  const int lanes = kBlock ? static_cast<int>(blockDim.x) : p.lanes;
-  const int lane0 = static_cast<int>(threadIdx.x) % lanes;
+  const int lane = static_cast<int>(threadIdx.x) % kLanes;
   const float g = p.grad ? *p.grad : 1.0f;
   float share[kV];
 #pragma unroll
-  for (int i = 0; i < kV; ++i) share[i] = lane0 + i * lanes < p.E ? p.shares[lane0 + i * lanes] : 0.0f;
-  walk_rows<T, kV, kBlock>(
+  for (int i = 0; i < kV; ++i) {
+    const int e = expert_of<T, kVec, kLanes>(lane, i);
+    share[i] = e < p.E ? p.shares[e] : 0.0f;
+  }
+  walk_rows<T, kVec, kLanes>(
       p, warp_part,
-      [&](int64_t row, const float (&q)[kV], bool some, int lane, int n) {
+      [&](int64_t row, const float (&e)[kV], float inv, bool some) {
         float dot = 0.0f;
 #pragma unroll
-        for (int i = 0; i < kV; ++i) dot += q[i] * share[i];
-        dot = over_group<false, kBlock>(dot, n, warp_part);
+        for (int i = 0; i < kV; ++i) dot = fmaf(e[i], share[i], dot);
+        dot = over_group<false, kLanes>(dot, warp_part) * inv;
         if (row >= p.M) return;
-        TD* d = static_cast<TD*>(p.D) + row * p.ldd;
+        const float w = g * inv;
+        float v[kV];
 #pragma unroll
-        for (int i = 0; i < kV; ++i) {
-          const int e = lane + i * n;
-          if (e >= p.E) continue;
-          const float v = some ? g * q[i] * (share[i] - dot) : 0.0f;
-          if constexpr (sizeof(TD) == 2)
-            *reinterpret_cast<uint16_t*>(d + e) = static_cast<uint16_t>(pack_bf16x2(v, v) & 0xFFFFu);
-          else
-            *reinterpret_cast<float*>(d + e) = v;
-        }
+        for (int i = 0; i < kV; ++i) v[i] = some ? w * e[i] * (share[i] - dot) : 0.0f;
+        store_gradients<T, TD, kVec, kLanes>(static_cast<TD*>(p.D) + row * p.ldd, p.E, lane, v);
       },
       [](int) {});
 }
 
 template <class... P>
-int launch_chained(void (*kern)(P...), int64_t blocks, int threads, size_t smem,
+int launch_chained(void (*kern)(P...), int64_t blocks, int threads, size_t smem, int cluster,
                    cudaStream_t stream, P... args) {
   cudaLaunchConfig_t cfg{};
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = static_cast<unsigned>(cluster);
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
   cfg.gridDim = dim3(static_cast<unsigned>(blocks), 1, 1);
   cfg.blockDim = dim3(static_cast<unsigned>(threads), 1, 1);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
   const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, args...);
   return e == cudaSuccess ? TG_OK : cuda_fail(e);
 }
 
-// Lanes of a row's group and values each keeps: 16 at most, a whole block (256
-// lanes) from 513 experts on.
-struct BalanceShape {
-  int lanes, values;
-  bool block;
-};
-BalanceShape balance_shape(int E) {
-  if (E > 512) return BalanceShape{256, 16, true};
+// Lanes of a row's group: 1, 4, 16 (up to 16, 64, 256 experts), 32 or a block.
+int balance_lanes(int E) {
+  if (E > kGroupExperts) return kBlockLanes;
   int lanes = 1;
-  while (lanes < 32 && lanes < E) lanes *= 2;
-  int values = 1;
-  while (values * lanes < E) values *= 2;
-  return BalanceShape{lanes, values, false};
+  while (lanes * kV < E) lanes *= 4;
+  return lanes < 32 ? lanes : 32;
 }
 
-// Blocks of a pass: a group takes at least one step of rows.
-constexpr int kSumBlocks = 152;
-int64_t balance_blocks(int64_t M, int E, int64_t most) {
-  const BalanceShape s = balance_shape(E);
-  const int64_t groups = s.block ? 1 : 512 / s.lanes;
-  const int64_t b = (M + groups - 1) / groups;
-  return b < most ? b : most;
+// Blocks of a pass: one on each of 152 SMs (more would be more sums to join), every
+// group taking at least a row; one alone while that takes its groups no more than
+// four rows (500 rows of 64 experts: a launch less).
+constexpr int64_t kMostBlocks = 152;
+int64_t balance_blocks(int64_t M, int E) {
+  const int lanes = balance_lanes(E);
+  const int64_t rows = lanes == kBlockLanes ? 1 : kThreads / lanes;
+  const int64_t b = (M + rows - 1) / rows;
+  return b <= 4 ? 1 : b < kMostBlocks ? b : kMostBlocks;
 }
 
+// Whether rows may be read (or written) 16 bytes at a time.
+bool whole_pieces(const void* p, int64_t ld, int dtype) {
+  return (reinterpret_cast<uintptr_t>(p) & 15u) == 0 && ld * (dtype == TG_D_BF16 ? 2 : 4) % 16 == 0;
+}
 
-template <class T, int kV, bool kBlock>
+template <class T, bool kVec, int kLanes>
 int launch_sums(const BalanceArgs& a, int64_t blocks, cudaStream_t stream) {
-  auto kern = balance_sums_kernel<T, kV, kBlock>;
-  const int threads = kBlock ? 256 : 512;
-  const int groups = kBlock ? 1 : threads / a.lanes;
-  // (18 KB at most: 512 experts in 16 groups)
-  const size_t smem = 4 * (static_cast<size_t>(a.E) + 1 + static_cast<size_t>(groups / 2) * a.E);
-  return launch_chained(kern, blocks, threads, smem, stream, a);
+  constexpr int threads = block_threads<kLanes>();
+  // (43 KB at most: 512 experts in 20 groups)
+  const size_t smem = 4 * (static_cast<size_t>(a.E) + 1 + static_cast<size_t>(threads / kLanes) * a.E);
+  return launch_chained(balance_sums_kernel<T, kVec, kLanes>, blocks, threads, smem, 1, stream, a);
 }
 
-// f(V, block) with the template arguments of E.
+template <class T, class TD, bool kVec, int kLanes>
+int launch_gradients(const BalanceArgs& a, int64_t blocks, cudaStream_t stream) {
+  return launch_chained(balance_grad_kernel<T, TD, kVec, kLanes>, blocks, block_threads<kLanes>(),
+                        0, 1, stream, a);
+}
+
+// f(16-byte pieces, lanes of a group) with both as template arguments.
 template <class F>
-int by_shape(int E, F f) {
-  const BalanceShape s = balance_shape(E);
-  if (s.block) return f(std::integral_constant<int, 16>{}, std::true_type{});
-  switch (s.values) {
-    case 1: return f(std::integral_constant<int, 1>{}, std::false_type{});
-    case 2: return f(std::integral_constant<int, 2>{}, std::false_type{});
-    case 4: return f(std::integral_constant<int, 4>{}, std::false_type{});
-    case 8: return f(std::integral_constant<int, 8>{}, std::false_type{});
-    default: return f(std::integral_constant<int, 16>{}, std::false_type{});
-  }
+int by_form(bool vec, int lanes, F f) {
+  auto with = [&](auto v) {
+    switch (lanes) {
+      case 1: return f(v, std::integral_constant<int, 1>{});
+      case 4: return f(v, std::integral_constant<int, 4>{});
+      case 16: return f(v, std::integral_constant<int, 16>{});
+      case 32: return f(v, std::integral_constant<int, 32>{});
+      default: return f(v, std::integral_constant<int, kBlockLanes>{});
+    }
+  };
+  return vec ? with(std::true_type{}) : with(std::false_type{});
 }
 
 int check_balance(const void* logits, int64_t ld, int dtype, const int32_t* ids, int64_t choices,
@@ -396,7 +537,7 @@ int check_balance(const void* logits, int64_t ld, int dtype, const int32_t* ids,
 }  // namespace
 
 size_t balance_workspace_bytes(int64_t, int64_t E) {
-  return static_cast<size_t>(kSumBlocks) * static_cast<size_t>(2 * E + 1) * 4u;
+  return static_cast<size_t>(kMostBlocks) * static_cast<size_t>(2 * E + 1) * 4u;
 }
 
 }  // namespace tg
@@ -412,7 +553,7 @@ int tg_balance_loss(const void* logits, int64_t ld, int dtype, const int32_t* id
   DeviceCtx* ctx = current_ctx();
   if (!ctx) return TG_ERR_CUDA;
   cudaStream_t stream = static_cast<cudaStream_t>(cuda_stream);
-  const int64_t blocks = balance_blocks(M, static_cast<int>(E), kSumBlocks);
+  const int64_t blocks = balance_blocks(M, static_cast<int>(E));
   float* sums = static_cast<float*>(device_workspace(balance_workspace_bytes(M, E), stream, &rc));
   if (sums == nullptr) return rc;
   BalanceArgs a{};
@@ -422,22 +563,20 @@ int tg_balance_loss(const void* logits, int64_t ld, int dtype, const int32_t* id
   a.choices = static_cast<int>(choices);
   a.M = static_cast<int>(M);
   a.E = static_cast<int>(E);
-  a.lanes = balance_shape(a.E).lanes;
   a.sums = sums;
   a.counts_of = reinterpret_cast<int*>(sums + blocks * E);
-  if (blocks > 0) {
-    rc = by_shape(a.E, [&](auto v, auto block) {
-      constexpr int kV = decltype(v)::value;
-      constexpr bool kBlock = decltype(block)::value;
-      return dtype == TG_D_BF16 ? launch_sums<uint16_t, kV, kBlock>(a, blocks, stream)
-                                : launch_sums<float, kV, kBlock>(a, blocks, stream);
-    });
-    if (rc != TG_OK) return rc;
-  }
-  int width = 1;
-  while (width < E + 1 && width < 1024) width *= 2;
-  const size_t smem = static_cast<size_t>(1024 / width) * static_cast<size_t>(2 * E + 1) * 4u;
-  return launch_chained(balance_join_kernel, 1, 1024, smem, stream,
+  a.loss = loss;
+  a.counts = counts;
+  a.out_shares = shares;
+  rc = by_form(whole_pieces(logits, ld, dtype), balance_lanes(a.E), [&](auto vec, auto lanes) {
+    constexpr bool kVec = decltype(vec)::value;
+    constexpr int kLanes = decltype(lanes)::value;
+    return dtype == TG_D_BF16 ? launch_sums<uint16_t, kVec, kLanes>(a, blocks, stream)
+                              : launch_sums<float, kVec, kLanes>(a, blocks, stream);
+  });
+  if (rc != TG_OK || blocks == 1) return rc;
+  return launch_chained(balance_join_kernel, kJoinCtas, kJoinThreads,
+                        4 * static_cast<size_t>(2 * E + 1), kJoinCtas, stream,
                         static_cast<const float*>(a.sums), static_cast<const int*>(a.counts_of),
                         static_cast<int>(blocks), a.E, loss, counts, shares);
 }
@@ -460,28 +599,20 @@ int tg_balance_loss_grad(const void* logits, int64_t ld, int dtype, const int32_
   a.choices = static_cast<int>(choices);
   a.M = static_cast<int>(M);
   a.E = static_cast<int>(E);
-  a.lanes = balance_shape(a.E).lanes;
   a.shares = shares;
   a.grad = grad;
   a.D = D;
   a.ldd = ldd;
-  const int64_t blocks = balance_blocks(M, a.E, 4 * static_cast<int64_t>(ctx->num_sms));
-  return by_shape(a.E, [&](auto v, auto block) {
-    constexpr int kV = decltype(v)::value;
-    constexpr bool kBlock = decltype(block)::value;
-    const int threads = kBlock ? 256 : 512;
+  const int64_t blocks = balance_blocks(M, a.E);
+  const bool whole = whole_pieces(logits, ld, dtype) && whole_pieces(D, ldd, d_dtype);
+  return by_form(whole, balance_lanes(a.E), [&](auto vec, auto lanes) {
+    constexpr bool kVec = decltype(vec)::value;
+    constexpr int kLanes = decltype(lanes)::value;
     const bool in16 = dtype == TG_D_BF16, out16 = d_dtype == TG_D_BF16;
-    if (in16 && out16)
-      return launch_chained(balance_grad_kernel<uint16_t, uint16_t, kV, kBlock>, blocks, threads, 0,
-                            stream, a);
-    if (in16)
-      return launch_chained(balance_grad_kernel<uint16_t, float, kV, kBlock>, blocks, threads, 0,
-                            stream, a);
-    if (out16)
-      return launch_chained(balance_grad_kernel<float, uint16_t, kV, kBlock>, blocks, threads, 0,
-                            stream, a);
-    return launch_chained(balance_grad_kernel<float, float, kV, kBlock>, blocks, threads, 0, stream,
-                          a);
+    if (in16 && out16) return launch_gradients<uint16_t, uint16_t, kVec, kLanes>(a, blocks, stream);
+    if (in16) return launch_gradients<uint16_t, float, kVec, kLanes>(a, blocks, stream);
+    if (out16) return launch_gradients<float, uint16_t, kVec, kLanes>(a, blocks, stream);
+    return launch_gradients<float, float, kVec, kLanes>(a, blocks, stream);
   });
 }
 

@@ -25,6 +25,7 @@ namespace {
 
 constexpr int64_t kMaxDim = (int64_t{1} << 31) - 1;
 constexpr int64_t kMaxTokens = int64_t{1} << 30;   // as tg_group_rows
+constexpr int64_t kMostColumns = int64_t{256} * 65535;
 
 template <class K, class... T>
 int launch_chained(K kern, int64_t blocks, int threads, cudaStream_t stream, T... args) {
@@ -41,42 +42,48 @@ int launch_chained(K kern, int64_t blocks, int threads, cudaStream_t stream, T..
   return e == cudaSuccess ? TG_OK : cuda_fail(e);
 }
 
-// Eight values of a row, from column k on; what lies past column K is neither
-// read nor written.
+// Eight values of a row, from column k on, as they lie in memory; what lies past
+// column K is neither read nor written.
 template <class T>
-__device__ __forceinline__ void load8(const T* row, int k, int K, float (&v)[8]) {
-  if constexpr (sizeof(T) == 2) {
-    uint4 q = make_uint4(0u, 0u, 0u, 0u);
+struct Eight {
+  uint4 q[sizeof(T) / 2];
+
+  __device__ __forceinline__ void load(const T* row, int k, int K) {
+    constexpr int kPer = 16 / static_cast<int>(sizeof(T));
     if (k + 8 <= K) {
-      q = __ldcs(reinterpret_cast<const uint4*>(row + k));
+#pragma unroll
+      for (int h = 0; h < static_cast<int>(sizeof(T)) / 2; ++h)
+        q[h] = __ldcs(reinterpret_cast<const uint4*>(row + k + kPer * h));
     } else {
-      uint32_t w[4] = {0u, 0u, 0u, 0u};
-      for (int e = 0; k + e < K; ++e) w[e / 2] |= static_cast<uint32_t>(row[k + e]) << (16 * (e & 1));
-      q = make_uint4(w[0], w[1], w[2], w[3]);
-    }
-    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+      uint32_t w[4 * sizeof(T) / 2] = {};
 #pragma unroll
-    for (int e = 0; e < 8; ++e)
-      v[e] = __uint_as_float(e & 1 ? w[e / 2] & 0xFFFF0000u : w[e / 2] << 16);
-  } else {
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      float4 q = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-      if (k + 4 * h + 4 <= K) {
-        q = __ldcs(reinterpret_cast<const float4*>(row + k + 4 * h));
-      } else {
-        float t[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          if (k + 4 * h + e < K) t[e] = row[k + 4 * h + e];
-        q = make_float4(t[0], t[1], t[2], t[3]);
+      for (int e = 0; e < 7; ++e) {
+        if (k + e >= K) continue;
+        if constexpr (sizeof(T) == 2)
+          w[e / 2] |= static_cast<uint32_t>(row[k + e]) << (16 * (e & 1));
+        else
+          w[e] = __float_as_uint(row[k + e]);
       }
-      v[4 * h] = q.x;
-      v[4 * h + 1] = q.y;
-      v[4 * h + 2] = q.z;
-      v[4 * h + 3] = q.w;
+#pragma unroll
+      for (int h = 0; h < static_cast<int>(sizeof(T)) / 2; ++h)
+        q[h] = make_uint4(w[4 * h], w[4 * h + 1], w[4 * h + 2], w[4 * h + 3]);
     }
   }
+  __device__ __forceinline__ float value(int e) const {
+    const uint4& p = q[e * static_cast<int>(sizeof(T)) / 16];
+    const int i = sizeof(T) == 2 ? e / 2 : e % 4;
+    const uint32_t w = i == 0 ? p.x : i == 1 ? p.y : i == 2 ? p.z : p.w;
+    if constexpr (sizeof(T) == 2) return __uint_as_float(e & 1 ? w & 0xFFFF0000u : w << 16);
+    return __uint_as_float(w);
+  }
+};
+
+template <class T>
+__device__ __forceinline__ void load8(const T* row, int k, int K, float (&v)[8]) {
+  Eight<T> r;
+  r.load(row, k, K);
+#pragma unroll
+  for (int e = 0; e < 8; ++e) v[e] = r.value(e);
 }
 
 template <class T>
@@ -85,10 +92,13 @@ __device__ __forceinline__ void store8(T* row, int k, int K, const float (&v)[8]
     uint32_t w[4];
 #pragma unroll
     for (int e = 0; e < 4; ++e) w[e] = pack_bf16x2(v[2 * e], v[2 * e + 1]);
-    if (k + 8 <= K)
+    if (k + 8 <= K) {
       __stcs(reinterpret_cast<uint4*>(row + k), make_uint4(w[0], w[1], w[2], w[3]));
-    else
-      for (int e = 0; k + e < K; ++e) row[k + e] = static_cast<T>(w[e / 2] >> (16 * (e & 1)));
+    } else {
+#pragma unroll
+      for (int e = 0; e < 7; ++e)
+        if (k + e < K) row[k + e] = static_cast<T>(w[e / 2] >> (16 * (e & 1)));
+    }
   } else {
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
@@ -156,14 +166,18 @@ struct EmbedGradArgs {
   float scale;
   void* D;
   int64_t ldd;
+  int* note_count;        // runs to be joined, zero before; for each a note:
+  int2* notes;            // its first chunk, its first slice (long runs: -1 - slice)
   float* parts;           // [chunk][2][ldp]: sums of a chunk's first and last run
   int64_t ldp;
-  int chunk;              // sorted rows per block
-  int chunks, slices;     // blocks of sums: chunks x slices of kSlice columns
+  int chunk;              // sorted rows per warp, a multiple of kBatch
+  int chunks, slices;     // warps of sums: chunks x slices of kSlice columns
 };
 
-constexpr int kSlice = 1024;      // columns of a block: 128 threads x 8
+constexpr int kSlice = 256;       // columns of a warp
+constexpr int kWarps = 4;         // of a block, each with a slice of its own
 constexpr int kBatch = 8;         // rows loaded together
+constexpr int kLongRun = 32;      // chunks, from which on a whole block joins a slice
 
 // The finished sum of an id's rows.
 template <class TD, bool kAdd>
@@ -180,117 +194,185 @@ __device__ __forceinline__ void finish_run(const EmbedGradArgs& p, int id, int k
   store8(d, k, p.K, v);
 }
 
+// Untiled bulk copy shared -> global (16-byte aligned, size % 16 == 0).
+__device__ __forceinline__ void bulk_store(void* dst, uint32_t src, uint32_t bytes) {
+  asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(src),
+               "r"(bytes)
+               : "memory");
+}
+
+// Rows that no token has, a thread each, as bulk copies of zeros: 1 GB of them by
+// 16-byte stores of whole warps, in blocks behind those of the sums, took 260 us
+// with the sums of 32768 rows x 4096 in 128000.
+constexpr int kZeros = 8192;      // bytes
+
+template <class TD>
+__device__ __forceinline__ void clear_unused(const EmbedGradArgs& p, int64_t block, int64_t blocks) {
+  __shared__ __align__(128) uint4 zeros[kZeros / 16];
+  for (int i = threadIdx.x; i < kZeros / 16; i += blockDim.x) zeros[i] = make_uint4(0u, 0u, 0u, 0u);
+  fence_proxy_async_smem();
+  __syncthreads();
+  const uint32_t src = smem_addr(zeros);
+  const int64_t bytes = static_cast<int64_t>(p.K) * sizeof(TD);
+  const int64_t whole = bytes / 16 * 16;
+  // (Rows far apart: a block's copies go out one after the other, and a small
+  // table needs many blocks.)
+  for (int64_t v = block + threadIdx.x * blocks; v < p.vocab; v += blocks * blockDim.x) {
+    if (p.n > 0 && (__ldcg(p.marks + (v >> 5)) >> (v & 31)) & 1u) continue;
+    uint8_t* d = reinterpret_cast<uint8_t*>(static_cast<TD*>(p.D) + v * p.ldd);
+    for (int64_t at = 0; at < whole; at += kZeros)
+      bulk_store(d + at, src, static_cast<uint32_t>(whole - at < kZeros ? whole - at : kZeros));
+    for (int64_t at = whole; at < bytes; at += sizeof(TD)) *reinterpret_cast<TD*>(d + at) = 0;
+  }
+  bulk_commit_group();
+  bulk_wait_group0();
+}
+
+// Blocks of sums (a warp has a chunk of the rows and a slice of the columns) and
+// blocks of zeros, evenly mixed: sums wait for memory's answers, zeros only for its
+// room.
 template <class TG, class TD, bool kAdd>
-__global__ void __launch_bounds__(128) sum_runs_kernel(const EmbedGradArgs p) {
+__global__ void __launch_bounds__(32 * kWarps) sum_runs_kernel(const EmbedGradArgs p) {
   griddep_wait();
   griddep_launch_dependents();
-  const int64_t sums = static_cast<int64_t>(p.chunks) * p.slices;
-  if (static_cast<int64_t>(blockIdx.x) >= sums) {
-    // Rows that no token has, a warp each.
-    const int lane = static_cast<int>(threadIdx.x & 31);
-    const int64_t warps = (gridDim.x - sums) * 4;
-    const float zero[8] = {};
-    for (int64_t v = (blockIdx.x - sums) * 4 + (threadIdx.x >> 5); v < p.vocab; v += warps) {
-      if (p.n > 0 && (__ldcg(p.marks + (v >> 5)) >> (v & 31)) & 1u) continue;
-      TD* d = static_cast<TD*>(p.D) + v * p.ldd;
-      for (int k = 8 * lane; k < p.K; k += 256) store8(d, k, p.K, zero);
-    }
+  const int64_t items = static_cast<int64_t>(p.chunks) * p.slices;
+  const int64_t zeros = gridDim.x - (items + kWarps - 1) / kWarps;
+  const int64_t before = blockIdx.x * zeros / gridDim.x;      // blocks of zeros
+  if ((blockIdx.x + 1) * zeros / gridDim.x > before) {
+    clear_unused<TD>(p, before, zeros);
     return;
   }
-  const int c = static_cast<int>(blockIdx.x) / p.slices;
-  const int k = (static_cast<int>(blockIdx.x) - c * p.slices) * kSlice +
-                8 * static_cast<int>(threadIdx.x);
-  if (k >= p.K) return;
+  const int64_t item = (blockIdx.x - before) * kWarps + (threadIdx.x >> 5);
+  if (item >= items) return;
+  const int lane = static_cast<int>(threadIdx.x & 31);
+  const int c = static_cast<int>(item / p.slices);
+  const int k = static_cast<int>(item - static_cast<int64_t>(c) * p.slices) * kSlice + 8 * lane;
+  const bool in = k < p.K;
   const int lo = c * p.chunk;
   const int hi = p.n - lo > p.chunk ? lo + p.chunk : p.n;
   const TG* G = static_cast<const TG*>(p.G);
-  int id = p.sorted[lo];
-  if (id < 0) return;
   // The first run may have begun in an earlier chunk: then its sum is a part.
+  int id = p.sorted[lo];
   bool whole = lo == 0 || p.sorted[lo - 1] != id;
+  const int behind = hi < p.n ? p.sorted[hi] : -1;
   float sum[8] = {};
-  for (int j0 = lo; j0 < hi; j0 += kBatch) {
-    int row[kBatch], of[kBatch];
+  for (int j0 = lo; j0 < hi && id >= 0; j0 += 32) {
+    // 32 rows and their ids, a lane each, for the warp's shuffles.
+    const int ids = j0 + lane < hi ? p.sorted[j0 + lane] : -1;
+    const int rows = j0 + lane < hi ? p.order[j0 + lane] : 0;
+    const int valid = __popc(__ballot_sync(0xFFFFFFFFu, ids >= 0));   // (sorted: the first ones)
+#pragma unroll 1
+    for (int u0 = 0; u0 < valid; u0 += kBatch) {
+      Eight<TG> v[kBatch];
 #pragma unroll
-    for (int u = 0; u < kBatch; ++u) {
-      of[u] = j0 + u < hi ? p.sorted[j0 + u] : -1;
-      row[u] = of[u] >= 0 ? p.order[j0 + u] : 0;
-    }
-    float v[kBatch][8];
-#pragma unroll
-    for (int u = 0; u < kBatch; ++u)
-      if (of[u] >= 0) load8(G + row[u] * p.ldg, k, p.K, v[u]);
-#pragma unroll
-    for (int u = 0; u < kBatch; ++u) {
-      if (j0 + u >= hi) break;
-      if (of[u] != id) {
-        if (whole)
-          finish_run<TD, kAdd>(p, id, k, sum);
-        else
-          store8(p.parts + 2LL * c * p.ldp, k, p.K, sum);
-        id = of[u];
-        if (id < 0) return;   // the rest has no id
-        whole = true;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) sum[e] = 0.0f;
+      for (int u = 0; u < kBatch; ++u) {
+        const int row = __shfl_sync(0xFFFFFFFFu, rows, u0 + u);
+        if (in && u0 + u < valid) v[u].load(G + row * p.ldg, k, p.K);
       }
 #pragma unroll
-      for (int e = 0; e < 8; ++e) sum[e] += v[u][e];
+      for (int u = 0; u < kBatch; ++u) {
+        const int of = __shfl_sync(0xFFFFFFFFu, ids, u0 + u);
+        if (u0 + u >= valid) break;
+        if (of != id) {
+          if (in) {
+            if (whole)
+              finish_run<TD, kAdd>(p, id, k, sum);
+            else
+              store8(p.parts + 2LL * c * p.ldp, k, p.K, sum);
+          }
+          id = of;
+          whole = true;
+#pragma unroll
+          for (int e = 0; e < 8; ++e) sum[e] = 0.0f;
+        }
+#pragma unroll
+        for (int e = 0; e < 8; ++e) sum[e] += v[u].value(e);
+      }
     }
   }
-  const bool goes_on = hi < p.n && p.sorted[hi] == id;
-  if (whole && !goes_on)
+  if (id < 0) return;
+  if (whole && behind == id && lane == 0) {
+    // The run goes on: one note for eight slices, or for each of a long run.
+    const int64_t far = lo + static_cast<int64_t>(kLongRun) * p.chunk;
+    const bool is_long = far < p.n && p.sorted[far] == id;
+    const int slice = static_cast<int>(item - static_cast<int64_t>(c) * p.slices);
+    if (is_long || slice % 8 == 0) {
+      p.notes[atomicAdd(p.note_count, 1)] = make_int2(c, is_long ? -1 - slice : slice);
+    }
+  }
+  if (!in) return;
+  if (whole && behind != id)
     finish_run<TD, kAdd>(p, id, k, sum);
   else
     store8(p.parts + (2LL * c + (whole ? 1 : 0)) * p.ldp, k, p.K, sum);
 }
 
-// Runs that cross the end of the chunk they begin in: the last part of that
-// chunk and the first of each further one, eight warps in turn, then the warps'
-// sums in order.
+// Runs that cross the end of the chunk they begin in, as noted by their first
+// chunk: its last part and the first of each further one.  A short run's parts are
+// added one after the other, a slice to each warp; a long one's slice by the block's
+// eight warps in turn, whose sums are then added in order.  (The notes' order is
+// chance, what each gives is not.)
 template <class TD, bool kAdd>
 __global__ void __launch_bounds__(256) join_runs_kernel(const EmbedGradArgs p) {
   __shared__ float shared[8][32][8];
   griddep_wait();
   griddep_launch_dependents();
-  const int c = static_cast<int>(blockIdx.x);
-  const int64_t lo = static_cast<int64_t>(c) * p.chunk;
-  const int64_t end = lo + p.chunk;   // (there is a chunk behind this one)
-  const int id = p.sorted[end - 1];
-  if (id < 0 || p.sorted[end] != id) return;
-  if (p.sorted[lo] == id && c > 0 && p.sorted[lo - 1] == id) return;   // begun before
   const int lane = static_cast<int>(threadIdx.x & 31), warp = static_cast<int>(threadIdx.x >> 5);
-  // The chunk in which the run ends.
-  int last = c + 1;
-  for (;; last += 32) {
-    const int64_t behind = static_cast<int64_t>(last + lane + 1) * p.chunk;
-    const unsigned over =
-        __ballot_sync(0xFFFFFFFFu, behind >= p.n || p.sorted[behind < p.n ? behind : 0] != id);
-    if (over) {
-      last += __ffs(over) - 1;
-      break;
+  const int notes = __ldcg(p.note_count);
+  for (int i = blockIdx.x; i < notes; i += gridDim.x) {
+    const int2 note = __ldcg(p.notes + i);
+    const int c = note.x, code = note.y;
+    auto id_behind = [&](int chunk) {
+      const int64_t behind = static_cast<int64_t>(chunk + 1) * p.chunk;
+      return behind < p.n ? p.sorted[behind] : -1;
+    };
+    const int id = id_behind(c);
+    int last = c + 1;               // the chunk in which the run ends
+    for (;;) {
+      const unsigned over = __ballot_sync(0xFFFFFFFFu, id_behind(last + lane) != id);
+      if (over) {
+        last += __ffs(over) - 1;
+        break;
+      }
+      last += 32;
     }
-  }
-  const int count = last - c + 1;
-  const int k = static_cast<int>(blockIdx.y) * 256 + 8 * lane;
-  float sum[8] = {};
-  if (k < p.K) {
+    const int count = last - c + 1;
     const int64_t step = 2 * p.ldp;
-    for (int q = warp; q < count; q += 8) {
-      float v[8];
-      load8(p.parts + (c + q) * step + (q == 0 ? p.ldp : 0), k, p.K, v);
+    const float* parts = p.parts + c * step;
+    const bool is_long = code < 0;
+    const int k = (is_long ? -1 - code : code + warp) * kSlice + 8 * lane;
+    // Parts from, from + by, ..., eight in flight.
+    const int from = is_long ? warp : 0, by = is_long ? 8 : 1;
+    float sum[8] = {};
+    if (k < p.K) {
+      for (int q0 = from; q0 < count; q0 += 8 * by) {
+        Eight<float> v[8];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) sum[e] += v[e];
+        for (int u = 0; u < 8; ++u) {
+          const int q = q0 + u * by;
+          if (q < count) v[u].load(parts + q * step + (q == 0 ? p.ldp : 0), k, p.K);
+        }
+#pragma unroll
+        for (int u = 0; u < 8; ++u)
+          if (q0 + u * by < count) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) sum[e] += v[u].value(e);
+          }
+      }
     }
+    if (is_long) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) shared[warp][lane][e] = sum[e];
+      __syncthreads();
+      if (warp == 0) {
+        for (int w = 1; w < 8; ++w)
+#pragma unroll
+          for (int e = 0; e < 8; ++e) sum[e] += shared[w][lane][e];
+      }
+      __syncthreads();
+    }
+    if (k < p.K && (!is_long || warp == 0)) finish_run<TD, kAdd>(p, id, k, sum);
   }
-#pragma unroll
-  for (int e = 0; e < 8; ++e) shared[warp][lane][e] = sum[e];
-  __syncthreads();
-  if (warp != 0 || k >= p.K) return;
-  for (int w = 1; w < 8 && w < count; ++w)
-#pragma unroll
-    for (int e = 0; e < 8; ++e) sum[e] += shared[w][lane][e];
-  finish_run<TD, kAdd>(p, id, k, sum);
 }
 
 // Sorted rows per block: about a thousand chunks, so that a run as long as all of
@@ -301,15 +383,18 @@ int grad_chunk(int64_t n) {
   return static_cast<int>(c);
 }
 
+constexpr size_t kNoteCount = 256;   // bytes
+
 struct EmbedPlan {
-  int chunk, chunks;
+  int chunk, chunks, slices;
   int64_t ldp;
-  size_t other, sorted, count, marks, hist, parts, bytes;
+  size_t other, sorted, count, notes, marks, hist, parts, bytes;   // (marks: the count before)
 };
 EmbedPlan embed_plan(int64_t n, int64_t rows, int64_t K) {
   EmbedPlan q{};
   q.chunk = grad_chunk(n);
   q.chunks = static_cast<int>((n + q.chunk - 1) / q.chunk);
+  q.slices = static_cast<int>((K + kSlice - 1) / kSlice);
   q.ldp = (K + 7) / 8 * 8;
   size_t at = 0;
   auto take = [&](size_t bytes) {
@@ -322,7 +407,8 @@ EmbedPlan embed_plan(int64_t n, int64_t rows, int64_t K) {
   q.other = take(list);
   q.sorted = take(list);
   q.count = take(4 * ((size_t{1} << kSortDigit) + 1));
-  q.marks = take(static_cast<size_t>((rows + 31) / 32 * 4));
+  q.notes = take(8 * static_cast<size_t>(q.chunks) * static_cast<size_t>(q.slices));
+  q.marks = take(kNoteCount + static_cast<size_t>((rows + 31) / 32 * 4));
   q.hist = take(sort_ids_workspace_bytes(n));
   q.parts = take(q.chunks > 1 ? static_cast<size_t>(8 * q.chunks) * static_cast<size_t>(q.ldp) : 0);
   q.bytes = at;
@@ -333,25 +419,18 @@ template <class TG, class TD, bool kAdd>
 int launch_grad(const EmbedGradArgs& a, DeviceCtx* ctx, cudaStream_t stream) {
   int64_t zero_blocks = 0;
   if (!kAdd) {
-    zero_blocks = (a.vocab + 3) / 4;
-    const int64_t most = 16 * static_cast<int64_t>(ctx->num_sms);
+    zero_blocks = (static_cast<int64_t>(a.vocab) + 7) / 8;
+    const int64_t most = 8 * static_cast<int64_t>(ctx->num_sms);
     if (zero_blocks > most) zero_blocks = most;
   }
-  const int64_t blocks = static_cast<int64_t>(a.chunks) * a.slices + zero_blocks;
+  const int64_t blocks =
+      (static_cast<int64_t>(a.chunks) * a.slices + kWarps - 1) / kWarps + zero_blocks;
   if (blocks == 0) return TG_OK;
-  int rc = launch_chained(sum_runs_kernel<TG, TD, kAdd>, blocks, 128, stream, a);
+  int rc = launch_chained(sum_runs_kernel<TG, TD, kAdd>, blocks, 32 * kWarps, stream, a);
   if (rc != TG_OK || a.chunks < 2) return rc;
-  cudaLaunchConfig_t cfg{};
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.gridDim = dim3(static_cast<unsigned>(a.chunks - 1), static_cast<unsigned>((a.K + 255) / 256));
-  cfg.blockDim = dim3(256);
-  cfg.stream = stream;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, join_runs_kernel<TD, kAdd>, a);
-  return e == cudaSuccess ? TG_OK : cuda_fail(e);
+  const int64_t notes = static_cast<int64_t>(a.chunks - 1) * a.slices;
+  const int64_t most = 4 * static_cast<int64_t>(ctx->num_sms);
+  return launch_chained(join_runs_kernel<TD, kAdd>, notes < most ? notes : most, 256, stream, a);
 }
 
 template <class TG, class TD>
@@ -371,8 +450,7 @@ int check_embed(int64_t n, int64_t rows, int64_t K, int a_dtype, int d_dtype) {
     return TG_ERR_INVALID_ARG;
   if (a_dtype != TG_D_F32 && a_dtype != TG_D_BF16) return TG_ERR_INVALID_ARG;
   if (d_dtype != TG_D_F32 && d_dtype != TG_D_BF16) return TG_ERR_INVALID_ARG;
-  // Blocks of a launch: slices of columns in its second dimension.
-  if (K > int64_t{256} * 65535) return TG_ERR_UNSUPPORTED;
+  if (K > kMostColumns) return TG_ERR_UNSUPPORTED;
   return TG_OK;
 }
 
@@ -440,16 +518,17 @@ int embed_rows_grad(const void* G, int64_t ldg, int g_dtype, const int32_t* ids,
   a.ldd = ldd;
   if (n > 0) {
     const EmbedPlan plan = embed_plan(n, rows, K);
-    if (static_cast<int64_t>(plan.chunks) * ((K + kSlice - 1) / kSlice) > kMaxDim / 2)
-      return TG_ERR_UNSUPPORTED;
+    if (static_cast<int64_t>(plan.chunks) * plan.slices > kMaxDim / 2) return TG_ERR_UNSUPPORTED;
     uint8_t* ws = static_cast<uint8_t*>(device_workspace(plan.bytes, stream, &rc));
     if (ws == nullptr) return rc;
-    unsigned* marks = accumulate ? nullptr : reinterpret_cast<unsigned*>(ws + plan.marks);
-    if (marks != nullptr) {
-      const cudaError_t e =
-          cudaMemsetAsync(marks, 0, static_cast<size_t>((rows + 31) / 32 * 4), stream);
-      if (e != cudaSuccess) return cuda_fail(e);
-    }
+    unsigned* marks =
+        accumulate ? nullptr : reinterpret_cast<unsigned*>(ws + plan.marks + kNoteCount);
+    a.notes = reinterpret_cast<int2*>(ws + plan.notes);
+    a.note_count = reinterpret_cast<int*>(ws + plan.marks);
+    const cudaError_t e = cudaMemsetAsync(
+        a.note_count, 0,
+        kNoteCount + (accumulate ? 0 : static_cast<size_t>((rows + 31) / 32 * 4)), stream);
+    if (e != cudaSuccess) return cuda_fail(e);
     int* order = reinterpret_cast<int*>(ws);
     int* sorted = reinterpret_cast<int*>(ws + plan.sorted);
     rc = sort_ids(ids, n, rows, order, reinterpret_cast<int*>(ws + plan.other), sorted,
@@ -462,7 +541,7 @@ int embed_rows_grad(const void* G, int64_t ldg, int g_dtype, const int32_t* ids,
     a.ldp = plan.ldp;
     a.chunk = plan.chunk;
     a.chunks = plan.chunks;
-    a.slices = static_cast<int>((K + kSlice - 1) / kSlice);
+    a.slices = plan.slices;
   }
   const bool add = accumulate != 0, g16 = g_dtype == TG_D_BF16, d16 = d_dtype == TG_D_BF16;
   if (g16 && d16) return launch_grad<uint16_t, uint16_t>(a, add, ctx, stream);
