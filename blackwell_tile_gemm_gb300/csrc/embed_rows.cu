@@ -5,14 +5,15 @@
 //
 // Both are bound by HBM: every row is moved once.  The lookup gives each warp a
 // part of a row.  The gradient must not depend on the order in which anything
-// runs, so the rows are first sorted by id (stable; group_rows.cu, digit by
-// digit), and a run of equal ids is summed in the order of its rows, in f32.
-// Runs are as uneven as words are: the sorted rows are cut into chunks of equal
-// length, a block each; a run that lies inside its chunk goes straight to dW,
-// what crosses a chunk's end goes to the workspace as an f32 partial sum, and a
-// second kernel adds a run's partial sums in their order.  The rows of dW that no
-// token has (nearly all of a large table's) are written as zeros by further
-// blocks of the first kernel, meanwhile.
+// runs, so the rows are first sorted by id (stable; few by counting the smaller
+// ones, many digit by digit with the sort of group_rows.cu), and a run of equal ids
+// is summed in the order of its rows, in f32.  Runs are as uneven as words are: the
+// sorted rows are cut into chunks of equal length, a warp for each and 256 columns;
+// a run that lies inside its chunk goes straight to dW, what crosses a chunk's end
+// goes to the workspace as an f32 partial sum, and a second kernel adds a run's
+// partial sums in their order.  The rows of dW that no token has (nearly all of a
+// large table's) are written as zeros by further blocks of the first kernel,
+// meanwhile.
 #include <atomic>
 
 #include "tg_internal.h"
@@ -28,13 +29,14 @@ constexpr int64_t kMaxTokens = int64_t{1} << 30;   // as tg_group_rows
 constexpr int64_t kMostColumns = int64_t{256} * 65535;
 
 template <class K, class... T>
-int launch_chained(K kern, int64_t blocks, int threads, cudaStream_t stream, T... args) {
+int launch_chained(K kern, int64_t blocks, int threads, cudaStream_t stream, size_t smem, T... args) {
   cudaLaunchConfig_t cfg{};
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.gridDim = dim3(static_cast<unsigned>(blocks), 1, 1);
   cfg.blockDim = dim3(static_cast<unsigned>(threads), 1, 1);
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
@@ -156,13 +158,56 @@ __global__ void __launch_bounds__(256) embed_kernel(const uint16_t* W, int64_t l
 // Gradient
 // ---------------------------------------------------------------------------
 
+// Sorting up to kFewTokens ids in one launch: a row's place is the number of smaller
+// (id, row) pairs, packed into 32 bits.  A block holds all pairs in shared memory and
+// places 64 rows, 16 threads to each.
+constexpr int kFewTokens = 8192;
+constexpr int kFewBits = 13;
+constexpr int64_t kFewRows = (int64_t{1} << (32 - kFewBits)) - 1;
+
+__global__ void __launch_bounds__(1024) rank_ids_kernel(const int* ids, int n, int vocab,
+                                                        int* order, int* sorted, int* note_count) {
+  extern __shared__ uint4 keys4[];
+  uint32_t* keys = reinterpret_cast<uint32_t*>(keys4);
+  griddep_wait();
+  griddep_launch_dependents();
+  const int tid = static_cast<int>(threadIdx.x);
+  const int n4 = (n + 3) / 4;
+  for (int i = tid; i < 4 * n4; i += 1024) {
+    uint32_t key = 0xFFFFFFFFu;
+    if (i < n) {
+      const int id = ids[i];
+      const bool in = static_cast<unsigned>(id) < static_cast<unsigned>(vocab);
+      key = static_cast<uint32_t>(in ? id : vocab) << kFewBits | static_cast<uint32_t>(i);
+    }
+    keys[i] = key;
+  }
+  if (blockIdx.x == 0 && tid == 0) *note_count = 0;
+  __syncthreads();
+  const int i = static_cast<int>(blockIdx.x) * 64 + tid / 16;
+  const uint32_t mine = keys[i < n ? i : 0];
+  int rank = 0;
+#pragma unroll 4
+  for (int j = tid % 16; j < n4; j += 16) {
+    const uint4 k = keys4[j];
+    rank += (k.x < mine) + (k.y < mine) + (k.z < mine) + (k.w < mine);
+  }
+#pragma unroll
+  for (int d = 8; d > 0; d /= 2) rank += __shfl_xor_sync(0xFFFFFFFFu, rank, d);
+  if (i < n && tid % 16 == 0) {
+    const int id = static_cast<int>(mine >> kFewBits);
+    order[rank] = i;
+    sorted[rank] = id < vocab ? id : -1;
+  }
+}
+
 struct EmbedGradArgs {
   const void* G;
   int64_t ldg;
   int n, vocab, K;
   const int* order;       // rows by id
   const int* sorted;      // their ids, -1 for rows of none (last)
-  const unsigned* marks;  // a bit for each id that occurs; null: D is added to
+  const unsigned* marks;  // a bit for each id that occurs, or null: looked up in `sorted`
   float scale;
   void* D;
   int64_t ldd;
@@ -201,6 +246,21 @@ __device__ __forceinline__ void bulk_store(void* dst, uint32_t src, uint32_t byt
                : "memory");
 }
 
+// Whether v is among the sorted ids (behind which those of no row lie as -1).
+__device__ __forceinline__ bool has_token(const EmbedGradArgs& p, int64_t v) {
+  int lo = 0, hi = p.n;
+  while (lo < hi) {
+    const int mid = (lo + hi) / 2;
+    const int id = p.sorted[mid];
+    if (id == v) return true;
+    if (id >= 0 && id < v)
+      lo = mid + 1;
+    else
+      hi = mid;
+  }
+  return false;
+}
+
 // Rows that no token has, a thread each, as bulk copies of zeros: 1 GB of them by
 // 16-byte stores of whole warps, in blocks behind those of the sums, took 260 us
 // with the sums of 32768 rows x 4096 in 128000.
@@ -218,7 +278,8 @@ __device__ __forceinline__ void clear_unused(const EmbedGradArgs& p, int64_t blo
   // (Rows far apart: a block's copies go out one after the other, and a small
   // table needs many blocks.)
   for (int64_t v = block + threadIdx.x * blocks; v < p.vocab; v += blocks * blockDim.x) {
-    if (p.n > 0 && (__ldcg(p.marks + (v >> 5)) >> (v & 31)) & 1u) continue;
+    if (p.marks != nullptr ? (__ldcg(p.marks + (v >> 5)) >> (v & 31)) & 1u : has_token(p, v))
+      continue;
     uint8_t* d = reinterpret_cast<uint8_t*>(static_cast<TD*>(p.D) + v * p.ldd);
     for (int64_t at = 0; at < whole; at += kZeros)
       bulk_store(d + at, src, static_cast<uint32_t>(whole - at < kZeros ? whole - at : kZeros));
@@ -426,11 +487,11 @@ int launch_grad(const EmbedGradArgs& a, DeviceCtx* ctx, cudaStream_t stream) {
   const int64_t blocks =
       (static_cast<int64_t>(a.chunks) * a.slices + kWarps - 1) / kWarps + zero_blocks;
   if (blocks == 0) return TG_OK;
-  int rc = launch_chained(sum_runs_kernel<TG, TD, kAdd>, blocks, 32 * kWarps, stream, a);
+  int rc = launch_chained(sum_runs_kernel<TG, TD, kAdd>, blocks, 32 * kWarps, stream, 0, a);
   if (rc != TG_OK || a.chunks < 2) return rc;
   const int64_t notes = static_cast<int64_t>(a.chunks - 1) * a.slices;
   const int64_t most = 4 * static_cast<int64_t>(ctx->num_sms);
-  return launch_chained(join_runs_kernel<TD, kAdd>, notes < most ? notes : most, 256, stream, a);
+  return launch_chained(join_runs_kernel<TD, kAdd>, notes < most ? notes : most, 256, stream, 0, a);
 }
 
 template <class TG, class TD>
@@ -484,9 +545,9 @@ int embed_rows(const void* W, int64_t ldw, int64_t rows, const int32_t* ids, int
   const uint16_t* w = static_cast<const uint16_t*>(W);
   const int v = static_cast<int>(rows), k = static_cast<int>(K);
   if (d_dtype == TG_D_BF16)
-    return launch_chained(embed_kernel<uint16_t>, blocks, 256, stream, w, ldw, v, ids, n, k, parts,
+    return launch_chained(embed_kernel<uint16_t>, blocks, 256, stream, 0, w, ldw, v, ids, n, k, parts,
                           scale, static_cast<uint16_t*>(D), ldd);
-  return launch_chained(embed_kernel<float>, blocks, 256, stream, w, ldw, v, ids, n, k, parts,
+  return launch_chained(embed_kernel<float>, blocks, 256, stream, 0, w, ldw, v, ids, n, k, parts,
                         scale, static_cast<float*>(D), ldd);
 }
 
@@ -521,22 +582,28 @@ int embed_rows_grad(const void* G, int64_t ldg, int g_dtype, const int32_t* ids,
     if (static_cast<int64_t>(plan.chunks) * plan.slices > kMaxDim / 2) return TG_ERR_UNSUPPORTED;
     uint8_t* ws = static_cast<uint8_t*>(device_workspace(plan.bytes, stream, &rc));
     if (ws == nullptr) return rc;
-    unsigned* marks =
-        accumulate ? nullptr : reinterpret_cast<unsigned*>(ws + plan.marks + kNoteCount);
     a.notes = reinterpret_cast<int2*>(ws + plan.notes);
     a.note_count = reinterpret_cast<int*>(ws + plan.marks);
-    const cudaError_t e = cudaMemsetAsync(
-        a.note_count, 0,
-        kNoteCount + (accumulate ? 0 : static_cast<size_t>((rows + 31) / 32 * 4)), stream);
-    if (e != cudaSuccess) return cuda_fail(e);
     int* order = reinterpret_cast<int*>(ws);
     int* sorted = reinterpret_cast<int*>(ws + plan.sorted);
-    rc = sort_ids(ids, n, rows, order, reinterpret_cast<int*>(ws + plan.other), sorted,
-                  reinterpret_cast<int*>(ws + plan.count), marks, ws + plan.hist, stream, ctx);
+    if (n <= kFewTokens && rows <= kFewRows) {
+      rc = launch_chained(rank_ids_kernel, (n + 63) / 64, 1024, stream,
+                          static_cast<size_t>((n + 3) / 4 * 16), ids, static_cast<int>(n),
+                          static_cast<int>(rows), order, sorted, a.note_count);
+    } else {
+      unsigned* marks =
+          accumulate ? nullptr : reinterpret_cast<unsigned*>(ws + plan.marks + kNoteCount);
+      const cudaError_t e = cudaMemsetAsync(
+          a.note_count, 0,
+          kNoteCount + (accumulate ? 0 : static_cast<size_t>((rows + 31) / 32 * 4)), stream);
+      if (e != cudaSuccess) return cuda_fail(e);
+      rc = sort_ids(ids, n, rows, order, reinterpret_cast<int*>(ws + plan.other), sorted,
+                    reinterpret_cast<int*>(ws + plan.count), marks, ws + plan.hist, stream, ctx);
+      a.marks = marks;
+    }
     if (rc != TG_OK) return rc;
     a.order = order;
     a.sorted = sorted;
-    a.marks = marks;
     a.parts = reinterpret_cast<float*>(ws + plan.parts);
     a.ldp = plan.ldp;
     a.chunk = plan.chunk;

@@ -80,7 +80,7 @@ struct XentOperands {
   const void* B;
   int64_t ldb;
   int64_t K;
-  void* dz;            // kXentGrad: [terms][M][ld_dz]
+  void* dz;            // kXentGrad: [M][terms][ld_dz]
   int64_t ld_dz;
 };
 
@@ -98,6 +98,7 @@ int launch_xent_cfg(const XentOperands& o, const XentArgs& args, const XentTiles
   // Bands of 4096 rows: the units that run at the same time share panels of B.
   a.raster_group = 4096 / (128 * kCtaGroup);
   a.a_box = kCtaGroup == 2 ? 128 : ceil_div_i(a.M, 8) * 8;
+  a.a_bytes = xent_ring(a.a_box, a.bn / kCtaGroup, &a.b_bytes, &a.stages);
   a.status = ctx->status;
   a.timeout_ns = wait_timeout_ns();
   const CUtensorMapDataType bf = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
@@ -109,11 +110,12 @@ int launch_xent_cfg(const XentOperands& o, const XentArgs& args, const XentTiles
   if (rc != TG_OK) return rc;
   CUtensorMap tD = tA, tD2 = tA;
   if constexpr (kMode != kXentLoss) {
-    rc = make_tensor_map_2d(&tD, bf, o.dz, o.ld_dz, a.M, o.ld_dz * 2, 64, 32, sw);
+    const int64_t row_bytes = o.ld_dz * (C::kTwo ? 4 : 2);
+    rc = make_tensor_map_2d(&tD, bf, o.dz, o.ld_dz, a.M, row_bytes, 64, 32, sw);
     if (rc != TG_OK) return rc;
     if constexpr (C::kTwo) {
-      rc = make_tensor_map_2d(&tD2, bf, static_cast<uint16_t*>(o.dz) + a.M * o.ld_dz, o.ld_dz, a.M,
-                              o.ld_dz * 2, 64, 32, sw);
+      rc = make_tensor_map_2d(&tD2, bf, static_cast<uint16_t*>(o.dz) + o.ld_dz, o.ld_dz, a.M,
+                              row_bytes, 64, 32, sw);
       if (rc != TG_OK) return rc;
     }
   }
@@ -225,8 +227,7 @@ __global__ void xent_zero_kernel(const int* targets, float* loss, float* lse, in
 // The gradient's rows of A, and dA's rounding
 // ---------------------------------------------------------------------------
 
-// dst[i] (and dst[M + i] for two terms) = A[i] where row i has a target, else
-// zeros: dz is 0 there, but 0 times what padding holds may be NaN.  Whole
+// dst[terms * i + t] = A[i] for each term t where row i has a target, else zeros: dz is 0 there, but 0 times what padding holds may be NaN.  Whole
 // 16-byte pieces, a warp a row; the pitch makes room for the last.
 __global__ void __launch_bounds__(256) learned_rows_kernel(const uint16_t* A, int64_t lda,
                                                            const int* targets, int vocab,
@@ -241,7 +242,7 @@ __global__ void __launch_bounds__(256) learned_rows_kernel(const uint16_t* A, in
     const int t = targets[i];
     const bool learned = t >= 0 && t < vocab;
     const uint16_t* s = A + i * lda;
-    uint16_t* d = dst + i * ld;
+    uint16_t* d = dst + i * terms * ld;
     for (int k0 = 0; k0 < whole; k0 += 128) {
       uint4 v[4];
 #pragma unroll
@@ -255,12 +256,12 @@ __global__ void __launch_bounds__(256) learned_rows_kernel(const uint16_t* A, in
         const int k = k0 + 32 * u + lane;
         if (k < whole)
           for (int h = 0; h < terms; ++h)
-            reinterpret_cast<uint4*>(d + static_cast<int64_t>(h) * M * ld)[k] = v[u];
+            reinterpret_cast<uint4*>(d + h * ld)[k] = v[u];
       }
     }
     const int k = whole * 8 + lane;
     if (lane < 8 && k < K)
-      for (int h = 0; h < terms; ++h) d[static_cast<int64_t>(h) * M * ld + k] = learned ? s[k] : 0;
+      for (int h = 0; h < terms; ++h) d[h * ld + k] = learned ? s[k] : 0;
   }
 }
 
@@ -424,10 +425,11 @@ int gemm_bf16_xent_grad(const void* A, int64_t lda, const void* B, int64_t ldb,
   a.grad = grad;
   for (int64_t col0 = 0; col0 < N; col0 += plan.piece) {
     const int64_t n = N - col0 < plan.piece ? N - col0 : plan.piece;
+    const int64_t ld_dz = xent_up(n, 64);   // (the piece's own: nothing of another's is left in it)
     const uint16_t* b = static_cast<const uint16_t*>(B) + col0 * ldb;
     a.N = static_cast<int>(n);
     a.col0 = static_cast<int>(col0);
-    const XentOperands o{a_rows, plan.ld_a, b, ldb, K, dz, plan.ld_dz};
+    const XentOperands o{a_rows, plan.terms * plan.ld_a, b, ldb, K, dz, ld_dz};
     const XentTiles tiles = xent_tiles(M, n, 64);
     rc = bf16 ? launch_xent<kXentGrad>(o, a, tiles, stream, ctx)
               : launch_xent<kXentGradTwo>(o, a, tiles, stream, ctx);
@@ -436,32 +438,32 @@ int gemm_bf16_xent_grad(const void* A, int64_t lda, const void* B, int64_t ldb,
       GroupedArgs g = grouped_args(ctx);
       g.M = m;
       g.wide = static_cast<int>(K);
-      g.num_k_blocks = ceil_div_i(n, 64);
       GroupedOperands p{};
       p.wide = b;
       p.wide_ld = ldb;
       p.wide_rows = n;
       p.wide_slices = 1;
       p.wide_slice_stride = ldb * n;
-      p.cols_ld = plan.ld_dz;
-      p.k = n;
-      for (int term = 0; term < plan.terms; ++term) {
-        p.cols = dz + static_cast<int64_t>(term) * M * plan.ld_dz;
-        g.add = col0 > 0 || term > 0;
-        if (bf16 && plan.pieces == 1) {
-          g.D = dA;
-          g.ldd = ldda;
-          rc = launch_grouped_dgrad(true, p, g, stream, ctx);
-        } else {
-          g.D = bf16 ? static_cast<void*>(sums) : dA;
-          g.ldd = bf16 ? plan.ld_sum : ldda;
-          rc = launch_grouped_dgrad_add(!bf16, p, g, stream, ctx);
-        }
-        if (rc != TG_OK) return rc;
+      p.cols = dz;
+      p.cols_ld = plan.terms * ld_dz;
+      // (dz is zero from column n on, and past B's row n nothing is read.)
+      p.k = plan.terms * ld_dz;
+      g.wrap = static_cast<int>(ld_dz);
+      g.num_k_blocks = static_cast<int>(p.k / 64);
+      g.add = col0 > 0;
+      if (bf16 && plan.pieces == 1) {
+        g.D = dA;
+        g.ldd = ldda;
+        rc = launch_grouped_dgrad(true, p, g, stream, ctx);
+      } else {
+        g.D = bf16 ? static_cast<void*>(sums) : dA;
+        g.ldd = bf16 ? plan.ld_sum : ldda;
+        rc = launch_grouped_dgrad_add(!bf16, p, g, stream, ctx);
       }
+      if (rc != TG_OK) return rc;
     }
     if (weights) {
-      // Both terms in one contraction: dz and the rows of A lie below each other.
+      // (Two terms: 2 M rows of dz against as many of A.)
       const int64_t terms_rows = plan.terms * M;
       GroupedArgs g = grouped_args(ctx);
       g.M = static_cast<int>(terms_rows);
@@ -477,7 +479,7 @@ int gemm_bf16_xent_grad(const void* A, int64_t lda, const void* B, int64_t ldb,
       p.wide_rows = terms_rows;
       p.wide_slices = 1;
       p.cols = dz;
-      p.cols_ld = plan.ld_dz;
+      p.cols_ld = ld_dz;
       p.k = terms_rows;
       rc = launch_grouped_wgrad(bf16, p, g, stream, ctx);
       if (rc != TG_OK) return rc;

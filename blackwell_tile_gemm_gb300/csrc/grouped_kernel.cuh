@@ -112,6 +112,8 @@ struct GroupedArgs {
   int64_t ldd;
   int64_t group_stride_d;  // wgrad
   int add;                 // kAdd: D += instead of D =
+  int wrap;                // kAdd: contraction index from which the wide operand's rows
+                           // begin again (a multiple of 64; the column operand's do not)
   Epi epi;                 // bias: [groups][wide]
   // adapters
   const int* ids;          // [M]
@@ -1271,11 +1273,12 @@ __global__ void __launch_bounds__(C::kThreads, 1)
             }
           } else if constexpr (C::kCtaGroup == 2) {
             if (do_wide) {
+              const int kw = C::kAdd && kx >= p.wrap ? kx - p.wrap : kx;
               if (C::kWideMn && w_chunks) {
-                tma_load_4d_pair(dW, &tmW2, fb, 0, kx, wx / 64, w.g, pol);
+                tma_load_4d_pair(dW, &tmW2, fb, 0, kw, wx / 64, w.g, pol);
               } else if constexpr (C::kWideMn) {
                 for (int c = 0; c < 2; ++c)
-                  tma_load_3d_pair(dW + 8192 * c, &tmW, fb, wx + 64 * c, kx, w.g, pol);
+                  tma_load_3d_pair(dW + 8192 * c, &tmW, fb, wx + 64 * c, kw, w.g, pol);
               } else {
                 tma_load_3d_pair(dW, &tmW, fb, kx, wx, w.g, pol);
               }

@@ -46,6 +46,7 @@ struct XentArgs {
   int bn;
   int raster_group;    // m-tiles per band of the tile order
   int a_box;           // rows of A per load (128; few rows: theirs, rounded up to 8)
+  int stages, a_bytes, b_bytes;   // the ring: slots, bytes of A and of B in each
   float scale2;        // scale * log2(e)
   float scale;
   const int* targets;  // [M]
@@ -65,12 +66,14 @@ struct XentCfg {
   static constexpr int kMode = kMode_;
   static constexpr bool kTwo = kMode == kXentGradTwo;
   static constexpr int BN = 256;                       // most columns of a tile
-  static constexpr int kStages = kCtaGroup == 2 ? 6 : 4;
-  static constexpr int A_BYTES = 128 * 128;
-  static constexpr int B_BYTES = BN / kCtaGroup * 128;
-  static constexpr int OFF_A = 0;
-  static constexpr int OFF_B = kStages * A_BYTES;
-  static constexpr int OFF_STG = OFF_B + kStages * B_BYTES;
+  // The ring, 192 KB.  CTA pairs: 6 slots of 128 rows of A and of B.  Few rows: as
+  // many as fit of what they load, so that 6 MB and more are on their way to the SMs
+  // (one token x 32000 x 4096 with 4 slots of 128 + 256 rows: 47.6 us).  The MMA
+  // reads 128 rows of A all the same: what follows them is a later slot or B, and
+  // lands in lanes that no row has.
+  static constexpr int RING_BYTES = 192 * 1024;
+  static constexpr int kStages = kCtaGroup == 2 ? 6 : 16;
+  static constexpr int OFF_STG = RING_BYTES;
   static constexpr int kEpiWarps = 8;
   static constexpr int kAccBufs = 2;
   static constexpr int kStgBytes = kMode == kXentLoss ? 0 : 4096;   // a box of 32 rows x 64 bf16
@@ -150,8 +153,14 @@ __global__ void __launch_bounds__(C::kThreads, 1)
   const uint32_t rank = C::kCtaGroup == 2 ? cluster_ctarank() : 0u;
   const bool leader = rank == 0;
 
+  const int stages = C::kCtaGroup == 2 ? C::kStages : p.stages;
+  const uint32_t a_bytes = C::kCtaGroup == 2 ? 128u * 128u : static_cast<uint32_t>(p.a_bytes);
+  const uint32_t b_bytes = C::kCtaGroup == 2 ? 128u * 128u : static_cast<uint32_t>(p.b_bytes);
+  const uint32_t ring_a = smem_addr(smem);
+  const uint32_t ring_b = ring_a + static_cast<uint32_t>(stages) * a_bytes;
+
   if (threadIdx.x == 0) {
-    for (int s = 0; s < C::kStages; ++s) {
+    for (int s = 0; s < stages; ++s) {
       mbar_init(&full_bar[s], 1);
       mbar_init(&empty_bar[s], 1);
     }
@@ -195,8 +204,9 @@ __global__ void __launch_bounds__(C::kThreads, 1)
     // ------------------------------------------------------------ producer
     if (lane == 0) {
       const uint64_t pol = policy_evict_last();
-      const uint32_t sA = smem_addr(smem + C::OFF_A);
-      const uint32_t sB = smem_addr(smem + C::OFF_B);
+      // (The loss of few rows reads B once and for all.)
+      const uint64_t pol_b =
+          C::kCtaGroup == 1 && C::kMode == kXentLoss ? policy_evict_first() : pol;
       const uint32_t empty0 = smem_addr(&empty_bar[0]);
       const uint32_t full0 = smem_addr(&full_bar[0]);
       const uint32_t full_dst0 = C::kCtaGroup == 2 ? map_to_cta(full0, 0u) : full0;
@@ -222,15 +232,15 @@ __global__ void __launch_bounds__(C::kThreads, 1)
           const uint32_t fb = full_dst0 + 8u * stage;
           if (leader) mbar_arrive_expect_tx(&full_bar[stage], bytes);
           if constexpr (C::kCtaGroup == 1) {
-            tma_load_2d(sA + stage * C::A_BYTES, &tmA, fb, kx, a_row, pol);
-            tma_load_2d(sB + stage * C::B_BYTES, &tmB, fb, kx, b_row, pol);
+            tma_load_2d(ring_a + stage * a_bytes, &tmA, fb, kx, a_row, pol);
+            tma_load_2d(ring_b + stage * b_bytes, &tmB, fb, kx, b_row, pol_b);
           } else {
-            tma_load_2d_pair(sA + stage * C::A_BYTES, &tmA, fb, kx, a_row, pol);
-            tma_load_2d_pair(sB + stage * C::B_BYTES, &tmB, fb, kx, b_row, pol);
+            tma_load_2d_pair(ring_a + stage * a_bytes, &tmA, fb, kx, a_row, pol);
+            tma_load_2d_pair(ring_b + stage * b_bytes, &tmB, fb, kx, b_row, pol);
           }
           issued |= 1u << stage;
           issued_parity = (issued_parity & ~(1u << stage)) | (phase << stage);
-          if (++stage == C::kStages) {
+          if (++stage == stages) {
             stage = 0;
             phase ^= 1u;
           }
@@ -239,7 +249,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
       griddep_launch_dependents();
       if (!ok && leader) {
         // Gave up: the loads already issued land before the CTA exits.
-        for (int s = 0; s < C::kStages; ++s)
+        for (int s = 0; s < stages; ++s)
           if (issued & (1u << s))
             mbar_wait_drain(&full_bar[s], (issued_parity >> s) & 1u, p.timeout_ns);
       }
@@ -250,9 +260,9 @@ __global__ void __launch_bounds__(C::kThreads, 1)
       const uint32_t acce0 = smem_addr(&acce_bar[0]);
       const uint32_t full0 = smem_addr(&full_bar[0]);
       const uint64_t adesc0 =
-          make_smem_desc(smem_addr(smem + C::OFF_A), 16, 1024, kDescSwizzle128B);
+          make_smem_desc(ring_a, 16, 1024, kDescSwizzle128B);
       const uint64_t bdesc0 =
-          make_smem_desc(smem_addr(smem + C::OFF_B), 16, 1024, kDescSwizzle128B);
+          make_smem_desc(ring_b, 16, 1024, kDescSwizzle128B);
       const uint32_t idesc = idesc_bf16_f32(128 * C::kCtaGroup, static_cast<uint32_t>(p.bn));
       int stage = 0;
       uint32_t phase = 0;
@@ -279,10 +289,10 @@ __global__ void __launch_bounds__(C::kThreads, 1)
               break;
             }
             tc_fence_after_sync();
-            const int ns = stage + 1 == C::kStages ? 0 : stage + 1;
-            const uint32_t nph = stage + 1 == C::kStages ? phase ^ 1u : phase;
-            const uint64_t ad = adesc0 + static_cast<uint64_t>(stage * (C::A_BYTES >> 4));
-            const uint64_t bd = bdesc0 + static_cast<uint64_t>(stage * (C::B_BYTES >> 4));
+            const int ns = stage + 1 == stages ? 0 : stage + 1;
+            const uint32_t nph = stage + 1 == stages ? phase ^ 1u : phase;
+            const uint64_t ad = adesc0 + static_cast<uint64_t>(stage * (a_bytes >> 4));
+            const uint64_t bd = bdesc0 + static_cast<uint64_t>(stage * (b_bytes >> 4));
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
               mma_bf16<C::kCtaGroup>(d_tmem, ad + 2 * k, bd + 2 * k, idesc, add || k != 0);

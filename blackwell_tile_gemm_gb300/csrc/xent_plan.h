@@ -22,23 +22,39 @@ struct XentTiles {
 
 // Columns per tile: the width whose waves over the units take least.  A stage of
 // a CTA pair costs the larger of its MMAs (2 cycles a column) and its loads (128
-// rows of A and half the columns of B at 64 bytes a cycle); one of few rows
-// streams B from HBM, and what it adds to a tile is A and the epilogue.
+// rows of A and half the columns of B at 64 bytes a cycle); one of few rows streams B
+// from HBM, and what it adds is A's rows for each tile and the last tile's epilogue,
+// which nothing hides (one token x 32000 x 4096: tiles of 112 columns, two a CTA).
 inline XentTiles xent_tiles(int64_t M, int64_t N, int step) {
   const bool few = M <= kXentFewRows;
   const int64_t units = few ? kXentSms : kXentSms / 2;
   const int64_t mt = few ? 1 : (M + 255) / 256;
-  const int64_t least = few ? (step > 32 ? step : 32) : (step > 64 ? step : 64);
+  const int64_t least = few ? (step > 48 ? step : 48) : (step > 64 ? step : 64);
   int64_t best = 0, bn = 256;
   for (int64_t c = 256; c >= least; c -= step) {
     const int64_t waves = (mt * ((N + c - 1) / c) + units - 1) / units;
-    const int64_t tile = few ? c + 8 + M / 8 : (2 * c > 256 + c ? 2 * c : 256 + c) + 48;
-    if (best == 0 || waves * tile < best) {
-      best = waves * tile;
+    const int64_t cost = few ? waves * (c + M / 8) + c / 4
+                             : waves * ((2 * c > 256 + c ? 2 * c : 256 + c) + 48);
+    if (best == 0 || cost < best) {
+      best = cost;
       bn = c;
     }
   }
   return XentTiles{static_cast<int>(bn), static_cast<int>(mt), static_cast<int>((N + bn - 1) / bn)};
+}
+
+// The ring of single CTAs: slots of a_box rows of A (from the start of the ring) and b_box
+// of B (behind all of A's), 128 bytes a row, whole 1 KB swizzle atoms.  The MMA reads
+// 128 rows from each slot of A: the last has to have as many bytes of the ring behind
+// its start.
+constexpr int kXentRing = 192 * 1024;
+inline int xent_ring(int a_box, int b_box, int* b_bytes, int* stages) {
+  const int a_bytes = static_cast<int>(xent_up(a_box, 8)) * 128;
+  *b_bytes = static_cast<int>(xent_up(b_box, 8)) * 128;
+  int s = kXentRing / (a_bytes + *b_bytes);
+  if (s > 16) s = 16;
+  *stages = s;
+  return a_bytes;
 }
 
 // Workspace of the loss: [2 * n_tiles][M] pairs, then the targets' logits.
@@ -54,9 +70,11 @@ inline XentLossPlan xent_loss_plan(int64_t M, int64_t N) {
   return q;
 }
 
-// Workspace of the gradient: the rows of A that have a target (the others as
-// zeros; `terms` times below each other), dz of one piece of the vocabulary
-// (`terms` of M rows) and the f32 sums of dA.
+// Workspace of the gradient: the rows of A that have a target (the others as zeros),
+// dz of one piece of the vocabulary and the f32 sums of dA.  With two terms of dz a
+// row's second follows its first: [M][2][ld_dz].  Read as M rows twice as long, one
+// contraction of dA takes both (B's rows a second time); read as 2 M rows, so does
+// one of dB, with each row of A twice.
 //
 // Pieces are as wide as kXentDzBytes allow, but at least kXentLeastPiece columns:
 // every piece adds its share of dA to all of it in memory, 8 bytes for 2 * width
