@@ -224,46 +224,8 @@ __global__ void xent_zero_kernel(const int* targets, float* loss, float* lse, in
 }
 
 // ---------------------------------------------------------------------------
-// The gradient's rows of A, and dA's rounding
+// dA's rounding
 // ---------------------------------------------------------------------------
-
-// dst[terms * i + t] = A[i] for each term t where row i has a target, else zeros: dz is 0 there, but 0 times what padding holds may be NaN.  Whole
-// 16-byte pieces, a warp a row; the pitch makes room for the last.
-__global__ void __launch_bounds__(256) learned_rows_kernel(const uint16_t* A, int64_t lda,
-                                                           const int* targets, int vocab,
-                                                           uint16_t* dst, int64_t ld, int M, int K,
-                                                           int terms) {
-  griddep_wait();
-  griddep_launch_dependents();
-  const int lane = static_cast<int>(threadIdx.x & 31);
-  const int64_t warps = static_cast<int64_t>(gridDim.x) * 8;
-  const int whole = K / 8;
-  for (int64_t i = blockIdx.x * 8LL + (threadIdx.x >> 5); i < M; i += warps) {
-    const int t = targets[i];
-    const bool learned = t >= 0 && t < vocab;
-    const uint16_t* s = A + i * lda;
-    uint16_t* d = dst + i * terms * ld;
-    for (int k0 = 0; k0 < whole; k0 += 128) {
-      uint4 v[4];
-#pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        const int k = k0 + 32 * u + lane;
-        v[u] = make_uint4(0u, 0u, 0u, 0u);
-        if (learned && k < whole) v[u] = __ldcs(reinterpret_cast<const uint4*>(s) + k);
-      }
-#pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        const int k = k0 + 32 * u + lane;
-        if (k < whole)
-          for (int h = 0; h < terms; ++h)
-            reinterpret_cast<uint4*>(d + h * ld)[k] = v[u];
-      }
-    }
-    const int k = whole * 8 + lane;
-    if (lane < 8 && k < K)
-      for (int h = 0; h < terms; ++h) d[h * ld + k] = learned ? s[k] : 0;
-  }
-}
 
 __global__ void __launch_bounds__(256) round_rows_kernel(const float* src, int64_t ld,
                                                          uint16_t* dst, int64_t ldd, int M, int K) {
@@ -409,12 +371,6 @@ int gemm_bf16_xent_grad(const void* A, int64_t lda, const void* B, int64_t ldb,
   uint16_t* dz = reinterpret_cast<uint16_t*>(ws + plan.off_dz);
   float* sums = reinterpret_cast<float*>(ws + plan.off_sum);
   const int m = static_cast<int>(M);
-  const int64_t row_blocks = (M + 7) / 8 < 16 * ctx->num_sms ? (M + 7) / 8 : 16 * ctx->num_sms;
-  rc = launch_chained(learned_rows_kernel, row_blocks, 256, stream,
-                      static_cast<const uint16_t*>(A), lda, targets, static_cast<int>(N), a_rows,
-                      plan.ld_a, m, static_cast<int>(K), plan.terms);
-  if (rc != TG_OK) return rc;
-
   XentArgs a{};
   a.M = m;
   a.vocab = static_cast<int>(N);
@@ -423,13 +379,18 @@ int gemm_bf16_xent_grad(const void* A, int64_t lda, const void* B, int64_t ldb,
   a.targets = targets;
   a.lse = lse;
   a.grad = grad;
+  a.A = static_cast<const uint16_t*>(A);
+  a.lda = lda;
+  a.ld_copy = plan.ld_a;
+  a.K = static_cast<int>(K);
   for (int64_t col0 = 0; col0 < N; col0 += plan.piece) {
     const int64_t n = N - col0 < plan.piece ? N - col0 : plan.piece;
     const int64_t ld_dz = xent_up(n, 64);   // (the piece's own: nothing of another's is left in it)
     const uint16_t* b = static_cast<const uint16_t*>(B) + col0 * ldb;
     a.N = static_cast<int>(n);
     a.col0 = static_cast<int>(col0);
-    const XentOperands o{a_rows, plan.terms * plan.ld_a, b, ldb, K, dz, ld_dz};
+    a.copy = weights && col0 == 0 ? a_rows : nullptr;
+    const XentOperands o{A, lda, b, ldb, K, dz, ld_dz};
     const XentTiles tiles = xent_tiles(M, n, 64);
     rc = bf16 ? launch_xent<kXentGrad>(o, a, tiles, stream, ctx)
               : launch_xent<kXentGradTwo>(o, a, tiles, stream, ctx);

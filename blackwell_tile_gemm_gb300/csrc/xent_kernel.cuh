@@ -56,6 +56,13 @@ struct XentArgs {
   // kXentGrad
   const float* lse;    // [M]
   const float* grad;   // [M], or null for 1
+  // Where not null, the kernel also copies A's rows there (`terms` times in a row,
+  // ld_copy apart), zeros for rows without a target: dz is 0 in those, but 0 times
+  // what padding holds may be NaN, so the product for dB reads the copy.
+  const uint16_t* A;
+  int64_t lda, ld_copy;
+  uint16_t* copy;
+  int K;
   uint32_t* status;
   uint64_t timeout_ns;
 };
@@ -129,6 +136,38 @@ __device__ __forceinline__ void xent_read(uint32_t taddr, float (&z)[kN]) {
   for (int e = 0; e < kN; ++e) {
     const float x = __uint_as_float(v[e]);
     z[e] = kAdd ? z[e] + x : x;
+  }
+}
+
+// Rows warp, warp + warps, ... of A to the copy: whole 16-byte pieces, four a lane in
+// flight, then the last K % 8 values.
+template <int kTerms>
+__device__ __forceinline__ void copy_learned_rows(const XentArgs& p, int warp, int warps,
+                                                  int lane) {
+  const int whole = p.K / 8;
+#pragma unroll 1
+  for (int i = warp; i < p.M; i += warps) {
+    const int t = p.targets[i];
+    const bool learned = t >= 0 && t < p.vocab;
+    const uint16_t* s = p.A + i * p.lda;
+    uint16_t* d = p.copy + static_cast<int64_t>(i) * kTerms * p.ld_copy;
+#pragma unroll 1
+    for (int k0 = lane; k0 < whole; k0 += 128) {
+      uint4 v[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        v[u] = make_uint4(0u, 0u, 0u, 0u);
+        if (learned && k0 + 32 * u < whole) v[u] = reinterpret_cast<const uint4*>(s)[k0 + 32 * u];
+      }
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+        if (k0 + 32 * u < whole)
+          for (int h = 0; h < kTerms; ++h)
+            reinterpret_cast<uint4*>(d + h * p.ld_copy)[k0 + 32 * u] = v[u];
+    }
+    const int k = whole * 8 + lane;
+    if (lane < 8 && k < p.K)
+      for (int h = 0; h < kTerms; ++h) d[h * p.ld_copy + k] = learned ? s[k] : 0;
   }
 }
 
@@ -360,6 +399,13 @@ __global__ void __launch_bounds__(C::kThreads, 1)
         acc_phase ^= 1u;
       }
     };
+    if constexpr (C::kMode != kXentLoss) {
+      // The copy, while the first tile's product is under way.
+      if (p.copy != nullptr)
+        copy_learned_rows<C::kTwo ? 2 : 1>(p, static_cast<int>(blockIdx.x) * C::kEpiWarps + warp - 2,
+                                           static_cast<int>(gridDim.x) * C::kEpiWarps,
+                                           static_cast<int>(lane));
+    }
     int last_tm = -1;
     int target = -1;                 // column of this launch, or negative
     bool learned = false;            // the row has a target in the vocabulary
@@ -400,10 +446,12 @@ __global__ void __launch_bounds__(C::kThreads, 1)
           const uint32_t t_row = t_slab + static_cast<uint32_t>(acc * C::BN);
 #pragma unroll
           for (int i = 0; i < 4; ++i)
-            if (32 * (half + 2 * i) < cols) xent_read<true>(t_row + 32 * (half + 2 * i), v[i]);
+            if (32 * (half + 2 * i) < cols && row0 < p.M)
+              xent_read<true>(t_row + 32 * (half + 2 * i), v[i]);
           hand_back();
         }
         if (!ok) break;
+        if (row0 >= p.M) continue;   // (lanes that no row has)
         const float none = __uint_as_float(0xFF800000u);   // -inf
         float m = none;
 #pragma unroll

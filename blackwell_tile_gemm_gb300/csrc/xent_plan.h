@@ -22,9 +22,10 @@ struct XentTiles {
 
 // Columns per tile: the width whose waves over the units take least.  A stage of
 // a CTA pair costs the larger of its MMAs (2 cycles a column) and its loads (128
-// rows of A and half the columns of B at 64 bytes a cycle); one of few rows streams B
-// from HBM, and what it adds is A's rows for each tile and the last tile's epilogue,
-// which nothing hides (one token x 32000 x 4096: tiles of 112 columns, two a CTA).
+// rows of A and half the columns of B at 64 bytes a cycle).  One of few rows streams
+// B from HBM, and A's rows with it, but no stage takes less than the 0.3 us in which a
+// producer issues its loads (one token x 64000 x 4096: tiles of 48 columns 186 us, 112
+// 90, 224 78, i.e. 6.7 TB/s); the last tile's epilogue is hidden by nothing.
 inline XentTiles xent_tiles(int64_t M, int64_t N, int step) {
   const bool few = M <= kXentFewRows;
   const int64_t units = few ? kXentSms : kXentSms / 2;
@@ -33,7 +34,8 @@ inline XentTiles xent_tiles(int64_t M, int64_t N, int step) {
   int64_t best = 0, bn = 256;
   for (int64_t c = 256; c >= least; c -= step) {
     const int64_t waves = (mt * ((N + c - 1) / c) + units - 1) / units;
-    const int64_t cost = few ? waves * (c + M / 8) + c / 4
+    const int64_t stage = c + M > 112 ? c + M : 112;
+    const int64_t cost = few ? waves * (stage + 16) + c / 8
                              : waves * ((2 * c > 256 + c ? 2 * c : 256 + c) + 48);
     if (best == 0 || cost < best) {
       best = cost;
