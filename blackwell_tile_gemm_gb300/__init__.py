@@ -485,8 +485,8 @@ def _on_device(first, *others):
 
 def _result(D, shape, out_dtype, device):
     """(D, its type's code, its row stride), allocated where the caller gave
-    none: rows start on 16-byte boundaries (a padded view where the width asks
-    for it)."""
+    none: rows start on 16-byte boundaries (further apart than the width where
+    that asks for it)."""
     if D is None:
         torch = _torch()
         dtype = out_dtype or torch.float32
@@ -495,8 +495,8 @@ def _result(D, shape, out_dtype, device):
         pad = -width % (4 if code == TG_D_F32 else 8)
         if pad or not width:
             ld = width + pad or 8
-            return torch.empty(shape[:-1] + (ld,), dtype=dtype,
-                               device=device)[..., :width], code, ld
+            strides = (ld, 1) if len(shape) == 2 else (ld * shape[1], ld, 1)
+            return torch.empty_strided(shape, strides, dtype=dtype, device=device), code, ld
         return torch.empty(shape, dtype=dtype, device=device), code, width
     if D.shape != shape:
         raise ValueError(f"D must be {list(shape)}")
@@ -587,7 +587,7 @@ def gemm_bf16_grouped(A, B, offsets, D=None, *, row_idx=None, out_dtype=None, ep
     ``bias`` is float32 [groups, N]; other epilogue keywords as for
     ``make_epilogue``.  D: float32 or bfloat16 [M, N] (default float32); rows
     in no group are zero.  Where none is given it is allocated with rows that
-    start on 16-byte boundaries: a view of a wider tensor where N asks for it
+    start on 16-byte boundaries: further apart than N where N asks for it
     (not a multiple of 4, for bfloat16 of 8).  So do the three calls below.
     """
     bf16 = _torch().bfloat16

@@ -6,8 +6,9 @@
 // Both are bound by HBM: every row is moved once.  The lookup gives each warp a
 // part of a row.  The gradient must not depend on the order in which anything
 // runs, so the rows are first sorted by id (stable; few by counting the smaller
-// ones, many digit by digit with the sort of group_rows.cu), and a run of equal ids
-// is summed in the order of its rows, in f32.  Runs are as uneven as words are: the
+// ones, many digit by digit with the sort of group_rows.cu; very few not at all: a
+// block looks its row's id up among all), and a run of equal ids is summed in the
+// order of its rows, in f32.  Runs are as uneven as words are: the
 // sorted rows are cut into chunks of equal length, a warp for each and 256 columns;
 // a run that lies inside its chunk goes straight to dW, what crosses a chunk's end
 // goes to the workspace as an f32 partial sum, and a second kernel adds a run's
@@ -120,10 +121,10 @@ __device__ __forceinline__ void store8(T* row, int k, int K, const float (&v)[8]
 // ---------------------------------------------------------------------------
 
 // A warp's item: up to kLookup * 256 columns of one row, all loads in flight.
-constexpr int kLookup = 4;
+constexpr int kLookup = 2;
 
 template <class TD>
-__global__ void __launch_bounds__(256) embed_kernel(const uint16_t* W, int64_t ldw, int vocab,
+__global__ void __launch_bounds__(256, 8) embed_kernel(const uint16_t* W, int64_t ldw, int vocab,
                                                     const int* ids, int64_t n, int K, int parts,
                                                     float scale, TD* D, int64_t ldd) {
   griddep_wait();
@@ -135,21 +136,19 @@ __global__ void __launch_bounds__(256) embed_kernel(const uint16_t* W, int64_t l
     const int k0 = static_cast<int>(i - row * parts) * (256 * kLookup) + 8 * lane;
     const int id = ids[row];
     const bool in = static_cast<unsigned>(id) < static_cast<unsigned>(vocab);
-    float v[kLookup][8];
+    Eight<uint16_t> w[kLookup];
 #pragma unroll
     for (int u = 0; u < kLookup; ++u) {
-#pragma unroll
-      for (int e = 0; e < 8; ++e) v[u][e] = 0.0f;
-      if (in && k0 + 256 * u < K) load8(W + id * ldw, k0 + 256 * u, K, v[u]);
+      w[u].q[0] = make_uint4(0u, 0u, 0u, 0u);
+      if (in && k0 + 256 * u < K) w[u].load(W + id * ldw, k0 + 256 * u, K);
     }
 #pragma unroll
     for (int u = 0; u < kLookup; ++u) {
       if (k0 + 256 * u >= K) continue;
-      if (in) {
+      float v[8];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) v[u][e] *= scale;
-      }
-      store8(D + row * ldd, k0 + 256 * u, K, v[u]);
+      for (int e = 0; e < 8; ++e) v[e] = in ? w[u].value(e) * scale : 0.0f;
+      store8(D + row * ldd, k0 + 256 * u, K, v);
     }
   }
 }
@@ -205,6 +204,7 @@ struct EmbedGradArgs {
   const void* G;
   int64_t ldg;
   int n, vocab, K;
+  const int* ids;
   const int* order;       // rows by id
   const int* sorted;      // their ids, -1 for rows of none (last)
   const unsigned* marks;  // a bit for each id that occurs, or null: looked up in `sorted`
@@ -247,11 +247,11 @@ __device__ __forceinline__ void bulk_store(void* dst, uint32_t src, uint32_t byt
 }
 
 // Whether v is among the sorted ids (behind which those of no row lie as -1).
-__device__ __forceinline__ bool has_token(const EmbedGradArgs& p, int64_t v) {
-  int lo = 0, hi = p.n;
+__device__ __forceinline__ bool has_token(const int* sorted, int n, int64_t v) {
+  int lo = 0, hi = n;
   while (lo < hi) {
     const int mid = (lo + hi) / 2;
-    const int id = p.sorted[mid];
+    const int id = sorted[mid];
     if (id == v) return true;
     if (id >= 0 && id < v)
       lo = mid + 1;
@@ -266,8 +266,10 @@ __device__ __forceinline__ bool has_token(const EmbedGradArgs& p, int64_t v) {
 // with the sums of 32768 rows x 4096 in 128000.
 constexpr int kZeros = 8192;      // bytes
 
-template <class TD>
-__device__ __forceinline__ void clear_unused(const EmbedGradArgs& p, int64_t block, int64_t blocks) {
+// used(v): whether row v has a token.
+template <class TD, class F>
+__device__ __forceinline__ void clear_unused(const EmbedGradArgs& p, int64_t block, int64_t blocks,
+                                             F used) {
   __shared__ __align__(128) uint4 zeros[kZeros / 16];
   for (int i = threadIdx.x; i < kZeros / 16; i += blockDim.x) zeros[i] = make_uint4(0u, 0u, 0u, 0u);
   fence_proxy_async_smem();
@@ -278,8 +280,7 @@ __device__ __forceinline__ void clear_unused(const EmbedGradArgs& p, int64_t blo
   // (Rows far apart: a block's copies go out one after the other, and a small
   // table needs many blocks.)
   for (int64_t v = block + threadIdx.x * blocks; v < p.vocab; v += blocks * blockDim.x) {
-    if (p.marks != nullptr ? (__ldcg(p.marks + (v >> 5)) >> (v & 31)) & 1u : has_token(p, v))
-      continue;
+    if (used(v)) continue;
     uint8_t* d = reinterpret_cast<uint8_t*>(static_cast<TD*>(p.D) + v * p.ldd);
     for (int64_t at = 0; at < whole; at += kZeros)
       bulk_store(d + at, src, static_cast<uint32_t>(whole - at < kZeros ? whole - at : kZeros));
@@ -300,7 +301,10 @@ __global__ void __launch_bounds__(32 * kWarps) sum_runs_kernel(const EmbedGradAr
   const int64_t zeros = gridDim.x - (items + kWarps - 1) / kWarps;
   const int64_t before = blockIdx.x * zeros / gridDim.x;      // blocks of zeros
   if ((blockIdx.x + 1) * zeros / gridDim.x > before) {
-    clear_unused<TD>(p, before, zeros);
+    clear_unused<TD>(p, before, zeros, [&](int64_t v) -> bool {
+      if (p.marks != nullptr) return (__ldcg(p.marks + (v >> 5)) >> (v & 31)) & 1u;
+      return has_token(p.sorted, p.n, v);
+    });
     return;
   }
   const int64_t item = (blockIdx.x - before) * kWarps + (threadIdx.x >> 5);
@@ -366,6 +370,103 @@ __global__ void __launch_bounds__(32 * kWarps) sum_runs_kernel(const EmbedGradAr
     finish_run<TD, kAdd>(p, id, k, sum);
   else
     store8(p.parts + (2LL * c + (whole ? 1 : 0)) * p.ldp, k, p.K, sum);
+}
+
+// Very few tokens, in one launch: a block for each token and slice of the columns, of
+// which that of an id's first token sums all of them, in order; up to kRunOfWarp by
+// one warp, more by the four in turn.
+constexpr int kVeryFew = 1024;
+constexpr int kVeryFewBlocks = 1536;
+constexpr int kRunOfWarp = 32;
+
+template <class TG, class TD, bool kAdd>
+__global__ void __launch_bounds__(32 * kWarps) sum_few_kernel(const EmbedGradArgs p) {
+  __shared__ int4 ids4[kVeryFew / 4];
+  int* ids = reinterpret_cast<int*>(ids4);
+  __shared__ int list[kVeryFew];
+  __shared__ int counts[kWarps];
+  __shared__ float part[kWarps][32][8];
+  griddep_wait();
+  griddep_launch_dependents();
+  const int tid = static_cast<int>(threadIdx.x), warp = tid >> 5, lane = tid & 31;
+  const int n4 = (p.n + 3) / 4;
+  for (int i = tid; i < 4 * n4; i += 32 * kWarps) {
+    const int id = i < p.n ? p.ids[i] : -1;
+    ids[i] = static_cast<unsigned>(id) < static_cast<unsigned>(p.vocab) ? id : -1;
+  }
+  __syncthreads();
+  const int64_t items = static_cast<int64_t>(p.n) * p.slices;
+  const int64_t zeros = gridDim.x - items;
+  const int64_t before = blockIdx.x * zeros / gridDim.x;      // blocks of zeros
+  if ((blockIdx.x + 1) * zeros / gridDim.x > before) {
+    clear_unused<TD>(p, before, zeros, [&](int64_t v) -> bool {
+      bool found = false;
+      for (int i = 0; i < n4; ++i) {
+        const int4 q = ids4[i];
+        found |= q.x == v || q.y == v || q.z == v || q.w == v;
+      }
+      return found;
+    });
+    return;
+  }
+  const int item = static_cast<int>(blockIdx.x - before);
+  const int first = item / p.slices;
+  const int k = (item - first * p.slices) * kSlice + 8 * lane;
+  const int id = ids[first];
+  if (id < 0) return;
+  // The id's tokens in order: each warp has a quarter of them all.
+  const int quarter = (p.n + 32 * kWarps - 1) / (32 * kWarps) * 32;
+  const int lo = warp * quarter, hi = min(p.n, lo + quarter);
+  int found = 0;
+  bool earlier = false;
+  for (int i0 = lo; i0 < hi; i0 += 32) {
+    const bool same = i0 + lane < hi && ids[i0 + lane] == id;
+    earlier |= same && i0 + lane < first;
+    found += __popc(__ballot_sync(0xFFFFFFFFu, same));
+  }
+  if (lane == 0) counts[warp] = found;
+  if (__syncthreads_or(earlier)) return;   // another block's
+  int at = 0, count = 0;
+  for (int w = 0; w < kWarps; ++w) {
+    if (w < warp) at += counts[w];
+    count += counts[w];
+  }
+  for (int i0 = lo; i0 < hi; i0 += 32) {
+    const bool same = i0 + lane < hi && ids[i0 + lane] == id;
+    const unsigned votes = __ballot_sync(0xFFFFFFFFu, same);
+    if (same) list[at + __popc(votes & ((1u << lane) - 1u))] = i0 + lane;
+    at += __popc(votes);
+  }
+  __syncthreads();
+  const bool shared_out = count > kRunOfWarp;
+  if (!shared_out && warp != 0) return;
+  const TG* G = static_cast<const TG*>(p.G);
+  const int by = shared_out ? kWarps : 1;
+  float sum[8] = {};
+  if (k < p.K) {
+    for (int q0 = warp; q0 < count; q0 += kBatch * by) {
+      Eight<TG> v[kBatch];
+#pragma unroll
+      for (int u = 0; u < kBatch; ++u)
+        if (q0 + u * by < count) v[u].load(G + list[q0 + u * by] * p.ldg, k, p.K);
+#pragma unroll
+      for (int u = 0; u < kBatch; ++u)
+        if (q0 + u * by < count) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) sum[e] += v[u].value(e);
+        }
+    }
+  }
+  if (shared_out) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) part[warp][lane][e] = sum[e];
+    __syncthreads();
+    if (warp != 0) return;
+    for (int w = 1; w < kWarps; ++w)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) sum[e] += part[w][lane][e];
+  }
+  if (k < p.K) finish_run<TD, kAdd>(p, id, k, sum);
 }
 
 // Runs that cross the end of the chunk they begin in, as noted by their first
@@ -484,6 +585,12 @@ int launch_grad(const EmbedGradArgs& a, DeviceCtx* ctx, cudaStream_t stream) {
     const int64_t most = 8 * static_cast<int64_t>(ctx->num_sms);
     if (zero_blocks > most) zero_blocks = most;
   }
+  if (a.ids != nullptr) {
+    // (The zeros look every row up: 1000 tokens are 1000 comparisons a thread.)
+    return launch_chained(sum_few_kernel<TG, TD, kAdd>,
+                          static_cast<int64_t>(a.n) * a.slices + zero_blocks, 32 * kWarps, stream,
+                          0, a);
+  }
   const int64_t blocks =
       (static_cast<int64_t>(a.chunks) * a.slices + kWarps - 1) / kWarps + zero_blocks;
   if (blocks == 0) return TG_OK;
@@ -535,13 +642,13 @@ int embed_rows(const void* W, int64_t ldw, int64_t rows, const int32_t* ids, int
   rc = check_rows(D, ldd, K, esize(d_dtype));
   if (rc == TG_OK && rows > 0) rc = check_rows(W, ldw, K, 2);
   if (rc != TG_OK) return rc;
-  DeviceCtx* ctx = current_ctx();
-  if (!ctx) return TG_ERR_CUDA;
+  if (!current_ctx()) return TG_ERR_CUDA;
   cudaStream_t stream = static_cast<cudaStream_t>(cuda_stream);
   const int parts = static_cast<int>((K + 256 * kLookup - 1) / (256 * kLookup));
+  // A warp for each part (32768 rows x 4096 of 128000, f32: 126 us; with four pieces a
+  // lane 131; in a grid that stays, 150 to 200).
   int64_t blocks = (n * parts + 7) / 8;
-  const int64_t most = 8 * static_cast<int64_t>(ctx->num_sms);
-  if (blocks > most) blocks = most;
+  if (blocks > kMaxDim / 2) blocks = kMaxDim / 2;
   const uint16_t* w = static_cast<const uint16_t*>(W);
   const int v = static_cast<int>(rows), k = static_cast<int>(K);
   if (d_dtype == TG_D_BF16)
@@ -577,7 +684,10 @@ int embed_rows_grad(const void* G, int64_t ldg, int g_dtype, const int32_t* ids,
   a.scale = scale;
   a.D = D;
   a.ldd = ldd;
-  if (n > 0) {
+  a.slices = static_cast<int>((K + kSlice - 1) / kSlice);
+  if (n > 0 && n <= kVeryFew && n * a.slices <= kVeryFewBlocks) {
+    a.ids = ids;
+  } else if (n > 0) {
     const EmbedPlan plan = embed_plan(n, rows, K);
     if (static_cast<int64_t>(plan.chunks) * plan.slices > kMaxDim / 2) return TG_ERR_UNSUPPORTED;
     uint8_t* ws = static_cast<uint8_t*>(device_workspace(plan.bytes, stream, &rc));
@@ -608,7 +718,6 @@ int embed_rows_grad(const void* G, int64_t ldg, int g_dtype, const int32_t* ids,
     a.ldp = plan.ldp;
     a.chunk = plan.chunk;
     a.chunks = plan.chunks;
-    a.slices = plan.slices;
   }
   const bool add = accumulate != 0, g16 = g_dtype == TG_D_BF16, d16 = d_dtype == TG_D_BF16;
   if (g16 && d16) return launch_grad<uint16_t, uint16_t>(a, add, ctx, stream);

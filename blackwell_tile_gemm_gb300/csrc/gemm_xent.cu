@@ -111,10 +111,10 @@ int launch_xent_cfg(const XentOperands& o, const XentArgs& args, const XentTiles
   CUtensorMap tD = tA, tD2 = tA;
   if constexpr (kMode != kXentLoss) {
     const int64_t row_bytes = o.ld_dz * (C::kTwo ? 4 : 2);
-    rc = make_tensor_map_2d(&tD, bf, o.dz, o.ld_dz, a.M, row_bytes, 64, 32, sw);
+    rc = make_tensor_map_2d(&tD, bf, o.dz, o.ld_dz, a.padded, row_bytes, 64, 32, sw);
     if (rc != TG_OK) return rc;
     if constexpr (C::kTwo) {
-      rc = make_tensor_map_2d(&tD2, bf, static_cast<uint16_t*>(o.dz) + o.ld_dz, o.ld_dz, a.M,
+      rc = make_tensor_map_2d(&tD2, bf, static_cast<uint16_t*>(o.dz) + o.ld_dz, o.ld_dz, a.padded,
                               row_bytes, 64, 32, sw);
       if (rc != TG_OK) return rc;
     }
@@ -382,6 +382,7 @@ int gemm_bf16_xent_grad(const void* A, int64_t lda, const void* B, int64_t ldb,
   a.A = static_cast<const uint16_t*>(A);
   a.lda = lda;
   a.ld_copy = plan.ld_a;
+  a.padded = static_cast<int>(plan.rows);
   a.K = static_cast<int>(K);
   for (int64_t col0 = 0; col0 < N; col0 += plan.piece) {
     const int64_t n = N - col0 < plan.piece ? N - col0 : plan.piece;
@@ -424,8 +425,8 @@ int gemm_bf16_xent_grad(const void* A, int64_t lda, const void* B, int64_t ldb,
       if (rc != TG_OK) return rc;
     }
     if (weights) {
-      // (Two terms: 2 M rows of dz against as many of A.)
-      const int64_t terms_rows = plan.terms * M;
+      // (Two terms: twice the rows of dz against as many of A.)
+      const int64_t terms_rows = plan.terms * plan.rows;
       GroupedArgs g = grouped_args(ctx);
       g.M = static_cast<int>(terms_rows);
       g.wide = static_cast<int>(K);

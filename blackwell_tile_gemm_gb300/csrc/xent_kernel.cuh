@@ -39,6 +39,7 @@ enum : uint32_t {
 
 struct XentArgs {
   int M, N;            // rows; columns of this launch
+  int padded;          // kXentGrad: rows of dz and of the copy (zeros from M on)
   int col0, vocab;     // vocabulary index of its first column; size of the vocabulary
   int num_k_blocks;    // stages of 64 terms
   int num_m_tiles;     // of kCtaGroup * 128 rows
@@ -146,8 +147,8 @@ __device__ __forceinline__ void copy_learned_rows(const XentArgs& p, int warp, i
                                                   int lane) {
   const int whole = p.K / 8;
 #pragma unroll 1
-  for (int i = warp; i < p.M; i += warps) {
-    const int t = p.targets[i];
+  for (int i = warp; i < p.padded; i += warps) {
+    const int t = i < p.M ? p.targets[i] : -1;
     const bool learned = t >= 0 && t < p.vocab;
     const uint16_t* s = p.A + i * p.lda;
     uint16_t* d = p.copy + static_cast<int64_t>(i) * kTerms * p.ld_copy;
@@ -532,7 +533,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
           }
           fence_proxy_async_smem();
           __syncwarp();
-          // Rows past M are clipped; dz has whole boxes of columns.
+          // Rows past the last are clipped; dz has whole boxes of columns.
           if (lane == 0) {
             tma_store_2d_hint(map, stg, tile0 + box0, row0, pol_d);
             bulk_commit_group();
@@ -547,7 +548,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
             float z[64];
             xent_read<false>(t_row + 64 * b, z);
             gradient(z, 64 * b);
-            if (row0 < p.M) store(z, 64 * b, &tmD);
+            if (row0 < p.padded) store(z, 64 * b, &tmD);
           }
           hand_back();
         } else {
@@ -573,7 +574,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
             const int b = half + 2 * i;
             if (b >= boxes) continue;
             gradient(z[i], 64 * b);
-            if (row0 < p.M) {
+            if (row0 < p.padded) {
               store(z[i], 64 * b, &tmD);
               store(z[i], 64 * b, &tmD2);
             }

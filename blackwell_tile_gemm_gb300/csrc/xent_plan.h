@@ -74,9 +74,11 @@ inline XentLossPlan xent_loss_plan(int64_t M, int64_t N) {
 
 // Workspace of the gradient: the rows of A that have a target (the others as zeros),
 // dz of one piece of the vocabulary and the f32 sums of dA.  With two terms of dz a
-// row's second follows its first: [M][2][ld_dz].  Read as M rows twice as long, one
-// contraction of dA takes both (B's rows a second time); read as 2 M rows, so does
-// one of dB, with each row of A twice.
+// row's second follows its first: [rows][2][ld_dz].  Read as rows twice as long, one
+// contraction of dA takes both (B's rows a second time); read as twice the rows, so
+// does one of dB, with each row of A twice.  Zeros fill the rows up to whole stages
+// of that contraction: a ragged one takes a detour (1000 rows x 50304 x 1024 89 us,
+// 1024 rows 74).
 //
 // Pieces are as wide as kXentDzBytes allow, but at least kXentLeastPiece columns:
 // every piece adds its share of dA to all of it in memory, 8 bytes for 2 * width
@@ -86,6 +88,7 @@ constexpr int64_t kXentLeastPiece = 8192;
 
 struct XentGradPlan {
   int terms;          // of dz: 2 where the gradients are f32
+  int64_t rows;       // of dz: M in steps of 64
   int64_t piece;      // columns of a piece, a multiple of 256 (or all)
   int64_t pieces;
   int64_t ld_a, ld_dz, ld_sum;
@@ -94,7 +97,8 @@ struct XentGradPlan {
 inline XentGradPlan xent_grad_plan(int64_t M, int64_t N, int64_t K, bool bf16) {
   XentGradPlan q{};
   q.terms = bf16 ? 1 : 2;
-  int64_t most = kXentDzBytes / (2 * q.terms * M) / 256 * 256;
+  q.rows = xent_up(M, 64);
+  int64_t most = kXentDzBytes / (2 * q.terms * q.rows) / 256 * 256;
   if (most < kXentLeastPiece) most = kXentLeastPiece;
   q.pieces = (N + most - 1) / most;
   q.piece = q.pieces == 1 ? N : xent_up((N + q.pieces - 1) / q.pieces, 256);
@@ -102,8 +106,8 @@ inline XentGradPlan xent_grad_plan(int64_t M, int64_t N, int64_t K, bool bf16) {
   q.ld_a = xent_up(K, 64);
   q.ld_dz = xent_up(q.piece, 64);
   q.ld_sum = xent_up(K, 4);
-  q.off_dz = static_cast<size_t>(xent_up(2 * q.terms * M * q.ld_a, 1024));
-  q.off_sum = q.off_dz + static_cast<size_t>(xent_up(2 * q.terms * M * q.ld_dz, 1024));
+  q.off_dz = static_cast<size_t>(xent_up(2 * q.terms * q.rows * q.ld_a, 1024));
+  q.off_sum = q.off_dz + static_cast<size_t>(xent_up(2 * q.terms * q.rows * q.ld_dz, 1024));
   q.bytes = q.off_sum + (bf16 && q.pieces > 1 ? static_cast<size_t>(4 * M * q.ld_sum) : 0);
   return q;
 }
