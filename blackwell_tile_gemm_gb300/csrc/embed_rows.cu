@@ -537,11 +537,12 @@ __global__ void __launch_bounds__(256) join_runs_kernel(const EmbedGradArgs p) {
   }
 }
 
-// Sorted rows per block: about a thousand chunks, so that a run as long as all of
-// them still joins in little time, and no block has few rows for its launch.
+// Sorted rows per warp: at most about a thousand chunks, so that a run as long as all
+// of them still joins in little time, and no chunk of fewer than kBatch.
+constexpr int64_t kMostChunks = 1024;
 int grad_chunk(int64_t n) {
   int64_t c = kBatch;
-  while (c * 1024 < n) c *= 2;
+  while (c * kMostChunks < n) c *= 2;
   return static_cast<int>(c);
 }
 
@@ -569,10 +570,12 @@ EmbedPlan embed_plan(int64_t n, int64_t rows, int64_t K) {
   q.other = take(list);
   q.sorted = take(list);
   q.count = take(4 * ((size_t{1} << kSortDigit) + 1));
-  q.notes = take(8 * static_cast<size_t>(q.chunks) * static_cast<size_t>(q.slices));
+  // (As many chunks as fewer tokens may have: it grows with n.)
+  const int64_t most = (n + kBatch - 1) / kBatch < kMostChunks ? (n + kBatch - 1) / kBatch : kMostChunks;
+  q.notes = take(8 * static_cast<size_t>(most) * static_cast<size_t>(q.slices));
   q.marks = take(kNoteCount + static_cast<size_t>((rows + 31) / 32 * 4));
   q.hist = take(sort_ids_workspace_bytes(n));
-  q.parts = take(q.chunks > 1 ? static_cast<size_t>(8 * q.chunks) * static_cast<size_t>(q.ldp) : 0);
+  q.parts = take(8 * static_cast<size_t>(most) * static_cast<size_t>(q.ldp));
   q.bytes = at;
   return q;
 }

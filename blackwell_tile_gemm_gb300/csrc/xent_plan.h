@@ -13,6 +13,10 @@ constexpr int kXentSms = 152;
 // Up to this many rows run as single CTAs.
 constexpr int64_t kXentFewRows = 128;
 
+// Fewest columns of a tile.
+constexpr int64_t kXentFewLeast = 48;
+constexpr int64_t kXentLeast = 128;
+
 inline int64_t xent_up(int64_t a, int64_t b) { return (a + b - 1) / b * b; }
 
 struct XentTiles {
@@ -30,7 +34,7 @@ inline XentTiles xent_tiles(int64_t M, int64_t N, int step) {
   const bool few = M <= kXentFewRows;
   const int64_t units = few ? kXentSms : kXentSms / 2;
   const int64_t mt = few ? 1 : (M + 255) / 256;
-  const int64_t least = few ? (step > 48 ? step : 48) : (step > 64 ? step : 64);
+  const int64_t least = few ? (step > kXentFewLeast ? step : kXentFewLeast) : kXentLeast;
   int64_t best = 0, bn = 256;
   for (int64_t c = 256; c >= least; c -= step) {
     const int64_t waves = (mt * ((N + c - 1) / c) + units - 1) / units;
@@ -59,7 +63,9 @@ inline int xent_ring(int a_box, int b_box, int* b_bytes, int* stages) {
   return a_bytes;
 }
 
-// Workspace of the loss: [2 * n_tiles][M] pairs, then the targets' logits.
+// Workspace of the loss: [2 * n_tiles][M] pairs, then the targets' logits.  `bytes` is
+// what the narrowest tiles would take, for this many rows or for few: it grows with M
+// and N, so that a reservation for the largest call serves all smaller ones.
 struct XentLossPlan {
   XentTiles tiles;
   size_t off_z, bytes;
@@ -67,7 +73,9 @@ struct XentLossPlan {
 inline XentLossPlan xent_loss_plan(int64_t M, int64_t N) {
   XentLossPlan q{};
   q.tiles = xent_tiles(M, N, M <= kXentFewRows ? 16 : 32);   // (MMAs of a pair: 16 a CTA)
-  q.off_z = static_cast<size_t>(xent_up(16 * static_cast<int64_t>(q.tiles.n_tiles) * M, 256));
+  const int64_t few = (N + kXentFewLeast - 1) / kXentFewLeast * (M < kXentFewRows ? M : kXentFewRows);
+  const int64_t many = M > kXentFewRows ? (N + kXentLeast - 1) / kXentLeast * M : 0;
+  q.off_z = static_cast<size_t>(xent_up(16 * (few > many ? few : many), 256));
   q.bytes = q.off_z + static_cast<size_t>(4 * M);
   return q;
 }
@@ -91,23 +99,27 @@ struct XentGradPlan {
   int64_t rows;       // of dz: M in steps of 64
   int64_t piece;      // columns of a piece, a multiple of 256 (or all)
   int64_t pieces;
-  int64_t ld_a, ld_dz, ld_sum;
+  int64_t ld_a, ld_sum;
   size_t off_dz, off_sum, bytes;
 };
 inline XentGradPlan xent_grad_plan(int64_t M, int64_t N, int64_t K, bool bf16) {
   XentGradPlan q{};
   q.terms = bf16 ? 1 : 2;
   q.rows = xent_up(M, 64);
-  int64_t most = kXentDzBytes / (2 * q.terms * q.rows) / 256 * 256;
+  const int64_t column = 2 * q.terms * q.rows;               // bytes of dz
+  int64_t most = kXentDzBytes / column / 256 * 256;
   if (most < kXentLeastPiece) most = kXentLeastPiece;
   q.pieces = (N + most - 1) / most;
   q.piece = q.pieces == 1 ? N : xent_up((N + q.pieces - 1) / q.pieces, 256);
   q.pieces = (N + q.piece - 1) / q.piece;
   q.ld_a = xent_up(K, 64);
-  q.ld_dz = xent_up(q.piece, 64);
   q.ld_sum = xent_up(K, 4);
-  q.off_dz = static_cast<size_t>(xent_up(2 * q.terms * q.rows * q.ld_a, 1024));
-  q.off_sum = q.off_dz + static_cast<size_t>(xent_up(2 * q.terms * q.rows * q.ld_dz, 1024));
+  // (Room for the widest piece there could be: it grows with M and N.)
+  const int64_t wide = column * kXentLeastPiece > kXentDzBytes ? column * kXentLeastPiece
+                                                               : kXentDzBytes;
+  const int64_t all = column * xent_up(N, 64);
+  q.off_dz = static_cast<size_t>(xent_up(column * q.ld_a, 1024));
+  q.off_sum = q.off_dz + static_cast<size_t>(xent_up(all < wide ? all : wide, 1024));
   q.bytes = q.off_sum + (bf16 && q.pieces > 1 ? static_cast<size_t>(4 * M * q.ld_sum) : 0);
   return q;
 }
