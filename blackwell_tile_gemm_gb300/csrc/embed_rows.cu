@@ -6,8 +6,8 @@
 // Both are bound by HBM: every row is moved once.  The lookup gives each warp a
 // part of a row.  The gradient must not depend on the order in which anything
 // runs, so the rows are first sorted by id (stable; few by counting the smaller
-// ones, many digit by digit with the sort of group_rows.cu; very few not at all: a
-// block looks its row's id up among all), and a run of equal ids is summed in the
+// ones, more by merging sorted chunks, many digit by digit with the sort of
+// group_rows.cu; very few not at all: a block looks its row's id up among all), and a run of equal ids is summed in the
 // order of its rows, in f32.  Runs are as uneven as words are: the
 // sorted rows are cut into chunks of equal length, a warp for each and 256 columns;
 // a run that lies inside its chunk goes straight to dW, what crosses a chunk's end
@@ -198,6 +198,123 @@ __global__ void __launch_bounds__(1024) rank_ids_kernel(const int* ids, int n, i
     order[rank] = i;
     sorted[rank] = id < vocab ? id : -1;
   }
+}
+
+// Up to kMergeTokens in two launches.  The first sorts chunks of 1024 in the same way
+// (64 rows a block); the second holds the sorted chunks' ids in shared memory, and an
+// id's place is the sum of its places in all of them, one lane's binary search in
+// each: behind equal ids in the chunks before its own, before those in later ones.
+// (32768 ids, two digits of the counting sort: 30 us for four launches.)
+constexpr int kChunkBits = 10;
+constexpr int kChunkIds = 1 << kChunkBits;
+constexpr int kMergeTokens = 48 * kChunkIds;
+constexpr int64_t kMergeRows = (int64_t{1} << (32 - kChunkBits)) - 1;
+
+__global__ void __launch_bounds__(1024) sort_chunks_kernel(const int* ids, int n, int vocab,
+                                                           int* chunk_ids, int* chunk_rows,
+                                                           int* note_count) {
+  __shared__ uint4 keys4[kChunkIds / 4];
+  uint32_t* keys = reinterpret_cast<uint32_t*>(keys4);
+  griddep_wait();
+  griddep_launch_dependents();
+  const int tid = static_cast<int>(threadIdx.x);
+  const int base = static_cast<int>(blockIdx.x) / (kChunkIds / 64) * kChunkIds;
+  uint32_t key = 0xFFFFFFFFu;
+  if (base + tid < n) {
+    const int id = ids[base + tid];
+    const bool in = static_cast<unsigned>(id) < static_cast<unsigned>(vocab);
+    key = static_cast<uint32_t>(in ? id : vocab) << kChunkBits | static_cast<uint32_t>(tid);
+  }
+  keys[tid] = key;
+  if (blockIdx.x == 0 && tid == 0) *note_count = 0;
+  __syncthreads();
+  const int i = static_cast<int>(blockIdx.x) % (kChunkIds / 64) * 64 + tid / 16;
+  const uint32_t mine = keys[i];
+  int rank = 0;
+#pragma unroll 4
+  for (int j = tid % 16; j < kChunkIds / 4; j += 16) {
+    const uint4 k = keys4[j];
+    rank += (k.x < mine) + (k.y < mine) + (k.z < mine) + (k.w < mine);
+  }
+#pragma unroll
+  for (int d = 8; d > 0; d /= 2) rank += __shfl_xor_sync(0xFFFFFFFFu, rank, d);
+  if (base + i < n && tid % 16 == 0) {
+    chunk_ids[base + rank] = static_cast<int>(mine >> kChunkBits);
+    chunk_rows[base + rank] = base + i;
+  }
+}
+
+__global__ void __launch_bounds__(1024) merge_chunks_kernel(const int* chunk_ids,
+                                                            const int* chunk_rows, int n, int vocab,
+                                                            int* order, int* sorted) {
+  // (Chunks a word further apart than they are long: the lanes' searches, each in its
+  // own, would else meet in one bank: 32768 ids 40 us.)
+  extern __shared__ int ids[];
+  constexpr int kStride = kChunkIds + 1;
+  griddep_wait();
+  griddep_launch_dependents();
+  const int tid = static_cast<int>(threadIdx.x), lane = tid & 31;
+  for (int i0 = tid; i0 < n; i0 += 8 * 1024) {
+    int v[8];
+#pragma unroll
+    for (int u = 0; u < 8; ++u) v[u] = i0 + 1024 * u < n ? __ldcg(chunk_ids + i0 + 1024 * u) : 0;
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+      const int i = i0 + 1024 * u;
+      if (i < n) ids[(i >> kChunkBits) * kStride + (i & (kChunkIds - 1))] = v[u];
+    }
+  }
+  __syncthreads();
+  const int chunks = (n + kChunkIds - 1) >> kChunkBits;
+  for (int e = static_cast<int>(blockIdx.x) * 32 + (tid >> 5); e < n;
+       e += static_cast<int>(gridDim.x) * 32) {
+    const int own = e >> kChunkBits, id = ids[own * kStride + (e & (kChunkIds - 1))];
+    int rank = 0;
+    for (int c = lane; c < chunks; c += 32) {
+      if (c == own) {
+        rank += e & (kChunkIds - 1);
+        continue;
+      }
+      // The first place whose id is above (chunks before) or not below (behind).
+      const int bound = c < own ? id : id - 1;
+      const int* at = ids + c * kStride;
+      int lo = 0, hi = min(kChunkIds, n - (c << kChunkBits));
+      while (lo < hi) {
+        const int mid = (lo + hi) / 2;
+        if (at[mid] <= bound)
+          lo = mid + 1;
+        else
+          hi = mid;
+      }
+      rank += lo;
+    }
+    rank = __reduce_add_sync(0xFFFFFFFFu, rank);
+    if (lane == 0) {
+      order[rank] = __ldcg(chunk_rows + e);
+      sorted[rank] = id < vocab ? id : -1;
+    }
+  }
+}
+
+int launch_merge_sort(const int* ids, int n, int vocab, int* order, int* sorted, int* chunk_ids,
+                      int* chunk_rows, int* note_count, cudaStream_t stream, DeviceCtx* ctx) {
+  static std::atomic<int> prepared[64];
+  if (prepared[ctx->device].load(std::memory_order_acquire) == 0) {
+    const cudaError_t e = cudaFuncSetAttribute(
+        merge_chunks_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        4 * (kMergeTokens + kMergeTokens / kChunkIds));
+    if (e != cudaSuccess) return cuda_fail(e);
+    prepared[ctx->device].store(1, std::memory_order_release);
+  }
+  // (Whole chunks of 16 blocks; those past the last row have nothing to place.)
+  int rc = launch_chained(sort_chunks_kernel, (n + 63) / 64, 1024, stream, 0, ids, n, vocab,
+                          chunk_ids, chunk_rows, note_count);
+  if (rc != TG_OK) return rc;
+  const int blocks = (n + 31) / 32 < ctx->num_sms ? (n + 31) / 32 : ctx->num_sms;
+  return launch_chained(merge_chunks_kernel, blocks, 1024, stream,
+                        static_cast<size_t>(4 * (n + (n + kChunkIds - 1) / kChunkIds)),
+                        static_cast<const int*>(chunk_ids),
+                        static_cast<const int*>(chunk_rows), n, vocab, order, sorted);
 }
 
 struct EmbedGradArgs {
@@ -551,7 +668,7 @@ constexpr size_t kNoteCount = 256;   // bytes
 struct EmbedPlan {
   int chunk, chunks, slices;
   int64_t ldp;
-  size_t other, sorted, count, notes, marks, hist, parts, bytes;   // (marks: the count before)
+  size_t other, rows, sorted, count, notes, marks, hist, parts, bytes;   // (marks: the count before)
 };
 EmbedPlan embed_plan(int64_t n, int64_t rows, int64_t K) {
   EmbedPlan q{};
@@ -568,6 +685,7 @@ EmbedPlan embed_plan(int64_t n, int64_t rows, int64_t K) {
   const size_t list = static_cast<size_t>(4 * n);
   take(list);
   q.other = take(list);
+  q.rows = take(n < kMergeTokens ? list : 4 * kMergeTokens);
   q.sorted = take(list);
   q.count = take(4 * ((size_t{1} << kSortDigit) + 1));
   // (As many chunks as fewer tokens may have: it grows with n.)
@@ -703,6 +821,10 @@ int embed_rows_grad(const void* G, int64_t ldg, int g_dtype, const int32_t* ids,
       rc = launch_chained(rank_ids_kernel, (n + 63) / 64, 1024, stream,
                           static_cast<size_t>((n + 3) / 4 * 16), ids, static_cast<int>(n),
                           static_cast<int>(rows), order, sorted, a.note_count);
+    } else if (n <= kMergeTokens && rows <= kMergeRows) {
+      rc = launch_merge_sort(ids, static_cast<int>(n), static_cast<int>(rows), order, sorted,
+                             reinterpret_cast<int*>(ws + plan.other),
+                             reinterpret_cast<int*>(ws + plan.rows), a.note_count, stream, ctx);
     } else {
       unsigned* marks =
           accumulate ? nullptr : reinterpret_cast<unsigned*>(ws + plan.marks + kNoteCount);

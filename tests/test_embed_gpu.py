@@ -96,7 +96,8 @@ def half(dtype):
     (1, 1, 1), (1, 7, 8), (9, 5, 24), (100, 40, 1001), (2048, 512, 64), (2049, 513, 72),
     (5000, 100, 1032), (3000, 40000, 136), (20000, 300000, 40), (70000, 20, 16),
     (7, 262145, 8), (64, 1, 2056), (1024, 600, 1100), (1024, 600, 1025), (1030, 600, 200),
-    (8192, 3000, 40), (8193, 3000, 40), (900, 524288, 16), (1500, 524287, 16), (1500, 524288, 16)])
+    (8192, 3000, 40), (8193, 3000, 40), (900, 524288, 16), (1500, 524287, 16), (1500, 524288, 16),
+    (9217, 900, 40), (49152, 70000, 8), (49153, 70000, 8), (33333, 4194303, 8), (9000, 4194304, 8)])
 @pytest.mark.parametrize("kind", ["uneven", "one", "spread"])
 def test_gradient(tg, n, rows, K, kind):
     import torch
@@ -154,7 +155,7 @@ def test_long_runs_join_in_order(tg):
     """Whole numbers: every order of f32 sums is exact, and none is lost or doubled."""
     import torch
     gen = torch.Generator(device="cuda").manual_seed(2)
-    for n in (15, 16, 17, 97, 1023, 1024, 1025, 8191, 8192, 8193, 100000):
+    for n in (15, 16, 17, 97, 1023, 1024, 1025, 8191, 8192, 8193, 49152, 49153, 100000):
         G = torch.randint(-3, 4, (n, 40), generator=gen, device="cuda").float()
         ids = (torch.arange(n, device="cuda") * 3 // n).int()      # three runs
         D = tg.embed_rows_grad(G, ids, 5)
