@@ -112,6 +112,7 @@ struct GroupedArgs {
   int64_t ldd;
   int64_t group_stride_d;  // wgrad
   int add;                 // kAdd: D += instead of D =
+  int tile_cols;           // kAdd: most columns of a tile (a multiple of 32, at most kTileN)
   int wrap;                // kAdd: contraction index from which the wide operand's rows
                            // begin again (a multiple of 64; the column operand's do not)
   Epi epi;                 // bias: [groups][wide]
@@ -268,6 +269,9 @@ struct GroupWalk {
   // The group found last: its tiles [begin, end), rows [r0, r1), column tiles.
   int begin, end, r0, r1, group, nct, size;
 
+  static __device__ __forceinline__ int tile_cols(const GroupedArgs& p) {
+    return C::kAdd ? p.tile_cols : C::kTileN;
+  }
   __device__ __forceinline__ void load(const GroupedArgs& p, int lane) {
     const int g = g0 + lane;
     int end = lo0;
@@ -293,7 +297,7 @@ struct GroupWalk {
     if constexpr (C::kColMn) {
       if (g < p.groups) tiles = p.num_wide_tiles * p.num_col_tiles;
     } else {
-      tiles = (hi - lo + C::kTileN - 1) / C::kTileN * p.num_wide_tiles;
+      tiles = (hi - lo + tile_cols(p) - 1) / tile_cols(p) * p.num_wide_tiles;
     }
     incl = tiles;
 #pragma unroll
@@ -347,7 +351,7 @@ struct GroupWalk {
     begin = t0 + (src > 0 ? before : 0);
     end = t0 + __shfl_sync(0xFFFFFFFFu, incl, src);
     group = C::kMode == kAdapter ? 0 : g0 + src;   // (adapters: one shared operand)
-    nct = C::kColMn ? p.num_col_tiles : (r1 - r0 + C::kTileN - 1) / C::kTileN;
+    nct = C::kColMn ? p.num_col_tiles : (r1 - r0 + tile_cols(p) - 1) / tile_cols(p);
     // The group's rows in nct tiles of equal size (a multiple of kColStep).
     size = C::kMode == kAdapterDown || C::kColMn
                ? C::kTileN
