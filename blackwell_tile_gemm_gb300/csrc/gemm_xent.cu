@@ -272,8 +272,9 @@ int check_rows(const void* p, int64_t ld, int64_t width, int esize) {
 int check_xent(int64_t M, int64_t N, int64_t K, float scale, unsigned flags) {
   if (M < 0 || N < 0 || K < 0 || M > kMaxDim || N > kMaxDim || K > kMaxDim)
     return TG_ERR_INVALID_ARG;
-  // (A negative scale would make the smallest product the largest logit.)
-  if (!(scale > 0.0f) || scale > 3.0e38f) return TG_ERR_INVALID_ARG;
+  // (A negative scale would make the smallest product the largest logit; log2(e)
+  // times the largest is still finite.)
+  if (!(scale > 0.0f) || scale > 1.0e38f) return TG_ERR_INVALID_ARG;
   if (flags != 0) return TG_ERR_UNSUPPORTED;
   if (M > kGroupedMaxExtent || N > kGroupedMaxExtent || K > kGroupedMaxExtent)
     return TG_ERR_UNSUPPORTED;

@@ -392,8 +392,9 @@ int gemm_bf16_lora(const void* A, int64_t lda, const void* B, int64_t ldb, const
 /*
  * The two ends of a language model's training step: its loss over a vocabulary,
  * the rows of its tokens, and the balance of its router.  These calls take the
- * current stream like all others; vectors (targets, ids, losses, ...) need only
- * their type's alignment.  Results have the same bits every time, with one
+ * stream they are given like all others; vectors (targets, ids, losses, ...) need
+ * only their type's alignment.  Several kernels of a call share the stream's
+ * workspace: calls of two host threads on one stream must not overlap.  Results have the same bits every time, with one
  * exception: gemm_bf16_xent_grad's products may be split as described above
  * ("Products whose weights change with the row").
  */
@@ -406,7 +407,7 @@ int gemm_bf16_lora(const void* A, int64_t lda, const void* B, int64_t ldb, const
  *   A       : device, bf16 [M, K], row stride lda (tokens).
  *   B       : device, bf16 [N, K], row stride ldb.
  *   targets : device, int32 [M].
- *   scale   : positive and finite (a temperature's inverse); otherwise
+ *   scale   : positive, at most 1e38 (a temperature's inverse); otherwise
  *             TG_ERR_INVALID_ARG.
  *   loss, lse : device, f32 [M].  flags: 0.
  * M, N and K are at most 2^31 - 4096.  N = 0 gives lse = -inf; K = 0 gives
@@ -421,8 +422,8 @@ int gemm_bf16_xent(const void* A, int64_t lda, const void* B, int64_t ldb, const
  * gemm_bf16_xent_grad -- the gradients of sum_i grad[i] * loss[i]:
  *   dz[i, j] = grad[i] * scale * (exp(z[i, j] - lse[i]) - [j = targets[i]])
  *   dA = dz * B,  dB = dz^T * A
- * Rows without a target have dz = 0: their row of dA is 0 and they have no part in
- * dB, whatever their row of A holds.  z is computed again in pieces of the
+ * Rows without a target have dz = 0: their row of dA is 0 (B being finite) and they
+ * have no part in dB, whatever their row of A, lse and grad hold.  z is computed again in pieces of the
  * vocabulary; dz passes to the products as bf16, for f32 gradients as two bf16
  * terms (17 significant bits).
  *   lse     : device, f32 [M], of gemm_bf16_xent with the same A, B and scale.

@@ -23,7 +23,7 @@ SIZES = [(dict(M=-1), BAD), (dict(N=-1), BAD), (dict(K=-1), BAD), (dict(M=2 ** 3
          (dict(N=2 ** 31 - 4095, ldb=2 ** 31), UNSUP), (dict(M=2 ** 31 - 1), UNSUP),
          (dict(M=2 ** 31 - 4096, N=2 ** 31 - 4096), UNSUP),          # tiles
          (dict(scale=0.0), BAD), (dict(scale=-1.0), BAD), (dict(scale=math.nan), BAD),
-         (dict(scale=math.inf), BAD), (dict(flags=1), UNSUP), (dict(t=None), BAD),
+         (dict(scale=math.inf), BAD), (dict(scale=2e38), BAD), (dict(flags=1), UNSUP), (dict(t=None), BAD),
          (dict(A=None), BAD), (dict(B=None), BAD), (dict(lda=56), BAD), (dict(ldb=56), BAD),
          (dict(lda=68), ALIGN), (dict(ldb=68), ALIGN), (dict(A=A16 + 2), ALIGN),
          (dict(B=A16 + 8), ALIGN), (dict(lse=None), BAD)]
