@@ -171,6 +171,7 @@ __device__ __forceinline__ float softmax_row(float (&z)[kV], float* shared) {
 template <class T, bool kVec, int kLanes, class F, class N>
 __device__ __forceinline__ void walk_rows(const BalanceArgs& p, float* shared, F f, N count) {
   constexpr int kR = rows_together<T>();
+  constexpr int kIds = kLanes < 16 ? 2 : 1;
   constexpr int kGroups = block_threads<kLanes>() / kLanes;
   const int lane = static_cast<int>(threadIdx.x) % kLanes;
   const int all = static_cast<int>(gridDim.x) * kGroups;
@@ -183,11 +184,18 @@ __device__ __forceinline__ void walk_rows(const BalanceArgs& p, float* shared, F
   const T* at = static_cast<const T*>(p.logits) + mine * p.ld;
   const int64_t stride = all * p.ld;
   Logits<T> next[kR];
-  auto load = [&](int64_t row) {
+  int next_id[kR][kIds];      // choices lane and lane + kLanes
+  auto load = [&](int64_t row0) {
 #pragma unroll
     for (int r = 0; r < kR; ++r) {
-      next[r].template load<kVec, kLanes>(at, row + static_cast<int64_t>(r) * all < p.M, p.E, lane);
+      const int64_t row = row0 + static_cast<int64_t>(r) * all;
+      next[r].template load<kVec, kLanes>(at, row < p.M, p.E, lane);
       at += stride;
+#pragma unroll
+      for (int i = 0; i < kIds; ++i) {
+        const int c = lane + i * kLanes;
+        next_id[r][i] = row < p.M && c < p.choices ? p.ids[row * p.choices + c] : -1;
+      }
     }
   };
   load(mine);
@@ -198,14 +206,17 @@ __device__ __forceinline__ void walk_rows(const BalanceArgs& p, float* shared, F
     for (int r = 0; r < kR; ++r) {
       const int64_t row = first + static_cast<int64_t>(r) * all;
       some[r] = 0;
-      if (row < p.M)
-        for (int c = lane; c < p.choices; c += kLanes) {
-          const int id = p.ids[row * p.choices + c];
-          if (static_cast<unsigned>(id) < static_cast<unsigned>(p.E)) {
-            some[r] = 1;
-            count(id);
-          }
+      auto take = [&](int id) {
+        if (static_cast<unsigned>(id) < static_cast<unsigned>(p.E)) {
+          some[r] = 1;
+          count(id);
         }
+      };
+#pragma unroll
+      for (int i = 0; i < kIds; ++i) take(next_id[r][i]);
+      if (row < p.M)
+        for (int c = lane + kIds * kLanes; c < p.choices; c += kLanes)
+          take(p.ids[row * p.choices + c]);
 #pragma unroll
       for (int i = 0; i < kV; ++i) z[r][i] = next[r].value(i);
     }
@@ -230,6 +241,7 @@ __device__ __forceinline__ void finish_loss(const float* sum_of, const int* coun
                                             float* loss, int* counts, float* shares) {
   __shared__ int choice_part[32];
   __shared__ float loss_part[32];
+  __shared__ float2 scale_of;
   const int tid = static_cast<int>(threadIdx.x), warp = tid >> 5, lane = tid & 31;
   const int warps = static_cast<int>(blockDim.x) / 32;
   int choices = 0;
@@ -240,15 +252,23 @@ __device__ __forceinline__ void finish_loss(const float* sum_of, const int* coun
   choices = __reduce_add_sync(0xFFFFFFFFu, choices);
   if (lane == 0) choice_part[warp] = choices;
   __syncthreads();
-  int64_t total = 0;
-  for (int w = 0; w < warps; ++w) total += choice_part[w];
-  const int tokens = count_of[E];
+  if (tid == 0) {
+    // share_e / count_e as a sum of two f32 (one thread's 64-bit division: every
+    // thread's own took 3 us).
+    int64_t total = 0;
+    for (int w = 0; w < warps; ++w) total += choice_part[w];
+    const int tokens = count_of[E];
+    const double scale =
+        tokens > 0 ? static_cast<double>(E) / (static_cast<double>(total) * tokens) : 0.0;
+    scale_of = make_float2(static_cast<float>(scale),
+                           static_cast<float>(scale - static_cast<float>(scale)));
+  }
+  __syncthreads();
+  const float2 scale = scale_of;
   float l = 0.0f;
   for (int e = tid; e < E; e += blockDim.x) {
-    // (In 64 bits: a count, and the product below, may pass 2^24.)
-    const float s = tokens > 0 ? static_cast<float>(static_cast<double>(E) * count_of[e] /
-                                                    (static_cast<double>(total) * tokens))
-                               : 0.0f;
+    const float count = static_cast<float>(count_of[e]);
+    const float s = fmaf(count, scale.x, count * scale.y);
     shares[e] = s;
     l = fmaf(s, sum_of[e], l);
   }
@@ -285,13 +305,21 @@ __global__ void __launch_bounds__(block_threads<kLanes>(), 1)
         for (int i = 0; i < kV; ++i) sum[i] = fmaf(e[i], inv, sum[i]);
       },
       [&](int id) { atomicAdd(hist + id, 1); });   // (counts: any order gives them)
-  // Over the groups: all of their sums, then each expert's in order.
-  const int group = static_cast<int>(threadIdx.x) / kLanes;
-  constexpr int kGroups = block_threads<kLanes>() / kLanes;
+  // Over the groups of a warp, then all warps' sums, each expert's in order.
 #pragma unroll
-  for (int i = 0; i < kV; ++i) {
-    const int e = expert_of<T, kVec, kLanes>(lane, i);
-    if (e < p.E) sums_of[group * p.E + e] = sum[i];
+  for (int d = kLanes; d < 32; d *= 2) {
+#pragma unroll
+    for (int i = 0; i < kV; ++i) sum[i] += __shfl_xor_sync(0xFFFFFFFFu, sum[i], d);
+  }
+  constexpr int kParts = kLanes < 32 ? 32 : kLanes;       // lanes of a part
+  constexpr int kGroups = block_threads<kLanes>() / kParts;
+  const int group = static_cast<int>(threadIdx.x) / kParts;
+  if (static_cast<int>(threadIdx.x) % kParts < kLanes) {
+#pragma unroll
+    for (int i = 0; i < kV; ++i) {
+      const int e = expert_of<T, kVec, kLanes>(lane, i);
+      if (e < p.E) sums_of[group * p.E + e] = sum[i];
+    }
   }
   __syncthreads();
   const bool alone = gridDim.x == 1;
@@ -478,14 +506,19 @@ int balance_lanes(int E) {
 }
 
 // Blocks of a pass: one on each of 152 SMs (more would be more sums to join), every
-// group taking at least a row; one alone while that takes its groups no more than
-// four rows (500 rows of 64 experts: a launch less).
+// group taking at least a row.
 constexpr int64_t kMostBlocks = 152;
 int64_t balance_blocks(int64_t M, int E) {
   const int lanes = balance_lanes(E);
   const int64_t rows = lanes == kBlockLanes ? 1 : kThreads / lanes;
   const int64_t b = (M + rows - 1) / rows;
-  return b <= 4 ? 1 : b < kMostBlocks ? b : kMostBlocks;
+  return b < 1 ? 1 : b < kMostBlocks ? b : kMostBlocks;
+}
+// Of sums: one alone while that takes its groups no more than four rows (500 rows of
+// 64 experts: a launch less).
+int64_t sum_blocks(int64_t M, int E) {
+  const int64_t b = balance_blocks(M, E);
+  return b <= 4 ? 1 : b;
 }
 
 // Whether rows may be read (or written) 16 bytes at a time.
@@ -496,8 +529,9 @@ bool whole_pieces(const void* p, int64_t ld, int dtype) {
 template <class T, bool kVec, int kLanes>
 int launch_sums(const BalanceArgs& a, int64_t blocks, cudaStream_t stream) {
   constexpr int threads = block_threads<kLanes>();
-  // (43 KB at most: 512 experts in 20 groups)
-  const size_t smem = 4 * (static_cast<size_t>(a.E) + 1 + static_cast<size_t>(threads / kLanes) * a.E);
+  // (43 KB at most: 512 experts in 20 warps)
+  const size_t smem = 4 * (static_cast<size_t>(a.E) + 1 +
+                           static_cast<size_t>(threads / (kLanes < 32 ? 32 : kLanes)) * a.E);
   return launch_chained(balance_sums_kernel<T, kVec, kLanes>, blocks, threads, smem, 1, stream, a);
 }
 
@@ -553,7 +587,7 @@ int tg_balance_loss(const void* logits, int64_t ld, int dtype, const int32_t* id
   DeviceCtx* ctx = current_ctx();
   if (!ctx) return TG_ERR_CUDA;
   cudaStream_t stream = static_cast<cudaStream_t>(cuda_stream);
-  const int64_t blocks = balance_blocks(M, static_cast<int>(E));
+  const int64_t blocks = sum_blocks(M, static_cast<int>(E));
   float* sums = static_cast<float*>(device_workspace(balance_workspace_bytes(M, E), stream, &rc));
   if (sums == nullptr) return rc;
   BalanceArgs a{};
