@@ -32,7 +32,7 @@ SOURCES = ["api.cu", "gemm_bf16.cu", "gemm_blockscaled.cu", "gemm_fp4.cu", "gemm
 PROBE_SOURCES = ["probes.cu"]
 HEADERS = ["tg_ptx.cuh", "gemm_kernel.cuh", "gemm_launch.cuh", "tg_internal.h", "epilogue.cuh",
            "gemm_kinds.h", "grouped_ptx.cuh", "grouped_kernel.cuh", "grouped_launch.cuh",
-           "tail_plan.h", "xent_kernel.cuh", "xent_plan.h"]
+           "tail_plan.h", "xent_kernel.cuh", "xent_plan.h", "chained_launch.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

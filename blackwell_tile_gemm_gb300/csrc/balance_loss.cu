@@ -20,7 +20,7 @@
 // backward).
 #include <type_traits>
 
-#include "tg_internal.h"
+#include "chained_launch.cuh"
 #include "tg_ptx.cuh"
 
 using namespace tg;
@@ -476,27 +476,6 @@ __global__ void __launch_bounds__(block_threads<kLanes>(), 1)
       [](int) {});
 }
 
-template <class... P>
-int launch_chained(void (*kern)(P...), int64_t blocks, int threads, size_t smem, int cluster,
-                   cudaStream_t stream, P... args) {
-  cudaLaunchConfig_t cfg{};
-  cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = static_cast<unsigned>(cluster);
-  attr[1].val.clusterDim.y = 1;
-  attr[1].val.clusterDim.z = 1;
-  cfg.gridDim = dim3(static_cast<unsigned>(blocks), 1, 1);
-  cfg.blockDim = dim3(static_cast<unsigned>(threads), 1, 1);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = stream;
-  cfg.attrs = attr;
-  cfg.numAttrs = cluster > 1 ? 2 : 1;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, args...);
-  return e == cudaSuccess ? TG_OK : cuda_fail(e);
-}
-
 // Lanes of a row's group: 1, 4, 16 (up to 16, 64, 256 experts), 32 or a block.
 int balance_lanes(int E) {
   if (E > kGroupExperts) return kBlockLanes;
@@ -611,8 +590,7 @@ int tg_balance_loss(const void* logits, int64_t ld, int dtype, const int32_t* id
   if (rc != TG_OK || blocks == 1) return rc;
   return launch_chained(balance_join_kernel, kJoinCtas, kJoinThreads,
                         4 * static_cast<size_t>(2 * E + 1), kJoinCtas, stream,
-                        static_cast<const float*>(a.sums), static_cast<const int*>(a.counts_of),
-                        static_cast<int>(blocks), a.E, loss, counts, shares);
+                        a.sums, a.counts_of, static_cast<int>(blocks), a.E, loss, counts, shares);
 }
 
 int tg_balance_loss_grad(const void* logits, int64_t ld, int dtype, const int32_t* ids,

@@ -7,17 +7,17 @@
 // part of a row.  The gradient must not depend on the order in which anything
 // runs, so the rows are first sorted by id (stable; few by counting the smaller
 // ones, more by merging sorted chunks, many digit by digit with the sort of
-// group_rows.cu; very few not at all: a block looks its row's id up among all), and a run of equal ids is summed in the
-// order of its rows, in f32.  Runs are as uneven as words are: the
-// sorted rows are cut into chunks of equal length, a warp for each and 256 columns;
-// a run that lies inside its chunk goes straight to dW, what crosses a chunk's end
-// goes to the workspace as an f32 partial sum, and a second kernel adds a run's
-// partial sums in their order.  The rows of dW that no token has (nearly all of a
-// large table's) are written as zeros by further blocks of the first kernel,
-// meanwhile.
+// group_rows.cu; very few not at all: a block looks its row's id up among all), and
+// a run of equal ids is summed in the order of its rows, in f32.  Runs are as uneven
+// as words are: the sorted rows are cut into chunks of equal length, a warp for each
+// and 256 columns; a run that lies inside its chunk goes straight to dW, what
+// crosses a chunk's end goes to the workspace as an f32 partial sum, and a second
+// kernel adds a run's partial sums in their order.  The rows of dW that no token has
+// (nearly all of a large table's) are written as zeros by further blocks of the
+// first kernel, meanwhile.
 #include <atomic>
 
-#include "tg_internal.h"
+#include "chained_launch.cuh"
 #include "tg_ptx.cuh"
 
 using namespace tg;
@@ -28,22 +28,6 @@ namespace {
 constexpr int64_t kMaxDim = (int64_t{1} << 31) - 1;
 constexpr int64_t kMaxTokens = int64_t{1} << 30;   // as tg_group_rows
 constexpr int64_t kMostColumns = int64_t{256} * 65535;
-
-template <class K, class... T>
-int launch_chained(K kern, int64_t blocks, int threads, cudaStream_t stream, size_t smem, T... args) {
-  cudaLaunchConfig_t cfg{};
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.gridDim = dim3(static_cast<unsigned>(blocks), 1, 1);
-  cfg.blockDim = dim3(static_cast<unsigned>(threads), 1, 1);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = stream;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, args...);
-  return e == cudaSuccess ? TG_OK : cuda_fail(e);
-}
 
 // Eight values of a row, from column k on, as they lie in memory; what lies past
 // column K is neither read nor written.
@@ -307,14 +291,13 @@ int launch_merge_sort(const int* ids, int n, int vocab, int* order, int* sorted,
     prepared[ctx->device].store(1, std::memory_order_release);
   }
   // (Whole chunks of 16 blocks; those past the last row have nothing to place.)
-  int rc = launch_chained(sort_chunks_kernel, (n + 63) / 64, 1024, stream, 0, ids, n, vocab,
+  int rc = launch_chained(sort_chunks_kernel, (n + 63) / 64, 1024, 0, 1, stream, ids, n, vocab,
                           chunk_ids, chunk_rows, note_count);
   if (rc != TG_OK) return rc;
   const int blocks = (n + 31) / 32 < ctx->num_sms ? (n + 31) / 32 : ctx->num_sms;
-  return launch_chained(merge_chunks_kernel, blocks, 1024, stream,
-                        static_cast<size_t>(4 * (n + (n + kChunkIds - 1) / kChunkIds)),
-                        static_cast<const int*>(chunk_ids),
-                        static_cast<const int*>(chunk_rows), n, vocab, order, sorted);
+  return launch_chained(merge_chunks_kernel, blocks, 1024,
+                        static_cast<size_t>(4 * (n + (n + kChunkIds - 1) / kChunkIds)), 1, stream,
+                        chunk_ids, chunk_rows, n, vocab, order, sorted);
 }
 
 struct EmbedGradArgs {
@@ -709,17 +692,18 @@ int launch_grad(const EmbedGradArgs& a, DeviceCtx* ctx, cudaStream_t stream) {
   if (a.ids != nullptr) {
     // (The zeros look every row up: 1000 tokens are 1000 comparisons a thread.)
     return launch_chained(sum_few_kernel<TG, TD, kAdd>,
-                          static_cast<int64_t>(a.n) * a.slices + zero_blocks, 32 * kWarps, stream,
-                          0, a);
+                          static_cast<int64_t>(a.n) * a.slices + zero_blocks, 32 * kWarps, 0, 1,
+                          stream, a);
   }
   const int64_t blocks =
       (static_cast<int64_t>(a.chunks) * a.slices + kWarps - 1) / kWarps + zero_blocks;
   if (blocks == 0) return TG_OK;
-  int rc = launch_chained(sum_runs_kernel<TG, TD, kAdd>, blocks, 32 * kWarps, stream, 0, a);
+  int rc = launch_chained(sum_runs_kernel<TG, TD, kAdd>, blocks, 32 * kWarps, 0, 1, stream, a);
   if (rc != TG_OK || a.chunks < 2) return rc;
   const int64_t notes = static_cast<int64_t>(a.chunks - 1) * a.slices;
   const int64_t most = 4 * static_cast<int64_t>(ctx->num_sms);
-  return launch_chained(join_runs_kernel<TD, kAdd>, notes < most ? notes : most, 256, stream, 0, a);
+  return launch_chained(join_runs_kernel<TD, kAdd>, notes < most ? notes : most, 256, 0, 1,
+                        stream, a);
 }
 
 template <class TG, class TD>
@@ -773,9 +757,9 @@ int embed_rows(const void* W, int64_t ldw, int64_t rows, const int32_t* ids, int
   const uint16_t* w = static_cast<const uint16_t*>(W);
   const int v = static_cast<int>(rows), k = static_cast<int>(K);
   if (d_dtype == TG_D_BF16)
-    return launch_chained(embed_kernel<uint16_t>, blocks, 256, stream, 0, w, ldw, v, ids, n, k, parts,
+    return launch_chained(embed_kernel<uint16_t>, blocks, 256, 0, 1, stream, w, ldw, v, ids, n, k, parts,
                           scale, static_cast<uint16_t*>(D), ldd);
-  return launch_chained(embed_kernel<float>, blocks, 256, stream, 0, w, ldw, v, ids, n, k, parts,
+  return launch_chained(embed_kernel<float>, blocks, 256, 0, 1, stream, w, ldw, v, ids, n, k, parts,
                         scale, static_cast<float*>(D), ldd);
 }
 
@@ -818,9 +802,9 @@ int embed_rows_grad(const void* G, int64_t ldg, int g_dtype, const int32_t* ids,
     int* order = reinterpret_cast<int*>(ws);
     int* sorted = reinterpret_cast<int*>(ws + plan.sorted);
     if (n <= kFewTokens && rows <= kFewRows) {
-      rc = launch_chained(rank_ids_kernel, (n + 63) / 64, 1024, stream,
-                          static_cast<size_t>((n + 3) / 4 * 16), ids, static_cast<int>(n),
-                          static_cast<int>(rows), order, sorted, a.note_count);
+      rc = launch_chained(rank_ids_kernel, (n + 63) / 64, 1024,
+                          static_cast<size_t>((n + 3) / 4 * 16), 1, stream, ids, n, rows, order,
+                          sorted, a.note_count);
     } else if (n <= kMergeTokens && rows <= kMergeRows) {
       rc = launch_merge_sort(ids, static_cast<int>(n), static_cast<int>(rows), order, sorted,
                              reinterpret_cast<int*>(ws + plan.other),

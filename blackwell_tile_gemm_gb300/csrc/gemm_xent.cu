@@ -13,6 +13,7 @@
 // gradients as two bf16 terms (2^-17), in one contraction over both.
 #include <atomic>
 
+#include "chained_launch.cuh"
 #include "grouped_launch.cuh"
 #include "xent_kernel.cuh"
 #include "xent_plan.h"
@@ -21,21 +22,6 @@ using namespace tg;
 
 namespace tg {
 namespace {
-
-template <class K, class... T>
-int launch_chained(K kern, int64_t blocks, int threads, cudaStream_t stream, T... args) {
-  cudaLaunchConfig_t cfg{};
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.gridDim = dim3(static_cast<unsigned>(blocks), 1, 1);
-  cfg.blockDim = dim3(static_cast<unsigned>(threads), 1, 1);
-  cfg.stream = stream;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, args...);
-  return e == cudaSuccess ? TG_OK : cuda_fail(e);
-}
 
 // ---------------------------------------------------------------------------
 // The product
@@ -333,9 +319,9 @@ int gemm_bf16_xent(const void* A, int64_t lda, const void* B, int64_t ldb, const
   if (rc != TG_OK) return rc;
   int rows = 1;
   while (rows < 32 && rows * 2 * ctx->num_sms < m) rows *= 2;
-  return launch_chained(xent_finish_kernel, (M + rows - 1) / rows, kFinishThreads, stream,
-                        static_cast<const float2*>(a.parts), 2 * plan.tiles.n_tiles,
-                        static_cast<const float*>(a.target_z), targets, loss, lse, m, n, rows, a.scale, a.scale2);
+  return launch_chained(xent_finish_kernel, (M + rows - 1) / rows, kFinishThreads, 0, 1, stream,
+                        a.parts, 2 * plan.tiles.n_tiles, a.target_z, targets, loss, lse, m, n, rows,
+                        a.scale, a.scale2);
 }
 
 int gemm_bf16_xent_grad(const void* A, int64_t lda, const void* B, int64_t ldb,
@@ -451,8 +437,8 @@ int gemm_bf16_xent_grad(const void* A, int64_t lda, const void* B, int64_t ldb,
   if (rows && bf16 && plan.pieces > 1) {
     const int64_t blocks = (M * ((K + 3) / 4) + 255) / 256;
     rc = launch_chained(round_rows_kernel, blocks < 16 * ctx->num_sms ? blocks : 16 * ctx->num_sms,
-                        256, stream, static_cast<const float*>(sums), plan.ld_sum,
-                        static_cast<uint16_t*>(dA), ldda, m, static_cast<int>(K));
+                        256, 0, 1, stream, sums, plan.ld_sum, static_cast<uint16_t*>(dA), ldda, m,
+                        static_cast<int>(K));
   }
   return rc;
 }
