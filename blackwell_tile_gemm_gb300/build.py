@@ -27,7 +27,7 @@ PROBE_LIB = os.path.join(BUILD, "libtgemm_probes.so")
 SOURCES = ["api.cu", "gemm_bf16.cu", "gemm_blockscaled.cu", "gemm_fp4.cu", "gemm_skinny.cu",
            "gemm_gather.cu", "gemm_grouped.cu", "gemm_lora.cu", "group_rows.cu",
            "grouped_forward.cu", "grouped_dgrad.cu", "grouped_wgrad.cu", "grouped_adapter.cu",
-           "gemm_xent.cu", "grouped_dgrad_add.cu", "embed_rows.cu", "balance_loss.cu",
+           "gemm_xent.cu", "grouped_sliced.cu", "embed_rows.cu", "balance_loss.cu",
            "gemm_mxfp8_noalloc.cu", "transpose.cu"]
 PROBE_SOURCES = ["probes.cu"]
 HEADERS = ["tg_ptx.cuh", "gemm_kernel.cuh", "gemm_launch.cuh", "tg_internal.h", "epilogue.cuh",

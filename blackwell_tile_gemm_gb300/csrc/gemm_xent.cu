@@ -8,7 +8,8 @@
 // per row and 128 columns, which xent_finish_kernel joins.  Backward: the
 // vocabulary in pieces; for each, dz from the product made again, then the
 // grouped gradients' kernels on it: dA's share (added up in f32 over the pieces)
-// and the piece's rows of dB, which are complete.  dz passes between them as
+// and the piece's rows of dB, which are complete.  Where their tiles are few, both are
+// cut into slices of the contraction whose f32 sums are added in order.  dz passes between them as
 // bf16, rounded once at 2^-9, as any gradient of a bf16 layer is; for f32
 // gradients as two bf16 terms (2^-17), in one contraction over both.
 #include <atomic>
@@ -210,11 +211,14 @@ __global__ void xent_zero_kernel(const int* targets, float* loss, float* lse, in
 }
 
 // ---------------------------------------------------------------------------
-// dA's rounding
+// Sums of slices
 // ---------------------------------------------------------------------------
 
-__global__ void __launch_bounds__(256) round_rows_kernel(const float* src, int64_t ld,
-                                                         uint16_t* dst, int64_t ldd, int M, int K) {
+// dst = the sum of `slices` arrays of f32 rows, in their order.
+template <class TD>
+__global__ void __launch_bounds__(256) sum_slices_kernel(const float* src, int slices,
+                                                         int64_t stride, int64_t ld, TD* dst,
+                                                         int64_t ldd, int M, int K) {
   griddep_wait();
   griddep_launch_dependents();
   const int per = (K + 3) / 4;       // the sums' rows end on 16 bytes
@@ -222,16 +226,55 @@ __global__ void __launch_bounds__(256) round_rows_kernel(const float* src, int64
   for (int64_t i = blockIdx.x * 256LL + threadIdx.x; i < total; i += 256LL * gridDim.x) {
     const int64_t row = i / per;
     const int k = 4 * static_cast<int>(i - row * per);
-    const float4 v = __ldcs(reinterpret_cast<const float4*>(src + row * ld + k));
-    uint16_t* d = dst + row * ldd + k;
-    const uint32_t lo = pack_bf16x2(v.x, v.y), hi = pack_bf16x2(v.z, v.w);
-    if (k + 4 <= K) {
-      *reinterpret_cast<uint2*>(d) = make_uint2(lo, hi);
+    const float* at = src + row * ld + k;
+    float4 v = __ldcs(reinterpret_cast<const float4*>(at));
+    for (int s = 1; s < slices; s += 4) {
+      float4 t[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+        if (s + u < slices) t[u] = __ldcs(reinterpret_cast<const float4*>(at + (s + u) * stride));
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+        if (s + u < slices) {
+          v.x += t[u].x;
+          v.y += t[u].y;
+          v.z += t[u].z;
+          v.w += t[u].w;
+        }
+    }
+    TD* d = dst + row * ldd + k;
+    const float f[4] = {v.x, v.y, v.z, v.w};
+    if constexpr (sizeof(TD) == 2) {
+      const uint32_t w[2] = {pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w)};
+      if (k + 4 <= K) {
+        *reinterpret_cast<uint2*>(d) = make_uint2(w[0], w[1]);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 3; ++e)
+          if (k + e < K) d[e] = static_cast<TD>(w[e / 2] >> (16 * (e & 1)));
+      }
     } else {
-      const uint32_t w[2] = {lo, hi};
-      for (int e = 0; k + e < K; ++e) d[e] = static_cast<uint16_t>(w[e / 2] >> (16 * (e & 1)));
+      if (k + 4 <= K) {
+        *reinterpret_cast<float4*>(d) = v;
+      } else {
+#pragma unroll
+        for (int e = 0; e < 3; ++e)
+          if (k + e < K) d[e] = f[e];
+      }
     }
   }
+}
+
+int launch_sum_slices(const float* src, int slices, int64_t stride, int64_t ld, void* dst,
+                      int64_t ldd, int64_t M, int64_t K, bool bf16, cudaStream_t stream,
+                      DeviceCtx* ctx) {
+  int64_t blocks = (M * ((K + 3) / 4) + 255) / 256;
+  if (blocks > 16 * ctx->num_sms) blocks = 16 * ctx->num_sms;
+  const int m = static_cast<int>(M), k = static_cast<int>(K);
+  return bf16 ? launch_chained(sum_slices_kernel<uint16_t>, blocks, 256, 0, 1, stream, src, slices,
+                               stride, ld, static_cast<uint16_t*>(dst), ldd, m, k)
+              : launch_chained(sum_slices_kernel<float>, blocks, 256, 0, 1, stream, src, slices,
+                               stride, ld, static_cast<float*>(dst), ldd, m, k);
 }
 
 int clear_rows(void* D, int64_t ldd, int64_t rows, int64_t width, int esize, cudaStream_t stream) {
@@ -357,6 +400,11 @@ int gemm_bf16_xent_grad(const void* A, int64_t lda, const void* B, int64_t ldb,
   uint16_t* a_rows = reinterpret_cast<uint16_t*>(ws);
   uint16_t* dz = reinterpret_cast<uint16_t*>(ws + plan.off_dz);
   float* sums = reinterpret_cast<float*>(ws + plan.off_sum);
+  float* weight_sums = reinterpret_cast<float*>(ws + plan.off_weights);
+  const int64_t one_sum = M * plan.ld_sum;
+  // dA directly: bf16 from one contraction, f32 from contractions that are not sliced.
+  const bool whole = plan.rows_by.count == 1 && plan.pieces == 1;
+  const bool direct = plan.rows_by.count == 1 && (!bf16 || plan.pieces == 1);
   const int m = static_cast<int>(M);
   XentArgs a{};
   a.M = m;
@@ -397,30 +445,38 @@ int gemm_bf16_xent_grad(const void* A, int64_t lda, const void* B, int64_t ldb,
       p.cols_ld = plan.terms * ld_dz;
       // (dz is zero from column n on, and past B's row n nothing is read.)
       p.k = plan.terms * ld_dz;
-      g.wrap = static_cast<int>(ld_dz);
-      g.num_k_blocks = static_cast<int>(p.k / 64);
-      g.add = col0 > 0;
-      if (bf16 && plan.pieces == 1) {
+      if (bf16 && whole) {
+        g.num_k_blocks = static_cast<int>(p.k / 64);
         g.D = dA;
         g.ldd = ldda;
         rc = launch_grouped_dgrad(true, p, g, stream, ctx);
       } else {
-        g.D = bf16 ? static_cast<void*>(sums) : dA;
-        g.ldd = bf16 ? plan.ld_sum : ldda;
-        rc = launch_grouped_dgrad_add(!bf16, p, g, stream, ctx);
+        const int slices = plan.rows_by.count;
+        g.M = static_cast<int>(slices * M);
+        g.groups = slices;
+        g.even = m;
+        g.tile_cols = plan.rows_by.columns;
+        g.slice = static_cast<int>(xent_up((ld_dz + slices - 1) / slices, 64));
+        g.second = static_cast<int>(ld_dz);
+        g.num_k_blocks = plan.terms * g.slice / 64;
+        g.add = col0 > 0;
+        g.D = direct ? dA : sums;
+        g.ldd = direct ? ldda : plan.ld_sum;
+        rc = launch_sliced_dgrad(!bf16, p, g, stream, ctx);
       }
       if (rc != TG_OK) return rc;
     }
     if (weights) {
       // (Two terms: twice the rows of dz against as many of A.)
       const int64_t terms_rows = plan.terms * plan.rows;
+      const int slices = plan.weights_by.count;
+      void* D = static_cast<uint8_t*>(dB) + col0 * lddb * esize;
       GroupedArgs g = grouped_args(ctx);
       g.M = static_cast<int>(terms_rows);
       g.wide = static_cast<int>(K);
       g.cols = static_cast<int>(n);
       g.num_col_tiles = ceil_div_i(n, 256);
-      g.num_k_blocks = ceil_div_i(terms_rows, 64);
-      g.D = static_cast<uint8_t*>(dB) + col0 * lddb * esize;
+      g.D = D;
       g.ldd = lddb;
       GroupedOperands p{};
       p.wide = a_rows;
@@ -430,16 +486,27 @@ int gemm_bf16_xent_grad(const void* A, int64_t lda, const void* B, int64_t ldb,
       p.cols = dz;
       p.cols_ld = ld_dz;
       p.k = terms_rows;
-      rc = launch_grouped_wgrad(bf16, p, g, stream, ctx);
+      if (slices == 1) {
+        g.num_k_blocks = ceil_div_i(terms_rows, 64);
+        rc = launch_grouped_wgrad(bf16, p, g, stream, ctx);
+      } else {
+        g.groups = slices;
+        g.even = static_cast<int>(xent_up((terms_rows + slices - 1) / slices, 64));
+        g.num_k_blocks = g.even / 64;
+        g.D = weight_sums;
+        g.ldd = plan.ld_sum;
+        g.group_stride_d = n * plan.ld_sum;
+        rc = launch_sliced_wgrad(p, g, stream, ctx);
+        if (rc != TG_OK) return rc;
+        rc = launch_sum_slices(weight_sums, slices, g.group_stride_d, plan.ld_sum, D, lddb, n, K,
+                               bf16, stream, ctx);
+      }
       if (rc != TG_OK) return rc;
     }
   }
-  if (rows && bf16 && plan.pieces > 1) {
-    const int64_t blocks = (M * ((K + 3) / 4) + 255) / 256;
-    rc = launch_chained(round_rows_kernel, blocks < 16 * ctx->num_sms ? blocks : 16 * ctx->num_sms,
-                        256, 0, 1, stream, sums, plan.ld_sum, static_cast<uint16_t*>(dA), ldda, m,
-                        static_cast<int>(K));
-  }
+  if (rows && !direct)
+    rc = launch_sum_slices(sums, plan.rows_by.count, one_sum, plan.ld_sum, dA, ldda, M, K, bf16,
+                           stream, ctx);
   return rc;
 }
 

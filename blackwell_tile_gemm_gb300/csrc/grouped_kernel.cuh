@@ -111,10 +111,14 @@ struct GroupedArgs {
   void* D;
   int64_t ldd;
   int64_t group_stride_d;  // wgrad
-  int add;                 // kAdd: D += instead of D =
-  int tile_cols;           // kAdd: most columns of a tile (a multiple of 32, at most kTileN)
-  int wrap;                // kAdd: contraction index from which the wide operand's rows
-                           // begin again (a multiple of 64; the column operand's do not)
+  // kAdd
+  int even;                // rows of a group: all but the last have as many
+  int add;                 // dgrad: D += instead of D =
+  int tile_cols;           // dgrad: most columns of a tile (a multiple of 32, at most kTileN)
+  int slice;               // dgrad: contraction indices of a group (a multiple of 64) ...
+  int second;              // ... after which follow as many of a second term: the column
+                           // operand's, `second` columns behind the first, against the
+                           // wide operand's rows again
   Epi epi;                 // bias: [groups][wide]
   // adapters
   const int* ids;          // [M]
@@ -169,9 +173,12 @@ struct GroupedCfg {
   // Adapter stages (MMA form) and ragged contractions are fixed up in shared
   // memory before the MMAs read them.
   static constexpr bool kExt = kMode == kAdapter && kCtaGroup == 2;
-  // A contraction given in parts (f32 D of CTA pairs): GroupedArgs::add adds the
-  // tile to D instead of writing it.  1: sums that a rounding to bf16 follows, one
-  // accumulator each; 2: sums that stay f32, in chunks.
+  // A contraction in slices (f32 D of CTA pairs), each the group of an equal share
+  // (GroupedArgs::even, slice) with a D of its own.  Dgrad: of one operand's columns
+  // and the other's rows; GroupedArgs::add adds the tile to D instead of writing it,
+  // for contractions given one after the other.  1: sums that a rounding to bf16
+  // follows, one accumulator each; 2: sums that stay f32, in chunks.  Wgrad (3): of
+  // the rows.
   static constexpr int kAdd = kAdd_;
   static constexpr int kTerms = kBf16Out ? 2 : 3;   // bf16 terms of H
   static constexpr int kFixWarps = kExt ? 2 : kMode == kGroupedWgrad ? 1 : 0;
@@ -223,7 +230,7 @@ struct GroupedCfg {
   static_assert(C_BYTES % 1024 == 0, "swizzle atoms");
   static_assert(!kColMn || (kCtaGroup == 2 && kTileN == 256), "wgrad tiles");
   static_assert(!kWideMn || kCtaGroup == 2, "the gradients run as CTA pairs");
-  static_assert(!kAdd || (kCtaGroup == 2 && !kBf16Out && !kColMn), "added to in f32");
+  static_assert(!kAdd || (kCtaGroup == 2 && !kBf16Out && kColMn == (kAdd == 3)), "slices are f32");
 };
 
 // One work item.
@@ -270,12 +277,17 @@ struct GroupWalk {
   int begin, end, r0, r1, group, nct, size;
 
   static __device__ __forceinline__ int tile_cols(const GroupedArgs& p) {
-    return C::kAdd ? p.tile_cols : C::kTileN;
+    return C::kAdd && !C::kColMn ? p.tile_cols : C::kTileN;
   }
   __device__ __forceinline__ void load(const GroupedArgs& p, int lane) {
     const int g = g0 + lane;
     int end = lo0;
-    if (p.offsets == nullptr) {
+    if constexpr (C::kAdd) {
+      if (g < p.groups) {
+        const int64_t all = static_cast<int64_t>(g + 1) * p.even;
+        end = all < p.M ? static_cast<int>(all) : p.M;
+      }
+    } else if (p.offsets == nullptr) {
       end = g0 == 0 ? p.M : lo0;
     } else if (g < p.groups) {
       const int raw = p.offsets[g + 1];
@@ -1153,7 +1165,9 @@ __global__ void __launch_bounds__(C::kThreads, 1)
       const int crows = w.ncols / C::kCtaGroup;       // column-operand rows of this CTA
       const int cbox = (crows - 1) / C::kBoxStep;     // K-major: the box that holds them
       const int loaded = C::kColMn ? crows : (cbox + 1) * C::kBoxStep;
-      const int crow0 = w.row0 + static_cast<int>(rank) * crows;
+      // (Slices of dgrad read the same rows.)
+      const int crow0 = w.row0 + static_cast<int>(rank) * crows -
+                        (C::kAdd && !C::kColMn ? w.g * p.even : 0);
       // MN-major: both of a box pair's 64-element chunks lie inside the row.
       const bool w_chunks = C::kWideMn && wx + 128 <= p.wide;
       // Read here, used after the K stages.
@@ -1277,17 +1291,23 @@ __global__ void __launch_bounds__(C::kThreads, 1)
             }
           } else if constexpr (C::kCtaGroup == 2) {
             if (do_wide) {
-              const int kw = C::kAdd && kx >= p.wrap ? kx - p.wrap : kx;
+              const int kw = C::kAdd ? w.g * p.slice + (kx < p.slice ? kx : kx - p.slice) : kx;
+              const int wg = C::kAdd ? 0 : w.g;
               if (C::kWideMn && w_chunks) {
-                tma_load_4d_pair(dW, &tmW2, fb, 0, kw, wx / 64, w.g, pol);
+                tma_load_4d_pair(dW, &tmW2, fb, 0, kw, wx / 64, wg, pol);
               } else if constexpr (C::kWideMn) {
                 for (int c = 0; c < 2; ++c)
-                  tma_load_3d_pair(dW + 8192 * c, &tmW, fb, wx + 64 * c, kw, w.g, pol);
+                  tma_load_3d_pair(dW + 8192 * c, &tmW, fb, wx + 64 * c, kw, wg, pol);
               } else {
                 tma_load_3d_pair(dW, &tmW, fb, kx, wx, w.g, pol);
               }
             }
-            if (do_cols) tma_load_2d_pair(dC, &tmC.box[cbox], fb, kx, crow0, pol);
+            if (do_cols) {
+              const int kc = C::kAdd ? w.g * p.slice +
+                                           (kx < p.slice ? kx : p.second + kx - p.slice)
+                                     : kx;
+              tma_load_2d_pair(dC, &tmC.box[cbox], fb, kc, crow0, pol);
+            }
           } else {
             tma_load_3d(dW, &tmW, fb, kx, wx, w.g, pol);
             tma_load_2d(dC, &tmC.box[cbox], fb, kx, crow0, pol);

@@ -143,7 +143,8 @@ int launch_grouped(const GroupedOperands& operands, const GroupedArgs& args, cud
     if (rc != TG_OK) return rc;
     for (int b = 0; b < kColBoxes; ++b) {
       const bool gather = C::kGather && a.row_idx != nullptr;
-      rc = make_tensor_map_2d(&tC.box[b], bf, o.cols, o.k, gather ? a.num_rows : a.M,
+      rc = make_tensor_map_2d(&tC.box[b], bf, o.cols, o.k,
+                              gather ? a.num_rows : C::kAdd ? a.even : a.M,
                               o.cols_ld * 2, 64, gather ? 1 : C::kBoxStep * (b + 1), sw);
       if (rc != TG_OK) return rc;
     }
@@ -203,9 +204,12 @@ int launch_grouped_dgrad(bool bf16, const GroupedOperands& o, const GroupedArgs&
                          cudaStream_t stream, DeviceCtx* ctx);
 int launch_grouped_wgrad(bool bf16, const GroupedOperands& o, const GroupedArgs& a,
                          cudaStream_t stream, DeviceCtx* ctx);
-// D += (a.add) or D = in f32; `chunked`: for sums that stay f32.
-int launch_grouped_dgrad_add(bool chunked, const GroupedOperands& o, const GroupedArgs& a,
-                             cudaStream_t stream, DeviceCtx* ctx);
+// A contraction in a.groups slices, each with an f32 D of its own (GroupedCfg::kAdd).
+// Dgrad: `chunked` for sums that stay f32.
+int launch_sliced_dgrad(bool chunked, const GroupedOperands& o, const GroupedArgs& a,
+                        cudaStream_t stream, DeviceCtx* ctx);
+int launch_sliced_wgrad(const GroupedOperands& o, const GroupedArgs& a, cudaStream_t stream,
+                        DeviceCtx* ctx);
 int launch_grouped_adapter(bool bf16, const GroupedOperands& o, const GroupedArgs& a,
                            cudaStream_t stream, DeviceCtx* ctx);
 

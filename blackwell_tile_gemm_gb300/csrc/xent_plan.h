@@ -80,13 +80,51 @@ inline XentLossPlan xent_loss_plan(int64_t M, int64_t N) {
   return q;
 }
 
+// Slices of a contraction: with few tiles the gradients' products are cut along it, the
+// slices' f32 sums added afterwards.  A product of `tiles(columns)` tiles and `stages`
+// stages; columns per tile and slices whose waves over the pairs of CTAs take least, in
+// cycles: a stage the larger of its MMAs (2 a column) and its loads (128 rows and half
+// the columns at 64 bytes a cycle); a tile its start and its stores; slices their
+// `bytes` (of one) written and read at 3 KB a cycle, and a launch.
+// Loss and gradients, without slices and with: 202 rows x 120448 x 384 in bf16 200 ->
+// 143 us, 1 x 69040 x 149 90 -> 58, 20000 x 130 x 257 in f32 151 -> 107, 2259 x 1281 x
+// 392 80 -> 60; 4096 x 128000 x 4096 has tiles enough and takes none.
+constexpr int kXentMostSlices = 64;
+constexpr int64_t kXentSliceBytes = int64_t{24} << 20;
+
+struct XentSlices {
+  int count;         // 1: none
+  int columns;       // of a tile
+};
+inline XentSlices xent_slices(int64_t wide_tiles, int64_t rows, int64_t least_columns, int64_t stages,
+                              int64_t bytes) {
+  XentSlices q{1, 256};
+  int64_t best = 0;
+  for (int64_t c = 256; c >= least_columns; c -= 32) {
+    const int64_t tiles = wide_tiles * ((rows + c - 1) / c);
+    for (int64_t n = 1; n <= kXentMostSlices; ++n) {
+      if (n > 1 && (n * bytes > kXentSliceBytes || stages < 4 * n)) break;
+      const int64_t waves = (tiles * n + kXentSms / 2 - 1) / (kXentSms / 2);
+      const int64_t stage = (2 * c > 256 + c ? 2 * c : 256 + c) + 70;
+      const int64_t cost = waves * ((stages + n - 1) / n * stage + 4000) +
+                           (n > 1 ? 6000 + n * bytes / 1500 : 0);
+      if (best == 0 || cost < best) {
+        best = cost;
+        q = XentSlices{static_cast<int>(n), static_cast<int>(c)};
+      }
+      if (waves > 8) break;
+    }
+  }
+  return q;
+}
+
 // Workspace of the gradient: the rows of A that have a target (the others as zeros),
-// dz of one piece of the vocabulary and the f32 sums of dA.  With two terms of dz a
-// row's second follows its first: [rows][2][ld_dz].  Read as rows twice as long, one
-// contraction of dA takes both (B's rows a second time); read as twice the rows, so
-// does one of dB, with each row of A twice.  Zeros fill the rows up to whole stages
-// of that contraction: a ragged one takes a detour (1000 rows x 50304 x 1024 89 us,
-// 1024 rows 74).
+// dz of one piece of the vocabulary, dA's f32 sums (of all pieces, each slice's) and
+// dB's (of a piece).  With two terms of dz a row's second follows its first:
+// [rows][2][ld_dz].  Read as rows twice as long, one contraction of dA takes both (B's
+// rows a second time); read as twice the rows, so does one of dB, with each row of A
+// twice.  Zeros fill the rows up to whole stages of that contraction: a ragged one takes
+// a detour (1000 rows x 50304 x 1024 89 us, 1024 rows 74).
 //
 // Pieces are as wide as kXentDzBytes allow, but at least kXentLeastPiece columns:
 // every piece adds its share of dA to all of it in memory, 8 bytes for 2 * width
@@ -99,8 +137,9 @@ struct XentGradPlan {
   int64_t rows;       // of dz: M in steps of 64
   int64_t piece;      // columns of a piece, a multiple of 256 (or all)
   int64_t pieces;
+  XentSlices rows_by, weights_by;   // slices of dA's and of dB's contractions
   int64_t ld_a, ld_sum;
-  size_t off_dz, off_sum, bytes;
+  size_t off_dz, off_sum, off_weights, bytes;
 };
 inline XentGradPlan xent_grad_plan(int64_t M, int64_t N, int64_t K, bool bf16) {
   XentGradPlan q{};
@@ -114,13 +153,24 @@ inline XentGradPlan xent_grad_plan(int64_t M, int64_t N, int64_t K, bool bf16) {
   q.pieces = (N + q.piece - 1) / q.piece;
   q.ld_a = xent_up(K, 64);
   q.ld_sum = xent_up(K, 4);
-  // (Room for the widest piece there could be: it grows with M and N.)
-  const int64_t wide = column * kXentLeastPiece > kXentDzBytes ? column * kXentLeastPiece
-                                                               : kXentDzBytes;
+  const int64_t wide = (K + 255) / 256;
+  const int64_t a_bytes = 4 * M * q.ld_sum, b_bytes = 4 * q.piece * q.ld_sum;
+  q.rows_by = xent_slices(wide, M, 160, q.terms * ((q.piece + 63) / 64), a_bytes);
+  q.weights_by = xent_slices(wide, q.piece, 256, q.terms * q.rows / 64, b_bytes);
+  // Room for the widest piece and the most slices there could be: it grows with M, N
+  // and K, so that a reservation for the largest call serves all smaller ones.
+  const int64_t widest = column * kXentLeastPiece > kXentDzBytes ? column * kXentLeastPiece
+                                                                 : kXentDzBytes;
   const int64_t all = column * xent_up(N, 64);
+  auto sliced = [](int64_t one) {
+    return kXentMostSlices * one < kXentSliceBytes ? kXentMostSlices * one : kXentSliceBytes;
+  };
+  int64_t sums = sliced(a_bytes);
+  if (bf16 && q.pieces > 1 && sums < a_bytes) sums = a_bytes;
   q.off_dz = static_cast<size_t>(xent_up(column * q.ld_a, 1024));
-  q.off_sum = q.off_dz + static_cast<size_t>(xent_up(all < wide ? all : wide, 1024));
-  q.bytes = q.off_sum + (bf16 && q.pieces > 1 ? static_cast<size_t>(4 * M * q.ld_sum) : 0);
+  q.off_sum = q.off_dz + static_cast<size_t>(xent_up(all < widest ? all : widest, 1024));
+  q.off_weights = q.off_sum + static_cast<size_t>(xent_up(sums, 1024));
+  q.bytes = q.off_weights + static_cast<size_t>(sliced(4 * N * q.ld_sum));
   return q;
 }
 

@@ -15,7 +15,7 @@ def code(name):
 
 
 @pytest.mark.parametrize("name", ["xent_kernel.cuh", "gemm_xent.cu", "embed_rows.cu",
-                                  "balance_loss.cu", "grouped_dgrad_add.cu"])
+                                  "balance_loss.cu", "grouped_sliced.cu"])
 def test_no_read_only_loads(name):
     text = code(name)
     assert "__ldg(" not in text and "__restrict__" not in text and "ld_global_nc" not in text

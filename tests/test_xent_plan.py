@@ -95,3 +95,54 @@ def test_a_reservation_serves_smaller_calls(call, kw):
         small = tuple(rng.randint(1, x) for x in large)
         assert tg.workspace_bytes(call, *small, **kw) <= tg.workspace_bytes(call, *large, **kw), (
             small, large)
+
+
+SLICES = r"""
+#include <cmath>
+#include <cstdio>
+#include <cstdlib>
+#include <random>
+#include "xent_plan.h"
+using namespace tg;
+
+int main() {
+  std::mt19937_64 gen(2);
+  auto between = [&](double lo, double hi) {
+    return static_cast<int64_t>(exp(std::uniform_real_distribution<>(log(lo), log(hi))(gen)));
+  };
+  int most = 0, both = 0;
+  for (int i = 0; i < 200000; ++i) {
+    const int64_t M = between(1, 200000), N = between(1, 600000), K = between(1, 20000);
+    for (int bf16 = 0; bf16 < 2; ++bf16) {
+      const XentGradPlan g = xent_grad_plan(M, N, K, bf16);
+      const XentSlices a = g.rows_by, b = g.weights_by;
+      const int64_t a_room = g.off_weights - g.off_sum, b_room = g.bytes - g.off_weights;
+      const int64_t n = g.pieces > 1 ? g.piece : N;
+      bool good = a.count >= 1 && a.count <= kXentMostSlices && b.count >= 1 &&
+                  b.count <= kXentMostSlices;
+      good &= a.columns % 32 == 0 && a.columns >= 160 && a.columns <= 256 && b.columns == 256;
+      good &= (a.count == 1 && (!bf16 || g.pieces == 1)) || 4 * M * g.ld_sum * a.count <= a_room;
+      good &= b.count == 1 || 4 * n * g.ld_sum * b.count <= b_room;
+      // Rows of all slices and indices of all terms fit 32 bits.
+      good &= a.count * M < int64_t{1} << 31 && b.count * (g.terms * g.rows + 64) < int64_t{1} << 31;
+      good &= g.off_sum % 1024 == 0 && g.off_weights % 1024 == 0;
+      if (!good) {
+        printf("%lld %lld %lld %d\n", (long long)M, (long long)N, (long long)K, bf16);
+        return 1;
+      }
+      most = a.count > most ? a.count : most;
+      both += a.count > 1 && b.count > 1;
+    }
+  }
+  puts(most > 16 && both > 100 ? "ok" : "never sliced");
+}
+"""
+
+
+@pytest.mark.skipif(shutil.which("g++") is None, reason="needs g++")
+def test_slices(tmp_path):
+    src, exe = tmp_path / "slices.cpp", tmp_path / "slices"
+    src.write_text(SLICES)
+    subprocess.run(["g++", "-std=c++17", "-O2", "-I", CSRC, str(src), "-o", str(exe)], check=True)
+    r = subprocess.run([str(exe)], capture_output=True, text=True)
+    assert r.returncode == 0 and r.stdout.strip() == "ok", r.stdout
