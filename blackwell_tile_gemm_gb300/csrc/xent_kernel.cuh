@@ -435,28 +435,25 @@ __global__ void __launch_bounds__(C::kThreads, 1)
       const int here = target - tile0;
       if constexpr (C::kMode == kXentLoss) {
         // The warp's whole share stays in registers: the maximum and the sum are
-        // two passes over them.
+        // two passes over them.  (Short contractions are bound by these instructions: the
+        // first chunk not added to zeros, and four maxima, 20000 x 10000 x 64 113 -> 97 us.)
         float v[4][32];
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-#pragma unroll
-          for (int e = 0; e < 32; ++e) v[i][e] = 0.0f;
-        for (int c = 0; c < chunks; ++c) {
-          if (!acc_ready()) {
-            ok = false;
-            break;
-          }
+        auto read = [&](auto add) {
+          if (!acc_ready()) return false;
           const uint32_t t_row = t_slab + static_cast<uint32_t>(acc * C::BN);
 #pragma unroll
           for (int i = 0; i < 4; ++i)
             if (32 * (half + 2 * i) < cols && row0 < p.M)
-              xent_read<true>(t_row + 32 * (half + 2 * i), v[i]);
+              xent_read<decltype(add)::value>(t_row + 32 * (half + 2 * i), v[i]);
           hand_back();
-        }
+          return true;
+        };
+        ok = read(std::false_type{});
+        for (int c = 1; ok && c < chunks; ++c) ok = read(std::true_type{});
         if (!ok) break;
         if (row0 >= p.M) continue;   // (lanes that no row has)
         const float none = __uint_as_float(0xFF800000u);   // -inf
-        float m = none;
+        float most[4] = {none, none, none, none};
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const int left = cols - 32 * (half + 2 * i);
@@ -467,8 +464,9 @@ __global__ void __launch_bounds__(C::kThreads, 1)
               if (e >= left) v[i][e] = none;
           }
 #pragma unroll
-          for (int e = 0; e < 32; ++e) m = fmaxf(m, v[i][e]);
+          for (int e = 0; e < 32; ++e) most[e & 3] = fmaxf(most[e & 3], v[i][e]);
         }
+        const float m = fmaxf(fmaxf(most[0], most[1]), fmaxf(most[2], most[3]));
         // (An infinite maximum is no reference.)  The difference first: it is exact
         // for the logits that count, whatever their size.
         const float r = fabsf(m) < __uint_as_float(0x7F800000u) ? m : 0.0f;
