@@ -214,34 +214,61 @@ __global__ void xent_zero_kernel(const int* targets, float* loss, float* lse, in
 // Sums of slices
 // ---------------------------------------------------------------------------
 
-// dst = the sum of `slices` arrays of f32 rows, in their order.
-template <class TD>
+// dst = the sum of `slices` arrays of f32 rows, in an order that the sizes alone give.
+// kParts threads share the slices of four neighbouring elements: with few elements one
+// thread's turns at memory would take longest (53 x 192, 63 slices: one thread 12 us, 16
+// 3).
+template <class TD, int kParts>
 __global__ void __launch_bounds__(256) sum_slices_kernel(const float* src, int slices,
                                                          int64_t stride, int64_t ld, TD* dst,
                                                          int64_t ldd, int M, int K) {
+  constexpr int kOwn = 256 / kParts;
+  __shared__ float4 sums[kParts > 1 ? 256 : 1];
   griddep_wait();
   griddep_launch_dependents();
   const int per = (K + 3) / 4;       // the sums' rows end on 16 bytes
   const int64_t total = static_cast<int64_t>(M) * per;
-  for (int64_t i = blockIdx.x * 256LL + threadIdx.x; i < total; i += 256LL * gridDim.x) {
+  const int part = static_cast<int>(threadIdx.x) / kOwn;
+  const int first = slices * part / kParts, end = slices * (part + 1) / kParts;
+  for (int64_t i0 = static_cast<int64_t>(blockIdx.x) * kOwn; i0 < total;
+       i0 += static_cast<int64_t>(gridDim.x) * kOwn) {
+    const int64_t i = i0 + threadIdx.x % kOwn;
     const int64_t row = i / per;
     const int k = 4 * static_cast<int>(i - row * per);
-    const float* at = src + row * ld + k;
-    float4 v = __ldcs(reinterpret_cast<const float4*>(at));
-    for (int s = 1; s < slices; s += 4) {
-      float4 t[4];
+    float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    if (i < total) {
+      const float* at = src + row * ld + k;
+      for (int s = first; s < end; s += 4) {
+        float4 t[4];
 #pragma unroll
-      for (int u = 0; u < 4; ++u)
-        if (s + u < slices) t[u] = __ldcs(reinterpret_cast<const float4*>(at + (s + u) * stride));
+        for (int u = 0; u < 4; ++u)
+          if (s + u < end) t[u] = __ldcs(reinterpret_cast<const float4*>(at + (s + u) * stride));
 #pragma unroll
-      for (int u = 0; u < 4; ++u)
-        if (s + u < slices) {
-          v.x += t[u].x;
-          v.y += t[u].y;
-          v.z += t[u].z;
-          v.w += t[u].w;
-        }
+        for (int u = 0; u < 4; ++u)
+          if (s + u < end) {
+            v.x += t[u].x;
+            v.y += t[u].y;
+            v.z += t[u].z;
+            v.w += t[u].w;
+          }
+      }
     }
+    if constexpr (kParts > 1) {
+      sums[threadIdx.x] = v;
+      __syncthreads();
+      if (part == 0) {
+#pragma unroll
+        for (int q = 1; q < kParts; ++q) {
+          const float4 t = sums[q * kOwn + threadIdx.x];
+          v.x += t.x;
+          v.y += t.y;
+          v.z += t.z;
+          v.w += t.w;
+        }
+      }
+      __syncthreads();
+    }
+    if (part != 0 || i >= total) continue;
     TD* d = dst + row * ldd + k;
     const float f[4] = {v.x, v.y, v.z, v.w};
     if constexpr (sizeof(TD) == 2) {
@@ -265,16 +292,29 @@ __global__ void __launch_bounds__(256) sum_slices_kernel(const float* src, int s
   }
 }
 
+template <class TD>
+int launch_sum_slices_to(const float* src, int slices, int64_t stride, int64_t ld, TD* dst,
+                         int64_t ldd, int64_t M, int64_t K, cudaStream_t stream, DeviceCtx* ctx) {
+  const int64_t total = M * ((K + 3) / 4);
+  int parts = 1;
+  while (parts < 16 && slices >= 4 * parts && total * parts < 256LL * 2 * ctx->num_sms) parts *= 4;
+  const int own = 256 / parts;
+  int64_t blocks = (total + own - 1) / own;
+  if (blocks > 16 * ctx->num_sms) blocks = 16 * ctx->num_sms;
+  auto* kern = parts == 1   ? &sum_slices_kernel<TD, 1>
+               : parts == 4 ? &sum_slices_kernel<TD, 4>
+                            : &sum_slices_kernel<TD, 16>;
+  return launch_chained(kern, blocks, 256, 0, 1, stream, src, slices, stride, ld, dst, ldd,
+                        static_cast<int>(M), static_cast<int>(K));
+}
+
 int launch_sum_slices(const float* src, int slices, int64_t stride, int64_t ld, void* dst,
                       int64_t ldd, int64_t M, int64_t K, bool bf16, cudaStream_t stream,
                       DeviceCtx* ctx) {
-  int64_t blocks = (M * ((K + 3) / 4) + 255) / 256;
-  if (blocks > 16 * ctx->num_sms) blocks = 16 * ctx->num_sms;
-  const int m = static_cast<int>(M), k = static_cast<int>(K);
-  return bf16 ? launch_chained(sum_slices_kernel<uint16_t>, blocks, 256, 0, 1, stream, src, slices,
-                               stride, ld, static_cast<uint16_t*>(dst), ldd, m, k)
-              : launch_chained(sum_slices_kernel<float>, blocks, 256, 0, 1, stream, src, slices,
-                               stride, ld, static_cast<float*>(dst), ldd, m, k);
+  return bf16 ? launch_sum_slices_to(src, slices, stride, ld, static_cast<uint16_t*>(dst), ldd, M,
+                                     K, stream, ctx)
+              : launch_sum_slices_to(src, slices, stride, ld, static_cast<float*>(dst), ldd, M, K,
+                                     stream, ctx);
 }
 
 int clear_rows(void* D, int64_t ldd, int64_t rows, int64_t width, int esize, cudaStream_t stream) {
