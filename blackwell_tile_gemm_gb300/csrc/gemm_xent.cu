@@ -503,6 +503,9 @@ int gemm_bf16_xent_grad(const void* A, int64_t lda, const void* B, int64_t ldb,
         g.D = direct ? dA : sums;
         g.ldd = direct ? ldda : plan.ld_sum;
         rc = launch_sliced_dgrad(!bf16, p, g, stream, ctx);
+        if (rc == TG_OK && !direct && col0 + plan.piece >= N)
+          rc = launch_sum_slices(sums, slices, one_sum, plan.ld_sum, dA, ldda, M, K, bf16, stream,
+                                 ctx);
       }
       if (rc != TG_OK) return rc;
     }
@@ -544,9 +547,6 @@ int gemm_bf16_xent_grad(const void* A, int64_t lda, const void* B, int64_t ldb,
       if (rc != TG_OK) return rc;
     }
   }
-  if (rows && !direct)
-    rc = launch_sum_slices(sums, plan.rows_by.count, one_sum, plan.ld_sum, dA, ldda, M, K, bf16,
-                           stream, ctx);
   return rc;
 }
 

@@ -90,7 +90,7 @@ inline XentLossPlan xent_loss_plan(int64_t M, int64_t N) {
 // 143 us, 1 x 69040 x 149 90 -> 58, 20000 x 130 x 257 in f32 151 -> 107, 2259 x 1281 x
 // 392 80 -> 60; 4096 x 128000 x 4096 has tiles enough and takes none.
 constexpr int kXentMostSlices = 64;
-constexpr int64_t kXentSliceBytes = int64_t{24} << 20;
+constexpr int64_t kXentSliceBytes = int64_t{40} << 20;
 
 struct XentSlices {
   int count;         // 1: none
@@ -169,8 +169,10 @@ inline XentGradPlan xent_grad_plan(int64_t M, int64_t N, int64_t K, bool bf16) {
   if (bf16 && q.pieces > 1 && sums < a_bytes) sums = a_bytes;
   q.off_dz = static_cast<size_t>(xent_up(column * q.ld_a, 1024));
   q.off_sum = q.off_dz + static_cast<size_t>(xent_up(all < widest ? all : widest, 1024));
-  q.off_weights = q.off_sum + static_cast<size_t>(xent_up(sums, 1024));
-  q.bytes = q.off_weights + static_cast<size_t>(sliced(4 * N * q.ld_sum));
+  const int64_t weights = sliced(4 * N * q.ld_sum);
+  // One piece: dA's slices are added before dB's are made, in the same room.
+  q.off_weights = q.off_sum + static_cast<size_t>(q.pieces == 1 ? 0 : xent_up(sums, 1024));
+  q.bytes = q.off_weights + static_cast<size_t>(q.pieces == 1 && sums > weights ? sums : weights);
   return q;
 }
 

@@ -116,7 +116,9 @@ int main() {
     for (int bf16 = 0; bf16 < 2; ++bf16) {
       const XentGradPlan g = xent_grad_plan(M, N, K, bf16);
       const XentSlices a = g.rows_by, b = g.weights_by;
-      const int64_t a_room = g.off_weights - g.off_sum, b_room = g.bytes - g.off_weights;
+      // (One piece: the same room, one after the other.)
+      const int64_t a_room = (g.pieces == 1 ? g.bytes : g.off_weights) - g.off_sum;
+      const int64_t b_room = g.bytes - g.off_weights;
       const int64_t n = g.pieces > 1 ? g.piece : N;
       bool good = a.count >= 1 && a.count <= kXentMostSlices && b.count >= 1 &&
                   b.count <= kXentMostSlices;
