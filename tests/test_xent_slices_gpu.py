@@ -42,3 +42,34 @@ def test_nan_rows_stay_in_their_row(tg):
         assert torch.isnan(dA[17]).all() and torch.isnan(dB).all()
         rest = torch.cat((dA[:17], dA[18:]))
         assert torch.isfinite(rest).all()
+
+
+@pytest.mark.parametrize("M,N,K", [(150, 20011, 300), (9001, 300, 72), (7000, 3001, 33)])
+@pytest.mark.parametrize("f32", [False, True])
+def test_captured_into_given_rows_with_what_it_asks_for(tg, M, N, K, f32):
+    """On a stream that has the bytes the call asks for and no more, into results whose
+    rows lie apart, replayed while another stream makes the same call: the eager bits, and
+    what lies between the rows stays."""
+    import torch
+    A, B, t, grad = inputs(M + K, M, N, K)
+    _, lse = tg.gemm_bf16_xent(A, B, t)
+    dtype = torch.float32 if f32 else torch.bfloat16
+    want = tg.gemm_bf16_xent_grad(A, B, t, lse, grad, out_dtype=dtype)
+    ld = -(-K // 8) * 8 + 8
+    dA, dB = (torch.full((n, ld), 7.0, device="cuda", dtype=dtype) for n in (M, N))
+    s = torch.cuda.Stream()
+    need = tg.workspace_bytes(tg.TG_CALL_GEMM_BF16_XENT_GRAD, M, N, K,
+                              d_dtype=tg.TG_D_F32 if f32 else tg.TG_D_BF16)
+    tg.reserve_workspace(need, stream=s)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=s):
+        tg.gemm_bf16_xent_grad(A, B, t, lse, grad, dA[:, :K], dB[:, :K])
+    for _ in range(3):
+        with torch.cuda.stream(s):
+            graph.replay()
+        other = tg.gemm_bf16_xent_grad(A, B, t, lse, grad, out_dtype=dtype)
+    torch.cuda.synchronize()
+    for got, tall, ref in zip(other, (dA, dB), want):
+        assert torch.equal(got, ref) and torch.equal(tall[:, :K], ref)
+        assert (tall[:, K:] == 7).all()
