@@ -27,9 +27,11 @@ struct XentTiles {
 // Columns per tile: the width whose waves over the units take least.  A stage of
 // a CTA pair costs the larger of its MMAs (2 cycles a column) and its loads (128
 // rows of A and half the columns of B at 64 bytes a cycle).  One of few rows streams
-// B from HBM, and A's rows with it, but no stage takes less than the 0.3 us in which a
-// producer issues its loads (one token x 64000 x 4096: tiles of 48 columns 186 us, 112
-// 90, 224 78, i.e. 6.7 TB/s); the last tile's epilogue is hidden by nothing.
+// B from HBM, and A's rows with it, but no stage takes less than the 0.3 us of its four
+// MMAs (0.1 whatever their width), its wait and commit, and its share of a chunk's
+// hand-over (0.1); fewer loads or slots change nothing (one token x 64000 x 4096: tiles
+// of 48 columns 186 us, 112 90, 224 78, i.e. 6.7 TB/s).  The last tile's epilogue is
+// hidden by nothing.
 inline XentTiles xent_tiles(int64_t M, int64_t N, int step) {
   const bool few = M <= kXentFewRows;
   const int64_t units = few ? kXentSms : kXentSms / 2;
