@@ -153,6 +153,9 @@ def lib() -> ctypes.CDLL:
         L.gemm_bf16_xent_grad.restype = i32
         L.gemm_bf16_xent_grad.argtypes = [vp, i64, vp, i64, vp, vp, vp, f32, vp, i64, vp, i64, i64,
                                           i64, i64, i32, u32, vp]
+        L.gemm_bf16_xent_grad_ex.restype = i32
+        L.gemm_bf16_xent_grad_ex.argtypes = [vp, i64, vp, i64, vp, vp, vp, vp, f32, vp, i64, vp, i64,
+                                             i64, i64, i64, i32, u32, vp]
         L.embed_rows.restype = i32
         L.embed_rows.argtypes = [vp, i64, i64, vp, i64, i64, f32, vp, i64, i32, vp]
         L.embed_rows_grad.restype = i32
@@ -524,15 +527,17 @@ TG_FN_EMBED_ROWS = 7
 TG_FN_EMBED_ROWS_GRAD = 8
 TG_FN_BALANCE_LOSS = 9
 TG_FN_BALANCE_LOSS_GRAD = 10
+TG_FN_GEMM_BF16_XENT_GRAD_EX = 11
 # Each call's arguments as 64-bit words (pointers as addresses, None as 0; "f4x":
 # a float and the word's other half).
 _WORDS = [struct.Struct(f).pack for f in
           ("=7q", "=18q", "=15q", "=17q", "=23q", "=5qf4x7q", "=7qf4x10q", "=6qf4x4q", "=7qf4x5q",
-           "=11q", "=13q")]
-_COUNT = (7, 18, 15, 17, 23, 13, 18, 11, 13, 11, 13)
+           "=11q", "=13q", "=8qf4x10q")]
+_COUNT = (7, 18, 15, 17, 23, 13, 18, 11, 13, 11, 13, 19)
 _NAMES = ("tg_group_rows", "gemm_bf16_grouped", "gemm_bf16_grouped_dgrad",
           "gemm_bf16_grouped_wgrad", "gemm_bf16_lora", "gemm_bf16_xent", "gemm_bf16_xent_grad",
-          "embed_rows", "embed_rows_grad", "tg_balance_loss", "tg_balance_loss_grad")
+          "embed_rows", "embed_rows_grad", "tg_balance_loss", "tg_balance_loss_grad",
+          "gemm_bf16_xent_grad_ex")
 
 
 def _call(fn, *words):
@@ -720,12 +725,14 @@ def gemm_bf16_xent(A, B, targets, *, scale=1.0, stream=None):
     return loss, lse
 
 
-def gemm_bf16_xent_grad(A, B, targets, lse, grad=None, dA=None, dB=None, *, scale=1.0,
+def gemm_bf16_xent_grad(A, B, targets, lse, grad=None, dA=None, dB=None, *, loss=None, scale=1.0,
                         out_dtype=None, rows=True, weights=True, stream=None):
     """(dA, dB): the gradients of sum(grad * loss) of ``gemm_bf16_xent``.
 
-    lse: its second result for the same A, B and scale; grad: float32 [M], or
-    None for 1.  Rows without a target get a zero row of dA and have no part in
+    lse: its second result for the same A, B and scale; loss: its first, with
+    which rows whose target has nearly all of the probability keep the digits
+    of what is left (without it that is off by up to 1e-6 (|z| + |lse|)); grad:
+    float32 [M], or None for 1.  Rows without a target get a zero row of dA and have no part in
     dB.  ``rows=False`` or ``weights=False`` leaves out dA or dB (None then).
     dA: [M, K], dB: [N, K], both of one type, bfloat16 or float32 (default
     bfloat16); where none is given it is allocated with rows that start on
@@ -740,6 +747,7 @@ def gemm_bf16_xent_grad(A, B, targets, lse, grad=None, dA=None, dB=None, *, scal
     if lse is None:
         raise TypeError("lse is the second result of gemm_bf16_xent")
     pl, pg = _f32_vector(lse, "lse", M), _f32_vector(grad, "grad", M)
+    po = _f32_vector(loss, "loss", M)
     for D in (dA, dB):
         if out_dtype is None and D is not None:
             out_dtype = D.dtype
@@ -759,9 +767,9 @@ def gemm_bf16_xent_grad(A, B, targets, lse, grad=None, dA=None, dB=None, *, scal
             raise ValueError("dA and dB must have one type")
     elif dB is not None:
         raise ValueError("dB is given, but weights=False")
-    _on_device(A, B, targets, lse, grad, dA, dB)
-    _call(TG_FN_GEMM_BF16_XENT_GRAD, a, lda, b, ldb, t, pl, pg, scale, pa, ldda, pb, lddb, M, N, K,
-          code, 0, _raw_stream(stream))
+    _on_device(A, B, targets, lse, loss, grad, dA, dB)
+    _call(TG_FN_GEMM_BF16_XENT_GRAD_EX, a, lda, b, ldb, t, pl, po, pg, scale, pa, ldda, pb, lddb, M,
+          N, K, code, 0, _raw_stream(stream))
     return dA, dB
 
 

@@ -874,6 +874,7 @@ extern "C" int tg_call_packed(int fn, const int64_t* args, int count) {
     case TG_FN_EMBED_ROWS_GRAD: return call_packed(embed_rows_grad, args, count);
     case TG_FN_BALANCE_LOSS: return call_packed(tg_balance_loss, args, count);
     case TG_FN_BALANCE_LOSS_GRAD: return call_packed(tg_balance_loss_grad, args, count);
+    case TG_FN_GEMM_BF16_XENT_GRAD_EX: return call_packed(gemm_bf16_xent_grad_ex, args, count);
     default: return TG_ERR_INVALID_ARG;
   }
 }

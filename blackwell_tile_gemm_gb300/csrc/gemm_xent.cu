@@ -407,10 +407,11 @@ int gemm_bf16_xent(const void* A, int64_t lda, const void* B, int64_t ldb, const
                         a.scale, a.scale2);
 }
 
-int gemm_bf16_xent_grad(const void* A, int64_t lda, const void* B, int64_t ldb,
-                        const int32_t* targets, const float* lse, const float* grad, float scale,
-                        void* dA, int64_t ldda, void* dB, int64_t lddb, int64_t M, int64_t N,
-                        int64_t K, int d_dtype, unsigned flags, void* cuda_stream) {
+int gemm_bf16_xent_grad_ex(const void* A, int64_t lda, const void* B, int64_t ldb,
+                           const int32_t* targets, const float* lse, const float* loss,
+                           const float* grad, float scale, void* dA, int64_t ldda, void* dB,
+                           int64_t lddb, int64_t M, int64_t N, int64_t K, int d_dtype,
+                           unsigned flags, void* cuda_stream) {
   int rc = check_xent(M, N, K, scale, flags);
   if (rc != TG_OK) return rc;
   if (d_dtype != TG_D_F32 && d_dtype != TG_D_BF16) return TG_ERR_INVALID_ARG;
@@ -453,6 +454,7 @@ int gemm_bf16_xent_grad(const void* A, int64_t lda, const void* B, int64_t ldb,
   a.scale2 = scale * 1.4426950408889634f;
   a.targets = targets;
   a.lse = lse;
+  a.loss = loss;
   a.grad = grad;
   a.A = static_cast<const uint16_t*>(A);
   a.lda = lda;
@@ -548,6 +550,14 @@ int gemm_bf16_xent_grad(const void* A, int64_t lda, const void* B, int64_t ldb,
     }
   }
   return rc;
+}
+
+int gemm_bf16_xent_grad(const void* A, int64_t lda, const void* B, int64_t ldb,
+                        const int32_t* targets, const float* lse, const float* grad, float scale,
+                        void* dA, int64_t ldda, void* dB, int64_t lddb, int64_t M, int64_t N,
+                        int64_t K, int d_dtype, unsigned flags, void* cuda_stream) {
+  return gemm_bf16_xent_grad_ex(A, lda, B, ldb, targets, lse, nullptr, grad, scale, dA, ldda, dB,
+                                lddb, M, N, K, d_dtype, flags, cuda_stream);
 }
 
 }  // extern "C"

@@ -57,6 +57,7 @@ struct XentArgs {
   float* target_z;     // [M] accumulator of the target, where that is among the columns
   // kXentGrad
   const float* lse;    // [M]
+  const float* loss;   // [M], or null: the target's dz from z and lse
   const float* grad;   // [M], or null for 1
   // Where not null, the kernel also copies A's rows there (`terms` times in a row,
   // ld_copy apart), zeros for rows without a target: dz is 0 in those, but 0 times
@@ -93,15 +94,16 @@ struct XentCfg {
   static constexpr int kThreads = 64 + 32 * kEpiWarps;
   // The tensor cores truncate each time they add to an accumulator: z comes out
   // too small by 1e-6 of itself for each 1000 terms.  A loss between 0.1 and 1 of
-  // a target far above the others takes ten times that on, and f32 gradients take
-  // it on as well; so for those long contractions are cut into chunks of kChunk
-  // stages that are added in registers with rounding to nearest.  Few rows wait for
+  // a target far above the others takes ten times that on, f32 gradients take it on as
+  // well, and bf16 ones where they are a rest: the target's dz, p - 1, takes on whatever
+  // sets this z apart from the one that lse has seen.  So long contractions are cut into
+  // chunks of kChunk stages, the same in every mode, that are added in registers with
+  // rounding to nearest.  Few rows wait for
   // HBM, unless the vocabulary is small (83 x 2282 x 3734 with chunks of 256, 512 and
   // 1024 terms: 31.1, 28.9 and 26.9 us; error of 64 losses over 32000 x 2048 1.4e-7 and
   // 3.1e-7 with 256 and 512).  For pairs a chunk costs (1024 x 48640 x 4096, chunks of
   // 4096, 2048, 1024 and 512 terms: 217, 220, 226 and 234 us, error of the loss 2.8e-6,
-  // 1.4e-6, 6e-7 and 3e-7).  dz that is rounded to bf16 needs none.
-  static constexpr bool kChunked = kMode != kXentGrad;
+  // 1.4e-6, 6e-7 and 3e-7).
   static constexpr int kChunk = kCtaGroup == 1 ? 4 : 16;
   static_assert(SMEM_BYTES <= 227 * 1024, "shared memory per CTA");
 };
@@ -131,17 +133,20 @@ __device__ __forceinline__ float rest_of_bf16(float x, float r) {
   return fabsf(r) < __uint_as_float(0x7F800000u) ? x - r : 0.0f;
 }
 
-// kN accumulator columns of this lane's row, to z or added to it.
+// kN accumulator columns of this lane's row, to z or added to it, 32 at a time.
 template <bool kAdd, int kN>
 __device__ __forceinline__ void xent_read(uint32_t taddr, float (&z)[kN]) {
-  uint32_t v[kN];
 #pragma unroll
-  for (int e = 0; e < kN; e += 16) tmem_ld_32x32b_x16(taddr + e, v + e);
-  tmem_ld_wait();
+  for (int e0 = 0; e0 < kN; e0 += 32) {
+    uint32_t v[32];
+    tmem_ld_32x32b_x16(taddr + e0, v);
+    tmem_ld_32x32b_x16(taddr + e0 + 16, v + 16);
+    tmem_ld_wait();
 #pragma unroll
-  for (int e = 0; e < kN; ++e) {
-    const float x = __uint_as_float(v[e]);
-    z[e] = kAdd ? z[e] + x : x;
+    for (int e = 0; e < 32; ++e) {
+      const float x = __uint_as_float(v[e]);
+      z[e0 + e] = kAdd ? z[e0 + e] + x : x;
+    }
   }
 }
 
@@ -240,10 +245,8 @@ __global__ void __launch_bounds__(C::kThreads, 1)
   const int num_units = gridDim.x / C::kCtaGroup;
   const int num_tiles = p.num_m_tiles * p.num_n_tiles;
   const int nk = p.num_k_blocks;
-  const int chunks = C::kChunked ? (nk + C::kChunk - 1) / C::kChunk : 1;
-  auto chunk_end = [&](int c) {
-    return C::kChunked ? static_cast<int>(static_cast<int64_t>(nk) * (c + 1) / chunks) : nk;
-  };
+  const int chunks = (nk + C::kChunk - 1) / C::kChunk;
+  auto chunk_end = [&](int c) { return static_cast<int>(static_cast<int64_t>(nk) * (c + 1) / chunks); };
 
   if (warp == 0) {
     // ------------------------------------------------------------ producer
@@ -415,7 +418,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
     int last_tm = -1;
     int target = -1;                 // column of this launch, or negative
     bool learned = false;            // the row has a target in the vocabulary
-    float lse = 0.0f, weight = 0.0f;
+    float lse = 0.0f, weight = 0.0f, own_dz = 0.0f;
     bool ok = true;
     for (int t = unit; ok && t < num_tiles; t += num_units) {
       int tm, tn;
@@ -432,6 +435,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
         if constexpr (C::kMode != kXentLoss) {
           lse = learned ? p.lse[row] : 0.0f;
           weight = learned ? (p.grad ? p.grad[row] : 1.0f) * p.scale : 0.0f;
+          if (p.loss != nullptr) own_dz = learned ? expm1f(-p.loss[row]) : 0.0f;
         }
       }
       // The target's place in the tile, if this warp has it (else negative).
@@ -507,12 +511,22 @@ __global__ void __launch_bounds__(C::kThreads, 1)
         // dz of a box of 64 columns, from its accumulators, in place.
         auto gradient = [&](float (&z)[64], int box0) {
 #pragma unroll
-          for (int e = 0; e < 64; ++e) z[e] = exp2_approx(fmaf(z[e], p.scale, -lse) * 1.4426950408889634f);
+          for (int e = 0; e < 64; ++e) z[e] = fmaf(z[e], p.scale, -lse);
+          // The target's p - 1 without the subtraction: where p is near 1 the digits that
+          // count are those of the exponent, and the loss has more of them than z - lse,
+          // which two rounded numbers of its size leave.
           const int own = here - box0;
           if (own >= 0 && own < 64) {
+            float x = 0.0f;
 #pragma unroll
             for (int e = 0; e < 64; ++e)
-              if (own == e) z[e] -= 1.0f;
+              if (own == e) x = z[e];
+            own_dz = p.loss != nullptr ? own_dz : expm1f(x);
+          }
+#pragma unroll
+          for (int e = 0; e < 64; ++e) {
+            const float pe = exp2_approx(z[e] * 1.4426950408889634f);
+            z[e] = own == e ? own_dz : pe;
           }
 #pragma unroll
           for (int e = 0; e < 64; ++e) z[e] = learned ? weight * z[e] : 0.0f;
@@ -551,46 +565,34 @@ __global__ void __launch_bounds__(C::kThreads, 1)
             bulk_commit_group();
           }
         };
+        // The warp's share of the tile stays in registers while the chunks are added (with
+        // them, 4096 x 32000 x 4096 pieces in bf16 cost 0.5% of a step, 64 x 32000 x 2048 1.5%).
         const int boxes = (cols + 63) / 64;
-        if constexpr (!C::kTwo) {
-          if (!acc_ready()) break;
-          const uint32_t t_row = t_slab + static_cast<uint32_t>(acc * C::BN);
-#pragma unroll 1
-          for (int b = half; b < boxes; b += 2) {
-            float z[64];
-            xent_read<false>(t_row + 64 * b, z);
-            gradient(z, 64 * b);
-            if (row0 < p.padded) store(z, 64 * b, &tmD);
+        float z[2][64];
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+          for (int e = 0; e < 64; ++e) z[i][e] = 0.0f;
+        for (int c = 0; c < chunks; ++c) {
+          if (!acc_ready()) {
+            ok = false;
+            break;
           }
-          hand_back();
-        } else {
-          float z[2][64];
+          const uint32_t t_row = t_slab + static_cast<uint32_t>(acc * C::BN);
 #pragma unroll
           for (int i = 0; i < 2; ++i)
+            if (half + 2 * i < boxes) xent_read<true>(t_row + 64 * (half + 2 * i), z[i]);
+          hand_back();
+        }
+        if (!ok) break;
 #pragma unroll
-            for (int e = 0; e < 64; ++e) z[i][e] = 0.0f;
-          for (int c = 0; c < chunks; ++c) {
-            if (!acc_ready()) {
-              ok = false;
-              break;
-            }
-            const uint32_t t_row = t_slab + static_cast<uint32_t>(acc * C::BN);
-#pragma unroll
-            for (int i = 0; i < 2; ++i)
-              if (half + 2 * i < boxes) xent_read<true>(t_row + 64 * (half + 2 * i), z[i]);
-            hand_back();
-          }
-          if (!ok) break;
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const int b = half + 2 * i;
-            if (b >= boxes) continue;
-            gradient(z[i], 64 * b);
-            if (row0 < p.padded) {
-              store(z[i], 64 * b, &tmD);
-              store(z[i], 64 * b, &tmD2);
-            }
-          }
+        for (int i = 0; i < 2; ++i) {
+          const int b = half + 2 * i;
+          if (b >= boxes) continue;
+          gradient(z[i], 64 * b);
+          if (row0 >= p.padded) continue;
+          store(z[i], 64 * b, &tmD);
+          if constexpr (C::kTwo) store(z[i], 64 * b, &tmD2);
         }
       }
     }

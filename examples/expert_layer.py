@@ -102,7 +102,7 @@ def step(ids, targets, table, w_router, w_in, w_out, k, balance=0.01):
     learned /= learned.sum().clamp(min=1)
     loss = (losses * learned).sum() + balance * uneven
     # Back.
-    g_h, g_table = tg.gemm_bf16_xent_grad(h, table, targets, lse, learned,
+    g_h, g_table = tg.gemm_bf16_xent_grad(h, table, targets, lse, learned, loss=losses,
                                           out_dtype=torch.float32)
     g_x, g_weights, g_in, g_out = experts_back(x, weights, plan, k, w_in, w_out, kept, g_h)
     g_best = weights * (g_weights - (weights * g_weights).sum(1, keepdim=True))

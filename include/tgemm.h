@@ -425,7 +425,9 @@ int gemm_bf16_xent(const void* A, int64_t lda, const void* B, int64_t ldb, const
  * Rows without a target have dz = 0: their row of dA is 0 (B being finite) and they
  * have no part in dB, whatever their row of A, lse and grad hold.  z is computed again in pieces of the
  * vocabulary; dz passes to the products as bf16, for f32 gradients as two bf16
- * terms (17 significant bits).
+ * terms (17 significant bits).  The target's entry is a rest where its p is near 1, and z
+ * and lse leave it off by up to 1e-6 (|z| + |lse|) whatever its size;
+ * gemm_bf16_xent_grad_ex keeps its digits.
  *   lse     : device, f32 [M], of gemm_bf16_xent with the same A, B and scale.
  *   grad    : device, f32 [M], or NULL for 1.
  *   dA      : device, [M, K] of d_dtype, row stride ldda, or NULL: not wanted.
@@ -438,6 +440,18 @@ int gemm_bf16_xent_grad(const void* A, int64_t lda, const void* B, int64_t ldb,
                         const int32_t* targets, const float* lse, const float* grad, float scale,
                         void* dA, int64_t ldda, void* dB, int64_t lddb, int64_t M, int64_t N,
                         int64_t K, int d_dtype, unsigned flags, void* cuda_stream);
+
+/*
+ * gemm_bf16_xent_grad_ex -- the same, with the target's entry from the loss:
+ *   dz[i, targets[i]] = grad[i] * scale * (exp(-loss[i]) - 1)
+ * which is as exact as the loss is, however small.
+ *   loss    : device, f32 [M], of the call that gave lse, or NULL: as above.
+ */
+int gemm_bf16_xent_grad_ex(const void* A, int64_t lda, const void* B, int64_t ldb,
+                           const int32_t* targets, const float* lse, const float* loss,
+                           const float* grad, float scale, void* dA, int64_t ldda, void* dB,
+                           int64_t lddb, int64_t M, int64_t N, int64_t K, int d_dtype,
+                           unsigned flags, void* cuda_stream);
 
 /*
  * embed_rows -- D[i, :] = scale * W[ids[i], :], zeros where ids[i] is outside
@@ -516,7 +530,8 @@ enum {
   TG_FN_EMBED_ROWS = 7,
   TG_FN_EMBED_ROWS_GRAD = 8,
   TG_FN_BALANCE_LOSS = 9,
-  TG_FN_BALANCE_LOSS_GRAD = 10
+  TG_FN_BALANCE_LOSS_GRAD = 10,
+  TG_FN_GEMM_BF16_XENT_GRAD_EX = 11
 };
 int tg_call_packed(int fn, const int64_t* args, int count);
 

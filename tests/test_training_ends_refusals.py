@@ -1,0 +1,45 @@
+"""Calls of the loss, token rows and balance that the binding or the library has to
+refuse, without a GPU."""
+import pytest
+import torch
+
+import blackwell_tile_gemm_gb300 as tg
+from blackwell_tile_gemm_gb300 import build as tgbuild
+
+A16 = 0x10000           # a 16-byte aligned fake device address (never dereferenced)
+BAD, ALIGN, UNSUP = tg.TG_ERR_INVALID_ARG, tg.TG_ERR_MISALIGNED, tg.TG_ERR_UNSUPPORTED
+
+
+@pytest.fixture(scope="module")
+def L():
+    tgbuild.build()
+    return tg.lib()
+
+
+@pytest.fixture
+def no_library(monkeypatch):
+    class Refuse:
+        def __getattr__(self, name):
+            raise AssertionError("the binding called the library")
+    monkeypatch.setattr(tg, "_lib", Refuse())
+
+
+@pytest.mark.parametrize("loss", [None, A16])
+@pytest.mark.parametrize("kw,code", [
+    (dict(M=-1), BAD), (dict(scale=0.0), BAD), (dict(lse=None), BAD), (dict(t=None), BAD),
+    (dict(d=2), BAD), (dict(ldda=60), BAD), (dict(ldda=66), ALIGN), (dict(M=2 ** 30), UNSUP),
+    (dict(flags=1), UNSUP), (dict(dA=None, dB=None), 0), (dict(K=0), 0)])
+def test_gradient_with_the_loss_rejects_before_launch(L, kw, code, loss):
+    a = dict(t=A16, lse=A16, scale=1.0, dA=A16, ldda=64, dB=A16, M=100, N=500, K=64, d=0, flags=0)
+    a.update(kw)
+    assert L.gemm_bf16_xent_grad_ex(A16, 64, A16, 64, a["t"], a["lse"], loss, None, a["scale"],
+                                    a["dA"], a["ldda"], a["dB"], 64, a["M"], a["N"], a["K"], a["d"],
+                                    a["flags"], None) == code
+
+
+@pytest.mark.parametrize("loss", [torch.zeros(7), torch.zeros(8, 1), torch.zeros(8).double(),
+                                  torch.zeros(16)[::2]])
+def test_a_loss_of_another_form_is_refused(no_library, loss):
+    A, B = torch.zeros(8, 16, dtype=torch.bfloat16), torch.zeros(9, 16, dtype=torch.bfloat16)
+    with pytest.raises(TypeError):
+        tg.gemm_bf16_xent_grad(A, B, torch.zeros(8, dtype=torch.int32), torch.zeros(8), loss=loss)
