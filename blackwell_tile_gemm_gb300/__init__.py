@@ -826,7 +826,9 @@ def _router(logits, ids):
         raise TypeError("ids must be a contiguous int32 matrix")
     if ids.shape[0] != M:
         raise ValueError("logits are [tokens, experts] and ids [tokens, choices]")
-    return M, E, max(ld, E), z, _d_code(logits.dtype), ids.shape[1], ids.data_ptr()
+    if ld < E:
+        raise ValueError("rows of logits overlap")
+    return M, E, ld, z, _d_code(logits.dtype), ids.shape[1], ids.data_ptr()
 
 
 def balance_loss(logits, ids, *, stream=None):
@@ -870,8 +872,10 @@ def balance_loss_grad(logits, ids, shares, grad=None, D=None, *, out_dtype=None,
     elif D.shape != (M, E):
         raise ValueError(f"D must be {[M, E]}")
     _, _, ldd, d = _matrix(D, "D", D.dtype)
+    if ldd < E:
+        raise ValueError("rows of D overlap")
     _on_device(logits, ids, shares, grad, D)
-    _call(TG_FN_BALANCE_LOSS_GRAD, z, ld, code, ip, choices, M, E, ps, pg, d, max(ldd, E),
+    _call(TG_FN_BALANCE_LOSS_GRAD, z, ld, code, ip, choices, M, E, ps, pg, d, ldd,
           _d_code(D.dtype), _raw_stream(stream))
     return D
 

@@ -43,3 +43,19 @@ def test_a_loss_of_another_form_is_refused(no_library, loss):
     A, B = torch.zeros(8, 16, dtype=torch.bfloat16), torch.zeros(9, 16, dtype=torch.bfloat16)
     with pytest.raises(TypeError):
         tg.gemm_bf16_xent_grad(A, B, torch.zeros(8, dtype=torch.int32), torch.zeros(8), loss=loss)
+
+
+@pytest.mark.parametrize("rows", [2, 5])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_rows_of_a_router_that_share_memory_are_refused(no_library, rows, dtype):
+    """One row for all tokens, or rows that overlap: reading them a row's width apart would
+    leave the tensor."""
+    ids = torch.zeros(rows, 2, dtype=torch.int32)
+    fine = torch.zeros(rows, 8, dtype=dtype)
+    for shared in (torch.zeros(8, dtype=dtype).expand(rows, 8),
+                   torch.zeros(64, dtype=dtype).as_strided((rows, 8), (4, 1))):
+        for call in (lambda: tg.balance_loss(shared, ids),
+                     lambda: tg.balance_loss_grad(shared, ids, torch.zeros(8)),
+                     lambda: tg.balance_loss_grad(fine, ids, torch.zeros(8), D=shared)):
+            with pytest.raises(ValueError, match="overlap"):
+                call()
