@@ -567,8 +567,11 @@ int tg_balance_loss(const void* logits, int64_t ld, int dtype, const int32_t* id
   if (!ctx) return TG_ERR_CUDA;
   cudaStream_t stream = static_cast<cudaStream_t>(cuda_stream);
   const int64_t blocks = sum_blocks(M, static_cast<int>(E));
-  float* sums = static_cast<float*>(device_workspace(balance_workspace_bytes(M, E), stream, &rc));
-  if (sums == nullptr) return rc;
+  float* sums = nullptr;   // (one block keeps its own)
+  if (blocks > 1) {
+    sums = static_cast<float*>(device_workspace(balance_workspace_bytes(M, E), stream, &rc));
+    if (sums == nullptr) return rc;
+  }
   BalanceArgs a{};
   a.logits = logits;
   a.ld = ld;
@@ -577,7 +580,7 @@ int tg_balance_loss(const void* logits, int64_t ld, int dtype, const int32_t* id
   a.M = static_cast<int>(M);
   a.E = static_cast<int>(E);
   a.sums = sums;
-  a.counts_of = reinterpret_cast<int*>(sums + blocks * E);
+  a.counts_of = blocks > 1 ? reinterpret_cast<int*>(sums + blocks * E) : nullptr;
   a.loss = loss;
   a.counts = counts;
   a.out_shares = shares;
