@@ -682,14 +682,13 @@ int64_t tg_workspace_bytes(int call, int64_t M, int64_t N, int64_t K, int64_t ld
     case TG_CALL_GEMM_BF16_LORA:
       return static_cast<int64_t>(lora_workspace_bytes(M, N));
     case TG_CALL_GEMM_BF16_XENT:
-      return static_cast<int64_t>(xent_workspace_bytes(M, N));
+      return xent_workspace_bytes(M, N, K);
     case TG_CALL_GEMM_BF16_XENT_GRAD:
-      if (d_dtype != TG_D_F32 && d_dtype != TG_D_BF16) return -TG_ERR_INVALID_ARG;
-      return static_cast<int64_t>(xent_grad_workspace_bytes(M, N, K, d_dtype));
+      return xent_grad_workspace_bytes(M, N, K, d_dtype);
     case TG_CALL_EMBED_ROWS_GRAD:
-      return static_cast<int64_t>(embed_grad_workspace_bytes(M, N, K));
+      return embed_grad_workspace_bytes(M, N, K);
     case TG_CALL_BALANCE_LOSS:
-      return static_cast<int64_t>(balance_workspace_bytes(M, N));
+      return balance_workspace_bytes(N);
     default:
       return -TG_ERR_INVALID_ARG;
   }

@@ -549,8 +549,8 @@ int check_balance(const void* logits, int64_t ld, int dtype, const int32_t* ids,
 
 }  // namespace
 
-size_t balance_workspace_bytes(int64_t, int64_t E) {
-  return static_cast<size_t>(kMostBlocks) * static_cast<size_t>(2 * E + 1) * 4u;
+int64_t balance_workspace_bytes(int64_t E) {
+  return E < 1 || E > TG_MAX_GROUPS ? -TG_ERR_INVALID_ARG : kMostBlocks * (2 * E + 1) * 4;
 }
 
 }  // namespace tg
@@ -569,7 +569,7 @@ int tg_balance_loss(const void* logits, int64_t ld, int dtype, const int32_t* id
   const int64_t blocks = sum_blocks(M, static_cast<int>(E));
   float* sums = nullptr;   // (one block keeps its own)
   if (blocks > 1) {
-    sums = static_cast<float*>(device_workspace(balance_workspace_bytes(M, E), stream, &rc));
+    sums = static_cast<float*>(device_workspace(static_cast<size_t>(balance_workspace_bytes(E)), stream, &rc));
     if (sums == nullptr) return rc;
   }
   BalanceArgs a{};

@@ -731,8 +731,9 @@ int esize(int dtype) { return dtype == TG_D_BF16 ? 2 : 4; }
 
 }  // namespace
 
-size_t embed_grad_workspace_bytes(int64_t n, int64_t rows, int64_t K) {
-  return embed_plan(n, rows, K).bytes;
+int64_t embed_grad_workspace_bytes(int64_t n, int64_t rows, int64_t K) {
+  const int rc = check_embed(n, rows, K, TG_D_F32, TG_D_F32);
+  return rc != TG_OK ? -rc : static_cast<int64_t>(embed_plan(n, rows, K).bytes);
 }
 
 }  // namespace tg

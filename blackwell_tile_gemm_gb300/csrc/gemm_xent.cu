@@ -338,13 +338,9 @@ int check_rows(const void* p, int64_t ld, int64_t width, int esize) {
   return TG_OK;
 }
 
-int check_xent(int64_t M, int64_t N, int64_t K, float scale, unsigned flags) {
+int check_sizes(int64_t M, int64_t N, int64_t K) {
   if (M < 0 || N < 0 || K < 0 || M > kMaxDim || N > kMaxDim || K > kMaxDim)
     return TG_ERR_INVALID_ARG;
-  // (A negative scale would make the smallest product the largest logit; log2(e)
-  // times the largest is still finite.)
-  if (!(scale > 0.0f) || scale > 1.0e38f) return TG_ERR_INVALID_ARG;
-  if (flags != 0) return TG_ERR_UNSUPPORTED;
   if (M > kGroupedMaxExtent || N > kGroupedMaxExtent || K > kGroupedMaxExtent)
     return TG_ERR_UNSUPPORTED;
   // Tile counts stay below 2^31, also those of the gradients' products.
@@ -354,11 +350,31 @@ int check_xent(int64_t M, int64_t N, int64_t K, float scale, unsigned flags) {
   return TG_OK;
 }
 
+// (f32 gradients: two rows of dz for one of A.)
+int check_grad_sizes(int64_t M, int64_t N, int64_t K, int d_dtype) {
+  const int rc = check_sizes(M, N, K);
+  if (rc != TG_OK) return rc;
+  if (d_dtype != TG_D_F32 && d_dtype != TG_D_BF16) return TG_ERR_INVALID_ARG;
+  return d_dtype == TG_D_F32 && 2 * M > kGroupedMaxExtent ? TG_ERR_UNSUPPORTED : TG_OK;
+}
+
+int check_form(float scale, unsigned flags) {
+  // (A negative scale would make the smallest product the largest logit; log2(e)
+  // times the largest is still finite.)
+  if (!(scale > 0.0f) || scale > 1.0e38f) return TG_ERR_INVALID_ARG;
+  return flags != 0 ? TG_ERR_UNSUPPORTED : TG_OK;
+}
+
 }  // namespace
 
-size_t xent_workspace_bytes(int64_t M, int64_t N) { return xent_loss_plan(M, N).bytes; }
-size_t xent_grad_workspace_bytes(int64_t M, int64_t N, int64_t K, int d_dtype) {
-  return xent_grad_plan(M, N, K, d_dtype == TG_D_BF16).bytes;
+int64_t xent_workspace_bytes(int64_t M, int64_t N, int64_t K) {
+  const int rc = check_sizes(M, N, K);
+  return rc != TG_OK ? -rc : static_cast<int64_t>(xent_loss_plan(M, N).bytes);
+}
+int64_t xent_grad_workspace_bytes(int64_t M, int64_t N, int64_t K, int d_dtype) {
+  const int rc = check_grad_sizes(M, N, K, d_dtype);
+  return rc != TG_OK ? -rc
+                     : static_cast<int64_t>(xent_grad_plan(M, N, K, d_dtype == TG_D_BF16).bytes);
 }
 
 }  // namespace tg
@@ -368,7 +384,8 @@ extern "C" {
 int gemm_bf16_xent(const void* A, int64_t lda, const void* B, int64_t ldb, const int32_t* targets,
                    float scale, float* loss, float* lse, int64_t M, int64_t N, int64_t K,
                    unsigned flags, void* cuda_stream) {
-  int rc = check_xent(M, N, K, scale, flags);
+  int rc = check_sizes(M, N, K);
+  if (rc == TG_OK) rc = check_form(scale, flags);
   if (rc != TG_OK || M == 0) return rc;
   if (targets == nullptr || loss == nullptr || lse == nullptr) return TG_ERR_INVALID_ARG;
   if (N > 0 && K > 0) {
@@ -412,11 +429,10 @@ int gemm_bf16_xent_grad_ex(const void* A, int64_t lda, const void* B, int64_t ld
                            const float* grad, float scale, void* dA, int64_t ldda, void* dB,
                            int64_t lddb, int64_t M, int64_t N, int64_t K, int d_dtype,
                            unsigned flags, void* cuda_stream) {
-  int rc = check_xent(M, N, K, scale, flags);
+  int rc = check_grad_sizes(M, N, K, d_dtype);
+  if (rc == TG_OK) rc = check_form(scale, flags);
   if (rc != TG_OK) return rc;
-  if (d_dtype != TG_D_F32 && d_dtype != TG_D_BF16) return TG_ERR_INVALID_ARG;
   const bool bf16 = d_dtype == TG_D_BF16;
-  if (!bf16 && 2 * M > kGroupedMaxExtent) return TG_ERR_UNSUPPORTED;
   if (K == 0) return TG_OK;
   const int esize = bf16 ? 2 : 4;
   const bool rows = dA != nullptr && M > 0, weights = dB != nullptr && N > 0;

@@ -208,11 +208,11 @@ int sort_ids(const int* ids, int64_t n, int64_t limit, int* order, int* other, i
              int* count, unsigned* marks, void* histograms, cudaStream_t stream, DeviceCtx* ctx);
 
 // Workspaces of gemm_bf16_xent, gemm_bf16_xent_grad, embed_rows_grad and
-// tg_balance_loss.
-size_t xent_workspace_bytes(int64_t M, int64_t N);
-size_t xent_grad_workspace_bytes(int64_t M, int64_t N, int64_t K, int d_dtype);
-size_t embed_grad_workspace_bytes(int64_t n, int64_t rows, int64_t K);
-size_t balance_workspace_bytes(int64_t M, int64_t N);
+// tg_balance_loss; minus the status of sizes that these calls refuse.
+int64_t xent_workspace_bytes(int64_t M, int64_t N, int64_t K);
+int64_t xent_grad_workspace_bytes(int64_t M, int64_t N, int64_t K, int d_dtype);
+int64_t embed_grad_workspace_bytes(int64_t n, int64_t rows, int64_t K);
+int64_t balance_workspace_bytes(int64_t E);
 
 // Workspace of gemm_bf16_lora.
 size_t lora_workspace_bytes(int64_t M, int64_t rank);

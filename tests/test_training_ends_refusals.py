@@ -59,3 +59,30 @@ def test_rows_of_a_router_that_share_memory_are_refused(no_library, rows, dtype)
                      lambda: tg.balance_loss_grad(fine, ids, torch.zeros(8), D=shared)):
             with pytest.raises(ValueError, match="overlap"):
                 call()
+
+
+XENT, GRAD, TABLE, BALANCE = (tg.TG_CALL_GEMM_BF16_XENT, tg.TG_CALL_GEMM_BF16_XENT_GRAD,
+                              tg.TG_CALL_EMBED_ROWS_GRAD, tg.TG_CALL_BALANCE_LOSS)
+MOST = 2 ** 31 - 1
+
+
+@pytest.mark.parametrize("call,sizes,d,code", [
+    (XENT, (MOST, 1, 1), 0, UNSUP), (XENT, (2 ** 31 - 4096, 2 ** 31 - 4096, 1), 0, UNSUP),
+    (GRAD, (MOST, 1, MOST), 1, UNSUP), (GRAD, (1, MOST, MOST), 1, UNSUP),
+    (GRAD, (MOST, MOST, MOST), 0, UNSUP), (GRAD, (2 ** 30, 1000, 64), 0, UNSUP),
+    (GRAD, (100, 1000, 64), 2, BAD), (TABLE, (2 ** 30 + 1, 1, 1), 0, BAD),
+    (TABLE, (1, 1, 256 * 65535 + 1), 0, UNSUP), (BALANCE, (9, tg.TG_MAX_GROUPS + 1, 1), 0, BAD)])
+def test_no_workspace_is_named_for_sizes_that_are_refused(L, call, sizes, d, code):
+    """(Some of them have no 64-bit number of bytes at all.)"""
+    with pytest.raises(tg.TgError) as e:
+        tg.workspace_bytes(call, *sizes, d_dtype=d)
+    assert e.value.code == code
+
+
+@pytest.mark.parametrize("call,sizes,d", [
+    (XENT, (2 ** 31 - 4096, 16000, 64), 0), (XENT, (1, 2 ** 31 - 4096, 64), 0),
+    (GRAD, (2 ** 31 - 4096, 1000, 64), 1), (GRAD, (2 ** 30 - 2048, 1000, 64), 0),
+    (GRAD, (1000, 2 ** 31 - 4096, 64), 0), (GRAD, (64, 1000, 2 ** 31 - 4096), 0),
+    (TABLE, (2 ** 30, MOST, 256 * 65535), 0), (BALANCE, (9, tg.TG_MAX_GROUPS, 1), 0)])
+def test_the_largest_sizes_have_a_workspace(L, call, sizes, d):
+    assert 0 < tg.workspace_bytes(call, *sizes, d_dtype=d) < 2 ** 50
