@@ -467,7 +467,6 @@ int gemm_bf16_xent_grad_ex(const void* A, int64_t lda, const void* B, int64_t ld
   a.M = m;
   a.vocab = static_cast<int>(N);
   a.scale = scale;
-  a.scale2 = scale * 1.4426950408889634f;
   a.targets = targets;
   a.lse = lse;
   a.loss = loss;

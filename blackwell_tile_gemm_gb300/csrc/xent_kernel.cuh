@@ -49,10 +49,10 @@ struct XentArgs {
   int raster_group;    // m-tiles per band of the tile order
   int a_box;           // rows of A per load (128; few rows: theirs, rounded up to 8)
   int stages, a_bytes, b_bytes;   // the ring: slots, bytes of A and of B in each
-  float scale2;        // scale * log2(e)
   float scale;
   const int* targets;  // [M]
   // kXentLoss
+  float scale2;        // scale * log2(e)
   float2* parts;       // [2 * num_n_tiles][M]: largest accumulator m, sum of exp(scale (a - m))
   float* target_z;     // [M] accumulator of the target, where that is among the columns
   // kXentGrad
