@@ -22,7 +22,8 @@ def test_what_the_call_names_is_enough(tg, M, E):
     gen = torch.Generator(device="cuda").manual_seed(M + E)
     logits = torch.randn(M, E, generator=gen, device="cuda")
     ids = torch.randint(0, E, (M, 2), generator=gen, device="cuda", dtype=torch.int32)
-    s = torch.cuda.Stream()
+    # (Of the other pool: tests that want a stream without a workspace find one.)
+    s = torch.cuda.Stream(priority=-1)
     s.wait_stream(torch.cuda.current_stream())
     tg.reserve_workspace(tg.workspace_bytes(tg.TG_CALL_BALANCE_LOSS, M, E, 1), stream=s)
     count = tg.workspace_alloc_count()

@@ -33,7 +33,8 @@ def test_digits_call_after_call(tg, n, rows, captured):
         draws.append(torch.where(hot > 0.98, -1 - v, v))
     ids = draws[0].clone()
     D = torch.zeros(rows, K, device="cuda", dtype=torch.bfloat16)
-    s = torch.cuda.Stream()
+    # (Of the other pool: tests that want a stream without a workspace find one.)
+    s = torch.cuda.Stream(priority=-1)
     s.wait_stream(torch.cuda.current_stream())
     tg.reserve_workspace(tg.workspace_bytes(tg.TG_CALL_EMBED_ROWS_GRAD, n, rows, K), stream=s)
     out = []

@@ -112,7 +112,8 @@ def test_a_loss_beside_rows_without_a_target(tg, M):
 def test_captured_with_the_loss(tg):
     import torch
     A, B, t, grad = confident(7, 150, 2000, 520)
-    s = torch.cuda.Stream()
+    # (Of the other pool: tests that want a stream without a workspace find one.)
+    s = torch.cuda.Stream(priority=-1)
     tg.reserve_workspace(max(tg.workspace_bytes(tg.TG_CALL_GEMM_BF16_XENT, 150, 2000, 520),
                              tg.workspace_bytes(tg.TG_CALL_GEMM_BF16_XENT_GRAD, 150, 2000, 520,
                                                 d_dtype=tg.TG_D_BF16)), stream=s)
