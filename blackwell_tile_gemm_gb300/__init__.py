@@ -23,6 +23,12 @@ Entry points (same names as the C ABI):
 * ``balance_loss(logits, ids)``                   -- balance loss and counts of a
   router; with ``_grad`` its gradient
 * ``tg_device_status(stream=None)``               -- device-side error record
+
+``stream``: where a call's kernels run (default: torch's current stream).  Results
+that a call allocates belong to the current stream all the same; with another one
+given, let it wait for the current stream right before the call and the current
+one for it before the results are used or dropped, or make the call under
+``torch.cuda.stream(s)``.
 """
 from __future__ import annotations
 
@@ -732,8 +738,8 @@ def gemm_bf16_xent_grad(A, B, targets, lse, grad=None, dA=None, dB=None, *, loss
     lse: its second result for the same A, B and scale; loss: its first, with
     which rows whose target has nearly all of the probability keep the digits
     of what is left (without it that is off by up to 1e-6 (|z| + |lse|)); grad:
-    float32 [M], or None for 1.  Rows without a target get a zero row of dA and have no part in
-    dB.  ``rows=False`` or ``weights=False`` leaves out dA or dB (None then).
+    float32 [M], or None for 1.  Rows without a target get a zero row of dA and
+    have no part in dB.  ``rows=False`` or ``weights=False`` leaves out dA or dB (None then).
     dA: [M, K], dB: [N, K], both of one type, bfloat16 or float32 (default
     bfloat16); where none is given it is allocated with rows that start on
     16-byte boundaries, as for ``gemm_bf16_grouped``.

@@ -412,7 +412,8 @@ int gemm_bf16_lora(const void* A, int64_t lda, const void* B, int64_t ldb, const
  *   loss, lse : device, f32 [M].  flags: 0.
  * M, N and K are at most 2^31 - 4096.  N = 0 gives lse = -inf; K = 0 gives
  * lse = log N.  An infinite or NaN logit gives what the formulas give, in its own
- * row.  Workspace: TG_CALL_GEMM_BF16_XENT.
+ * row.  Workspace: TG_CALL_GEMM_BF16_XENT: 16 bytes for each row and 128 columns of the
+ * vocabulary, a maximum and a sum from every tile (8192 x 128000: 131 MB).
  */
 int gemm_bf16_xent(const void* A, int64_t lda, const void* B, int64_t ldb, const int32_t* targets,
                    float scale, float* loss, float* lse, int64_t M, int64_t N, int64_t K,
@@ -433,8 +434,10 @@ int gemm_bf16_xent(const void* A, int64_t lda, const void* B, int64_t ldb, const
  *   dA      : device, [M, K] of d_dtype, row stride ldda, or NULL: not wanted.
  *   dB      : device, [N, K] of d_dtype, row stride lddb, or NULL: not wanted.
  * dA and dB must not overlap the inputs.  f32 gradients take M <= 2^30 - 2048.
- * Workspace: TG_CALL_GEMM_BF16_XENT_GRAD (M rows of A and dz of a piece, 256 MiB
- * or 8192 columns, once or, for f32, twice; M rows of f32 sums).
+ * Workspace: TG_CALL_GEMM_BF16_XENT_GRAD: M rows of A (for f32 twice); dz of a piece, up to
+ * 256 MiB with both of its terms, or 8192 columns where these are more; f32 sums, up to
+ * 40 MiB for slices of dA (or M rows where these are more: bf16 from several pieces) and
+ * up to 40 MiB for slices of dB, the larger alone where one piece is all.
  */
 int gemm_bf16_xent_grad(const void* A, int64_t lda, const void* B, int64_t ldb,
                         const int32_t* targets, const float* lse, const float* grad, float scale,
