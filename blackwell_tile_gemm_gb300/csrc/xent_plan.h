@@ -89,8 +89,8 @@ inline XentLossPlan xent_loss_plan(int64_t M, int64_t N) {
 // the columns at 64 bytes a cycle); a tile its start and its stores; slices their
 // `bytes` (of one) written and read at 3 KB a cycle, and a launch.
 // Loss and gradients, without slices and with: 202 rows x 120448 x 384 in bf16 200 ->
-// 143 us, 1 x 69040 x 149 90 -> 58, 20000 x 130 x 257 in f32 151 -> 107, 2259 x 1281 x
-// 392 80 -> 60; 4096 x 128000 x 4096 has tiles enough and takes none.
+// 145 us, 1 x 69040 x 149 90 -> 57, 20000 x 130 x 257 in f32 151 -> 79, 2259 x 1281 x
+// 392 80 -> 50; 4096 x 128000 x 4096 has tiles enough and takes none.
 constexpr int kXentMostSlices = 64;
 constexpr int64_t kXentSliceBytes = int64_t{40} << 20;
 
