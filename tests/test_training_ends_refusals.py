@@ -86,3 +86,18 @@ def test_no_workspace_is_named_for_sizes_that_are_refused(L, call, sizes, d, cod
     (TABLE, (2 ** 30, MOST, 256 * 65535), 0), (BALANCE, (9, tg.TG_MAX_GROUPS, 1), 0)])
 def test_the_largest_sizes_have_a_workspace(L, call, sizes, d):
     assert 0 < tg.workspace_bytes(call, *sizes, d_dtype=d) < 2 ** 50
+
+
+def test_the_gradient_with_the_loss_as_packed_words(L):
+    import struct
+
+    def call(words):
+        return L.tg_call_packed(tg.TG_FN_GEMM_BF16_XENT_GRAD_EX,
+                                struct.pack("=%dq" % len(words), *words), len(words))
+    one = struct.unpack("=I", struct.pack("=f", 1.0))[0]
+    # A, lda, B, ldb, targets, lse, loss, grad, scale, dA, ldda, dB, lddb, M, N, K, type, flags, stream
+    words = [A16, 64, A16, 64, A16, A16, A16, 0, one, 0, 64, 0, 64, 100, 500, 64, 0, 0, 0]
+    assert call(words) == 0                                   # neither gradient is wanted
+    assert call(words[:-1]) == BAD
+    assert call(words[:8] + [-1] + words[9:]) == BAD          # no float
+    assert call(words[:9] + [A16, 60] + words[11:]) == BAD
